@@ -314,6 +314,131 @@ moe_status moe_quantize_q4(const moe_bf16 *w, int rows, int cols, uint8_t *q, fl
 moe_status moe_quantize_e4m3(const moe_bf16 *w, int rows, int cols, uint8_t *q, float *scale,
                              void *stream);
 
+/* ---- the rest of a decoder layer: block norms, the paged 8-bit cache, attention ----
+ *
+ * The MoE layer above is one half of a decoder layer; these three calls are the other half
+ * ("AIMA AMD395 Qwen3.6 35B Windows Engine", "性能优化做了什么": the engine whose timed path the
+ * MoE kernel is part of; the pages give no formulas for the rest, so every reading is this
+ * library's).  The conventions above hold, with these differences: activations are bf16 or
+ * fp16 (moe_dtype), rows may lie apart (a row stride in elements, a multiple of 8, so that q,
+ * k and v can be columns of one product), and the workspace is moe_attn_workspace_size's. */
+
+typedef enum { MOE_DTYPE_BF16 = 0, MOE_DTYPE_F16 = 1 } moe_dtype;
+
+typedef enum {
+    MOE_GATE_NONE = 0,    /* g = 1 */
+    MOE_GATE_CHANNEL = 1, /* gate [H]: one value a channel (a learned layer scale) */
+    MOE_GATE_TOKEN = 2,   /* gate [T], row stride gate_ld: one value a token */
+    MOE_GATE_ELEMENT = 3  /* gate [T,H], row stride gate_ld */
+} moe_gate;
+
+/* Norms before and after a block, fused with its gate and residual scale. */
+typedef struct {
+    int hidden;           /* H, a multiple of 8, at most 16384 */
+    int dtype;            /* moe_dtype of every tensor of the call, weights included */
+    int gate;             /* moe_gate */
+    int gate_sigmoid;     /* 1: g = 1 / (1 + e^-gate) */
+    int unit_offset;      /* 1: the norm weights are stored as w - 1 */
+    float eps;            /* added to the mean square, >= 0 */
+    float residual_scale; /* alpha */
+} moe_norm_config;
+
+typedef struct {
+    const void *x;      /* [T,H] the block's output, or NULL: no block, only the norm before one */
+    const void *resid;  /* [T,H] the residual stream, or NULL: 0 */
+    const void *gate;   /* see moe_gate; NULL with MOE_GATE_NONE */
+    const void *w_post; /* [H] weight of the norm after the block, or NULL: no such norm */
+    const void *w_pre;  /* [H] weight of the norm before the next block; needed with y */
+    void *resid_out;    /* [T,H] the new residual stream, or NULL; may be resid */
+    void *y;            /* [T,H] the next block's input, or NULL; may be x */
+    int64_t x_ld, resid_ld, gate_ld, resid_out_ld, y_ld; /* row strides in elements */
+} moe_norm_io;
+
+/* Per row, in fp32, each output rounded once:
+ *   n  = x * w_post / sqrt(mean(x^2) + eps)    (n = x when w_post is NULL)
+ *   r' = resid + alpha * g * n                 -> resid_out
+ *   y  = r' * w_pre / sqrt(mean(r'^2) + eps)   (from r' before its rounding) -> y
+ * At least one of x and resid, and one of resid_out and y, must be given.  No workspace;
+ * deterministic.  Tensors 16-byte aligned (a per-token gate: 2), strides multiples of 8 and at
+ * least H (gate_ld of a per-token gate: at least 1). */
+moe_status moe_block_norm(const moe_norm_config *cfg, const moe_norm_io *io, int T, void *stream);
+
+/* Heads and cache layout.  kv head h serves q heads h*G .. h*G+G-1, G = q_heads / kv_heads. */
+typedef struct {
+    int q_heads;     /* a multiple of kv_heads, G <= 128 */
+    int kv_heads;
+    int head_dim;    /* D: 64, 128 or 256 */
+    int page_size;   /* P tokens a page: 16, 32, 64 or 128 */
+    int rotary_dim;  /* leading dims that are rotated: 0, or a multiple of 16 up to D */
+    int interleaved; /* 0: pairs (i, i + rotary_dim/2); 1: pairs (2i, 2i+1) */
+    int dtype;       /* moe_dtype of q, k, v and the outputs */
+} moe_attn_config;
+
+/* The paged cache: keys (after the rotation) and values as E4M3 codes, each page's tokens of one
+ * kv head under one fp32 scale: value = scale * code.  Scales are powers of two, 2^-60 .. 2^120:
+ * the code is a float itself, so a finer scale would not add precision, and with a power of
+ * two a page can move to a larger scale by an exact shift of its codes (those that become
+ * subnormal round once more). */
+typedef struct {
+    uint8_t *k_codes; /* [n_pages, kv_heads, P, D] */
+    uint8_t *v_codes; /* [n_pages, kv_heads, P, D] */
+    float *k_scale;   /* [n_pages, kv_heads] */
+    float *v_scale;   /* [n_pages, kv_heads] */
+    int n_pages;
+} moe_kv_cache;
+
+/* A batch of sequences.  Sequence b's new tokens are rows q_start[b] .. q_start[b+1]-1 of q, k
+ * and v; with n of them they have positions kv_len[b] - n .. kv_len[b] - 1.  Position p lies in
+ * page page_table[b, p / P], slot p % P. */
+typedef struct {
+    int n_seqs;                /* B >= 0, at most 65536 */
+    int n_tokens;              /* T = q_start[B] */
+    int max_pages;             /* columns of page_table */
+    const int32_t *q_start;    /* [B+1], q_start[0] = 0, not descending */
+    const int32_t *kv_len;     /* [B] cached tokens, this batch's included */
+    const int32_t *page_table; /* [B, max_pages] */
+} moe_kv_batch;
+
+/* Bytes of workspace for the two calls below on batches of up to max_seqs sequences and max_tokens
+ * new tokens (the lengths in the cache do not matter).  0 for an invalid or unsupported config.
+ * 256-byte aligned; zero it once after allocating: it begins with the status word that
+ * moe_check_status reads, and holds tickets that every call leaves at zero.  Calls that overlap
+ * must not share one. */
+size_t moe_attn_workspace_size(const moe_attn_config *cfg, int max_seqs, int max_tokens);
+
+/* Rotates q and k at their positions, writes q to q_out and k and v into the cache.
+ *   rotation  (a, b) -> (a cos - b sin, b cos + a sin), cos/sin from row p of rope, fp32
+ *             [rope_rows, rotary_dim]: rotary_dim/2 cosines, then rotary_dim/2 sines
+ *   q_out     the rotated q rounded once to dtype (correctly: from the exact value)
+ *   scale     per (page, kv head) the smallest power of two s with |value| <= 448 s over the
+ *             page's new tokens; a page that held tokens before keeps its scale if that is
+ *             larger, else its codes are re-rounded (to nearest even) under the new one
+ *   codes     the E4M3 value nearest to value / s, ties to even, of the exact rotated value
+ * A page written by one sequence of a call must not be written by another.  Tokens at negative
+ * positions (padding in front) are not cached and give q_out rows of 0.  NaN is stored as 0 and
+ * infinities as +-448 s; they, a page id outside [0, n_pages), and a position past the table or
+ * rope are reported as MOE_ERR_INVALID_ARG in the status word (the token is then not cached).
+ * q [T, q_heads, D] row stride q_ld, k and v [T, kv_heads, D] strides k_ld, v_ld, q_out stride
+ * q_out_ld (q_out may be q).  q and q_out may both be NULL. */
+moe_status moe_kv_append(const moe_attn_config *cfg, const moe_kv_cache *cache, const moe_kv_batch *batch,
+                         const void *q, int64_t q_ld, const void *k, int64_t k_ld, const void *v, int64_t v_ld,
+                         const float *rope, int rope_rows, void *q_out, int64_t q_out_ld, void *ws,
+                         size_t ws_bytes, void *stream);
+
+/* Attention of the batch's rows over their sequences' cached tokens:
+ *   out[t, h] = sum_j p_j v_j / sum_j p_j,  p_j = exp(softmax_scale * q[t,h] . k_j)
+ * over the positions j < kv_len that the masks leave for the row's position p: causal != 0:
+ * j <= p; window > 0: j > p - window.  A row that sees nothing (a negative position, an empty
+ * cache) gives 0, and lse -infinity.  lse [T, q_heads] fp32 (natural log of the sum) or NULL.
+ * Slots past kv_len are never used, whatever they hold.  q rows are scaled by a power of two
+ * into fp16 and multiplied with the exact codes, sums and softmax statistics in fp32; p is
+ * rounded to fp16 (11 bits) for the product with the values; out is rounded once.
+ * softmax_scale > 0.  Deterministic.  A bad page id or a kv_len past the table is reported in
+ * the status word (those rows are then unspecified). */
+moe_status moe_attention(const moe_attn_config *cfg, const moe_kv_cache *cache, const moe_kv_batch *batch,
+                         const void *q, int64_t q_ld, float softmax_scale, int causal, int window, void *out,
+                         int64_t out_ld, float *lse, void *ws, size_t ws_bytes, void *stream);
+
 /* Reads and clears the device status word in `ws` (synchronises `stream`).  *device_status
  * receives MOE_OK or the first error recorded by a kernel (MOE_ERR_TIMEOUT for a wait that
  * ran out, MOE_ERR_INVALID_ARG for an out-of-range expert id).  Returns MOE_ERR_CUDA if the

@@ -27,7 +27,8 @@ EXPORTS = ["moe_status_string", "moe_workspace_size", "moe_route", "moe_route_fr
            "moe_timing_name", "moe_timing_classes", "moe_selftest_wait", "moe_decode_chain",
            "moe_decode_chain_q8", "moe_quantize_e4m3", "moe_graph_create", "moe_graph_launch",
            "moe_graph_kernel_count", "moe_graph_destroy", "moe_forward_q8", "moe_debug_build",
-           "moe_decode_chain_q4", "moe_quantize_q4"]
+           "moe_decode_chain_q4", "moe_quantize_q4", "moe_block_norm", "moe_attn_workspace_size",
+           "moe_kv_append", "moe_attention"]
 
 
 class MoeError(RuntimeError):
@@ -57,8 +58,35 @@ class WeightsQ4(ctypes.Structure):
     _fields_ = WeightsQ8._fields_
 
 
+class NormConfig(ctypes.Structure):
+    _fields_ = [("hidden", ctypes.c_int), ("dtype", ctypes.c_int), ("gate", ctypes.c_int),
+                ("gate_sigmoid", ctypes.c_int), ("unit_offset", ctypes.c_int), ("eps", ctypes.c_float),
+                ("residual_scale", ctypes.c_float)]
+
+
+class NormIO(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("x", "resid", "gate", "w_post", "w_pre", "resid_out", "y")] + \
+               [(n, ctypes.c_int64) for n in ("x_ld", "resid_ld", "gate_ld", "resid_out_ld", "y_ld")]
+
+
+class AttnConfig(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int) for n in
+                ("q_heads", "kv_heads", "head_dim", "page_size", "rotary_dim", "interleaved", "dtype")]
+
+
+class _KVCache(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("k_codes", "v_codes", "k_scale", "v_scale")] + \
+               [("n_pages", ctypes.c_int)]
+
+
+class _KVBatch(ctypes.Structure):
+    _fields_ = [("n_seqs", ctypes.c_int), ("n_tokens", ctypes.c_int), ("max_pages", ctypes.c_int),
+                ("q_start", ctypes.c_void_p), ("kv_len", ctypes.c_void_p), ("page_table", ctypes.c_void_p)]
+
+
 _P = ctypes.c_void_p
 _I = ctypes.c_int
+_I64 = ctypes.c_int64
 _SZ = ctypes.c_size_t
 _lib = None
 
@@ -90,6 +118,12 @@ def load(path: str = LIB_PATH):
     L.moe_quantize_e4m3.argtypes = [_P, _I, _I, _P, _P, _P]
     L.moe_decode_chain_q4.argtypes = [C, ctypes.POINTER(WeightsQ4), _I, _P, _P, _P, _P, _P, _SZ, _P]
     L.moe_quantize_q4.argtypes = [_P, _I, _I, _P, _P, _P]
+    A, KC, KB = ctypes.POINTER(AttnConfig), ctypes.POINTER(_KVCache), ctypes.POINTER(_KVBatch)
+    L.moe_block_norm.argtypes = [ctypes.POINTER(NormConfig), ctypes.POINTER(NormIO), _I, _P]
+    L.moe_attn_workspace_size.argtypes = [A, _I, _I]
+    L.moe_attn_workspace_size.restype = _SZ
+    L.moe_kv_append.argtypes = [A, KC, KB, _P, _I64, _P, _I64, _P, _I64, _P, _I, _P, _I64, _P, _SZ, _P]
+    L.moe_attention.argtypes = [A, KC, KB, _P, _I64, ctypes.c_float, _I, _I, _P, _I64, _P, _P, _SZ, _P]
     L.moe_check_status.argtypes = [_P, _SZ, ctypes.POINTER(_I), _P]
     L.moe_selftest_wait.argtypes = [_P, _SZ, ctypes.c_ulonglong, _I, _P]
     L.moe_graph_create.argtypes = [C, W, _I, _I, _P, _P, _P, _P, _P, _P, _SZ, _P, ctypes.POINTER(_P)]
@@ -112,7 +146,8 @@ def load(path: str = LIB_PATH):
                "moe_combine", "moe_forward", "moe_check_status", "moe_timing_enable",
                "moe_timing_read", "moe_timing_classes", "moe_selftest_wait", "moe_decode_chain",
                "moe_decode_chain_q8", "moe_quantize_e4m3", "moe_graph_create", "moe_graph_launch",
-               "moe_graph_destroy", "moe_forward_q8", "moe_decode_chain_q4", "moe_quantize_q4"):
+               "moe_graph_destroy", "moe_forward_q8", "moe_decode_chain_q4", "moe_quantize_q4", "moe_block_norm",
+               "moe_kv_append", "moe_attention"):
         getattr(L, fn).restype = _I
     _lib = L
     return L
@@ -355,6 +390,159 @@ def quantize_layer(layer: dict, stream=None) -> dict:
         out[sc] = torch.empty(w.shape[:-1], dtype=torch.float32, device=w.device)
         moe_quantize_e4m3(w, out[q], out[sc], stream)
     return out
+
+
+# ------------------------------------------- norms, paged cache, attention (include/moe.h) --
+
+_DTYPES = {torch.bfloat16: 0, torch.float16: 1}
+_GATES = {"none": 0, "channel": 1, "token": 2, "element": 3}
+
+
+def _rows(t, name, width, dtype, rows=None):
+    """Row stride of an activation tensor: [T, width], or [T, heads, dim] with heads * dim == width,
+    whose rows may lie apart but are themselves contiguous."""
+    if not t.is_cuda:
+        raise ValueError("%s must be on a CUDA device" % name)
+    if _DTYPES.get(t.dtype) != dtype:
+        raise ValueError("%s has dtype %s, not the config's" % (name, t.dtype))
+    shape, stride = t.shape, t.stride()
+    if len(shape) == 3:
+        ok = shape[1] * shape[2] == width and stride[2] == 1 and (stride[1] == shape[2] or shape[1] == 1)
+    else:
+        ok = len(shape) == 2 and shape[1] == width and (stride[1] == 1 or width == 1)
+    if not ok or (rows is not None and shape[0] != rows):
+        raise ValueError("%s has shape %s and strides %s, not %s rows of %d values" %
+                         (name, tuple(shape), tuple(stride), "T" if rows is None else rows, width))
+    return stride[0] if shape[0] > 1 else max(stride[0], width)
+
+
+def _device_array(t, name, dtype, shape=None):
+    if not t.is_cuda or not t.is_contiguous() or t.dtype != dtype:
+        raise ValueError("%s must be a contiguous CUDA tensor of %s" % (name, dtype))
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError("%s has shape %s, not %s" % (name, tuple(t.shape), tuple(shape)))
+    return t.data_ptr()
+
+
+def norm_config(hidden, dtype=torch.bfloat16, gate="none", sigmoid=False, unit_offset=False, eps=1e-6,
+                residual_scale=1.0) -> NormConfig:
+    return NormConfig(int(hidden), _DTYPES[dtype], _GATES[gate], int(sigmoid), int(unit_offset), eps, residual_scale)
+
+
+def moe_block_norm(cfg: NormConfig, x, resid, resid_out, y, gate=None, w_post=None, w_pre=None, stream=None):
+    """resid_out = resid + scale * g * norm(x); y = norm(resid_out).  x, resid, resid_out, y: [T, H] or
+    None; gate as the config says: [H] or [1, H], [T] or [T, 1], [T, H]; w_post, w_pre: [H] or None."""
+    H, dt = cfg.hidden, cfg.dtype
+    io = NormIO()
+    T = None
+    for name, t in (("x", x), ("resid", resid), ("resid_out", resid_out), ("y", y)):
+        if t is not None:
+            setattr(io, name + "_ld", _rows(t, name, H, dt, T))
+            setattr(io, name, t.data_ptr())
+            T = t.shape[0]
+    for name, t in (("w_post", w_post), ("w_pre", w_pre)):
+        if t is not None:
+            if t.numel() != H or not t.is_cuda or not t.is_contiguous() or _DTYPES.get(t.dtype) != dt:
+                raise ValueError("%s must be %d contiguous values of the config's dtype" % (name, H))
+            setattr(io, name, t.data_ptr())
+    if gate is not None:
+        if cfg.gate == 1:
+            if gate.numel() != H or not gate.is_cuda or not gate.is_contiguous() or _DTYPES.get(gate.dtype) != dt:
+                raise ValueError("a channel gate must be %d contiguous values of the config's dtype" % H)
+        elif cfg.gate == 2:
+            io.gate_ld = _rows(gate if gate.dim() == 2 else gate[:, None], "gate", 1, dt, T)
+        else:
+            io.gate_ld = _rows(gate, "gate", H, dt, T)
+        io.gate = gate.data_ptr()
+    st = lib().moe_block_norm(ctypes.byref(cfg), ctypes.byref(io), T or 0, _stream(stream))
+    _check("moe_block_norm", st)
+
+
+def attn_config(q_heads, kv_heads, head_dim, page_size, rotary_dim=None, interleaved=False,
+                dtype=torch.bfloat16) -> AttnConfig:
+    """rotary_dim None: the whole head."""
+    return AttnConfig(int(q_heads), int(kv_heads), int(head_dim), int(page_size),
+                      int(head_dim if rotary_dim is None else rotary_dim), int(interleaved), _DTYPES[dtype])
+
+
+class KVCache:
+    """The paged 8-bit cache (moe_kv_cache): codes uint8 [n_pages, kv_heads, page_size, head_dim], scales
+    fp32 [n_pages, kv_heads].  Keeps the tensors alive."""
+
+    def __init__(self, cfg: AttnConfig, k_codes, v_codes, k_scale, v_scale):
+        n = k_codes.shape[0]
+        shape = (n, cfg.kv_heads, cfg.page_size, cfg.head_dim)
+        self.c = _KVCache(_device_array(k_codes, "k_codes", torch.uint8, shape),
+                          _device_array(v_codes, "v_codes", torch.uint8, shape),
+                          _device_array(k_scale, "k_scale", torch.float32, shape[:2]),
+                          _device_array(v_scale, "v_scale", torch.float32, shape[:2]), n)
+        self.k_codes, self.v_codes, self.k_scale, self.v_scale = k_codes, v_codes, k_scale, v_scale
+
+    @classmethod
+    def alloc(cls, cfg: AttnConfig, n_pages, device="cuda"):
+        shape = (int(n_pages), cfg.kv_heads, cfg.page_size, cfg.head_dim)
+        codes = [torch.zeros(shape, dtype=torch.uint8, device=device) for _ in range(2)]
+        scales = [torch.ones(shape[:2], dtype=torch.float32, device=device) for _ in range(2)]
+        return cls(cfg, *codes, *scales)
+
+
+class KVBatch:
+    """A batch of sequences (moe_kv_batch): q_start int32 [B + 1], kv_len int32 [B], page_table int32
+    [B, max_pages], all on the device; their contents may change between calls, n_tokens may not."""
+
+    def __init__(self, q_start, kv_len, page_table, n_tokens):
+        B = kv_len.shape[0]
+        _device_array(page_table, "page_table", torch.int32)
+        if page_table.dim() != 2 or page_table.shape[0] != B:
+            raise ValueError("page_table must be [%d, max_pages]" % B)
+        self.c = _KVBatch(B, int(n_tokens), page_table.shape[1],
+                          _device_array(q_start, "q_start", torch.int32, (B + 1,)),
+                          _device_array(kv_len, "kv_len", torch.int32, (B,)), page_table.data_ptr())
+        self.q_start, self.kv_len, self.page_table = q_start, kv_len, page_table
+        self.n_tokens = int(n_tokens)
+
+
+def attn_workspace_size(cfg: AttnConfig, max_seqs, max_tokens) -> int:
+    return int(lib().moe_attn_workspace_size(ctypes.byref(cfg), int(max_seqs), int(max_tokens)))
+
+
+def alloc_attn_workspace(cfg: AttnConfig, max_seqs, max_tokens, device="cuda") -> torch.Tensor:
+    n = attn_workspace_size(cfg, max_seqs, max_tokens)
+    if n == 0:
+        raise MoeError("moe_attn_workspace_size", 3)
+    # zeroed once: the status word and the tickets
+    return torch.zeros(n, dtype=torch.uint8, device=device)
+
+
+def moe_kv_append(cfg: AttnConfig, cache: KVCache, batch: KVBatch, q, k, v, rope, q_out, ws, stream=None):
+    """Rotates q [T, q_heads, D] into q_out and writes k, v [T, kv_heads, D] into the cache at the batch's
+    positions.  rope: fp32 [positions, rotary_dim], cosines then sines (None with rotary_dim 0)."""
+    T, D, dt = batch.n_tokens, cfg.head_dim, cfg.dtype
+    qw, kw = cfg.q_heads * D, cfg.kv_heads * D
+    rope_ptr, rope_rows = None, 0
+    if rope is not None:
+        rope_rows = rope.shape[0]
+        rope_ptr = _device_array(rope, "rope", torch.float32, (rope_rows, cfg.rotary_dim))
+    st = lib().moe_kv_append(
+        ctypes.byref(cfg), ctypes.byref(cache.c), ctypes.byref(batch.c),
+        None if q is None else q.data_ptr(), 0 if q is None else _rows(q, "q", qw, dt, T),
+        k.data_ptr(), _rows(k, "k", kw, dt, T), v.data_ptr(), _rows(v, "v", kw, dt, T), rope_ptr, rope_rows,
+        None if q_out is None else q_out.data_ptr(), 0 if q_out is None else _rows(q_out, "q_out", qw, dt, T),
+        _ptr(ws), ws.numel(), _stream(stream))
+    _check("moe_kv_append", st)
+
+
+def moe_attention(cfg: AttnConfig, cache: KVCache, batch: KVBatch, q, out, ws, lse=None, softmax_scale=None,
+                  causal=True, window=0, stream=None):
+    """Attention of q [T, q_heads, D] over the batch's cached tokens into out (and lse fp32
+    [T, q_heads]).  softmax_scale None: 1 / sqrt(D)."""
+    T, qw = batch.n_tokens, cfg.q_heads * cfg.head_dim
+    lse_ptr = None if lse is None else _device_array(lse, "lse", torch.float32, (T, cfg.q_heads))
+    st = lib().moe_attention(
+        ctypes.byref(cfg), ctypes.byref(cache.c), ctypes.byref(batch.c), q.data_ptr(), _rows(q, "q", qw, cfg.dtype, T),
+        cfg.head_dim ** -0.5 if softmax_scale is None else softmax_scale, int(bool(causal)), int(window),
+        out.data_ptr(), _rows(out, "out", qw, cfg.dtype, T), lse_ptr, _ptr(ws), ws.numel(), _stream(stream))
+    _check("moe_attention", st)
 
 
 def moe_forward_status(cfg, w: Weights, x, T, out, x_next, ws, stream=None, resid=None) -> int:

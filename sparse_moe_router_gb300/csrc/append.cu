@@ -1,0 +1,292 @@
+// append.cu -- moe_kv_append: position rotation of q and k, and k and v written into the paged
+// cache as E4M3 codes with one power-of-two scale a (page, kv head).
+//
+// One launch.  Its first blocks own one (page, kv head, k or v) each: such a block holds all of the
+// page's new values of that head in registers, reduces their largest magnitude, settles the
+// page's scale, re-rounds the codes that the page held before if the scale grew, and writes the
+// new codes -- no other block touches that page and head, so no scale is ever contended.  The
+// blocks after them rotate q.
+//
+// Exact codes.  The rotation a cos - b sin of 16-bit a, b with an fp32 table is carried as an
+// unevaluated fp32 pair (products and the sum with their rounding errors, error-free
+// transformations after Dekker and Knuth) and rounded to odd: the low bit of the fp32 result is
+// set when anything was lost.  Rounding that once more to 4 or 8 bits (or comparing it with a scale's
+// border) then gives what the exact value would give, so codes and scales do not depend on how
+// the rotation was summed.
+#include "layer.h"
+
+namespace moe {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kSeqCache = 1024;  // sequences whose q_start a block stages in shared memory
+
+// a*c - b*s rounded to odd (see above).  Explicit _rn operations: none may be contracted.
+__device__ __forceinline__ float rotate_odd(float a, float c, float b, float s) {
+    const float p = __fmul_rn(a, c), q = -__fmul_rn(b, s);
+    const float ep = __fmaf_rn(a, c, -p), eq = __fmaf_rn(-b, s, -q);
+    const float r = __fadd_rn(p, q);
+    const float z = __fsub_rn(r, p);
+    const float er = __fadd_rn(__fsub_rn(p, __fsub_rn(r, z)), __fsub_rn(q, z));
+    const float err = __fadd_rn(er, __fadd_rn(ep, eq));
+    const float r2 = __fadd_rn(r, err);
+    const float lost = __fsub_rn(err, __fsub_rn(r2, r));
+    int bits = __float_as_int(r2);
+    if (lost != 0.f && !(bits & 1)) bits += ((lost > 0.f) == (r2 > 0.f)) ? 1 : -1;
+    return __int_as_float(bits);
+}
+
+// The exponent e of the smallest 2^e with amax <= 448 * 2^e (448 = 1.75 * 2^8), not below the floor.
+__device__ __forceinline__ int scale_exp(float amax) {
+    const uint32_t u = __float_as_uint(fminf(amax, 3.402823466e38f));
+    const int e = (int)(u >> 23) - 127 - 8 + ((u & 0x7fffffu) > 0x600000u ? 1 : 0);
+    return max(e, kScaleMinExp);
+}
+__device__ __forceinline__ float pow2f(int e) { return __int_as_float((e + 127) << 23); }
+
+__device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d) {
+    const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
+    const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(c, d), __NV_SATFINITE, __NV_E4M3);
+    return lo | (hi << 16);
+}
+__device__ __forceinline__ uint32_t rescale4(uint32_t w, float ratio) {
+    const __half2 lo = __half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w & 0xffffu), __NV_E4M3));
+    const __half2 hi = __half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w >> 16), __NV_E4M3));
+    const float2 a = __half22float2(lo), b = __half22float2(hi);
+    return codes4(a.x * ratio, a.y * ratio, b.x * ratio, b.y * ratio);
+}
+
+// A unit is 16 values of a row in two 8-value chunks that the rotation needs together: chunks
+// (8u, 8u + rot/2) of half-split pairs, (16u, 16u + 8) of interleaved ones and of the dims past rot.
+__device__ __forceinline__ void unit_dims(int u, int rot, bool interleaved, int &d0, int &d1) {
+    const bool half_split = !interleaved && u < (rot >> 4);
+    d0 = half_split ? 8 * u : 16 * u;
+    d1 = half_split ? 8 * u + (rot >> 1) : 16 * u + 8;
+}
+
+// The unit's values after the rotation (to odd), or as they are past rot.
+template <bool F16>
+__device__ __forceinline__ void unit_values(const uint4 &lo, const uint4 &hi, const float *__restrict__ rope_row, int u,
+                                            int rot, bool interleaved, float (&a)[8], float (&b)[8]) {
+    unpack8<F16>(lo, a);
+    unpack8<F16>(hi, b);
+    if (!rope_row || u >= (rot >> 4)) return;
+    float c[8], s[8];
+    // rows of the table are rot floats, a multiple of 16: every 8 of them start on 16 bytes
+    const float4 *cp = reinterpret_cast<const float4 *>(rope_row + 8 * u);
+    const float4 *sp = reinterpret_cast<const float4 *>(rope_row + (rot >> 1) + 8 * u);
+    const float4 c0 = __ldg(cp), c1 = __ldg(cp + 1), s0 = __ldg(sp), s1 = __ldg(sp + 1);
+    c[0] = c0.x, c[1] = c0.y, c[2] = c0.z, c[3] = c0.w, c[4] = c1.x, c[5] = c1.y, c[6] = c1.z, c[7] = c1.w;
+    s[0] = s0.x, s[1] = s0.y, s[2] = s0.z, s[3] = s0.w, s[4] = s1.x, s[5] = s1.y, s[6] = s1.z, s[7] = s1.w;
+    if (!interleaved) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const float x = a[j], y = b[j];
+            a[j] = rotate_odd(x, c[j], y, s[j]);
+            b[j] = rotate_odd(y, c[j], x, -s[j]);
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            float x = a[2 * j], y = a[2 * j + 1];
+            a[2 * j] = rotate_odd(x, c[j], y, s[j]);
+            a[2 * j + 1] = rotate_odd(y, c[j], x, -s[j]);
+            x = b[2 * j], y = b[2 * j + 1];
+            b[2 * j] = rotate_odd(x, c[4 + j], y, s[4 + j]);
+            b[2 * j + 1] = rotate_odd(y, c[4 + j], x, -s[4 + j]);
+        }
+    }
+}
+
+// The last sequence b with f(b) <= i, f not descending, f(0) <= i.
+template <typename F>
+__device__ __forceinline__ int last_at_most(int n, int i, F f) {
+    int lo = 0, hi = n - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (f(mid) <= i) lo = mid; else hi = mid - 1;
+    }
+    return lo;
+}
+
+// U: units a thread of a page block holds (P * D / 16 / blockDim)
+template <int D, int U, bool F16>
+__global__ void __launch_bounds__(kThreads) kv_append_kernel(const __grid_constant__ AppendArgs p) {
+    constexpr int kUnits = D / 16;  // of a row
+    const KvView &v = p.kv;
+    __shared__ int starts[kSeqCache];
+    __shared__ float red[kThreads / 32];
+    const int tid = (int)threadIdx.x, nt = (int)blockDim.x;
+    const int P = 1 << v.log_p;
+    const bool staged = v.n_seqs <= kSeqCache;
+    if (staged) {
+        for (int i = tid; i < v.n_seqs; i += nt) starts[i] = v.q_start[i];
+        __syncthreads();
+    }
+    auto start_of = [&](int b) { return staged ? starts[b] : v.q_start[b]; };
+
+    if ((int)blockIdx.x >= p.page_items) {
+        // ---------------------------------------------------------------- rotation of q --
+        const int t0 = ((int)blockIdx.x - p.page_items) * p.q_tokens;
+        const int t1 = min(t0 + p.q_tokens, v.n_tokens);
+        const int row_units = v.QH * kUnits;
+        constexpr int kBatch = 4;  // units with their loads in flight together
+        for (int base = 0; base < (t1 - t0) * row_units; base += kBatch * nt) {
+            uint4 lo[kBatch], hi[kBatch];
+            int tok[kBatch], rem[kBatch];
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) {
+                const int k = base + i * nt + tid;
+                tok[i] = -1;
+                if (k >= (t1 - t0) * row_units) continue;
+                tok[i] = t0 + k / row_units;
+                rem[i] = k % row_units;
+                int d0, d1;
+                unit_dims(rem[i] % kUnits, p.rot, p.interleaved, d0, d1);
+                const uint16_t *src = p.q + tok[i] * p.q_ld + rem[i] / kUnits * D;
+                lo[i] = *reinterpret_cast<const uint4 *>(src + d0);
+                hi[i] = *reinterpret_cast<const uint4 *>(src + d1);
+            }
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) {
+                if (tok[i] < 0) continue;
+                const int b = last_at_most(v.n_seqs, tok[i], start_of);
+                const Seq q = load_seq(v, b);
+                const int pos = q.kv - q.n + tok[i] - q.q0;
+                const int u = rem[i] % kUnits;
+                float x[8], y[8];
+                const bool ok = pos >= 0 && (pos < p.rope_rows || p.rot == 0) && tok[i] - q.q0 < q.n;
+                if (ok) {
+                    unit_values<F16>(lo[i], hi[i], p.rot ? p.rope + (int64_t)pos * p.rot : nullptr, u, p.rot, p.interleaved, x, y);
+                } else {
+                    if (pos >= 0) layer_error(v.status);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) x[j] = y[j] = 0.f;
+                }
+                int d0, d1;
+                unit_dims(u, p.rot, p.interleaved, d0, d1);
+                uint16_t *dst = p.q_out + tok[i] * p.q_out_ld + rem[i] / kUnits * D;
+                *reinterpret_cast<uint4 *>(dst + d0) = pack8<F16>(x);
+                *reinterpret_cast<uint4 *>(dst + d1) = pack8<F16>(y);
+            }
+        }
+        return;
+    }
+
+    // ------------------------------------------------------------- one page of one head --
+    // Sequence b has the page slots base(b) .. base(b+1)-1: its n new tokens touch at most n/P + 2 pages.
+    const int slot = (int)blockIdx.x / (2 * v.KH), which = (int)blockIdx.x / v.KH & 1, head = (int)blockIdx.x % v.KH;
+    const int b = last_at_most(v.n_seqs, slot, [&](int i) { return (start_of(i) >> v.log_p) + 2 * i; });
+    const Seq q = load_seq(v, b);
+    const int first = q.kv - q.n;  // position of the first new token
+    const int col = (max(first, 0) >> v.log_p) + slot - ((q.q0 >> v.log_p) + 2 * b);
+    const int pos0 = col << v.log_p;
+    if (col < 0 || q.n == 0 || pos0 >= q.kv) return;  // no such page (col < 0: descending q_start)
+    const int page = v.table[(int64_t)b * v.max_pages + col];
+    if (page < 0 || page >= v.n_pages) {
+        if (tid == 0) layer_error(v.status);
+        return;
+    }
+    const int64_t ph = (int64_t)page * v.KH + head;
+    uint8_t *codes = (which ? v.v_codes : v.k_codes) + ph * P * D;
+    float *scale = (which ? v.v_scale : v.k_scale) + ph;
+    const bool begun = pos0 < first;  // the page holds earlier tokens
+    const float old = begun ? *scale : 0.f;
+    const uint16_t *src = which ? p.v : p.k;
+    const int64_t ld = which ? p.v_ld : p.k_ld;
+    const int rot = which ? 0 : p.rot;  // values are not rotated
+
+    float x[U][8], y[U][8];
+    float amax = 0.f;
+    bool odd = false;
+    uint4 lo[U], hi[U];
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+        const int k = i * nt + tid, pos = pos0 + k / kUnits;
+        lo[i] = hi[i] = make_uint4(0, 0, 0, 0);
+        if (pos < max(first, 0) || pos >= q.kv || k >= P * kUnits) continue;
+        int d0, d1;
+        unit_dims(k % kUnits, rot, p.interleaved, d0, d1);
+        const uint16_t *row = src + (int64_t)(q.q0 + pos - first) * ld + head * D;
+        lo[i] = *reinterpret_cast<const uint4 *>(row + d0);
+        hi[i] = *reinterpret_cast<const uint4 *>(row + d1);
+    }
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+        const int k = i * nt + tid, pos = pos0 + k / kUnits;
+        const bool live = pos >= max(first, 0) && pos < q.kv && k < P * kUnits;
+        if (live && rot && pos >= p.rope_rows) {  // no angle: stored as zeros, reported
+            odd = true;
+            lo[i] = hi[i] = make_uint4(0, 0, 0, 0);
+        }
+        const float *angle = (live && rot && pos < p.rope_rows) ? p.rope + (int64_t)pos * rot : nullptr;
+        unit_values<F16>(lo[i], hi[i], angle, k % kUnits, rot, p.interleaved, x[i], y[i]);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            odd |= !(fabsf(x[i][j]) <= 3.402823466e38f) || !(fabsf(y[i][j]) <= 3.402823466e38f);
+            if (x[i][j] != x[i][j]) x[i][j] = 0.f;
+            if (y[i][j] != y[i][j]) y[i][j] = 0.f;
+            amax = fmaxf(amax, fmaxf(fabsf(x[i][j]), fabsf(y[i][j])));
+        }
+    }
+    if (odd) layer_error(v.status);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+    if ((tid & 31) == 0) red[tid >> 5] = amax;
+    __syncthreads();
+    for (int w = 0; w < nt >> 5; ++w) amax = fmaxf(amax, red[w]);
+    float s = pow2f(scale_exp(amax));
+    if (begun) s = fmaxf(s, old);
+    const float inv = 1.0f / s;  // exact: s is a power of two
+    const bool grow = begun && s > old;
+    const float ratio = old * inv;
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+        const int k = i * nt + tid, pos = pos0 + k / kUnits;
+        if (k >= P * kUnits) continue;
+        int d0, d1;
+        unit_dims(k % kUnits, rot, p.interleaved, d0, d1);
+        uint8_t *row = codes + k / kUnits * D;
+        if (pos >= max(first, 0) && pos < q.kv) {
+            uint2 a, c;
+            a.x = codes4(x[i][0] * inv, x[i][1] * inv, x[i][2] * inv, x[i][3] * inv);
+            a.y = codes4(x[i][4] * inv, x[i][5] * inv, x[i][6] * inv, x[i][7] * inv);
+            c.x = codes4(y[i][0] * inv, y[i][1] * inv, y[i][2] * inv, y[i][3] * inv);
+            c.y = codes4(y[i][4] * inv, y[i][5] * inv, y[i][6] * inv, y[i][7] * inv);
+            *reinterpret_cast<uint2 *>(row + d0) = a;
+            *reinterpret_cast<uint2 *>(row + d1) = c;
+        } else if (grow) {
+            uint2 a = *reinterpret_cast<const uint2 *>(row + d0), c = *reinterpret_cast<const uint2 *>(row + d1);
+            a.x = rescale4(a.x, ratio), a.y = rescale4(a.y, ratio);
+            c.x = rescale4(c.x, ratio), c.y = rescale4(c.y, ratio);
+            *reinterpret_cast<uint2 *>(row + d0) = a;
+            *reinterpret_cast<uint2 *>(row + d1) = c;
+        }
+    }
+    if (tid == 0 && s != old) *scale = s;
+}
+
+template <int D, bool F16>
+cudaError_t launch(const AppendArgs &a, cudaStream_t s) {
+    LaunchScope scope(KC_KV_APPEND, s);
+    const int q_blocks = a.q ? (a.kv.n_tokens + a.q_tokens - 1) / a.q_tokens : 0;
+    const int grid = a.page_items + q_blocks;
+    const int units = a.kv.P * D / 16;
+    const int u = units / kThreads;
+    if (u <= 1) kv_append_kernel<D, 1, F16><<<grid, kThreads, 0, s>>>(a);
+    else if (u == 2) kv_append_kernel<D, 2, F16><<<grid, kThreads, 0, s>>>(a);
+    else if (u == 4) kv_append_kernel<D, 4, F16><<<grid, kThreads, 0, s>>>(a);
+    else kv_append_kernel<D, 8, F16><<<grid, kThreads, 0, s>>>(a);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_kv_append(const AppendArgs &a, int D, int dtype, cudaStream_t s) {
+    const bool f16 = dtype == MOE_DTYPE_F16;
+    if (D == 64) return f16 ? launch<64, true>(a, s) : launch<64, false>(a, s);
+    if (D == 128) return f16 ? launch<128, true>(a, s) : launch<128, false>(a, s);
+    return f16 ? launch<256, true>(a, s) : launch<256, false>(a, s);
+}
+
+}  // namespace moe

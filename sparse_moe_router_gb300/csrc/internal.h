@@ -27,6 +27,10 @@ enum KernelClass {
     KC_GATHER_X,          // token rows copied into expert-sorted order
     KC_DECODE_CHAIN,      // decode: a chain of layers in one cooperative launch
     KC_QUANTIZE,          // row-wise E4M3 quantisation of weights
+    KC_BLOCK_NORM,        // norms before and after a block, gate and residual scale
+    KC_KV_APPEND,         // rotation and append into the paged cache
+    KC_ATTN_SPLIT,        // attention over the cache, split along the keys (decode)
+    KC_ATTN_PROMPT,       // attention over the cache on the 5th-generation tensor cores (prompts)
     KC_COUNT
 };
 

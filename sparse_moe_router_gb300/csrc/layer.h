@@ -1,0 +1,128 @@
+// layer.h -- declarations shared by the kernels of the decoder layer's other half: block norms,
+// append into the paged 8-bit cache, attention over it.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
+
+#include "internal.h"
+
+namespace moe {
+
+// The cache and the batch as the kernels see them (include/moe.h: moe_kv_cache, moe_kv_batch).
+struct KvView {
+    const int32_t *q_start, *kv_len, *table;
+    uint8_t *k_codes, *v_codes;
+    float *k_scale, *v_scale;
+    int n_seqs, n_tokens, max_pages, n_pages;
+    int QH, KH, G, P, log_p;
+    int *status;
+};
+
+// Exponents of a cache scale (a power of two): amax <= 448 * 2^e, and 448 = 1.75 * 2^8.
+constexpr int kScaleMinExp = -60;
+
+struct AppendArgs {
+    KvView kv;
+    const uint16_t *q, *k, *v;
+    int64_t q_ld, k_ld, v_ld, q_out_ld;
+    const float *rope;
+    int rope_rows, rot, interleaved;
+    uint16_t *q_out;
+    int q_tokens;    // tokens a block of the q part handles
+    int page_items;  // blocks of the cache part: (page slots) x 2 x kv heads
+};
+cudaError_t launch_kv_append(const AppendArgs &a, int D, int dtype, cudaStream_t s);
+
+struct AttnArgs {
+    KvView kv;
+    const uint16_t *q;
+    uint16_t *out;
+    float *lse;
+    int64_t q_ld, out_ld;
+    float scale_log2;  // softmax_scale * log2(e)
+    int causal, window;
+    // split kernel: partial results and tickets, one pair of slots and one ticket a block
+    float *part;
+    unsigned *ticket;
+};
+// Blocks the split kernel may have (its workspace is sized for them).
+constexpr int kSplitMaxBlocks = 1024;
+// Floats of workspace the split kernel needs for partial results.
+size_t split_part_floats(int D);
+cudaError_t launch_attn_split(const AttnArgs &a, int D, int dtype, cudaStream_t s);
+
+struct NormArgs {
+    const uint16_t *x, *resid, *gate, *w_post, *w_pre;
+    uint16_t *resid_out, *y;
+    int64_t x_ld, resid_ld, gate_ld, resid_out_ld, y_ld;
+    int T, H, gate_kind, sigmoid, unit_offset;
+    float eps, alpha;
+};
+cudaError_t launch_block_norm(const NormArgs &a, int dtype, cudaStream_t s);
+
+#ifdef __CUDACC__
+__device__ __forceinline__ void layer_error(int *status) { atomicCAS(status, 0, (int)MOE_ERR_INVALID_ARG); }
+
+// 16-bit activations <-> fp32, by the call's dtype.
+template <bool F16>
+__device__ __forceinline__ float2 unpack2(uint32_t w) {
+    if (F16) return __half22float2(*reinterpret_cast<const __half2 *>(&w));
+    return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+}
+template <bool F16>
+__device__ __forceinline__ uint32_t pack2(float a, float b) {
+    if (F16) {
+        const __half2 v = __floats2half2_rn(a, b);
+        return *reinterpret_cast<const uint32_t *>(&v);
+    }
+    const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t *>(&v);
+}
+template <bool F16>
+__device__ __forceinline__ float load1(const uint16_t *p) {
+    const uint32_t v = *p;
+    return F16 ? __half2float(__ushort_as_half((unsigned short)v)) : __uint_as_float(v << 16);
+}
+template <bool F16>
+__device__ __forceinline__ void unpack8(const uint4 &v, float (&f)[8]) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 t = unpack2<F16>(w[i]);
+        f[2 * i] = t.x;
+        f[2 * i + 1] = t.y;
+    }
+}
+template <bool F16>
+__device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
+    return make_uint4(pack2<F16>(f[0], f[1]), pack2<F16>(f[2], f[3]), pack2<F16>(f[4], f[5]), pack2<F16>(f[6], f[7]));
+}
+
+// One sequence of the batch.  What the device arrays say is checked before it is used: a range
+// outside the batch's tokens counts as no tokens, a length outside the table as the nearest end.
+struct Seq {
+    int q0, n, kv;
+};
+__device__ __forceinline__ Seq load_seq(const KvView &v, int b) {
+    Seq s;
+    s.q0 = v.q_start[b];
+    s.n = v.q_start[b + 1] - s.q0;
+    s.kv = v.kv_len[b];
+    const long long most = (long long)v.max_pages << v.log_p;
+    bool bad = false;
+    if (s.q0 < 0 || s.n < 0 || s.q0 > v.n_tokens - s.n) {
+        s.q0 = s.n = 0;
+        bad = true;
+    }
+    if (s.kv < 0 || s.kv > most) {
+        s.kv = s.kv < 0 ? 0 : (int)most;
+        bad = true;
+    }
+    if (bad) layer_error(v.status);
+    return s;
+}
+#endif
+
+}  // namespace moe
