@@ -84,6 +84,7 @@ struct SeqWork {
 __device__ __forceinline__ SeqWork seq_work(const AttnArgs &p, int b) {
     SeqWork w;
     w.q = load_seq(p.kv, b);
+    if ((int64_t)w.q.n * p.kv.G >= p.prompt_rows) w.q.n = 0;  // the prompt kernel's
     w.tiles = (int)(((int64_t)w.q.n * p.kv.G + kRows - 1) / kRows);
     int lo, hi;
     key_range(p, w.q, 0, max(w.q.n, 1), lo, hi);

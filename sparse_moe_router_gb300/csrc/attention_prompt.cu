@@ -1,0 +1,439 @@
+// attention_prompt.cu -- attention over the paged 8-bit cache for runs of many new tokens, on the
+// 5th-generation tensor cores (tcgen05, TMEM).
+//
+// A block takes 256 query rows (token, q head) of one kv head as two 128-row tiles and walks the
+// keys they see in tiles of 128: S = Q K^T into TMEM, softmax weights back into TMEM as fp16 over S,
+// O += P V from there.  All rows of a group of q heads share each key and value tile, so a tile
+// of K and V is widened once for 256 rows.
+//
+// Bound: 4 D flops a (row, key) on the tensor cores; one tile pair is 4 x 512 tensor cycles at
+// D = 128, and the weights of its 2 x 16,384 logits take about as long on two warpgroups, so the two
+// row tiles alternate: while the tensor cores work on one, the other's softmax runs.  The 8-bit
+// codes cannot be an operand beside fp16 weights (both operands of an MMA have one type, and queries in 8
+// bits would lose what the 16-bit ones hold), so four warps read codes from global memory (L2,
+// mostly: all tiles of a head read the same pages), widen them exactly to fp16 and store them in the
+// swizzled layout that the MMA reads: 96 KB of shared-memory traffic a tile against the MMA's own
+// 192 KB.  The exponents of the pages are drawn into the codes relative to the largest one the block
+// will meet (exact in fp16 unless a page is 2^-15 below it, and then off by at most 2^-25 of the
+// largest), so one factor a row holds for all keys.
+//
+// Roles: warps 0-3 and 4-7 softmax of row tiles 0 and 1 (one row a thread), warps 8-11 widen K and V,
+// one thread of warp 12 issues the MMAs.  Row maxima move lazily: a row's reference changes only when a
+// logit passes it by 2^8 (weights stay below 256), so O is rarely rescaled, by the thread that
+// owns the row.
+#include "layer.h"
+#include "ptx.cuh"
+
+namespace moe {
+namespace {
+
+constexpr int kRowTile = 128, kRowsBlock = 2 * kRowTile;
+constexpr int kKeys = 128;  // keys a tile
+constexpr int kStages = 4;  // K and V tiles in flight, in the order K0 V0 K1 V1 ...
+constexpr int kSoftWarps = 8, kConvWarp0 = 8, kConvWarps = 4, kMmaWarp = 12;
+constexpr int kThreads = 13 * 32;
+constexpr uint64_t kWaitNs = 2000000000ull;  // 2 s: far above any legitimate wait
+constexpr float kLazy = 8.f;
+
+template <int D>
+struct Prompt {
+    static constexpr int kBlocks = D / 64;                    // 128-byte column blocks of a row
+    static constexpr int kBlockBytes = kKeys * 128;           // one column block of a 128-row tile
+    static constexpr int kTileBytes = kBlocks * kBlockBytes;  // a tile of Q, K or V
+    static constexpr int kSmem = 1024 + (2 + kStages) * kTileBytes + 256;
+    static constexpr uint32_t kColO = 2 * kKeys;              // TMEM: S0 S1 O0 O1
+    static constexpr uint32_t kCols = 512;
+};
+
+__device__ __forceinline__ float exp2_fast(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+__device__ __forceinline__ int exponent_of(float s) { return (int)((__float_as_uint(s) >> 23) & 0xffu) - 127; }
+__device__ __forceinline__ float pow2f(int e) { return __int_as_float((min(max(e, -126), 127) + 127) << 23); }
+__device__ __forceinline__ uint32_t widen2(uint32_t codes) {
+    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)codes, __NV_E4M3);
+    return (uint32_t)h.x | ((uint32_t)h.y << 16);
+}
+__device__ __forceinline__ uint32_t mul2(uint32_t a, __half2 f) {
+    const __half2 r = __hmul2(*reinterpret_cast<const __half2 *>(&a), f);
+    return *reinterpret_cast<const uint32_t *>(&r);
+}
+
+// Block (slot, head): sequence b owns the 256-row slots base(b) .. base(b+1)-1 of every head, with
+// base(b) = q_start[b] G / 256 + b (its n G rows need at most n G / 256 + 1 of them).
+__device__ __forceinline__ int slot_base(const KvView &v, int b) {
+    return (int)((int64_t)v.q_start[b] * v.G / kRowsBlock) + b;
+}
+
+template <int D, bool F16>
+__global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_constant__ AttnArgs p, int slots) {
+    using C = Prompt<D>;
+    const KvView &v = p.kv;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = smem_raw + ((1024u - (ptx::smem_u32(smem_raw) & 1023u)) & 1023u);
+    uint8_t *q_smem = smem, *kv_smem = smem + 2 * C::kTileBytes;
+    uint64_t *bars = reinterpret_cast<uint64_t *>(kv_smem + kStages * C::kTileBytes);
+    uint64_t *full = bars, *empty = bars + kStages;  // of a stage
+    uint64_t *s_full = empty + kStages;              // [2] logits of a row tile are in TMEM
+    uint64_t *p_full = s_full + 2;                   // [2] its weights are
+    uint64_t *o_full = p_full + 2;                   // [2] its output is complete
+    uint64_t *q_full = o_full + 2;
+    uint64_t *drain = q_full + 1;
+    uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(drain + 1);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_holder + 1);
+    int *max_exp = reinterpret_cast<int *>(tmem_holder + 2);  // [2] of K and V
+
+    const int tid = (int)threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+    // ------------------------------------------------------------------- the block's rows --
+    const int head = (int)blockIdx.x % v.KH;
+    const int slot = slots - 1 - (int)blockIdx.x / v.KH;  // a sequence's last rows see most keys: first
+    int lo_b = 0, hi_b = v.n_seqs - 1;
+    while (lo_b < hi_b) {
+        const int mid = (lo_b + hi_b + 1) >> 1;
+        if (slot_base(v, mid) <= slot) lo_b = mid; else hi_b = mid - 1;
+    }
+    const int b = lo_b;
+    const Seq q = load_seq(v, b);
+    const int row0 = (slot - slot_base(v, b)) * kRowsBlock;
+    const int rows = min(kRowsBlock, q.n * v.G - row0);
+    if (row0 < 0 || rows <= 0 || q.n * v.G < p.prompt_rows) return;  // (short runs are the split kernel's)
+    const int first_pos = q.kv - q.n;
+    // keys that any of the rows sees
+    const int pos_lo = first_pos + row0 / v.G, pos_hi = first_pos + (row0 + rows - 1) / v.G;
+    const int key_hi = p.causal ? min(q.kv, pos_hi + 1) : q.kv;
+    const int key_lo = p.window > 0 ? max(0, pos_lo + 1 - p.window) : 0;
+    const int tile0 = key_lo / kKeys;
+    const int tiles = key_hi > key_lo ? (key_hi + kKeys - 1) / kKeys - tile0 : 0;
+    const int32_t *table = v.table + (int64_t)b * v.max_pages;
+
+    if (tid == 0) {
+        for (int s = 0; s < kStages; ++s) {
+            ptx::mbar_init(&full[s], kConvWarps);
+            ptx::mbar_init(&empty[s], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            ptx::mbar_init(&s_full[i], 1);
+            ptx::mbar_init(&p_full[i], 4);
+            ptx::mbar_init(&o_full[i], 1);
+        }
+        ptx::mbar_init(q_full, kSoftWarps);
+        ptx::mbar_init(drain, 1);
+        *abort_flag = 0;
+        max_exp[0] = max_exp[1] = -127;
+        ptx::fence_mbar_init();
+    }
+    if (warp == kMmaWarp) ptx::tmem_alloc(tmem_holder, C::kCols);
+    ptx::tc_fence_before();
+    __syncthreads();
+    ptx::tc_fence_after();
+    const uint32_t tmem = *tmem_holder;
+    // the largest exponents among the pages the block reads
+    {
+        int ek = -127, ev = -127;
+        const int pages0 = (tile0 * kKeys) >> v.log_p, pages1 = (key_hi + v.P - 1) >> v.log_p;
+        for (int i = pages0 + tid; tiles > 0 && i < pages1; i += kThreads) {
+            int page = __ldg(table + i);
+            if (page < 0 || page >= v.n_pages) {
+                layer_error(v.status);
+                page = 0;
+            }
+            ek = max(ek, exponent_of(__ldg(v.k_scale + (int64_t)page * v.KH + head)));
+            ev = max(ev, exponent_of(__ldg(v.v_scale + (int64_t)page * v.KH + head)));
+        }
+        ek = __reduce_max_sync(0xffffffffu, ek);
+        ev = __reduce_max_sync(0xffffffffu, ev);
+        if (lane == 0) {
+            atomicMax(&max_exp[0], ek);
+            atomicMax(&max_exp[1], ev);
+        }
+    }
+    __syncthreads();
+    const int k_exp = max_exp[0], v_exp = max_exp[1];
+    bool ok = true;
+
+    if (warp < kSoftWarps) {
+        // ----------------------------------------------------------------- softmax, rows --
+        const int i = warp >> 2;                        // row tile
+        const int r = i * kRowTile + (warp & 3) * 32 + lane;  // row of the block = TMEM lane of tile i
+        const bool live = r < rows;
+        const int tok = (row0 + r) / v.G, qh = head * v.G + (row0 + r) % v.G;
+        const int pos = first_pos + tok;
+        const int hi = p.causal ? min(q.kv, pos + 1) : q.kv;
+        const int lo = p.window > 0 ? max(0, pos + 1 - p.window) : 0;
+        // Q: the row scaled by a power of two into [1, 2) at its largest, as fp16, K-major swizzled
+        const int rr = r & (kRowTile - 1);
+        uint8_t *dst = q_smem + i * C::kTileBytes + rr * 128;
+        float amax = 0.f;
+        uint4 qv[D / 8];
+        const uint16_t *src = p.q + (int64_t)(q.q0 + tok) * p.q_ld + (int64_t)qh * D;
+#pragma unroll
+        for (int c = 0; c < D / 8; ++c) {
+            qv[c] = live ? *reinterpret_cast<const uint4 *>(src + c * 8) : make_uint4(0, 0, 0, 0);
+        }
+#pragma unroll
+        for (int c = 0; c < D / 8; ++c) {
+            float f[8];
+            unpack8<F16>(qv[c], f);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) amax = fmaxf(amax, fabsf(f[j]));
+        }
+        const int q_exp = amax > 0.f ? max(min((int)(__float_as_uint(amax) >> 23) - 127, 126), -126) : 0;
+        const float q_inv = pow2f(-q_exp);
+#pragma unroll
+        for (int c = 0; c < D / 8; ++c) {
+            float f[8];
+            unpack8<F16>(qv[c], f);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) f[j] *= q_inv;
+            *reinterpret_cast<uint4 *>(dst + (c >> 3) * C::kBlockBytes + (((c & 7) ^ (rr & 7)) << 4)) = pack8<true>(f);
+        }
+        ptx::fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(q_full);
+
+        const float mul = p.scale_log2 * pow2f(q_exp) * pow2f(k_exp);
+        const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+        const uint32_t s_addr = tmem + lanes + i * kKeys, o_addr = tmem + lanes + C::kColO + i * D;
+        float m = -INFINITY, l = 0.f;
+        for (int j = 0; j < tiles && ok; ++j) {
+            ok = ptx::mbar_wait(&s_full[i], j & 1, kWaitNs, abort_flag);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+            ptx::tc_fence_after();
+            const int key0 = (tile0 + j) * kKeys;
+            const bool masked = __any_sync(0xffffffffu, live && (key0 < lo || key0 + kKeys > hi));
+            const int c_lo = lo - key0, c_hi = hi - key0;
+            float top = -INFINITY;
+            uint32_t s[32];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                ptx::tmem_ld_32(s_addr + c * 32, s);
+                ptx::tmem_ld_wait();
+                if (masked) {
+#pragma unroll
+                    for (int k = 0; k < 32; ++k)
+                        if (c * 32 + k >= c_lo && c * 32 + k < c_hi) top = fmaxf(top, __uint_as_float(s[k]));
+                } else {
+#pragma unroll
+                    for (int k = 0; k < 32; ++k) top = fmaxf(top, __uint_as_float(s[k]));
+                }
+            }
+            top *= mul;  // mul > 0
+            if (__any_sync(0xffffffffu, top > m + kLazy)) {
+                const float to = fmaxf(m, top);
+                const float f = to == -INFINITY ? 1.f : exp2_fast(m - to);
+                m = to;
+                l *= f;
+                if (j > 0) {  // the logits came after the last product of this tile was complete
+                    uint32_t o[32];
+                    __syncwarp();
+#pragma unroll
+                    for (int c = 0; c < D / 32; ++c) {
+                        ptx::tmem_ld_32(o_addr + c * 32, o);
+                        ptx::tmem_ld_wait();
+#pragma unroll
+                        for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
+                        ptx::tmem_st_32(o_addr + c * 32, o);
+                    }
+                }
+            }
+            const float ref = m == -INFINITY ? 0.f : m;
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                uint32_t w[16];
+                ptx::tmem_ld_32(s_addr + c * 32, s);
+                ptx::tmem_ld_wait();
+                if (masked) {
+#pragma unroll
+                    for (int k = 0; k < 32; ++k)
+                        if (c * 32 + k < c_lo || c * 32 + k >= c_hi) s[k] = 0xff800000u;  // -inf
+                }
+#pragma unroll
+                for (int k = 0; k < 16; ++k) {
+                    const float a = exp2_fast(fmaf(__uint_as_float(s[2 * k]), mul, -ref));
+                    const float e = exp2_fast(fmaf(__uint_as_float(s[2 * k + 1]), mul, -ref));
+                    l += a + e;
+                    w[k] = pack2<true>(a, e);
+                }
+                ptx::tmem_st_16(s_addr + c * 16, w);  // behind what has been read of S
+            }
+            ptx::tmem_st_wait();
+            ptx::tc_fence_before();
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(&p_full[i]);
+        }
+        if (ok && tiles > 0) ok = ptx::mbar_wait(&o_full[i], 0, kWaitNs, abort_flag);
+        ok = __all_sync(0xffffffffu, ok);
+        if (ok) {
+            ptx::tc_fence_after();
+            const float inv = (l > 0.f || l != l) && tiles > 0 ? pow2f(v_exp) / l : 0.f;
+            uint16_t *out = p.out + (int64_t)(q.q0 + tok) * p.out_ld + (int64_t)qh * D;
+#pragma unroll
+            for (int c = 0; c < D / 32; ++c) {
+                uint32_t o[32];
+                __syncwarp();
+                if (tiles > 0) {
+                    ptx::tmem_ld_32(o_addr + c * 32, o);
+                    ptx::tmem_ld_wait();
+                }
+#pragma unroll
+                for (int k = 0; k < 4 && live; ++k) {
+                    float f[8];
+#pragma unroll
+                    for (int x = 0; x < 8; ++x) f[x] = inv == 0.f ? 0.f : __uint_as_float(o[8 * k + x]) * inv;
+                    *reinterpret_cast<uint4 *>(out + c * 32 + k * 8) = pack8<F16>(f);
+                }
+            }
+            if (live && p.lse) p.lse[(int64_t)(q.q0 + tok) * v.QH + qh] = (m + log2f(l)) * 0.6931471805599453f;
+        }
+    } else if (warp < kMmaWarp) {
+        // ------------------------------------------------------------- K and V, widened --
+        // A warp's load takes 8 rows x 64 codes: lane = 4 * row + 16-code piece, so that its two
+        // 16-byte stores of 8 lanes fall on all the banks.
+        constexpr int kLoads = (kKeys / 8) * C::kBlocks / kConvWarps;  // a warp's loads of a tile
+        const int cw = warp - kConvWarp0, piece = lane & 3, sub = lane >> 2;
+        for (int it = 0; it < 2 * tiles && ok; ++it) {
+            const bool is_v = it & 1;
+            const int key0 = (tile0 + (it >> 1)) * kKeys, s = it % kStages;
+            const uint8_t *codes = is_v ? v.v_codes : v.k_codes;
+            const float *scale = is_v ? v.v_scale : v.k_scale;
+            const int ref = is_v ? v_exp : k_exp;
+            uint4 raw[kLoads];
+            int shift[kLoads];
+#pragma unroll
+            for (int n = 0; n < kLoads; ++n) {
+                const int unit = n * kConvWarps + cw, block = unit % C::kBlocks;
+                const int key = key0 + unit / C::kBlocks * 8;  // 8 rows of one page
+                raw[n] = make_uint4(0, 0, 0, 0);
+                shift[n] = 0;
+                if (key >= q.kv) continue;
+                int page = __ldg(table + (key >> v.log_p));
+                if (page < 0 || page >= v.n_pages) page = 0;  // reported above
+                shift[n] = exponent_of(__ldg(scale + (int64_t)page * v.KH + head)) - ref;
+                if (key + sub < q.kv)  // slots past the end hold anything
+                    raw[n] = *reinterpret_cast<const uint4 *>(
+                        codes + (((int64_t)page * v.KH + head) * v.P + ((key + sub) & (v.P - 1))) * D + block * 64 + piece * 16);
+            }
+            if (it >= kStages) {
+                ok = ptx::mbar_wait(&empty[s], (it / kStages - 1) & 1, kWaitNs, abort_flag);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+            }
+            uint8_t *st = kv_smem + s * C::kTileBytes;
+#pragma unroll
+            for (int n = 0; n < kLoads; ++n) {
+                const int unit = n * kConvWarps + cw, block = unit % C::kBlocks;
+                const int row = unit / C::kBlocks * 8 + sub;
+                const uint32_t w[4] = {raw[n].x, raw[n].y, raw[n].z, raw[n].w};
+                uint32_t h[8];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    h[2 * k] = widen2(w[k] & 0xffffu);
+                    h[2 * k + 1] = widen2(w[k] >> 16);
+                }
+                if (shift[n] != 0) {  // the same for the whole warp
+                    // two factors, powers of two that fp16 has: the first product is exact, the second rounds
+                    const int a = max(shift[n], -14), c = max(shift[n] - a, -24);
+                    const __half2 fa = __float2half2_rn(pow2f(a)), fc = __float2half2_rn(pow2f(c));
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) h[k] = mul2(mul2(h[k], fa), fc);
+                }
+                uint8_t *dst = st + block * C::kBlockBytes + row * 128;
+                *reinterpret_cast<uint4 *>(dst + (((2 * piece) ^ (row & 7)) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
+                *reinterpret_cast<uint4 *>(dst + (((2 * piece + 1) ^ (row & 7)) << 4)) = make_uint4(h[4], h[5], h[6], h[7]);
+            }
+            ptx::fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(&full[s]);
+        }
+    } else if (lane == 0 && tiles > 0) {
+        // ---------------------------------------------------------------------- the MMAs --
+        const uint32_t idesc_s = ptx::idesc_f16_f32(kRowTile, kKeys, false);
+        const uint32_t idesc_o = ptx::idesc_f16_f32(kRowTile, D, true);
+        const uint32_t q_addr = ptx::smem_u32(q_smem), kv_addr = ptx::smem_u32(kv_smem);
+        auto logits = [&](int i, int s) {
+#pragma unroll
+            for (int k = 0; k < D / 16; ++k) {
+                const uint32_t off = (uint32_t)((k >> 2) * C::kBlockBytes + (k & 3) * 32);
+                ptx::mma_f16_ss(tmem + i * kKeys, ptx::sw128_desc(q_addr + i * C::kTileBytes + off),
+                                ptx::sw128_desc(kv_addr + s * C::kTileBytes + off), idesc_s, k > 0);
+            }
+        };
+        auto output = [&](int i, int s, bool more) {
+#pragma unroll
+            for (int k = 0; k < kKeys / 16; ++k)
+                ptx::mma_f16_ts(tmem + C::kColO + i * D, tmem + i * kKeys + k * 8,
+                                ptx::sw128_desc_mn(kv_addr + s * C::kTileBytes + k * 2048, C::kBlockBytes), idesc_o,
+                                more || k > 0);
+        };
+        auto filled = [&](int it) { return ptx::mbar_wait(&full[it % kStages], (it / kStages) & 1, kWaitNs, abort_flag); };
+        ok = ptx::mbar_wait(q_full, 0, kWaitNs, abort_flag) && filled(0);
+        if (ok) {
+            ptx::tc_fence_after();
+            for (int i = 0; i < 2; ++i) {
+                logits(i, 0);
+                ptx::mma_commit(&s_full[i]);
+            }
+            ptx::mma_commit(&empty[0]);
+        }
+        for (int j = 0; j < tiles && ok; ++j) {
+            const int vs = (2 * j + 1) % kStages, ks = (2 * j + 2) % kStages;
+            const bool next = j + 1 < tiles;
+            ok = filled(2 * j + 1);
+            for (int i = 0; i < 2 && ok; ++i) {
+                ok = ptx::mbar_wait(&p_full[i], j & 1, kWaitNs, abort_flag);
+                if (!ok) break;
+                ptx::tc_fence_after();
+                output(i, vs, j > 0);
+                if (!next) ptx::mma_commit(&o_full[i]);
+                if (i == 1) ptx::mma_commit(&empty[vs]);
+                if (!next) continue;
+                if (i == 0) ok = filled(2 * j + 2);
+                if (!ok) break;
+                ptx::tc_fence_after();
+                logits(i, ks);
+                ptx::mma_commit(&s_full[i]);
+                if (i == 1) ptx::mma_commit(&empty[ks]);
+            }
+        }
+        if (!ok) {  // nothing of this block may still run when its TMEM is freed
+            ptx::mma_commit(drain);
+            int zero = 0;
+            ptx::mbar_wait(drain, 0, kWaitNs, &zero);
+        }
+    }
+    if (!ok) {
+        *abort_flag = 1;
+        atomicCAS(v.status, 0, (int)MOE_ERR_TIMEOUT);
+    }
+    __syncwarp();
+    ptx::tc_fence_before();
+    __syncthreads();
+    ptx::tc_fence_after();
+    if (warp == kMmaWarp) ptx::tmem_dealloc(tmem, C::kCols);
+}
+
+template <int D, bool F16>
+cudaError_t launch(const AttnArgs &a, cudaStream_t s) {
+    constexpr int smem = Prompt<D>::kSmem;
+    static_assert(smem <= 227 * 1024, "shared memory over the per-block limit");
+    cudaError_t e = cudaFuncSetAttribute(attn_prompt_kernel<D, F16>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    LaunchScope scope(KC_ATTN_PROMPT, s);
+    const int slots = (int)((int64_t)a.kv.n_tokens * a.kv.G / kRowsBlock) + a.kv.n_seqs;
+    attn_prompt_kernel<D, F16><<<slots * a.kv.KH, kThreads, smem, s>>>(a, slots);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_attn_prompt(const AttnArgs &a, int D, int dtype, cudaStream_t s) {
+    const bool f16 = dtype == MOE_DTYPE_F16;
+    if (D == 64) return f16 ? launch<64, true>(a, s) : launch<64, false>(a, s);
+    return f16 ? launch<128, true>(a, s) : launch<128, false>(a, s);
+}
+
+}  // namespace moe

@@ -46,12 +46,16 @@ struct AttnArgs {
     // split kernel: partial results and tickets, one pair of slots and one ticket a block
     float *part;
     unsigned *ticket;
+    // sequences with at least this many query rows a kv head (new tokens x G) are the prompt
+    // kernel's, the others the split kernel's
+    int prompt_rows;
 };
 // Blocks the split kernel may have (its workspace is sized for them).
 constexpr int kSplitMaxBlocks = 1024;
 // Floats of workspace the split kernel needs for partial results.
 size_t split_part_floats(int D);
 cudaError_t launch_attn_split(const AttnArgs &a, int D, int dtype, cudaStream_t s);
+cudaError_t launch_attn_prompt(const AttnArgs &a, int D, int dtype, cudaStream_t s);  // D 64 or 128
 
 struct NormArgs {
     const uint16_t *x, *resid, *gate, *w_post, *w_pre;

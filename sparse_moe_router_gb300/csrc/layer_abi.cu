@@ -1,5 +1,6 @@
 // layer_abi.cu -- the extern "C" entry points of the decoder layer's other half (include/moe.h):
 // argument checks, workspace carving, launches.
+#include <climits>
 #include <cmath>
 
 #include <nvtx3/nvToolsExt.h>
@@ -57,6 +58,9 @@ moe_status check_batch(const moe_attn_config &c, const moe_kv_cache *k, const mo
     if (!aligned16(k->k_codes) || !aligned16(k->v_codes)) return MOE_ERR_INVALID_ARG;
     return MOE_OK;
 }
+
+// Query rows a kv head from which a sequence goes to the prompt kernel.
+constexpr int kPromptRows = 128;
 
 struct Layout {
     size_t ticket, part, total;
@@ -224,7 +228,13 @@ moe_status moe_attention(const moe_attn_config *cfg, const moe_kv_cache *cache, 
     a.window = window;
     a.ticket = reinterpret_cast<unsigned *>(static_cast<char *>(ws) + l.ticket);
     a.part = reinterpret_cast<float *>(static_cast<char *>(ws) + l.part);
-    MOE_CUDA(launch_attn_split(a, c.head_dim, c.dtype, static_cast<cudaStream_t>(stream)));
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    // Which sequences the prompt kernel takes goes by their own rows, which only the device knows; the host
+    // leaves out a kernel that cannot have any.
+    const int64_t rows = (int64_t)batch->n_tokens * a.kv.G;
+    a.prompt_rows = c.head_dim <= 128 ? kPromptRows : INT_MAX;
+    if (rows >= a.prompt_rows) MOE_CUDA(launch_attn_prompt(a, c.head_dim, c.dtype, s));
+    if (batch->n_seqs > 1 || rows < a.prompt_rows) MOE_CUDA(launch_attn_split(a, c.head_dim, c.dtype, s));
     return MOE_OK;
 }
 
