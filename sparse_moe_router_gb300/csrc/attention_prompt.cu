@@ -30,8 +30,11 @@ namespace {
 constexpr int kRowTile = 128, kRowsBlock = 2 * kRowTile;
 constexpr int kKeys = 128;  // keys a tile
 constexpr int kStages = 4;  // K and V tiles in flight, in the order K0 V0 K1 V1 ...
-constexpr int kSoftWarps = 8, kConvWarp0 = 8, kConvWarps = 4, kMmaWarp = 12;
-constexpr int kThreads = 13 * 32;
+constexpr int kSoftWarps = 8, kConvWarp0 = 8, kConvWarps = 7, kMmaWarp = 15;
+constexpr int kThreads = 16 * 32;
+// Registers a thread: 128 at launch (four warps a scheduler); the softmax warps hold a row's 128
+// logits and take 2 x 168 of a scheduler's 4 x 128, the others keep 88.
+constexpr int kSoftRegs = 168, kOtherRegs = 88;
 constexpr uint64_t kWaitNs = 2000000000ull;  // 2 s: far above any legitimate wait
 constexpr float kLazy = 8.f;
 
@@ -56,9 +59,27 @@ __device__ __forceinline__ uint32_t widen2(uint32_t codes) {
     const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)codes, __NV_E4M3);
     return (uint32_t)h.x | ((uint32_t)h.y << 16);
 }
-__device__ __forceinline__ uint32_t mul2(uint32_t a, __half2 f) {
-    const __half2 r = __hmul2(*reinterpret_cast<const __half2 *>(&a), f);
+__device__ __forceinline__ uint32_t mul2(uint32_t a, uint32_t f) {
+    const __half2 r = __hmul2(*reinterpret_cast<const __half2 *>(&a), *reinterpret_cast<const __half2 *>(&f));
     return *reinterpret_cast<const uint32_t *>(&r);
+}
+
+// Values read from TMEM are used only past this point (after the wait that completes the read).
+__device__ __forceinline__ void tie32(uint32_t (&r)[32]) {
+#pragma unroll
+    for (int k = 0; k < 32; ++k) asm volatile("" : "+r"(r[k]));
+}
+// a * b + c on two values at once.
+__device__ __forceinline__ float2 fma2(float2 a, float b, float c) {
+    return __ffma2_rn(a, make_float2(b, b), make_float2(c, c));
+}
+template <int R>
+__device__ __forceinline__ void regs_up() {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R));
+}
+template <int R>
+__device__ __forceinline__ void regs_down() {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R));
 }
 
 // Block (slot, head): sequence b owns the 256-row slots base(b) .. base(b+1)-1 of every head, with
@@ -155,6 +176,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
     bool ok = true;
 
     if (warp < kSoftWarps) {
+        regs_up<kSoftRegs>();
         // ----------------------------------------------------------------- softmax, rows --
         const int i = warp >> 2;                        // row tile
         const int r = i * kRowTile + (warp & 3) * 32 + lane;  // row of the block = TMEM lane of tile i
@@ -197,46 +219,55 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
         const float mul = p.scale_log2 * pow2f(q_exp) * pow2f(k_exp);
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t s_addr = tmem + lanes + i * kKeys, o_addr = tmem + lanes + C::kColO + i * D;
-        float m = -INFINITY, l = 0.f;
+        float m = -INFINITY;
+        float l0 = 0.f, l1 = 0.f;  // sums of the even and odd columns' weights
         for (int j = 0; j < tiles && ok; ++j) {
             ok = ptx::mbar_wait(&s_full[i], j & 1, kWaitNs, abort_flag);
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
             ptx::tc_fence_after();
             const int key0 = (tile0 + j) * kKeys;
-            const bool masked = __any_sync(0xffffffffu, live && (key0 < lo || key0 + kKeys > hi));
-            const int c_lo = lo - key0, c_hi = hi - key0;
-            float top = -INFINITY;
-            uint32_t s[32];
+            uint32_t s[4][32];
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                ptx::tmem_ld_32(s_addr + c * 32, s);
-                ptx::tmem_ld_wait();
-                if (masked) {
+            for (int c = 0; c < 4; ++c) ptx::tmem_ld_32(s_addr + c * 32, s[c]);
+            ptx::tmem_ld_wait();
+#pragma unroll
+            for (int c = 0; c < 4; ++c) tie32(s[c]);
+            if (__any_sync(0xffffffffu, live && (key0 < lo || key0 + kKeys > hi))) {
+                const int c_lo = lo - key0, c_hi = hi - key0;
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
 #pragma unroll
                     for (int k = 0; k < 32; ++k)
-                        if (c * 32 + k >= c_lo && c * 32 + k < c_hi) top = fmaxf(top, __uint_as_float(s[k]));
-                } else {
-#pragma unroll
-                    for (int k = 0; k < 32; ++k) top = fmaxf(top, __uint_as_float(s[k]));
-                }
+                        if (c * 32 + k < c_lo || c * 32 + k >= c_hi) s[c][k] = 0xff800000u;  // -inf
             }
-            top *= mul;  // mul > 0
+            float tops[4];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                tops[c] = __uint_as_float(s[c][0]);
+#pragma unroll
+                for (int k = 1; k < 32; ++k) tops[c] = fmaxf(tops[c], __uint_as_float(s[c][k]));
+            }
+            const float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3])) * mul;  // mul > 0
             if (__any_sync(0xffffffffu, top > m + kLazy)) {
                 const float to = fmaxf(m, top);
                 const float f = to == -INFINITY ? 1.f : exp2_fast(m - to);
                 m = to;
-                l *= f;
+                l0 *= f;
+                l1 *= f;
                 if (j > 0) {  // the logits came after the last product of this tile was complete
-                    uint32_t o[32];
+                    uint32_t o[16];
                     __syncwarp();
 #pragma unroll
-                    for (int c = 0; c < D / 32; ++c) {
-                        ptx::tmem_ld_32(o_addr + c * 32, o);
+                    for (int c = 0; c < D / 16; ++c) {
+                        ptx::tmem_ld_16(o_addr + c * 16, o);
                         ptx::tmem_ld_wait();
 #pragma unroll
-                        for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
-                        ptx::tmem_st_32(o_addr + c * 32, o);
+                        for (int k = 0; k < 16; ++k) {
+                            asm volatile("" : "+r"(o[k]));
+                            o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
+                        }
+                        ptx::tmem_st_16(o_addr + c * 16, o);
                     }
                 }
             }
@@ -244,27 +275,22 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
                 uint32_t w[16];
-                ptx::tmem_ld_32(s_addr + c * 32, s);
-                ptx::tmem_ld_wait();
-                if (masked) {
-#pragma unroll
-                    for (int k = 0; k < 32; ++k)
-                        if (c * 32 + k < c_lo || c * 32 + k >= c_hi) s[k] = 0xff800000u;  // -inf
-                }
 #pragma unroll
                 for (int k = 0; k < 16; ++k) {
-                    const float a = exp2_fast(fmaf(__uint_as_float(s[2 * k]), mul, -ref));
-                    const float e = exp2_fast(fmaf(__uint_as_float(s[2 * k + 1]), mul, -ref));
-                    l += a + e;
+                    const float2 z = fma2(make_float2(__uint_as_float(s[c][2 * k]), __uint_as_float(s[c][2 * k + 1])), mul, -ref);
+                    const float a = exp2_fast(z.x), e = exp2_fast(z.y);
+                    l0 += a;
+                    l1 += e;
                     w[k] = pack2<true>(a, e);
                 }
-                ptx::tmem_st_16(s_addr + c * 16, w);  // behind what has been read of S
+                ptx::tmem_st_16(s_addr + c * 16, w);  // over S, all of which is in registers
             }
             ptx::tmem_st_wait();
             ptx::tc_fence_before();
             __syncwarp();
             if (lane == 0) ptx::mbar_arrive(&p_full[i]);
         }
+        const float l = l0 + l1;
         if (ok && tiles > 0) ok = ptx::mbar_wait(&o_full[i], 0, kWaitNs, abort_flag);
         ok = __all_sync(0xffffffffu, ok);
         if (ok) {
@@ -289,67 +315,88 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
             }
             if (live && p.lse) p.lse[(int64_t)(q.q0 + tok) * v.QH + qh] = (m + log2f(l)) * 0.6931471805599453f;
         }
-    } else if (warp < kMmaWarp) {
+    } else {
+        regs_down<kOtherRegs>();
+        if (warp < kMmaWarp) {
         // ------------------------------------------------------------- K and V, widened --
-        // A warp's load takes 8 rows x 64 codes: lane = 4 * row + 16-code piece, so that its two
-        // 16-byte stores of 8 lanes fall on all the banks.
-        constexpr int kLoads = (kKeys / 8) * C::kBlocks / kConvWarps;  // a warp's loads of a tile
+        // A unit is 8 rows x 64 codes, one load of a warp: lane = 4 * row + 16-code piece, so that the
+        // two 16-byte stores of 8 lanes fall on all the banks.  A unit's registers take the next
+        // tile's codes as soon as they are widened: their latency runs under the other units and
+        // the wait for the next stage.
+        constexpr int kUnits = kKeys / 8 * C::kBlocks;
+        constexpr int kLoads = (kUnits + kConvWarps - 1) / kConvWarps;
         const int cw = warp - kConvWarp0, piece = lane & 3, sub = lane >> 2;
-        for (int it = 0; it < 2 * tiles && ok; ++it) {
-            const bool is_v = it & 1;
-            const int key0 = (tile0 + (it >> 1)) * kKeys, s = it % kStages;
-            const uint8_t *codes = is_v ? v.v_codes : v.k_codes;
-            const float *scale = is_v ? v.v_scale : v.k_scale;
-            const int ref = is_v ? v_exp : k_exp;
-            uint4 raw[kLoads];
-            int shift[kLoads];
+        // lane x holds the page (with the head: page * KH + head) of keys x P .. of a tile, and the
+        // factors 2^(exponent - the block's largest) of its codes
+        auto page_at = [&](int tile) {
+            const int key = (tile0 + tile) * kKeys + (lane << v.log_p);
+            int page = 0;
+            if (lane < (kKeys >> v.log_p) && key < q.kv && tile < tiles) page = __ldg(table + (key >> v.log_p));
+            return (page < 0 || page >= v.n_pages ? 0 : page) * v.KH + head;  // (reported above)
+        };
+        auto factor = [&](float scale, int largest) {
+            const int e = min(exponent_of(scale) - largest, 0);  // (lanes without a page)
+            const __half2 f = __float2half2_rn(e < -24 ? 0.f : pow2f(e));
+            return *reinterpret_cast<const uint32_t *>(&f);
+        };
+        uint4 raw[kLoads];
+        const int log_pd = v.log_p + (D == 128 ? 7 : 6);
+        auto load = [&](int n, int tile, int pages, const uint8_t *codes) {
+            const int unit = n * kConvWarps + cw, row = unit / C::kBlocks * 8 + sub;
+            const int page = __shfl_sync(0xffffffffu, pages, row >> v.log_p);
+            raw[n] = make_uint4(0, 0, 0, 0);
+            if (unit < kUnits && (tile0 + tile) * kKeys + row < q.kv)  // slots past the end hold anything
+                raw[n] = __ldg(reinterpret_cast<const uint4 *>(
+                    codes + ((uint64_t)(uint32_t)page << log_pd) + (row & (v.P - 1)) * D + unit % C::kBlocks * 64 + piece * 16));
+        };
+        int page0 = page_at(0), page1 = page_at(1), page2 = page_at(2);
+        uint32_t fk = factor(__ldg(v.k_scale + page0), k_exp), fv = factor(__ldg(v.v_scale + page0), v_exp);
+        float sk1 = __ldg(v.k_scale + page1), sv1 = __ldg(v.v_scale + page1);
 #pragma unroll
-            for (int n = 0; n < kLoads; ++n) {
-                const int unit = n * kConvWarps + cw, block = unit % C::kBlocks;
-                const int key = key0 + unit / C::kBlocks * 8;  // 8 rows of one page
-                raw[n] = make_uint4(0, 0, 0, 0);
-                shift[n] = 0;
-                if (key >= q.kv) continue;
-                int page = __ldg(table + (key >> v.log_p));
-                if (page < 0 || page >= v.n_pages) page = 0;  // reported above
-                shift[n] = exponent_of(__ldg(scale + (int64_t)page * v.KH + head)) - ref;
-                if (key + sub < q.kv)  // slots past the end hold anything
-                    raw[n] = *reinterpret_cast<const uint4 *>(
-                        codes + (((int64_t)page * v.KH + head) * v.P + ((key + sub) & (v.P - 1))) * D + block * 64 + piece * 16);
-            }
+        for (int n = 0; n < kLoads; ++n)
+            if (tiles > 0) load(n, 0, page0, v.k_codes);
+        for (int it = 0; it < 2 * tiles; ++it) {
+            const bool is_v = it & 1;
+            const int tile = it >> 1, s = it % kStages;
             if (it >= kStages) {
                 ok = ptx::mbar_wait(&empty[s], (it / kStages - 1) & 1, kWaitNs, abort_flag);
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
             }
             uint8_t *st = kv_smem + s * C::kTileBytes;
+            const uint32_t f_lane = is_v ? fv : fk;
+            const uint8_t *codes = is_v ? v.k_codes : v.v_codes;  // of the next stage
+            const int next_tile = tile + (is_v ? 1 : 0), next_page = is_v ? page1 : page0;
 #pragma unroll
             for (int n = 0; n < kLoads; ++n) {
-                const int unit = n * kConvWarps + cw, block = unit % C::kBlocks;
-                const int row = unit / C::kBlocks * 8 + sub;
+                const int unit = n * kConvWarps + cw, row = unit / C::kBlocks * 8 + sub;
+                // the 8 rows lie in one page, so the factor is the same for the whole warp
+                const uint32_t f = __shfl_sync(0xffffffffu, f_lane, row >> v.log_p);
                 const uint32_t w[4] = {raw[n].x, raw[n].y, raw[n].z, raw[n].w};
                 uint32_t h[8];
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
-                    h[2 * k] = widen2(w[k] & 0xffffu);
-                    h[2 * k + 1] = widen2(w[k] >> 16);
+                    h[2 * k] = mul2(widen2(w[k] & 0xffffu), f);
+                    h[2 * k + 1] = mul2(widen2(w[k] >> 16), f);
                 }
-                if (shift[n] != 0) {  // the same for the whole warp
-                    // two factors, powers of two that fp16 has: the first product is exact, the second rounds
-                    const int a = max(shift[n], -14), c = max(shift[n] - a, -24);
-                    const __half2 fa = __float2half2_rn(pow2f(a)), fc = __float2half2_rn(pow2f(c));
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) h[k] = mul2(mul2(h[k], fa), fc);
+                if (unit < kUnits) {
+                    uint8_t *dst = st + unit % C::kBlocks * C::kBlockBytes + row * 128;
+                    *reinterpret_cast<uint4 *>(dst + (((2 * piece) ^ (row & 7)) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
+                    *reinterpret_cast<uint4 *>(dst + (((2 * piece + 1) ^ (row & 7)) << 4)) = make_uint4(h[4], h[5], h[6], h[7]);
                 }
-                uint8_t *dst = st + block * C::kBlockBytes + row * 128;
-                *reinterpret_cast<uint4 *>(dst + (((2 * piece) ^ (row & 7)) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
-                *reinterpret_cast<uint4 *>(dst + (((2 * piece + 1) ^ (row & 7)) << 4)) = make_uint4(h[4], h[5], h[6], h[7]);
+                if (next_tile < tiles) load(n, next_tile, next_page, codes);
             }
             ptx::fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) ptx::mbar_arrive(&full[s]);
+            if (is_v) {
+                fk = factor(sk1, k_exp), fv = factor(sv1, v_exp);
+                page0 = page1, page1 = page2;
+                sk1 = __ldg(v.k_scale + page1), sv1 = __ldg(v.v_scale + page1);
+                page2 = page_at(tile + 3);
+            }
         }
-    } else if (lane == 0 && tiles > 0) {
+        } else if (lane == 0 && tiles > 0) {
         // ---------------------------------------------------------------------- the MMAs --
         const uint32_t idesc_s = ptx::idesc_f16_f32(kRowTile, kKeys, false);
         const uint32_t idesc_o = ptx::idesc_f16_f32(kRowTile, D, true);
@@ -403,6 +450,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
             ptx::mma_commit(drain);
             int zero = 0;
             ptx::mbar_wait(drain, 0, kWaitNs, &zero);
+        }
         }
     }
     if (!ok) {

@@ -51,6 +51,7 @@ moe_status check_batch(const moe_attn_config &c, const moe_kv_cache *k, const mo
     if (b->n_seqs == 0 && b->n_tokens > 0) return MOE_ERR_INVALID_ARG;
     if (b->n_seqs > kMaxSeqs || b->n_tokens > kMaxTokens) return MOE_ERR_UNSUPPORTED_SHAPE;
     if ((int64_t)b->max_pages * c.page_size > (1 << 30)) return MOE_ERR_UNSUPPORTED_SHAPE;
+    if ((int64_t)k->n_pages * c.kv_heads > INT_MAX) return MOE_ERR_UNSUPPORTED_SHAPE;
     if (b->n_tokens == 0) return MOE_OK;
     if (!b->q_start || !b->kv_len) return MOE_ERR_INVALID_ARG;
     if (b->max_pages > 0 && !b->page_table) return MOE_ERR_INVALID_ARG;
