@@ -10,15 +10,15 @@
 // D = 128, and the weights of its 2 x 16,384 logits take about as long on two warpgroups, so the two
 // row tiles alternate: while the tensor cores work on one, the other's softmax runs.  The 8-bit
 // codes cannot be an operand beside fp16 weights (both operands of an MMA have one type, and queries in 8
-// bits would lose what the 16-bit ones hold), so four warps read codes from global memory (L2,
+// bits would lose what the 16-bit ones hold), so eight warps read codes from global memory (L2,
 // mostly: all tiles of a head read the same pages), widen them exactly to fp16 and store them in the
 // swizzled layout that the MMA reads: 96 KB of shared-memory traffic a tile against the MMA's own
 // 192 KB.  The exponents of the pages are drawn into the codes relative to the largest one the block
 // will meet (exact in fp16 unless a page is 2^-15 below it, and then off by at most 2^-25 of the
 // largest), so one factor a row holds for all keys.
 //
-// Roles: warps 0-3 and 4-7 softmax of row tiles 0 and 1 (one row a thread), warps 8-11 widen K and V,
-// one thread of warp 12 issues the MMAs.  Row maxima move lazily: a row's reference changes only when a
+// Roles: warps 0-3 and 4-7 are row tiles 0 and 1, one row a thread; a thread of each also issues its
+// tile's MMAs, so the hand-over from weights to products is one barrier.  Warps 8-15 widen K and V.  Row maxima move lazily: a row's reference changes only when a
 // logit passes it by 2^8 (weights stay below 256), so O is rarely rescaled, by the thread that
 // owns the row.
 #include "layer.h"
@@ -30,8 +30,8 @@ namespace {
 constexpr int kRowTile = 128, kRowsBlock = 2 * kRowTile;
 constexpr int kKeys = 128;  // keys a tile
 constexpr int kStages = 4;  // K and V tiles in flight, in the order K0 V0 K1 V1 ...
-constexpr int kSoftWarps = 8, kConvWarp0 = 8, kConvWarps = 7, kMmaWarp = 15;
-constexpr int kThreads = 16 * 32;
+constexpr int kSoftWarps = 8, kConvWarps = 8;
+constexpr int kThreads = (kSoftWarps + kConvWarps) * 32;
 // Registers a thread: 128 at launch (four warps a scheduler); the softmax warps hold a row's 128
 // logits and take 2 x 168 of a scheduler's 4 x 128, the others keep 88.
 constexpr int kSoftRegs = 168, kOtherRegs = 88;
@@ -73,6 +73,11 @@ __device__ __forceinline__ void tie32(uint32_t (&r)[32]) {
 __device__ __forceinline__ float2 fma2(float2 a, float b, float c) {
     return __ffma2_rn(a, make_float2(b, b), make_float2(c, c));
 }
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
 template <int R>
 __device__ __forceinline__ void regs_up() {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R));
@@ -100,13 +105,15 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
     uint64_t *s_full = empty + kStages;              // [2] logits of a row tile are in TMEM
     uint64_t *p_full = s_full + 2;                   // [2] its weights are
     uint64_t *o_full = p_full + 2;                   // [2] its output is complete
-    uint64_t *q_full = o_full + 2;
-    uint64_t *drain = q_full + 1;
-    uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(drain + 1);
+    uint64_t *q_full = o_full + 2;                   // [2] its queries are in shared memory
+    uint64_t *drain = q_full + 2;                    // [2]
+    uint64_t *turn = drain + 2;                      // [2] the row tile may issue its next MMAs
+    uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(turn + 2);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_holder + 1);
     int *max_exp = reinterpret_cast<int *>(tmem_holder + 2);  // [2] of K and V
 
-    const int tid = (int)threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = (int)threadIdx.x, lane = tid & 31;
+    const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);  // known to be the same in all lanes
 
     // ------------------------------------------------------------------- the block's rows --
     const int head = (int)blockIdx.x % v.KH;
@@ -133,20 +140,21 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
     if (tid == 0) {
         for (int s = 0; s < kStages; ++s) {
             ptx::mbar_init(&full[s], kConvWarps);
-            ptx::mbar_init(&empty[s], 1);
+            ptx::mbar_init(&empty[s], 2);  // both row tiles are done with it
         }
         for (int i = 0; i < 2; ++i) {
             ptx::mbar_init(&s_full[i], 1);
             ptx::mbar_init(&p_full[i], 4);
             ptx::mbar_init(&o_full[i], 1);
+            ptx::mbar_init(&q_full[i], 4);
+            ptx::mbar_init(&drain[i], 1);
+            ptx::mbar_init(&turn[i], 1);
         }
-        ptx::mbar_init(q_full, kSoftWarps);
-        ptx::mbar_init(drain, 1);
         *abort_flag = 0;
         max_exp[0] = max_exp[1] = -127;
         ptx::fence_mbar_init();
     }
-    if (warp == kMmaWarp) ptx::tmem_alloc(tmem_holder, C::kCols);
+    if (warp == 0) ptx::tmem_alloc(tmem_holder, C::kCols);
     ptx::tc_fence_before();
     __syncthreads();
     ptx::tc_fence_after();
@@ -214,13 +222,65 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
         }
         ptx::fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(q_full);
+        if (lane == 0) ptx::mbar_arrive(&q_full[i]);
+
+        // --------------------------------------- the MMAs, by one warp of each row tile --
+        const bool issuer = (warp & 3) == 0;
+        const uint32_t idesc_s = ptx::idesc_f16_f32(kRowTile, kKeys, false);
+        const uint32_t idesc_o = ptx::idesc_f16_f32(kRowTile, D, true);
+        const uint32_t s_tmem = tmem + i * kKeys, o_tmem = tmem + C::kColO + i * D;
+        const uint64_t q_desc = ptx::sw128_desc(ptx::smem_u32(q_smem) + i * C::kTileBytes);
+        const uint64_t k_desc = ptx::sw128_desc(ptx::smem_u32(kv_smem));
+        const uint64_t v_desc = ptx::sw128_desc_mn(ptx::smem_u32(kv_smem), C::kBlockBytes);
+        auto all = [](bool x) { return __all_sync(0xffffffffu, x) != 0; };
+        auto filled = [&](int it) { return ptx::mbar_wait(&full[it % kStages], (it / kStages) & 1, kWaitNs, abort_flag); };
+        auto logits = [&](int j) {  // S = Q K_j^T
+            const int s = 2 * j % kStages;
+            if (!all(filled(2 * j))) return false;
+            ptx::tc_fence_after();
+            if (ptx::elect_one()) {
+                const uint64_t kd = k_desc + (uint64_t)(s * (C::kTileBytes >> 4));
+#pragma unroll
+                for (int k = 0; k < D / 16; ++k) {
+                    constexpr int kBlock16 = C::kBlockBytes >> 4;
+                    const int off = (k >> 2) * kBlock16 + (k & 3) * 2;
+                    ptx::mma_f16_ss(s_tmem, q_desc + off, kd + off, idesc_s, k > 0);
+                }
+                ptx::mma_commit(&s_full[i]);
+                ptx::mma_commit(&empty[s]);
+            }
+            __syncwarp();
+            return true;
+        };
+        auto output = [&](int j) {  // O += P V_j
+            const int s = (2 * j + 1) % kStages;
+            if (!all(filled(2 * j + 1))) return false;
+            ptx::tc_fence_after();
+            if (ptx::elect_one()) {
+                const uint64_t vd = v_desc + (uint64_t)(s * (C::kTileBytes >> 4));
+#pragma unroll
+                for (int k = 0; k < kKeys / 16; ++k)
+                    ptx::mma_f16_ts(o_tmem, s_tmem + k * 8, vd + k * (2048 >> 4), idesc_o, j > 0 || k > 0);
+                ptx::mma_commit(&empty[s]);
+                if (j + 1 == tiles) ptx::mma_commit(&o_full[i]);
+            }
+            __syncwarp();
+            return true;
+        };
+        // The tiles take turns: O_0, S_0, O_1, S_1, ...  Issued at will, the two tiles' MMAs interleave, both
+        // softmaxes get their logits at the same time, and the tensor cores idle while both run.
+        auto my_turn = [&](int n) { return ptx::mbar_wait(&turn[i], n & 1, kWaitNs, abort_flag); };
+        if (issuer && tiles > 0) {
+            ok = all(ptx::mbar_wait(&q_full[i], 0, kWaitNs, abort_flag) && (i == 0 || my_turn(0)));
+            if (ok) ok = logits(0);
+            if (lane == 0) ptx::mbar_arrive(&turn[i ^ 1]);
+        }
 
         const float mul = p.scale_log2 * pow2f(q_exp) * pow2f(k_exp);
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t s_addr = tmem + lanes + i * kKeys, o_addr = tmem + lanes + C::kColO + i * D;
         float m = -INFINITY;
-        float l0 = 0.f, l1 = 0.f;  // sums of the even and odd columns' weights
+        float2 l0 = make_float2(0.f, 0.f), l1 = l0;  // sums of every fourth column's weights
         for (int j = 0; j < tiles && ok; ++j) {
             ok = ptx::mbar_wait(&s_full[i], j & 1, kWaitNs, abort_flag);
             ok = __all_sync(0xffffffffu, ok);
@@ -244,17 +304,17 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
             float tops[4];
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
-                tops[c] = __uint_as_float(s[c][0]);
+                tops[c] = max3(__uint_as_float(s[c][0]), __uint_as_float(s[c][1]), __uint_as_float(s[c][2]));
 #pragma unroll
-                for (int k = 1; k < 32; ++k) tops[c] = fmaxf(tops[c], __uint_as_float(s[c][k]));
+                for (int k = 3; k < 31; k += 2) tops[c] = max3(tops[c], __uint_as_float(s[c][k]), __uint_as_float(s[c][k + 1]));
+                tops[c] = fmaxf(tops[c], __uint_as_float(s[c][31]));
             }
             const float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3])) * mul;  // mul > 0
             if (__any_sync(0xffffffffu, top > m + kLazy)) {
                 const float to = fmaxf(m, top);
                 const float f = to == -INFINITY ? 1.f : exp2_fast(m - to);
                 m = to;
-                l0 *= f;
-                l1 *= f;
+                l0.x *= f, l0.y *= f, l1.x *= f, l1.y *= f;
                 if (j > 0) {  // the logits came after the last product of this tile was complete
                     uint32_t o[16];
                     __syncwarp();
@@ -278,10 +338,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
 #pragma unroll
                 for (int k = 0; k < 16; ++k) {
                     const float2 z = fma2(make_float2(__uint_as_float(s[c][2 * k]), __uint_as_float(s[c][2 * k + 1])), mul, -ref);
-                    const float a = exp2_fast(z.x), e = exp2_fast(z.y);
-                    l0 += a;
-                    l1 += e;
-                    w[k] = pack2<true>(a, e);
+                    const float2 e = make_float2(exp2_fast(z.x), exp2_fast(z.y));
+                    if (k & 1) l1 = __fadd2_rn(l1, e); else l0 = __fadd2_rn(l0, e);
+                    w[k] = pack2<true>(e.x, e.y);
                 }
                 ptx::tmem_st_16(s_addr + c * 16, w);  // over S, all of which is in registers
             }
@@ -289,8 +348,19 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
             ptx::tc_fence_before();
             __syncwarp();
             if (lane == 0) ptx::mbar_arrive(&p_full[i]);
+            if (issuer) {
+                ok = all(ptx::mbar_wait(&p_full[i], j & 1, kWaitNs, abort_flag) && my_turn(j + i));
+                if (ok) ok = output(j);
+                if (ok && j + 1 < tiles) ok = logits(j + 1);
+                if (lane == 0) ptx::mbar_arrive(&turn[i ^ 1]);
+            }
         }
-        const float l = l0 + l1;
+        if (!ok && issuer) {  // nothing of this block may still run when its TMEM is freed
+            if (ptx::elect_one()) ptx::mma_commit(&drain[i]);
+            int zero = 0;
+            ptx::mbar_wait(&drain[i], 0, kWaitNs, &zero);
+        }
+        const float l = l0.x + l0.y + (l1.x + l1.y);
         if (ok && tiles > 0) ok = ptx::mbar_wait(&o_full[i], 0, kWaitNs, abort_flag);
         ok = __all_sync(0xffffffffu, ok);
         if (ok) {
@@ -317,61 +387,41 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
         }
     } else {
         regs_down<kOtherRegs>();
-        if (warp < kMmaWarp) {
         // ------------------------------------------------------------- K and V, widened --
-        // A unit is 8 rows x 64 codes, one load of a warp: lane = 4 * row + 16-code piece, so that the
-        // two 16-byte stores of 8 lanes fall on all the banks.  A unit's registers take the next
-        // tile's codes as soon as they are widened: their latency runs under the other units and
-        // the wait for the next stage.
-        constexpr int kUnits = kKeys / 8 * C::kBlocks;
-        constexpr int kLoads = (kUnits + kConvWarps - 1) / kConvWarps;
-        const int cw = warp - kConvWarp0, piece = lane & 3, sub = lane >> 2;
-        // lane x holds the page (with the head: page * KH + head) of keys x P .. of a tile, and the
-        // factors 2^(exponent - the block's largest) of its codes
-        auto page_at = [&](int tile) {
-            const int key = (tile0 + tile) * kKeys + (lane << v.log_p);
+        // Warp w owns keys 16 w .. 16 w + 15 of every tile: they lie in one page.  A load takes 8 rows x 64
+        // codes: lane = 4 * row + 16-code piece, so that the two 16-byte stores of 8 lanes fall on
+        // all the banks.  The registers of a tile's codes take the next tile's as soon as they are
+        // widened, so a load has a whole tile's time to arrive.
+        constexpr int kLoads = 2 * C::kBlocks;
+        const int cw = warp - kSoftWarps, piece = lane & 3, sub = lane >> 2;
+        auto page_at = [&](int tile) {  // page * KH + head
+            const int key = (tile0 + tile) * kKeys + cw * 16;
             int page = 0;
-            if (lane < (kKeys >> v.log_p) && key < q.kv && tile < tiles) page = __ldg(table + (key >> v.log_p));
+            if (key < key_hi) page = __ldg(table + (key >> v.log_p));
             return (page < 0 || page >= v.n_pages ? 0 : page) * v.KH + head;  // (reported above)
         };
-        auto factor = [&](float scale, int largest) {
-            const int e = min(exponent_of(scale) - largest, 0);  // (lanes without a page)
+        auto factor = [&](float scale, int largest) {  // 2^(exponent - the block's largest)
+            const int e = min(exponent_of(scale) - largest, 0);  // (past the end: any page)
             const __half2 f = __float2half2_rn(e < -24 ? 0.f : pow2f(e));
             return *reinterpret_cast<const uint32_t *>(&f);
         };
-        uint4 raw[kLoads];
         const int log_pd = v.log_p + (D == 128 ? 7 : 6);
-        auto load = [&](int n, int tile, int pages, const uint8_t *codes) {
-            const int unit = n * kConvWarps + cw, row = unit / C::kBlocks * 8 + sub;
-            const int page = __shfl_sync(0xffffffffu, pages, row >> v.log_p);
-            raw[n] = make_uint4(0, 0, 0, 0);
-            if (unit < kUnits && (tile0 + tile) * kKeys + row < q.kv)  // slots past the end hold anything
-                raw[n] = __ldg(reinterpret_cast<const uint4 *>(
-                    codes + ((uint64_t)(uint32_t)page << log_pd) + (row & (v.P - 1)) * D + unit % C::kBlocks * 64 + piece * 16));
-        };
-        int page0 = page_at(0), page1 = page_at(1), page2 = page_at(2);
-        uint32_t fk = factor(__ldg(v.k_scale + page0), k_exp), fv = factor(__ldg(v.v_scale + page0), v_exp);
-        float sk1 = __ldg(v.k_scale + page1), sv1 = __ldg(v.v_scale + page1);
-#pragma unroll
-        for (int n = 0; n < kLoads; ++n)
-            if (tiles > 0) load(n, 0, page0, v.k_codes);
-        for (int it = 0; it < 2 * tiles; ++it) {
-            const bool is_v = it & 1;
-            const int tile = it >> 1, s = it % kStages;
-            if (it >= kStages) {
-                ok = ptx::mbar_wait(&empty[s], (it / kStages - 1) & 1, kWaitNs, abort_flag);
-                ok = __all_sync(0xffffffffu, ok);
-                if (!ok) break;
-            }
-            uint8_t *st = kv_smem + s * C::kTileBytes;
-            const uint32_t f_lane = is_v ? fv : fk;
-            const uint8_t *codes = is_v ? v.k_codes : v.v_codes;  // of the next stage
-            const int next_tile = tile + (is_v ? 1 : 0), next_page = is_v ? page1 : page0;
+        auto load = [&](uint4 (&raw)[kLoads], int tile, int page, const uint8_t *codes) {
+            const int key0 = (tile0 + tile) * kKeys + cw * 16;
+            const uint8_t *src = codes + ((uint64_t)(uint32_t)page << log_pd) + ((key0 & (v.P - 1)) + sub) * D + piece * 16;
 #pragma unroll
             for (int n = 0; n < kLoads; ++n) {
-                const int unit = n * kConvWarps + cw, row = unit / C::kBlocks * 8 + sub;
-                // the 8 rows lie in one page, so the factor is the same for the whole warp
-                const uint32_t f = __shfl_sync(0xffffffffu, f_lane, row >> v.log_p);
+                raw[n] = make_uint4(0, 0, 0, 0);
+                if (key0 + n / C::kBlocks * 8 + sub < key_hi)  // slots past the end hold anything
+                    raw[n] = __ldg(reinterpret_cast<const uint4 *>(src + n / C::kBlocks * 8 * D + n % C::kBlocks * 64));
+            }
+        };
+        const uint32_t row_off = (uint32_t)(cw * 16 + sub) * 128;
+        const uint32_t off0 = row_off + (((2 * piece) ^ sub) << 4), off1 = row_off + (((2 * piece + 1) ^ sub) << 4);
+        auto widen = [&](const uint4 (&raw)[kLoads], int it, uint32_t f) {
+            uint8_t *st = kv_smem + it % kStages * C::kTileBytes;
+#pragma unroll
+            for (int n = 0; n < kLoads; ++n) {
                 const uint32_t w[4] = {raw[n].x, raw[n].y, raw[n].z, raw[n].w};
                 uint32_t h[8];
 #pragma unroll
@@ -379,78 +429,40 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
                     h[2 * k] = mul2(widen2(w[k] & 0xffffu), f);
                     h[2 * k + 1] = mul2(widen2(w[k] >> 16), f);
                 }
-                if (unit < kUnits) {
-                    uint8_t *dst = st + unit % C::kBlocks * C::kBlockBytes + row * 128;
-                    *reinterpret_cast<uint4 *>(dst + (((2 * piece) ^ (row & 7)) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
-                    *reinterpret_cast<uint4 *>(dst + (((2 * piece + 1) ^ (row & 7)) << 4)) = make_uint4(h[4], h[5], h[6], h[7]);
-                }
-                if (next_tile < tiles) load(n, next_tile, next_page, codes);
+                uint8_t *dst = st + n % C::kBlocks * C::kBlockBytes + n / C::kBlocks * 8 * 128;
+                *reinterpret_cast<uint4 *>(dst + off0) = make_uint4(h[0], h[1], h[2], h[3]);
+                *reinterpret_cast<uint4 *>(dst + off1) = make_uint4(h[4], h[5], h[6], h[7]);
             }
+        };
+        auto free_stage = [&](int it) {
+            bool f = it < kStages || ptx::mbar_wait(&empty[it % kStages], (it / kStages - 1) & 1, kWaitNs, abort_flag);
+            return __all_sync(0xffffffffu, f) != 0;
+        };
+        auto publish = [&](int it) {
             ptx::fence_proxy_async_smem();
             __syncwarp();
-            if (lane == 0) ptx::mbar_arrive(&full[s]);
-            if (is_v) {
-                fk = factor(sk1, k_exp), fv = factor(sv1, v_exp);
-                page0 = page1, page1 = page2;
-                sk1 = __ldg(v.k_scale + page1), sv1 = __ldg(v.v_scale + page1);
-                page2 = page_at(tile + 3);
-            }
-        }
-        } else if (lane == 0 && tiles > 0) {
-        // ---------------------------------------------------------------------- the MMAs --
-        const uint32_t idesc_s = ptx::idesc_f16_f32(kRowTile, kKeys, false);
-        const uint32_t idesc_o = ptx::idesc_f16_f32(kRowTile, D, true);
-        const uint32_t q_addr = ptx::smem_u32(q_smem), kv_addr = ptx::smem_u32(kv_smem);
-        auto logits = [&](int i, int s) {
-#pragma unroll
-            for (int k = 0; k < D / 16; ++k) {
-                const uint32_t off = (uint32_t)((k >> 2) * C::kBlockBytes + (k & 3) * 32);
-                ptx::mma_f16_ss(tmem + i * kKeys, ptx::sw128_desc(q_addr + i * C::kTileBytes + off),
-                                ptx::sw128_desc(kv_addr + s * C::kTileBytes + off), idesc_s, k > 0);
-            }
+            if (lane == 0) ptx::mbar_arrive(&full[it % kStages]);
         };
-        auto output = [&](int i, int s, bool more) {
-#pragma unroll
-            for (int k = 0; k < kKeys / 16; ++k)
-                ptx::mma_f16_ts(tmem + C::kColO + i * D, tmem + i * kKeys + k * 8,
-                                ptx::sw128_desc_mn(kv_addr + s * C::kTileBytes + k * 2048, C::kBlockBytes), idesc_o,
-                                more || k > 0);
-        };
-        auto filled = [&](int it) { return ptx::mbar_wait(&full[it % kStages], (it / kStages) & 1, kWaitNs, abort_flag); };
-        ok = ptx::mbar_wait(q_full, 0, kWaitNs, abort_flag) && filled(0);
-        if (ok) {
-            ptx::tc_fence_after();
-            for (int i = 0; i < 2; ++i) {
-                logits(i, 0);
-                ptx::mma_commit(&s_full[i]);
-            }
-            ptx::mma_commit(&empty[0]);
+        uint4 rk[kLoads], rv[kLoads];
+        int page1 = page_at(0), page2 = page_at(1);
+        float sk = __ldg(v.k_scale + page1), sv = __ldg(v.v_scale + page1);
+        if (tiles > 0) {
+            load(rk, 0, page1, v.k_codes);
+            load(rv, 0, page1, v.v_codes);
         }
-        for (int j = 0; j < tiles && ok; ++j) {
-            const int vs = (2 * j + 1) % kStages, ks = (2 * j + 2) % kStages;
-            const bool next = j + 1 < tiles;
-            ok = filled(2 * j + 1);
-            for (int i = 0; i < 2 && ok; ++i) {
-                ok = ptx::mbar_wait(&p_full[i], j & 1, kWaitNs, abort_flag);
-                if (!ok) break;
-                ptx::tc_fence_after();
-                output(i, vs, j > 0);
-                if (!next) ptx::mma_commit(&o_full[i]);
-                if (i == 1) ptx::mma_commit(&empty[vs]);
-                if (!next) continue;
-                if (i == 0) ok = filled(2 * j + 2);
-                if (!ok) break;
-                ptx::tc_fence_after();
-                logits(i, ks);
-                ptx::mma_commit(&s_full[i]);
-                if (i == 1) ptx::mma_commit(&empty[ks]);
-            }
-        }
-        if (!ok) {  // nothing of this block may still run when its TMEM is freed
-            ptx::mma_commit(drain);
-            int zero = 0;
-            ptx::mbar_wait(drain, 0, kWaitNs, &zero);
-        }
+        for (int j = 0; j < tiles; ++j) {
+            const uint32_t fk = factor(sk, k_exp), fv = factor(sv, v_exp);
+            page1 = page2;  // of tile j + 1
+            sk = __ldg(v.k_scale + page1), sv = __ldg(v.v_scale + page1);
+            page2 = page_at(j + 2);
+            if (!(ok = free_stage(2 * j))) break;
+            widen(rk, 2 * j, fk);
+            if (j + 1 < tiles) load(rk, j + 1, page1, v.k_codes);
+            publish(2 * j);
+            if (!(ok = free_stage(2 * j + 1))) break;
+            widen(rv, 2 * j + 1, fv);
+            if (j + 1 < tiles) load(rv, j + 1, page1, v.v_codes);
+            publish(2 * j + 1);
         }
     }
     if (!ok) {
@@ -461,7 +473,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
     ptx::tc_fence_before();
     __syncthreads();
     ptx::tc_fence_after();
-    if (warp == kMmaWarp) ptx::tmem_dealloc(tmem, C::kCols);
+    if (warp == 0) ptx::tmem_dealloc(tmem, C::kCols);
 }
 
 template <int D, bool F16>
