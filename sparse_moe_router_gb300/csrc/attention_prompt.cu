@@ -17,8 +17,9 @@
 // will meet (exact in fp16 unless a page is 2^-15 below it, and then off by at most 2^-25 of the
 // largest), so one factor a row holds for all keys.
 //
-// Roles: warps 0-3 and 4-7 are row tiles 0 and 1, one row a thread; a thread of each also issues its
-// tile's MMAs, so the hand-over from weights to products is one barrier.  Warps 8-15 widen K and V.  Row maxima move lazily: a row's reference changes only when a
+// Roles: warps 0-7 do the softmax of both row tiles in turn, two threads a row (64 columns each: half
+// the time from logits to weights, and no warp waits for the tensor cores' turn); warps 8-15 widen K
+// and V; warp 16 issues the MMAs.  Row maxima move lazily: a row's reference changes only when a
 // logit passes it by 2^8 (weights stay below 256), so O is rarely rescaled, by the thread that
 // owns the row.
 #include "layer.h"
@@ -30,11 +31,12 @@ namespace {
 constexpr int kRowTile = 128, kRowsBlock = 2 * kRowTile;
 constexpr int kKeys = 128;  // keys a tile
 constexpr int kStages = 4;  // K and V tiles in flight, in the order K0 V0 K1 V1 ...
-constexpr int kSoftWarps = 8, kConvWarps = 8;
-constexpr int kThreads = (kSoftWarps + kConvWarps) * 32;
-// Registers a thread: 128 at launch (four warps a scheduler); the softmax warps hold a row's 128
-// logits and take 2 x 168 of a scheduler's 4 x 128, the others keep 88.
-constexpr int kSoftRegs = 168, kOtherRegs = 88;
+constexpr int kSoftWarps = 8, kConvWarps = 8, kMmaWarp = 16;
+constexpr int kThreads = 20 * 32;  // (three warps beside the MMA warp only complete its warpgroup)
+// Registers a thread: 96 at launch (five warps a scheduler); of a scheduler's 5 x 96 the two softmax
+// warps, which hold 64 logits a thread, take 2 x 136, the converters 2 x 80, the MMA warp 40.
+constexpr int kLaunchRegs = 96, kSoftRegs = 136, kConvRegs = 80, kMmaRegs = 40;
+static_assert(8 * kSoftRegs + 8 * kConvRegs + 4 * kMmaRegs <= 20 * kLaunchRegs, "more registers than the block has");
 constexpr uint64_t kWaitNs = 2000000000ull;  // 2 s: far above any legitimate wait
 constexpr float kLazy = 8.f;
 
@@ -43,7 +45,8 @@ struct Prompt {
     static constexpr int kBlocks = D / 64;                    // 128-byte column blocks of a row
     static constexpr int kBlockBytes = kKeys * 128;           // one column block of a 128-row tile
     static constexpr int kTileBytes = kBlocks * kBlockBytes;  // a tile of Q, K or V
-    static constexpr int kSmem = 1024 + (2 + kStages) * kTileBytes + 256;
+    // 1 KB to align, the tiles, barriers and holders, q exponents, exchanged maxima and flags
+    static constexpr int kSmem = 1024 + (2 + kStages) * kTileBytes + 256 + kRowsBlock * 8 + 64;
     static constexpr uint32_t kColO = 2 * kKeys;              // TMEM: S0 S1 O0 O1
     static constexpr uint32_t kCols = 512;
 };
@@ -78,6 +81,19 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
     asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
     return r;
 }
+// Whether `x` holds in any thread of the two warps of a lane quarter; a barrier of the two.
+__device__ __forceinline__ bool any_of_pair(int quarter, bool x) {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.u32 p, %1, 0;\n\t"
+        "bar.red.or.pred q, %2, 64, p;\n\t"
+        "selp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(r)
+        : "r"((uint32_t)x), "r"(2 + quarter)
+        : "memory");
+    return r != 0;
+}
 template <int R>
 __device__ __forceinline__ void regs_up() {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R));
@@ -105,12 +121,14 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
     uint64_t *s_full = empty + kStages;              // [2] logits of a row tile are in TMEM
     uint64_t *p_full = s_full + 2;                   // [2] its weights are
     uint64_t *o_full = p_full + 2;                   // [2] its output is complete
-    uint64_t *q_full = o_full + 2;                   // [2] its queries are in shared memory
-    uint64_t *drain = q_full + 2;                    // [2]
-    uint64_t *turn = drain + 2;                      // [2] the row tile may issue its next MMAs
-    uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(turn + 2);
+    uint64_t *q_full = o_full + 2;
+    uint64_t *drain = q_full + 1;
+    uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(drain + 1);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_holder + 1);
-    int *max_exp = reinterpret_cast<int *>(tmem_holder + 2);  // [2] of K and V
+    int *max_exp = reinterpret_cast<int *>(tmem_holder + 2);              // [2] of K and V
+    int *q_exps = reinterpret_cast<int *>(reinterpret_cast<uint8_t *>(bars) + 256);  // [256] of the rows
+    float *ex_val = reinterpret_cast<float *>(q_exps + kRowsBlock);       // [2 halves][128]
+    int *ex_dead = reinterpret_cast<int *>(ex_val + kRowsBlock);          // [8 warps]
 
     const int tid = (int)threadIdx.x, lane = tid & 31;
     const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);  // known to be the same in all lanes
@@ -140,21 +158,20 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
     if (tid == 0) {
         for (int s = 0; s < kStages; ++s) {
             ptx::mbar_init(&full[s], kConvWarps);
-            ptx::mbar_init(&empty[s], 2);  // both row tiles are done with it
+            ptx::mbar_init(&empty[s], 1);
         }
         for (int i = 0; i < 2; ++i) {
             ptx::mbar_init(&s_full[i], 1);
-            ptx::mbar_init(&p_full[i], 4);
+            ptx::mbar_init(&p_full[i], kSoftWarps);
             ptx::mbar_init(&o_full[i], 1);
-            ptx::mbar_init(&q_full[i], 4);
-            ptx::mbar_init(&drain[i], 1);
-            ptx::mbar_init(&turn[i], 1);
         }
+        ptx::mbar_init(q_full, kSoftWarps);
+        ptx::mbar_init(drain, 1);
         *abort_flag = 0;
         max_exp[0] = max_exp[1] = -127;
         ptx::fence_mbar_init();
     }
-    if (warp == 0) ptx::tmem_alloc(tmem_holder, C::kCols);
+    if (warp == kMmaWarp) ptx::tmem_alloc(tmem_holder, C::kCols);
     ptx::tc_fence_before();
     __syncthreads();
     ptx::tc_fence_after();
@@ -185,215 +202,184 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
 
     if (warp < kSoftWarps) {
         regs_up<kSoftRegs>();
-        // ----------------------------------------------------------------- softmax, rows --
-        const int i = warp >> 2;                        // row tile
-        const int r = i * kRowTile + (warp & 3) * 32 + lane;  // row of the block = TMEM lane of tile i
-        const bool live = r < rows;
-        const int tok = (row0 + r) / v.G, qh = head * v.G + (row0 + r) % v.G;
-        const int pos = first_pos + tok;
-        const int hi = p.causal ? min(q.kv, pos + 1) : q.kv;
-        const int lo = p.window > 0 ? max(0, pos + 1 - p.window) : 0;
-        // Q: the row scaled by a power of two into [1, 2) at its largest, as fp16, K-major swizzled
-        const int rr = r & (kRowTile - 1);
-        uint8_t *dst = q_smem + i * C::kTileBytes + rr * 128;
-        float amax = 0.f;
-        uint4 qv[D / 8];
-        const uint16_t *src = p.q + (int64_t)(q.q0 + tok) * p.q_ld + (int64_t)qh * D;
+        // ---------------------------------------------------------------------- softmax --
+        // Q first: thread t brings row t of the block, scaled by a power of two into [1, 2) at its
+        // largest, as fp16, K-major swizzled.
+        {
+            const int r = tid, rr = r & (kRowTile - 1);
+            const int tok = (row0 + r) / v.G, qh = head * v.G + (row0 + r) % v.G;
+            const uint16_t *src = p.q + (int64_t)(q.q0 + tok) * p.q_ld + (int64_t)qh * D;
+            uint8_t *dst = q_smem + (r >> 7) * C::kTileBytes + rr * 128;
+            float amax = 0.f;
 #pragma unroll
-        for (int c = 0; c < D / 8; ++c) {
-            qv[c] = live ? *reinterpret_cast<const uint4 *>(src + c * 8) : make_uint4(0, 0, 0, 0);
+            for (int c = 0; c < D / 8; ++c) {
+                float f[8];
+                unpack8<F16>(r < rows ? *reinterpret_cast<const uint4 *>(src + c * 8) : make_uint4(0, 0, 0, 0), f);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) amax = fmaxf(amax, fabsf(f[j]));
+            }
+            const int q_exp = amax > 0.f ? max(min((int)(__float_as_uint(amax) >> 23) - 127, 126), -126) : 0;
+            const float q_inv = pow2f(-q_exp);
+#pragma unroll
+            for (int c = 0; c < D / 8; ++c) {
+                float f[8];
+                unpack8<F16>(r < rows ? *reinterpret_cast<const uint4 *>(src + c * 8) : make_uint4(0, 0, 0, 0), f);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) f[j] *= q_inv;
+                *reinterpret_cast<uint4 *>(dst + (c >> 3) * C::kBlockBytes + (((c & 7) ^ (rr & 7)) << 4)) = pack8<true>(f);
+            }
+            q_exps[r] = q_exp;
+            ptx::fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(q_full);
         }
-#pragma unroll
-        for (int c = 0; c < D / 8; ++c) {
-            float f[8];
-            unpack8<F16>(qv[c], f);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) amax = fmaxf(amax, fabsf(f[j]));
-        }
-        const int q_exp = amax > 0.f ? max(min((int)(__float_as_uint(amax) >> 23) - 127, 126), -126) : 0;
-        const float q_inv = pow2f(-q_exp);
-#pragma unroll
-        for (int c = 0; c < D / 8; ++c) {
-            float f[8];
-            unpack8<F16>(qv[c], f);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) f[j] *= q_inv;
-            *reinterpret_cast<uint4 *>(dst + (c >> 3) * C::kBlockBytes + (((c & 7) ^ (rr & 7)) << 4)) = pack8<true>(f);
-        }
-        ptx::fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(&q_full[i]);
+        ptx::named_bar(1, kSoftWarps * 32);
 
-        // --------------------------------------- the MMAs, by one warp of each row tile --
-        const bool issuer = (warp & 3) == 0;
-        const uint32_t idesc_s = ptx::idesc_f16_f32(kRowTile, kKeys, false);
-        const uint32_t idesc_o = ptx::idesc_f16_f32(kRowTile, D, true);
-        const uint32_t s_tmem = tmem + i * kKeys, o_tmem = tmem + C::kColO + i * D;
-        const uint64_t q_desc = ptx::sw128_desc(ptx::smem_u32(q_smem) + i * C::kTileBytes);
-        const uint64_t k_desc = ptx::sw128_desc(ptx::smem_u32(kv_smem));
-        const uint64_t v_desc = ptx::sw128_desc_mn(ptx::smem_u32(kv_smem), C::kBlockBytes);
-        auto all = [](bool x) { return __all_sync(0xffffffffu, x) != 0; };
-        auto filled = [&](int it) { return ptx::mbar_wait(&full[it % kStages], (it / kStages) & 1, kWaitNs, abort_flag); };
-        auto logits = [&](int j) {  // S = Q K_j^T
-            const int s = 2 * j % kStages;
-            if (!all(filled(2 * j))) return false;
-            ptx::tc_fence_after();
-            if (ptx::elect_one()) {
-                const uint64_t kd = k_desc + (uint64_t)(s * (C::kTileBytes >> 4));
+        // Warps w and w + 4 share the 32 rows of TMEM lane quarter w % 4 of both row tiles: the first takes
+        // columns 0-63 of the logits, the second 64-127.
+        const int half = warp >> 2, quarter = warp & 3, rr = quarter * 32 + lane;
+        const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
+        float mul[2], m[2] = {-INFINITY, -INFINITY};
+        float2 l[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+        int lo[2], hi[2];
+        bool live[2];
 #pragma unroll
-                for (int k = 0; k < D / 16; ++k) {
-                    constexpr int kBlock16 = C::kBlockBytes >> 4;
-                    const int off = (k >> 2) * kBlock16 + (k & 3) * 2;
-                    ptx::mma_f16_ss(s_tmem, q_desc + off, kd + off, idesc_s, k > 0);
+        for (int i = 0; i < 2; ++i) {
+            const int r = i * kRowTile + rr, pos = first_pos + (row0 + r) / v.G;
+            live[i] = r < rows;
+            hi[i] = p.causal ? min(q.kv, pos + 1) : q.kv;
+            lo[i] = p.window > 0 ? max(0, pos + 1 - p.window) : 0;
+            mul[i] = p.scale_log2 * pow2f(q_exps[r]) * pow2f(k_exp);
+        }
+        bool dead = false;
+        for (int j = 0; j < tiles && !dead; ++j) {
+            const int key0 = (tile0 + j) * kKeys + half * 64;
+#pragma unroll
+            for (int i = 0; i < 2 && !dead; ++i) {
+                const uint32_t s_addr = tmem + lanes + i * kKeys, o_addr = tmem + lanes + C::kColO + i * D + half * (D / 2);
+                if (!ptx::mbar_wait(&s_full[i], j & 1, kWaitNs, abort_flag)) ok = false;
+                const bool stop = __any_sync(0xffffffffu, !ok) || *abort_flag;
+                ptx::tc_fence_after();
+                uint32_t s[2][32];
+                ptx::tmem_ld_32(s_addr + half * 64, s[0]);
+                ptx::tmem_ld_32(s_addr + half * 64 + 32, s[1]);
+                ptx::tmem_ld_wait();
+                tie32(s[0]);
+                tie32(s[1]);
+                if (__any_sync(0xffffffffu, live[i] && (key0 < lo[i] || key0 + 64 > hi[i]))) {
+                    const int c_lo = lo[i] - key0, c_hi = hi[i] - key0;
+#pragma unroll
+                    for (int c = 0; c < 2; ++c)
+#pragma unroll
+                        for (int k = 0; k < 32; ++k)
+                            if (c * 32 + k < c_lo || c * 32 + k >= c_hi) s[c][k] = 0xff800000u;  // -inf
                 }
-                ptx::mma_commit(&s_full[i]);
-                ptx::mma_commit(&empty[s]);
-            }
-            __syncwarp();
-            return true;
-        };
-        auto output = [&](int j) {  // O += P V_j
-            const int s = (2 * j + 1) % kStages;
-            if (!all(filled(2 * j + 1))) return false;
-            ptx::tc_fence_after();
-            if (ptx::elect_one()) {
-                const uint64_t vd = v_desc + (uint64_t)(s * (C::kTileBytes >> 4));
+                float tops[4];
 #pragma unroll
-                for (int k = 0; k < kKeys / 16; ++k)
-                    ptx::mma_f16_ts(o_tmem, s_tmem + k * 8, vd + k * (2048 >> 4), idesc_o, j > 0 || k > 0);
-                ptx::mma_commit(&empty[s]);
-                if (j + 1 == tiles) ptx::mma_commit(&o_full[i]);
-            }
-            __syncwarp();
-            return true;
-        };
-        // The tiles take turns: O_0, S_0, O_1, S_1, ...  Issued at will, the two tiles' MMAs interleave, both
-        // softmaxes get their logits at the same time, and the tensor cores idle while both run.
-        auto my_turn = [&](int n) { return ptx::mbar_wait(&turn[i], n & 1, kWaitNs, abort_flag); };
-        if (issuer && tiles > 0) {
-            ok = all(ptx::mbar_wait(&q_full[i], 0, kWaitNs, abort_flag) && (i == 0 || my_turn(0)));
-            if (ok) ok = logits(0);
-            if (lane == 0) ptx::mbar_arrive(&turn[i ^ 1]);
-        }
-
-        const float mul = p.scale_log2 * pow2f(q_exp) * pow2f(k_exp);
-        const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-        const uint32_t s_addr = tmem + lanes + i * kKeys, o_addr = tmem + lanes + C::kColO + i * D;
-        float m = -INFINITY;
-        float2 l0 = make_float2(0.f, 0.f), l1 = l0;  // sums of every fourth column's weights
-        for (int j = 0; j < tiles && ok; ++j) {
-            ok = ptx::mbar_wait(&s_full[i], j & 1, kWaitNs, abort_flag);
-            ok = __all_sync(0xffffffffu, ok);
-            if (!ok) break;
-            ptx::tc_fence_after();
-            const int key0 = (tile0 + j) * kKeys;
-            uint32_t s[4][32];
+                for (int c = 0; c < 4; ++c) {
+                    const uint32_t *x = &s[c >> 1][(c & 1) * 16];
+                    tops[c] = __uint_as_float(x[0]);
 #pragma unroll
-            for (int c = 0; c < 4; ++c) ptx::tmem_ld_32(s_addr + c * 32, s[c]);
-            ptx::tmem_ld_wait();
+                    for (int k = 1; k < 15; k += 2) tops[c] = max3(tops[c], __uint_as_float(x[k]), __uint_as_float(x[k + 1]));
+                }
+                float top = max3(fmaxf(tops[0], __uint_as_float(s[0][15])), fmaxf(tops[1], __uint_as_float(s[0][31])),
+                                 max3(tops[2], tops[3], fmaxf(__uint_as_float(s[1][15]), __uint_as_float(s[1][31]))));
+                top *= mul[i];  // mul > 0
+                // One barrier of the two warps: both have read their logits (P will lie over them), and
+                // whether a row of either needs a new reference.
+                if (any_of_pair(quarter, stop || top > m[i] + kLazy)) {
+                    ex_val[half * kRowTile + rr] = top;
+                    if (lane == 0) ex_dead[warp] = stop;
+                    ptx::named_bar(2 + quarter, 64);
+                    dead = ex_dead[quarter] || ex_dead[quarter + 4];
+                    const float to = max3(m[i], ex_val[rr], ex_val[kRowTile + rr]);
+                    const float f = to == -INFINITY ? 1.f : exp2_fast(m[i] - to);
+                    m[i] = to;
+                    l[i].x *= f, l[i].y *= f;
+                    if (j > 0) {  // the logits came after the last product of this tile was complete
+                        uint32_t o[16];
 #pragma unroll
-            for (int c = 0; c < 4; ++c) tie32(s[c]);
-            if (__any_sync(0xffffffffu, live && (key0 < lo || key0 + kKeys > hi))) {
-                const int c_lo = lo - key0, c_hi = hi - key0;
+                        for (int c = 0; c < D / 32; ++c) {
+                            ptx::tmem_ld_16(o_addr + c * 16, o);
+                            ptx::tmem_ld_wait();
 #pragma unroll
-                for (int c = 0; c < 4; ++c)
-#pragma unroll
-                    for (int k = 0; k < 32; ++k)
-                        if (c * 32 + k < c_lo || c * 32 + k >= c_hi) s[c][k] = 0xff800000u;  // -inf
-            }
-            float tops[4];
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                tops[c] = max3(__uint_as_float(s[c][0]), __uint_as_float(s[c][1]), __uint_as_float(s[c][2]));
-#pragma unroll
-                for (int k = 3; k < 31; k += 2) tops[c] = max3(tops[c], __uint_as_float(s[c][k]), __uint_as_float(s[c][k + 1]));
-                tops[c] = fmaxf(tops[c], __uint_as_float(s[c][31]));
-            }
-            const float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3])) * mul;  // mul > 0
-            if (__any_sync(0xffffffffu, top > m + kLazy)) {
-                const float to = fmaxf(m, top);
-                const float f = to == -INFINITY ? 1.f : exp2_fast(m - to);
-                m = to;
-                l0.x *= f, l0.y *= f, l1.x *= f, l1.y *= f;
-                if (j > 0) {  // the logits came after the last product of this tile was complete
-                    uint32_t o[16];
-                    __syncwarp();
-#pragma unroll
-                    for (int c = 0; c < D / 16; ++c) {
-                        ptx::tmem_ld_16(o_addr + c * 16, o);
-                        ptx::tmem_ld_wait();
-#pragma unroll
-                        for (int k = 0; k < 16; ++k) {
-                            asm volatile("" : "+r"(o[k]));
-                            o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
+                            for (int k = 0; k < 16; ++k) {
+                                asm volatile("" : "+r"(o[k]));
+                                o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
+                            }
+                            ptx::tmem_st_16(o_addr + c * 16, o);
                         }
-                        ptx::tmem_st_16(o_addr + c * 16, o);
                     }
+                    ptx::named_bar(2 + quarter, 64);  // ex_* are free again
                 }
-            }
-            const float ref = m == -INFINITY ? 0.f : m;
+                const float ref = m[i] == -INFINITY ? 0.f : m[i];
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                uint32_t w[16];
+                for (int c = 0; c < 2; ++c) {
+                    uint32_t w[16];
 #pragma unroll
-                for (int k = 0; k < 16; ++k) {
-                    const float2 z = fma2(make_float2(__uint_as_float(s[c][2 * k]), __uint_as_float(s[c][2 * k + 1])), mul, -ref);
-                    const float2 e = make_float2(exp2_fast(z.x), exp2_fast(z.y));
-                    if (k & 1) l1 = __fadd2_rn(l1, e); else l0 = __fadd2_rn(l0, e);
-                    w[k] = pack2<true>(e.x, e.y);
+                    for (int k = 0; k < 16; ++k) {
+                        const float2 z =
+                            fma2(make_float2(__uint_as_float(s[c][2 * k]), __uint_as_float(s[c][2 * k + 1])), mul[i], -ref);
+                        const float2 e = make_float2(exp2_fast(z.x), exp2_fast(z.y));
+                        l[i] = __fadd2_rn(l[i], e);
+                        w[k] = pack2<true>(e.x, e.y);
+                    }
+                    ptx::tmem_st_16(s_addr + half * 32 + c * 16, w);
                 }
-                ptx::tmem_st_16(s_addr + c * 16, w);  // over S, all of which is in registers
-            }
-            ptx::tmem_st_wait();
-            ptx::tc_fence_before();
-            __syncwarp();
-            if (lane == 0) ptx::mbar_arrive(&p_full[i]);
-            if (issuer) {
-                ok = all(ptx::mbar_wait(&p_full[i], j & 1, kWaitNs, abort_flag) && my_turn(j + i));
-                if (ok) ok = output(j);
-                if (ok && j + 1 < tiles) ok = logits(j + 1);
-                if (lane == 0) ptx::mbar_arrive(&turn[i ^ 1]);
+                ptx::tmem_st_wait();
+                ptx::tc_fence_before();
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive(&p_full[i]);
             }
         }
-        if (!ok && issuer) {  // nothing of this block may still run when its TMEM is freed
-            if (ptx::elect_one()) ptx::mma_commit(&drain[i]);
-            int zero = 0;
-            ptx::mbar_wait(&drain[i], 0, kWaitNs, &zero);
-        }
-        const float l = l0.x + l0.y + (l1.x + l1.y);
-        if (ok && tiles > 0) ok = ptx::mbar_wait(&o_full[i], 0, kWaitNs, abort_flag);
-        ok = __all_sync(0xffffffffu, ok);
-        if (ok) {
+        // ---------------------------------------------------------------- output, normalised --
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            if (dead) break;
+            const int r = i * kRowTile + rr, tok = (row0 + r) / v.G, qh = head * v.G + (row0 + r) % v.G;
+            // row sums of the two halves
+            ex_val[half * kRowTile + rr] = l[i].x + l[i].y;
+            if (tiles > 0 && !ptx::mbar_wait(&o_full[i], 0, kWaitNs, abort_flag)) ok = false;
+            ptx::named_bar(2 + quarter, 64);
+            const float sum = ex_val[rr] + ex_val[kRowTile + rr];
+            ptx::named_bar(2 + quarter, 64);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) continue;
             ptx::tc_fence_after();
-            const float inv = (l > 0.f || l != l) && tiles > 0 ? pow2f(v_exp) / l : 0.f;
-            uint16_t *out = p.out + (int64_t)(q.q0 + tok) * p.out_ld + (int64_t)qh * D;
+            const float inv = (sum > 0.f || sum != sum) && tiles > 0 ? pow2f(v_exp) / sum : 0.f;
+            uint16_t *out = p.out + (int64_t)(q.q0 + tok) * p.out_ld + (int64_t)qh * D + half * (D / 2);
 #pragma unroll
-            for (int c = 0; c < D / 32; ++c) {
+            for (int c = 0; c < D / 64; ++c) {
                 uint32_t o[32];
                 __syncwarp();
                 if (tiles > 0) {
-                    ptx::tmem_ld_32(o_addr + c * 32, o);
+                    ptx::tmem_ld_32(tmem + lanes + C::kColO + i * D + half * (D / 2) + c * 32, o);
                     ptx::tmem_ld_wait();
+                    tie32(o);
                 }
 #pragma unroll
-                for (int k = 0; k < 4 && live; ++k) {
+                for (int k = 0; k < 4 && live[i]; ++k) {
                     float f[8];
 #pragma unroll
                     for (int x = 0; x < 8; ++x) f[x] = inv == 0.f ? 0.f : __uint_as_float(o[8 * k + x]) * inv;
                     *reinterpret_cast<uint4 *>(out + c * 32 + k * 8) = pack8<F16>(f);
                 }
             }
-            if (live && p.lse) p.lse[(int64_t)(q.q0 + tok) * v.QH + qh] = (m + log2f(l)) * 0.6931471805599453f;
+            if (live[i] && p.lse && half == 0) p.lse[(int64_t)(q.q0 + tok) * v.QH + qh] = (m[i] + log2f(sum)) * 0.6931471805599453f;
         }
-    } else {
-        regs_down<kOtherRegs>();
+        ok = ok && !dead;
+    } else if (warp < kMmaWarp) {
+        regs_down<kConvRegs>();
         // ------------------------------------------------------------- K and V, widened --
-        // Warp w owns keys 16 w .. 16 w + 15 of every tile: they lie in one page.  A load takes 8 rows x 64
-        // codes: lane = 4 * row + 16-code piece, so that the two 16-byte stores of 8 lanes fall on
-        // all the banks.  The registers of a tile's codes take the next tile's as soon as they are
-        // widened, so a load has a whole tile's time to arrive.
-        constexpr int kLoads = 2 * C::kBlocks;
-        const int cw = warp - kSoftWarps, piece = lane & 3, sub = lane >> 2;
+        // Warp w owns keys 16 w .. 16 w + 15 of every tile: they lie in one page.  A load takes whole rows,
+        // lane = 16-code piece of a row, so that it reads full lines; a piece's two 16-byte stores go
+        // out in the order that spreads 8 lanes over all the banks (at D = 128 the upper four pieces
+        // of a row, which lie in the next column block, store their second half first).  The registers of
+        // a tile's codes take the next tile's as soon as they are widened, so a load has a whole
+        // tile's time to arrive.
+        constexpr int kPieces = D / 16, kRowsLoad = 32 / kPieces, kLoads = 16 / kRowsLoad;
+        const int cw = warp - kSoftWarps, piece = lane % kPieces, sub = lane / kPieces;
+        const bool swap = piece >= 4;
         auto page_at = [&](int tile) {  // page * KH + head
             const int key = (tile0 + tile) * kKeys + cw * 16;
             int page = 0;
@@ -412,26 +398,29 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
 #pragma unroll
             for (int n = 0; n < kLoads; ++n) {
                 raw[n] = make_uint4(0, 0, 0, 0);
-                if (key0 + n / C::kBlocks * 8 + sub < key_hi)  // slots past the end hold anything
-                    raw[n] = __ldg(reinterpret_cast<const uint4 *>(src + n / C::kBlocks * 8 * D + n % C::kBlocks * 64));
+                if (key0 + n * kRowsLoad + sub < key_hi)  // slots past the end hold anything
+                    raw[n] = __ldg(reinterpret_cast<const uint4 *>(src + n * kRowsLoad * D));
             }
         };
-        const uint32_t row_off = (uint32_t)(cw * 16 + sub) * 128;
-        const uint32_t off0 = row_off + (((2 * piece) ^ sub) << 4), off1 = row_off + (((2 * piece + 1) ^ sub) << 4);
+        // offsets of a piece's first and second store, for rows whose number is below 4 modulo 8 (or any: D = 64)
+        const uint32_t base = (uint32_t)(piece >> 2) * C::kBlockBytes + (uint32_t)(cw * 16 + sub) * 128;
+        const uint32_t c0 = ((2 * (piece & 3) + (swap ? 1 : 0)) ^ sub) << 4, c1 = c0 ^ 16u;
         auto widen = [&](const uint4 (&raw)[kLoads], int it, uint32_t f) {
-            uint8_t *st = kv_smem + it % kStages * C::kTileBytes;
+            uint8_t *st = kv_smem + it % kStages * C::kTileBytes + base;
 #pragma unroll
             for (int n = 0; n < kLoads; ++n) {
-                const uint32_t w[4] = {raw[n].x, raw[n].y, raw[n].z, raw[n].w};
+                const uint32_t w[4] = {swap ? raw[n].z : raw[n].x, swap ? raw[n].w : raw[n].y, swap ? raw[n].x : raw[n].z,
+                                       swap ? raw[n].y : raw[n].w};
                 uint32_t h[8];
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
                     h[2 * k] = mul2(widen2(w[k] & 0xffffu), f);
                     h[2 * k + 1] = mul2(widen2(w[k] >> 16), f);
                 }
-                uint8_t *dst = st + n % C::kBlocks * C::kBlockBytes + n / C::kBlocks * 8 * 128;
-                *reinterpret_cast<uint4 *>(dst + off0) = make_uint4(h[0], h[1], h[2], h[3]);
-                *reinterpret_cast<uint4 *>(dst + off1) = make_uint4(h[4], h[5], h[6], h[7]);
+                const uint32_t flip = (n * kRowsLoad & 4) << 4;  // row bit 2 of the swizzle
+                uint8_t *dst = st + n * kRowsLoad * 128;
+                *reinterpret_cast<uint4 *>(dst + (c0 ^ flip)) = make_uint4(h[0], h[1], h[2], h[3]);
+                *reinterpret_cast<uint4 *>(dst + (c1 ^ flip)) = make_uint4(h[4], h[5], h[6], h[7]);
             }
         };
         auto free_stage = [&](int it) {
@@ -464,6 +453,74 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
             if (j + 1 < tiles) load(rv, j + 1, page1, v.v_codes);
             publish(2 * j + 1);
         }
+    }     else {
+        regs_down<kMmaRegs>();
+        if (warp == kMmaWarp && tiles > 0) {
+            // ------------------------------------------------------------------ the MMAs --
+            // In the order O_0 S_0 O_1 S_1 ...: while the tensor cores are at one row tile's output and next
+            // logits, the softmax warps are at the other's logits.
+            const uint32_t idesc_s = ptx::idesc_f16_f32(kRowTile, kKeys, false);
+            const uint32_t idesc_o = ptx::idesc_f16_f32(kRowTile, D, true);
+            const uint64_t q_desc = ptx::sw128_desc(ptx::smem_u32(q_smem));
+            const uint64_t k_desc = ptx::sw128_desc(ptx::smem_u32(kv_smem));
+            const uint64_t v_desc = ptx::sw128_desc_mn(ptx::smem_u32(kv_smem), C::kBlockBytes);
+            auto wait = [&](uint64_t *bar, int parity) {
+                return __all_sync(0xffffffffu, ptx::mbar_wait(bar, parity & 1, kWaitNs, abort_flag)) != 0;
+            };
+            auto logits = [&](int i, int j) {  // S = Q K_j^T
+                const int s = 2 * j % kStages;
+                if (ptx::elect_one()) {
+                    const uint64_t qd = q_desc + (uint64_t)(i * (C::kTileBytes >> 4));
+                    const uint64_t kd = k_desc + (uint64_t)(s * (C::kTileBytes >> 4));
+#pragma unroll
+                    for (int k = 0; k < D / 16; ++k) {
+                        constexpr int kBlock16 = C::kBlockBytes >> 4;
+                        const int off = (k >> 2) * kBlock16 + (k & 3) * 2;
+                        ptx::mma_f16_ss(tmem + i * kKeys, qd + off, kd + off, idesc_s, k > 0);
+                    }
+                    ptx::mma_commit(&s_full[i]);
+                    if (i == 1) ptx::mma_commit(&empty[s]);
+                }
+                __syncwarp();
+            };
+            auto output = [&](int i, int j) {  // O += P V_j
+                const int s = (2 * j + 1) % kStages;
+                if (ptx::elect_one()) {
+                    const uint64_t vd = v_desc + (uint64_t)(s * (C::kTileBytes >> 4));
+#pragma unroll
+                    for (int k = 0; k < kKeys / 16; ++k)
+                        ptx::mma_f16_ts(tmem + C::kColO + i * D, tmem + i * kKeys + k * 8, vd + k * (2048 >> 4), idesc_o,
+                                        j > 0 || k > 0);
+                    if (i == 1) ptx::mma_commit(&empty[s]);
+                    if (j + 1 == tiles) ptx::mma_commit(&o_full[i]);
+                }
+                __syncwarp();
+            };
+            auto filled = [&](int it) { return wait(&full[it % kStages], it / kStages); };
+            ok = wait(q_full, 0) && filled(0);
+            ptx::tc_fence_after();
+            if (ok) {
+                logits(0, 0);
+                logits(1, 0);
+            }
+            for (int j = 0; j < tiles && ok; ++j) {
+                ok = filled(2 * j + 1);
+                for (int i = 0; i < 2 && ok; ++i) {
+                    ok = wait(&p_full[i], j);
+                    ptx::tc_fence_after();
+                    if (ok) output(i, j);
+                    if (j + 1 == tiles || !ok) continue;
+                    if (i == 0) ok = filled(2 * j + 2);
+                    ptx::tc_fence_after();
+                    if (ok) logits(i, j + 1);
+                }
+            }
+            if (!ok) {  // nothing of this block may still run when its TMEM is freed
+                if (ptx::elect_one()) ptx::mma_commit(drain);
+                int zero = 0;
+                ptx::mbar_wait(drain, 0, kWaitNs, &zero);
+            }
+        }
     }
     if (!ok) {
         *abort_flag = 1;
@@ -473,7 +530,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
     ptx::tc_fence_before();
     __syncthreads();
     ptx::tc_fence_after();
-    if (warp == 0) ptx::tmem_dealloc(tmem, C::kCols);
+    if (warp == kMmaWarp) ptx::tmem_dealloc(tmem, C::kCols);
 }
 
 template <int D, bool F16>
