@@ -50,9 +50,9 @@ __device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d) {
     return lo | (hi << 16);
 }
 __device__ __forceinline__ uint32_t rescale4(uint32_t w, float ratio) {
-    const __half2 lo = __half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w & 0xffffu), __NV_E4M3));
-    const __half2 hi = __half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w >> 16), __NV_E4M3));
-    const float2 a = __half22float2(lo), b = __half22float2(hi);
+    uint32_t lo, hi;
+    widen4(w, lo, hi);
+    const float2 a = unpack2<true>(lo), b = unpack2<true>(hi);
     return codes4(a.x * ratio, a.y * ratio, b.x * ratio, b.y * ratio);
 }
 

@@ -40,22 +40,10 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t v) {
     asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
     return r;
 }
-// Two E4M3 codes as two fp16 values (exact).
-__device__ __forceinline__ uint32_t widen2(uint32_t codes) {
-    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)codes, __NV_E4M3);
-    return (uint32_t)h.x | ((uint32_t)h.y << 16);
-}
 __device__ __forceinline__ float exp2_fast(float x) {
     float r;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
     return r;
-}
-__device__ __forceinline__ uint4 load_codes16(const uint8_t *p) {
-    uint4 v;
-    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
-                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                 : "l"(p));
-    return v;
 }
 __device__ __forceinline__ uint2 load_codes8(const uint8_t *p) {
     uint2 v;
@@ -309,9 +297,12 @@ __global__ void __launch_bounds__(kThreads, D <= 128 ? 3 : 2) attn_split_kernel(
                 const uint32_t w0[4] = {kr[0][i].x, kr[0][i].y, kr[0][i].z, kr[0][i].w};
                 const uint32_t w1[4] = {kr[1][i].x, kr[1][i].y, kr[1][i].z, kr[1][i].w};
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    mma_f16(j & 1 ? s2 : s, widen2(w0[j] & 0xffffu), widen2(w1[j] & 0xffffu), widen2(w0[j] >> 16),
-                            widen2(w1[j] >> 16), qf[i][j][0], qf[i][j][1]);
+                for (int j = 0; j < 4; ++j) {
+                    uint32_t a0, a1, a2, a3;
+                    widen4(w0[j], a0, a2);
+                    widen4(w1[j], a1, a3);
+                    mma_f16(j & 1 ? s2 : s, a0, a1, a2, a3, qf[i][j][0], qf[i][j][1]);
+                }
             }
             const float ev = (float)exponent_of(sv), inv_sv = 1.0f / sv;
             const float mk[2] = {mul[0] * sk, mul[1] * sk};
@@ -365,8 +356,13 @@ __global__ void __launch_bounds__(kThreads, D <= 128 ? 3 : 2) attn_split_kernel(
                 // four dims of keys 2t, 2t+1 (and 2t+8, 2t+9): pairs of keys a dim
                 const uint32_t x = __byte_perm(vr[0][j], vr[1][j], 0x5140), y = __byte_perm(vr[0][j], vr[1][j], 0x7362);
                 const uint32_t x8 = __byte_perm(vr[2][j], vr[3][j], 0x5140), y8 = __byte_perm(vr[2][j], vr[3][j], 0x7362);
-                mma_f16(o[2 * j], widen2(x & 0xffffu), widen2(x >> 16), widen2(x8 & 0xffffu), widen2(x8 >> 16), b0, b1);
-                mma_f16(o[2 * j + 1], widen2(y & 0xffffu), widen2(y >> 16), widen2(y8 & 0xffffu), widen2(y8 >> 16), b0, b1);
+                uint32_t a0, a1, a2, a3;
+                widen4(x, a0, a1);
+                widen4(x8, a2, a3);
+                mma_f16(o[2 * j], a0, a1, a2, a3, b0, b1);
+                widen4(y, a0, a1);
+                widen4(y8, a2, a3);
+                mma_f16(o[2 * j + 1], a0, a1, a2, a3, b0, b1);
             }
             if (next < ke) load_v(next, page1);
             page = page1;

@@ -17,11 +17,10 @@
 // will meet (exact in fp16 unless a page is 2^-15 below it, and then off by at most 2^-25 of the
 // largest), so one factor a row holds for all keys.
 //
-// Roles: warps 0-7 do the softmax of both row tiles in turn, two threads a row (64 columns each: half
-// the time from logits to weights, and no warp waits for the tensor cores' turn); warps 8-15 widen K
-// and V; warp 16 issues the MMAs.  Row maxima move lazily: a row's reference changes only when a
-// logit passes it by 2^8 (weights stay below 256), so O is rarely rescaled, by the thread that
-// owns the row.
+// Roles: warps 0-3 and 4-7 do the softmax of row tiles 0 and 1, one row a thread; warps 8-15 widen K
+// and V; warp 16 issues the MMAs.  A row's maximum is not looked for in every tile: the weights are
+// taken under the reference so far, and their sum (needed anyway) shows when that has become too
+// small; the row's thread then finds the maximum, rescales its row of O and takes the weights again.
 #include "layer.h"
 #include "ptx.cuh"
 
@@ -34,19 +33,18 @@ constexpr int kStages = 4;  // K and V tiles in flight, in the order K0 V0 K1 V1
 constexpr int kSoftWarps = 8, kConvWarps = 8, kMmaWarp = 16;
 constexpr int kThreads = 20 * 32;  // (three warps beside the MMA warp only complete its warpgroup)
 // Registers a thread: 96 at launch (five warps a scheduler); of a scheduler's 5 x 96 the two softmax
-// warps, which hold 64 logits a thread, take 2 x 136, the converters 2 x 80, the MMA warp 40.
-constexpr int kLaunchRegs = 96, kSoftRegs = 136, kConvRegs = 80, kMmaRegs = 40;
+// warps, which hold a row's 128 weights and 64 logits, take 2 x 152, the converters 2 x 72, the MMA warp 32.
+constexpr int kLaunchRegs = 96, kSoftRegs = 152, kConvRegs = 72, kMmaRegs = 32;
 static_assert(8 * kSoftRegs + 8 * kConvRegs + 4 * kMmaRegs <= 20 * kLaunchRegs, "more registers than the block has");
 constexpr uint64_t kWaitNs = 2000000000ull;  // 2 s: far above any legitimate wait
-constexpr float kLazy = 8.f;
+constexpr float kMostSum = 4096.f;  // a tile's weights of one row may add up to this
 
 template <int D>
 struct Prompt {
     static constexpr int kBlocks = D / 64;                    // 128-byte column blocks of a row
     static constexpr int kBlockBytes = kKeys * 128;           // one column block of a 128-row tile
     static constexpr int kTileBytes = kBlocks * kBlockBytes;  // a tile of Q, K or V
-    // 1 KB to align, the tiles, barriers and holders, q exponents, exchanged maxima and flags
-    static constexpr int kSmem = 1024 + (2 + kStages) * kTileBytes + 256 + kRowsBlock * 8 + 64;
+    static constexpr int kSmem = 1024 + (2 + kStages) * kTileBytes + 256;  // 1 KB to align; barriers
     static constexpr uint32_t kColO = 2 * kKeys;              // TMEM: S0 S1 O0 O1
     static constexpr uint32_t kCols = 512;
 };
@@ -58,10 +56,6 @@ __device__ __forceinline__ float exp2_fast(float x) {
 }
 __device__ __forceinline__ int exponent_of(float s) { return (int)((__float_as_uint(s) >> 23) & 0xffu) - 127; }
 __device__ __forceinline__ float pow2f(int e) { return __int_as_float((min(max(e, -126), 127) + 127) << 23); }
-__device__ __forceinline__ uint32_t widen2(uint32_t codes) {
-    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)codes, __NV_E4M3);
-    return (uint32_t)h.x | ((uint32_t)h.y << 16);
-}
 __device__ __forceinline__ uint32_t mul2(uint32_t a, uint32_t f) {
     const __half2 r = __hmul2(*reinterpret_cast<const __half2 *>(&a), *reinterpret_cast<const __half2 *>(&f));
     return *reinterpret_cast<const uint32_t *>(&r);
@@ -80,19 +74,6 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
     float r;
     asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
     return r;
-}
-// Whether `x` holds in any thread of the two warps of a lane quarter; a barrier of the two.
-__device__ __forceinline__ bool any_of_pair(int quarter, bool x) {
-    uint32_t r;
-    asm volatile(
-        "{\n\t.reg .pred p, q;\n\t"
-        "setp.ne.u32 p, %1, 0;\n\t"
-        "bar.red.or.pred q, %2, 64, p;\n\t"
-        "selp.u32 %0, 1, 0, q;\n\t}"
-        : "=r"(r)
-        : "r"((uint32_t)x), "r"(2 + quarter)
-        : "memory");
-    return r != 0;
 }
 template <int R>
 __device__ __forceinline__ void regs_up() {
@@ -126,9 +107,6 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
     uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(drain + 1);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_holder + 1);
     int *max_exp = reinterpret_cast<int *>(tmem_holder + 2);              // [2] of K and V
-    int *q_exps = reinterpret_cast<int *>(reinterpret_cast<uint8_t *>(bars) + 256);  // [256] of the rows
-    float *ex_val = reinterpret_cast<float *>(q_exps + kRowsBlock);       // [2 halves][128]
-    int *ex_dead = reinterpret_cast<int *>(ex_val + kRowsBlock);          // [8 warps]
 
     const int tid = (int)threadIdx.x, lane = tid & 31;
     const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);  // known to be the same in all lanes
@@ -162,7 +140,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
         }
         for (int i = 0; i < 2; ++i) {
             ptx::mbar_init(&s_full[i], 1);
-            ptx::mbar_init(&p_full[i], kSoftWarps);
+            ptx::mbar_init(&p_full[i], kSoftWarps / 2);
             ptx::mbar_init(&o_full[i], 1);
         }
         ptx::mbar_init(q_full, kSoftWarps);
@@ -203,183 +181,173 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
     if (warp < kSoftWarps) {
         regs_up<kSoftRegs>();
         // ---------------------------------------------------------------------- softmax --
-        // Q first: thread t brings row t of the block, scaled by a power of two into [1, 2) at its
-        // largest, as fp16, K-major swizzled.
+        // Thread t has row t of the block: lane t % 128 of row tile t / 128.
+        const int i = warp >> 2, r = tid, rr = r & (kRowTile - 1);
+        const bool live = r < rows;
+        const int tok = (row0 + r) / v.G, qh = head * v.G + (row0 + r) % v.G;
+        const int pos = first_pos + tok;
+        const int hi = p.causal ? min(q.kv, pos + 1) : q.kv;
+        const int lo = p.window > 0 ? max(0, pos + 1 - p.window) : 0;
+        const bool sees = live && hi > lo;
+        // Q: the row scaled by a power of two into [1, 2) at its largest, as fp16, K-major swizzled
+        int q_exp;
         {
-            const int r = tid, rr = r & (kRowTile - 1);
-            const int tok = (row0 + r) / v.G, qh = head * v.G + (row0 + r) % v.G;
             const uint16_t *src = p.q + (int64_t)(q.q0 + tok) * p.q_ld + (int64_t)qh * D;
-            uint8_t *dst = q_smem + (r >> 7) * C::kTileBytes + rr * 128;
+            uint8_t *dst = q_smem + i * C::kTileBytes + rr * 128;
+            uint4 qv[D / 8];
+#pragma unroll
+            for (int c = 0; c < D / 8; ++c)
+                qv[c] = live ? __ldg(reinterpret_cast<const uint4 *>(src + c * 8)) : make_uint4(0, 0, 0, 0);
             float amax = 0.f;
 #pragma unroll
             for (int c = 0; c < D / 8; ++c) {
                 float f[8];
-                unpack8<F16>(r < rows ? *reinterpret_cast<const uint4 *>(src + c * 8) : make_uint4(0, 0, 0, 0), f);
+                unpack8<F16>(qv[c], f);
 #pragma unroll
                 for (int j = 0; j < 8; ++j) amax = fmaxf(amax, fabsf(f[j]));
             }
-            const int q_exp = amax > 0.f ? max(min((int)(__float_as_uint(amax) >> 23) - 127, 126), -126) : 0;
+            q_exp = amax > 0.f ? max(min((int)(__float_as_uint(amax) >> 23) - 127, 126), -126) : 0;
             const float q_inv = pow2f(-q_exp);
 #pragma unroll
             for (int c = 0; c < D / 8; ++c) {
                 float f[8];
-                unpack8<F16>(r < rows ? *reinterpret_cast<const uint4 *>(src + c * 8) : make_uint4(0, 0, 0, 0), f);
+                unpack8<F16>(qv[c], f);
 #pragma unroll
                 for (int j = 0; j < 8; ++j) f[j] *= q_inv;
                 *reinterpret_cast<uint4 *>(dst + (c >> 3) * C::kBlockBytes + (((c & 7) ^ (rr & 7)) << 4)) = pack8<true>(f);
             }
-            q_exps[r] = q_exp;
             ptx::fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) ptx::mbar_arrive(q_full);
         }
-        ptx::named_bar(1, kSoftWarps * 32);
-
-        // Warps w and w + 4 share the 32 rows of TMEM lane quarter w % 4 of both row tiles: the first takes
-        // columns 0-63 of the logits, the second 64-127.
-        const int half = warp >> 2, quarter = warp & 3, rr = quarter * 32 + lane;
-        const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
-        float mul[2], m[2] = {-INFINITY, -INFINITY};
-        float2 l[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-        int lo[2], hi[2];
-        bool live[2];
+        const float mul = p.scale_log2 * pow2f(q_exp) * pow2f(k_exp);
+        const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+        const uint32_t s_addr = tmem + lanes + i * kKeys, o_addr = tmem + lanes + C::kColO + i * D;
+        float m = 0.f, l = 0.f;  // reference of the weights, and their sum (0: none so far)
+        for (int j = 0; j < tiles; ++j) {
+            ok = __all_sync(0xffffffffu, ptx::mbar_wait(&s_full[i], j & 1, kWaitNs, abort_flag)) != 0;
+            if (!ok) break;
+            ptx::tc_fence_after();
+            const int key0 = (tile0 + j) * kKeys, c_lo = lo - key0, c_hi = hi - key0;
+            const bool masked = __any_sync(0xffffffffu, live && (c_lo > 0 || c_hi < kKeys));
+            auto hide = [&](uint32_t (&s)[32], int c) {
+                if (!masked) return;
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int r = i * kRowTile + rr, pos = first_pos + (row0 + r) / v.G;
-            live[i] = r < rows;
-            hi[i] = p.causal ? min(q.kv, pos + 1) : q.kv;
-            lo[i] = p.window > 0 ? max(0, pos + 1 - p.window) : 0;
-            mul[i] = p.scale_log2 * pow2f(q_exps[r]) * pow2f(k_exp);
-        }
-        bool dead = false;
-        for (int j = 0; j < tiles && !dead; ++j) {
-            const int key0 = (tile0 + j) * kKeys + half * 64;
-#pragma unroll
-            for (int i = 0; i < 2 && !dead; ++i) {
-                const uint32_t s_addr = tmem + lanes + i * kKeys, o_addr = tmem + lanes + C::kColO + i * D + half * (D / 2);
-                if (!ptx::mbar_wait(&s_full[i], j & 1, kWaitNs, abort_flag)) ok = false;
-                const bool stop = __any_sync(0xffffffffu, !ok) || *abort_flag;
-                ptx::tc_fence_after();
+                for (int k = 0; k < 32; ++k)
+                    if (c * 32 + k < c_lo || c * 32 + k >= c_hi) s[k] = 0xff800000u;  // -inf
+            };
+            uint32_t w[2][32];
+            auto weights = [&]() {  // from the logits in TMEM, under the present m; returns their sum
+                float2 sum = make_float2(0.f, 0.f);
                 uint32_t s[2][32];
-                ptx::tmem_ld_32(s_addr + half * 64, s[0]);
-                ptx::tmem_ld_32(s_addr + half * 64 + 32, s[1]);
-                ptx::tmem_ld_wait();
-                tie32(s[0]);
-                tie32(s[1]);
-                if (__any_sync(0xffffffffu, live[i] && (key0 < lo[i] || key0 + 64 > hi[i]))) {
-                    const int c_lo = lo[i] - key0, c_hi = hi[i] - key0;
-#pragma unroll
-                    for (int c = 0; c < 2; ++c)
-#pragma unroll
-                        for (int k = 0; k < 32; ++k)
-                            if (c * 32 + k < c_lo || c * 32 + k >= c_hi) s[c][k] = 0xff800000u;  // -inf
-                }
-                float tops[4];
+                ptx::tmem_ld_32(s_addr, s[0]);
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
-                    const uint32_t *x = &s[c >> 1][(c & 1) * 16];
-                    tops[c] = __uint_as_float(x[0]);
-#pragma unroll
-                    for (int k = 1; k < 15; k += 2) tops[c] = max3(tops[c], __uint_as_float(x[k]), __uint_as_float(x[k + 1]));
-                }
-                float top = max3(fmaxf(tops[0], __uint_as_float(s[0][15])), fmaxf(tops[1], __uint_as_float(s[0][31])),
-                                 max3(tops[2], tops[3], fmaxf(__uint_as_float(s[1][15]), __uint_as_float(s[1][31]))));
-                top *= mul[i];  // mul > 0
-                // One barrier of the two warps: both have read their logits (P will lie over them), and
-                // whether a row of either needs a new reference.
-                if (any_of_pair(quarter, stop || top > m[i] + kLazy)) {
-                    ex_val[half * kRowTile + rr] = top;
-                    if (lane == 0) ex_dead[warp] = stop;
-                    ptx::named_bar(2 + quarter, 64);
-                    dead = ex_dead[quarter] || ex_dead[quarter + 4];
-                    const float to = max3(m[i], ex_val[rr], ex_val[kRowTile + rr]);
-                    const float f = to == -INFINITY ? 1.f : exp2_fast(m[i] - to);
-                    m[i] = to;
-                    l[i].x *= f, l[i].y *= f;
-                    if (j > 0) {  // the logits came after the last product of this tile was complete
-                        uint32_t o[16];
-#pragma unroll
-                        for (int c = 0; c < D / 32; ++c) {
-                            ptx::tmem_ld_16(o_addr + c * 16, o);
-                            ptx::tmem_ld_wait();
-#pragma unroll
-                            for (int k = 0; k < 16; ++k) {
-                                asm volatile("" : "+r"(o[k]));
-                                o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
-                            }
-                            ptx::tmem_st_16(o_addr + c * 16, o);
-                        }
-                    }
-                    ptx::named_bar(2 + quarter, 64);  // ex_* are free again
-                }
-                const float ref = m[i] == -INFINITY ? 0.f : m[i];
-#pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    uint32_t w[16];
+                    ptx::tmem_ld_wait();
+                    tie32(s[c & 1]);
+                    if (c < 3) ptx::tmem_ld_32(s_addr + (c + 1) * 32, s[(c + 1) & 1]);
+                    hide(s[c & 1], c);
 #pragma unroll
                     for (int k = 0; k < 16; ++k) {
-                        const float2 z =
-                            fma2(make_float2(__uint_as_float(s[c][2 * k]), __uint_as_float(s[c][2 * k + 1])), mul[i], -ref);
+                        const float2 z = fma2(
+                            make_float2(__uint_as_float(s[c & 1][2 * k]), __uint_as_float(s[c & 1][2 * k + 1])), mul, -m);
                         const float2 e = make_float2(exp2_fast(z.x), exp2_fast(z.y));
-                        l[i] = __fadd2_rn(l[i], e);
-                        w[k] = pack2<true>(e.x, e.y);
+                        sum = __fadd2_rn(sum, e);
+                        w[c >> 1][(c & 1) * 16 + k] = pack2<true>(e.x, e.y);
                     }
-                    ptx::tmem_st_16(s_addr + half * 32 + c * 16, w);
                 }
-                ptx::tmem_st_wait();
-                ptx::tc_fence_before();
-                __syncwarp();
-                if (lane == 0) ptx::mbar_arrive(&p_full[i]);
+                return sum.x + sum.y;
+            };
+            // The sum itself tells when the reference is too small: as long as it stays below 2^12 every weight
+            // fits fp16.  Only then (and where a row begins) is the row's maximum looked for.
+            float sum = 0.f;
+            bool renew = j == 0;
+            if (j > 0) {
+                sum = weights();
+                renew = __any_sync(0xffffffffu, !(sum <= kMostSum) || (l == 0.f && sees));
             }
+            if (renew) {
+                float top = -INFINITY;
+                uint32_t s[32];
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    ptx::tmem_ld_32(s_addr + c * 32, s);
+                    ptx::tmem_ld_wait();
+                    tie32(s);
+                    hide(s, c);
+#pragma unroll
+                    for (int k = 0; k < 32; k += 2) top = max3(top, __uint_as_float(s[k]), __uint_as_float(s[k + 1]));
+                }
+                top *= mul;  // mul > 0
+                float f = 1.f;
+                if (l == 0.f) {
+                    m = top == -INFINITY ? 0.f : top;
+                } else if (top > m) {
+                    f = exp2_fast(m - top);
+                    m = top;
+                }
+                l *= f;
+                if (j > 0) {  // the logits came after the last product of this tile was complete
+                    uint32_t o[16];
+#pragma unroll
+                    for (int c = 0; c < D / 16; ++c) {
+                        ptx::tmem_ld_16(o_addr + c * 16, o);
+                        ptx::tmem_ld_wait();
+#pragma unroll
+                        for (int k = 0; k < 16; ++k) {
+                            asm volatile("" : "+r"(o[k]));
+                            o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
+                        }
+                        ptx::tmem_st_16(o_addr + c * 16, o);
+                    }
+                }
+                sum = weights();
+            }
+            l += sum;
+            ptx::tmem_st_32(s_addr, w[0]);  // P over S
+            ptx::tmem_st_32(s_addr + 32, w[1]);
+            ptx::tmem_st_wait();
+            ptx::tc_fence_before();
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(&p_full[i]);
         }
         // ---------------------------------------------------------------- output, normalised --
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            if (dead) break;
-            const int r = i * kRowTile + rr, tok = (row0 + r) / v.G, qh = head * v.G + (row0 + r) % v.G;
-            // row sums of the two halves
-            ex_val[half * kRowTile + rr] = l[i].x + l[i].y;
-            if (tiles > 0 && !ptx::mbar_wait(&o_full[i], 0, kWaitNs, abort_flag)) ok = false;
-            ptx::named_bar(2 + quarter, 64);
-            const float sum = ex_val[rr] + ex_val[kRowTile + rr];
-            ptx::named_bar(2 + quarter, 64);
-            ok = __all_sync(0xffffffffu, ok);
-            if (!ok) continue;
+        if (ok && tiles > 0) ok = __all_sync(0xffffffffu, ptx::mbar_wait(&o_full[i], 0, kWaitNs, abort_flag)) != 0;
+        if (ok) {
             ptx::tc_fence_after();
-            const float inv = (sum > 0.f || sum != sum) && tiles > 0 ? pow2f(v_exp) / sum : 0.f;
-            uint16_t *out = p.out + (int64_t)(q.q0 + tok) * p.out_ld + (int64_t)qh * D + half * (D / 2);
+            const float inv = (l > 0.f || l != l) && tiles > 0 ? pow2f(v_exp) / l : 0.f;
+            uint16_t *out = p.out + (int64_t)(q.q0 + tok) * p.out_ld + (int64_t)qh * D;
 #pragma unroll
-            for (int c = 0; c < D / 64; ++c) {
+            for (int c = 0; c < D / 32; ++c) {
                 uint32_t o[32];
                 __syncwarp();
                 if (tiles > 0) {
-                    ptx::tmem_ld_32(tmem + lanes + C::kColO + i * D + half * (D / 2) + c * 32, o);
+                    ptx::tmem_ld_32(o_addr + c * 32, o);
                     ptx::tmem_ld_wait();
                     tie32(o);
                 }
 #pragma unroll
-                for (int k = 0; k < 4 && live[i]; ++k) {
+                for (int k = 0; k < 4 && live; ++k) {
                     float f[8];
 #pragma unroll
                     for (int x = 0; x < 8; ++x) f[x] = inv == 0.f ? 0.f : __uint_as_float(o[8 * k + x]) * inv;
                     *reinterpret_cast<uint4 *>(out + c * 32 + k * 8) = pack8<F16>(f);
                 }
             }
-            if (live[i] && p.lse && half == 0) p.lse[(int64_t)(q.q0 + tok) * v.QH + qh] = (m[i] + log2f(sum)) * 0.6931471805599453f;
+            if (live && p.lse) p.lse[(int64_t)(q.q0 + tok) * v.QH + qh] = (m + log2f(l)) * 0.6931471805599453f;
         }
-        ok = ok && !dead;
     } else if (warp < kMmaWarp) {
         regs_down<kConvRegs>();
         // ------------------------------------------------------------- K and V, widened --
-        // Warp w owns keys 16 w .. 16 w + 15 of every tile: they lie in one page.  A load takes whole rows,
-        // lane = 16-code piece of a row, so that it reads full lines; a piece's two 16-byte stores go
-        // out in the order that spreads 8 lanes over all the banks (at D = 128 the upper four pieces
-        // of a row, which lie in the next column block, store their second half first).  The registers of
-        // a tile's codes take the next tile's as soon as they are widened, so a load has a whole
-        // tile's time to arrive.
-        constexpr int kPieces = D / 16, kRowsLoad = 32 / kPieces, kLoads = 16 / kRowsLoad;
-        const int cw = warp - kSoftWarps, piece = lane % kPieces, sub = lane / kPieces;
-        const bool swap = piece >= 4;
+        // Warp w owns keys 16 w .. 16 w + 15 of every tile: they lie in one page.  A load takes whole rows
+        // (4 of 128 codes, 8 of 64), so that it reads full lines, 16 codes a lane; lanes are laid out
+        // so that each 8 of them hold 4 pieces of two neighbouring rows, whose 16-byte stores fall on
+        // all the banks.  The registers of a tile's codes take the next tile's as soon as they are
+        // widened, so a load has a whole tile's time to arrive.
+        constexpr int kRowsLoad = 512 / D, kLoads = 16 / kRowsLoad;
+        const int cw = warp - kSoftWarps;
+        const int piece = D == 128 ? (lane >> 1 & 4) | (lane & 3) : lane & 3;
+        const int sub = D == 128 ? (lane >> 3 & 2) | (lane >> 2 & 1) : lane >> 2;
         auto page_at = [&](int tile) {  // page * KH + head
             const int key = (tile0 + tile) * kKeys + cw * 16;
             int page = 0;
@@ -399,23 +367,23 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
             for (int n = 0; n < kLoads; ++n) {
                 raw[n] = make_uint4(0, 0, 0, 0);
                 if (key0 + n * kRowsLoad + sub < key_hi)  // slots past the end hold anything
-                    raw[n] = __ldg(reinterpret_cast<const uint4 *>(src + n * kRowsLoad * D));
+                    raw[n] = load_codes16(src + n * kRowsLoad * D);
             }
         };
-        // offsets of a piece's first and second store, for rows whose number is below 4 modulo 8 (or any: D = 64)
+        // offsets of a piece's two stores in rows that are below 4 modulo 8 (D = 64: in any)
         const uint32_t base = (uint32_t)(piece >> 2) * C::kBlockBytes + (uint32_t)(cw * 16 + sub) * 128;
-        const uint32_t c0 = ((2 * (piece & 3) + (swap ? 1 : 0)) ^ sub) << 4, c1 = c0 ^ 16u;
+        const uint32_t c0 = ((2 * (piece & 3)) ^ sub) << 4, c1 = c0 ^ 16u;
         auto widen = [&](const uint4 (&raw)[kLoads], int it, uint32_t f) {
             uint8_t *st = kv_smem + it % kStages * C::kTileBytes + base;
 #pragma unroll
             for (int n = 0; n < kLoads; ++n) {
-                const uint32_t w[4] = {swap ? raw[n].z : raw[n].x, swap ? raw[n].w : raw[n].y, swap ? raw[n].x : raw[n].z,
-                                       swap ? raw[n].y : raw[n].w};
+                const uint32_t w[4] = {raw[n].x, raw[n].y, raw[n].z, raw[n].w};
                 uint32_t h[8];
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
-                    h[2 * k] = mul2(widen2(w[k] & 0xffffu), f);
-                    h[2 * k + 1] = mul2(widen2(w[k] >> 16), f);
+                    widen4(w[k], h[2 * k], h[2 * k + 1]);
+                    h[2 * k] = mul2(h[2 * k], f);
+                    h[2 * k + 1] = mul2(h[2 * k + 1], f);
                 }
                 const uint32_t flip = (n * kRowsLoad & 4) << 4;  // row bit 2 of the swizzle
                 uint8_t *dst = st + n * kRowsLoad * 128;

@@ -104,6 +104,25 @@ __device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
     return make_uint4(pack2<F16>(f[0], f[1]), pack2<F16>(f[2], f[3]), pack2<F16>(f[4], f[5]), pack2<F16>(f[6], f[7]));
 }
 
+// Four E4M3 codes as two pairs of fp16 values (exact: every E4M3 value is an fp16 value).
+__device__ __forceinline__ void widen4(uint32_t codes, uint32_t &lo, uint32_t &hi) {
+    asm("{\n\t.reg .b16 a, b;\n\t"
+        "mov.b32 {a, b}, %2;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %0, a;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+        : "=r"(lo), "=r"(hi)
+        : "r"(codes));
+}
+
+// 16 codes, read once by this block: not kept in L1.
+__device__ __forceinline__ uint4 load_codes16(const uint8_t *p) {
+    uint4 v;
+    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "l"(p));
+    return v;
+}
+
 // One sequence of the batch.  What the device arrays say is checked before it is used: a range
 // outside the batch's tokens counts as no tokens, a length outside the table as the nearest end.
 struct Seq {
