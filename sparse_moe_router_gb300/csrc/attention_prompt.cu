@@ -33,11 +33,11 @@ constexpr int kStages = 4;  // K and V tiles in flight, in the order K0 V0 K1 V1
 constexpr int kSoftWarps = 8, kConvWarps = 8, kMmaWarp = 16;
 constexpr int kThreads = 20 * 32;  // (three warps beside the MMA warp only complete its warpgroup)
 // Registers a thread: 96 at launch (five warps a scheduler); of a scheduler's 5 x 96 the two softmax
-// warps, which hold a row's 128 weights and 64 logits, take 2 x 152, the converters 2 x 72, the MMA warp 32.
-constexpr int kLaunchRegs = 96, kSoftRegs = 152, kConvRegs = 72, kMmaRegs = 32;
+// warps, which hold 64 logits and 32 pairs of weights, take 2 x 136, the converters 2 x 88, the MMA warp 32.
+constexpr int kLaunchRegs = 96, kSoftRegs = 136, kConvRegs = 88, kMmaRegs = 32;
 static_assert(8 * kSoftRegs + 8 * kConvRegs + 4 * kMmaRegs <= 20 * kLaunchRegs, "more registers than the block has");
 constexpr uint64_t kWaitNs = 2000000000ull;  // 2 s: far above any legitimate wait
-constexpr float kMostSum = 4096.f;  // a tile's weights of one row may add up to this
+constexpr float kMostSum = 32768.f;  // 64 weights of one row may add up to this
 
 template <int D>
 struct Prompt {
@@ -236,47 +236,40 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
                 for (int k = 0; k < 32; ++k)
                     if (c * 32 + k < c_lo || c * 32 + k >= c_hi) s[k] = 0xff800000u;  // -inf
             };
-            uint32_t w[2][32];
-            auto weights = [&]() {  // from the logits in TMEM, under the present m; returns their sum
+            // The sum of the weights itself tells when the reference is too small: as long as it stays within
+            // kMostSum every weight fits fp16.  Only then (and where a row begins) is the maximum looked for.
+            uint32_t s[2][32], w[32];
+            auto weights = [&](int h) {  // of columns 64 h .. 64 h + 63, from the logits in TMEM; returns their sum
                 float2 sum = make_float2(0.f, 0.f);
-                uint32_t s[2][32];
-                ptx::tmem_ld_32(s_addr, s[0]);
+                ptx::tmem_ld_32(s_addr + h * 64, s[0]);
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
+                for (int c = 0; c < 2; ++c) {
                     ptx::tmem_ld_wait();
-                    tie32(s[c & 1]);
-                    if (c < 3) ptx::tmem_ld_32(s_addr + (c + 1) * 32, s[(c + 1) & 1]);
-                    hide(s[c & 1], c);
+                    tie32(s[c]);
+                    if (c == 0) ptx::tmem_ld_32(s_addr + h * 64 + 32, s[1]);
+                    hide(s[c], 2 * h + c);
 #pragma unroll
                     for (int k = 0; k < 16; ++k) {
-                        const float2 z = fma2(
-                            make_float2(__uint_as_float(s[c & 1][2 * k]), __uint_as_float(s[c & 1][2 * k + 1])), mul, -m);
+                        const float2 z =
+                            fma2(make_float2(__uint_as_float(s[c][2 * k]), __uint_as_float(s[c][2 * k + 1])), mul, -m);
                         const float2 e = make_float2(exp2_fast(z.x), exp2_fast(z.y));
                         sum = __fadd2_rn(sum, e);
-                        w[c >> 1][(c & 1) * 16 + k] = pack2<true>(e.x, e.y);
+                        w[c * 16 + k] = pack2<true>(e.x, e.y);
                     }
                 }
                 return sum.x + sum.y;
             };
-            // The sum itself tells when the reference is too small: as long as it stays below 2^12 every weight
-            // fits fp16.  Only then (and where a row begins) is the row's maximum looked for.
-            float sum = 0.f;
-            bool renew = j == 0;
-            if (j > 0) {
-                sum = weights();
-                renew = __any_sync(0xffffffffu, !(sum <= kMostSum) || (l == 0.f && sees));
-            }
-            if (renew) {
+            // A larger reference: from the logits of columns 64 h .. 127; what was summed under the old one
+            // (O, l, and with h = 1 the tile's first 64 weights) is scaled.
+            auto renew = [&](int h) {
                 float top = -INFINITY;
-                uint32_t s[32];
-#pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    ptx::tmem_ld_32(s_addr + c * 32, s);
+                for (int c = 2 * h; c < 4; ++c) {
+                    ptx::tmem_ld_32(s_addr + c * 32, s[0]);
                     ptx::tmem_ld_wait();
-                    tie32(s);
-                    hide(s, c);
+                    tie32(s[0]);
+                    hide(s[0], c);
 #pragma unroll
-                    for (int k = 0; k < 32; k += 2) top = max3(top, __uint_as_float(s[k]), __uint_as_float(s[k + 1]));
+                    for (int k = 0; k < 32; k += 2) top = max3(top, __uint_as_float(s[0][k]), __uint_as_float(s[0][k + 1]));
                 }
                 top *= mul;  // mul > 0
                 float f = 1.f;
@@ -287,25 +280,36 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
                     m = top;
                 }
                 l *= f;
+                auto scale = [&](uint32_t addr, auto by) {
+                    ptx::tmem_ld_32(addr, s[0]);
+                    ptx::tmem_ld_wait();
+                    tie32(s[0]);
+#pragma unroll
+                    for (int k = 0; k < 32; ++k) s[0][k] = by(s[0][k]);
+                    ptx::tmem_st_32(addr, s[0]);
+                };
                 if (j > 0) {  // the logits came after the last product of this tile was complete
-                    uint32_t o[16];
-#pragma unroll
-                    for (int c = 0; c < D / 16; ++c) {
-                        ptx::tmem_ld_16(o_addr + c * 16, o);
-                        ptx::tmem_ld_wait();
-#pragma unroll
-                        for (int k = 0; k < 16; ++k) {
-                            asm volatile("" : "+r"(o[k]));
-                            o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
-                        }
-                        ptx::tmem_st_16(o_addr + c * 16, o);
-                    }
+                    for (int c = 0; c < D / 32; ++c)
+                        scale(o_addr + c * 32, [&](uint32_t x) { return __float_as_uint(__uint_as_float(x) * f); });
                 }
-                sum = weights();
+                if (h == 1) {  // (rounded to fp16 a second time: 2^-12 of those weights)
+                    scale(s_addr, [&](uint32_t x) {
+                        const float2 v2 = unpack2<true>(x);
+                        return pack2<true>(v2.x * f, v2.y * f);
+                    });
+                    ptx::tmem_st_wait();
+                }
+            };
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                float sum = weights(h);
+                if (__any_sync(0xffffffffu, !(sum <= kMostSum) || (h == 0 && l == 0.f && sees))) {
+                    renew(h);
+                    sum = weights(h);
+                }
+                l += sum;
+                ptx::tmem_st_32(s_addr + h * 32, w);  // P over S, whose columns up to 64 h + 63 are done with
             }
-            l += sum;
-            ptx::tmem_st_32(s_addr, w[0]);  // P over S
-            ptx::tmem_st_32(s_addr + 32, w[1]);
             ptx::tmem_st_wait();
             ptx::tc_fence_before();
             __syncwarp();
