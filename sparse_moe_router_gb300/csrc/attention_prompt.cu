@@ -101,7 +101,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
     uint64_t *full = bars, *empty = bars + kStages;  // of a stage
     uint64_t *s_full = empty + kStages;              // [2] logits of a row tile are in TMEM
     uint64_t *p_full = s_full + 2;                   // [2] its weights are
-    uint64_t *o_full = p_full + 2;                   // [2] its output is complete
+    uint64_t *p_half = p_full + 2;                   // [2] the first half of them
+    uint64_t *o_half = p_half + 2;                   // [2] and that half's product is complete
+    uint64_t *o_full = o_half + 2;                   // [2] its output is complete
     uint64_t *q_full = o_full + 2;
     uint64_t *drain = q_full + 1;
     uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(drain + 1);
@@ -141,6 +143,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
         for (int i = 0; i < 2; ++i) {
             ptx::mbar_init(&s_full[i], 1);
             ptx::mbar_init(&p_full[i], kSoftWarps / 2);
+            ptx::mbar_init(&p_half[i], kSoftWarps / 2);
+            ptx::mbar_init(&o_half[i], 1);
             ptx::mbar_init(&o_full[i], 1);
         }
         ptx::mbar_init(q_full, kSoftWarps);
@@ -239,34 +243,31 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
             // The sum of the weights itself tells when the reference is too small: as long as it stays within
             // kMostSum every weight fits fp16.  Only then (and where a row begins) is the maximum looked for.
             uint32_t s[2][32], w[32];
-            auto weights = [&](int h) {  // of columns 64 h .. 64 h + 63, from the logits in TMEM; returns their sum
-                float2 sum = make_float2(0.f, 0.f);
-                ptx::tmem_ld_32(s_addr + h * 64, s[0]);
-#pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    ptx::tmem_ld_wait();
-                    tie32(s[c]);
-                    if (c == 0) ptx::tmem_ld_32(s_addr + h * 64 + 32, s[1]);
-                    hide(s[c], 2 * h + c);
-#pragma unroll
-                    for (int k = 0; k < 16; ++k) {
-                        const float2 z =
-                            fma2(make_float2(__uint_as_float(s[c][2 * k]), __uint_as_float(s[c][2 * k + 1])), mul, -m);
-                        const float2 e = make_float2(exp2_fast(z.x), exp2_fast(z.y));
-                        sum = __fadd2_rn(sum, e);
-                        w[c * 16 + k] = pack2<true>(e.x, e.y);
-                    }
-                }
-                return sum.x + sum.y;
+            auto fetch = [&](int c) { ptx::tmem_ld_32(s_addr + c * 32, s[c & 1]); };
+            auto fetched = [&]() {
+                ptx::tmem_ld_wait();
+                tie32(s[0]);
+                tie32(s[1]);
             };
-            // A larger reference: from the logits of columns 64 h .. 127; what was summed under the old one
-            // (O, l, and with h = 1 the tile's first 64 weights) is scaled.
+            auto weights = [&](int c, float2 sum) {  // of the 32 columns from 32 c, whose logits are in s[c & 1]
+                hide(s[c & 1], c);
+#pragma unroll
+                for (int k = 0; k < 16; ++k) {
+                    const float2 z =
+                        fma2(make_float2(__uint_as_float(s[c & 1][2 * k]), __uint_as_float(s[c & 1][2 * k + 1])), mul, -m);
+                    const float2 e = make_float2(exp2_fast(z.x), exp2_fast(z.y));
+                    sum = __fadd2_rn(sum, e);
+                    w[(c & 1) * 16 + k] = pack2<true>(e.x, e.y);
+                }
+                return sum;
+            };
+            // A larger reference, from the logits of columns 64 h .. 127; O and l, summed under the old one, are
+            // scaled (with h = 1 once the tile's first 64 weights have gone into O).
             auto renew = [&](int h) {
                 float top = -INFINITY;
                 for (int c = 2 * h; c < 4; ++c) {
                     ptx::tmem_ld_32(s_addr + c * 32, s[0]);
-                    ptx::tmem_ld_wait();
-                    tie32(s[0]);
+                    fetched();
                     hide(s[0], c);
 #pragma unroll
                     for (int k = 0; k < 32; k += 2) top = max3(top, __uint_as_float(s[0][k]), __uint_as_float(s[0][k + 1]));
@@ -280,40 +281,58 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
                     m = top;
                 }
                 l *= f;
-                auto scale = [&](uint32_t addr, auto by) {
-                    ptx::tmem_ld_32(addr, s[0]);
-                    ptx::tmem_ld_wait();
-                    tie32(s[0]);
+                if (h == 1) {
+                    ok = ok && ptx::mbar_wait(&o_half[i], j & 1, kWaitNs, abort_flag);
+                    __syncwarp();
+                    ptx::tc_fence_after();
+                }
+                // (h = 0: the logits came after the product of the tile before was complete)
+                for (int c = 0; c < D / 32 && (h == 1 || j > 0); ++c) {
+                    ptx::tmem_ld_32(o_addr + c * 32, s[0]);
+                    fetched();
 #pragma unroll
-                    for (int k = 0; k < 32; ++k) s[0][k] = by(s[0][k]);
-                    ptx::tmem_st_32(addr, s[0]);
-                };
-                if (j > 0) {  // the logits came after the last product of this tile was complete
-                    for (int c = 0; c < D / 32; ++c)
-                        scale(o_addr + c * 32, [&](uint32_t x) { return __float_as_uint(__uint_as_float(x) * f); });
+                    for (int k = 0; k < 32; ++k) s[0][k] = __float_as_uint(__uint_as_float(s[0][k]) * f);
+                    ptx::tmem_st_32(o_addr + c * 32, s[0]);
                 }
-                if (h == 1) {  // (rounded to fp16 a second time: 2^-12 of those weights)
-                    scale(s_addr, [&](uint32_t x) {
-                        const float2 v2 = unpack2<true>(x);
-                        return pack2<true>(v2.x * f, v2.y * f);
-                    });
-                    ptx::tmem_st_wait();
-                }
+                fetch(2 * h);
+                fetch(2 * h + 1);
+                fetched();
             };
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                float sum = weights(h);
-                if (__any_sync(0xffffffffu, !(sum <= kMostSum) || (h == 0 && l == 0.f && sees))) {
-                    renew(h);
-                    sum = weights(h);
-                }
-                l += sum;
-                ptx::tmem_st_32(s_addr + h * 32, w);  // P over S, whose columns up to 64 h + 63 are done with
+            auto too_small = [&](float2 sum) { return !(sum.x + sum.y <= kMostSum); };
+            const float2 zero = make_float2(0.f, 0.f);
+            fetch(0);
+            fetch(1);
+            fetched();
+            if (__any_sync(0xffffffffu, l == 0.f && sees)) renew(0);
+            float2 sum = weights(1, weights(0, zero));
+            if (__any_sync(0xffffffffu, too_small(sum))) {
+                renew(0);
+                sum = weights(1, weights(0, zero));
             }
+            fetch(2);
+            fetch(3);
+            l += sum.x + sum.y;
+            ptx::tmem_st_32(s_addr, w);  // P over S, whose columns up to 63 are done with
+            fetched();
+            sum = weights(2, zero);
+            // the first half's product may begin
+            ptx::tmem_st_wait();
+            ptx::tc_fence_before();
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(&p_half[i]);
+            sum = weights(3, sum);
+            if (__any_sync(0xffffffffu, too_small(sum))) {
+                renew(1);
+                sum = weights(3, weights(2, zero));
+            }
+            l += sum.x + sum.y;
+            ptx::tmem_st_32(s_addr + 32, w);
             ptx::tmem_st_wait();
             ptx::tc_fence_before();
             __syncwarp();
             if (lane == 0) ptx::mbar_arrive(&p_full[i]);
+            ok = __all_sync(0xffffffffu, ok) != 0;
+            if (!ok) break;
         }
         // ---------------------------------------------------------------- output, normalised --
         if (ok && tiles > 0) ok = __all_sync(0xffffffffu, ptx::mbar_wait(&o_full[i], 0, kWaitNs, abort_flag)) != 0;
@@ -455,16 +474,19 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
                 }
                 __syncwarp();
             };
-            auto output = [&](int i, int j) {  // O += P V_j
+            auto output = [&](int i, int j, int h) {  // O += P V_j, keys 64 h .. 64 h + 63 of the tile
                 const int s = (2 * j + 1) % kStages;
                 if (ptx::elect_one()) {
                     const uint64_t vd = v_desc + (uint64_t)(s * (C::kTileBytes >> 4));
 #pragma unroll
-                    for (int k = 0; k < kKeys / 16; ++k)
-                        ptx::mma_f16_ts(tmem + C::kColO + i * D, tmem + i * kKeys + k * 8, vd + k * (2048 >> 4), idesc_o,
-                                        j > 0 || k > 0);
-                    if (i == 1) ptx::mma_commit(&empty[s]);
-                    if (j + 1 == tiles) ptx::mma_commit(&o_full[i]);
+                    for (int k = 0; k < kKeys / 32; ++k) {
+                        const int kk = h * (kKeys / 32) + k;
+                        ptx::mma_f16_ts(tmem + C::kColO + i * D, tmem + i * kKeys + kk * 8, vd + kk * (2048 >> 4), idesc_o,
+                                        j > 0 || kk > 0);
+                    }
+                    if (h == 0) ptx::mma_commit(&o_half[i]);
+                    if (h == 1 && i == 1) ptx::mma_commit(&empty[s]);
+                    if (h == 1 && j + 1 == tiles) ptx::mma_commit(&o_full[i]);
                 }
                 __syncwarp();
             };
@@ -476,15 +498,16 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
                 logits(1, 0);
             }
             for (int j = 0; j < tiles && ok; ++j) {
-                ok = filled(2 * j + 1);
+                const bool next = j + 1 < tiles;
+                ok = filled(2 * j + 1) && (!next || filled(2 * j + 2));
                 for (int i = 0; i < 2 && ok; ++i) {
-                    ok = wait(&p_full[i], j);
+                    ok = wait(&p_half[i], j);
                     ptx::tc_fence_after();
-                    if (ok) output(i, j);
-                    if (j + 1 == tiles || !ok) continue;
-                    if (i == 0) ok = filled(2 * j + 2);
+                    if (ok) output(i, j, 0);
+                    ok = ok && wait(&p_full[i], j);
                     ptx::tc_fence_after();
-                    if (ok) logits(i, j + 1);
+                    if (ok) output(i, j, 1);
+                    if (ok && next) logits(i, j + 1);
                 }
             }
             if (!ok) {  // nothing of this block may still run when its TMEM is freed
