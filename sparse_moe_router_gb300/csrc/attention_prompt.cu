@@ -470,7 +470,6 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
                         ptx::mma_f16_ss(tmem + i * kKeys, qd + off, kd + off, idesc_s, k > 0);
                     }
                     ptx::mma_commit(&s_full[i]);
-                    if (i == 1) ptx::mma_commit(&empty[s]);
                 }
                 __syncwarp();
             };
@@ -478,6 +477,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
                 const int s = (2 * j + 1) % kStages;
                 if (ptx::elect_one()) {
                     const uint64_t vd = v_desc + (uint64_t)(s * (C::kTileBytes >> 4));
+                    // K_j is free (committed here: a second commit behind the logits' own holds the warp
+                    // until the first is through)
+                    if (h == 0 && i == 0) ptx::mma_commit(&empty[2 * j % kStages]);
 #pragma unroll
                     for (int k = 0; k < kKeys / 32; ++k) {
                         const int kk = h * (kKeys / 32) + k;
