@@ -7,17 +7,20 @@
 // the products then run on the codes alone, which are exact in fp16, and pages of any scales mix.
 //
 // Bound: every code byte is read once and takes part in 2 x (rows of its head) products, so a
-// decode step is bound by HBM.  The kernel streams the codes straight from global memory into the
-// register fragments of mma.sync.m16n8k16: with keys (or value dims) on the 16-row side and up to
-// 8 query rows on the 8-wide side no product is wasted for a group of 8 heads, the contraction
-// index is free to be permuted, so each thread reads its fragment as 16-byte runs of a row, and
-// nothing passes through shared memory.  (tcgen05 would need 128 rows on one side and the codes
-// widened in shared memory first: with 8 rows a head the tensor cores are nearly idle either way.)
+// decode step is bound by HBM.  Each warp streams its own keys, 16 at a time, through a ring of its
+// own in shared memory (cp.async, no barrier between warps; 8 KB a warp in flight at D = 128, 128 KB
+// an SM) into the register fragments of mma.sync.m16n8k16.  With keys (or value dims) on the 16-row
+// side and 8 query rows on the 8-wide side no product is wasted for a group of 8 heads; the
+// contraction index may be permuted freely, so a thread reads its fragments as 16-byte runs of a
+// row, placed so that no two lanes meet on a bank.  (tcgen05 would need 128 rows on one side and
+// the codes widened in shared memory first: with 8 rows a head the tensor cores are nearly idle
+// either way.)
 //
 // Split: the batch's work is laid out as one line of 64-key steps (sequence by sequence, kv
-// head by kv head, 8-row tile by tile) and cut into equal runs, one a block, whatever the
-// lengths.  A run that ends inside a segment leaves partial sums; the block that finishes a
-// segment last joins them in order, so the result does not depend on which one that is.
+// head by kv head, row tile by row tile, each with a fixed cost in front) and cut into equal runs, one
+// a block, whatever the lengths.  A run that ends inside a segment leaves partial sums; the block
+// that finishes a segment last joins them in order, so the result does not depend on which one
+// that is.
 #include "layer.h"
 
 namespace moe {
@@ -45,11 +48,6 @@ __device__ __forceinline__ float exp2_fast(float x) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
     return r;
 }
-__device__ __forceinline__ uint2 load_codes8(const uint8_t *p) {
-    uint2 v;
-    asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));
-    return v;
-}
 __device__ __forceinline__ int exponent_of(float s) { return (int)((__float_as_uint(s) >> 23) & 0xffu) - 127; }
 __device__ __forceinline__ float pow2f(int e) { return __int_as_float((e + 127) << 23); }
 
@@ -61,56 +59,106 @@ __device__ __forceinline__ void key_range(const AttnArgs &p, const Seq &q, int t
     if (hi < lo) hi = lo;
 }
 
-// Rows a tile holds: 8 query rows (token, head) of one kv head.
-constexpr int kRows = 8;
+// Cost of a segment beside its steps (finding it, its queries, the first pages, the join), in steps: about
+// 2.5 us against 0.5 us a step.
+constexpr int kSegCost = 5;
+constexpr int kSeqCache = 256;  // sequences kept in shared memory
 
-// A sequence's share of the line of steps: tiles * steps * kv heads.
+// A sequence's share of the line: tiles * kv heads segments of kSegCost + steps each.
 struct SeqWork {
     Seq q;
     int tiles, step0, steps;
 };
-__device__ __forceinline__ SeqWork seq_work(const AttnArgs &p, int b) {
+__device__ __forceinline__ SeqWork seq_work(const AttnArgs &p, const Seq &q, int rows_tile) {
     SeqWork w;
-    w.q = load_seq(p.kv, b);
+    w.q = q;
     if ((int64_t)w.q.n * p.kv.G >= p.prompt_rows) w.q.n = 0;  // the prompt kernel's
-    w.tiles = (int)(((int64_t)w.q.n * p.kv.G + kRows - 1) / kRows);
+    w.tiles = (int)(((int64_t)w.q.n * p.kv.G + rows_tile - 1) / rows_tile);
     int lo, hi;
     key_range(p, w.q, 0, max(w.q.n, 1), lo, hi);
     w.step0 = lo / kStep;
     w.steps = max((hi + kStep - 1) / kStep - w.step0, 1);  // one at least: it writes the empty rows
     return w;
 }
-__device__ __forceinline__ int64_t line_steps(const AttnArgs &p, const SeqWork &w) {
-    return (int64_t)w.tiles * w.steps * p.kv.KH;
+__device__ __forceinline__ int64_t line_length(const AttnArgs &p, const SeqWork &w) {
+    return (int64_t)w.tiles * (w.steps + kSegCost) * p.kv.KH;
 }
 
-template <int D, bool F16>
+// NB: query row tiles of 8 that share a key tile.
+template <int D, int NB>
 struct Split {
-    static constexpr int kKLoads = D / 64;     // 16-byte runs of a key row a thread reads
-    static constexpr int kVRun = D / 8;        // value dims a thread owns (of every 4th..: 4 tokens)
-    static constexpr int kMT = D / 16;         // 16-dim output tiles
+    static constexpr int kRows = 8 * NB;
+    static constexpr int kKLoads = D / 64;   // 16-byte runs of a key row a thread reads
+    static constexpr int kVRun = D / 8;      // value dims a thread owns, of 4 keys
+    static constexpr int kMT = D / 16;       // 16-dim output tiles
     static constexpr int kPart = kRows * D + 2 * kRows;  // floats of a partial result: sums, m, l
+    static constexpr int kTile = 16 * D;     // bytes of 16 keys (or values)
+    static constexpr int kRing = 3;          // tiles of K and V in a warp's ring
+    static constexpr int kRingBytes = kWarps * kRing * 2 * kTile;
+    static constexpr int kMergeBytes = kWarps * kRows * D * 4;  // over the ring, once it is drained
+    static constexpr int kSmem = kRingBytes > kMergeBytes ? kRingBytes : kMergeBytes;
+    static constexpr int kBlocks = D * NB <= 128 ? 4 : D * NB <= 256 ? 2 : 1;  // resident a SM
 };
 
-template <int D, bool F16>
-__global__ void __launch_bounds__(kThreads, D <= 128 ? 3 : 2) attn_split_kernel(const __grid_constant__ AttnArgs p) {
-    using C = Split<D, F16>;
-    constexpr int kMT = C::kMT;
+__device__ __forceinline__ void copy16(uint32_t dst, const void *src, bool live) {  // zeros if not live
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(live ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copies_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ uint4 lds16(uint32_t a) {
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
+    return v;
+}
+__device__ __forceinline__ uint2 lds8(uint32_t a) {
+    uint2 v;
+    asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a) : "memory");
+    return v;
+}
+// Where 16-byte chunk c of row r of a tile lies.  A key fragment is read by 8 lanes at 4 chunks of rows 2x and
+// 2x + 1, a value fragment at 2 neighbouring chunks of rows 0, 2, 4, 6 (or 1, 3, 5, 7): both fall on all banks.
+template <int D>
+__device__ __forceinline__ uint32_t chunk_at(int r, int c) {
+    if (D == 64) return (uint32_t)((r >> 1) * 128 + (((r ^ (r >> 2)) & 1) * 4 + (c ^ (r & 2))) * 16);
+    return (uint32_t)(r * D + (c ^ (((r >> 1) & 3) << 1) ^ ((r & 1) << 2)) * 16);
+}
+
+template <int D, int NB, bool F16>
+__global__ void __launch_bounds__(kThreads, Split<D, NB>::kBlocks) attn_split_kernel(const __grid_constant__ AttnArgs p) {
+    using C = Split<D, NB>;
+    constexpr int kMT = C::kMT, kRows = C::kRows;
     const KvView &v = p.kv;
-    __shared__ int64_t scan[kWarps + 1];
+    extern __shared__ __align__(128) uint8_t ring[];
+    float *merge_o = reinterpret_cast<float *>(ring);  // [kWarps][kRows][D], once the ring is drained
+    __shared__ int64_t scan[kWarps];
     __shared__ int64_t found_at;
     __shared__ int found_b;
+    __shared__ int seq_q0[kSeqCache], seq_n[kSeqCache], seq_kv[kSeqCache];
     __shared__ float merge_m[kWarps][kRows], merge_l[kWarps][kRows];
-    __shared__ __align__(16) float merge_o[kWarps][kRows][D];  // read and written as float4
     __shared__ int last_flag;
 
     const int tid = (int)threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int g = lane >> 2, t = lane & 3;
 
     // ------------------------------------------------- this block's run of the line --
-    // total steps, then the sequence that holds the run's first step
-    int64_t total = 0;
-    for (int b = tid; b < v.n_seqs; b += kThreads) total += line_steps(p, seq_work(p, b));
+    // its length, then the sequence that holds the run's first place
+    int64_t total = 0, own0 = 0;
+    for (int b = tid; b < v.n_seqs; b += kThreads) {
+        const Seq q = load_seq(v, b);
+        if (b < kSeqCache) seq_q0[b] = q.q0, seq_n[b] = q.n, seq_kv[b] = q.kv;
+        const int64_t own = line_length(p, seq_work(p, q, kRows));
+        if (b < kThreads) own0 = own;
+        total += own;
+    }
+    auto seq_at = [&](int b) {
+        Seq q;
+        if (b < kSeqCache) q.q0 = seq_q0[b], q.n = seq_n[b], q.kv = seq_kv[b];
+        else q = load_seq(v, b);
+        return seq_work(p, q, kRows);
+    };
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
     if (lane == 0) scan[warp] = total;
@@ -120,11 +168,11 @@ __global__ void __launch_bounds__(kThreads, D <= 128 ? 3 : 2) attn_split_kernel(
     const int64_t per = (total + gridDim.x - 1) / gridDim.x;
     const int64_t begin = per * blockIdx.x, end = min(total, begin + per);
     if (begin >= end) return;
-    int64_t before = 0;  // steps of the sequences before the chunk
+    int64_t before = 0;  // the line up to the sequences of this chunk
     for (int b0 = 0;; b0 += kThreads) {
         __syncthreads();
         const int b = b0 + tid;
-        const int64_t own = b < v.n_seqs ? line_steps(p, seq_work(p, b)) : 0;
+        const int64_t own = b0 == 0 ? own0 : b < v.n_seqs ? line_length(p, seq_at(b)) : 0;
         int64_t inc = own;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -148,75 +196,117 @@ __global__ void __launch_bounds__(kThreads, D <= 128 ? 3 : 2) attn_split_kernel(
         before += all;
     }
     int b = found_b;
-    int64_t seq_at = found_at;  // where sequence b begins on the line
-    SeqWork sw = seq_work(p, b);
+    int64_t seq_begin = found_at;  // where sequence b begins on the line
+    SeqWork sw = seq_at(b);
 
+    const uint32_t my_ring = (uint32_t)__cvta_generic_to_shared(ring) + warp * C::kRing * 2 * C::kTile;
     for (int64_t at = begin; at < end;) {
-        while (at >= seq_at + line_steps(p, sw)) {
-            seq_at += line_steps(p, sw);
-            sw = seq_work(p, ++b);
+        while (at >= seq_begin + line_length(p, sw)) {
+            seq_begin += line_length(p, sw);
+            sw = seq_at(++b);
         }
         // ---------------------------------------------------------------- a segment --
-        const int64_t seg = (at - seq_at) / sw.steps;  // (head, tile) of the sequence
-        const int64_t seg_at = seq_at + seg * sw.steps, seg_end = seg_at + sw.steps;
+        const int seg_len = sw.steps + kSegCost;
+        const int64_t seg = (at - seq_begin) / seg_len;  // (head, tile) of the sequence
+        const int64_t seg_at = seq_begin + seg * seg_len, seg_end = seg_at + seg_len;
         const int head = (int)(seg / sw.tiles), tile = (int)(seg % sw.tiles);
-        const int s0 = (int)(at - seg_at), s1 = (int)(min(end, seg_end) - seg_at);
-        at = seg_at + s1;
+        const int s0 = max((int)(at - seg_at) - kSegCost, 0), s1 = max((int)(min(end, seg_end) - seg_at) - kSegCost, 0);
+        at = min(end, seg_end);
+        if (s1 <= s0) continue;  // only the cost in front lies in this run
         const int row0 = tile * kRows, rows = min(kRows, sw.q.n * v.G - row0);
         const int first_pos = sw.q.kv - sw.q.n;
 
-        // q rows: fragment rows are n = g, dims i*64 + t*16 + 4s of the four k-steps of run i
-        uint32_t qf[C::kKLoads][4][2];
-        int q_exp = 0;
-        {
-            float amax = 0.f;
-            float qv[C::kKLoads][16];
-            const int r = row0 + g;
-            const uint16_t *row = p.q + (int64_t)(sw.q.q0 + r / v.G) * p.q_ld + (int64_t)(head * v.G + r % v.G) * D + t * 16;
-#pragma unroll
-            for (int i = 0; i < C::kKLoads; ++i) {
-                uint4 a = make_uint4(0, 0, 0, 0), c = a;
-                if (g < rows) {
-                    a = *reinterpret_cast<const uint4 *>(row + i * 64);
-                    c = *reinterpret_cast<const uint4 *>(row + i * 64 + 8);
-                }
-                float x[8], y[8];
-                unpack8<F16>(a, x);
-                unpack8<F16>(c, y);
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    qv[i][j] = x[j];
-                    qv[i][8 + j] = y[j];
-                    amax = fmaxf(amax, fmaxf(fabsf(x[j]), fabsf(y[j])));
+        // tiles of 16 keys: tile n is keys [ks0 + n * kStep, + 16), up to the last that a row of this segment sees
+        int klo, khi;
+        key_range(p, sw.q, row0 / v.G, (row0 + rows - 1) / v.G + 1, klo, khi);
+        const int32_t *table = v.table + (int64_t)b * v.max_pages;
+        const int ks0 = max((sw.step0 + s0) * kStep, klo / kStep * kStep) + warp * 16;
+        const int ke = min((sw.step0 + s1) * kStep, khi);
+        const int tiles = ks0 < ke ? (ke - ks0 + kStep - 1) / kStep : 0;
+        // lane x holds page * KH + head and the scales of tile (a multiple of 32) + x, and of the 32 after
+        auto page_at = [&](int n) {
+            int page = 0;
+            if (n < tiles) {
+                page = __ldg(table + ((ks0 + n * kStep) >> v.log_p));
+                if (page < 0 || page >= v.n_pages) {
+                    layer_error(v.status);
+                    page = 0;
                 }
             }
+            return page * v.KH + head;
+        };
+        int page = page_at(lane), page_next = 0;
+        float sk = __ldg(v.k_scale + page), sv = __ldg(v.v_scale + page), sk_next = 1.f, sv_next = 1.f;
+        auto fill = [&](int n) {  // tile n into its place of the ring
+            if (n < tiles) {
+                const int pg = __shfl_sync(0xffffffffu, (n & 31) >= C::kRing - 1 || n < 32 ? page : page_next, n & 31);
+                const int key = ks0 + n * kStep;
+                const int64_t off = (((int64_t)pg << v.log_p) + (key & (v.P - 1))) * D + lane * 16;
+                const uint32_t dst = my_ring + n % C::kRing * 2 * C::kTile;
+#pragma unroll
+                for (int i = 0; i < D / 32; ++i) {
+                    const int r = (i * 32 + lane) / (D / 16), c = (i * 32 + lane) % (D / 16);
+                    const bool live = key + r < sw.q.kv;  // slots past the end hold anything
+                    copy16(dst + chunk_at<D>(r, c), v.k_codes + off + i * 512, live);
+                    copy16(dst + C::kTile + chunk_at<D>(r, c), v.v_codes + off + i * 512, live);
+                }
+            }
+            copies_commit();
+        };
+#pragma unroll
+        for (int n = 0; n < C::kRing - 1; ++n) fill(n);
+
+        // q rows: fragment rows are n = g, dims i*64 + t*16 + 4s of the four k-steps of run i
+        uint32_t qf[NB][C::kKLoads][4][2];
+        float mul[NB][2];
+        int lo[NB][2], hi[NB][2];  // the keys that rows 2t, 2t + 1 see
+        int all_lo = 0, all_hi = 0x7fffffff;  // keys in [all_lo, all_hi) are seen by every row
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) {
+            float amax = 0.f;
+            uint4 qv[C::kKLoads][2];
+            const int r = row0 + nb * 8 + g;
+            const bool live = nb * 8 + g < rows;
+            const uint16_t *row = p.q + (int64_t)(sw.q.q0 + r / v.G) * p.q_ld + (int64_t)(head * v.G + r % v.G) * D + t * 16;
+#pragma unroll
+            for (int i = 0; i < C::kKLoads; ++i)
+#pragma unroll
+                for (int c = 0; c < 2; ++c)
+                    qv[i][c] = live ? *reinterpret_cast<const uint4 *>(row + i * 64 + c * 8) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+            for (int i = 0; i < C::kKLoads; ++i)
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    float x[8];
+                    unpack8<F16>(qv[i][c], x);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) amax = fmaxf(amax, fabsf(x[j]));
+                }
             amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
             amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
             // largest magnitude into [1, 2): fp16 then holds every bf16 digit down to 2^-17 of it
-            q_exp = amax > 0.f ? max(min((int)(__float_as_uint(amax) >> 23) - 127, 126), -126) : 0;
+            const int q_exp = amax > 0.f ? max(min((int)(__float_as_uint(amax) >> 23) - 127, 126), -126) : 0;
             const float inv = pow2f(-q_exp);
 #pragma unroll
             for (int i = 0; i < C::kKLoads; ++i)
 #pragma unroll
-                for (int s = 0; s < 4; ++s) {
-                    qf[i][s][0] = pack2<true>(qv[i][4 * s] * inv, qv[i][4 * s + 1] * inv);
-                    qf[i][s][1] = pack2<true>(qv[i][4 * s + 2] * inv, qv[i][4 * s + 3] * inv);
-                }
-        }
-        // the two rows whose logits and sums this thread holds: n = 2t, 2t + 1
-        float mul[2];
-        int lo[2], hi[2];
-        int all_lo = 0, all_hi = 0x7fffffff;  // keys in [all_lo, all_hi) are seen by every row
+                for (int c = 0; c < 2; ++c) {
+                    float x[8];
+                    unpack8<F16>(qv[i][c], x);
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-            const int e = __shfl_sync(0xffffffffu, q_exp, (2 * t + c) * 4);
-            mul[c] = p.scale_log2 * pow2f(e);
-            const int pos = first_pos + (row0 + 2 * t + c) / v.G;
-            hi[c] = p.causal ? min(sw.q.kv, pos + 1) : sw.q.kv;
-            lo[c] = p.window > 0 ? max(0, pos + 1 - p.window) : 0;
-            if (2 * t + c < rows) {
-                all_lo = max(all_lo, lo[c]);
-                all_hi = min(all_hi, hi[c]);
+                    for (int j = 0; j < 4; ++j) qf[nb][i][2 * c + (j >> 1)][j & 1] = pack2<true>(x[2 * j] * inv, x[2 * j + 1] * inv);
+                }
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                const int e = __shfl_sync(0xffffffffu, q_exp, (2 * t + c) * 4);
+                mul[nb][c] = p.scale_log2 * pow2f(e);
+                const int rr = nb * 8 + 2 * t + c, pos = first_pos + (row0 + rr) / v.G;
+                hi[nb][c] = p.causal ? min(sw.q.kv, pos + 1) : sw.q.kv;
+                lo[nb][c] = p.window > 0 ? max(0, pos + 1 - p.window) : 0;
+                if (rr < rows) {
+                    all_lo = max(all_lo, lo[nb][c]);
+                    all_hi = min(all_hi, hi[nb][c]);
+                }
             }
         }
 #pragma unroll
@@ -225,132 +315,109 @@ __global__ void __launch_bounds__(kThreads, D <= 128 ? 3 : 2) attn_split_kernel(
             all_hi = min(all_hi, __shfl_xor_sync(0xffffffffu, all_hi, o));
         }
 
-        float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
-        float o[kMT][4];
+        float m[NB][2], l[NB][2], o[NB][kMT][4];
 #pragma unroll
-        for (int i = 0; i < kMT; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
-
-        // tiles of 16 keys: [key0, key0 + 16), key0 = (step0 + s) * 64 + warp * 16, up to the last
-        // key that a row of this tile sees
-        int klo, khi;
-        key_range(p, sw.q, row0 / v.G, (row0 + rows - 1) / v.G + 1, klo, khi);
-        const int32_t *table = v.table + (int64_t)b * v.max_pages;
-        int ks = max((sw.step0 + s0) * kStep, klo / kStep * kStep) + warp * 16;
-        const int ke = min((sw.step0 + s1) * kStep, khi);
-        auto page_of = [&](int key) {
-            int page = 0;
-            if (key < ke) {
-                page = __ldg(table + (key >> v.log_p));
-                if (page < 0 || page >= v.n_pages) {
-                    layer_error(v.status);
-                    page = 0;
-                }
-            }
-            return page;
-        };
-        uint4 kr[2][C::kKLoads];
-        uint32_t vr[4][C::kVRun / 4];
-        auto load_k = [&](int key, int page) {
-            const uint8_t *base = v.k_codes + (((int64_t)page * v.KH + head) * v.P + (key & (v.P - 1))) * D + t * 16;
+        for (int nb = 0; nb < NB; ++nb) {
+            m[nb][0] = m[nb][1] = -INFINITY;
+            l[nb][0] = l[nb][1] = 0.f;
 #pragma unroll
-            for (int h = 0; h < 2; ++h)
-#pragma unroll
-                for (int i = 0; i < C::kKLoads; ++i) kr[h][i] = load_codes16(base + (h * 8 + g) * D + i * 64);
-        };
-        auto load_v = [&](int key, int page) {
-            const uint8_t *base = v.v_codes + (((int64_t)page * v.KH + head) * v.P + (key & (v.P - 1))) * D;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int tok = 2 * t + (j & 1) + (j >> 1) * 8;
-                const bool live = key + tok < sw.q.kv;  // slots past the end hold anything
-                if (D == 64) {
-                    const uint2 x = load_codes8(base + tok * D + g * 8);
-                    vr[j][0] = live ? x.x : 0u;
-                    vr[j][1] = live ? x.y : 0u;
-                } else {
-#pragma unroll
-                    for (int i = 0; i < D / 128; ++i) {
-                        const uint4 x = load_codes16(base + tok * D + i * 128 + g * 16);
-                        vr[j][4 * i] = live ? x.x : 0u;
-                        vr[j][4 * i + 1] = live ? x.y : 0u;
-                        vr[j][4 * i + 2] = live ? x.z : 0u;
-                        vr[j][4 * i + 3] = live ? x.w : 0u;
-                    }
-                }
-            }
-        };
-        int page = page_of(ks), page1 = page_of(ks + kStep);
-        float sk = 1.f, sv = 1.f;
-        if (ks < ke) {
-            load_k(ks, page);
-            load_v(ks, page);
-            sk = __ldg(v.k_scale + (int64_t)page * v.KH + head);
-            sv = __ldg(v.v_scale + (int64_t)page * v.KH + head);
+            for (int i = 0; i < kMT; ++i) o[nb][i][0] = o[nb][i][1] = o[nb][i][2] = o[nb][i][3] = 0.f;
         }
-        for (; ks < ke; ks += kStep) {
-            const int next = ks + kStep;
-            const int page2 = page_of(next + kStep);
+        for (int n = 0; n < tiles; ++n) {
+            copies_wait<C::kRing - 2>();
+            __syncwarp();  // tile n is there for all lanes, and all are done with the tile before it
+            if ((n & 31) == 0 && n + 32 < tiles) page_next = page_at(n + 32 + lane);
+            if ((n & 31) == 16 && n + 16 < tiles) sk_next = __ldg(v.k_scale + page_next), sv_next = __ldg(v.v_scale + page_next);
+            fill(n + C::kRing - 1);
+            const uint32_t kt = my_ring + n % C::kRing * 2 * C::kTile, vt = kt + C::kTile;
+            const float tsk = __shfl_sync(0xffffffffu, sk, n & 31), tsv = __shfl_sync(0xffffffffu, sv, n & 31);
+            const int key0 = ks0 + n * kStep;
             // ------------------------------------------------------------ S = K q --
-            float s[4] = {0.f, 0.f, 0.f, 0.f}, s2[4] = {0.f, 0.f, 0.f, 0.f};
+            float s[NB][4], s2[NB][4];
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) s[nb][i] = s2[nb][i] = 0.f;
 #pragma unroll
             for (int i = 0; i < C::kKLoads; ++i) {
-                const uint32_t w0[4] = {kr[0][i].x, kr[0][i].y, kr[0][i].z, kr[0][i].w};
-                const uint32_t w1[4] = {kr[1][i].x, kr[1][i].y, kr[1][i].z, kr[1][i].w};
+                const uint4 x0 = lds16(kt + chunk_at<D>(g, 4 * i + t)), x1 = lds16(kt + chunk_at<D>(8 + g, 4 * i + t));
+                const uint32_t w0[4] = {x0.x, x0.y, x0.z, x0.w}, w1[4] = {x1.x, x1.y, x1.z, x1.w};
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     uint32_t a0, a1, a2, a3;
                     widen4(w0[j], a0, a2);
                     widen4(w1[j], a1, a3);
-                    mma_f16(j & 1 ? s2 : s, a0, a1, a2, a3, qf[i][j][0], qf[i][j][1]);
+#pragma unroll
+                    for (int nb = 0; nb < NB; ++nb) mma_f16(j & 1 ? s2[nb] : s[nb], a0, a1, a2, a3, qf[nb][i][j][0], qf[nb][i][j][1]);
                 }
-            }
-            const float ev = (float)exponent_of(sv), inv_sv = 1.0f / sv;
-            const float mk[2] = {mul[0] * sk, mul[1] * sk};
-            if (next < ke) {
-                load_k(next, page1);
-                sk = __ldg(v.k_scale + (int64_t)page1 * v.KH + head);
-                sv = __ldg(v.v_scale + (int64_t)page1 * v.KH + head);
             }
             // ------------------------------------------------------------- softmax --
-            float z[4];  // keys g, g, g + 8, g + 8 of rows 2t, 2t + 1
+            const float ev = (float)exponent_of(tsv), inv_sv = pow2f(-exponent_of(tsv));
+            float z[NB][4];  // keys g, g, g + 8, g + 8 of rows 2t, 2t + 1
+            bool up = false;
+            const bool masked = key0 < all_lo || key0 + 16 > all_hi;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) z[i] = fmaf(s[i] + s2[i], mk[i & 1], ev);
-            if (ks < all_lo || ks + 16 > all_hi) {
+            for (int nb = 0; nb < NB; ++nb) {
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int key = ks + g + (i >> 1) * 8;
-                    if (key < lo[i & 1] || key >= hi[i & 1]) z[i] = -INFINITY;
+                for (int i = 0; i < 4; ++i) z[nb][i] = fmaf(s[nb][i] + s2[nb][i], mul[nb][i & 1] * tsk, ev);
+                if (masked) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int key = key0 + g + (i >> 1) * 8;
+                        if (key < lo[nb][i & 1] || key >= hi[nb][i & 1]) z[nb][i] = -INFINITY;
+                    }
                 }
+                up |= fmaxf(z[nb][0], z[nb][2]) > m[nb][0] + 8.f || fmaxf(z[nb][1], z[nb][3]) > m[nb][1] + 8.f;
             }
             // The reference m of a row moves only when a logit passes it by more than 2^8 (the
             // weights then stay below 256, well inside fp16); most steps change nothing.
-            const bool up = fmaxf(z[0], z[2]) > m[0] + 8.f || fmaxf(z[1], z[3]) > m[1] + 8.f;
             if (__any_sync(0xffffffffu, up)) {
 #pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    float mx = fmaxf(m[c], fmaxf(z[c], z[2 + c]));
-                    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
-                    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
-                    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-                    const float f = mx == -INFINITY ? 1.f : exp2_fast(m[c] - mx);
-                    m[c] = mx;
-                    l[c] *= f;
+                for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-                    for (int i = 0; i < kMT; ++i) {
-                        o[i][c] *= f;
-                        o[i][2 + c] *= f;
+                    for (int c = 0; c < 2; ++c) {
+                        float mx = fmaxf(m[nb][c], fmaxf(z[nb][c], z[nb][2 + c]));
+                        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
+                        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+                        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+                        const float f = mx == -INFINITY ? 1.f : exp2_fast(m[nb][c] - mx);
+                        m[nb][c] = mx;
+                        l[nb][c] *= f;
+#pragma unroll
+                        for (int i = 0; i < kMT; ++i) {
+                            o[nb][i][c] *= f;
+                            o[nb][i][2 + c] *= f;
+                        }
+                    }
+            }
+            uint32_t b0[NB], b1[NB];
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb) {
+                float w[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) w[i] = exp2_fast(z[nb][i] - (m[nb][i & 1] == -INFINITY ? 0.f : m[nb][i & 1]));
+                l[nb][0] = fmaf(w[0] + w[2], inv_sv, l[nb][0]);
+                l[nb][1] = fmaf(w[1] + w[3], inv_sv, l[nb][1]);
+                // w as [key][row] pairs of rows; transposed into [row][key] pairs of keys
+                b0[nb] = transpose8(pack2<true>(w[0], w[1]));
+                b1[nb] = transpose8(pack2<true>(w[2], w[3]));
+            }
+            // -------------------------------------------------------- O += V^T w --
+            uint32_t vr[4][C::kVRun / 4];  // the thread's dims of keys 2t, 2t + 1, 2t + 8, 2t + 9
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int r = 2 * t + (j & 1) + (j >> 1) * 8;
+                if (D == 64) {
+                    const uint2 x = lds8(vt + chunk_at<D>(r, g >> 1) + (g & 1) * 8);
+                    vr[j][0] = x.x, vr[j][1] = x.y;
+                } else {
+#pragma unroll
+                    for (int i = 0; i < D / 128; ++i) {
+                        const uint4 x = lds16(vt + chunk_at<D>(r, i * 8 + g));
+                        vr[j][4 * i] = x.x, vr[j][4 * i + 1] = x.y, vr[j][4 * i + 2] = x.z, vr[j][4 * i + 3] = x.w;
                     }
                 }
             }
-            float w[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) w[i] = exp2_fast(z[i] - (m[i & 1] == -INFINITY ? 0.f : m[i & 1]));
-            l[0] = fmaf(w[0] + w[2], inv_sv, l[0]);
-            l[1] = fmaf(w[1] + w[3], inv_sv, l[1]);
-            // -------------------------------------------------------- O += V^T w --
-            // w as [key][row] pairs of rows; transposed into [row][key] pairs of keys
-            const uint32_t b0 = transpose8(pack2<true>(w[0], w[1]));
-            const uint32_t b1 = transpose8(pack2<true>(w[2], w[3]));
 #pragma unroll
             for (int j = 0; j < C::kVRun / 4; ++j) {
                 // four dims of keys 2t, 2t+1 (and 2t+8, 2t+9): pairs of keys a dim
@@ -359,37 +426,50 @@ __global__ void __launch_bounds__(kThreads, D <= 128 ? 3 : 2) attn_split_kernel(
                 uint32_t a0, a1, a2, a3;
                 widen4(x, a0, a1);
                 widen4(x8, a2, a3);
-                mma_f16(o[2 * j], a0, a1, a2, a3, b0, b1);
+#pragma unroll
+                for (int nb = 0; nb < NB; ++nb) mma_f16(o[nb][2 * j], a0, a1, a2, a3, b0[nb], b1[nb]);
                 widen4(y, a0, a1);
                 widen4(y8, a2, a3);
-                mma_f16(o[2 * j + 1], a0, a1, a2, a3, b0, b1);
+#pragma unroll
+                for (int nb = 0; nb < NB; ++nb) mma_f16(o[nb][2 * j + 1], a0, a1, a2, a3, b0[nb], b1[nb]);
             }
-            if (next < ke) load_v(next, page1);
-            page = page1;
-            page1 = page2;
+            if ((n & 31) == 31) page = page_next, sk = sk_next, sv = sv_next;
         }
 
         // ------------------------------------------------- join the block's four warps --
-        // o[2j][0], o[2j][2], o[2j+1][0], o[2j+1][2] of thread (g, t): four dims of row 2t
+        copies_wait<0>();
+        __syncthreads();  // every ring is drained
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
+        for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-            for (int d = 4; d < 32; d <<= 1) l[c] += __shfl_xor_sync(0xffffffffu, l[c], d);
-            if (g == 0) {
-                merge_m[warp][2 * t + c] = m[c];
-                merge_l[warp][2 * t + c] = l[c];
+            for (int c = 0; c < 2; ++c) {
+                const int r = nb * 8 + 2 * t + c;
+#pragma unroll
+                for (int d = 4; d < 32; d <<= 1) l[nb][c] += __shfl_xor_sync(0xffffffffu, l[nb][c], d);
+                if (g == 0) {
+                    merge_m[warp][r] = m[nb][c];
+                    merge_l[warp][r] = l[nb][c];
+                }
+#pragma unroll
+                for (int j = 0; j < C::kVRun / 4; ++j) {
+                    // o[2j][c], o[2j][2+c], o[2j+1][c], o[2j+1][2+c] of thread (g, t): four dims of row 2t + c
+                    const int dim = (D == 64) ? g * 8 + 4 * j : (j / 4) * 128 + g * 16 + (j % 4) * 4;
+                    *reinterpret_cast<float4 *>(merge_o + (warp * kRows + r) * D + dim) =
+                        make_float4(o[nb][2 * j][c], o[nb][2 * j][2 + c], o[nb][2 * j + 1][c], o[nb][2 * j + 1][2 + c]);
+                }
             }
-#pragma unroll
-            for (int j = 0; j < C::kVRun / 4; ++j) {
-                const int dim = (D == 64) ? g * 8 + 4 * j : (j / 4) * 128 + g * 16 + (j % 4) * 4;
-                *reinterpret_cast<float4 *>(&merge_o[warp][2 * t + c][dim]) =
-                    make_float4(o[2 * j][c], o[2 * j][2 + c], o[2 * j + 1][c], o[2 * j + 1][2 + c]);
-            }
-        }
         __syncthreads();
         const bool whole = s0 == 0 && s1 == sw.steps;
         // a block has at most two unfinished segments: the one it begins inside, and its last
         float *slot = p.part + ((int64_t)blockIdx.x * 2 + (s0 > 0 ? 0 : 1)) * C::kPart;
+        auto finish = [&](int r, int d, float4 acc, float top, float sum) {
+            const float inv = sum > 0.f || sum != sum ? 1.0f / sum : 0.f;
+            const int64_t tok = sw.q.q0 + (row0 + r) / v.G;
+            const int qh = head * v.G + (row0 + r) % v.G;
+            *reinterpret_cast<uint2 *>(p.out + tok * p.out_ld + (int64_t)qh * D + d) =
+                make_uint2(pack2<F16>(acc.x * inv, acc.y * inv), pack2<F16>(acc.z * inv, acc.w * inv));
+            if (p.lse && d == 0) p.lse[tok * v.QH + qh] = (top + log2f(sum)) * 0.6931471805599453f;
+        };
         for (int i = tid; i < rows * D / 4; i += kThreads) {
             const int r = i / (D / 4), d = i % (D / 4) * 4;
             float top = merge_m[0][r];
@@ -399,18 +479,13 @@ __global__ void __launch_bounds__(kThreads, D <= 128 ? 3 : 2) attn_split_kernel(
             float sum = 0.f;
             for (int k = 0; k < kWarps; ++k) {
                 const float f = exp2_fast(merge_m[k][r] - ref);
-                const float4 x = *reinterpret_cast<const float4 *>(&merge_o[k][r][d]);
+                const float4 x = *reinterpret_cast<const float4 *>(merge_o + (k * kRows + r) * D + d);
                 acc.x = fmaf(x.x, f, acc.x), acc.y = fmaf(x.y, f, acc.y);
                 acc.z = fmaf(x.z, f, acc.z), acc.w = fmaf(x.w, f, acc.w);
                 sum = fmaf(merge_l[k][r], f, sum);
             }
             if (whole) {
-                const float inv = sum > 0.f || sum != sum ? 1.0f / sum : 0.f;
-                const int64_t tok = sw.q.q0 + (row0 + r) / v.G;
-                const int qh = head * v.G + (row0 + r) % v.G;
-                *reinterpret_cast<uint2 *>(p.out + tok * p.out_ld + (int64_t)qh * D + d) =
-                    make_uint2(pack2<F16>(acc.x * inv, acc.y * inv), pack2<F16>(acc.z * inv, acc.w * inv));
-                if (p.lse && d == 0) p.lse[tok * v.QH + qh] = (top + log2f(sum)) * 0.6931471805599453f;
+                finish(r, d, acc, top, sum);
             } else {
                 __stcg(reinterpret_cast<float4 *>(slot + r * D + d), acc);
                 if (d == 0) {
@@ -421,11 +496,11 @@ __global__ void __launch_bounds__(kThreads, D <= 128 ? 3 : 2) attn_split_kernel(
         }
         if (!whole) {
             // ------------------------------- the last block of the segment joins its parts --
-            const int64_t c0 = seg_at / per, c1 = (seg_end - 1) / per;  // blocks that hold a part
+            const int64_t c0 = (seg_at + kSegCost) / per, c1 = (seg_end - 1) / per;  // blocks that hold a part
             __threadfence();
             __syncthreads();
             if (tid == 0) {
-                // the segment's ticket: only one segment can begin inside block c0 and leave it
+                // the segment's ticket: only one segment's first step can lie in block c0 and its last beyond
                 const unsigned n = (unsigned)(c1 - c0 + 1);
                 const unsigned got = atomicAdd(p.ticket + c0, 1u);
                 last_flag = got + 1 == n;
@@ -434,31 +509,27 @@ __global__ void __launch_bounds__(kThreads, D <= 128 ? 3 : 2) attn_split_kernel(
             __syncthreads();
             if (last_flag) {
                 __threadfence();
-                auto part = [&](int64_t c) {
-                    const bool inside = seg_at < c * per;  // block c begins inside the segment
-                    return p.part + (c * 2 + (inside ? 0 : 1)) * C::kPart;
-                };
+                const int parts = (int)(c1 - c0 + 1);
+                // the part of block c0 began with the segment's first step (slot 1), the others inside it (slot 0)
+                auto part = [&](int k) { return p.part + ((c0 + k) * 2 + (k > 0 ? 0 : 1)) * C::kPart; };
                 for (int i = tid; i < rows * D / 4; i += kThreads) {
                     const int r = i / (D / 4), d = i % (D / 4) * 4;
                     float top = -INFINITY;
-                    for (int64_t c = c0; c <= c1; ++c) top = fmaxf(top, __ldcg(part(c) + kRows * D + r));
+#pragma unroll 4
+                    for (int k = 0; k < parts; ++k) top = fmaxf(top, __ldcg(part(k) + kRows * D + r));
                     const float ref = top == -INFINITY ? 0.f : top;
                     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
                     float sum = 0.f;
-                    for (int64_t c = c0; c <= c1; ++c) {
-                        const float *x = part(c);
+#pragma unroll 4
+                    for (int k = 0; k < parts; ++k) {
+                        const float *x = part(k);
                         const float f = exp2_fast(__ldcg(x + kRows * D + r) - ref);
                         const float4 y = __ldcg(reinterpret_cast<const float4 *>(x + r * D + d));
                         acc.x = fmaf(y.x, f, acc.x), acc.y = fmaf(y.y, f, acc.y);
                         acc.z = fmaf(y.z, f, acc.z), acc.w = fmaf(y.w, f, acc.w);
                         sum = fmaf(__ldcg(x + kRows * D + kRows + r), f, sum);
                     }
-                    const float inv = sum > 0.f || sum != sum ? 1.0f / sum : 0.f;
-                    const int64_t tok = sw.q.q0 + (row0 + r) / v.G;
-                    const int qh = head * v.G + (row0 + r) % v.G;
-                    *reinterpret_cast<uint2 *>(p.out + tok * p.out_ld + (int64_t)qh * D + d) =
-                        make_uint2(pack2<F16>(acc.x * inv, acc.y * inv), pack2<F16>(acc.z * inv, acc.w * inv));
-                    if (p.lse && d == 0) p.lse[tok * v.QH + qh] = (top + log2f(sum)) * 0.6931471805599453f;
+                    finish(r, d, acc, top, sum);
                 }
             }
         }
@@ -466,24 +537,27 @@ __global__ void __launch_bounds__(kThreads, D <= 128 ? 3 : 2) attn_split_kernel(
     }
 }
 
-template <int D, bool F16>
+template <int D, int NB, bool F16>
 cudaError_t launch(const AttnArgs &a, cudaStream_t s) {
+    using C = Split<D, NB>;
+    cudaError_t e = cudaFuncSetAttribute(attn_split_kernel<D, NB, F16>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+    if (e != cudaSuccess) return e;
     LaunchScope scope(KC_ATTN_SPLIT, s);
-    int grid = device_info().sm_count * (D <= 128 ? 3 : 2);
+    int grid = device_info().sm_count * C::kBlocks;
     if (grid > kSplitMaxBlocks) grid = kSplitMaxBlocks;
-    attn_split_kernel<D, F16><<<grid, kThreads, 0, s>>>(a);
+    attn_split_kernel<D, NB, F16><<<grid, kThreads, C::kSmem, s>>>(a);
     return cudaGetLastError();
 }
 
 }  // namespace
 
-size_t split_part_floats(int D) { return (size_t)kSplitMaxBlocks * 2 * (kRows * D + 2 * kRows); }
+size_t split_part_floats(int D) { return (size_t)kSplitMaxBlocks * 2 * (8 * D + 16); }
 
 cudaError_t launch_attn_split(const AttnArgs &a, int D, int dtype, cudaStream_t s) {
     const bool f16 = dtype == MOE_DTYPE_F16;
-    if (D == 64) return f16 ? launch<64, true>(a, s) : launch<64, false>(a, s);
-    if (D == 128) return f16 ? launch<128, true>(a, s) : launch<128, false>(a, s);
-    return f16 ? launch<256, true>(a, s) : launch<256, false>(a, s);
+    if (D == 64) return f16 ? launch<64, 1, true>(a, s) : launch<64, 1, false>(a, s);
+    if (D == 128) return f16 ? launch<128, 1, true>(a, s) : launch<128, 1, false>(a, s);
+    return f16 ? launch<256, 1, true>(a, s) : launch<256, 1, false>(a, s);
 }
 
 }  // namespace moe
