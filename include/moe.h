@@ -401,9 +401,8 @@ typedef struct {
 
 /* Bytes of workspace for the two calls below on batches of up to max_seqs sequences and max_tokens
  * new tokens (the lengths in the cache do not matter).  0 for an invalid or unsupported config.
- * 256-byte aligned; zero it once after allocating: it begins with the status word that
- * moe_check_status reads, and holds tickets that every call leaves at zero.  Calls that overlap
- * must not share one. */
+ * 256-byte aligned; zero its first 256 bytes once after allocating: they hold the status word that
+ * moe_check_status reads.  The rest is scratch.  Calls that overlap must not share one. */
 size_t moe_attn_workspace_size(const moe_attn_config *cfg, int max_seqs, int max_tokens);
 
 /* Rotates q and k at their positions, writes q to q_out and k and v into the cache.

@@ -510,7 +510,7 @@ def alloc_attn_workspace(cfg: AttnConfig, max_seqs, max_tokens, device="cuda") -
     n = attn_workspace_size(cfg, max_seqs, max_tokens)
     if n == 0:
         raise MoeError("moe_attn_workspace_size", 3)
-    # zeroed once: the status word and the tickets
+    # zeroed once: the first 256 bytes are the device status word
     return torch.zeros(n, dtype=torch.uint8, device=device)
 
 

@@ -18,9 +18,8 @@
 //
 // Split: the batch's work is laid out as one line of 64-key steps (sequence by sequence, kv
 // head by kv head, row tile by row tile, each with a fixed cost in front) and cut into equal runs, one
-// a block, whatever the lengths.  A run that ends inside a segment leaves partial sums; the block
-// that finishes a segment last joins them in order, so the result does not depend on which one
-// that is.
+// a block, whatever the lengths.  A run that ends inside a segment leaves partial sums, which a second
+// kernel joins in order.
 #include "layer.h"
 
 namespace moe {
@@ -126,6 +125,90 @@ __device__ __forceinline__ uint32_t chunk_at(int r, int c) {
     return (uint32_t)(r * D + (c ^ (((r >> 1) & 3) << 1) ^ ((r & 1) << 2)) * 16);
 }
 
+// Four dims of a row's output, and its lse.
+template <int D, bool F16>
+__device__ __forceinline__ void finish_row(const AttnArgs &p, int q0, int row, int head, int d, float4 acc, float top, float sum) {
+    const float inv = sum > 0.f || sum != sum ? 1.0f / sum : 0.f;
+    const int64_t tok = q0 + row / p.kv.G;
+    const int qh = head * p.kv.G + row % p.kv.G;
+    *reinterpret_cast<uint2 *>(p.out + tok * p.out_ld + (int64_t)qh * D + d) =
+        make_uint2(pack2<F16>(acc.x * inv, acc.y * inv), pack2<F16>(acc.z * inv, acc.w * inv));
+    if (p.lse && d == 0) p.lse[tok * p.kv.QH + qh] = (top + log2f(sum)) * 0.6931471805599453f;
+}
+
+// Joins the parts of the segment whose first step block blockIdx.x of the split kernel had.  Two warps a
+// row, each every other part, in order: the result is the same whatever block was done when.  (One
+// block joining inside the split kernel, the last to arrive, took 25 us for the 76 parts of each
+// head of a 131,071-key cache; here all rows of all segments are joined at once.)
+template <int D, int NB, bool F16>
+__global__ void __launch_bounds__(512) attn_join_kernel(const __grid_constant__ AttnArgs p) {
+    using C = Split<D, NB>;
+    constexpr int kPer = D / 32;  // dims a lane
+    __shared__ float half[8][D];
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const SplitDesc d = p.desc[blockIdx.x];
+    if (d.parts <= 1) return;
+    const int warp = (int)threadIdx.x >> 5, lane = (int)threadIdx.x & 31, odd = warp & 1;
+    for (int r0 = 0; r0 < d.rows; r0 += 8) {
+        const int r = r0 + (warp >> 1);
+        float acc[kPer], sum = 0.f, top = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) acc[i] = 0.f;
+        // part k: slot 1 of the first block (the segment begins there), slot 0 of the others
+        const float *base = p.part + (int64_t)blockIdx.x * 2 * C::kPart;
+        auto part = [&](int k) { return base + (int64_t)(2 * k + (k > 0 ? 0 : 1)) * C::kPart; };
+        if (r < d.rows) {
+            for (int k = lane; k < d.parts; k += 32) top = fmaxf(top, __ldcg(part(k) + C::kRows * D + r));
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+            const float ref = top == -INFINITY ? 0.f : top;
+            for (int k0 = 0; k0 < d.parts; k0 += 32) {
+                float f = 0.f;  // of part k0 + lane
+                if (k0 + lane < d.parts) {
+                    const float *x = part(k0 + lane) + C::kRows * D + r;
+                    f = exp2_fast(__ldcg(x) - ref);
+                    sum = fmaf(__ldcg(x + C::kRows), f, sum);
+                }
+                const int n = min(32, d.parts - k0);
+#pragma unroll 8
+                for (int k = odd; k < n; k += 2) {
+                    const float fk = __shfl_sync(0xffffffffu, f, k);
+                    const float *x = part(k0 + k) + r * D + lane * kPer;
+                    float y[kPer];
+                    if (kPer == 2) {
+                        *reinterpret_cast<float2 *>(y) = __ldcg(reinterpret_cast<const float2 *>(x));
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < kPer; i += 4)
+                            *reinterpret_cast<float4 *>(y + i) = __ldcg(reinterpret_cast<const float4 *>(x + i));
+                    }
+#pragma unroll
+                    for (int i = 0; i < kPer; ++i) acc[i] = fmaf(y[i], fk, acc[i]);
+                }
+            }
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        }
+        if (odd && r < d.rows) {
+#pragma unroll
+            for (int i = 0; i < kPer; ++i) half[warp >> 1][lane + 32 * i] = acc[i];
+        }
+        __syncthreads();
+        if (!odd && r < d.rows) {
+#pragma unroll
+            for (int i = 0; i < kPer; ++i) acc[i] += half[warp >> 1][lane + 32 * i];
+            const float inv = sum > 0.f || sum != sum ? 1.0f / sum : 0.f;
+            const int64_t tok = d.q0 + (d.row0 + r) / p.kv.G;
+            const int qh = d.head * p.kv.G + (d.row0 + r) % p.kv.G;
+            uint32_t *out = reinterpret_cast<uint32_t *>(p.out + tok * p.out_ld + (int64_t)qh * D + lane * kPer);
+#pragma unroll
+            for (int i = 0; i < kPer; i += 2) out[i / 2] = pack2<F16>(acc[i] * inv, acc[i + 1] * inv);
+            if (p.lse && lane == 0) p.lse[tok * p.kv.QH + qh] = (top + log2f(sum)) * 0.6931471805599453f;
+        }
+        __syncthreads();
+    }
+}
+
 template <int D, int NB, bool F16>
 __global__ void __launch_bounds__(kThreads, Split<D, NB>::kBlocks) attn_split_kernel(const __grid_constant__ AttnArgs p) {
     using C = Split<D, NB>;
@@ -138,10 +221,11 @@ __global__ void __launch_bounds__(kThreads, Split<D, NB>::kBlocks) attn_split_ke
     __shared__ int found_b;
     __shared__ int seq_q0[kSeqCache], seq_n[kSeqCache], seq_kv[kSeqCache];
     __shared__ float merge_m[kWarps][kRows], merge_l[kWarps][kRows];
-    __shared__ int last_flag;
 
     const int tid = (int)threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int g = lane >> 2, t = lane & 3;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the join waits for this grid's end by itself
+    if (tid == 0) p.desc[blockIdx.x].parts = 0;
 
     // ------------------------------------------------- this block's run of the line --
     // its length, then the sequence that holds the run's first place
@@ -462,14 +546,6 @@ __global__ void __launch_bounds__(kThreads, Split<D, NB>::kBlocks) attn_split_ke
         const bool whole = s0 == 0 && s1 == sw.steps;
         // a block has at most two unfinished segments: the one it begins inside, and its last
         float *slot = p.part + ((int64_t)blockIdx.x * 2 + (s0 > 0 ? 0 : 1)) * C::kPart;
-        auto finish = [&](int r, int d, float4 acc, float top, float sum) {
-            const float inv = sum > 0.f || sum != sum ? 1.0f / sum : 0.f;
-            const int64_t tok = sw.q.q0 + (row0 + r) / v.G;
-            const int qh = head * v.G + (row0 + r) % v.G;
-            *reinterpret_cast<uint2 *>(p.out + tok * p.out_ld + (int64_t)qh * D + d) =
-                make_uint2(pack2<F16>(acc.x * inv, acc.y * inv), pack2<F16>(acc.z * inv, acc.w * inv));
-            if (p.lse && d == 0) p.lse[tok * v.QH + qh] = (top + log2f(sum)) * 0.6931471805599453f;
-        };
         for (int i = tid; i < rows * D / 4; i += kThreads) {
             const int r = i / (D / 4), d = i % (D / 4) * 4;
             float top = merge_m[0][r];
@@ -485,7 +561,7 @@ __global__ void __launch_bounds__(kThreads, Split<D, NB>::kBlocks) attn_split_ke
                 sum = fmaf(merge_l[k][r], f, sum);
             }
             if (whole) {
-                finish(r, d, acc, top, sum);
+                finish_row<D, F16>(p, sw.q.q0, row0 + r, head, d, acc, top, sum);
             } else {
                 __stcg(reinterpret_cast<float4 *>(slot + r * D + d), acc);
                 if (d == 0) {
@@ -494,45 +570,9 @@ __global__ void __launch_bounds__(kThreads, Split<D, NB>::kBlocks) attn_split_ke
                 }
             }
         }
-        if (!whole) {
-            // ------------------------------- the last block of the segment joins its parts --
-            const int64_t c0 = (seg_at + kSegCost) / per, c1 = (seg_end - 1) / per;  // blocks that hold a part
-            __threadfence();
-            __syncthreads();
-            if (tid == 0) {
-                // the segment's ticket: only one segment's first step can lie in block c0 and its last beyond
-                const unsigned n = (unsigned)(c1 - c0 + 1);
-                const unsigned got = atomicAdd(p.ticket + c0, 1u);
-                last_flag = got + 1 == n;
-                if (got + 1 == n) p.ticket[c0] = 0;
-            }
-            __syncthreads();
-            if (last_flag) {
-                __threadfence();
-                const int parts = (int)(c1 - c0 + 1);
-                // the part of block c0 began with the segment's first step (slot 1), the others inside it (slot 0)
-                auto part = [&](int k) { return p.part + ((c0 + k) * 2 + (k > 0 ? 0 : 1)) * C::kPart; };
-                for (int i = tid; i < rows * D / 4; i += kThreads) {
-                    const int r = i / (D / 4), d = i % (D / 4) * 4;
-                    float top = -INFINITY;
-#pragma unroll 4
-                    for (int k = 0; k < parts; ++k) top = fmaxf(top, __ldcg(part(k) + kRows * D + r));
-                    const float ref = top == -INFINITY ? 0.f : top;
-                    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-                    float sum = 0.f;
-#pragma unroll 4
-                    for (int k = 0; k < parts; ++k) {
-                        const float *x = part(k);
-                        const float f = exp2_fast(__ldcg(x + kRows * D + r) - ref);
-                        const float4 y = __ldcg(reinterpret_cast<const float4 *>(x + r * D + d));
-                        acc.x = fmaf(y.x, f, acc.x), acc.y = fmaf(y.y, f, acc.y);
-                        acc.z = fmaf(y.z, f, acc.z), acc.w = fmaf(y.w, f, acc.w);
-                        sum = fmaf(__ldcg(x + kRows * D + kRows + r), f, sum);
-                    }
-                    finish(r, d, acc, top, sum);
-                }
-            }
-        }
+        // the block with the segment's first step tells the join where its parts are
+        if (!whole && s0 == 0 && tid == 0)
+            p.desc[blockIdx.x] = SplitDesc{(int)((seg_end - 1) / per - blockIdx.x + 1), rows, sw.q.q0, row0, head};
         __syncthreads();  // merge buffers are free again
     }
 }
@@ -542,11 +582,26 @@ cudaError_t launch(const AttnArgs &a, cudaStream_t s) {
     using C = Split<D, NB>;
     cudaError_t e = cudaFuncSetAttribute(attn_split_kernel<D, NB, F16>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
     if (e != cudaSuccess) return e;
-    LaunchScope scope(KC_ATTN_SPLIT, s);
     int grid = device_info().sm_count * C::kBlocks;
     if (grid > kSplitMaxBlocks) grid = kSplitMaxBlocks;
-    attn_split_kernel<D, NB, F16><<<grid, kThreads, C::kSmem, s>>>(a);
-    return cudaGetLastError();
+    {
+        LaunchScope scope(KC_ATTN_SPLIT, s);
+        attn_split_kernel<D, NB, F16><<<grid, kThreads, C::kSmem, s>>>(a);
+        e = cudaGetLastError();
+        if (e != cudaSuccess) return e;
+    }
+    // launched while the split kernel still runs; its blocks wait for that kernel's end
+    LaunchScope scope(KC_ATTN_JOIN, s);
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)grid);
+    cfg.blockDim = dim3(512);
+    cfg.stream = s;
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, attn_join_kernel<D, NB, F16>, a);
 }
 
 }  // namespace

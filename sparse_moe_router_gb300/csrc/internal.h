@@ -30,6 +30,7 @@ enum KernelClass {
     KC_BLOCK_NORM,        // norms before and after a block, gate and residual scale
     KC_KV_APPEND,         // rotation and append into the paged cache
     KC_ATTN_SPLIT,        // attention over the cache, split along the keys (decode)
+    KC_ATTN_JOIN,         // the split parts of a sequence joined
     KC_ATTN_PROMPT,       // attention over the cache on the 5th-generation tensor cores (prompts)
     KC_COUNT
 };

@@ -35,6 +35,10 @@ struct AppendArgs {
 };
 cudaError_t launch_kv_append(const AppendArgs &a, int D, int dtype, cudaStream_t s);
 
+struct SplitDesc {
+    int parts, rows, q0, row0, head;  // parts 0: none
+};
+
 struct AttnArgs {
     KvView kv;
     const uint16_t *q;
@@ -43,9 +47,10 @@ struct AttnArgs {
     int64_t q_ld, out_ld;
     float scale_log2;  // softmax_scale * log2(e)
     int causal, window;
-    // split kernel: partial results and tickets, one pair of slots and one ticket a block
+    // split kernel: partial results, two slots a block, and where the segment is that begins in a block and
+    // goes on in others
     float *part;
-    unsigned *ticket;
+    SplitDesc *desc;
     // sequences with at least this many query rows a kv head (new tokens x G) are the prompt
     // kernel's, the others the split kernel's
     int prompt_rows;

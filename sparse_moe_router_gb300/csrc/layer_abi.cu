@@ -64,12 +64,12 @@ moe_status check_batch(const moe_attn_config &c, const moe_kv_cache *k, const mo
 constexpr int kPromptRows = 128;
 
 struct Layout {
-    size_t ticket, part, total;
+    size_t desc, part, total;
 };
 Layout layout(const moe_attn_config &c) {
     Layout l;
-    l.ticket = 256;  // behind the status word
-    l.part = l.ticket + kSplitMaxBlocks * sizeof(unsigned);
+    l.desc = 256;  // behind the status word
+    l.part = l.desc + (kSplitMaxBlocks * sizeof(SplitDesc) + 255) / 256 * 256;
     l.total = l.part + split_part_floats(c.head_dim) * sizeof(float);
     return l;
 }
@@ -227,7 +227,7 @@ moe_status moe_attention(const moe_attn_config *cfg, const moe_kv_cache *cache, 
     a.scale_log2 = softmax_scale * 1.4426950408889634f;
     a.causal = causal != 0;
     a.window = window;
-    a.ticket = reinterpret_cast<unsigned *>(static_cast<char *>(ws) + l.ticket);
+    a.desc = reinterpret_cast<SplitDesc *>(static_cast<char *>(ws) + l.desc);
     a.part = reinterpret_cast<float *>(static_cast<char *>(ws) + l.part);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     // Which sequences the prompt kernel takes goes by their own rows, which only the device knows; the host

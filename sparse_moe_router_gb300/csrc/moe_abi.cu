@@ -36,7 +36,7 @@ const char *const kClassNames[KC_COUNT] = {
     "router_gemm", "topk",          "permute",     "tile_prefix",   "gateup_gemm",
     "down_gemm",   "shared_gateup", "shared_down", "finalize",      "combine",
     "zero",        "decode_router", "decode_experts", "gather_x",
-    "decode_chain", "quantize", "block_norm", "kv_append", "attn_split", "attn_prompt"};
+    "decode_chain", "quantize", "block_norm", "kv_append", "attn_split", "attn_join", "attn_prompt"};
 }  // namespace
 
 const char *kernel_class_name(int kc) { return (kc >= 0 && kc < KC_COUNT) ? kClassNames[kc] : nullptr; }

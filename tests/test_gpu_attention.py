@@ -28,7 +28,6 @@ def run(s, q, causal=True, window=0, scale=None, spoil=True, out=None):
     lse = torch.full((s.T, s.QH), 9.0, device="cuda")
     abi.moe_attention(s.cfg, cache, batch, q, out, ws, lse=lse, softmax_scale=scale, causal=causal, window=window)
     assert abi.moe_check_status(ws) == 0
-    assert not ws[256:256 + 4096].any()  # tickets are back at zero
     return out, lse
 
 
