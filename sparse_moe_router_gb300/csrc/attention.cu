@@ -136,67 +136,81 @@ __device__ __forceinline__ void finish_row(const AttnArgs &p, int q0, int row, i
     if (p.lse && d == 0) p.lse[tok * p.kv.QH + qh] = (top + log2f(sum)) * 0.6931471805599453f;
 }
 
-// Joins the parts of the segment whose first step block blockIdx.x of the split kernel had.  Two warps a
-// row, each every other part, in order: the result is the same whatever block was done when.  (One
-// block joining inside the split kernel, the last to arrive, took 25 us for the 76 parts of each
-// head of a 131,071-key cache; here all rows of all segments are joined at once.)
+// Joins the parts of the segment whose first step block blockIdx.x of the split kernel had.  Its 16 warps
+// share the rows evenly; the warps of a row take every n-th part and are added in order: the result is the
+// same whatever block was done when.  (One block joining inside the split kernel, the last to arrive,
+// took 25 us for the 76 parts of each head of a 131,071-key cache.)
 template <int D, int NB, bool F16>
 __global__ void __launch_bounds__(512) attn_join_kernel(const __grid_constant__ AttnArgs p) {
     using C = Split<D, NB>;
     constexpr int kPer = D / 32;  // dims a lane
-    __shared__ float half[8][D];
+    constexpr int kBatch = D <= 128 ? 16 : 8;  // parts whose loads are in flight together
+    __shared__ float sums[16][D], tops[16], totals[16];
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const SplitDesc d = p.desc[blockIdx.x];
     if (d.parts <= 1) return;
-    const int warp = (int)threadIdx.x >> 5, lane = (int)threadIdx.x & 31, odd = warp & 1;
-    for (int r0 = 0; r0 < d.rows; r0 += 8) {
-        const int r = r0 + (warp >> 1);
+    const int warp = (int)threadIdx.x >> 5, lane = (int)threadIdx.x & 31;
+    int each = 16;  // warps a row, a power of two
+    while (each > 1 && each * d.rows > 16) each >>= 1;
+    const int w = warp % each;
+    // part k: slot 1 of the first block (the segment begins there), slot 0 of the others
+    const float *base = p.part + (int64_t)blockIdx.x * 2 * C::kPart;
+    auto part = [&](int k) { return base + (int64_t)(2 * k + (k > 0 ? 0 : 1)) * C::kPart; };
+    for (int r0 = 0; r0 < d.rows; r0 += 16 / each) {
+        const int r = r0 + warp / each;
+        const bool live = r < d.rows;
         float acc[kPer], sum = 0.f, top = -INFINITY;
 #pragma unroll
         for (int i = 0; i < kPer; ++i) acc[i] = 0.f;
-        // part k: slot 1 of the first block (the segment begins there), slot 0 of the others
-        const float *base = p.part + (int64_t)blockIdx.x * 2 * C::kPart;
-        auto part = [&](int k) { return base + (int64_t)(2 * k + (k > 0 ? 0 : 1)) * C::kPart; };
-        if (r < d.rows) {
-            for (int k = lane; k < d.parts; k += 32) top = fmaxf(top, __ldcg(part(k) + C::kRows * D + r));
+        for (int k0 = w; live && k0 < d.parts; k0 += kBatch * each) {
+            float y[kBatch][kPer], m[kBatch], l[kBatch];
 #pragma unroll
-            for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-            const float ref = top == -INFINITY ? 0.f : top;
-            for (int k0 = 0; k0 < d.parts; k0 += 32) {
-                float f = 0.f;  // of part k0 + lane
-                if (k0 + lane < d.parts) {
-                    const float *x = part(k0 + lane) + C::kRows * D + r;
-                    f = exp2_fast(__ldcg(x) - ref);
-                    sum = fmaf(__ldcg(x + C::kRows), f, sum);
-                }
-                const int n = min(32, d.parts - k0);
-#pragma unroll 8
-                for (int k = odd; k < n; k += 2) {
-                    const float fk = __shfl_sync(0xffffffffu, f, k);
-                    const float *x = part(k0 + k) + r * D + lane * kPer;
-                    float y[kPer];
-                    if (kPer == 2) {
-                        *reinterpret_cast<float2 *>(y) = __ldcg(reinterpret_cast<const float2 *>(x));
-                    } else {
+            for (int j = 0; j < kBatch; ++j) {
+                const int k = k0 + j * each;
+                const bool in = k < d.parts;
+                const float *x = part(in ? k : w);
+                m[j] = in ? __ldcg(x + C::kRows * D + r) : -INFINITY;
+                l[j] = __ldcg(x + C::kRows * D + C::kRows + r);
+                if (kPer == 2) {
+                    *reinterpret_cast<float2 *>(y[j]) = __ldcg(reinterpret_cast<const float2 *>(x + r * D + lane * kPer));
+                } else {
 #pragma unroll
-                        for (int i = 0; i < kPer; i += 4)
-                            *reinterpret_cast<float4 *>(y + i) = __ldcg(reinterpret_cast<const float4 *>(x + i));
-                    }
-#pragma unroll
-                    for (int i = 0; i < kPer; ++i) acc[i] = fmaf(y[i], fk, acc[i]);
+                    for (int i = 0; i < kPer; i += 4)
+                        *reinterpret_cast<float4 *>(y[j] + i) = __ldcg(reinterpret_cast<const float4 *>(x + r * D + lane * kPer + i));
                 }
             }
+            float to = top;
 #pragma unroll
-            for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-        }
-        if (odd && r < d.rows) {
+            for (int j = 0; j < kBatch; ++j) to = fmaxf(to, m[j]);
+            const float ref = to == -INFINITY ? 0.f : to, f = exp2_fast(top - ref);
+            top = to;
+            sum *= f;
 #pragma unroll
-            for (int i = 0; i < kPer; ++i) half[warp >> 1][lane + 32 * i] = acc[i];
+            for (int i = 0; i < kPer; ++i) acc[i] *= f;
+#pragma unroll
+            for (int j = 0; j < kBatch; ++j) {
+                const float e = exp2_fast(m[j] - ref);
+                sum = fmaf(l[j], e, sum);
+#pragma unroll
+                for (int i = 0; i < kPer; ++i) acc[i] = fmaf(y[j][i], e, acc[i]);
+            }
         }
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) sums[warp][lane + 32 * i] = acc[i];
+        if (lane == 0) tops[warp] = top, totals[warp] = sum;
         __syncthreads();
-        if (!odd && r < d.rows) {
+        if (live && w == 0) {
+            for (int x = 1; x < each; ++x) top = fmaxf(top, tops[warp + x]);
+            const float ref = top == -INFINITY ? 0.f : top;
+            sum = 0.f;
 #pragma unroll
-            for (int i = 0; i < kPer; ++i) acc[i] += half[warp >> 1][lane + 32 * i];
+            for (int i = 0; i < kPer; ++i) acc[i] = 0.f;
+            for (int x = 0; x < each; ++x) {
+                const float e = exp2_fast(tops[warp + x] - ref);
+                sum = fmaf(totals[warp + x], e, sum);
+#pragma unroll
+                for (int i = 0; i < kPer; ++i) acc[i] = fmaf(sums[warp + x][lane + 32 * i], e, acc[i]);
+            }
             const float inv = sum > 0.f || sum != sum ? 1.0f / sum : 0.f;
             const int64_t tok = d.q0 + (d.row0 + r) / p.kv.G;
             const int qh = d.head * p.kv.G + (d.row0 + r) % p.kv.G;
