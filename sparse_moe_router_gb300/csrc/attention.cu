@@ -25,7 +25,7 @@
 namespace moe {
 namespace {
 
-constexpr int kWarps = 4;
+constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
 constexpr int kStep = 16 * kWarps;  // keys a block takes at once, 16 a warp
 
@@ -96,7 +96,7 @@ struct Split {
     static constexpr int kRingBytes = kWarps * kRing * 2 * kTile;
     static constexpr int kMergeBytes = kWarps * kRows * D * 4;  // over the ring, once it is drained
     static constexpr int kSmem = kRingBytes > kMergeBytes ? kRingBytes : kMergeBytes;
-    static constexpr int kBlocks = D * NB <= 128 ? 4 : D * NB <= 256 ? 2 : 1;  // resident a SM
+    static constexpr int kBlocks = D * NB <= 128 ? 2 : 1;  // resident a SM
 };
 
 __device__ __forceinline__ void copy16(uint32_t dst, const void *src, bool live) {  // zeros if not live
