@@ -97,9 +97,14 @@ struct Split {
     static constexpr int kMergeBytes = kWarps * kRows * D * 4;  // over the ring, once it is drained
     static constexpr int kSmem = kRingBytes > kMergeBytes ? kRingBytes : kMergeBytes;
     static constexpr int kBlocks = D * NB <= 128 ? 2 : 1;  // resident a SM
+    static constexpr bool kQShared = NB > 1;               // query fragments in shared memory, not registers
+    static constexpr int kGrid = kSplitMaxSms * kBlocks;   // blocks at most
 };
 
-__device__ __forceinline__ void copy16(uint32_t dst, const void *src, bool live) {  // zeros if not live
+__device__ __forceinline__ void copy16(uint32_t dst, const void *src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy16_or_zero(uint32_t dst, const void *src, bool live) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(live ? 16 : 0) : "memory");
 }
 __device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
@@ -235,6 +240,8 @@ __global__ void __launch_bounds__(kThreads, Split<D, NB>::kBlocks) attn_split_ke
     __shared__ int found_b;
     __shared__ int seq_q0[kSeqCache], seq_n[kSeqCache], seq_kv[kSeqCache];
     __shared__ float merge_m[kWarps][kRows], merge_l[kWarps][kRows];
+    __shared__ uint2 q_frag[C::kQShared ? NB * C::kKLoads * 4 * 32 : 1];  // [nb][run][k-step][lane]
+    __shared__ int q_exps[C::kQShared ? kRows : 1];
 
     const int tid = (int)threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int g = lane >> 2, t = lane & 3;
@@ -335,19 +342,31 @@ __global__ void __launch_bounds__(kThreads, Split<D, NB>::kBlocks) attn_split_ke
         };
         int page = page_at(lane), page_next = 0;
         float sk = __ldg(v.k_scale + page), sv = __ldg(v.v_scale + page), sk_next = 1.f, sv_next = 1.f;
-        auto fill = [&](int n) {  // tile n into its place of the ring
+        // chunk i of a lane is chunk i * 32 + lane of the tile; rows 4 apart differ in bit 2 of the place
+        const int cr = lane / (D / 16), cc = lane % (D / 16);
+        uint32_t fill_at = my_ring;  // the ring place that is filled next
+        auto fill = [&](int n) {     // tile n
             if (n < tiles) {
                 const int pg = __shfl_sync(0xffffffffu, (n & 31) >= C::kRing - 1 || n < 32 ? page : page_next, n & 31);
                 const int key = ks0 + n * kStep;
                 const int64_t off = (((int64_t)pg << v.log_p) + (key & (v.P - 1))) * D + lane * 16;
-                const uint32_t dst = my_ring + n % C::kRing * 2 * C::kTile;
+                const uint8_t *ks = v.k_codes + off, *vs = v.v_codes + off;
+                if (key + 16 <= sw.q.kv) {
 #pragma unroll
-                for (int i = 0; i < D / 32; ++i) {
-                    const int r = (i * 32 + lane) / (D / 16), c = (i * 32 + lane) % (D / 16);
-                    const bool live = key + r < sw.q.kv;  // slots past the end hold anything
-                    copy16(dst + chunk_at<D>(r, c), v.k_codes + off + i * 512, live);
-                    copy16(dst + C::kTile + chunk_at<D>(r, c), v.v_codes + off + i * 512, live);
+                    for (int i = 0; i < D / 32; ++i) {
+                        const uint32_t dst = fill_at + chunk_at<D>(i * (512 / D) + cr, cc);
+                        copy16(dst, ks + i * 512);
+                        copy16(dst + C::kTile, vs + i * 512);
+                    }
+                } else {  // slots past the end hold anything: zeros instead
+#pragma unroll
+                    for (int i = 0; i < D / 32; ++i) {
+                        const int r = i * (512 / D) + cr;
+                        copy16_or_zero(fill_at + chunk_at<D>(r, cc), ks + i * 512, key + r < sw.q.kv);
+                        copy16_or_zero(fill_at + C::kTile + chunk_at<D>(r, cc), vs + i * 512, key + r < sw.q.kv);
+                    }
                 }
+                fill_at = fill_at == my_ring + (C::kRing - 1) * 2 * C::kTile ? my_ring : fill_at + 2 * C::kTile;
             }
             copies_commit();
         };
@@ -355,12 +374,14 @@ __global__ void __launch_bounds__(kThreads, Split<D, NB>::kBlocks) attn_split_ke
         for (int n = 0; n < C::kRing - 1; ++n) fill(n);
 
         // q rows: fragment rows are n = g, dims i*64 + t*16 + 4s of the four k-steps of run i
-        uint32_t qf[NB][C::kKLoads][4][2];
+        uint2 qf[C::kQShared ? 1 : C::kKLoads][4];
         float mul[NB][2];
         int lo[NB][2], hi[NB][2];  // the keys that rows 2t, 2t + 1 see
         int all_lo = 0, all_hi = 0x7fffffff;  // keys in [all_lo, all_hi) are seen by every row
-#pragma unroll
-        for (int nb = 0; nb < NB; ++nb) {
+        int q_exp = 0;
+        // every warp makes the one tile's fragments, or warp nb those of row tile nb for all
+        if (!C::kQShared || warp < NB) {
+            const int nb = C::kQShared ? warp : 0;
             float amax = 0.f;
             uint4 qv[C::kKLoads][2];
             const int r = row0 + nb * 8 + g;
@@ -383,7 +404,7 @@ __global__ void __launch_bounds__(kThreads, Split<D, NB>::kBlocks) attn_split_ke
             amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
             amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
             // largest magnitude into [1, 2): fp16 then holds every bf16 digit down to 2^-17 of it
-            const int q_exp = amax > 0.f ? max(min((int)(__float_as_uint(amax) >> 23) - 127, 126), -126) : 0;
+            q_exp = amax > 0.f ? max(min((int)(__float_as_uint(amax) >> 23) - 127, 126), -126) : 0;
             const float inv = pow2f(-q_exp);
 #pragma unroll
             for (int i = 0; i < C::kKLoads; ++i)
@@ -392,13 +413,22 @@ __global__ void __launch_bounds__(kThreads, Split<D, NB>::kBlocks) attn_split_ke
                     float x[8];
                     unpack8<F16>(qv[i][c], x);
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) qf[nb][i][2 * c + (j >> 1)][j & 1] = pack2<true>(x[2 * j] * inv, x[2 * j + 1] * inv);
+                    for (int j = 0; j < 2; ++j) {
+                        const uint2 f = make_uint2(pack2<true>(x[4 * j] * inv, x[4 * j + 1] * inv),
+                                                   pack2<true>(x[4 * j + 2] * inv, x[4 * j + 3] * inv));
+                        if (C::kQShared) q_frag[((nb * C::kKLoads + i) * 4 + 2 * c + j) * 32 + lane] = f;
+                        else qf[i][2 * c + j] = f;
+                    }
                 }
+            if (C::kQShared && t == 0) q_exps[nb * 8 + g] = q_exp;
+        }
+        if (C::kQShared) __syncthreads();
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
-                const int e = __shfl_sync(0xffffffffu, q_exp, (2 * t + c) * 4);
-                mul[nb][c] = p.scale_log2 * pow2f(e);
                 const int rr = nb * 8 + 2 * t + c, pos = first_pos + (row0 + rr) / v.G;
+                mul[nb][c] = p.scale_log2 * pow2f(C::kQShared ? q_exps[rr] : __shfl_sync(0xffffffffu, q_exp, (2 * t + c) * 4));
                 hi[nb][c] = p.causal ? min(sw.q.kv, pos + 1) : sw.q.kv;
                 lo[nb][c] = p.window > 0 ? max(0, pos + 1 - p.window) : 0;
                 if (rr < rows) {
@@ -406,7 +436,6 @@ __global__ void __launch_bounds__(kThreads, Split<D, NB>::kBlocks) attn_split_ke
                     all_hi = min(all_hi, hi[nb][c]);
                 }
             }
-        }
 #pragma unroll
         for (int o = 1; o < 4; o <<= 1) {
             all_lo = max(all_lo, __shfl_xor_sync(0xffffffffu, all_lo, o));
@@ -421,13 +450,15 @@ __global__ void __launch_bounds__(kThreads, Split<D, NB>::kBlocks) attn_split_ke
 #pragma unroll
             for (int i = 0; i < kMT; ++i) o[nb][i][0] = o[nb][i][1] = o[nb][i][2] = o[nb][i][3] = 0.f;
         }
+        uint32_t read_at = my_ring;
         for (int n = 0; n < tiles; ++n) {
             copies_wait<C::kRing - 2>();
             __syncwarp();  // tile n is there for all lanes, and all are done with the tile before it
             if ((n & 31) == 0 && n + 32 < tiles) page_next = page_at(n + 32 + lane);
             if ((n & 31) == 16 && n + 16 < tiles) sk_next = __ldg(v.k_scale + page_next), sv_next = __ldg(v.v_scale + page_next);
             fill(n + C::kRing - 1);
-            const uint32_t kt = my_ring + n % C::kRing * 2 * C::kTile, vt = kt + C::kTile;
+            const uint32_t kt = read_at, vt = kt + C::kTile;
+            read_at = read_at == my_ring + (C::kRing - 1) * 2 * C::kTile ? my_ring : read_at + 2 * C::kTile;
             const float tsk = __shfl_sync(0xffffffffu, sk, n & 31), tsv = __shfl_sync(0xffffffffu, sv, n & 31);
             const int key0 = ks0 + n * kStep;
             // ------------------------------------------------------------ S = K q --
@@ -446,7 +477,10 @@ __global__ void __launch_bounds__(kThreads, Split<D, NB>::kBlocks) attn_split_ke
                     widen4(w0[j], a0, a2);
                     widen4(w1[j], a1, a3);
 #pragma unroll
-                    for (int nb = 0; nb < NB; ++nb) mma_f16(j & 1 ? s2[nb] : s[nb], a0, a1, a2, a3, qf[nb][i][j][0], qf[nb][i][j][1]);
+                    for (int nb = 0; nb < NB; ++nb) {
+                        const uint2 f = C::kQShared ? q_frag[((nb * C::kKLoads + i) * 4 + j) * 32 + lane] : qf[C::kQShared ? 0 : i][j];
+                        mma_f16(j & 1 ? s2[nb] : s[nb], a0, a1, a2, a3, f.x, f.y);
+                    }
                 }
             }
             // ------------------------------------------------------------- softmax --
@@ -596,8 +630,8 @@ cudaError_t launch(const AttnArgs &a, cudaStream_t s) {
     using C = Split<D, NB>;
     cudaError_t e = cudaFuncSetAttribute(attn_split_kernel<D, NB, F16>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
     if (e != cudaSuccess) return e;
-    int grid = device_info().sm_count * C::kBlocks;
-    if (grid > kSplitMaxBlocks) grid = kSplitMaxBlocks;
+    const int sms = device_info().sm_count < kSplitMaxSms ? device_info().sm_count : kSplitMaxSms;
+    const int grid = sms * C::kBlocks;
     {
         LaunchScope scope(KC_ATTN_SPLIT, s);
         attn_split_kernel<D, NB, F16><<<grid, kThreads, C::kSmem, s>>>(a);
@@ -620,13 +654,24 @@ cudaError_t launch(const AttnArgs &a, cudaStream_t s) {
 
 }  // namespace
 
-size_t split_part_floats(int D) { return (size_t)kSplitMaxBlocks * 2 * (8 * D + 16); }
+size_t split_part_floats(int D) {
+    auto most = [](size_t a, size_t b) { return a > b ? a : b; };
+    if (D == 64) return most(Split<64, 1>::kGrid * 2 * Split<64, 1>::kPart, Split<64, 4>::kGrid * 2 * Split<64, 4>::kPart);
+    if (D == 128) return most(Split<128, 1>::kGrid * 2 * Split<128, 1>::kPart, Split<128, 4>::kGrid * 2 * Split<128, 4>::kPart);
+    return most(Split<256, 1>::kGrid * 2 * Split<256, 1>::kPart, Split<256, 2>::kGrid * 2 * Split<256, 2>::kPart);
+}
 
-cudaError_t launch_attn_split(const AttnArgs &a, int D, int dtype, cudaStream_t s) {
-    const bool f16 = dtype == MOE_DTYPE_F16;
-    if (D == 64) return f16 ? launch<64, 1, true>(a, s) : launch<64, 1, false>(a, s);
-    if (D == 128) return f16 ? launch<128, 1, true>(a, s) : launch<128, 1, false>(a, s);
-    return f16 ? launch<256, 1, true>(a, s) : launch<256, 1, false>(a, s);
+template <int D, int NB>
+cudaError_t by_dtype(const AttnArgs &a, int dtype, cudaStream_t s) {
+    return dtype == MOE_DTYPE_F16 ? launch<D, NB, true>(a, s) : launch<D, NB, false>(a, s);
+}
+
+// rows: query rows a sequence and kv head, on average.  One tile of 8 rows up to 8 of them; beyond, 4 tiles
+// (2 at D = 256) share each key tile that is read and widened.
+cudaError_t launch_attn_split(const AttnArgs &a, int D, int dtype, int rows, cudaStream_t s) {
+    if (D == 64) return rows > 8 ? by_dtype<64, 4>(a, dtype, s) : by_dtype<64, 1>(a, dtype, s);
+    if (D == 128) return rows > 8 ? by_dtype<128, 4>(a, dtype, s) : by_dtype<128, 1>(a, dtype, s);
+    return rows > 8 ? by_dtype<256, 2>(a, dtype, s) : by_dtype<256, 1>(a, dtype, s);
 }
 
 }  // namespace moe

@@ -55,11 +55,11 @@ struct AttnArgs {
     // kernel's, the others the split kernel's
     int prompt_rows;
 };
-// Blocks the split kernel may have (its workspace is sized for them).
-constexpr int kSplitMaxBlocks = 1024;
+// The workspace is sized for so many SMs; the split kernel has one or two blocks on each.
+constexpr int kSplitMaxSms = 160, kSplitMaxBlocks = 2 * kSplitMaxSms;
 // Floats of workspace the split kernel needs for partial results.
 size_t split_part_floats(int D);
-cudaError_t launch_attn_split(const AttnArgs &a, int D, int dtype, cudaStream_t s);
+cudaError_t launch_attn_split(const AttnArgs &a, int D, int dtype, int rows, cudaStream_t s);
 cudaError_t launch_attn_prompt(const AttnArgs &a, int D, int dtype, cudaStream_t s);  // D 64 or 128
 
 struct NormArgs {

@@ -62,6 +62,8 @@ moe_status check_batch(const moe_attn_config &c, const moe_kv_cache *k, const mo
 
 // Query rows a kv head from which a sequence goes to the prompt kernel.
 constexpr int kPromptRows = 128;
+// Mean rows a sequence and kv head below which a batch is a decode step, all of it the split kernel's.
+constexpr int kPromptMean = 33;
 
 struct Layout {
     size_t desc, part, total;
@@ -230,12 +232,15 @@ moe_status moe_attention(const moe_attn_config *cfg, const moe_kv_cache *cache, 
     a.desc = reinterpret_cast<SplitDesc *>(static_cast<char *>(ws) + l.desc);
     a.part = reinterpret_cast<float *>(static_cast<char *>(ws) + l.part);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    // Which sequences the prompt kernel takes goes by their own rows, which only the device knows; the host
-    // leaves out a kernel that cannot have any.
-    const int64_t rows = (int64_t)batch->n_tokens * a.kv.G;
-    a.prompt_rows = c.head_dim <= 128 ? kPromptRows : INT_MAX;
-    if (rows >= a.prompt_rows) MOE_CUDA(launch_attn_prompt(a, c.head_dim, c.dtype, s));
-    if (batch->n_seqs > 1 || rows < a.prompt_rows) MOE_CUDA(launch_attn_split(a, c.head_dim, c.dtype, s));
+    // Which sequences the prompt kernel takes goes by their own rows, which only the device knows.  The host
+    // leaves a kernel out that has none for sure, and the prompt kernel in a step of few tokens a
+    // sequence: its launch would cost more (5 us) than the rare long run among them.
+    const int64_t rows = (int64_t)batch->n_tokens * a.kv.G, mean = rows / batch->n_seqs;
+    const bool prompts = c.head_dim <= 128 && rows >= kPromptRows && mean >= kPromptMean;
+    a.prompt_rows = prompts ? kPromptRows : INT_MAX;
+    if (prompts) MOE_CUDA(launch_attn_prompt(a, c.head_dim, c.dtype, s));
+    if (batch->n_seqs > 1 || !prompts)
+        MOE_CUDA(launch_attn_split(a, c.head_dim, c.dtype, (int)(mean < kPromptRows ? mean : kPromptRows), s));
     return MOE_OK;
 }
 
