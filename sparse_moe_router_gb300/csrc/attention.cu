@@ -666,12 +666,11 @@ cudaError_t by_dtype(const AttnArgs &a, int dtype, cudaStream_t s) {
     return dtype == MOE_DTYPE_F16 ? launch<D, NB, true>(a, s) : launch<D, NB, false>(a, s);
 }
 
-// rows: query rows a sequence and kv head, on average.  One tile of 8 rows up to 8 of them; beyond, 4 tiles
-// (2 at D = 256) share each key tile that is read and widened.
-cudaError_t launch_attn_split(const AttnArgs &a, int D, int dtype, int rows, cudaStream_t s) {
-    if (D == 64) return rows > 8 ? by_dtype<64, 4>(a, dtype, s) : by_dtype<64, 1>(a, dtype, s);
-    if (D == 128) return rows > 8 ? by_dtype<128, 4>(a, dtype, s) : by_dtype<128, 1>(a, dtype, s);
-    return rows > 8 ? by_dtype<256, 2>(a, dtype, s) : by_dtype<256, 1>(a, dtype, s);
+// shared: 4 row tiles (2 at D = 256) share each key tile that is read and widened.
+cudaError_t launch_attn_split(const AttnArgs &a, int D, int dtype, bool shared, cudaStream_t s) {
+    if (D == 64) return shared ? by_dtype<64, 4>(a, dtype, s) : by_dtype<64, 1>(a, dtype, s);
+    if (D == 128) return shared ? by_dtype<128, 4>(a, dtype, s) : by_dtype<128, 1>(a, dtype, s);
+    return shared ? by_dtype<256, 2>(a, dtype, s) : by_dtype<256, 1>(a, dtype, s);
 }
 
 }  // namespace moe

@@ -64,6 +64,10 @@ moe_status check_batch(const moe_attn_config &c, const moe_kv_cache *k, const mo
 constexpr int kPromptRows = 128;
 // Mean rows a sequence and kv head below which a batch is a decode step, all of it the split kernel's.
 constexpr int kPromptMean = 33;
+// Cached tokens (as many as the page table can name) from which the split kernel's row tiles share key
+// tiles.  Below, the SMs are short of work and more, smaller segments end sooner: 8 sequences of 32 rows, D = 128,
+// 64,000 keys 25.7 us shared and 26.7 not, 256,000 keys 53.6 and 76.6; one of 8,000 keys 27.4 and 14.2.
+constexpr int kManyKeys = 1 << 17;
 
 struct Layout {
     size_t desc, part, total;
@@ -240,7 +244,8 @@ moe_status moe_attention(const moe_attn_config *cfg, const moe_kv_cache *cache, 
     a.prompt_rows = prompts ? kPromptRows : INT_MAX;
     if (prompts) MOE_CUDA(launch_attn_prompt(a, c.head_dim, c.dtype, s));
     if (batch->n_seqs > 1 || !prompts)
-        MOE_CUDA(launch_attn_split(a, c.head_dim, c.dtype, (int)(mean < kPromptRows ? mean : kPromptRows), s));
+        MOE_CUDA(launch_attn_split(a, c.head_dim, c.dtype,
+                                   mean > 8 && (int64_t)batch->n_seqs * batch->max_pages * c.page_size >= kManyKeys, s));
     return MOE_OK;
 }
 

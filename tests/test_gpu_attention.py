@@ -97,6 +97,23 @@ def test_prompt_masks(causal, window, QH, KH, D, P):
     check(s, q, out, lse, causal, window)
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("QH,KH,D,P", [(16, 2, 128, 64), (6, 2, 64, 16), (4, 1, 256, 32), (24, 2, 128, 128)])
+def test_row_tiles_that_share_keys(dtype, QH, KH, D, P):
+    """A few tokens a sequence in a table that could name more than 2^17 tokens: the form whose row tiles
+    share key tiles."""
+    s = Setup([(4, 300), (7, 7), (3, 1000), (9, 4), (0, 20), (5, 129)], QH, KH, D, P, dtype=dtype, seed=D)
+    pages = (1 << 17) // (6 * P) + 1
+    wide = torch.full((6, pages), -7, dtype=torch.int32)
+    wide[:, :s.table.shape[1]] = s.table
+    s.table = wide
+    q = make_q(s)
+    out, lse = run(s, q)
+    check(s, q, out, lse)
+    out, lse = run(s, q, window=70)
+    check(s, q, out, lse, window=70)
+
+
 @pytest.mark.parametrize("lens", [[(1, 900), (2, 77)], [(300, 700)]], ids=["tokens", "prompt"])
 def test_sharp_and_shifted_logits(lens):
     """Logits in the hundreds: the running reference moves often, most weights vanish; pages whose scales
