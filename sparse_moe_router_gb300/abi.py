@@ -217,6 +217,14 @@ def _stream(stream):
     return ctypes.c_void_p(stream.cuda_stream)
 
 
+def _raw_stream(stream, device):
+    """The stream's handle as a number; without one, the current stream of the tensors' device, looked up
+    without building a Stream object (a microsecond of a small call)."""
+    if stream is not None:
+        return stream.cuda_stream
+    return torch._C._cuda_getCurrentRawStream(device)
+
+
 def _check(fn, st):
     if st != MOE_OK:
         raise MoeError(fn, st)
@@ -395,31 +403,35 @@ def quantize_layer(layer: dict, stream=None) -> dict:
 # ------------------------------------------- norms, paged cache, attention (include/moe.h) --
 
 _DTYPES = {torch.bfloat16: 0, torch.float16: 1}
+_TORCH_DTYPES = (torch.bfloat16, torch.float16)
 _GATES = {"none": 0, "channel": 1, "token": 2, "element": 3}
 
 
-def _rows(t, name, width, dtype, rows=None):
+def _rows(t, name, width, dtype, rows):
     """Row stride of an activation tensor: [T, width], or [T, heads, dim] with heads * dim == width,
-    whose rows may lie apart but are themselves contiguous."""
-    if not t.is_cuda:
-        raise ValueError("%s must be on a CUDA device" % name)
-    if _DTYPES.get(t.dtype) != dtype:
-        raise ValueError("%s has dtype %s, not the config's" % (name, t.dtype))
+    whose rows may lie apart but are themselves contiguous.  rows: T, or -1 if it is not known yet."""
     shape, stride = t.shape, t.stride()
-    if len(shape) == 3:
-        ok = shape[1] * shape[2] == width and stride[2] == 1 and (stride[1] == shape[2] or shape[1] == 1)
+    if len(shape) == 2:
+        ok = shape[1] == width and (stride[1] == 1 or width == 1)
     else:
-        ok = len(shape) == 2 and shape[1] == width and (stride[1] == 1 or width == 1)
-    if not ok or (rows is not None and shape[0] != rows):
-        raise ValueError("%s has shape %s and strides %s, not %s rows of %d values" %
-                         (name, tuple(shape), tuple(stride), "T" if rows is None else rows, width))
-    return stride[0] if shape[0] > 1 else max(stride[0], width)
+        ok = len(shape) == 3 and shape[1] * shape[2] == width and stride[2] == 1 and (stride[1] == shape[2] or shape[1] == 1)
+    if not ok or (shape[0] != rows and rows >= 0) or t.dtype is not dtype or not t.is_cuda:
+        raise ValueError("%s (%s, %s, strides %s, %s) is not %s rows of %d values of %s on a CUDA device" %
+                         (name, tuple(shape), t.dtype, tuple(stride), t.device, "T" if rows < 0 else rows, width, dtype))
+    return stride[0] if shape[0] > 1 or stride[0] > width else width
+
+
+def _vector(t, name, width, dtype):
+    """Pointer of a weight: `width` contiguous values."""
+    if t.numel() != width or t.dtype is not dtype or not t.is_cuda or not t.is_contiguous():
+        raise ValueError("%s must be %d contiguous values of %s on a CUDA device" % (name, width, dtype))
+    return t.data_ptr()
 
 
 def _device_array(t, name, dtype, shape=None):
-    if not t.is_cuda or not t.is_contiguous() or t.dtype != dtype:
+    if not t.is_cuda or not t.is_contiguous() or t.dtype is not dtype:
         raise ValueError("%s must be a contiguous CUDA tensor of %s" % (name, dtype))
-    if shape is not None and tuple(t.shape) != tuple(shape):
+    if shape is not None and t.shape != shape:
         raise ValueError("%s has shape %s, not %s" % (name, tuple(t.shape), tuple(shape)))
     return t.data_ptr()
 
@@ -432,29 +444,35 @@ def norm_config(hidden, dtype=torch.bfloat16, gate="none", sigmoid=False, unit_o
 def moe_block_norm(cfg: NormConfig, x, resid, resid_out, y, gate=None, w_post=None, w_pre=None, stream=None):
     """resid_out = resid + scale * g * norm(x); y = norm(resid_out).  x, resid, resid_out, y: [T, H] or
     None; gate as the config says: [H] or [1, H], [T] or [T, 1], [T, H]; w_post, w_pre: [H] or None."""
-    H, dt = cfg.hidden, cfg.dtype
-    io = NormIO()
-    T = None
-    for name, t in (("x", x), ("resid", resid), ("resid_out", resid_out), ("y", y)):
-        if t is not None:
-            setattr(io, name + "_ld", _rows(t, name, H, dt, T))
-            setattr(io, name, t.data_ptr())
-            T = t.shape[0]
-    for name, t in (("w_post", w_post), ("w_pre", w_pre)):
-        if t is not None:
-            if t.numel() != H or not t.is_cuda or not t.is_contiguous() or _DTYPES.get(t.dtype) != dt:
-                raise ValueError("%s must be %d contiguous values of the config's dtype" % (name, H))
-            setattr(io, name, t.data_ptr())
+    H, dt, T = cfg.hidden, _TORCH_DTYPES[cfg.dtype], -1
+    x_p = r_p = g_p = post_p = pre_p = ro_p = y_p = None
+    x_ld = r_ld = g_ld = ro_ld = y_ld = 0
+    if x is not None:
+        x_ld, x_p = _rows(x, "x", H, dt, T), x.data_ptr()
+        T = x.shape[0]
+    if resid is not None:
+        r_ld, r_p = _rows(resid, "resid", H, dt, T), resid.data_ptr()
+        T = resid.shape[0]
+    if resid_out is not None:
+        ro_ld, ro_p = _rows(resid_out, "resid_out", H, dt, T), resid_out.data_ptr()
+    if y is not None:
+        y_ld, y_p = _rows(y, "y", H, dt, T), y.data_ptr()
+    if w_post is not None:
+        post_p = _vector(w_post, "w_post", H, dt)
+    if w_pre is not None:
+        pre_p = _vector(w_pre, "w_pre", H, dt)
     if gate is not None:
         if cfg.gate == 1:
-            if gate.numel() != H or not gate.is_cuda or not gate.is_contiguous() or _DTYPES.get(gate.dtype) != dt:
-                raise ValueError("a channel gate must be %d contiguous values of the config's dtype" % H)
-        elif cfg.gate == 2:
-            io.gate_ld = _rows(gate if gate.dim() == 2 else gate[:, None], "gate", 1, dt, T)
+            g_p = _vector(gate, "a channel gate", H, dt)
         else:
-            io.gate_ld = _rows(gate, "gate", H, dt, T)
-        io.gate = gate.data_ptr()
-    st = lib().moe_block_norm(ctypes.byref(cfg), ctypes.byref(io), T or 0, _stream(stream))
+            if cfg.gate == 2:
+                g_ld = _rows(gate if gate.dim() == 2 else gate[:, None], "gate", 1, dt, T)
+            else:
+                g_ld = _rows(gate, "gate", H, dt, T)
+            g_p = gate.data_ptr()
+    ref = x if x is not None else resid
+    io = NormIO(x_p, r_p, g_p, post_p, pre_p, ro_p, y_p, x_ld, r_ld, g_ld, ro_ld, y_ld)
+    st = lib().moe_block_norm(cfg, io, max(T, 0), _raw_stream(stream, ref.device.index if ref is not None else -1))
     _check("moe_block_norm", st)
 
 
@@ -517,18 +535,19 @@ def alloc_attn_workspace(cfg: AttnConfig, max_seqs, max_tokens, device="cuda") -
 def moe_kv_append(cfg: AttnConfig, cache: KVCache, batch: KVBatch, q, k, v, rope, q_out, ws, stream=None):
     """Rotates q [T, q_heads, D] into q_out and writes k, v [T, kv_heads, D] into the cache at the batch's
     positions.  rope: fp32 [positions, rotary_dim], cosines then sines (None with rotary_dim 0)."""
-    T, D, dt = batch.n_tokens, cfg.head_dim, cfg.dtype
+    T, D, dt = batch.n_tokens, cfg.head_dim, _TORCH_DTYPES[cfg.dtype]
     qw, kw = cfg.q_heads * D, cfg.kv_heads * D
-    rope_ptr, rope_rows = None, 0
+    rope_p, rope_rows, q_p, q_ld, qo_p, qo_ld = None, 0, None, 0, None, 0
     if rope is not None:
         rope_rows = rope.shape[0]
-        rope_ptr = _device_array(rope, "rope", torch.float32, (rope_rows, cfg.rotary_dim))
+        rope_p = _device_array(rope, "rope", torch.float32, (rope_rows, cfg.rotary_dim))
+    if q is not None:
+        q_p, q_ld = q.data_ptr(), _rows(q, "q", qw, dt, T)
+    if q_out is not None:
+        qo_p, qo_ld = q_out.data_ptr(), _rows(q_out, "q_out", qw, dt, T)
     st = lib().moe_kv_append(
-        ctypes.byref(cfg), ctypes.byref(cache.c), ctypes.byref(batch.c),
-        None if q is None else q.data_ptr(), 0 if q is None else _rows(q, "q", qw, dt, T),
-        k.data_ptr(), _rows(k, "k", kw, dt, T), v.data_ptr(), _rows(v, "v", kw, dt, T), rope_ptr, rope_rows,
-        None if q_out is None else q_out.data_ptr(), 0 if q_out is None else _rows(q_out, "q_out", qw, dt, T),
-        _ptr(ws), ws.numel(), _stream(stream))
+        cfg, cache.c, batch.c, q_p, q_ld, k.data_ptr(), _rows(k, "k", kw, dt, T), v.data_ptr(), _rows(v, "v", kw, dt, T),
+        rope_p, rope_rows, qo_p, qo_ld, _device_array(ws, "ws", torch.uint8), ws.numel(), _raw_stream(stream, k.device.index))
     _check("moe_kv_append", st)
 
 
@@ -536,12 +555,13 @@ def moe_attention(cfg: AttnConfig, cache: KVCache, batch: KVBatch, q, out, ws, l
                   causal=True, window=0, stream=None):
     """Attention of q [T, q_heads, D] over the batch's cached tokens into out (and lse fp32
     [T, q_heads]).  softmax_scale None: 1 / sqrt(D)."""
-    T, qw = batch.n_tokens, cfg.q_heads * cfg.head_dim
-    lse_ptr = None if lse is None else _device_array(lse, "lse", torch.float32, (T, cfg.q_heads))
+    T, qw, dt = batch.n_tokens, cfg.q_heads * cfg.head_dim, _TORCH_DTYPES[cfg.dtype]
+    lse_p = None if lse is None else _device_array(lse, "lse", torch.float32, (T, cfg.q_heads))
     st = lib().moe_attention(
-        ctypes.byref(cfg), ctypes.byref(cache.c), ctypes.byref(batch.c), q.data_ptr(), _rows(q, "q", qw, cfg.dtype, T),
-        cfg.head_dim ** -0.5 if softmax_scale is None else softmax_scale, int(bool(causal)), int(window),
-        out.data_ptr(), _rows(out, "out", qw, cfg.dtype, T), lse_ptr, _ptr(ws), ws.numel(), _stream(stream))
+        cfg, cache.c, batch.c, q.data_ptr(), _rows(q, "q", qw, dt, T),
+        cfg.head_dim ** -0.5 if softmax_scale is None else softmax_scale, 1 if causal else 0, window, out.data_ptr(),
+        _rows(out, "out", qw, dt, T), lse_p, _device_array(ws, "ws", torch.uint8), ws.numel(),
+        _raw_stream(stream, q.device.index))
     _check("moe_attention", st)
 
 

@@ -5,7 +5,11 @@
 // page's new values of that head in registers, reduces their largest magnitude, settles the
 // page's scale, re-rounds the codes that the page held before if the scale grew, and writes the
 // new codes -- no other block touches that page and head, so no scale is ever contended.  The
-// blocks after them rotate q.
+// blocks after them rotate q: a thread takes the same 16 dims of four heads of a token, so that it reads
+// their cosines and sines once.
+//
+// Bound: every value is read and written once (HBM) for prompts; a decode step is two or three
+// dependent reads (sequence, page, values) and the launch.
 //
 // Exact codes.  The rotation a cos - b sin of 16-bit a, b with an fp32 table is carried as an
 // unevaluated fp32 pair (products and the sum with their rounding errors, error-free
@@ -19,7 +23,7 @@ namespace moe {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kSeqCache = 1024;  // sequences whose q_start a block stages in shared memory
+constexpr int kSeqCache = 1024;  // sequences whose places a block stages in shared memory
 
 // a*c - b*s rounded to odd (see above).  Explicit _rn operations: none may be contracted.
 __device__ __forceinline__ float rotate_odd(float a, float c, float b, float s) {
@@ -34,6 +38,19 @@ __device__ __forceinline__ float rotate_odd(float a, float c, float b, float s) 
     int bits = __float_as_int(r2);
     if (lost != 0.f && !(bits & 1)) bits += ((lost > 0.f) == (r2 > 0.f)) ? 1 : -1;
     return __int_as_float(bits);
+}
+
+// The same to nearest, and whether that is so near the middle between two 16-bit values that rounding it
+// again might go wrong: its error (of the products, exact, and two fp32 additions) is below 4 ulp.
+// For q, where it costs 7 operations an element against 20 and the second look is rare (2^-13).
+template <bool F16>
+__device__ __forceinline__ float rotate_near(float a, float c, float b, float s, bool &near) {
+    const float q = -__fmul_rn(b, s);
+    const float r = __fadd_rn(__fmaf_rn(a, c, q), __fmaf_rn(-b, s, -q));
+    const uint32_t u = __float_as_uint(r);
+    if (F16) near |= (u & 0x1fffu) - 0x1000u + 4u <= 8u || fabsf(r) < 0x1p-13f;  // (subnormal: coarser)
+    else near |= (u & 0xffffu) - 0x8000u + 4u <= 8u;
+    return r;
 }
 
 // The exponent e of the smallest 2^e with amax <= 448 * 2^e (448 = 1.75 * 2^8), not below the floor.
@@ -64,36 +81,39 @@ __device__ __forceinline__ void unit_dims(int u, int rot, bool interleaved, int 
     d1 = half_split ? 8 * u + (rot >> 1) : 16 * u + 8;
 }
 
-// The unit's values after the rotation (to odd), or as they are past rot.
-template <bool F16>
-__device__ __forceinline__ void unit_values(const uint4 &lo, const uint4 &hi, const float *__restrict__ rope_row, int u,
-                                            int rot, bool interleaved, float (&a)[8], float (&b)[8]) {
-    unpack8<F16>(lo, a);
-    unpack8<F16>(hi, b);
-    if (!rope_row || u >= (rot >> 4)) return;
+// The 8 cosines and sines of unit u.  Rows of the table are rot floats, a multiple of 16: every 8 of them
+// start on 16 bytes.
+struct Angles {
     float c[8], s[8];
-    // rows of the table are rot floats, a multiple of 16: every 8 of them start on 16 bytes
+};
+__device__ __forceinline__ void load_angles(const float *rope_row, int u, int rot, Angles &g) {
     const float4 *cp = reinterpret_cast<const float4 *>(rope_row + 8 * u);
     const float4 *sp = reinterpret_cast<const float4 *>(rope_row + (rot >> 1) + 8 * u);
     const float4 c0 = __ldg(cp), c1 = __ldg(cp + 1), s0 = __ldg(sp), s1 = __ldg(sp + 1);
-    c[0] = c0.x, c[1] = c0.y, c[2] = c0.z, c[3] = c0.w, c[4] = c1.x, c[5] = c1.y, c[6] = c1.z, c[7] = c1.w;
-    s[0] = s0.x, s[1] = s0.y, s[2] = s0.z, s[3] = s0.w, s[4] = s1.x, s[5] = s1.y, s[6] = s1.z, s[7] = s1.w;
+    g.c[0] = c0.x, g.c[1] = c0.y, g.c[2] = c0.z, g.c[3] = c0.w, g.c[4] = c1.x, g.c[5] = c1.y, g.c[6] = c1.z, g.c[7] = c1.w;
+    g.s[0] = s0.x, g.s[1] = s0.y, g.s[2] = s0.z, g.s[3] = s0.w, g.s[4] = s1.x, g.s[5] = s1.y, g.s[6] = s1.z, g.s[7] = s1.w;
+}
+
+// Turns the unit's 8 pairs: (a[j], b[j]), or interleaved (a[2j], a[2j+1]) and (b[2j], b[2j+1]).  turn(x, c, y, s)
+// is x c - y s.
+template <typename F>
+__device__ __forceinline__ void turn_unit(float (&a)[8], float (&b)[8], const Angles &g, bool interleaved, F turn) {
     if (!interleaved) {
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
             const float x = a[j], y = b[j];
-            a[j] = rotate_odd(x, c[j], y, s[j]);
-            b[j] = rotate_odd(y, c[j], x, -s[j]);
+            a[j] = turn(x, g.c[j], y, g.s[j]);
+            b[j] = turn(y, g.c[j], x, -g.s[j]);
         }
     } else {
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             float x = a[2 * j], y = a[2 * j + 1];
-            a[2 * j] = rotate_odd(x, c[j], y, s[j]);
-            a[2 * j + 1] = rotate_odd(y, c[j], x, -s[j]);
+            a[2 * j] = turn(x, g.c[j], y, g.s[j]);
+            a[2 * j + 1] = turn(y, g.c[j], x, -g.s[j]);
             x = b[2 * j], y = b[2 * j + 1];
-            b[2 * j] = rotate_odd(x, c[4 + j], y, s[4 + j]);
-            b[2 * j + 1] = rotate_odd(y, c[4 + j], x, -s[4 + j]);
+            b[2 * j] = turn(x, g.c[4 + j], y, g.s[4 + j]);
+            b[2 * j + 1] = turn(y, g.c[4 + j], x, -g.s[4 + j]);
         }
     }
 }
@@ -109,65 +129,74 @@ __device__ __forceinline__ int last_at_most(int n, int i, F f) {
     return lo;
 }
 
+constexpr int kHeads = 4;  // heads a thread of the q part turns with one set of angles
+
 // U: units a thread of a page block holds (P * D / 16 / blockDim)
 template <int D, int U, bool F16>
-__global__ void __launch_bounds__(kThreads) kv_append_kernel(const __grid_constant__ AppendArgs p) {
+__global__ void __launch_bounds__(kThreads, U <= 2 ? 3 : U == 4 ? 2 : 1) kv_append_kernel(const __grid_constant__ AppendArgs p) {
     constexpr int kUnits = D / 16;  // of a row
     const KvView &v = p.kv;
-    __shared__ int starts[kSeqCache];
+    __shared__ int starts[kSeqCache + 1], lens[kSeqCache];
     __shared__ float red[kThreads / 32];
     const int tid = (int)threadIdx.x, nt = (int)blockDim.x;
     const int P = 1 << v.log_p;
     const bool staged = v.n_seqs <= kSeqCache;
     if (staged) {
-        for (int i = tid; i < v.n_seqs; i += nt) starts[i] = v.q_start[i];
+        for (int i = tid; i <= v.n_seqs; i += nt) {
+            starts[i] = v.q_start[i];
+            if (i < v.n_seqs) lens[i] = v.kv_len[i];
+        }
         __syncthreads();
     }
     auto start_of = [&](int b) { return staged ? starts[b] : v.q_start[b]; };
+    auto seq_of = [&](int b) { return staged ? checked_seq(v, starts[b], starts[b + 1], lens[b]) : load_seq(v, b); };
 
     if ((int)blockIdx.x >= p.page_items) {
         // ---------------------------------------------------------------- rotation of q --
         const int t0 = ((int)blockIdx.x - p.page_items) * p.q_tokens;
         const int t1 = min(t0 + p.q_tokens, v.n_tokens);
-        const int row_units = v.QH * kUnits;
-        constexpr int kBatch = 4;  // units with their loads in flight together
-        for (int base = 0; base < (t1 - t0) * row_units; base += kBatch * nt) {
-            uint4 lo[kBatch], hi[kBatch];
-            int tok[kBatch], rem[kBatch];
+        const int groups = (v.QH + kHeads - 1) / kHeads;
+        const int u = tid % kUnits;
+        int d0, d1;
+        unit_dims(u, p.rot, p.interleaved, d0, d1);
+        for (int item = tid / kUnits; item < (t1 - t0) * groups; item += nt / kUnits) {
+            const int tok = t0 + item / groups, h0 = item % groups * kHeads;
+            const uint16_t *src = p.q + tok * p.q_ld + h0 * D;
+            uint4 lo[kHeads], hi[kHeads];
 #pragma unroll
-            for (int i = 0; i < kBatch; ++i) {
-                const int k = base + i * nt + tid;
-                tok[i] = -1;
-                if (k >= (t1 - t0) * row_units) continue;
-                tok[i] = t0 + k / row_units;
-                rem[i] = k % row_units;
-                int d0, d1;
-                unit_dims(rem[i] % kUnits, p.rot, p.interleaved, d0, d1);
-                const uint16_t *src = p.q + tok[i] * p.q_ld + rem[i] / kUnits * D;
-                lo[i] = *reinterpret_cast<const uint4 *>(src + d0);
-                hi[i] = *reinterpret_cast<const uint4 *>(src + d1);
-            }
-#pragma unroll
-            for (int i = 0; i < kBatch; ++i) {
-                if (tok[i] < 0) continue;
-                const int b = last_at_most(v.n_seqs, tok[i], start_of);
-                const Seq q = load_seq(v, b);
-                const int pos = q.kv - q.n + tok[i] - q.q0;
-                const int u = rem[i] % kUnits;
-                float x[8], y[8];
-                const bool ok = pos >= 0 && (pos < p.rope_rows || p.rot == 0) && tok[i] - q.q0 < q.n;
-                if (ok) {
-                    unit_values<F16>(lo[i], hi[i], p.rot ? p.rope + (int64_t)pos * p.rot : nullptr, u, p.rot, p.interleaved, x, y);
-                } else {
-                    if (pos >= 0) layer_error(v.status);
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) x[j] = y[j] = 0.f;
+            for (int i = 0; i < kHeads; ++i)
+                if (h0 + i < v.QH) {
+                    lo[i] = *reinterpret_cast<const uint4 *>(src + i * D + d0);
+                    hi[i] = *reinterpret_cast<const uint4 *>(src + i * D + d1);
                 }
-                int d0, d1;
-                unit_dims(u, p.rot, p.interleaved, d0, d1);
-                uint16_t *dst = p.q_out + tok[i] * p.q_out_ld + rem[i] / kUnits * D;
-                *reinterpret_cast<uint4 *>(dst + d0) = pack8<F16>(x);
-                *reinterpret_cast<uint4 *>(dst + d1) = pack8<F16>(y);
+            const Seq q = seq_of(last_at_most(v.n_seqs, tok, start_of));
+            const int pos = q.kv - q.n + tok - q.q0;
+            const bool ok = pos >= 0 && (pos < p.rope_rows || p.rot == 0) && tok - q.q0 < q.n;
+            if (!ok && pos >= 0) layer_error(v.status);
+            const bool turned = ok && u < (p.rot >> 4);
+            Angles g;
+            if (turned) load_angles(p.rope + (int64_t)pos * p.rot, u, p.rot, g);
+            uint16_t *dst = p.q_out + tok * p.q_out_ld + h0 * D;
+#pragma unroll
+            for (int i = 0; i < kHeads; ++i) {
+                if (h0 + i >= v.QH) break;
+                if (!ok) lo[i] = hi[i] = make_uint4(0, 0, 0, 0);
+                if (turned) {
+                    float x[8], y[8];
+                    unpack8<F16>(lo[i], x);
+                    unpack8<F16>(hi[i], y);
+                    bool near = false;
+                    turn_unit(x, y, g, p.interleaved, [&](float a, float c, float b, float s) { return rotate_near<F16>(a, c, b, s, near); });
+                    if (near) {
+                        unpack8<F16>(lo[i], x);
+                        unpack8<F16>(hi[i], y);
+                        turn_unit(x, y, g, p.interleaved, rotate_odd);
+                    }
+                    lo[i] = pack8<F16>(x);
+                    hi[i] = pack8<F16>(y);
+                }
+                *reinterpret_cast<uint4 *>(dst + i * D + d0) = lo[i];
+                *reinterpret_cast<uint4 *>(dst + i * D + d1) = hi[i];
             }
         }
         return;
@@ -177,7 +206,7 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(const __grid_consta
     // Sequence b has the page slots base(b) .. base(b+1)-1: its n new tokens touch at most n/P + 2 pages.
     const int slot = (int)blockIdx.x / (2 * v.KH), which = (int)blockIdx.x / v.KH & 1, head = (int)blockIdx.x % v.KH;
     const int b = last_at_most(v.n_seqs, slot, [&](int i) { return (start_of(i) >> v.log_p) + 2 * i; });
-    const Seq q = load_seq(v, b);
+    const Seq q = seq_of(b);
     const int first = q.kv - q.n;  // position of the first new token
     const int col = (max(first, 0) >> v.log_p) + slot - ((q.q0 >> v.log_p) + 2 * b);
     const int pos0 = col << v.log_p;
@@ -219,8 +248,13 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(const __grid_consta
             odd = true;
             lo[i] = hi[i] = make_uint4(0, 0, 0, 0);
         }
-        const float *angle = (live && rot && pos < p.rope_rows) ? p.rope + (int64_t)pos * rot : nullptr;
-        unit_values<F16>(lo[i], hi[i], angle, k % kUnits, rot, p.interleaved, x[i], y[i]);
+        unpack8<F16>(lo[i], x[i]);
+        unpack8<F16>(hi[i], y[i]);
+        if (live && k % kUnits < (rot >> 4) && pos < p.rope_rows) {
+            Angles g;
+            load_angles(p.rope + (int64_t)pos * rot, k % kUnits, rot, g);
+            turn_unit(x[i], y[i], g, p.interleaved, rotate_odd);
+        }
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
             odd |= !(fabsf(x[i][j]) <= 3.402823466e38f) || !(fabsf(y[i][j]) <= 3.402823466e38f);

