@@ -41,15 +41,16 @@ __device__ __forceinline__ float rotate_odd(float a, float c, float b, float s) 
 }
 
 // The same to nearest, and whether that is so near the middle between two 16-bit values that rounding it
-// again might go wrong: its error (of the products, exact, and two fp32 additions) is below 4 ulp.
-// For q, where it costs 7 operations an element against 20 and the second look is rare (2^-13).
+// again might go wrong.  Its error is half an ulp for each of two additions (the products are exact), 1.5 ulp
+// where the second leaves the binade, and the middle lies on the fp32 grid too: one ulp to either side.
+// For q, where it costs 7 operations an element against 20 and the second look is rare.
 template <bool F16>
 __device__ __forceinline__ float rotate_near(float a, float c, float b, float s, bool &near) {
     const float q = -__fmul_rn(b, s);
     const float r = __fadd_rn(__fmaf_rn(a, c, q), __fmaf_rn(-b, s, -q));
     const uint32_t u = __float_as_uint(r);
-    if (F16) near |= (u & 0x1fffu) - 0x1000u + 4u <= 8u || fabsf(r) < 0x1p-13f;  // (subnormal: coarser)
-    else near |= (u & 0xffffu) - 0x8000u + 4u <= 8u;
+    if (F16) near |= (u & 0x1fffu) - 0x1000u + 1u <= 2u || fabsf(r) < 0x1p-13f;  // (subnormal: coarser)
+    else near |= (u & 0xffffu) - 0x8000u + 1u <= 2u;
     return r;
 }
 
@@ -141,34 +142,43 @@ __global__ void __launch_bounds__(kThreads, U <= 2 ? 3 : U == 4 ? 2 : 1) kv_appe
     const int tid = (int)threadIdx.x, nt = (int)blockDim.x;
     const int P = 1 << v.log_p;
     const bool staged = v.n_seqs <= kSeqCache;
-    if (staged) {
-        for (int i = tid; i <= v.n_seqs; i += nt) {
-            starts[i] = v.q_start[i];
-            if (i < v.n_seqs) lens[i] = v.kv_len[i];
+    auto stage = [&]() {
+        if (staged) {
+            for (int i = tid; i <= v.n_seqs; i += nt) {
+                starts[i] = v.q_start[i];
+                if (i < v.n_seqs) lens[i] = v.kv_len[i];
+            }
+            __syncthreads();
         }
-        __syncthreads();
-    }
+    };
     auto start_of = [&](int b) { return staged ? starts[b] : v.q_start[b]; };
     auto seq_of = [&](int b) { return staged ? checked_seq(v, starts[b], starts[b + 1], lens[b]) : load_seq(v, b); };
 
-    if ((int)blockIdx.x >= p.page_items) {
+    if ((int)blockIdx.x >= p.page_blocks) {
         // ---------------------------------------------------------------- rotation of q --
-        const int t0 = ((int)blockIdx.x - p.page_items) * p.q_tokens;
+        const int t0 = ((int)blockIdx.x - p.page_blocks) * p.q_tokens;
         const int t1 = min(t0 + p.q_tokens, v.n_tokens);
         const int groups = (v.QH + kHeads - 1) / kHeads;
         const int u = tid % kUnits;
         int d0, d1;
         unit_dims(u, p.rot, p.interleaved, d0, d1);
-        for (int item = tid / kUnits; item < (t1 - t0) * groups; item += nt / kUnits) {
+        uint4 lo[kHeads], hi[kHeads];
+        auto load = [&](int item) {
             const int tok = t0 + item / groups, h0 = item % groups * kHeads;
             const uint16_t *src = p.q + tok * p.q_ld + h0 * D;
-            uint4 lo[kHeads], hi[kHeads];
 #pragma unroll
             for (int i = 0; i < kHeads; ++i)
                 if (h0 + i < v.QH) {
                     lo[i] = *reinterpret_cast<const uint4 *>(src + i * D + d0);
                     hi[i] = *reinterpret_cast<const uint4 *>(src + i * D + d1);
                 }
+        };
+        const int first_item = tid / kUnits, items = (t1 - t0) * groups;
+        if (first_item < items) load(first_item);  // under way while the sequences are read
+        stage();
+        for (int item = first_item; item < items; item += nt / kUnits) {
+            const int tok = t0 + item / groups, h0 = item % groups * kHeads;
+            if (item != first_item) load(item);
             const Seq q = seq_of(last_at_most(v.n_seqs, tok, start_of));
             const int pos = q.kv - q.n + tok - q.q0;
             const bool ok = pos >= 0 && (pos < p.rope_rows || p.rot == 0) && tok - q.q0 < q.n;
@@ -203,24 +213,21 @@ __global__ void __launch_bounds__(kThreads, U <= 2 ? 3 : U == 4 ? 2 : 1) kv_appe
     }
 
     // ------------------------------------------------------------- one page of one head --
+    // Pages of fewer than 256 units share a block: each takes the threads it needs.
     // Sequence b has the page slots base(b) .. base(b+1)-1: its n new tokens touch at most n/P + 2 pages.
-    const int slot = (int)blockIdx.x / (2 * v.KH), which = (int)blockIdx.x / v.KH & 1, head = (int)blockIdx.x % v.KH;
-    const int b = last_at_most(v.n_seqs, slot, [&](int i) { return (start_of(i) >> v.log_p) + 2 * i; });
+    stage();
+    const int team = min(P * kUnits, kThreads), item = (int)blockIdx.x * (kThreads / team) + tid / team;
+    const int k0 = tid % team;  // the thread's first unit
+    const bool any = item < p.page_items;
+    const int slot = item / (2 * v.KH), which = item / v.KH & 1, head = item % v.KH;
+    const int b = any ? last_at_most(v.n_seqs, slot, [&](int i) { return (start_of(i) >> v.log_p) + 2 * i; }) : 0;
     const Seq q = seq_of(b);
     const int first = q.kv - q.n;  // position of the first new token
     const int col = (max(first, 0) >> v.log_p) + slot - ((q.q0 >> v.log_p) + 2 * b);
     const int pos0 = col << v.log_p;
-    if (col < 0 || q.n == 0 || pos0 >= q.kv) return;  // no such page (col < 0: descending q_start)
-    const int page = v.table[(int64_t)b * v.max_pages + col];
-    if (page < 0 || page >= v.n_pages) {
-        if (tid == 0) layer_error(v.status);
-        return;
-    }
-    const int64_t ph = (int64_t)page * v.KH + head;
-    uint8_t *codes = (which ? v.v_codes : v.k_codes) + ph * P * D;
-    float *scale = (which ? v.v_scale : v.k_scale) + ph;
-    const bool begun = pos0 < first;  // the page holds earlier tokens
-    const float old = begun ? *scale : 0.f;
+    // (col < 0: a descending q_start)
+    bool here = any && col >= 0 && q.n > 0 && pos0 < q.kv;
+    const int page = here ? v.table[(int64_t)b * v.max_pages + col] : 0;
     const uint16_t *src = which ? p.v : p.k;
     const int64_t ld = which ? p.v_ld : p.k_ld;
     const int rot = which ? 0 : p.rot;  // values are not rotated
@@ -231,9 +238,9 @@ __global__ void __launch_bounds__(kThreads, U <= 2 ? 3 : U == 4 ? 2 : 1) kv_appe
     uint4 lo[U], hi[U];
 #pragma unroll
     for (int i = 0; i < U; ++i) {
-        const int k = i * nt + tid, pos = pos0 + k / kUnits;
+        const int k = i * team + k0, pos = pos0 + k / kUnits;
         lo[i] = hi[i] = make_uint4(0, 0, 0, 0);
-        if (pos < max(first, 0) || pos >= q.kv || k >= P * kUnits) continue;
+        if (!here || pos < max(first, 0) || pos >= q.kv) continue;
         int d0, d1;
         unit_dims(k % kUnits, rot, p.interleaved, d0, d1);
         const uint16_t *row = src + (int64_t)(q.q0 + pos - first) * ld + head * D;
@@ -242,8 +249,8 @@ __global__ void __launch_bounds__(kThreads, U <= 2 ? 3 : U == 4 ? 2 : 1) kv_appe
     }
 #pragma unroll
     for (int i = 0; i < U; ++i) {
-        const int k = i * nt + tid, pos = pos0 + k / kUnits;
-        const bool live = pos >= max(first, 0) && pos < q.kv && k < P * kUnits;
+        const int k = i * team + k0, pos = pos0 + k / kUnits;
+        const bool live = here && pos >= max(first, 0) && pos < q.kv;
         if (live && rot && pos >= p.rope_rows) {  // no angle: stored as zeros, reported
             odd = true;
             lo[i] = hi[i] = make_uint4(0, 0, 0, 0);
@@ -263,12 +270,22 @@ __global__ void __launch_bounds__(kThreads, U <= 2 ? 3 : U == 4 ? 2 : 1) kv_appe
             amax = fmaxf(amax, fmaxf(fabsf(x[i][j]), fabsf(y[i][j])));
         }
     }
+    if (here && (page < 0 || page >= v.n_pages)) {
+        odd = true;
+        here = false;
+    }
     if (odd) layer_error(v.status);
+    const int64_t ph = (int64_t)(here ? page : 0) * v.KH + head;
+    uint8_t *codes = (which ? v.v_codes : v.k_codes) + ph * P * D;
+    float *scale = (which ? v.v_scale : v.k_scale) + ph;
+    const bool begun = pos0 < first;  // the page holds earlier tokens
+    const float old = here && begun ? *scale : 0.f;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
     if ((tid & 31) == 0) red[tid >> 5] = amax;
     __syncthreads();
-    for (int w = 0; w < nt >> 5; ++w) amax = fmaxf(amax, red[w]);
+    if (!here) return;
+    for (int w = 0; w < team >> 5; ++w) amax = fmaxf(amax, red[(tid - k0 >> 5) + w]);
     float s = pow2f(scale_exp(amax));
     if (begun) s = fmaxf(s, old);
     const float inv = 1.0f / s;  // exact: s is a power of two
@@ -276,8 +293,7 @@ __global__ void __launch_bounds__(kThreads, U <= 2 ? 3 : U == 4 ? 2 : 1) kv_appe
     const float ratio = old * inv;
 #pragma unroll
     for (int i = 0; i < U; ++i) {
-        const int k = i * nt + tid, pos = pos0 + k / kUnits;
-        if (k >= P * kUnits) continue;
+        const int k = i * team + k0, pos = pos0 + k / kUnits;
         int d0, d1;
         unit_dims(k % kUnits, rot, p.interleaved, d0, d1);
         uint8_t *row = codes + k / kUnits * D;
@@ -297,20 +313,22 @@ __global__ void __launch_bounds__(kThreads, U <= 2 ? 3 : U == 4 ? 2 : 1) kv_appe
             *reinterpret_cast<uint2 *>(row + d1) = c;
         }
     }
-    if (tid == 0 && s != old) *scale = s;
+    if (k0 == 0 && s != old) *scale = s;
 }
 
 template <int D, bool F16>
 cudaError_t launch(const AppendArgs &a, cudaStream_t s) {
     LaunchScope scope(KC_KV_APPEND, s);
     const int q_blocks = a.q ? (a.kv.n_tokens + a.q_tokens - 1) / a.q_tokens : 0;
-    const int grid = a.page_items + q_blocks;
     const int units = a.kv.P * D / 16;
     const int u = units / kThreads;
-    if (u <= 1) kv_append_kernel<D, 1, F16><<<grid, kThreads, 0, s>>>(a);
-    else if (u == 2) kv_append_kernel<D, 2, F16><<<grid, kThreads, 0, s>>>(a);
-    else if (u == 4) kv_append_kernel<D, 4, F16><<<grid, kThreads, 0, s>>>(a);
-    else kv_append_kernel<D, 8, F16><<<grid, kThreads, 0, s>>>(a);
+    AppendArgs b = a;
+    b.page_blocks = u > 1 ? a.page_items : (a.page_items + kThreads / units - 1) / (kThreads / units);
+    const int grid = b.page_blocks + q_blocks;
+    if (u <= 1) kv_append_kernel<D, 1, F16><<<grid, kThreads, 0, s>>>(b);
+    else if (u == 2) kv_append_kernel<D, 2, F16><<<grid, kThreads, 0, s>>>(b);
+    else if (u == 4) kv_append_kernel<D, 4, F16><<<grid, kThreads, 0, s>>>(b);
+    else kv_append_kernel<D, 8, F16><<<grid, kThreads, 0, s>>>(b);
     return cudaGetLastError();
 }
 

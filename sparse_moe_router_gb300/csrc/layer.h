@@ -31,7 +31,8 @@ struct AppendArgs {
     int rope_rows, rot, interleaved;
     uint16_t *q_out;
     int q_tokens;    // tokens a block of the q part handles
-    int page_items;  // blocks of the cache part: (page slots) x 2 x kv heads
+    int page_items;  // (page slots) x 2 x kv heads
+    int page_blocks; // blocks that they take (set by the launch)
 };
 cudaError_t launch_kv_append(const AppendArgs &a, int D, int dtype, cudaStream_t s);
 
