@@ -201,7 +201,7 @@ moe_status moe_kv_append(const moe_attn_config *cfg, const moe_kv_cache *cache, 
     if (items > (1 << 30)) return MOE_ERR_UNSUPPORTED_SHAPE;
     a.page_items = (int)items;
     // a block of the q part takes as many tokens as fill its threads once, fewer while that leaves SMs idle
-    const int groups = (c.q_heads + 3) / 4, once = 256 / (c.head_dim / 16) / groups;
+    const int groups = (c.q_heads + 1) / 2, once = 256 / (c.head_dim / 16) / groups;
     const int spread = batch->n_tokens / (2 * device_info().sm_count);
     a.q_tokens = spread < 1 || once < 1 ? 1 : spread > once ? once : spread;
     MOE_CUDA(launch_kv_append(a, c.head_dim, c.dtype, static_cast<cudaStream_t>(stream)));
