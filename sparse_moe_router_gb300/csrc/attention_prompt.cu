@@ -99,14 +99,14 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
     uint8_t *q_smem = smem, *kv_smem = smem + 2 * C::kTileBytes;
     uint64_t *bars = reinterpret_cast<uint64_t *>(kv_smem + kStages * C::kTileBytes);
     uint64_t *full = bars, *empty = bars + kStages;  // of a stage
-    uint64_t *s_full = empty + kStages;              // [2] logits of a row tile are in TMEM
-    uint64_t *p_full = s_full + 2;                   // [2] its weights are
-    uint64_t *p_half = p_full + 2;                   // [2] the first half of them
-    uint64_t *o_half = p_half + 2;                   // [2] and that half's product is complete
-    uint64_t *o_full = o_half + 2;                   // [2] its output is complete
+    uint64_t *s_full = empty + kStages;              // [2] 64 logits of each row of a row tile are in TMEM
+    uint64_t *s_free = s_full + 2;                   // [2] and in registers: the next may take their place
+    uint64_t *p_full = s_free + 2;                   // [2 x 2] their weights are in TMEM, even and odd half tiles
+    uint64_t *o_half = p_full + 4;                   // [2] and have gone into the output
+    uint64_t *o_full = o_half + 2;                   // [2] all have
     uint64_t *q_full = o_full + 2;
     uint64_t *drain = q_full + 1;
-    uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(drain + 1);
+    uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(drain + 2);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_holder + 1);
     int *max_exp = reinterpret_cast<int *>(tmem_holder + 2);              // [2] of K and V
 
@@ -133,22 +133,25 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
     const int key_lo = p.window > 0 ? max(0, pos_lo + 1 - p.window) : 0;
     const int tile0 = key_lo / kKeys;
     const int tiles = key_hi > key_lo ? (key_hi + kKeys - 1) / kKeys - tile0 : 0;
+    const int halves = tiles > 0 ? (key_hi - tile0 * kKeys + 63) / 64 : 0;  // half tiles of 64 keys
     const int32_t *table = v.table + (int64_t)b * v.max_pages;
 
     if (tid == 0) {
         for (int s = 0; s < kStages; ++s) {
             ptx::mbar_init(&full[s], kConvWarps);
-            ptx::mbar_init(&empty[s], 1);
+            ptx::mbar_init(&empty[s], 2);  // both row tiles are done with it
         }
         for (int i = 0; i < 2; ++i) {
             ptx::mbar_init(&s_full[i], 1);
-            ptx::mbar_init(&p_full[i], kSoftWarps / 2);
-            ptx::mbar_init(&p_half[i], kSoftWarps / 2);
+            ptx::mbar_init(&p_full[2 * i], kSoftWarps / 2);
+            ptx::mbar_init(&p_full[2 * i + 1], kSoftWarps / 2);
+            ptx::mbar_init(&s_free[i], kSoftWarps / 2);
             ptx::mbar_init(&o_half[i], 1);
             ptx::mbar_init(&o_full[i], 1);
         }
         ptx::mbar_init(q_full, kSoftWarps);
-        ptx::mbar_init(drain, 1);
+        ptx::mbar_init(&drain[0], 1);
+        ptx::mbar_init(&drain[1], 1);
         *abort_flag = 0;
         max_exp[0] = max_exp[1] = -127;
         ptx::fence_mbar_init();
@@ -228,50 +231,55 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t s_addr = tmem + lanes + i * kKeys, o_addr = tmem + lanes + C::kColO + i * D;
         float m = 0.f, l = 0.f;  // reference of the weights, and their sum (0: none so far)
-        for (int j = 0; j < tiles; ++j) {
-            ok = __all_sync(0xffffffffu, ptx::mbar_wait(&s_full[i], j & 1, kWaitNs, abort_flag)) != 0;
+        for (int n = 0; n < halves; ++n) {
+            ok = __all_sync(0xffffffffu, ptx::mbar_wait(&s_full[i], n & 1, kWaitNs, abort_flag)) != 0;
             if (!ok) break;
             ptx::tc_fence_after();
-            const int key0 = (tile0 + j) * kKeys, c_lo = lo - key0, c_hi = hi - key0;
-            const bool masked = __any_sync(0xffffffffu, live && (c_lo > 0 || c_hi < kKeys));
-            auto hide = [&](uint32_t (&s)[32], int c) {
-                if (!masked) return;
+            uint32_t s[2][32], w[32];
+            ptx::tmem_ld_32(s_addr, s[0]);
+            ptx::tmem_ld_32(s_addr + 32, s[1]);
+            ptx::tmem_ld_wait();
+            tie32(s[0]);
+            tie32(s[1]);
+            ptx::tc_fence_before();
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(&s_free[i]);
+            const int key0 = tile0 * kKeys + n * 64, c_lo = lo - key0, c_hi = hi - key0;
+            if (__any_sync(0xffffffffu, live && (c_lo > 0 || c_hi < 64))) {
 #pragma unroll
-                for (int k = 0; k < 32; ++k)
-                    if (c * 32 + k < c_lo || c * 32 + k >= c_hi) s[k] = 0xff800000u;  // -inf
-            };
+                for (int c = 0; c < 2; ++c)
+#pragma unroll
+                    for (int k = 0; k < 32; ++k)
+                        if (c * 32 + k < c_lo || c * 32 + k >= c_hi) s[c][k] = 0xff800000u;  // -inf
+            }
             // The sum of the weights itself tells when the reference is too small: as long as it stays within
             // kMostSum every weight fits fp16.  Only then (and where a row begins) is the maximum looked for.
-            uint32_t s[2][32], w[32];
-            auto fetch = [&](int c) { ptx::tmem_ld_32(s_addr + c * 32, s[c & 1]); };
-            auto fetched = [&]() {
-                ptx::tmem_ld_wait();
-                tie32(s[0]);
-                tie32(s[1]);
-            };
-            auto weights = [&](int c, float2 sum) {  // of the 32 columns from 32 c, whose logits are in s[c & 1]
-                hide(s[c & 1], c);
+            auto weights = [&]() {
+                float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
-                for (int k = 0; k < 16; ++k) {
-                    const float2 z =
-                        fma2(make_float2(__uint_as_float(s[c & 1][2 * k]), __uint_as_float(s[c & 1][2 * k + 1])), mul, -m);
-                    const float2 e = make_float2(exp2_fast(z.x), exp2_fast(z.y));
-                    sum = __fadd2_rn(sum, e);
-                    w[(c & 1) * 16 + k] = pack2<true>(e.x, e.y);
-                }
-                return sum;
+                for (int c = 0; c < 2; ++c)
+#pragma unroll
+                    for (int k = 0; k < 16; ++k) {
+                        const float2 z =
+                            fma2(make_float2(__uint_as_float(s[c][2 * k]), __uint_as_float(s[c][2 * k + 1])), mul, -m);
+                        const float2 e = make_float2(exp2_fast(z.x), exp2_fast(z.y));
+                        sum = __fadd2_rn(sum, e);
+                        w[c * 16 + k] = pack2<true>(e.x, e.y);
+                    }
+                return sum.x + sum.y;
             };
-            // A larger reference, from the logits of columns 64 h .. 127; O and l, summed under the old one, are
-            // scaled (with h = 1 once the tile's first 64 weights have gone into O).
-            auto renew = [&](int h) {
+            bool renew = __any_sync(0xffffffffu, l == 0.f && sees);
+            float sum = 0.f;
+            if (!renew) {
+                sum = weights();
+                renew = __any_sync(0xffffffffu, !(sum <= kMostSum));
+            }
+            if (renew) {
                 float top = -INFINITY;
-                for (int c = 2 * h; c < 4; ++c) {
-                    ptx::tmem_ld_32(s_addr + c * 32, s[0]);
-                    fetched();
-                    hide(s[0], c);
 #pragma unroll
-                    for (int k = 0; k < 32; k += 2) top = max3(top, __uint_as_float(s[0][k]), __uint_as_float(s[0][k + 1]));
-                }
+                for (int c = 0; c < 2; ++c)
+#pragma unroll
+                    for (int k = 0; k < 32; k += 2) top = max3(top, __uint_as_float(s[c][k]), __uint_as_float(s[c][k + 1]));
                 top *= mul;  // mul > 0
                 float f = 1.f;
                 if (l == 0.f) {
@@ -281,57 +289,31 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
                     m = top;
                 }
                 l *= f;
-                if (h == 1) {
-                    ok = ok && ptx::mbar_wait(&o_half[i], j & 1, kWaitNs, abort_flag);
-                    __syncwarp();
+                if (n > 0) {  // O under the old reference, once the product of the half tile before is in it
+                    ok = __all_sync(0xffffffffu, ptx::mbar_wait(&o_half[i], (n - 1) & 1, kWaitNs, abort_flag)) != 0;
                     ptx::tc_fence_after();
-                }
-                // (h = 0: the logits came after the product of the tile before was complete)
-                for (int c = 0; c < D / 32 && (h == 1 || j > 0); ++c) {
-                    ptx::tmem_ld_32(o_addr + c * 32, s[0]);
-                    fetched();
+                    uint32_t o[16];
+                    for (int c = 0; c < D / 16; ++c) {
+                        ptx::tmem_ld_16(o_addr + c * 16, o);
+                        ptx::tmem_ld_wait();
 #pragma unroll
-                    for (int k = 0; k < 32; ++k) s[0][k] = __float_as_uint(__uint_as_float(s[0][k]) * f);
-                    ptx::tmem_st_32(o_addr + c * 32, s[0]);
+                        for (int k = 0; k < 16; ++k) {
+                            asm volatile("" : "+r"(o[k]));
+                            o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
+                        }
+                        ptx::tmem_st_16(o_addr + c * 16, o);
+                    }
                 }
-                fetch(2 * h);
-                fetch(2 * h + 1);
-                fetched();
-            };
-            auto too_small = [&](float2 sum) { return !(sum.x + sum.y <= kMostSum); };
-            const float2 zero = make_float2(0.f, 0.f);
-            fetch(0);
-            fetch(1);
-            fetched();
-            if (__any_sync(0xffffffffu, l == 0.f && sees)) renew(0);
-            float2 sum = weights(1, weights(0, zero));
-            if (__any_sync(0xffffffffu, too_small(sum))) {
-                renew(0);
-                sum = weights(1, weights(0, zero));
+                sum = weights();
             }
-            fetch(2);
-            fetch(3);
-            l += sum.x + sum.y;
-            ptx::tmem_st_32(s_addr, w);  // P over S, whose columns up to 63 are done with
-            fetched();
-            sum = weights(2, zero);
-            // the first half's product may begin
+            l += sum;
+            // two places for the weights in turn: the product that last read this one came before the logits
+            ptx::tmem_st_32(s_addr + 64 + (n & 1) * 32, w);
             ptx::tmem_st_wait();
             ptx::tc_fence_before();
             __syncwarp();
-            if (lane == 0) ptx::mbar_arrive(&p_half[i]);
-            sum = weights(3, sum);
-            if (__any_sync(0xffffffffu, too_small(sum))) {
-                renew(1);
-                sum = weights(3, weights(2, zero));
-            }
-            l += sum.x + sum.y;
-            ptx::tmem_st_32(s_addr + 32, w);
-            ptx::tmem_st_wait();
-            ptx::tc_fence_before();
-            __syncwarp();
-            if (lane == 0) ptx::mbar_arrive(&p_full[i]);
-            ok = __all_sync(0xffffffffu, ok) != 0;
+            // (a barrier for even and one for odd: a warp may be a half tile ahead of another)
+            if (lane == 0) ptx::mbar_arrive(&p_full[2 * i + (n & 1)]);
             if (!ok) break;
         }
         // ---------------------------------------------------------------- output, normalised --
@@ -446,11 +428,12 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
         }
     }     else {
         regs_down<kMmaRegs>();
-        if (warp == kMmaWarp && tiles > 0) {
+        if (warp < kMmaWarp + 2 && tiles > 0) {
+            const int i = warp - kMmaWarp;  // the row tile
             // ------------------------------------------------------------------ the MMAs --
             // In the order O_0 S_0 O_1 S_1 ...: while the tensor cores are at one row tile's output and next
             // logits, the softmax warps are at the other's logits.
-            const uint32_t idesc_s = ptx::idesc_f16_f32(kRowTile, kKeys, false);
+            const uint32_t idesc_s = ptx::idesc_f16_f32(kRowTile, 64, false);
             const uint32_t idesc_o = ptx::idesc_f16_f32(kRowTile, D, true);
             const uint64_t q_desc = ptx::sw128_desc(ptx::smem_u32(q_smem));
             const uint64_t k_desc = ptx::sw128_desc(ptx::smem_u32(kv_smem));
@@ -458,11 +441,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
             auto wait = [&](uint64_t *bar, int parity) {
                 return __all_sync(0xffffffffu, ptx::mbar_wait(bar, parity & 1, kWaitNs, abort_flag)) != 0;
             };
-            auto logits = [&](int i, int j) {  // S = Q K_j^T
-                const int s = 2 * j % kStages;
+            auto logits = [&](int n) {  // S = Q K^T for the 64 keys of half tile n
+                const int s = n / 2 * 2 % kStages;
                 if (ptx::elect_one()) {
                     const uint64_t qd = q_desc + (uint64_t)(i * (C::kTileBytes >> 4));
-                    const uint64_t kd = k_desc + (uint64_t)(s * (C::kTileBytes >> 4));
+                    const uint64_t kd = k_desc + (uint64_t)(s * (C::kTileBytes >> 4) + (n & 1) * (64 * 128 >> 4));
 #pragma unroll
                     for (int k = 0; k < D / 16; ++k) {
                         constexpr int kBlock16 = C::kBlockBytes >> 4;
@@ -470,52 +453,42 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
                         ptx::mma_f16_ss(tmem + i * kKeys, qd + off, kd + off, idesc_s, k > 0);
                     }
                     ptx::mma_commit(&s_full[i]);
+                    if ((n & 1) || n + 1 == halves) ptx::mma_commit(&empty[s]);
                 }
                 __syncwarp();
             };
-            auto output = [&](int i, int j, int h) {  // O += P V_j, keys 64 h .. 64 h + 63 of the tile
-                const int s = (2 * j + 1) % kStages;
+            auto output = [&](int n) {  // O += P V
+                const int s = (n / 2 * 2 + 1) % kStages;
                 if (ptx::elect_one()) {
-                    const uint64_t vd = v_desc + (uint64_t)(s * (C::kTileBytes >> 4));
-                    // K_j is free (committed here: a second commit behind the logits' own holds the warp
-                    // until the first is through)
-                    if (h == 0 && i == 0) ptx::mma_commit(&empty[2 * j % kStages]);
+                    const uint64_t vd = v_desc + (uint64_t)(s * (C::kTileBytes >> 4) + (n & 1) * (64 * 128 >> 4));
 #pragma unroll
-                    for (int k = 0; k < kKeys / 32; ++k) {
-                        const int kk = h * (kKeys / 32) + k;
-                        ptx::mma_f16_ts(tmem + C::kColO + i * D, tmem + i * kKeys + kk * 8, vd + kk * (2048 >> 4), idesc_o,
-                                        j > 0 || kk > 0);
-                    }
-                    if (h == 0) ptx::mma_commit(&o_half[i]);
-                    if (h == 1 && i == 1) ptx::mma_commit(&empty[s]);
-                    if (h == 1 && j + 1 == tiles) ptx::mma_commit(&o_full[i]);
+                    for (int k = 0; k < 4; ++k)
+                        ptx::mma_f16_ts(tmem + C::kColO + i * D, tmem + i * kKeys + 64 + (n & 1) * 32 + k * 8,
+                                        vd + k * (2048 >> 4), idesc_o, n > 0 || k > 0);
+                    ptx::mma_commit(&o_half[i]);
+                    if ((n & 1) || n + 1 == halves) ptx::mma_commit(&empty[s]);
+                    if (n + 1 == halves) ptx::mma_commit(&o_full[i]);
                 }
                 __syncwarp();
             };
             auto filled = [&](int it) { return wait(&full[it % kStages], it / kStages); };
             ok = wait(q_full, 0) && filled(0);
             ptx::tc_fence_after();
-            if (ok) {
-                logits(0, 0);
-                logits(1, 0);
-            }
-            for (int j = 0; j < tiles && ok; ++j) {
-                const bool next = j + 1 < tiles;
-                ok = filled(2 * j + 1) && (!next || filled(2 * j + 2));
-                for (int i = 0; i < 2 && ok; ++i) {
-                    ok = wait(&p_half[i], j);
+            if (ok) logits(0);
+            for (int n = 0; n < halves && ok; ++n) {
+                if (n + 1 < halves) {
+                    ok = (!(n & 1) || filled(n + 1)) && wait(&s_free[i], n);  // (K of the next tile)
                     ptx::tc_fence_after();
-                    if (ok) output(i, j, 0);
-                    ok = ok && wait(&p_full[i], j);
-                    ptx::tc_fence_after();
-                    if (ok) output(i, j, 1);
-                    if (ok && next) logits(i, j + 1);
+                    if (ok) logits(n + 1);
                 }
+                ok = ok && ((n & 1) || filled(n + 1)) && wait(&p_full[2 * i + (n & 1)], n >> 1);  // (V of this one)
+                ptx::tc_fence_after();
+                if (ok) output(n);
             }
             if (!ok) {  // nothing of this block may still run when its TMEM is freed
-                if (ptx::elect_one()) ptx::mma_commit(drain);
+                if (ptx::elect_one()) ptx::mma_commit(&drain[i]);
                 int zero = 0;
-                ptx::mbar_wait(drain, 0, kWaitNs, &zero);
+                ptx::mbar_wait(&drain[i], 0, kWaitNs, &zero);
             }
         }
     }
