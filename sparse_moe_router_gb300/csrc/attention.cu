@@ -272,7 +272,10 @@ __global__ void __launch_bounds__(kThreads, Split<D, NB>::kBlocks) attn_split_ke
     for (int w = 0; w < kWarps; ++w) total += scan[w];
     const int64_t per = (total + gridDim.x - 1) / gridDim.x;
     const int64_t begin = per * blockIdx.x, end = min(total, begin + per);
-    if (begin >= end) return;
+    if (begin >= end) {
+        asm volatile("griddepcontrol.wait;" ::: "memory");
+        return;
+    }
     int64_t before = 0;  // the line up to the sequences of this chunk
     for (int b0 = 0;; b0 += kThreads) {
         __syncthreads();
@@ -623,31 +626,37 @@ __global__ void __launch_bounds__(kThreads, Split<D, NB>::kBlocks) attn_split_ke
             p.desc[blockIdx.x] = SplitDesc{(int)((seg_end - 1) / per - blockIdx.x + 1), rows, sw.q.q0, row0, head};
         __syncthreads();  // merge buffers are free again
     }
+    asm volatile("griddepcontrol.wait;" ::: "memory");  // the prompt kernel's end: what follows this grid follows both
 }
 
 template <int D, int NB, bool F16>
-cudaError_t launch(const AttnArgs &a, cudaStream_t s) {
+cudaError_t launch(const AttnArgs &a, bool after_prompt, cudaStream_t s) {
     using C = Split<D, NB>;
     cudaError_t e = cudaFuncSetAttribute(attn_split_kernel<D, NB, F16>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
     if (e != cudaSuccess) return e;
     const int sms = device_info().sm_count < kSplitMaxSms ? device_info().sm_count : kSplitMaxSms;
     const int grid = sms * C::kBlocks;
-    {
-        LaunchScope scope(KC_ATTN_SPLIT, s);
-        attn_split_kernel<D, NB, F16><<<grid, kThreads, C::kSmem, s>>>(a);
-        e = cudaGetLastError();
-        if (e != cudaSuccess) return e;
-    }
-    // launched while the split kernel still runs; its blocks wait for that kernel's end
-    LaunchScope scope(KC_ATTN_JOIN, s);
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)grid);
-    cfg.blockDim = dim3(512);
-    cfg.stream = s;
+    // Each launch may begin before the one before it ends: the split kernel beside the last blocks of the
+    // prompt kernel, which it does not read and whose end it awaits at its own; the join while the split
+    // kernel drains.
     cudaLaunchAttribute attr{};
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)grid);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = C::kSmem;
+    cfg.stream = s;
     cfg.attrs = &attr;
+    cfg.numAttrs = after_prompt ? 1 : 0;
+    {
+        LaunchScope scope(KC_ATTN_SPLIT, s);
+        e = cudaLaunchKernelEx(&cfg, attn_split_kernel<D, NB, F16>, a);
+        if (e != cudaSuccess) return e;
+    }
+    LaunchScope scope(KC_ATTN_JOIN, s);
+    cfg.blockDim = dim3(512);
+    cfg.dynamicSmemBytes = 0;
     cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, attn_join_kernel<D, NB, F16>, a);
 }
@@ -662,15 +671,16 @@ size_t split_part_floats(int D) {
 }
 
 template <int D, int NB>
-cudaError_t by_dtype(const AttnArgs &a, int dtype, cudaStream_t s) {
-    return dtype == MOE_DTYPE_F16 ? launch<D, NB, true>(a, s) : launch<D, NB, false>(a, s);
+cudaError_t by_dtype(const AttnArgs &a, int dtype, bool after_prompt, cudaStream_t s) {
+    return dtype == MOE_DTYPE_F16 ? launch<D, NB, true>(a, after_prompt, s) : launch<D, NB, false>(a, after_prompt, s);
 }
 
 // shared: 4 row tiles (2 at D = 256) share each key tile that is read and widened.
-cudaError_t launch_attn_split(const AttnArgs &a, int D, int dtype, bool shared, cudaStream_t s) {
-    if (D == 64) return shared ? by_dtype<64, 4>(a, dtype, s) : by_dtype<64, 1>(a, dtype, s);
-    if (D == 128) return shared ? by_dtype<128, 4>(a, dtype, s) : by_dtype<128, 1>(a, dtype, s);
-    return shared ? by_dtype<256, 2>(a, dtype, s) : by_dtype<256, 1>(a, dtype, s);
+// after_prompt: the launch just before, on the same stream, is the same call's prompt kernel.
+cudaError_t launch_attn_split(const AttnArgs &a, int D, int dtype, bool shared, bool after_prompt, cudaStream_t s) {
+    if (D == 64) return shared ? by_dtype<64, 4>(a, dtype, after_prompt, s) : by_dtype<64, 1>(a, dtype, after_prompt, s);
+    if (D == 128) return shared ? by_dtype<128, 4>(a, dtype, after_prompt, s) : by_dtype<128, 1>(a, dtype, after_prompt, s);
+    return shared ? by_dtype<256, 2>(a, dtype, after_prompt, s) : by_dtype<256, 1>(a, dtype, after_prompt, s);
 }
 
 }  // namespace moe

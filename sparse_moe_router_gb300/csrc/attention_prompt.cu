@@ -33,8 +33,8 @@ constexpr int kStages = 4;  // K and V tiles in flight, in the order K0 V0 K1 V1
 constexpr int kSoftWarps = 8, kConvWarps = 8, kMmaWarp = 16;
 constexpr int kThreads = 20 * 32;  // (three warps beside the MMA warp only complete its warpgroup)
 // Registers a thread: 96 at launch (five warps a scheduler); of a scheduler's 5 x 96 the two softmax
-// warps, which hold 64 logits and 32 pairs of weights, take 2 x 136, the converters 2 x 88, the MMA warp 32.
-constexpr int kLaunchRegs = 96, kSoftRegs = 136, kConvRegs = 88, kMmaRegs = 32;
+// warps, which hold 64 logits and 32 pairs of weights, take 2 x 144, the converters 2 x 80, the MMA warp 32.
+constexpr int kLaunchRegs = 96, kSoftRegs = 144, kConvRegs = 80, kMmaRegs = 32;
 static_assert(8 * kSoftRegs + 8 * kConvRegs + 4 * kMmaRegs <= 20 * kLaunchRegs, "more registers than the block has");
 constexpr uint64_t kWaitNs = 2000000000ull;  // 2 s: far above any legitimate wait
 constexpr float kMostSum = 32768.f;  // 64 weights of one row may add up to this
@@ -113,17 +113,39 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
     const int tid = (int)threadIdx.x, lane = tid & 31;
     const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);  // known to be the same in all lanes
 
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // (the split kernel does not depend on this one)
+
     // ------------------------------------------------------------------- the block's rows --
+    // Blocks begin in the order of their number, so the ones with most keys come first: of up to 32 sequences the
+    // longest, and of each its last rows (a causal row sees the more the later it is).
     const int head = (int)blockIdx.x % v.KH;
-    const int slot = slots - 1 - (int)blockIdx.x / v.KH;  // a sequence's last rows see most keys: first
-    int lo_b = 0, hi_b = v.n_seqs - 1;
-    while (lo_b < hi_b) {
-        const int mid = (lo_b + hi_b + 1) >> 1;
-        if (slot_base(v, mid) <= slot) lo_b = mid; else hi_b = mid - 1;
+    int b, row0;
+    if (v.n_seqs <= 32) {
+        Seq own{0, 0, 0};
+        if (lane < v.n_seqs) own = load_seq(v, lane);
+        const int64_t own_rows = (int64_t)own.n * v.G;
+        const int count = own_rows >= p.prompt_rows ? (int)((own_rows + kRowsBlock - 1) / kRowsBlock) : 0;
+        int base = 0;  // blocks of the sequences before this lane's
+        for (int c = 0; c < v.n_seqs; ++c) {
+            const int kv = __shfl_sync(0xffffffffu, own.kv, c), n = __shfl_sync(0xffffffffu, count, c);
+            if (kv > own.kv || (kv == own.kv && c < lane)) base += n;
+        }
+        const int slot = (int)blockIdx.x / v.KH;
+        const uint32_t mine = __ballot_sync(0xffffffffu, slot >= base && slot < base + count);
+        if (mine == 0) return;
+        b = __ffs(mine) - 1;
+        row0 = (__shfl_sync(0xffffffffu, base + count, b) - 1 - slot) * kRowsBlock;
+    } else {
+        const int slot = slots - 1 - (int)blockIdx.x / v.KH;
+        int lo_b = 0, hi_b = v.n_seqs - 1;
+        while (lo_b < hi_b) {
+            const int mid = (lo_b + hi_b + 1) >> 1;
+            if (slot_base(v, mid) <= slot) lo_b = mid; else hi_b = mid - 1;
+        }
+        b = lo_b;
+        row0 = (slot - slot_base(v, b)) * kRowsBlock;
     }
-    const int b = lo_b;
     const Seq q = load_seq(v, b);
-    const int row0 = (slot - slot_base(v, b)) * kRowsBlock;
     const int rows = min(kRowsBlock, q.n * v.G - row0);
     if (row0 < 0 || rows <= 0 || q.n * v.G < p.prompt_rows) return;  // (short runs are the split kernel's)
     const int first_pos = q.kv - q.n;

@@ -244,7 +244,7 @@ moe_status moe_attention(const moe_attn_config *cfg, const moe_kv_cache *cache, 
     if (prompts) MOE_CUDA(launch_attn_prompt(a, c.head_dim, c.dtype, s));
     if (batch->n_seqs > 1 || !prompts)
         MOE_CUDA(launch_attn_split(a, c.head_dim, c.dtype,
-                                   mean > 8 && (int64_t)batch->n_seqs * batch->max_pages * c.page_size >= kManyKeys, s));
+                                   mean > 8 && (int64_t)batch->n_seqs * batch->max_pages * c.page_size >= kManyKeys, prompts, s));
     return MOE_OK;
 }
 
