@@ -414,9 +414,12 @@ size_t moe_attn_workspace_size(const moe_attn_config *cfg, int max_seqs, int max
  *             larger, else its codes are re-rounded (to nearest even) under the new one
  *   codes     the E4M3 value nearest to value / s, ties to even, of the exact rotated value
  * A page written by one sequence of a call must not be written by another.  Tokens at negative
- * positions (padding in front) are not cached and give q_out rows of 0.  NaN is stored as 0 and
- * infinities as +-448 s; they, a page id outside [0, n_pages), and a position past the table or
- * rope are reported as MOE_ERR_INVALID_ARG in the status word (the token is then not cached).
+ * positions (padding in front) are not cached and give q_out rows of 0.
+ * Reported as MOE_ERR_INVALID_ARG in the status word: NaN, stored as 0; infinities, stored as
+ * +-448 s under the largest scale (as 0 where a rotation makes them NaN); a position past rope,
+ * stored as zeros, its q_out row 0; a page id outside [0, n_pages), whose tokens are not cached; a
+ * kv_len past the table (the sequence's pages and q_out rows are then unspecified); rows of q from
+ * q_start[B] on, given 0.
  * q [T, q_heads, D] row stride q_ld, k and v [T, kv_heads, D] strides k_ld, v_ld, q_out stride
  * q_out_ld (q_out may be q).  q and q_out may both be NULL. */
 moe_status moe_kv_append(const moe_attn_config *cfg, const moe_kv_cache *cache, const moe_kv_batch *batch,
@@ -433,7 +436,7 @@ moe_status moe_kv_append(const moe_attn_config *cfg, const moe_kv_cache *cache, 
  * into fp16 and multiplied with the exact codes, sums and softmax statistics in fp32; p is
  * rounded to fp16 (11 bits) for the product with the values; out is rounded once.
  * softmax_scale > 0.  Deterministic.  A bad page id or a kv_len past the table is reported in
- * the status word (those rows are then unspecified). */
+ * the status word (those rows are then unspecified).  Rows from q_start[B] on stay untouched. */
 moe_status moe_attention(const moe_attn_config *cfg, const moe_kv_cache *cache, const moe_kv_batch *batch,
                          const void *q, int64_t q_ld, float softmax_scale, int causal, int window, void *out,
                          int64_t out_ld, float *lse, void *ws, size_t ws_bytes, void *stream);

@@ -1,37 +1,48 @@
 // attention_prompt.cu -- attention over the paged 8-bit cache for runs of many new tokens, on the
 // 5th-generation tensor cores (tcgen05, TMEM).
 //
-// A block takes 256 query rows (token, q head) of one kv head as two 128-row tiles and walks the
-// keys they see in tiles of 128: S = Q K^T into TMEM, softmax weights back into TMEM as fp16 over S,
-// O += P V from there.  All rows of a group of q heads share each key and value tile, so a tile
-// of K and V is widened once for 256 rows.
+// A block takes 256 query rows (token, q head) of one kv head as two 128-row tiles (one at D = 256,
+// where the output of one fills TMEM) and walks the keys they see in tiles of 128.  In halves of 64
+// keys a row tile computes S = Q K^T into TMEM, the softmax takes S into registers at once, which
+// frees it for the next half's logits, and puts the weights beside it as fp16; O += P V reads them
+// from there.  All rows of a group of q heads share each key and value tile, so a tile of K and V
+// is widened once for 256 rows.
 //
-// Bound: 4 D flops a (row, key) on the tensor cores; one tile pair is 4 x 512 tensor cycles at
-// D = 128, and the weights of its 2 x 16,384 logits take about as long on two warpgroups, so the two
-// row tiles alternate: while the tensor cores work on one, the other's softmax runs.  The 8-bit
-// codes cannot be an operand beside fp16 weights (both operands of an MMA have one type, and queries in 8
-// bits would lose what the 16-bit ones hold), so eight warps read codes from global memory (L2,
-// mostly: all tiles of a head read the same pages), widen them exactly to fp16 and store them in the
-// swizzled layout that the MMA reads: 96 KB of shared-memory traffic a tile against the MMA's own
-// 192 KB.  The exponents of the pages are drawn into the codes relative to the largest one the block
-// will meet (exact in fp16 unless a page is 2^-15 below it, and then off by at most 2^-25 of the
-// largest), so one factor a row holds for all keys.
+// Bound: 4 D flops a (row, key) on the tensor cores; at D = 128 a tile of keys is 4 x 512 tensor
+// cycles for the two row tiles, and their 2 x 16,384 exponentials take 1024 cycles of the SM's 32 a cycle
+// beside the other 5 instructions a logit, so that both have to run at once: logits a half tile ahead,
+// two row tiles apart.  The 8-bit codes cannot be an operand beside fp16 weights (both operands of an MMA
+// have one type, and queries in 8 bits would lose what the 16-bit ones hold), so eight warps read
+// codes from global memory (L2, mostly: all tiles of a head read the same pages), widen them
+// exactly to fp16 and store them in the swizzled layout that the MMA reads: 96 KB of shared-memory
+// traffic a tile against the MMA's own 192 KB.  The exponents of the pages are drawn into the codes
+// relative to the largest one the block will meet (exact in fp16 unless a page is 2^-15 below it, and
+// then off by at most 2^-25 of the largest), so one factor a row holds for all keys.
+//
+// Measured, 16 q heads, 2 kv heads, causal: 8192 tokens at D = 128 202 us (1360 TFLOP/s, 72% of the
+// measured cuBLAS rate, 79% of the sustained one); five pieces of up to 1031 tokens behind up to 6007, 24 q heads in
+// groups of 3, D = 64, 74 us; at D = 256 with 4 kv heads 597 us (922 TFLOP/s: with one row tile a block no second one hides the
+// softmax, and a converter has 128 rows to widen for instead of 256), where the split kernel takes
+// 4635.  On the way at D = 128: whole tiles of logits in the place their weights take 214 us; halves
+// from one MMA warp 284 (its waits for one row tile hold up the other); two threads a row 232 (a barrier a
+// half tile); four converter warps 277; the maximum looked for in every tile 221; scalar instead of paired
+// fp32 in the softmax 219; the next logits loaded before the weights are stored 233 (registers).
 //
 // Roles: warps 0-3 and 4-7 do the softmax of row tiles 0 and 1, one row a thread; warps 8-15 widen K
-// and V; warp 16 issues the MMAs.  A row's maximum is not looked for in every tile: the weights are
-// taken under the reference so far, and their sum (needed anyway) shows when that has become too
-// small; the row's thread then finds the maximum, rescales its row of O and takes the weights again.
+// and V; warps 16 and 17 issue the MMAs of row tiles 0 and 1.  A row's maximum is not looked for in
+// every tile: the weights are taken under the reference so far, and their sum (needed anyway) shows when that
+// has become too small; the row's thread then finds the maximum, rescales its row of O and takes the
+// weights again.
 #include "layer.h"
 #include "ptx.cuh"
 
 namespace moe {
 namespace {
 
-constexpr int kRowTile = 128, kRowsBlock = 2 * kRowTile;
+constexpr int kRowTile = 128;
 constexpr int kKeys = 128;  // keys a tile
-constexpr int kStages = 4;  // K and V tiles in flight, in the order K0 V0 K1 V1 ...
 constexpr int kSoftWarps = 8, kConvWarps = 8, kMmaWarp = 16;
-constexpr int kThreads = 20 * 32;  // (three warps beside the MMA warp only complete its warpgroup)
+constexpr int kThreads = 20 * 32;  // (the last two only complete the warpgroup)
 // Registers a thread: 96 at launch (five warps a scheduler); of a scheduler's 5 x 96 the two softmax
 // warps, which hold 64 logits and 32 pairs of weights, take 2 x 144, the converters 2 x 80, the MMA warp 32.
 constexpr int kLaunchRegs = 96, kSoftRegs = 144, kConvRegs = 80, kMmaRegs = 32;
@@ -44,8 +55,11 @@ struct Prompt {
     static constexpr int kBlocks = D / 64;                    // 128-byte column blocks of a row
     static constexpr int kBlockBytes = kKeys * 128;           // one column block of a 128-row tile
     static constexpr int kTileBytes = kBlocks * kBlockBytes;  // a tile of Q, K or V
-    static constexpr int kSmem = 1024 + (2 + kStages) * kTileBytes + 256;  // 1 KB to align; barriers
-    static constexpr uint32_t kColO = 2 * kKeys;              // TMEM: S0 S1 O0 O1
+    static constexpr int kTiles = D == 256 ? 1 : 2;           // row tiles a block: TMEM holds one output of 256 dims
+    static constexpr int kRows = kTiles * kRowTile;
+    static constexpr int kStages = D == 256 ? 2 : 4;          // K and V tiles in flight, in the order K0 V0 K1 V1 ...
+    static constexpr int kSmem = 1024 + (kTiles + kStages) * kTileBytes + 256;  // 1 KB to align; barriers
+    static constexpr uint32_t kColO = kTiles * kKeys;         // TMEM: S0 P0 (S1 P1) O0 (O1)
     static constexpr uint32_t kCols = 512;
 };
 
@@ -84,19 +98,21 @@ __device__ __forceinline__ void regs_down() {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R));
 }
 
-// Block (slot, head): sequence b owns the 256-row slots base(b) .. base(b+1)-1 of every head, with
-// base(b) = q_start[b] G / 256 + b (its n G rows need at most n G / 256 + 1 of them).
+// Block (slot, head): sequence b owns slots base(b) .. base(b+1)-1 of R rows each of every head, with
+// base(b) = q_start[b] G / R + b (its n G rows need at most n G / R + 1 of them).
+template <int R>
 __device__ __forceinline__ int slot_base(const KvView &v, int b) {
-    return (int)((int64_t)v.q_start[b] * v.G / kRowsBlock) + b;
+    return (int)((int64_t)v.q_start[b] * v.G / R) + b;
 }
 
 template <int D, bool F16>
 __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_constant__ AttnArgs p, int slots) {
     using C = Prompt<D>;
+    constexpr int kStages = C::kStages, kTiles = C::kTiles, kRows = C::kRows;
     const KvView &v = p.kv;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = smem_raw + ((1024u - (ptx::smem_u32(smem_raw) & 1023u)) & 1023u);
-    uint8_t *q_smem = smem, *kv_smem = smem + 2 * C::kTileBytes;
+    uint8_t *q_smem = smem, *kv_smem = smem + kTiles * C::kTileBytes;
     uint64_t *bars = reinterpret_cast<uint64_t *>(kv_smem + kStages * C::kTileBytes);
     uint64_t *full = bars, *empty = bars + kStages;  // of a stage
     uint64_t *s_full = empty + kStages;              // [2] 64 logits of each row of a row tile are in TMEM
@@ -124,7 +140,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
         Seq own{0, 0, 0};
         if (lane < v.n_seqs) own = load_seq(v, lane);
         const int64_t own_rows = (int64_t)own.n * v.G;
-        const int count = own_rows >= p.prompt_rows ? (int)((own_rows + kRowsBlock - 1) / kRowsBlock) : 0;
+        const int count = own_rows >= p.prompt_rows ? (int)((own_rows + kRows - 1) / kRows) : 0;
         int base = 0;  // blocks of the sequences before this lane's
         for (int c = 0; c < v.n_seqs; ++c) {
             const int kv = __shfl_sync(0xffffffffu, own.kv, c), n = __shfl_sync(0xffffffffu, count, c);
@@ -134,19 +150,19 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
         const uint32_t mine = __ballot_sync(0xffffffffu, slot >= base && slot < base + count);
         if (mine == 0) return;
         b = __ffs(mine) - 1;
-        row0 = (__shfl_sync(0xffffffffu, base + count, b) - 1 - slot) * kRowsBlock;
+        row0 = (__shfl_sync(0xffffffffu, base + count, b) - 1 - slot) * kRows;
     } else {
         const int slot = slots - 1 - (int)blockIdx.x / v.KH;
         int lo_b = 0, hi_b = v.n_seqs - 1;
         while (lo_b < hi_b) {
             const int mid = (lo_b + hi_b + 1) >> 1;
-            if (slot_base(v, mid) <= slot) lo_b = mid; else hi_b = mid - 1;
+            if (slot_base<kRows>(v, mid) <= slot) lo_b = mid; else hi_b = mid - 1;
         }
         b = lo_b;
-        row0 = (slot - slot_base(v, b)) * kRowsBlock;
+        row0 = (slot - slot_base<kRows>(v, b)) * kRows;
     }
     const Seq q = load_seq(v, b);
-    const int rows = min(kRowsBlock, q.n * v.G - row0);
+    const int rows = min(kRows, q.n * v.G - row0);
     if (row0 < 0 || rows <= 0 || q.n * v.G < p.prompt_rows) return;  // (short runs are the split kernel's)
     const int first_pos = q.kv - q.n;
     // keys that any of the rows sees
@@ -161,17 +177,17 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
     if (tid == 0) {
         for (int s = 0; s < kStages; ++s) {
             ptx::mbar_init(&full[s], kConvWarps);
-            ptx::mbar_init(&empty[s], 2);  // both row tiles are done with it
+            ptx::mbar_init(&empty[s], kTiles);  // every row tile is done with it
         }
         for (int i = 0; i < 2; ++i) {
             ptx::mbar_init(&s_full[i], 1);
-            ptx::mbar_init(&p_full[2 * i], kSoftWarps / 2);
-            ptx::mbar_init(&p_full[2 * i + 1], kSoftWarps / 2);
-            ptx::mbar_init(&s_free[i], kSoftWarps / 2);
+            ptx::mbar_init(&p_full[2 * i], 4);
+            ptx::mbar_init(&p_full[2 * i + 1], 4);
+            ptx::mbar_init(&s_free[i], 4);
             ptx::mbar_init(&o_half[i], 1);
             ptx::mbar_init(&o_full[i], 1);
         }
-        ptx::mbar_init(q_full, kSoftWarps);
+        ptx::mbar_init(q_full, 4 * kTiles);
         ptx::mbar_init(&drain[0], 1);
         ptx::mbar_init(&drain[1], 1);
         *abort_flag = 0;
@@ -209,6 +225,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
 
     if (warp < kSoftWarps) {
         regs_up<kSoftRegs>();
+        if (warp < 4 * kTiles) {
         // ---------------------------------------------------------------------- softmax --
         // Thread t has row t of the block: lane t % 128 of row tile t / 128.
         const int i = warp >> 2, r = tid, rr = r & (kRowTile - 1);
@@ -223,15 +240,18 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
         {
             const uint16_t *src = p.q + (int64_t)(q.q0 + tok) * p.q_ld + (int64_t)qh * D;
             uint8_t *dst = q_smem + i * C::kTileBytes + rr * 128;
-            uint4 qv[D / 8];
-#pragma unroll
-            for (int c = 0; c < D / 8; ++c)
-                qv[c] = live ? __ldg(reinterpret_cast<const uint4 *>(src + c * 8)) : make_uint4(0, 0, 0, 0);
+            constexpr int kHeld = D < 256 ? D / 8 : 16;  // pieces kept in registers; a wide row is read twice
+            uint4 qv[kHeld];
             float amax = 0.f;
 #pragma unroll
             for (int c = 0; c < D / 8; ++c) {
+                if (c % kHeld == 0) {
+#pragma unroll
+                    for (int x = 0; x < kHeld; ++x)
+                        qv[x] = live ? __ldg(reinterpret_cast<const uint4 *>(src + (c + x) * 8)) : make_uint4(0, 0, 0, 0);
+                }
                 float f[8];
-                unpack8<F16>(qv[c], f);
+                unpack8<F16>(qv[c % kHeld], f);
 #pragma unroll
                 for (int j = 0; j < 8; ++j) amax = fmaxf(amax, fabsf(f[j]));
             }
@@ -239,8 +259,13 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
             const float q_inv = pow2f(-q_exp);
 #pragma unroll
             for (int c = 0; c < D / 8; ++c) {
+                if (D / 8 > kHeld && c % kHeld == 0) {
+#pragma unroll
+                    for (int x = 0; x < kHeld; ++x)
+                        qv[x] = live ? __ldg(reinterpret_cast<const uint4 *>(src + (c + x) * 8)) : make_uint4(0, 0, 0, 0);
+                }
                 float f[8];
-                unpack8<F16>(qv[c], f);
+                unpack8<F16>(qv[c % kHeld], f);
 #pragma unroll
                 for (int j = 0; j < 8; ++j) f[j] *= q_inv;
                 *reinterpret_cast<uint4 *>(dst + (c >> 3) * C::kBlockBytes + (((c & 7) ^ (rr & 7)) << 4)) = pack8<true>(f);
@@ -363,18 +388,20 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
             }
             if (live && p.lse) p.lse[(int64_t)(q.q0 + tok) * v.QH + qh] = (m + log2f(l)) * 0.6931471805599453f;
         }
+        }
     } else if (warp < kMmaWarp) {
         regs_down<kConvRegs>();
         // ------------------------------------------------------------- K and V, widened --
         // Warp w owns keys 16 w .. 16 w + 15 of every tile: they lie in one page.  A load takes whole rows
-        // (4 of 128 codes, 8 of 64), so that it reads full lines, 16 codes a lane; lanes are laid out
-        // so that each 8 of them hold 4 pieces of two neighbouring rows, whose 16-byte stores fall on
+        // (2 of 256 codes, 4 of 128, 8 of 64), so that it reads full lines, 16 codes a lane; lanes are laid
+        // out so that each 8 of them hold 4 pieces of two neighbouring rows, whose 16-byte stores fall on
         // all the banks.  The registers of a tile's codes take the next tile's as soon as they are
-        // widened, so a load has a whole tile's time to arrive.
+        // widened, so a load has a whole tile's time to arrive (at D = 256, where K and V take turns in
+        // the same registers, half of it).
         constexpr int kRowsLoad = 512 / D, kLoads = 16 / kRowsLoad;
         const int cw = warp - kSoftWarps;
-        const int piece = D == 128 ? (lane >> 1 & 4) | (lane & 3) : lane & 3;
-        const int sub = D == 128 ? (lane >> 3 & 2) | (lane >> 2 & 1) : lane >> 2;
+        const int piece = D == 256 ? (lane >> 3 << 2) | (lane & 3) : D == 128 ? (lane >> 1 & 4) | (lane & 3) : lane & 3;
+        const int sub = D == 256 ? lane >> 2 & 1 : D == 128 ? (lane >> 3 & 2) | (lane >> 2 & 1) : lane >> 2;
         auto page_at = [&](int tile) {  // page * KH + head
             const int key = (tile0 + tile) * kKeys + cw * 16;
             int page = 0;
@@ -386,7 +413,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
             const __half2 f = __float2half2_rn(e < -24 ? 0.f : pow2f(e));
             return *reinterpret_cast<const uint32_t *>(&f);
         };
-        const int log_pd = v.log_p + (D == 128 ? 7 : 6);
+        const int log_pd = v.log_p + (D == 256 ? 8 : D == 128 ? 7 : 6);
         auto load = [&](uint4 (&raw)[kLoads], int tile, int page, const uint8_t *codes) {
             const int key0 = (tile0 + tile) * kKeys + cw * 16;
             const uint8_t *src = codes + ((uint64_t)(uint32_t)page << log_pd) + ((key0 & (v.P - 1)) + sub) * D + piece * 16;
@@ -397,7 +424,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
                     raw[n] = load_codes16(src + n * kRowsLoad * D);
             }
         };
-        // offsets of a piece's two stores in rows that are below 4 modulo 8 (D = 64: in any)
+        // offsets of a piece's two stores in the rows of the first load; later loads' rows differ in their upper bits
         const uint32_t base = (uint32_t)(piece >> 2) * C::kBlockBytes + (uint32_t)(cw * 16 + sub) * 128;
         const uint32_t c0 = ((2 * (piece & 3)) ^ sub) << 4, c1 = c0 ^ 16u;
         auto widen = [&](const uint4 (&raw)[kLoads], int it, uint32_t f) {
@@ -412,7 +439,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
                     h[2 * k] = mul2(h[2 * k], f);
                     h[2 * k + 1] = mul2(h[2 * k + 1], f);
                 }
-                const uint32_t flip = (n * kRowsLoad & 4) << 4;  // row bit 2 of the swizzle
+                const uint32_t flip = (n * kRowsLoad & 7) << 4;  // of the swizzle
                 uint8_t *dst = st + n * kRowsLoad * 128;
                 *reinterpret_cast<uint4 *>(dst + (c0 ^ flip)) = make_uint4(h[0], h[1], h[2], h[3]);
                 *reinterpret_cast<uint4 *>(dst + (c1 ^ flip)) = make_uint4(h[4], h[5], h[6], h[7]);
@@ -427,34 +454,44 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
             __syncwarp();
             if (lane == 0) ptx::mbar_arrive(&full[it % kStages]);
         };
-        uint4 rk[kLoads], rv[kLoads];
+        constexpr bool kBoth = D < 256;
+        uint4 rk[kLoads], rv[kBoth ? kLoads : 1];
         int page1 = page_at(0), page2 = page_at(1);
         float sk = __ldg(v.k_scale + page1), sv = __ldg(v.v_scale + page1);
         if (tiles > 0) {
             load(rk, 0, page1, v.k_codes);
-            load(rv, 0, page1, v.v_codes);
+            if constexpr (kBoth) load(rv, 0, page1, v.v_codes);
         }
         for (int j = 0; j < tiles; ++j) {
             const uint32_t fk = factor(sk, k_exp), fv = factor(sv, v_exp);
+            const int page0 = page1;
             page1 = page2;  // of tile j + 1
             sk = __ldg(v.k_scale + page1), sv = __ldg(v.v_scale + page1);
             page2 = page_at(j + 2);
             if (!(ok = free_stage(2 * j))) break;
             widen(rk, 2 * j, fk);
-            if (j + 1 < tiles) load(rk, j + 1, page1, v.k_codes);
-            publish(2 * j);
-            if (!(ok = free_stage(2 * j + 1))) break;
-            widen(rv, 2 * j + 1, fv);
-            if (j + 1 < tiles) load(rv, j + 1, page1, v.v_codes);
+            if constexpr (kBoth) {
+                if (j + 1 < tiles) load(rk, j + 1, page1, v.k_codes);
+                publish(2 * j);
+                if (!(ok = free_stage(2 * j + 1))) break;
+                widen(rv, 2 * j + 1, fv);
+                if (j + 1 < tiles) load(rv, j + 1, page1, v.v_codes);
+            } else {
+                load(rk, j, page0, v.v_codes);
+                publish(2 * j);
+                if (!(ok = free_stage(2 * j + 1))) break;
+                widen(rk, 2 * j + 1, fv);
+                if (j + 1 < tiles) load(rk, j + 1, page1, v.k_codes);
+            }
             publish(2 * j + 1);
         }
-    }     else {
+    } else {
         regs_down<kMmaRegs>();
-        if (warp < kMmaWarp + 2 && tiles > 0) {
-            const int i = warp - kMmaWarp;  // the row tile
+        if (warp < kMmaWarp + kTiles && tiles > 0) {
             // ------------------------------------------------------------------ the MMAs --
-            // In the order O_0 S_0 O_1 S_1 ...: while the tensor cores are at one row tile's output and next
-            // logits, the softmax warps are at the other's logits.
+            // A warp for each row tile: the next 64 logits as soon as the last are in registers, then the output of
+            // the last's weights.
+            const int i = warp - kMmaWarp;
             const uint32_t idesc_s = ptx::idesc_f16_f32(kRowTile, 64, false);
             const uint32_t idesc_o = ptx::idesc_f16_f32(kRowTile, D, true);
             const uint64_t q_desc = ptx::sw128_desc(ptx::smem_u32(q_smem));
@@ -532,7 +569,7 @@ cudaError_t launch(const AttnArgs &a, cudaStream_t s) {
     cudaError_t e = cudaFuncSetAttribute(attn_prompt_kernel<D, F16>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     LaunchScope scope(KC_ATTN_PROMPT, s);
-    const int slots = (int)((int64_t)a.kv.n_tokens * a.kv.G / kRowsBlock) + a.kv.n_seqs;
+    const int slots = (int)((int64_t)a.kv.n_tokens * a.kv.G / Prompt<D>::kRows) + a.kv.n_seqs;
     attn_prompt_kernel<D, F16><<<slots * a.kv.KH, kThreads, smem, s>>>(a, slots);
     return cudaGetLastError();
 }
@@ -542,7 +579,8 @@ cudaError_t launch(const AttnArgs &a, cudaStream_t s) {
 cudaError_t launch_attn_prompt(const AttnArgs &a, int D, int dtype, cudaStream_t s) {
     const bool f16 = dtype == MOE_DTYPE_F16;
     if (D == 64) return f16 ? launch<64, true>(a, s) : launch<64, false>(a, s);
-    return f16 ? launch<128, true>(a, s) : launch<128, false>(a, s);
+    if (D == 128) return f16 ? launch<128, true>(a, s) : launch<128, false>(a, s);
+    return f16 ? launch<256, true>(a, s) : launch<256, false>(a, s);
 }
 
 }  // namespace moe

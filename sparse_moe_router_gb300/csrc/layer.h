@@ -61,7 +61,7 @@ constexpr int kSplitMaxSms = 160, kSplitMaxBlocks = 2 * kSplitMaxSms;
 // Floats of workspace the split kernel needs for partial results.
 size_t split_part_floats(int D);
 cudaError_t launch_attn_split(const AttnArgs &a, int D, int dtype, bool shared, bool after_prompt, cudaStream_t s);
-cudaError_t launch_attn_prompt(const AttnArgs &a, int D, int dtype, cudaStream_t s);  // D 64 or 128
+cudaError_t launch_attn_prompt(const AttnArgs &a, int D, int dtype, cudaStream_t s);
 
 struct NormArgs {
     const uint16_t *x, *resid, *gate, *w_post, *w_pre;

@@ -64,10 +64,13 @@ moe_status check_batch(const moe_attn_config &c, const moe_kv_cache *k, const mo
 constexpr int kPromptRows = 128;
 // Mean rows a sequence and kv head below which a batch is a decode step, all of it the split kernel's.
 constexpr int kPromptMean = 33;
-// Cached tokens (as many as the page table can name) from which the split kernel's row tiles share key
-// tiles.  Below, the SMs are short of work and more, smaller segments end sooner: 8 sequences of 32 rows, D = 128,
-// 64,000 keys 25.7 us shared and 26.7 not, 256,000 keys 53.6 and 76.6; one of 8,000 keys 27.4 and 14.2.
-constexpr int kManyKeys = 1 << 17;
+// From this many steps a block times row tiles a sequence (4 at most), the split kernel's row tiles share key
+// tiles.  Below, the SMs are short of work and more, smaller segments end sooner.  us shared and not, at 304 blocks,
+// D = 128, groups of 8, 2 kv heads: 4 tiles, 8 sequences of 4000 keys (26) 20.5 and 20.0, of 10,000 (66) 27.9
+// and 29.8, of 32,000 (211) 53.6 and 76.6; 3 tiles, 16 of 4000 (30) 25.2 and 24.0, 32 of 4000 (61) 37.3 and 40.2;
+// 2 tiles, 32 of 4000 (27) 35.0 and 30.3, 32 of 16,000 (105) 87.1 and 94.1; D = 256, 4 kv heads, 4 tiles: 8 of
+// 4000 (54) 27.4 and 27.3, of 16,000 (211) 59.6 and 89.4.
+constexpr int kManySteps = 56;
 
 struct Layout {
     size_t desc, part, total;
@@ -239,12 +242,17 @@ moe_status moe_attention(const moe_attn_config *cfg, const moe_kv_cache *cache, 
     // leaves a kernel out that has none for sure, and the prompt kernel in a step of few tokens a
     // sequence: its launch would cost more (5 us) than the rare long run among them.
     const int64_t rows = (int64_t)batch->n_tokens * a.kv.G, mean = rows / batch->n_seqs;
-    const bool prompts = c.head_dim <= 128 && rows >= kPromptRows && mean >= kPromptMean;
-    a.prompt_rows = prompts ? kPromptRows : INT_MAX;
+    const bool prompts = rows >= kPromptRows && mean >= kPromptMean;
+    a.prompt_rows = !prompts ? INT_MAX : batch->n_seqs == 1 ? 1 : kPromptRows;
     if (prompts) MOE_CUDA(launch_attn_prompt(a, c.head_dim, c.dtype, s));
-    if (batch->n_seqs > 1 || !prompts)
-        MOE_CUDA(launch_attn_split(a, c.head_dim, c.dtype,
-                                   mean > 8 && (int64_t)batch->n_seqs * batch->max_pages * c.page_size >= kManyKeys, prompts, s));
+    if (batch->n_seqs > 1 || !prompts) {
+        // steps of the split kernel with one row tile a segment, at most
+        const int64_t seen = window > 0 ? (int64_t)window + batch->n_tokens : INT64_MAX;
+        const int64_t table = (int64_t)batch->max_pages * c.page_size, keys = seen < table ? seen : table;
+        const int64_t steps = (rows + 7) / 8 * c.kv_heads * ((keys + 127) / 128), tiles = mean > 24 ? 4 : (mean + 7) / 8;
+        const bool shared = tiles > 1 && steps * tiles >= (int64_t)kManySteps * 2 * device_info().sm_count;
+        MOE_CUDA(launch_attn_split(a, c.head_dim, c.dtype, shared, prompts, s));
+    }
     return MOE_OK;
 }
 

@@ -89,7 +89,7 @@ def test_prompts(dtype, QH, KH, D, P, lens):
 
 
 @pytest.mark.parametrize("causal,window", [(True, 100), (False, 0), (False, 200), (True, 1)])
-@pytest.mark.parametrize("QH,KH,D,P", [(16, 2, 128, 64), (12, 4, 64, 16)])
+@pytest.mark.parametrize("QH,KH,D,P", [(16, 2, 128, 64), (12, 4, 64, 16), (4, 2, 256, 32)])
 def test_prompt_masks(causal, window, QH, KH, D, P):
     s = Setup([(300, 700), (290, 200), (64, 64)], QH, KH, D, P, seed=6)
     q = make_q(s)
@@ -100,10 +100,10 @@ def test_prompt_masks(causal, window, QH, KH, D, P):
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
 @pytest.mark.parametrize("QH,KH,D,P", [(16, 2, 128, 64), (6, 2, 64, 16), (4, 1, 256, 32), (24, 2, 128, 128)])
 def test_row_tiles_that_share_keys(dtype, QH, KH, D, P):
-    """A few tokens a sequence in a table that could name more than 2^17 tokens: the form whose row tiles
-    share key tiles."""
+    """A few tokens a sequence in a table that could name 2^20 tokens: the form whose row tiles share key
+    tiles."""
     s = Setup([(4, 300), (7, 7), (3, 1000), (9, 4), (0, 20), (5, 129)], QH, KH, D, P, dtype=dtype, seed=D)
-    pages = (1 << 17) // (6 * P) + 1
+    pages = (1 << 20) // P
     wide = torch.full((6, pages), -7, dtype=torch.int32)
     wide[:, :s.table.shape[1]] = s.table
     s.table = wide
@@ -211,6 +211,25 @@ def test_many_sequences(n):
     q = make_q(s)
     out, lse = run(s, q)
     check(s, q, out, lse)
+
+
+@pytest.mark.parametrize("used", [0, 5, 30, 31, 299])
+@pytest.mark.parametrize("seqs", [1, 2])
+def test_rows_past_the_last_sequence(used, seqs):
+    """A batch held for more tokens than its sequences have: the rows behind them stay as they are."""
+    s = Setup([(300, 700)] + [(0, 9)] * (seqs - 1), 8, 2, 128, 64, seed=4)
+    q = make_q(s)
+    s.q_start[1:] = used
+    cache, batch, ws = s.device()
+    out = torch.full_like(q, 9.0)
+    lse = torch.full((s.T, 8), 9.0, device="cuda")
+    abi.moe_attention(s.cfg, cache, batch, q, out, ws, lse=lse)
+    assert abi.moe_check_status(ws) == 0
+    assert bool((out[used:] == 9).all()) and bool((lse[used:] == 9).all())
+    part = Setup([(300, 700)] + [(0, 9)] * (seqs - 1), 8, 2, 128, 64, seed=4)
+    part.q_start, part.T = s.q_start, used
+    if used:
+        check(part, q[:used], out[:used], lse[:used])
 
 
 @pytest.mark.slow
