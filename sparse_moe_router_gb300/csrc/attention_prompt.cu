@@ -3,33 +3,37 @@
 //
 // A block takes 256 query rows (token, q head) of one kv head as two 128-row tiles (one at D = 256,
 // where the output of one fills TMEM) and walks the keys they see in tiles of 128.  In halves of 64
-// keys a row tile computes S = Q K^T into TMEM, the softmax takes S into registers at once, which
-// frees it for the next half's logits, and puts the weights beside it as fp16; O += P V reads them
-// from there.  All rows of a group of q heads share each key and value tile, so a tile of K and V
+// keys a row tile computes S = Q K^T into TMEM, the softmax takes S into registers at once and puts
+// the weights back as fp16, and O += P V reads them from there, while the next half's logits are
+// computed.  All rows of a group of q heads share each key and value tile, so a tile of K and V
 // is widened once for 256 rows.
 //
 // Bound: 4 D flops a (row, key) on the tensor cores; at D = 128 a tile of keys is 4 x 512 tensor
-// cycles for the two row tiles, and their 2 x 16,384 exponentials take 1024 cycles of the SM's 32 a cycle
-// beside the other 5 instructions a logit, so that both have to run at once: logits a half tile ahead,
-// two row tiles apart.  The 8-bit codes cannot be an operand beside fp16 weights (both operands of an MMA
-// have one type, and queries in 8 bits would lose what the 16-bit ones hold), so eight warps read
-// codes from global memory (L2, mostly: all tiles of a head read the same pages), widen them
-// exactly to fp16 and store them in the swizzled layout that the MMA reads: 96 KB of shared-memory
-// traffic a tile against the MMA's own 192 KB.  The exponents of the pages are drawn into the codes
-// relative to the largest one the block will meet (exact in fp16 unless a page is 2^-15 below it, and
-// then off by at most 2^-25 of the largest), so one factor a row holds for all keys.
+// cycles for the two row tiles, and their 2 x 16,384 exponentials take 1024 cycles at the SM's 32 a cycle,
+// so both have to run at once: logits ahead, two row tiles apart.  The 8-bit codes cannot be an operand
+// beside fp16 weights (both operands of an MMA have one type, and queries in 8 bits would lose what
+// the 16-bit ones hold), so eight warps read codes from global memory (L2, mostly: all tiles of a head
+// read the same pages), widen them exactly to fp16 and store them in the swizzled layout that the MMA
+// reads.  At 128 bytes a cycle those 64 KB and the operands (6 KB an MMA of 64 keys' logits, 4 KB of the output)
+// take 2560 cycles a tile of keys: at D = 128 shared memory is the nearer limit, and 3500 are measured.  What is
+// between is the chain of each half tile (wait, TMEM load, weights, TMEM store, MMAs, each a few hundred
+// cycles): leaving out the exponentials gives 2% at D = 128 and 9% at D = 64, the widening 7% and 6%, 7/8 of the
+// logits' MMAs 10% and 0.  The exponents of the pages are drawn into the codes relative to the largest one the
+// block will meet (exact in fp16 unless a page is 2^-15 below it, and then off by at most 2^-25 of the
+// largest), so one factor a row holds for all keys.
 //
-// Measured, 16 q heads, 2 kv heads, causal: 8192 tokens at D = 128 202 us (1360 TFLOP/s, 72% of the
-// measured cuBLAS rate, 79% of the sustained one); five pieces of up to 1031 tokens behind up to 6007, 24 q heads in
-// groups of 3, D = 64, 74 us; at D = 256 with 4 kv heads 597 us (922 TFLOP/s: with one row tile a block no second one hides the
-// softmax, and a converter has 128 rows to widen for instead of 256), where the split kernel takes
-// 4635.  On the way at D = 128: whole tiles of logits in the place their weights take 214 us; halves
-// from one MMA warp 284 (its waits for one row tile hold up the other); two threads a row 232 (a barrier a
-// half tile); four converter warps 277; the maximum looked for in every tile 221; scalar instead of paired
-// fp32 in the softmax 219; the next logits loaded before the weights are stored 233 (registers).
+// Measured, causal: 8192 tokens, 16 q heads and 2 kv heads of 128 dims 202 us (1360 TFLOP/s, 72% of the
+// cuBLAS rate measured here, 80% of the sustained one); of 64 dims 162 us (850); 16 and 4 heads of 256 510 us (1077), where
+// the split kernel takes 4635; five pieces of up to 1031 tokens behind up to 6007, 24 q heads in groups of 3 of
+// 64 dims, 69.5 us (its 152 blocks run at once, and the longest has 1.3 times the mean's keys).  On the way at
+// D = 128: whole tiles of logits in the place their weights take 214 us; halves from one MMA warp 284 (its waits
+// for one row tile hold up the other); two threads a row 232 (a barrier a half tile); four converter warps 277; the
+// maximum looked for in every tile 221; scalar instead of paired fp32 in the softmax 219; the next logits
+// loaded before the weights are stored 233 (registers).
 //
 // Roles: warps 0-3 and 4-7 do the softmax of row tiles 0 and 1, one row a thread; warps 8-15 widen K
-// and V; warps 16 and 17 issue the MMAs of row tiles 0 and 1.  A row's maximum is not looked for in
+// and V; warps 16 and 17 issue the MMAs of row tiles 0 and 1 (with kAhead their logits, and 18 and 19
+// their outputs).  A row's maximum is not looked for in
 // every tile: the weights are taken under the reference so far, and their sum (needed anyway) shows when that
 // has become too small; the row's thread then finds the maximum, rescales its row of O and takes the
 // weights again.
@@ -42,9 +46,9 @@ namespace {
 constexpr int kRowTile = 128;
 constexpr int kKeys = 128;  // keys a tile
 constexpr int kSoftWarps = 8, kConvWarps = 8, kMmaWarp = 16;
-constexpr int kThreads = 20 * 32;  // (the last two only complete the warpgroup)
+constexpr int kThreads = 20 * 32;
 // Registers a thread: 96 at launch (five warps a scheduler); of a scheduler's 5 x 96 the two softmax
-// warps, which hold 64 logits and 32 pairs of weights, take 2 x 144, the converters 2 x 80, the MMA warp 32.
+// warps, which hold 64 logits and 32 pairs of weights, take 2 x 144, the converters 2 x 80, an MMA warp 32.
 constexpr int kLaunchRegs = 96, kSoftRegs = 144, kConvRegs = 80, kMmaRegs = 32;
 static_assert(8 * kSoftRegs + 8 * kConvRegs + 4 * kMmaRegs <= 20 * kLaunchRegs, "more registers than the block has");
 constexpr uint64_t kWaitNs = 2000000000ull;  // 2 s: far above any legitimate wait
@@ -59,8 +63,18 @@ struct Prompt {
     static constexpr int kRows = kTiles * kRowTile;
     static constexpr int kStages = D == 256 ? 2 : 4;          // K and V tiles in flight, in the order K0 V0 K1 V1 ...
     static constexpr int kSmem = 1024 + (kTiles + kStages) * kTileBytes + 256;  // 1 KB to align; barriers
-    static constexpr uint32_t kColO = kTiles * kKeys;         // TMEM: S0 P0 (S1 P1) O0 (O1)
+    static constexpr uint32_t kColO = kTiles * kKeys;         // TMEM: S0 (S1) O0 (O1); S of even and odd halves
     static constexpr uint32_t kCols = 512;
+    // Where a half tile's 64 logits and 64 weights (fp16: 32 columns) lie among a row tile's 128 columns, and
+    // how far the logits run ahead.  D = 64 and 256, where the softmax sets the pace: two places for logits, the
+    // weights in theirs, logits two half tiles ahead from a warp of their own.  D = 128, where the tensor cores and
+    // their operands' reads do (64-column logits read 6 KB a 32 cycles): one place for logits and two for weights,
+    // one warp for both, so that a row tile's next logits always come before its output.  us with the first
+    // form and the second: 8192 tokens at D = 64 (8 q heads a kv head) 162 and 167, at D = 128 207 and 202, at D = 256 510 and 597;
+    // five pieces at D = 64 69.5 and 73.6.  (The second with two warps at D = 128: 214.)
+    static constexpr bool kAhead = D != 128;
+    __device__ static uint32_t s_place(int n) { return kAhead ? (n & 1) * 64 : 0; }
+    __device__ static uint32_t p_place(int n) { return kAhead ? (n & 1) * 64 : 64 + (n & 1) * 32; }
 };
 
 __device__ __forceinline__ float exp2_fast(float x) {
@@ -115,14 +129,14 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
     uint8_t *q_smem = smem, *kv_smem = smem + kTiles * C::kTileBytes;
     uint64_t *bars = reinterpret_cast<uint64_t *>(kv_smem + kStages * C::kTileBytes);
     uint64_t *full = bars, *empty = bars + kStages;  // of a stage
-    uint64_t *s_full = empty + kStages;              // [2] 64 logits of each row of a row tile are in TMEM
-    uint64_t *s_free = s_full + 2;                   // [2] and in registers: the next may take their place
-    uint64_t *p_full = s_free + 2;                   // [2 x 2] their weights are in TMEM, even and odd half tiles
-    uint64_t *o_half = p_full + 4;                   // [2] and have gone into the output
-    uint64_t *o_full = o_half + 2;                   // [2] all have
-    uint64_t *q_full = o_full + 2;
+    uint64_t *s_full = empty + kStages;              // [2 x 2] 64 logits of a row tile, even and odd half tiles, are in TMEM
+    uint64_t *p_full = s_full + 4;                   // [2 x 2] and their weights are, in their place
+    uint64_t *o_half = p_full + 4;                   // [2 x 2] and have gone into the output
+    uint64_t *o_full = o_half + 4;                   // [2] all have
+    uint64_t *s_free = o_full + 2;                   // [2] the logits are in registers
+    uint64_t *q_full = s_free + 2;
     uint64_t *drain = q_full + 1;
-    uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(drain + 2);
+    uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(drain + 4);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_holder + 1);
     int *max_exp = reinterpret_cast<int *>(tmem_holder + 2);              // [2] of K and V
 
@@ -180,16 +194,17 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
             ptx::mbar_init(&empty[s], kTiles);  // every row tile is done with it
         }
         for (int i = 0; i < 2; ++i) {
-            ptx::mbar_init(&s_full[i], 1);
+            ptx::mbar_init(&s_full[2 * i], 1);
+            ptx::mbar_init(&s_full[2 * i + 1], 1);
             ptx::mbar_init(&p_full[2 * i], 4);
             ptx::mbar_init(&p_full[2 * i + 1], 4);
-            ptx::mbar_init(&s_free[i], 4);
-            ptx::mbar_init(&o_half[i], 1);
+            ptx::mbar_init(&o_half[2 * i], 1);
+            ptx::mbar_init(&o_half[2 * i + 1], 1);
             ptx::mbar_init(&o_full[i], 1);
+            ptx::mbar_init(&s_free[i], 4);
         }
         ptx::mbar_init(q_full, 4 * kTiles);
-        ptx::mbar_init(&drain[0], 1);
-        ptx::mbar_init(&drain[1], 1);
+        for (int i = 0; i < 4; ++i) ptx::mbar_init(&drain[i], 1);
         *abort_flag = 0;
         max_exp[0] = max_exp[1] = -127;
         ptx::fence_mbar_init();
@@ -276,21 +291,24 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
         }
         const float mul = p.scale_log2 * pow2f(q_exp) * pow2f(k_exp);
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-        const uint32_t s_addr = tmem + lanes + i * kKeys, o_addr = tmem + lanes + C::kColO + i * D;
+        const uint32_t o_addr = tmem + lanes + C::kColO + i * D;
         float m = 0.f, l = 0.f;  // reference of the weights, and their sum (0: none so far)
         for (int n = 0; n < halves; ++n) {
-            ok = __all_sync(0xffffffffu, ptx::mbar_wait(&s_full[i], n & 1, kWaitNs, abort_flag)) != 0;
+            ok = __all_sync(0xffffffffu, ptx::mbar_wait(&s_full[2 * i + (n & 1)], n >> 1 & 1, kWaitNs, abort_flag)) != 0;
             if (!ok) break;
             ptx::tc_fence_after();
+            const uint32_t s_addr = tmem + lanes + i * kKeys + C::s_place(n);
             uint32_t s[2][32], w[32];
             ptx::tmem_ld_32(s_addr, s[0]);
             ptx::tmem_ld_32(s_addr + 32, s[1]);
             ptx::tmem_ld_wait();
             tie32(s[0]);
             tie32(s[1]);
-            ptx::tc_fence_before();
-            __syncwarp();
-            if (lane == 0) ptx::mbar_arrive(&s_free[i]);
+            if (!C::kAhead) {
+                ptx::tc_fence_before();
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive(&s_free[i]);
+            }
             const int key0 = tile0 * kKeys + n * 64, c_lo = lo - key0, c_hi = hi - key0;
             if (__any_sync(0xffffffffu, live && (c_lo > 0 || c_hi < 64))) {
 #pragma unroll
@@ -337,7 +355,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
                 }
                 l *= f;
                 if (n > 0) {  // O under the old reference, once the product of the half tile before is in it
-                    ok = __all_sync(0xffffffffu, ptx::mbar_wait(&o_half[i], (n - 1) & 1, kWaitNs, abort_flag)) != 0;
+                    ok = __all_sync(0xffffffffu, ptx::mbar_wait(&o_half[2 * i + ((n - 1) & 1)], (n - 1) >> 1 & 1, kWaitNs, abort_flag)) != 0;
                     ptx::tc_fence_after();
                     uint32_t o[16];
                     for (int c = 0; c < D / 16; ++c) {
@@ -354,8 +372,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
                 sum = weights();
             }
             l += sum;
-            // two places for the weights in turn: the product that last read this one came before the logits
-            ptx::tmem_st_32(s_addr + 64 + (n & 1) * 32, w);
+            ptx::tmem_st_32(tmem + lanes + i * kKeys + C::p_place(n), w);
             ptx::tmem_st_wait();
             ptx::tc_fence_before();
             __syncwarp();
@@ -487,11 +504,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
         }
     } else {
         regs_down<kMmaRegs>();
-        if (warp < kMmaWarp + kTiles && tiles > 0) {
+        const int i = warp & 1;
+        if (i < kTiles && (C::kAhead || warp < kMmaWarp + 2) && tiles > 0) {
             // ------------------------------------------------------------------ the MMAs --
             // A warp for each row tile: the next 64 logits as soon as the last are in registers, then the output of
             // the last's weights.
-            const int i = warp - kMmaWarp;
             const uint32_t idesc_s = ptx::idesc_f16_f32(kRowTile, 64, false);
             const uint32_t idesc_o = ptx::idesc_f16_f32(kRowTile, D, true);
             const uint64_t q_desc = ptx::sw128_desc(ptx::smem_u32(q_smem));
@@ -509,9 +526,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
                     for (int k = 0; k < D / 16; ++k) {
                         constexpr int kBlock16 = C::kBlockBytes >> 4;
                         const int off = (k >> 2) * kBlock16 + (k & 3) * 2;
-                        ptx::mma_f16_ss(tmem + i * kKeys, qd + off, kd + off, idesc_s, k > 0);
+                        ptx::mma_f16_ss(tmem + i * kKeys + C::s_place(n), qd + off, kd + off, idesc_s, k > 0);
                     }
-                    ptx::mma_commit(&s_full[i]);
+                    ptx::mma_commit(&s_full[2 * i + (n & 1)]);
                     if ((n & 1) || n + 1 == halves) ptx::mma_commit(&empty[s]);
                 }
                 __syncwarp();
@@ -522,32 +539,50 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
                     const uint64_t vd = v_desc + (uint64_t)(s * (C::kTileBytes >> 4) + (n & 1) * (64 * 128 >> 4));
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
-                        ptx::mma_f16_ts(tmem + C::kColO + i * D, tmem + i * kKeys + 64 + (n & 1) * 32 + k * 8,
+                        ptx::mma_f16_ts(tmem + C::kColO + i * D, tmem + i * kKeys + C::p_place(n) + k * 8,
                                         vd + k * (2048 >> 4), idesc_o, n > 0 || k > 0);
-                    ptx::mma_commit(&o_half[i]);
+                    ptx::mma_commit(&o_half[2 * i + (n & 1)]);
                     if ((n & 1) || n + 1 == halves) ptx::mma_commit(&empty[s]);
                     if (n + 1 == halves) ptx::mma_commit(&o_full[i]);
                 }
                 __syncwarp();
             };
             auto filled = [&](int it) { return wait(&full[it % kStages], it / kStages); };
-            ok = wait(q_full, 0) && filled(0);
-            ptx::tc_fence_after();
-            if (ok) logits(0);
-            for (int n = 0; n < halves && ok; ++n) {
-                if (n + 1 < halves) {
-                    ok = (!(n & 1) || filled(n + 1)) && wait(&s_free[i], n);  // (K of the next tile)
-                    ptx::tc_fence_after();
-                    if (ok) logits(n + 1);
-                }
-                ok = ok && ((n & 1) || filled(n + 1)) && wait(&p_full[2 * i + (n & 1)], n >> 1);  // (V of this one)
+            if (!C::kAhead) {
+                ok = wait(q_full, 0) && filled(0);
                 ptx::tc_fence_after();
-                if (ok) output(n);
+                if (ok) logits(0);
+                for (int n = 0; n < halves && ok; ++n) {
+                    if (n + 1 < halves) {
+                        ok = (!(n & 1) || filled(n + 1)) && wait(&s_free[i], n);  // K of the next tile
+                        ptx::tc_fence_after();
+                        if (ok) logits(n + 1);
+                    }
+                    ok = ok && ((n & 1) || filled(n + 1)) && wait(&p_full[2 * i + (n & 1)], n >> 1);  // V of this one
+                    ptx::tc_fence_after();
+                    if (ok) output(n);
+                }
+            } else if (warp < kMmaWarp + 2) {
+                ok = wait(q_full, 0) && filled(0);
+                ptx::tc_fence_after();
+                for (int n = 0; n < halves && ok; ++n) {
+                    if (n > 1) {  // K; the weights whose place the logits take have been read
+                        ok = ((n & 1) || filled(n)) && wait(&o_half[2 * i + (n & 1)], (n - 2) >> 1);
+                        ptx::tc_fence_after();
+                    }
+                    if (ok) logits(n);
+                }
+            } else {
+                for (int n = 0; n < halves && ok; ++n) {
+                    ok = ((n & 1) || filled(n + 1)) && wait(&p_full[2 * i + (n & 1)], n >> 1);  // V, weights
+                    ptx::tc_fence_after();
+                    if (ok) output(n);
+                }
             }
             if (!ok) {  // nothing of this block may still run when its TMEM is freed
-                if (ptx::elect_one()) ptx::mma_commit(&drain[i]);
+                if (ptx::elect_one()) ptx::mma_commit(&drain[warp - kMmaWarp]);
                 int zero = 0;
-                ptx::mbar_wait(&drain[i], 0, kWaitNs, &zero);
+                ptx::mbar_wait(&drain[warp - kMmaWarp], 0, kWaitNs, &zero);
             }
         }
     }
