@@ -6,6 +6,11 @@
 // The two means are the only places where a row's values meet, so a block keeps its row in
 // registers between them: x, resid and the gate are read once, r' and y written once, and nothing
 // else touches memory.  Both sums of squares are fp32.
+//
+// Bound: HBM from a few hundred rows on, below that the launch and two dependent sums.  Measured: one
+// row of 2048 2.7 us; 1031 rows of 4096 with a channel gate 10.1 us (3.3 TB/s: 7 rows a block, so the first
+// row's way through the chip is a quarter of it); 8192 rows of 2048 with a gate on each element 33 us (5.1 TB/s, 76%
+// of the measured copy; before a block kept its weights and had its next row under way, 45).
 #include "layer.h"
 
 namespace moe {
