@@ -8,9 +8,9 @@
 // else touches memory.  Both sums of squares are fp32.
 //
 // Bound: HBM from a few hundred rows on, below that the launch and two dependent sums.  Measured: one
-// row of 2048 2.7 us; 1031 rows of 4096 with a channel gate 10.1 us (3.3 TB/s: 7 rows a block, so the first
-// row's way through the chip is a quarter of it); 8192 rows of 2048 with a gate on each element 33 us (5.1 TB/s, 76%
-// of the measured copy; before a block kept its weights and had its next row under way, 45).
+// row of 2048 2.7 us; 1031 rows of 4096 with a channel gate 10.1 us (3.3 TB/s: 7 rows an SM, so the first
+// row's way through the chip is a quarter of it); 8192 rows of 2048 with a gate on each element 32.6 us (5.1 TB/s,
+// 77% of the measured copy; before a block kept its weights and had its next row under way, 45).
 #include "layer.h"
 
 namespace moe {
@@ -149,22 +149,21 @@ __global__ void __launch_bounds__(C == 1 ? 1024 : 512) block_norm_kernel(const _
 template <int C, bool F16>
 void launch_rows(const NormArgs &a, cudaStream_t s) {
     const int threads = ((a.H / 8 + C - 1) / C + 31) / 32 * 32;
-    // blocks that are resident together (by registers, 768 or 512 threads an SM), each with as many rows as the
-    // others
-    const int resident = max(device_info().sm_count * (C == 1 ? 768 : 512) / threads, 1);
-    const int turns = (a.T + resident - 1) / resident;
-    block_norm_kernel<C, F16><<<(a.T + turns - 1) / turns, threads, 0, s>>>(a);
+    // as many blocks as are resident together (by registers, 1024 or 512 threads an SM)
+    const int resident = device_info().sm_count * max((C == 1 ? 1024 : 512) / threads, 1);
+    block_norm_kernel<C, F16><<<min(a.T, resident), threads, 0, s>>>(a);
 }
 
 template <bool F16>
 cudaError_t launch(const NormArgs &a, cudaStream_t s) {
     LaunchScope scope(KC_BLOCK_NORM, s);
-    // One chunk a thread has a row soonest (a few tokens: 2.8 us at H = 2048); two stream more bytes a block
-    // once every SM has several rows (8192 x 2048, gated: 33.0 us against 36.9; four: 51.9).
-    const int chunks = a.H / 8;
-    const bool many = a.T >= 4 * device_info().sm_count;
+    // One chunk a thread has a row soonest and the most warps an SM; two, in blocks that fit an SM twice, are
+    // ahead where an SM has a few rows, so that their start and end count.  us with one and two: 500 rows of
+    // 4096 6.1 and 6.1, 1000 of 2048 6.1 and 5.6, 1031 of 4096 10.5 and 10.1, 2048 of 2048 9.6 and 9.5, 4096 of 4096
+    // 29.7 and 30.1, 8192 of 2048, gated, 32.6 and 33.1 (four: 51.9).
+    const int chunks = a.H / 8, sms = device_info().sm_count;
     if (chunks > 1024) launch_rows<4, F16>(a, s);
-    else if (many && chunks >= 128) launch_rows<2, F16>(a, s);
+    else if (chunks >= 128 && chunks <= 512 && a.T >= 4 * sms && a.T < 16 * sms) launch_rows<2, F16>(a, s);
     else launch_rows<1, F16>(a, s);
     return cudaGetLastError();
 }
