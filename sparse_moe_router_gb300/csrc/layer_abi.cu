@@ -64,6 +64,12 @@ moe_status check_batch(const moe_attn_config &c, const moe_kv_cache *k, const mo
 constexpr int kPromptRows = 128;
 // Mean rows a sequence and kv head below which a batch is a decode step, all of it the split kernel's.
 constexpr int kPromptMean = 33;
+// Rows in all (tokens x q heads) from which the prompt kernel is worth it: a block of it takes 256 rows (D = 256: 128)
+// through all their keys, and the split kernel shares short work out over every SM.  us of the prompt kernel and
+// the split one, 8 q heads, 1 kv head, 16,384 keys: D = 128, 1024 rows 200 and 52, 2048 200 and 89, 4096 200 and 163,
+// 8192 200 and 308; D = 64, 4096 164 and 102, 8192 164 and 191; D = 256, 2048 254 and 155, 4096 255 and 294.  A prompt
+// without a past, D = 128: 1024 rows 12.9 and 8.9, 2048 14.3 and 13.7, 4096 17.8 and 22.4.
+constexpr int64_t kPromptWork = 4096;
 // From this many steps a block times row tiles a sequence (4 at most), the split kernel's row tiles share key
 // tiles.  Below, the SMs are short of work and more, smaller segments end sooner.  us shared and not, at 304 blocks,
 // D = 128, groups of 8, 2 kv heads: 4 tiles, 8 sequences of 4000 keys (26) 20.5 and 20.0, of 10,000 (66) 27.9
@@ -242,7 +248,7 @@ moe_status moe_attention(const moe_attn_config *cfg, const moe_kv_cache *cache, 
     // leaves a kernel out that has none for sure, and the prompt kernel in a step of few tokens a
     // sequence: its launch would cost more (5 us) than the rare long run among them.
     const int64_t rows = (int64_t)batch->n_tokens * a.kv.G, mean = rows / batch->n_seqs;
-    const bool prompts = rows >= kPromptRows && mean >= kPromptMean;
+    const bool prompts = rows >= kPromptRows && mean >= kPromptMean && rows * c.kv_heads >= kPromptWork;
     a.prompt_rows = !prompts ? INT_MAX : batch->n_seqs == 1 ? 1 : kPromptRows;
     if (prompts) MOE_CUDA(launch_attn_prompt(a, c.head_dim, c.dtype, s));
     if (batch->n_seqs > 1 || !prompts) {

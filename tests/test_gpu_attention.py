@@ -88,8 +88,23 @@ def test_prompts(dtype, QH, KH, D, P, lens):
     check(s, q, out, lse)
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("QH,KH,D,P", [(16, 2, 128, 64), (12, 4, 64, 16), (3, 1, 128, 128), (8, 1, 256, 32), (2, 2, 64, 32),
+                                       (2, 1, 256, 16), (40, 1, 64, 64)])
+@pytest.mark.parametrize("kind", ["one", "mixed", "odd", "short"])
+def test_prompts_of_many_rows(dtype, QH, KH, D, P, kind):
+    """4096 rows (tokens x q heads) and more in all, the tensor cores' share of the work."""
+    n = 4300 // QH + 3
+    lens = {"one": [(n, n)], "mixed": [(n, n + 643), (1, 33), (129, 129), (64, 1000)], "odd": [(n // 2 + 1, n), (n // 2 + 3, 2 * n + 5)],
+            "short": [(n, 9), (n // 3, n // 2)]}[kind]
+    s = Setup(lens, QH, KH, D, P, dtype=dtype, seed=QH)
+    q = make_q(s)
+    out, lse = run(s, q)
+    check(s, q, out, lse)
+
+
 @pytest.mark.parametrize("causal,window", [(True, 100), (False, 0), (False, 200), (True, 1)])
-@pytest.mark.parametrize("QH,KH,D,P", [(16, 2, 128, 64), (12, 4, 64, 16), (4, 2, 256, 32)])
+@pytest.mark.parametrize("QH,KH,D,P", [(16, 2, 128, 64), (12, 4, 64, 16), (8, 2, 256, 32)])
 def test_prompt_masks(causal, window, QH, KH, D, P):
     s = Setup([(300, 700), (290, 200), (64, 64)], QH, KH, D, P, seed=6)
     q = make_q(s)
@@ -114,7 +129,7 @@ def test_row_tiles_that_share_keys(dtype, QH, KH, D, P):
     check(s, q, out, lse, window=70)
 
 
-@pytest.mark.parametrize("lens", [[(1, 900), (2, 77)], [(300, 700)]], ids=["tokens", "prompt"])
+@pytest.mark.parametrize("lens", [[(1, 900), (2, 77)], [(300, 700)], [(600, 700)]], ids=["tokens", "run", "prompt"])
 def test_sharp_and_shifted_logits(lens):
     """Logits in the hundreds: the running reference moves often, most weights vanish; pages whose scales
     lie far apart; a softmax scale of the caller's."""
@@ -124,9 +139,10 @@ def test_sharp_and_shifted_logits(lens):
     check(s, q, out, lse, scale=0.05)
 
 
-def test_keys_that_grow_along_the_sequence():
+@pytest.mark.parametrize("n", [130, 530])
+def test_keys_that_grow_along_the_sequence(n):
     """Each page larger than the one before, values too: every step moves the reference and the unit."""
-    s = Setup([(1, 640), (130, 640)], 8, 1, 64, 16, seed=4)
+    s = Setup([(1, 640), (n, 640)], 8, 1, 64, 16, seed=4)
     for b in range(2):
         for j in range(40):
             page = int(s.table[b, j])
@@ -147,9 +163,9 @@ def test_the_result_does_not_change_from_run_to_run(n, kv):
         assert torch.equal(a, b) and torch.equal(la, lb)
 
 
-@pytest.mark.parametrize("n", [1, 300])
+@pytest.mark.parametrize("n", [1, 300, 560])
 def test_strided_rows_other_stream_and_graph(n):
-    s = Setup([(n, 500), (1, 333)], 8, 2, 64, 32, seed=8)
+    s = Setup([(n, max(500, n + 40)), (1, 333)], 8, 2, 64, 32, seed=8)
     q0 = make_q(s)
     wide = torch.zeros(s.T, 8 * 64 + 72, dtype=torch.bfloat16, device="cuda")
     wide[:, 8:8 + 512] = q0.flatten(1)
@@ -214,10 +230,11 @@ def test_many_sequences(n):
 
 
 @pytest.mark.parametrize("used", [0, 5, 30, 31, 299])
-@pytest.mark.parametrize("seqs", [1, 2])
-def test_rows_past_the_last_sequence(used, seqs):
+@pytest.mark.parametrize("n,seqs", [(300, 1), (300, 2), (600, 1), (600, 2)])
+def test_rows_past_the_last_sequence(used, n, seqs):
     """A batch held for more tokens than its sequences have: the rows behind them stay as they are."""
-    s = Setup([(300, 700)] + [(0, 9)] * (seqs - 1), 8, 2, 128, 64, seed=4)
+    lens = [(n, 700)] + [(0, 9)] * (seqs - 1)
+    s = Setup(lens, 8, 2, 128, 64, seed=4)
     q = make_q(s)
     s.q_start[1:] = used
     cache, batch, ws = s.device()
@@ -226,7 +243,7 @@ def test_rows_past_the_last_sequence(used, seqs):
     abi.moe_attention(s.cfg, cache, batch, q, out, ws, lse=lse)
     assert abi.moe_check_status(ws) == 0
     assert bool((out[used:] == 9).all()) and bool((lse[used:] == 9).all())
-    part = Setup([(300, 700)] + [(0, 9)] * (seqs - 1), 8, 2, 128, 64, seed=4)
+    part = Setup(lens, 8, 2, 128, 64, seed=4)
     part.q_start, part.T = s.q_start, used
     if used:
         check(part, q[:used], out[:used], lse[:used])
