@@ -22,6 +22,10 @@
 // block will meet (exact in fp16 unless a page is 2^-15 below it, and then off by at most 2^-25 of the
 // largest), so one factor a row holds for all keys.
 //
+// Parts: where the blocks leave SMs idle, several share one's keys, and the rows' parts are joined by a second
+// kernel (a warp a row, all parts' loads at once).  8 q heads and 1 kv head of 128 dims, 16,384 keys: 128 tokens 30 us, 512
+// 42, 1024 71, where one block for all keys takes 200.
+//
 // Measured, causal: 8192 tokens, 16 q heads and 2 kv heads of 128 dims 202 us (1360 TFLOP/s, 72% of the
 // cuBLAS rate measured here, 80% of the sustained one); of 64 dims 162 us (850); 16 and 4 heads of 256 510 us (1077), where
 // the split kernel takes 4635; five pieces of up to 1031 tokens behind up to 6007, 24 q heads in groups of 3 of
@@ -52,6 +56,7 @@ constexpr int kThreads = 20 * 32;
 constexpr int kLaunchRegs = 96, kSoftRegs = 144, kConvRegs = 80, kMmaRegs = 32;
 static_assert(8 * kSoftRegs + 8 * kConvRegs + 4 * kMmaRegs <= 20 * kLaunchRegs, "more registers than the block has");
 constexpr uint64_t kWaitNs = 2000000000ull;  // 2 s: far above any legitimate wait
+constexpr int kPartTiles = 8;  // key tiles of a part (of 8: 11 us at D = 128), about and at least
 constexpr float kMostSum = 32768.f;  // 64 weights of one row may add up to this
 
 template <int D>
@@ -119,7 +124,7 @@ __device__ __forceinline__ int slot_base(const KvView &v, int b) {
     return (int)((int64_t)v.q_start[b] * v.G / R) + b;
 }
 
-template <int D, bool F16>
+template <int D, bool F16, bool PARTS>
 __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_constant__ AttnArgs p, int slots) {
     using C = Prompt<D>;
     constexpr int kStages = C::kStages, kTiles = C::kTiles, kRows = C::kRows;
@@ -181,10 +186,17 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
     const int first_pos = q.kv - q.n;
     // keys that any of the rows sees
     const int pos_lo = first_pos + row0 / v.G, pos_hi = first_pos + (row0 + rows - 1) / v.G;
-    const int key_hi = p.causal ? min(q.kv, pos_hi + 1) : q.kv;
-    const int key_lo = p.window > 0 ? max(0, pos_lo + 1 - p.window) : 0;
-    const int tile0 = key_lo / kKeys;
-    const int tiles = key_hi > key_lo ? (key_hi + kKeys - 1) / kKeys - tile0 : 0;
+    int key_hi = p.causal ? min(q.kv, pos_hi + 1) : q.kv;
+    int key_lo = p.window > 0 ? max(0, pos_lo + 1 - p.window) : 0;
+    int tile0 = key_lo / kKeys;
+    int tiles = key_hi > key_lo ? (key_hi + kKeys - 1) / kKeys - tile0 : 0;
+    if (PARTS) {  // this block's part of them
+        const int parts = min(p.parts, max((tiles + kPartTiles / 2) / kPartTiles, 1)), share = (tiles + parts - 1) / parts;
+        tile0 += (int)blockIdx.y * share;
+        tiles = max(min(share, tiles - (int)blockIdx.y * share), 0);
+        key_lo = max(key_lo, tile0 * kKeys);
+        key_hi = max(min(key_hi, (tile0 + tiles) * kKeys), key_lo);
+    }
     const int halves = tiles > 0 ? (key_hi - tile0 * kKeys + 63) / 64 : 0;  // half tiles of 64 keys
     const int32_t *table = v.table + (int64_t)b * v.max_pages;
 
@@ -247,8 +259,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
         const bool live = r < rows;
         const int tok = (row0 + r) / v.G, qh = head * v.G + (row0 + r) % v.G;
         const int pos = first_pos + tok;
-        const int hi = p.causal ? min(q.kv, pos + 1) : q.kv;
-        const int lo = p.window > 0 ? max(0, pos + 1 - p.window) : 0;
+        const int hi = min(p.causal ? min(q.kv, pos + 1) : q.kv, key_hi);
+        const int lo = max(p.window > 0 ? max(0, pos + 1 - p.window) : 0, key_lo);
         const bool sees = live && hi > lo;
         // Q: the row scaled by a power of two into [1, 2) at its largest, as fp16, K-major swizzled
         int q_exp;
@@ -386,6 +398,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
             ptx::tc_fence_after();
             const float inv = (l > 0.f || l != l) && tiles > 0 ? pow2f(v_exp) / l : 0.f;
             uint16_t *out = p.out + (int64_t)(q.q0 + tok) * p.out_ld + (int64_t)qh * D;
+            const int64_t row = ((int64_t)blockIdx.y * v.n_tokens + q.q0 + tok) * v.QH + qh;  // among the parts'
 #pragma unroll
             for (int c = 0; c < D / 32; ++c) {
                 uint32_t o[32];
@@ -400,10 +413,17 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
                     float f[8];
 #pragma unroll
                     for (int x = 0; x < 8; ++x) f[x] = inv == 0.f ? 0.f : __uint_as_float(o[8 * k + x]) * inv;
-                    *reinterpret_cast<uint4 *>(out + c * 32 + k * 8) = pack8<F16>(f);
+                    if (PARTS) {
+                        float4 *part = reinterpret_cast<float4 *>(p.part_out + row * D + c * 32 + k * 8);
+                        part[0] = make_float4(f[0], f[1], f[2], f[3]);
+                        part[1] = make_float4(f[4], f[5], f[6], f[7]);
+                    } else {
+                        *reinterpret_cast<uint4 *>(out + c * 32 + k * 8) = pack8<F16>(f);
+                    }
                 }
             }
-            if (live && p.lse) p.lse[(int64_t)(q.q0 + tok) * v.QH + qh] = (m + log2f(l)) * 0.6931471805599453f;
+            if (live && PARTS) p.part_lse[row] = m + log2f(l);
+            else if (live && p.lse) p.lse[(int64_t)(q.q0 + tok) * v.QH + qh] = (m + log2f(l)) * 0.6931471805599453f;
         }
         }
     } else if (warp < kMmaWarp) {
@@ -597,15 +617,68 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
     if (warp == kMmaWarp) ptx::tmem_dealloc(tmem, C::kCols);
 }
 
+// Joins the parts of each row, a warp a row (up to 32 sequences).  A part in which a row sees nothing holds zeros.
 template <int D, bool F16>
-cudaError_t launch(const AttnArgs &a, cudaStream_t s) {
+__global__ void __launch_bounds__(256) attn_prompt_join_kernel(const __grid_constant__ AttnArgs p) {
+    const KvView &v = p.kv;
+    const int lane = (int)threadIdx.x & 31;
+    const int64_t rows = (int64_t)v.n_tokens * v.QH, row = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+    if (row >= rows) return;
+    const int tok = (int)(row / v.QH), qh = (int)(row % v.QH);
+    const float lse = lane < p.parts ? p.part_lse[lane * rows + row] : -INFINITY;
+    const int b = __popc(__ballot_sync(0xffffffffu, lane < v.n_seqs && v.q_start[min(lane + 1, v.n_seqs)] <= tok));
+    if (b >= v.n_seqs) return;
+    const Seq q = load_seq(v, b);
+    if (tok < q.q0 || tok >= q.q0 + q.n || q.n * v.G < p.prompt_rows) return;  // no row, or the split kernel's
+    float top = lse;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    const float w = top == -INFINITY && lse == lse ? 0.f : exp2_fast(lse - top);
+    float sum = w;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    const float inv = sum == 0.f ? 0.f : 1.0f / sum;
+    uint16_t *out = p.out + (int64_t)tok * p.out_ld + (int64_t)qh * D;
+    for (int d0 = 0; d0 < D; d0 += 128) {
+        const int d = d0 + lane * 4;
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        float4 o[kPromptParts];
+#pragma unroll
+        for (int i = 0; i < kPromptParts; ++i)
+            o[i] = i < p.parts && d < D ? *reinterpret_cast<const float4 *>(p.part_out + (i * rows + row) * D + d) : acc;
+#pragma unroll
+        for (int i = 0; i < kPromptParts; ++i) {
+            const float wi = __shfl_sync(0xffffffffu, w, i);
+            acc.x = fmaf(wi, o[i].x, acc.x), acc.y = fmaf(wi, o[i].y, acc.y);
+            acc.z = fmaf(wi, o[i].z, acc.z), acc.w = fmaf(wi, o[i].w, acc.w);
+        }
+        if (d < D)
+            *reinterpret_cast<uint2 *>(out + d) = make_uint2(pack2<F16>(acc.x * inv, acc.y * inv), pack2<F16>(acc.z * inv, acc.w * inv));
+    }
+    if (lane == 0 && p.lse) p.lse[row] = (top + log2f(sum)) * 0.6931471805599453f;
+}
+
+template <int D, bool F16, bool PARTS>
+cudaError_t launch_kernel(const AttnArgs &a, cudaStream_t s) {
     constexpr int smem = Prompt<D>::kSmem;
     static_assert(smem <= 227 * 1024, "shared memory over the per-block limit");
-    cudaError_t e = cudaFuncSetAttribute(attn_prompt_kernel<D, F16>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    cudaError_t e = cudaFuncSetAttribute(attn_prompt_kernel<D, F16, PARTS>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
-    LaunchScope scope(KC_ATTN_PROMPT, s);
+    static_assert(Prompt<D>::kRows == (D == 256 ? 128 : 256), "prompt_block_rows");
     const int slots = (int)((int64_t)a.kv.n_tokens * a.kv.G / Prompt<D>::kRows) + a.kv.n_seqs;
-    attn_prompt_kernel<D, F16><<<slots * a.kv.KH, kThreads, smem, s>>>(a, slots);
+    LaunchScope scope(KC_ATTN_PROMPT, s);
+    attn_prompt_kernel<D, F16, PARTS><<<dim3(slots * a.kv.KH, a.parts), kThreads, smem, s>>>(a, slots);
+    return cudaGetLastError();
+}
+
+template <int D, bool F16>
+cudaError_t launch(const AttnArgs &a, cudaStream_t s) {
+    if (a.parts == 1) return launch_kernel<D, F16, false>(a, s);
+    const cudaError_t e = launch_kernel<D, F16, true>(a, s);
+    if (e != cudaSuccess) return e;
+    LaunchScope scope(KC_ATTN_JOIN, s);
+    const int64_t rows = (int64_t)a.kv.n_tokens * a.kv.QH;
+    attn_prompt_join_kernel<D, F16><<<(unsigned)((rows + 7) / 8), 256, 0, s>>>(a);
     return cudaGetLastError();
 }
 

@@ -55,6 +55,10 @@ struct AttnArgs {
     // sequences with at least this many query rows a kv head (new tokens x G) are the prompt
     // kernel's, the others the split kernel's
     int prompt_rows;
+    // prompt kernel: the keys of a block in so many parts, and with more than one each part's rows, [parts, T, QH, D]
+    // normalised and [parts, T, QH] the log2 of their sums
+    int parts;
+    float *part_out, *part_lse;
 };
 // The workspace is sized for so many SMs; the split kernel has one or two blocks on each.
 constexpr int kSplitMaxSms = 160, kSplitMaxBlocks = 2 * kSplitMaxSms;
@@ -62,6 +66,8 @@ constexpr int kSplitMaxSms = 160, kSplitMaxBlocks = 2 * kSplitMaxSms;
 size_t split_part_floats(int D);
 cudaError_t launch_attn_split(const AttnArgs &a, int D, int dtype, bool shared, bool after_prompt, cudaStream_t s);
 cudaError_t launch_attn_prompt(const AttnArgs &a, int D, int dtype, cudaStream_t s);
+inline int prompt_block_rows(int D) { return D == 256 ? 128 : 256; }  // query rows a block of the prompt kernel
+constexpr int kPromptParts = 16;  // at most
 
 struct NormArgs {
     const uint16_t *x, *resid, *gate, *w_post, *w_pre;

@@ -65,11 +65,14 @@ constexpr int kPromptRows = 128;
 // Mean rows a sequence and kv head below which a batch is a decode step, all of it the split kernel's.
 constexpr int kPromptMean = 33;
 // Rows in all (tokens x q heads) from which the prompt kernel is worth it: a block of it takes 256 rows (D = 256: 128)
-// through all their keys, and the split kernel shares short work out over every SM.  us of the prompt kernel and
-// the split one, 8 q heads, 1 kv head, 16,384 keys: D = 128, 1024 rows 200 and 52, 2048 200 and 89, 4096 200 and 163,
-// 8192 200 and 308; D = 64, 4096 164 and 102, 8192 164 and 191; D = 256, 2048 254 and 155, 4096 255 and 294.  A prompt
-// without a past, D = 128: 1024 rows 12.9 and 8.9, 2048 14.3 and 13.7, 4096 17.8 and 22.4.
-constexpr int64_t kPromptWork = 4096;
+// at the price of a long start and a join of parts, the split kernel 8.  us of the prompt kernel and the split one,
+// 8 q heads, 1 kv head: 2048 rows, D = 64, 1024 keys 17.7 and 17.7, 4096 26.8 and 25.4, 16,384 26.8 and 57.6; D = 128, 22.9
+// and 23.4, 33.0 and 36.3, 31.8 and 89.0; D = 256, 28.1 and 29.2, 41 and 54, 52 and 155; 1024 rows, D = 128, 23.0 and 17.8,
+// 28.5 and 27.9, 29.7 and 52.4.  A prompt without a past, D = 128: 1024 rows 12.9 and 8.9, 2048 14.3 and 13.7, 4096 17.8
+// and 22.4.  So half as many from 8192 keys on.  Several sequences, some of which may be short and the split
+// kernel's after the other two, need twice as many: 6 of up to 247 tokens, 8 and 4 heads of 128, 4000 rows, 2356
+// keys, 45.7 and 32.4.
+constexpr int64_t kPromptWork = 2048, kPromptKeys = 8192;
 // From this many steps a block times row tiles a sequence (4 at most), the split kernel's row tiles share key
 // tiles.  Below, the SMs are short of work and more, smaller segments end sooner.  us shared and not, at 304 blocks,
 // D = 128, groups of 8, 2 kv heads: 4 tiles, 8 sequences of 4000 keys (26) 20.5 and 20.0, of 10,000 (66) 27.9
@@ -78,20 +81,43 @@ constexpr int64_t kPromptWork = 4096;
 // 4000 (54) 27.4 and 27.3, of 16,000 (211) 59.6 and 89.4.
 constexpr int kManySteps = 56;
 
+// Rows of partial results that the prompt kernel's parts may have: a block an SM twice over.
+int64_t part_rows(const moe_attn_config &c, int64_t n_tokens) {
+    const int64_t rows = n_tokens * c.q_heads, most = (int64_t)kSplitMaxBlocks * prompt_block_rows(c.head_dim);
+    return rows * kPromptParts < most ? rows * kPromptParts : most;
+}
 struct Layout {
-    size_t desc, part, total;
+    size_t desc, part, prompt_out, prompt_lse, total;
 };
-Layout layout(const moe_attn_config &c) {
+Layout layout(const moe_attn_config &c, int n_tokens) {
     Layout l;
     l.desc = 256;  // behind the status word
     l.part = l.desc + (kSplitMaxBlocks * sizeof(SplitDesc) + 255) / 256 * 256;
-    l.total = l.part + split_part_floats(c.head_dim) * sizeof(float);
+    l.prompt_out = l.part + (split_part_floats(c.head_dim) * sizeof(float) + 255) / 256 * 256;
+    l.prompt_lse = l.prompt_out + part_rows(c, n_tokens) * c.head_dim * sizeof(float);
+    l.total = l.prompt_lse + part_rows(c, n_tokens) * sizeof(float);
     return l;
 }
 
-moe_status check_ws(const moe_attn_config &c, const void *ws, size_t bytes) {
+// Parts of a prompt's keys: where its blocks leave SMs idle, each block's keys are shared out over several: as
+// many as end soonest, in tiles of 128 keys (1.4 us at D = 128), a block's start counted as 5 and the join as 4.
+int prompt_parts(const moe_attn_config &c, const moe_kv_batch &b, int64_t rows, int64_t keys) {
+    const int sms = device_info().sm_count, block = prompt_block_rows(c.head_dim);
+    const int64_t blocks = (rows + block - 1) / block * c.kv_heads, all = (int64_t)b.n_tokens * c.q_heads;
+    if (blocks >= sms || b.n_seqs > 32) return 1;
+    int best = 1;
+    const double tiles = (double)keys / 128;
+    double least = tiles + 5;
+    for (int k = 2; k <= kPromptParts && k * all <= part_rows(c, b.n_tokens) && k * 1024 <= keys; ++k) {
+        const double cost = (double)((blocks * k + sms - 1) / sms) * (tiles / k + 5) + 4 + 0.2 * k;
+        if (cost < least) least = cost, best = k;
+    }
+    return best;
+}
+
+moe_status check_ws(const moe_attn_config &c, int n_tokens, const void *ws, size_t bytes) {
     if (!ws || (reinterpret_cast<uintptr_t>(ws) & 255u)) return MOE_ERR_INVALID_ARG;
-    if (bytes < layout(c).total) return MOE_ERR_WORKSPACE_TOO_SMALL;
+    if (bytes < layout(c, n_tokens).total) return MOE_ERR_WORKSPACE_TOO_SMALL;
     return MOE_OK;
 }
 
@@ -174,7 +200,7 @@ moe_status moe_block_norm(const moe_norm_config *cfg, const moe_norm_io *io, int
 size_t moe_attn_workspace_size(const moe_attn_config *cfg, int max_seqs, int max_tokens) {
     if (check_attn_config(cfg) != MOE_OK || max_seqs < 0 || max_tokens < 0) return 0;
     if (max_seqs > kMaxSeqs || max_tokens > kMaxTokens) return 0;
-    return layout(*cfg).total;
+    return layout(*cfg, max_tokens).total;
 }
 
 moe_status moe_kv_append(const moe_attn_config *cfg, const moe_kv_cache *cache, const moe_kv_batch *batch,
@@ -191,7 +217,7 @@ moe_status moe_kv_append(const moe_attn_config *cfg, const moe_kv_cache *cache, 
     if ((q == nullptr) != (q_out == nullptr)) return MOE_ERR_INVALID_ARG;
     if (q && (!good_rows(q, q_ld, c.q_heads * D) || !good_rows(q_out, q_out_ld, c.q_heads * D))) return MOE_ERR_INVALID_ARG;
     if (c.rotary_dim > 0 && (!rope || !aligned16(rope) || rope_rows < 1)) return MOE_ERR_INVALID_ARG;
-    MOE_TRY(check_ws(c, ws, ws_bytes));
+    MOE_TRY(check_ws(c, batch->n_tokens, ws, ws_bytes));
     AppendArgs a{};
     a.kv = view(c, *cache, *batch, ws);
     a.q = static_cast<const uint16_t *>(q);
@@ -229,8 +255,8 @@ moe_status moe_attention(const moe_attn_config *cfg, const moe_kv_cache *cache, 
     const int64_t width = (int64_t)c.q_heads * c.head_dim;
     if (!good_rows(q, q_ld, width) || !good_rows(out, out_ld, width)) return MOE_ERR_INVALID_ARG;
     if (reinterpret_cast<uintptr_t>(lse) & 3u) return MOE_ERR_INVALID_ARG;
-    MOE_TRY(check_ws(c, ws, ws_bytes));
-    const Layout l = layout(c);
+    MOE_TRY(check_ws(c, batch->n_tokens, ws, ws_bytes));
+    const Layout l = layout(c, batch->n_tokens);
     AttnArgs a{};
     a.kv = view(c, *cache, *batch, ws);
     a.q = static_cast<const uint16_t *>(q);
@@ -243,21 +269,26 @@ moe_status moe_attention(const moe_attn_config *cfg, const moe_kv_cache *cache, 
     a.window = window;
     a.desc = reinterpret_cast<SplitDesc *>(static_cast<char *>(ws) + l.desc);
     a.part = reinterpret_cast<float *>(static_cast<char *>(ws) + l.part);
+    a.part_out = reinterpret_cast<float *>(static_cast<char *>(ws) + l.prompt_out);
+    a.part_lse = reinterpret_cast<float *>(static_cast<char *>(ws) + l.prompt_lse);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     // Which sequences the prompt kernel takes goes by their own rows, which only the device knows.  The host
     // leaves a kernel out that has none for sure, and the prompt kernel in a step of few tokens a
     // sequence: its launch would cost more (5 us) than the rare long run among them.
     const int64_t rows = (int64_t)batch->n_tokens * a.kv.G, mean = rows / batch->n_seqs;
-    const bool prompts = rows >= kPromptRows && mean >= kPromptMean && rows * c.kv_heads >= kPromptWork;
+    // keys a sequence has to look at, at most
+    const int64_t seen = window > 0 ? (int64_t)window + batch->n_tokens : INT64_MAX;
+    const int64_t table = (int64_t)batch->max_pages * c.page_size, keys = seen < table ? seen : table;
+    const int64_t work = kPromptWork * (batch->n_seqs == 1 ? 2 : 4) / (keys >= kPromptKeys ? 4 : 2);
+    const bool prompts = rows >= kPromptRows && mean >= kPromptMean && rows * c.kv_heads >= work;
     a.prompt_rows = !prompts ? INT_MAX : batch->n_seqs == 1 ? 1 : kPromptRows;
+    a.parts = prompts ? prompt_parts(c, *batch, rows, keys) : 1;
     if (prompts) MOE_CUDA(launch_attn_prompt(a, c.head_dim, c.dtype, s));
     if (batch->n_seqs > 1 || !prompts) {
         // steps of the split kernel with one row tile a segment, at most
-        const int64_t seen = window > 0 ? (int64_t)window + batch->n_tokens : INT64_MAX;
-        const int64_t table = (int64_t)batch->max_pages * c.page_size, keys = seen < table ? seen : table;
         const int64_t steps = (rows + 7) / 8 * c.kv_heads * ((keys + 127) / 128), tiles = mean > 24 ? 4 : (mean + 7) / 8;
         const bool shared = tiles > 1 && steps * tiles >= (int64_t)kManySteps * 2 * device_info().sm_count;
-        MOE_CUDA(launch_attn_split(a, c.head_dim, c.dtype, shared, prompts, s));
+        MOE_CUDA(launch_attn_split(a, c.head_dim, c.dtype, shared, prompts && a.parts == 1, s));
     }
     return MOE_OK;
 }

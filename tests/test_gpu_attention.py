@@ -93,7 +93,7 @@ def test_prompts(dtype, QH, KH, D, P, lens):
                                        (2, 1, 256, 16), (40, 1, 64, 64)])
 @pytest.mark.parametrize("kind", ["one", "mixed", "odd", "short"])
 def test_prompts_of_many_rows(dtype, QH, KH, D, P, kind):
-    """4096 rows (tokens x q heads) and more in all, the tensor cores' share of the work."""
+    """4300 rows (tokens x q heads) and more in all, the tensor cores' share of the work."""
     n = 4300 // QH + 3
     lens = {"one": [(n, n)], "mixed": [(n, n + 643), (1, 33), (129, 129), (64, 1000)], "odd": [(n // 2 + 1, n), (n // 2 + 3, 2 * n + 5)],
             "short": [(n, 9), (n // 3, n // 2)]}[kind]
@@ -101,6 +101,18 @@ def test_prompts_of_many_rows(dtype, QH, KH, D, P, kind):
     q = make_q(s)
     out, lse = run(s, q)
     check(s, q, out, lse)
+
+
+@pytest.mark.parametrize("causal,window", [(True, 0), (False, 0), (True, 3000), (False, 5)])
+@pytest.mark.parametrize("QH,KH,D,P", [(8, 1, 128, 64), (12, 2, 64, 16), (8, 1, 256, 32)])
+@pytest.mark.parametrize("lens", [[(560, 9000)], [(140, 9001)], [(333, 7001), (1, 40), (300, 2100), (0, 77), (64, 64)]],
+                         ids=["one", "few", "mixed"])
+def test_prompts_behind_long_caches(causal, window, QH, KH, D, P, lens):
+    """Few rows and many keys: the keys of a block are shared out and its parts joined."""
+    s = Setup(lens, QH, KH, D, P, seed=D)
+    q = make_q(s)
+    out, lse = run(s, q, causal, window)
+    check(s, q, out, lse, causal, window)
 
 
 @pytest.mark.parametrize("causal,window", [(True, 100), (False, 0), (False, 200), (True, 1)])
