@@ -23,12 +23,12 @@
 // largest), so one factor a row holds for all keys.
 //
 // Parts: where the blocks leave SMs idle, several share one's keys, and the rows' parts are joined by a second
-// kernel (a warp a row, all parts' loads at once).  8 q heads and 1 kv head of 128 dims, 16,384 keys: 128 tokens 30 us, 512
-// 42, 1024 71, where one block for all keys takes 200.
+// kernel (a warp a row, all parts' loads at once).  8 q heads and 1 kv head of 128 dims, 16,384 keys: 128
+// tokens 30 us, 512 42, 1024 71, where one block for all keys takes 200.
 //
 // Measured, causal: 8192 tokens, 16 q heads and 2 kv heads of 128 dims 202 us (1360 TFLOP/s, 72% of the
-// cuBLAS rate measured here, 80% of the sustained one); of 64 dims 162 us (850); 16 and 4 heads of 256 510 us (1077), where
-// the split kernel takes 4635; five pieces of up to 1031 tokens behind up to 6007, 24 q heads in groups of 3 of
+// cuBLAS rate measured here, 80% of the sustained one); of 64 dims 162 us (850); 16 and 4 heads of 256
+// 510 us (1077), where the split kernel takes 4635; five pieces of up to 1031 tokens behind up to 6007, 24 q heads in groups of 3 of
 // 64 dims, 69.5 us (its 152 blocks run at once, and the longest has 1.3 times the mean's keys).  On the way at
 // D = 128: whole tiles of logits in the place their weights take 214 us; halves from one MMA warp 284 (its waits
 // for one row tile hold up the other); two threads a row 232 (a barrier a half tile); four converter warps 277; the
@@ -75,8 +75,8 @@ struct Prompt {
     // weights in theirs, logits two half tiles ahead from a warp of their own.  D = 128, where the tensor cores and
     // their operands' reads do (64-column logits read 6 KB a 32 cycles): one place for logits and two for weights,
     // one warp for both, so that a row tile's next logits always come before its output.  us with the first
-    // form and the second: 8192 tokens at D = 64 (8 q heads a kv head) 162 and 167, at D = 128 207 and 202, at D = 256 510 and 597;
-    // five pieces at D = 64 69.5 and 73.6.  (The second with two warps at D = 128: 214.)
+    // form and the second: 8192 tokens at D = 64 (8 q heads a kv head) 162 and 167, at D = 128 207 and 202, at
+    // D = 256 510 and 597; five pieces at D = 64 69.5 and 73.6.  (The second with two warps at D = 128: 214.)
     static constexpr bool kAhead = D != 128;
     __device__ static uint32_t s_place(int n) { return kAhead ? (n & 1) * 64 : 0; }
     __device__ static uint32_t p_place(int n) { return kAhead ? (n & 1) * 64 : 64 + (n & 1) * 32; }
