@@ -430,7 +430,7 @@ moe_status moe_kv_append(const moe_attn_config *cfg, const moe_kv_cache *cache, 
 /* Attention of the batch's rows over their sequences' cached tokens:
  *   out[t, h] = sum_j p_j v_j / sum_j p_j,  p_j = exp(softmax_scale * q[t,h] . k_j)
  * over the positions j < kv_len that the masks leave for the row's position p: causal != 0:
- * j <= p; window > 0: j > p - window.  A row that sees nothing (a negative position, an empty
+ * j <= p; window > 0 (of any size): j > p - window.  A row that sees nothing (a negative position, an empty
  * cache) gives 0, and lse -infinity.  lse [T, q_heads] fp32 (natural log of the sum) or NULL.
  * Slots past kv_len are never used, whatever they hold.  q rows are scaled by a power of two
  * into fp16 and multiplied with the exact codes, sums and softmax statistics in fp32; p is

@@ -266,7 +266,10 @@ moe_status moe_attention(const moe_attn_config *cfg, const moe_kv_cache *cache, 
     a.out_ld = out_ld;
     a.scale_log2 = softmax_scale * 1.4426950408889634f;
     a.causal = causal != 0;
-    a.window = window;
+    // A window as long as the table masks nothing (a position is less than its length); the kernels' 32-bit
+    // pos + 1 - window, pos >= -n_tokens, could not hold a much longer one.
+    const int64_t table = (int64_t)batch->max_pages * c.page_size;
+    a.window = window < table ? window : 0;
     a.desc = reinterpret_cast<SplitDesc *>(static_cast<char *>(ws) + l.desc);
     a.part = reinterpret_cast<float *>(static_cast<char *>(ws) + l.part);
     a.part_out = reinterpret_cast<float *>(static_cast<char *>(ws) + l.prompt_out);
@@ -277,8 +280,7 @@ moe_status moe_attention(const moe_attn_config *cfg, const moe_kv_cache *cache, 
     // sequence: its launch would cost more (5 us) than the rare long run among them.
     const int64_t rows = (int64_t)batch->n_tokens * a.kv.G, mean = rows / batch->n_seqs;
     // keys a sequence has to look at, at most
-    const int64_t seen = window > 0 ? (int64_t)window + batch->n_tokens : INT64_MAX;
-    const int64_t table = (int64_t)batch->max_pages * c.page_size, keys = seen < table ? seen : table;
+    const int64_t seen = a.window > 0 ? (int64_t)a.window + batch->n_tokens : INT64_MAX, keys = seen < table ? seen : table;
     const int64_t work = kPromptWork * (batch->n_seqs == 1 ? 2 : 4) / (keys >= kPromptKeys ? 4 : 2);
     const bool prompts = rows >= kPromptRows && mean >= kPromptMean && rows * c.kv_heads >= work;
     a.prompt_rows = !prompts ? INT_MAX : batch->n_seqs == 1 ? 1 : kPromptRows;
