@@ -67,6 +67,7 @@ __device__ __forceinline__ void key_range(const AttnArgs &p, const Seq &q, int t
 // 2.5 us against 0.5 us a step.
 constexpr int kSegCost = 5;
 constexpr int kSeqCache = 256;  // sequences kept in shared memory
+constexpr float kMostWeight = 15.f;  // log2 of the largest weight under a row's reference: inside fp16
 
 // A sequence's share of the line: tiles * kv heads segments of kSegCost + steps each.
 struct SeqWork {
@@ -507,16 +508,16 @@ __global__ void __launch_bounds__(kThreads, Split<D, NB>::kBlocks) attn_split_ke
                         if (key < lo[nb][i & 1] || key >= hi[nb][i & 1]) z[nb][i] = -INFINITY;
                     }
                 }
-                up |= fmaxf(z[nb][0], z[nb][2]) > m[nb][0] + 8.f || fmaxf(z[nb][1], z[nb][3]) > m[nb][1] + 8.f;
+                up |= fmaxf(z[nb][0], z[nb][2]) > m[nb][0] + kMostWeight || fmaxf(z[nb][1], z[nb][3]) > m[nb][1] + kMostWeight;
             }
-            // The reference m of a row moves only when a logit passes it by more than 2^8 (the
-            // weights then stay below 256, well inside fp16); most steps change nothing.
+            // The reference m of a row moves only when a weight would pass 2^15, 2^6 above the largest that it
+            // was set by; most steps change nothing.
             if (__any_sync(0xffffffffu, up)) {
 #pragma unroll
                 for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
                     for (int c = 0; c < 2; ++c) {
-                        float mx = fmaxf(m[nb][c], fmaxf(z[nb][c], z[nb][2 + c]));
+                        float mx = fmaxf(m[nb][c], fmaxf(z[nb][c], z[nb][2 + c]) - kBelowTop);
                         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
                         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
                         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));

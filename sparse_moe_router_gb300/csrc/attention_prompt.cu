@@ -57,7 +57,7 @@ constexpr int kLaunchRegs = 96, kSoftRegs = 144, kConvRegs = 80, kMmaRegs = 32;
 static_assert(8 * kSoftRegs + 8 * kConvRegs + 4 * kMmaRegs <= 20 * kLaunchRegs, "more registers than the block has");
 constexpr uint64_t kWaitNs = 2000000000ull;  // 2 s: far above any legitimate wait
 constexpr int kPartTiles = 8;  // key tiles of a part (of 8: 11 us at D = 128), about and at least
-constexpr float kMostSum = 32768.f;  // 64 weights of one row may add up to this
+constexpr float kMostSum = 65504.f;  // 64 weights of one row may add up to this: fp16's largest value (64 equal ones: 32,768)
 
 template <int D>
 struct Prompt {
@@ -357,7 +357,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
                 for (int c = 0; c < 2; ++c)
 #pragma unroll
                     for (int k = 0; k < 32; k += 2) top = max3(top, __uint_as_float(s[c][k]), __uint_as_float(s[c][k + 1]));
-                top *= mul;  // mul > 0
+                top = top * mul - kBelowTop;  // mul > 0
                 float f = 1.f;
                 if (l == 0.f) {
                     m = top == -INFINITY ? 0.f : top;

@@ -69,6 +69,12 @@ cudaError_t launch_attn_prompt(const AttnArgs &a, int D, int dtype, cudaStream_t
 inline int prompt_block_rows(int D) { return D == 256 ? 128 : 256; }  // query rows a block of the prompt kernel
 constexpr int kPromptParts = 16;  // at most
 
+// Softmax weights 2^(z - m) are rounded to fp16 for the product with the values: 11 bits from 2^-14 on, an absolute 2^-25
+// below, 0 below that, while their sum keeps them in fp32.  So that keys far below a row's largest one still count
+// (together they may be most of its output, where that key's value is near 0), the reference m lies 2^9 under
+// the largest z when it is set: 11 bits down to 2^-23 of the largest weight, something down to 2^-34.
+constexpr float kBelowTop = 9.f;
+
 struct NormArgs {
     const uint16_t *x, *resid, *gate, *w_post, *w_pre;
     uint16_t *resid_out, *y;
