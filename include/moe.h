@@ -434,8 +434,9 @@ moe_status moe_kv_append(const moe_attn_config *cfg, const moe_kv_cache *cache, 
  * cache) gives 0, and lse -infinity.  lse [T, q_heads] fp32 (natural log of the sum) or NULL.
  * Slots past kv_len are never used, whatever they hold.  q rows are scaled by a power of two
  * into fp16 and multiplied with the exact codes, sums and softmax statistics in fp32; for the
- * product with the values' codes, p times the value's scale is rounded to fp16, to 11 bits down to
- * 2^-23 of the row's largest, and by at most 2^-34 of it below; out is rounded once.
+ * product with the values' codes, p (or p times its value's scale) is rounded to fp16, to 11 bits
+ * down to 2^-23 of the row's largest, and by at most 2^-34 of it below; out is rounded once.  A row
+ * does not depend on keys that it does not see, nor on their pages' scales.
  * softmax_scale > 0.  Deterministic.  A bad page id or a kv_len past the table is reported in
  * the status word (those rows are then unspecified).  Rows from q_start[B] on stay untouched. */
 moe_status moe_attention(const moe_attn_config *cfg, const moe_kv_cache *cache, const moe_kv_batch *batch,

@@ -18,9 +18,15 @@
 // take 2560 cycles a tile of keys: at D = 128 shared memory is the nearer limit, and 3500 are measured.  What is
 // between is the chain of each half tile (wait, TMEM load, weights, TMEM store, MMAs, each a few hundred
 // cycles): leaving out the exponentials gives 2% at D = 128 and 9% at D = 64, the widening 7% and 6%, 7/8 of the
-// logits' MMAs 10% and 0.  The exponents of the pages are drawn into the codes relative to the largest one the
-// block will meet (exact in fp16 unless a page is 2^-15 below it, and then off by at most 2^-25 of the
-// largest), so one factor a row holds for all keys.
+// logits' MMAs 10% and 0.
+//
+// Scales: the exponents of the pages are drawn into the codes relative to the largest that the block meets, exactly (the
+// least code is 2^-9, fp16's least value 2^-24, so 2^15 apart is the most), and one factor a row holds for all keys.  A block
+// whose pages lie further apart, one of all zeros or one with an infinity among them, leaves the codes as they are: the
+// softmax then goes by 16 keys, which share a page, with the key scale in the factor of the logits and the
+// value's exponent in the weights, z = S 2^ek c + ev, w = 2^(z - m), the row's sum taking w 2^-ev.  The converters, which look the
+// pages up anyway, hand the scales over in shared memory.  So a row's result does not depend on pages that it does
+// not see.  (That form for all blocks: the five pieces below 79.6 us instead of 72.0.)
 //
 // Parts: where the blocks leave SMs idle, several share one's keys, and the rows' parts are joined by a second
 // kernel (a warp a row, all parts' loads at once).  8 q heads and 1 kv head of 128 dims, 16,384 keys: 128
@@ -59,6 +65,18 @@ constexpr uint64_t kWaitNs = 2000000000ull;  // 2 s: far above any legitimate wa
 constexpr int kPartTiles = 8;  // key tiles of a part (of 8: 11 us at D = 128), about and at least
 constexpr float kMostSum = 65504.f;  // 64 weights of one row may add up to this: fp16's largest value (64 equal ones: 32,768)
 
+// Most that the exponents of a block's pages may differ by to go into the codes: of the keys what is exact, of the values
+// less, as a weight is then rounded in units of the row's largest whatever its value's scale.
+constexpr int kKeyShift = 15, kValueShift = 8;
+// Scales of the 8 times 16 keys of a tile: factors of the keys, exponents of the values and 2^-those, of the last 4
+// tiles.  A tile's place is written once the logits of the tile two before (D = 256: one) are done, which begin
+// once the weights of the half tile before them are; so whatever still reads is at most 3 tiles behind.
+constexpr int kScaleTiles = 4, kScaleFloats = 24, kScaleBytes = kScaleTiles * kScaleFloats * 4;
+template <bool B>
+struct Flag {
+    static constexpr bool value = B;
+};
+
 template <int D>
 struct Prompt {
     static constexpr int kBlocks = D / 64;                    // 128-byte column blocks of a row
@@ -67,7 +85,8 @@ struct Prompt {
     static constexpr int kTiles = D == 256 ? 1 : 2;           // row tiles a block: TMEM holds one output of 256 dims
     static constexpr int kRows = kTiles * kRowTile;
     static constexpr int kStages = D == 256 ? 2 : 4;          // K and V tiles in flight, in the order K0 V0 K1 V1 ...
-    static constexpr int kSmem = 1024 + (kTiles + kStages) * kTileBytes + 256;  // 1 KB to align; barriers
+    // 1 KB to align; barriers; scales
+    static constexpr int kSmem = 1024 + (kTiles + kStages) * kTileBytes + 256 + kScaleBytes;
     static constexpr uint32_t kColO = kTiles * kKeys;         // TMEM: S0 (S1) O0 (O1); S of even and odd halves
     static constexpr uint32_t kCols = 512;
     // Where a half tile's 64 logits and 64 weights (fp16: 32 columns) lie among a row tile's 128 columns, and
@@ -135,6 +154,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
     uint64_t *bars = reinterpret_cast<uint64_t *>(kv_smem + kStages * C::kTileBytes);
     uint64_t *full = bars, *empty = bars + kStages;  // of a stage
     uint64_t *s_full = empty + kStages;              // [2 x 2] 64 logits of a row tile, even and odd half tiles, are in TMEM
+                                                     // (and their keys' scales in shared memory)
     uint64_t *p_full = s_full + 4;                   // [2 x 2] and their weights are, in their place
     uint64_t *o_half = p_full + 4;                   // [2 x 2] and have gone into the output
     uint64_t *o_full = o_half + 4;                   // [2] all have
@@ -143,7 +163,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
     uint64_t *drain = q_full + 1;
     uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(drain + 4);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_holder + 1);
-    int *max_exp = reinterpret_cast<int *>(tmem_holder + 2);              // [2] of K and V
+    int *max_exp = reinterpret_cast<int *>(tmem_holder + 2);              // [4] largest of K and V, smallest negated
+    float *scales = reinterpret_cast<float *>(kv_smem + kStages * C::kTileBytes + 256);
 
     const int tid = (int)threadIdx.x, lane = tid & 31;
     const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);  // known to be the same in all lanes
@@ -206,8 +227,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
             ptx::mbar_init(&empty[s], kTiles);  // every row tile is done with it
         }
         for (int i = 0; i < 2; ++i) {
-            ptx::mbar_init(&s_full[2 * i], 1);
-            ptx::mbar_init(&s_full[2 * i + 1], 1);
+            ptx::mbar_init(&s_full[2 * i], 2);  // the MMAs' end, and the arrival of the warp that has seen the scales
+            ptx::mbar_init(&s_full[2 * i + 1], 2);
             ptx::mbar_init(&p_full[2 * i], 4);
             ptx::mbar_init(&p_full[2 * i + 1], 4);
             ptx::mbar_init(&o_half[2 * i], 1);
@@ -218,7 +239,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
         ptx::mbar_init(q_full, 4 * kTiles);
         for (int i = 0; i < 4; ++i) ptx::mbar_init(&drain[i], 1);
         *abort_flag = 0;
-        max_exp[0] = max_exp[1] = -127;
+        for (int i = 0; i < 4; ++i) max_exp[i] = -200;
         ptx::fence_mbar_init();
     }
     if (warp == kMmaWarp) ptx::tmem_alloc(tmem_holder, C::kCols);
@@ -226,9 +247,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
     __syncthreads();
     ptx::tc_fence_after();
     const uint32_t tmem = *tmem_holder;
-    // the largest exponents among the pages the block reads
+    // the largest and smallest exponents among the pages the block reads
     {
-        int ek = -127, ev = -127;
+        int e[4] = {-200, -200, -200, -200};
         const int pages0 = (tile0 * kKeys) >> v.log_p, pages1 = (key_hi + v.P - 1) >> v.log_p;
         for (int i = pages0 + tid; tiles > 0 && i < pages1; i += kThreads) {
             int page = __ldg(table + i);
@@ -236,18 +257,25 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
                 layer_error(v.status);
                 page = 0;
             }
-            ek = max(ek, exponent_of(__ldg(v.k_scale + (int64_t)page * v.KH + head)));
-            ev = max(ev, exponent_of(__ldg(v.v_scale + (int64_t)page * v.KH + head)));
+            const int ek = exponent_of(__ldg(v.k_scale + (int64_t)page * v.KH + head));
+            const int ev = exponent_of(__ldg(v.v_scale + (int64_t)page * v.KH + head));
+            e[0] = max(e[0], ek), e[1] = max(e[1], ev), e[2] = max(e[2], -ek), e[3] = max(e[3], -ev);
         }
-        ek = __reduce_max_sync(0xffffffffu, ek);
-        ev = __reduce_max_sync(0xffffffffu, ev);
-        if (lane == 0) {
-            atomicMax(&max_exp[0], ek);
-            atomicMax(&max_exp[1], ev);
-        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) e[i] = __reduce_max_sync(0xffffffffu, e[i]);
+        if (lane < 4) atomicMax(&max_exp[lane], lane == 0 ? e[0] : lane == 1 ? e[1] : lane == 2 ? e[2] : e[3]);
     }
     __syncthreads();
-    const int k_exp = max_exp[0], v_exp = max_exp[1];
+    // Read where they are needed: in registers over the softmax they cost 4% at D = 64.
+    struct Exps {
+        int k, v;
+        bool by16;
+    };
+    auto exps = [&]() {
+        const volatile int *e = max_exp;
+        const int k = e[0], v = e[1];
+        return Exps{k, v, k + e[2] > kKeyShift || v + e[3] > kValueShift};
+    };
     bool ok = true;
 
     if (warp < kSoftWarps) {
@@ -301,10 +329,13 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
             __syncwarp();
             if (lane == 0) ptx::mbar_arrive(q_full);
         }
-        const float mul = p.scale_log2 * pow2f(q_exp) * pow2f(k_exp);
+        const Exps pages = exps();
+        const float mul = p.scale_log2 * pow2f(q_exp) * (pages.by16 ? 1.f : pow2f(pages.k));
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t o_addr = tmem + lanes + C::kColO + i * D;
         float m = 0.f, l = 0.f;  // reference of the weights, and their sum (0: none so far)
+        auto walk = [&](auto flag) {
+        constexpr bool kBy16 = decltype(flag)::value;
         for (int n = 0; n < halves; ++n) {
             ok = __all_sync(0xffffffffu, ptx::mbar_wait(&s_full[2 * i + (n & 1)], n >> 1 & 1, kWaitNs, abort_flag)) != 0;
             if (!ok) break;
@@ -331,33 +362,56 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
             }
             // The sum of the weights itself tells when the reference is too small: as long as it stays within
             // kMostSum every weight fits fp16.  Only then (and where a row begins) is the maximum looked for.
+            const float *c16 = scales + (n >> 1) % kScaleTiles * kScaleFloats + (n & 1) * 4;  // with kBy16
+            float add = 0.f;                                                                  // what the weights add to l
             auto weights = [&]() {
                 float2 sum = make_float2(0.f, 0.f);
+                if constexpr (!kBy16) {
 #pragma unroll
-                for (int c = 0; c < 2; ++c)
+                    for (int c = 0; c < 2; ++c)
 #pragma unroll
-                    for (int k = 0; k < 16; ++k) {
-                        const float2 z =
-                            fma2(make_float2(__uint_as_float(s[c][2 * k]), __uint_as_float(s[c][2 * k + 1])), mul, -m);
-                        const float2 e = make_float2(exp2_fast(z.x), exp2_fast(z.y));
-                        sum = __fadd2_rn(sum, e);
-                        w[c * 16 + k] = pack2<true>(e.x, e.y);
+                        for (int k = 0; k < 16; ++k) {
+                            const float2 z =
+                                fma2(make_float2(__uint_as_float(s[c][2 * k]), __uint_as_float(s[c][2 * k + 1])), mul, -m);
+                            const float2 e = make_float2(exp2_fast(z.x), exp2_fast(z.y));
+                            sum = __fadd2_rn(sum, e);
+                            w[c * 16 + k] = pack2<true>(e.x, e.y);
+                        }
+                    return add = sum.x + sum.y;
+                } else {
+                    float all = 0.f;
+                    add = 0.f;
+#pragma unroll
+                    for (int g = 0; g < 4; ++g) {
+                        const float factor = mul * c16[g], offset = c16[8 + g] - m;
+                        sum = make_float2(0.f, 0.f);
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) {
+                            const uint32_t *x = s[g >> 1] + (g & 1) * 16 + 2 * k;
+                            const float2 z = fma2(make_float2(__uint_as_float(x[0]), __uint_as_float(x[1])), factor, offset);
+                            const float2 e = make_float2(exp2_fast(z.x), exp2_fast(z.y));
+                            sum = __fadd2_rn(sum, e);
+                            w[g * 8 + k] = pack2<true>(e.x, e.y);
+                        }
+                        all += sum.x + sum.y;
+                        add = fmaf(sum.x + sum.y, c16[16 + g], add);
                     }
-                return sum.x + sum.y;
+                    return all;
+                }
             };
             bool renew = __any_sync(0xffffffffu, l == 0.f && sees);
-            float sum = 0.f;
-            if (!renew) {
-                sum = weights();
-                renew = __any_sync(0xffffffffu, !(sum <= kMostSum));
-            }
+            if (!renew) renew = __any_sync(0xffffffffu, !(weights() <= kMostSum));
             if (renew) {
                 float top = -INFINITY;
 #pragma unroll
-                for (int c = 0; c < 2; ++c)
+                for (int g = 0; g < 4; ++g) {
+                    const uint32_t *x = s[g >> 1] + (g & 1) * 16;
+                    float t = kBy16 ? -INFINITY : top;
 #pragma unroll
-                    for (int k = 0; k < 32; k += 2) top = max3(top, __uint_as_float(s[c][k]), __uint_as_float(s[c][k + 1]));
-                top = top * mul - kBelowTop;  // mul > 0
+                    for (int k = 0; k < 16; k += 2) t = max3(t, __uint_as_float(x[k]), __uint_as_float(x[k + 1]));
+                    top = kBy16 ? fmaxf(top, fmaf(t, mul * c16[g], c16[8 + g])) : t;
+                }
+                top = (kBy16 ? top : top * mul) - kBelowTop;  // mul > 0
                 float f = 1.f;
                 if (l == 0.f) {
                     m = top == -INFINITY ? 0.f : top;
@@ -370,6 +424,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
                     ok = __all_sync(0xffffffffu, ptx::mbar_wait(&o_half[2 * i + ((n - 1) & 1)], (n - 1) >> 1 & 1, kWaitNs, abort_flag)) != 0;
                     ptx::tc_fence_after();
                     uint32_t o[16];
+                    constexpr int kUnroll = D == 256 ? 1 : D / 16;  // (16 addresses would be kept over the whole loop)
+#pragma unroll kUnroll
                     for (int c = 0; c < D / 16; ++c) {
                         ptx::tmem_ld_16(o_addr + c * 16, o);
                         ptx::tmem_ld_wait();
@@ -381,9 +437,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
                         ptx::tmem_st_16(o_addr + c * 16, o);
                     }
                 }
-                sum = weights();
+                weights();
             }
-            l += sum;
+            l += add;
             ptx::tmem_st_32(tmem + lanes + i * kKeys + C::p_place(n), w);
             ptx::tmem_st_wait();
             ptx::tc_fence_before();
@@ -392,11 +448,16 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
             if (lane == 0) ptx::mbar_arrive(&p_full[2 * i + (n & 1)]);
             if (!ok) break;
         }
+        };
+        if (pages.by16) walk(Flag<true>{});
+        else walk(Flag<false>{});
         // ---------------------------------------------------------------- output, normalised --
         if (ok && tiles > 0) ok = __all_sync(0xffffffffu, ptx::mbar_wait(&o_full[i], 0, kWaitNs, abort_flag)) != 0;
         if (ok) {
             ptx::tc_fence_after();
-            const float inv = (l > 0.f || l != l) && tiles > 0 ? pow2f(v_exp) / l : 0.f;
+            const Exps pages = exps();
+            const float unit = pages.by16 ? 1.f : pow2f(pages.v);
+            const float inv = (l > 0.f || l != l) && tiles > 0 ? unit / l : 0.f;
             uint16_t *out = p.out + (int64_t)(q.q0 + tok) * p.out_ld + (int64_t)qh * D;
             const int64_t row = ((int64_t)blockIdx.y * v.n_tokens + q.q0 + tok) * v.QH + qh;  // among the parts'
 #pragma unroll
@@ -445,9 +506,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
             if (key < key_hi) page = __ldg(table + (key >> v.log_p));
             return (page < 0 || page >= v.n_pages ? 0 : page) * v.KH + head;  // (reported above)
         };
+        const Exps pages = exps();
+        const bool by16 = pages.by16;
         auto factor = [&](float scale, int largest) {  // 2^(exponent - the block's largest)
-            const int e = min(exponent_of(scale) - largest, 0);  // (past the end: any page)
-            const __half2 f = __float2half2_rn(e < -24 ? 0.f : pow2f(e));
+            const int e = by16 ? 0 : min(exponent_of(scale) - largest, 0);  // (past the end: any page)
+            const __half2 f = __float2half2_rn(e < -kKeyShift ? 0.f : pow2f(e));
             return *reinterpret_cast<const uint32_t *>(&f);
         };
         const int log_pd = v.log_p + (D == 256 ? 8 : D == 128 ? 7 : 6);
@@ -500,12 +563,18 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
             if constexpr (kBoth) load(rv, 0, page1, v.v_codes);
         }
         for (int j = 0; j < tiles; ++j) {
-            const uint32_t fk = factor(sk, k_exp), fv = factor(sv, v_exp);
+            const uint32_t fk = factor(sk, pages.k), fv = factor(sv, pages.v);
+            const int ek = exponent_of(sk), ev = exponent_of(sv);
             const int page0 = page1;
             page1 = page2;  // of tile j + 1
             sk = __ldg(v.k_scale + page1), sv = __ldg(v.v_scale + page1);
             page2 = page_at(j + 2);
             if (!(ok = free_stage(2 * j))) break;
+            if (by16 && lane == 0) {  // (past the end: 1)
+                const bool in = (tile0 + j) * kKeys + cw * 16 < key_hi;
+                float *sc = scales + j % kScaleTiles * kScaleFloats + cw;
+                sc[0] = in ? pow2f(ek) : 1.f, sc[8] = in ? (float)ev : 0.f, sc[16] = in ? pow2f(-ev) : 1.f;
+            }
             widen(rk, 2 * j, fk);
             if constexpr (kBoth) {
                 if (j + 1 < tiles) load(rk, j + 1, page1, v.k_codes);
@@ -549,6 +618,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
                         ptx::mma_f16_ss(tmem + i * kKeys + C::s_place(n), qd + off, kd + off, idesc_s, k > 0);
                     }
                     ptx::mma_commit(&s_full[2 * i + (n & 1)]);
+                    ptx::mbar_arrive(&s_full[2 * i + (n & 1)]);
                     if ((n & 1) || n + 1 == halves) ptx::mma_commit(&empty[s]);
                 }
                 __syncwarp();
