@@ -118,6 +118,9 @@ __device__ __forceinline__ void tie32(uint32_t (&r)[32]) {
 #pragma unroll
     for (int k = 0; k < 32; ++k) asm volatile("" : "+r"(r[k]));
 }
+// A factor of logits that is small beyond fp32 (a tiny query over a tiny page): the logits are 0 either way, but
+// masked ones, -infinity before the factor, have to stay it.
+__device__ __forceinline__ float positive(float x) { return fmaxf(x, 1.17549435e-38f); }
 // a * b + c on two values at once.
 __device__ __forceinline__ float2 fma2(float2 a, float b, float c) {
     return __ffma2_rn(a, make_float2(b, b), make_float2(c, c));
@@ -330,7 +333,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
             if (lane == 0) ptx::mbar_arrive(q_full);
         }
         const Exps pages = exps();
-        const float mul = p.scale_log2 * pow2f(q_exp) * (pages.by16 ? 1.f : pow2f(pages.k));
+        const float q_mul = p.scale_log2 * pow2f(q_exp), mul = pages.by16 ? q_mul : positive(q_mul * pow2f(pages.k));
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t o_addr = tmem + lanes + C::kColO + i * D;
         float m = 0.f, l = 0.f;  // reference of the weights, and their sum (0: none so far)
@@ -383,7 +386,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
                     add = 0.f;
 #pragma unroll
                     for (int g = 0; g < 4; ++g) {
-                        const float factor = mul * c16[g], offset = c16[8 + g] - m;
+                        const float factor = positive(mul * c16[g]), offset = c16[8 + g] - m;
                         sum = make_float2(0.f, 0.f);
 #pragma unroll
                         for (int k = 0; k < 8; ++k) {
@@ -409,7 +412,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
                     float t = kBy16 ? -INFINITY : top;
 #pragma unroll
                     for (int k = 0; k < 16; k += 2) t = max3(t, __uint_as_float(x[k]), __uint_as_float(x[k + 1]));
-                    top = kBy16 ? fmaxf(top, fmaf(t, mul * c16[g], c16[8 + g])) : t;
+                    top = kBy16 ? fmaxf(top, fmaf(t, positive(mul * c16[g]), c16[8 + g])) : t;
                 }
                 top = (kBy16 ? top : top * mul) - kBelowTop;  // mul > 0
                 float f = 1.f;

@@ -90,3 +90,17 @@ def test_pages_of_mixed_scales(QH, KH, D, P, lens, most):
     q = make_q(s)
     out, lse = run(s, q)
     check(s, q, out, lse)
+
+
+@pytest.mark.parametrize("QH,KH,D,P", HEADS)
+@pytest.mark.parametrize("lens", [[(640, 700)], [(3, 640), (1, 400)]], ids=["prompt", "tokens"])
+@pytest.mark.parametrize("size", [1e-30, 1e-38])
+def test_tiny_queries_over_keys_of_the_smallest_scale(QH, KH, D, P, lens, size):
+    """Logits that round to 0: the weights are equal, masked places still have none."""
+    s = Setup(lens, QH, KH, D, P, seed=D)
+    s.cache["k_scale"][:] = 2.0 ** -60
+    q = (make_q(s).double() * size).to(torch.bfloat16)
+    out, lse = run(s, q)
+    check(s, q, out, lse)
+    out, lse = run(s, q, window=50)
+    check(s, q, out, lse, window=50)
