@@ -432,7 +432,8 @@ moe_status moe_kv_append(const moe_attn_config *cfg, const moe_kv_cache *cache, 
  * over the positions j < kv_len that the masks leave for the row's position p: causal != 0:
  * j <= p; window > 0 (of any size): j > p - window.  A row that sees nothing (a negative position, an empty
  * cache) gives 0, and lse -infinity.  lse [T, q_heads] fp32 (natural log of the sum) or NULL.
- * Slots past kv_len are never used, whatever they hold.  q rows are scaled by a power of two
+ * Slots past kv_len are never used, whatever they hold; table entries of pages that no row sees (past
+ * kv_len, behind every row's window) are not looked up and may hold anything.  q rows are scaled by a power of two
  * into fp16 and multiplied with the exact codes, sums and softmax statistics in fp32; for the
  * product with the values' codes, p (or p times its value's scale) is rounded to fp16, to 11 bits
  * down to 2^-23 of the row's largest, and by at most 2^-34 of it below; out is rounded once.  A row

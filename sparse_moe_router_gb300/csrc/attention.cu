@@ -330,11 +330,12 @@ __global__ void __launch_bounds__(kThreads, Split<D, NB>::kBlocks) attn_split_ke
         const int row0 = tile * kRows, rows = min(kRows, sw.q.n * v.G - row0);
         const int first_pos = sw.q.kv - sw.q.n;
 
-        // tiles of 16 keys: tile n is keys [ks0 + n * kStep, + 16), up to the last that a row of this segment sees
+        // tiles of 16 keys: tile n is keys [ks0 + n * kStep, + 16), from the first to the last that a row of this segment sees
         int klo, khi;
         key_range(p, sw.q, row0 / v.G, (row0 + rows - 1) / v.G + 1, klo, khi);
         const int32_t *table = v.table + (int64_t)b * v.max_pages;
-        const int ks0 = max((sw.step0 + s0) * kStep, klo / kStep * kStep) + warp * 16;
+        int ks0 = max((sw.step0 + s0) * kStep, klo / kStep * kStep) + warp * 16;
+        if (ks0 + 16 <= klo) ks0 += kStep;  // 16 keys that no row sees are not looked up: their page may be gone
         const int ke = min((sw.step0 + s1) * kStep, khi);
         const int tiles = ks0 < ke ? (ke - ks0 + kStep - 1) / kStep : 0;
         // lane x holds page * KH + head and the scales of tile (a multiple of 32) + x, and of the 32 after
@@ -577,7 +578,7 @@ __global__ void __launch_bounds__(kThreads, Split<D, NB>::kBlocks) attn_split_ke
             if ((n & 31) == 31) page = page_next, sk = sk_next, sv = sv_next;
         }
 
-        // ------------------------------------------------- join the block's four warps --
+        // ------------------------------------------------ join the block's eight warps --
         copies_wait<0>();
         __syncthreads();  // every ring is drained
 #pragma unroll

@@ -250,10 +250,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
     __syncthreads();
     ptx::tc_fence_after();
     const uint32_t tmem = *tmem_holder;
-    // the largest and smallest exponents among the pages the block reads
+    // the largest and smallest exponents among the pages that a row of the block sees
     {
         int e[4] = {-200, -200, -200, -200};
-        const int pages0 = (tile0 * kKeys) >> v.log_p, pages1 = (key_hi + v.P - 1) >> v.log_p;
+        const int pages0 = key_lo >> v.log_p, pages1 = (key_hi + v.P - 1) >> v.log_p;
         for (int i = pages0 + tid; tiles > 0 && i < pages1; i += kThreads) {
             int page = __ldg(table + i);
             if (page < 0 || page >= v.n_pages) {
@@ -512,18 +512,18 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
         const Exps pages = exps();
         const bool by16 = pages.by16;
         auto factor = [&](float scale, int largest) {  // 2^(exponent - the block's largest)
-            const int e = by16 ? 0 : min(exponent_of(scale) - largest, 0);  // (past the end: any page)
+            const int e = by16 ? 0 : min(exponent_of(scale) - largest, 0);  // (keys not looked up: any page)
             const __half2 f = __float2half2_rn(e < -kKeyShift ? 0.f : pow2f(e));
             return *reinterpret_cast<const uint32_t *>(&f);
         };
         const int log_pd = v.log_p + (D == 256 ? 8 : D == 128 ? 7 : 6);
-        auto load = [&](uint4 (&raw)[kLoads], int tile, int page, const uint8_t *codes) {
+        auto load = [&](uint4 (&raw)[kLoads], int tile, int page, const uint8_t *codes, int end) {
             const int key0 = (tile0 + tile) * kKeys + cw * 16;
             const uint8_t *src = codes + ((uint64_t)(uint32_t)page << log_pd) + ((key0 & (v.P - 1)) + sub) * D + piece * 16;
 #pragma unroll
             for (int n = 0; n < kLoads; ++n) {
                 raw[n] = make_uint4(0, 0, 0, 0);
-                if (key0 + n * kRowsLoad + sub < key_hi)  // slots past the end hold anything
+                if (key0 + n * kRowsLoad + sub < end)  // slots past the end hold anything
                     raw[n] = load_codes16(src + n * kRowsLoad * D);
             }
         };
@@ -559,11 +559,15 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
         };
         constexpr bool kBoth = D < 256;
         uint4 rk[kLoads], rv[kBoth ? kLoads : 1];
-        int page1 = page_at(0), page2 = page_at(1);
+        // In the first tile 16 keys may lie before all that the rows see: their page may be gone and is not looked up.
+        const bool gone = tile0 * kKeys + cw * 16 + 16 <= key_lo;
+        const int first_end = gone ? 0 : key_hi;
+        int end = first_end;  // of the keys of the tile in hand (at D = 256 by its number: 518 us instead of 528)
+        int page1 = gone ? head : page_at(0), page2 = page_at(1);
         float sk = __ldg(v.k_scale + page1), sv = __ldg(v.v_scale + page1);
         if (tiles > 0) {
-            load(rk, 0, page1, v.k_codes);
-            if constexpr (kBoth) load(rv, 0, page1, v.v_codes);
+            load(rk, 0, page1, v.k_codes, end);
+            if constexpr (kBoth) load(rv, 0, page1, v.v_codes, end);
         }
         for (int j = 0; j < tiles; ++j) {
             const uint32_t fk = factor(sk, pages.k), fv = factor(sv, pages.v);
@@ -573,26 +577,27 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
             sk = __ldg(v.k_scale + page1), sv = __ldg(v.v_scale + page1);
             page2 = page_at(j + 2);
             if (!(ok = free_stage(2 * j))) break;
-            if (by16 && lane == 0) {  // (past the end: 1)
-                const bool in = (tile0 + j) * kKeys + cw * 16 < key_hi;
+            if (by16 && lane == 0) {  // (not looked up: 1)
+                const bool in = (tile0 + j) * kKeys + cw * 16 < (kBoth ? end : j == 0 ? first_end : key_hi);
                 float *sc = scales + j % kScaleTiles * kScaleFloats + cw;
                 sc[0] = in ? pow2f(ek) : 1.f, sc[8] = in ? (float)ev : 0.f, sc[16] = in ? pow2f(-ev) : 1.f;
             }
             widen(rk, 2 * j, fk);
             if constexpr (kBoth) {
-                if (j + 1 < tiles) load(rk, j + 1, page1, v.k_codes);
+                if (j + 1 < tiles) load(rk, j + 1, page1, v.k_codes, key_hi);
                 publish(2 * j);
                 if (!(ok = free_stage(2 * j + 1))) break;
                 widen(rv, 2 * j + 1, fv);
-                if (j + 1 < tiles) load(rv, j + 1, page1, v.v_codes);
+                if (j + 1 < tiles) load(rv, j + 1, page1, v.v_codes, key_hi);
             } else {
-                load(rk, j, page0, v.v_codes);
+                load(rk, j, page0, v.v_codes, j == 0 ? first_end : key_hi);
                 publish(2 * j);
                 if (!(ok = free_stage(2 * j + 1))) break;
                 widen(rk, 2 * j + 1, fv);
-                if (j + 1 < tiles) load(rk, j + 1, page1, v.k_codes);
+                if (j + 1 < tiles) load(rk, j + 1, page1, v.k_codes, key_hi);
             }
             publish(2 * j + 1);
+            if constexpr (kBoth) end = key_hi;
         }
     } else {
         regs_down<kMmaRegs>();

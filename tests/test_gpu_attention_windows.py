@@ -50,3 +50,24 @@ def test_the_longest_window_that_masks(QH, KH, D, P, lens):
     for window in (s.table.shape[1] * P - 1, max(s.table.shape[1] * P - 3, 1)):
         out, lse = run(s, q, window=window)
         attention_bound.check(s.cfg, s.cache, s.q_start, s.kv_len, s.table, q, out, lse, window=window)
+
+
+@pytest.mark.parametrize("dead", [-1, 2 ** 31 - 1])
+@pytest.mark.parametrize("QH,KH,D,P", [(8, 2, 128, 16), (8, 1, 64, 16), (16, 2, 256, 32)])
+@pytest.mark.parametrize("window", [1, 100, 333])
+@pytest.mark.parametrize("lens", [[(1, 1000), (3, 777), (1, 130)], [(600, 1300)], [(300, 1300), (1, 999), (260, 700)], [(140, 9000)]],
+                         ids=["tokens", "prompt", "prompts", "parts"])
+def test_pages_behind_the_window_may_be_gone(dead, QH, KH, D, P, window, lens):
+    """Table entries of pages that no row sees are not looked up: they may be given back, and page 0, which bad
+    ids read in their place, may hold anything."""
+    s = Setup(lens, QH, KH, D, P, seed=D)
+    q = make_q(s)
+    for b, (n, kv) in enumerate(lens):
+        s.table[b, :max(kv - n + 1 - window, 0) // P] = dead
+    used = set(s.table.flatten().tolist())
+    for name in "kv":
+        free = [p for p in range(s.n_pages) if p not in used]
+        s.cache[name + "_codes"][free] = 127
+        s.cache[name + "_scale"][free] = float("nan")
+    out, lse = run(s, q, window=window)
+    attention_bound.check(s.cfg, s.cache, s.q_start, s.kv_len, s.table, q, out, lse, window=window)
