@@ -414,12 +414,12 @@ size_t moe_attn_workspace_size(const moe_attn_config *cfg, int max_seqs, int max
  *             larger, else its codes are re-rounded (to nearest even) under the new one
  *   codes     the E4M3 value nearest to value / s, ties to even, of the exact rotated value
  * A page written by one sequence of a call must not be written by another.  Tokens at negative
- * positions (padding in front) are not cached and give q_out rows of 0.
+ * positions (padding in front) are not cached and give q_out rows of 0; so do rows from q_start[B] on
+ * (a batch held for more tokens than it has).
  * Reported as MOE_ERR_INVALID_ARG in the status word: NaN, stored as 0; infinities, stored as
  * +-448 s under the largest scale (as 0 where a rotation makes them NaN); a position past rope,
  * stored as zeros, its q_out row 0; a page id outside [0, n_pages), whose tokens are not cached; a
- * kv_len past the table (the sequence's pages and q_out rows are then unspecified); rows of q from
- * q_start[B] on, given 0.
+ * kv_len past the table (the sequence's pages and q_out rows are then unspecified).
  * q [T, q_heads, D] row stride q_ld, k and v [T, kv_heads, D] strides k_ld, v_ld, q_out stride
  * q_out_ld (q_out may be q).  q and q_out may both be NULL. */
 moe_status moe_kv_append(const moe_attn_config *cfg, const moe_kv_cache *cache, const moe_kv_batch *batch,

@@ -189,8 +189,9 @@ __global__ void __launch_bounds__(kThreads, U <= 2 ? 4 : U == 4 ? 2 : 1) kv_appe
             if (item != first_item) load(item);
             const Seq q = seq_of(last_at_most(v.n_seqs, tok, start_of));
             const int pos = q.kv - q.n + tok - q.q0;
-            const bool ok = pos >= 0 && (pos < p.rope_rows || p.rot == 0) && tok - q.q0 < q.n;
-            if (!ok && pos >= 0) layer_error(v.status);
+            const bool held = tok - q.q0 < q.n;  // else a row behind the last sequence's
+            const bool ok = held && pos >= 0 && (pos < p.rope_rows || p.rot == 0);
+            if (!ok && held && pos >= 0) layer_error(v.status);
             const bool turned = ok && u < (p.rot >> 4);
             Angles g;
             if (turned) load_angles(p.rope + (int64_t)pos * p.rot, u, p.rot, g);
