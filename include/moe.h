@@ -408,7 +408,8 @@ size_t moe_attn_workspace_size(const moe_attn_config *cfg, int max_seqs, int max
 /* Rotates q and k at their positions, writes q to q_out and k and v into the cache.
  *   rotation  (a, b) -> (a cos - b sin, b cos + a sin), cos/sin from row p of rope, fp32
  *             [rope_rows, rotary_dim]: rotary_dim/2 cosines, then rotary_dim/2 sines
- *   q_out     the rotated q rounded once to dtype (correctly: from the exact value)
+ *   q_out     the rotated q rounded once to dtype (correctly: from the exact value; a pair with an
+ *             infinity may give NaN)
  *   scale     per (page, kv head) the smallest power of two s with |value| <= 448 s over the
  *             page's new tokens; a page that held tokens before keeps its scale if that is
  *             larger, else its codes are re-rounded (to nearest even) under the new one
@@ -416,9 +417,9 @@ size_t moe_attn_workspace_size(const moe_attn_config *cfg, int max_seqs, int max
  * A page written by one sequence of a call must not be written by another.  Tokens at negative
  * positions (padding in front) are not cached and give q_out rows of 0; so do rows from q_start[B] on
  * (a batch held for more tokens than it has).
- * Reported as MOE_ERR_INVALID_ARG in the status word: NaN, stored as 0; infinities, stored as
- * +-448 s under the largest scale (as 0 where a rotation makes them NaN); a position past rope,
- * stored as zeros, its q_out row 0; a page id outside [0, n_pages), whose tokens are not cached; a
+ * Reported as MOE_ERR_INVALID_ARG in the status word: NaN, stored as 0; infinities (rotated
+ * values past fp32 among them), stored as +-448 s under the largest scale, as 0 where the rotation's
+ * formula makes them NaN; a position past rope, stored as zeros, its q_out row 0; a page id outside [0, n_pages), whose tokens are not cached; a
  * kv_len past the table (the sequence's pages and q_out rows are then unspecified).
  * q [T, q_heads, D] row stride q_ld, k and v [T, kv_heads, D] strides k_ld, v_ld, q_out stride
  * q_out_ld (q_out may be q).  q and q_out may both be NULL. */

@@ -28,7 +28,8 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kSeqCache = 1024;  // sequences whose places a block stages in shared memory
 
-// a*c - b*s rounded to odd (see above).  Explicit _rn operations: none may be contracted.
+// a*c - b*s rounded to odd (see above); not finite, as the plain formula gives it (the errors of infinite products and
+// sums are NaN).  Explicit _rn operations: none may be contracted.
 __device__ __forceinline__ float rotate_odd(float a, float c, float b, float s) {
     const float p = __fmul_rn(a, c), q = -__fmul_rn(b, s);
     const float ep = __fmaf_rn(a, c, -p), eq = __fmaf_rn(-b, s, -q);
@@ -40,7 +41,7 @@ __device__ __forceinline__ float rotate_odd(float a, float c, float b, float s) 
     const float lost = __fsub_rn(err, __fsub_rn(r2, r));
     int bits = __float_as_int(r2);
     if (lost != 0.f && !(bits & 1)) bits += ((lost > 0.f) == (r2 > 0.f)) ? 1 : -1;
-    return __int_as_float(bits);
+    return fabsf(r) <= 3.402823466e38f ? __int_as_float(bits) : r;
 }
 
 // The same to nearest, and whether that is so near the middle between two 16-bit values that rounding it
