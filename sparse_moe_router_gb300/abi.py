@@ -495,6 +495,13 @@ class KVCache:
                           _device_array(k_scale, "k_scale", torch.float32, shape[:2]),
                           _device_array(v_scale, "v_scale", torch.float32, shape[:2]), n)
         self.k_codes, self.v_codes, self.k_scale, self.v_scale = k_codes, v_codes, k_scale, v_scale
+        self.layout = shape[1:]
+
+    def check(self, cfg: AttnConfig):
+        """A call of another layout would read and write past the pages."""
+        if (cfg.kv_heads, cfg.page_size, cfg.head_dim) != self.layout:
+            raise ValueError("the cache has (kv_heads, page_size, head_dim) %s, the config %s" %
+                             (self.layout, (cfg.kv_heads, cfg.page_size, cfg.head_dim)))
 
     @classmethod
     def alloc(cls, cfg: AttnConfig, n_pages, device="cuda"):
@@ -535,6 +542,7 @@ def alloc_attn_workspace(cfg: AttnConfig, max_seqs, max_tokens, device="cuda") -
 def moe_kv_append(cfg: AttnConfig, cache: KVCache, batch: KVBatch, q, k, v, rope, q_out, ws, stream=None):
     """Rotates q [T, q_heads, D] into q_out and writes k, v [T, kv_heads, D] into the cache at the batch's
     positions.  rope: fp32 [positions, rotary_dim], cosines then sines (None with rotary_dim 0)."""
+    cache.check(cfg)
     T, D, dt = batch.n_tokens, cfg.head_dim, _TORCH_DTYPES[cfg.dtype]
     qw, kw = cfg.q_heads * D, cfg.kv_heads * D
     rope_p, rope_rows, q_p, q_ld, qo_p, qo_ld = None, 0, None, 0, None, 0
@@ -555,6 +563,7 @@ def moe_attention(cfg: AttnConfig, cache: KVCache, batch: KVBatch, q, out, ws, l
                   causal=True, window=0, stream=None):
     """Attention of q [T, q_heads, D] over the batch's cached tokens into out (and lse fp32
     [T, q_heads]).  softmax_scale None: 1 / sqrt(D)."""
+    cache.check(cfg)
     T, qw, dt = batch.n_tokens, cfg.q_heads * cfg.head_dim, _TORCH_DTYPES[cfg.dtype]
     lse_p = None if lse is None else _device_array(lse, "lse", torch.float32, (T, cfg.q_heads))
     st = lib().moe_attention(
