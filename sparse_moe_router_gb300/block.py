@@ -38,6 +38,16 @@ class Pages:
         self.free = list(range(n_pages - 1, -1, -1))
         self.table = torch.zeros(n_seqs, self.max_pages, dtype=torch.int32, device=device)
 
+    def require(self, new_tokens):
+        """Raises, and takes nothing, unless every sequence has room for so many more tokens: a step that fails
+        halfway would leave lengths that count tokens which were never written."""
+        left = len(self.free)
+        for seq, tokens in enumerate(new_tokens):
+            need = -(-(self.lens[seq] + tokens) // self.page_size)
+            left -= need - len(self.pages[seq])
+            if need > self.max_pages or left < 0:
+                raise RuntimeError("no page left for sequence %d at %d tokens" % (seq, self.lens[seq] + tokens))
+
     def grow(self, seq, tokens):
         """Room for `tokens` more of a sequence; raises when the pool or the table is full."""
         need = -(-(self.lens[seq] + tokens) // self.page_size)
@@ -78,15 +88,18 @@ class DecoderLayers:
         self.max_tokens = max_tokens
 
     def batch(self, new_tokens):
-        """The abi.KVBatch of a step with new_tokens[b] new tokens of sequence b; takes their pages."""
-        for b, n in enumerate(new_tokens):
-            if n:
-                self.pages.grow(b, n)
+        """The abi.KVBatch of a step with new_tokens[b] new tokens of sequence b; takes their pages, all or none."""
+        if len(new_tokens) != len(self.pages.lens) or any(n < 0 for n in new_tokens):
+            raise ValueError("new_tokens has to name %d counts" % len(self.pages.lens))
         starts = [0]
         for n in new_tokens:
             starts.append(starts[-1] + n)
         if starts[-1] > self.max_tokens:
             raise ValueError("%d tokens in a step of at most %d" % (starts[-1], self.max_tokens))
+        self.pages.require(new_tokens)
+        for b, n in enumerate(new_tokens):
+            if n:
+                self.pages.grow(b, n)
         dev = self.rope.device
         return abi.KVBatch(torch.tensor(starts, dtype=torch.int32, device=dev),
                            torch.tensor(self.pages.lens, dtype=torch.int32, device=dev), self.pages.table, starts[-1])
@@ -147,6 +160,7 @@ class DecodeGraph:
             self.out = model.run(self.x, self.batch)
 
     def step(self, x):
+        self.model.pages.require([1] * len(self.model.pages.lens))
         for b in range(len(self.model.pages.lens)):
             self.model.pages.grow(b, 1)
         self.x.copy_(x)
