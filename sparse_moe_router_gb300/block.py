@@ -31,7 +31,7 @@ class Pages:
     """Page tables of a fixed set of sequences over one pool, the same for every layer."""
 
     def __init__(self, n_seqs, max_len, page_size, n_pages, device="cuda"):
-        self.page_size, self.n_pages = page_size, n_pages
+        self.page_size, self.n_pages, self.max_len = page_size, n_pages, max_len
         self.max_pages = -(-max_len // page_size)
         self.lens = [0] * n_seqs
         self.pages = [[] for _ in range(n_seqs)]
@@ -45,13 +45,13 @@ class Pages:
         for seq, tokens in enumerate(new_tokens):
             need = -(-(self.lens[seq] + tokens) // self.page_size)
             left -= need - len(self.pages[seq])
-            if need > self.max_pages or left < 0:
+            if self.lens[seq] + tokens > self.max_len or left < 0:
                 raise RuntimeError("no page left for sequence %d at %d tokens" % (seq, self.lens[seq] + tokens))
 
     def grow(self, seq, tokens):
-        """Room for `tokens` more of a sequence; raises when the pool or the table is full."""
+        """Room for `tokens` more of a sequence; raises when the pool is empty or max_len reached."""
         need = -(-(self.lens[seq] + tokens) // self.page_size)
-        if need > self.max_pages or need - len(self.pages[seq]) > len(self.free):
+        if self.lens[seq] + tokens > self.max_len or need - len(self.pages[seq]) > len(self.free):
             raise RuntimeError("no page left for sequence %d at %d tokens" % (seq, self.lens[seq] + tokens))
         new = [self.free.pop() for _ in range(need - len(self.pages[seq]))]
         if new:
@@ -72,6 +72,8 @@ class DecoderLayers:
 
     def __init__(self, moe_cfg, attn_cfg, layers, pages: Pages, max_tokens, rope, eps=1e-6, residual_scale=1.0):
         self.moe, self.attn, self.layers, self.pages, self.rope = moe_cfg, attn_cfg, layers, pages, rope
+        if attn_cfg.rotary_dim and rope.shape[0] < pages.max_len:
+            raise ValueError("angles for %d positions, sequences of up to %d" % (rope.shape[0], pages.max_len))
         H, dev = moe_cfg.hidden, rope.device
         self.caches = [abi.KVCache.alloc(attn_cfg, pages.n_pages, dev) for _ in layers]
         self.weights = [abi.weights(l) for l in layers]

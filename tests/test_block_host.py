@@ -48,3 +48,25 @@ def test_a_refused_graph_step_takes_nothing():
     with pytest.raises(RuntimeError):
         g.step(g.x)  # sequence 1 needs a page that is not there
     assert unchanged(m.pages, before)
+
+
+def test_lengths_end_at_max_len():
+    """Not at the end of the page that holds it: the table of angles may end there."""
+    p = block.Pages(2, 50, 16, 8, device="cpu")
+    p.grow(0, 50)
+    before = state(p)
+    with pytest.raises(RuntimeError):
+        p.grow(0, 1)
+    with pytest.raises(RuntimeError):
+        p.require([1, 1])
+    with pytest.raises(RuntimeError):
+        p.grow(1, 51)
+    assert unchanged(p, before)
+    p.require([0, 50])
+
+
+def test_a_table_of_angles_shorter_than_the_sequences():
+    moe = abi.config(hidden=16, n_experts=16, top_k=4, inter=128, shared_inter=128)
+    pages = block.Pages(2, 50, 16, 8, device="cpu")
+    with pytest.raises(ValueError, match="angles"):
+        block.DecoderLayers(moe, abi.attn_config(8, 2, 64, 16, rotary_dim=32), [], pages, 50, torch.zeros(49, 32))
