@@ -128,12 +128,18 @@ class DecoderLayers:
                                w_pre=None if last else self.layers[i + 1]["norm_attn"])
         return resid
 
+    def check_rows(self, x, tokens):
+        if tuple(x.shape) != (tokens, self.moe.hidden):  # (copying them would broadcast)
+            raise ValueError("x has shape %s, not %d rows of %d" % (tuple(x.shape), tokens, self.moe.hidden))
+
     def prefill(self, x, new_tokens):
         """x [sum(new_tokens), H]: the sequences' new tokens one after another."""
+        self.check_rows(x, sum(new_tokens))
         return self.run(x, self.batch(new_tokens))
 
     def decode(self, x):
-        """One token for every sequence."""
+        """One token for every sequence: x [sequences, H]."""
+        self.check_rows(x, len(self.pages.lens))
         return self.run(x, self.batch([1] * len(self.pages.lens)))
 
     def check(self):
@@ -162,6 +168,7 @@ class DecodeGraph:
             self.out = model.run(self.x, self.batch)
 
     def step(self, x):
+        self.model.check_rows(x, len(self.model.pages.lens))
         self.model.pages.require([1] * len(self.model.pages.lens))
         for b in range(len(self.model.pages.lens)):
             self.model.pages.grow(b, 1)

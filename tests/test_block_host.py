@@ -70,3 +70,19 @@ def test_a_table_of_angles_shorter_than_the_sequences():
     pages = block.Pages(2, 50, 16, 8, device="cpu")
     with pytest.raises(ValueError, match="angles"):
         block.DecoderLayers(moe, abi.attn_config(8, 2, 64, 16, rotary_dim=32), [], pages, 50, torch.zeros(49, 32))
+
+
+@pytest.mark.parametrize("shape", [(1, 16), (16,), (4, 16), (5, 8), (5, 1), (1, 5, 16)])
+def test_rows_of_another_shape(shape):
+    """One row would be broadcast to all tokens; nothing is taken."""
+    m = stack()
+    before = state(m.pages)
+    with pytest.raises(ValueError, match="rows"):
+        m.prefill(torch.zeros(shape, dtype=torch.bfloat16), [3, 0, 2])
+    with pytest.raises(ValueError, match="rows"):
+        m.decode(torch.zeros(shape, dtype=torch.bfloat16))
+    g = object.__new__(block.DecodeGraph)
+    g.model, g.x = m, torch.zeros(3, 16, dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="rows"):
+        g.step(torch.zeros(shape, dtype=torch.bfloat16))
+    assert unchanged(m.pages, before)
