@@ -67,7 +67,7 @@ class Pages:
 
 class DecoderLayers:
     """layers: a list of dicts with w_qkv [(QH + 2 KH) D, H], w_o [H, QH D], norm_attn, norm_attn_out,
-    norm_moe, norm_moe_out [H] (a missing *_out: no norm after that block), attn_gate [H] (optional), and the MoE
+    norm_moe, norm_moe_out [H] (a missing *_out: no norm after that block), attn_gate [H] (optional, layer by layer), and the MoE
     weights of abi.weights.  All bf16 on the device."""
 
     def __init__(self, moe_cfg, attn_cfg, layers, pages: Pages, max_tokens, rope, eps=1e-6, residual_scale=1.0):
@@ -79,9 +79,9 @@ class DecoderLayers:
         self.weights = [abi.weights(l) for l in layers]
         self.moe_ws = abi.alloc_workspace(moe_cfg, max_tokens, dev)
         self.attn_ws = abi.alloc_attn_workspace(attn_cfg, len(pages.lens), max_tokens, dev)
-        gate = "channel" if "attn_gate" in layers[0] else "none"
         self.norm_in = abi.norm_config(H, eps=eps)
-        self.norm_attn = abi.norm_config(H, gate=gate, eps=eps, residual_scale=residual_scale)
+        self.norm_attn = [abi.norm_config(H, gate="none" if l.get("attn_gate") is None else "channel", eps=eps,
+                                          residual_scale=residual_scale) for l in layers]
         self.norm_moe = abi.norm_config(H, eps=eps, residual_scale=residual_scale)
         new = lambda *s: torch.empty(*s, dtype=torch.bfloat16, device=dev)  # noqa: E731
         QD, KD = attn_cfg.q_heads * attn_cfg.head_dim, attn_cfg.kv_heads * attn_cfg.head_dim
@@ -120,7 +120,7 @@ class DecoderLayers:
             abi.moe_kv_append(c, self.caches[i], batch, q, k, v, self.rope, q, self.attn_ws)
             abi.moe_attention(c, self.caches[i], batch, q, ctx.view(T, QH, D), self.attn_ws)
             torch.mm(ctx, l["w_o"].T, out=block)
-            abi.moe_block_norm(self.norm_attn, block, resid, resid, y, gate=l.get("attn_gate"), w_post=l.get("norm_attn_out"),
+            abi.moe_block_norm(self.norm_attn[i], block, resid, resid, y, gate=l.get("attn_gate"), w_post=l.get("norm_attn_out"),
                                w_pre=l["norm_moe"])
             abi.moe_forward(self.moe, self.weights[i], y, T, block, None, self.moe_ws)
             last = i + 1 == len(self.layers)

@@ -34,3 +34,21 @@ def test_a_step_after_a_refused_one():
     assert torch.equal(a.prefill(x, [20, 10]), b.prefill(x, [20, 10]))
     assert a.pages.lens == b.pages.lens == [80, 50]
     a.check()
+
+
+@pytest.mark.parametrize("without", [0, 1, 2])
+@pytest.mark.parametrize("none", [False, True])
+def test_gates_on_some_layers(without, none):
+    """A layer without an attention gate (left out, or None) among gated ones is a layer with a gate of ones."""
+    moe = abi.config(hidden=256, n_experts=16, top_k=4, inter=128, shared_inter=128)
+    layers = block.random_layers(moe, abi.attn_config(8, 2, 64, 16, rotary_dim=32), 3)
+    ones = [dict(l) for l in layers]
+    ones[without]["attn_gate"] = torch.ones_like(layers[without]["attn_gate"])
+    if none:
+        layers[without]["attn_gate"] = None
+    else:
+        del layers[without]["attn_gate"]
+    a, b = make(layers=layers), make(layers=ones)
+    x = rows(100)
+    assert torch.equal(a.prefill(x, [60, 40]), b.prefill(x, [60, 40]))
+    a.check()
