@@ -85,8 +85,8 @@ struct Prompt {
     static constexpr int kTiles = D == 256 ? 1 : 2;           // row tiles a block: TMEM holds one output of 256 dims
     static constexpr int kRows = kTiles * kRowTile;
     static constexpr int kStages = D == 256 ? 2 : 4;          // K and V tiles in flight, in the order K0 V0 K1 V1 ...
-    // 1 KB to align; barriers; scales
-    static constexpr int kSmem = 1024 + (kTiles + kStages) * kTileBytes + 256 + kScaleBytes;
+    // 1 KB to align; barriers; scales; whether the block writes the output
+    static constexpr int kSmem = 1024 + (kTiles + kStages) * kTileBytes + 256 + kScaleBytes + 16;
     static constexpr uint32_t kColO = kTiles * kKeys;         // TMEM: S0 (S1) O0 (O1); S of even and odd halves
     static constexpr uint32_t kCols = 512;
     // Where a half tile's 64 logits and 64 weights (fp16: 32 columns) lie among a row tile's 128 columns, and
@@ -146,6 +146,26 @@ __device__ __forceinline__ int slot_base(const KvView &v, int b) {
     return (int)((int64_t)v.q_start[b] * v.G / R) + b;
 }
 
+// Keys that any of a block's rows sees, in tiles, and how many parts of so many tiles they are worked on in.  The
+// host's p.parts goes by what the table can name; a sequence that is shorter has fewer, down to one block that writes
+// the output itself (512 tokens of 16 q and 2 kv heads of 128 without a past: 17.0 us in a table of 512, 20.5 in one for 131,072, and
+// 35.6 with parts by the table).
+struct BlockKeys {
+    int lo, hi, tile0, tiles, parts, share;
+};
+__device__ __forceinline__ BlockKeys block_keys(const AttnArgs &p, const Seq &q, int row0, int rows) {
+    BlockKeys k;
+    const int first_pos = q.kv - q.n, pos_lo = first_pos + row0 / p.kv.G, pos_hi = first_pos + (row0 + rows - 1) / p.kv.G;
+    k.hi = p.causal ? min(q.kv, pos_hi + 1) : q.kv;
+    k.lo = p.window > 0 ? max(0, pos_lo + 1 - p.window) : 0;
+    k.tile0 = k.lo / kKeys;
+    k.tiles = k.hi > k.lo ? (k.hi + kKeys - 1) / kKeys - k.tile0 : 0;
+    k.parts = min(p.parts, max((k.tiles + kPartTiles / 2) / kPartTiles, 1));
+    k.share = (k.tiles + k.parts - 1) / k.parts;
+    if (k.tiles > 0) k.parts = (k.tiles + k.share - 1) / k.share;
+    return k;
+}
+
 template <int D, bool F16, bool PARTS>
 __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_constant__ AttnArgs p, int slots) {
     using C = Prompt<D>;
@@ -168,6 +188,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_holder + 1);
     int *max_exp = reinterpret_cast<int *>(tmem_holder + 2);              // [4] largest of K and V, smallest negated
     float *scales = reinterpret_cast<float *>(kv_smem + kStages * C::kTileBytes + 256);
+    volatile int *in_parts = reinterpret_cast<int *>(scales + kScaleTiles * kScaleFloats);
 
     const int tid = (int)threadIdx.x, lane = tid & 31;
     const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);  // known to be the same in all lanes
@@ -208,18 +229,18 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
     const int rows = min(kRows, q.n * v.G - row0);
     if (row0 < 0 || rows <= 0 || q.n * v.G < p.prompt_rows) return;  // (short runs are the split kernel's)
     const int first_pos = q.kv - q.n;
-    // keys that any of the rows sees
-    const int pos_lo = first_pos + row0 / v.G, pos_hi = first_pos + (row0 + rows - 1) / v.G;
-    int key_hi = p.causal ? min(q.kv, pos_hi + 1) : q.kv;
-    int key_lo = p.window > 0 ? max(0, pos_lo + 1 - p.window) : 0;
-    int tile0 = key_lo / kKeys;
-    int tiles = key_hi > key_lo ? (key_hi + kKeys - 1) / kKeys - tile0 : 0;
+    const BlockKeys all = block_keys(p, q, row0, rows);
+    int key_lo = all.lo, key_hi = all.hi, tile0 = all.tile0, tiles = all.tiles;
     if (PARTS) {  // this block's part of them
-        const int parts = min(p.parts, max((tiles + kPartTiles / 2) / kPartTiles, 1)), share = (tiles + parts - 1) / parts;
-        tile0 += (int)blockIdx.y * share;
-        tiles = max(min(share, tiles - (int)blockIdx.y * share), 0);
+        if ((int)blockIdx.y >= all.parts) {  // the join takes -infinity for no such part
+            const int tok = q.q0 + (row0 + tid) / v.G, qh = head * v.G + (row0 + tid) % v.G;
+            if (tid < rows) p.part_lse[((int64_t)blockIdx.y * v.n_tokens + tok) * v.QH + qh] = -INFINITY;
+            return;
+        }
+        tile0 += (int)blockIdx.y * all.share;
+        tiles = min(all.share, tiles - (int)blockIdx.y * all.share);
         key_lo = max(key_lo, tile0 * kKeys);
-        key_hi = max(min(key_hi, (tile0 + tiles) * kKeys), key_lo);
+        key_hi = min(key_hi, (tile0 + tiles) * kKeys);
     }
     const int halves = tiles > 0 ? (key_hi - tile0 * kKeys + 63) / 64 : 0;  // half tiles of 64 keys
     const int32_t *table = v.table + (int64_t)b * v.max_pages;
@@ -242,6 +263,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
         ptx::mbar_init(q_full, 4 * kTiles);
         for (int i = 0; i < 4; ++i) ptx::mbar_init(&drain[i], 1);
         *abort_flag = 0;
+        *in_parts = PARTS && all.parts > 1;
         for (int i = 0; i < 4; ++i) max_exp[i] = -200;
         ptx::fence_mbar_init();
     }
@@ -463,6 +485,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
             const float inv = (l > 0.f || l != l) && tiles > 0 ? unit / l : 0.f;
             uint16_t *out = p.out + (int64_t)(q.q0 + tok) * p.out_ld + (int64_t)qh * D;
             const int64_t row = ((int64_t)blockIdx.y * v.n_tokens + q.q0 + tok) * v.QH + qh;  // among the parts'
+            const bool part = PARTS && *in_parts != 0;
 #pragma unroll
             for (int c = 0; c < D / 32; ++c) {
                 uint32_t o[32];
@@ -477,17 +500,17 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
                     float f[8];
 #pragma unroll
                     for (int x = 0; x < 8; ++x) f[x] = inv == 0.f ? 0.f : __uint_as_float(o[8 * k + x]) * inv;
-                    if (PARTS) {
-                        float4 *part = reinterpret_cast<float4 *>(p.part_out + row * D + c * 32 + k * 8);
-                        part[0] = make_float4(f[0], f[1], f[2], f[3]);
-                        part[1] = make_float4(f[4], f[5], f[6], f[7]);
+                    if (part) {
+                        float4 *dst = reinterpret_cast<float4 *>(p.part_out + row * D + c * 32 + k * 8);
+                        dst[0] = make_float4(f[0], f[1], f[2], f[3]);
+                        dst[1] = make_float4(f[4], f[5], f[6], f[7]);
                     } else {
                         *reinterpret_cast<uint4 *>(out + c * 32 + k * 8) = pack8<F16>(f);
                     }
                 }
             }
-            if (live && PARTS) p.part_lse[row] = m + log2f(l);
-            else if (live && p.lse) p.lse[(int64_t)(q.q0 + tok) * v.QH + qh] = (m + log2f(l)) * 0.6931471805599453f;
+            if (live && PARTS) p.part_lse[row] = part ? m + log2f(l) : INFINITY;  // infinity: the output is written
+            if (live && !part && p.lse) p.lse[(int64_t)(q.q0 + tok) * v.QH + qh] = (m + log2f(l)) * 0.6931471805599453f;
         }
         }
     } else if (warp < kMmaWarp) {
@@ -695,7 +718,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prompt_kernel(const __grid_c
     if (warp == kMmaWarp) ptx::tmem_dealloc(tmem, C::kCols);
 }
 
-// Joins the parts of each row, a warp a row (up to 32 sequences).  A part in which a row sees nothing holds zeros.
+// Joins the parts of each row that has several, a warp a row (up to 32 sequences).  Parts in which a row sees nothing, or
+// that there are not, have -infinity and are not read.
 template <int D, bool F16>
 __global__ void __launch_bounds__(256) attn_prompt_join_kernel(const __grid_constant__ AttnArgs p) {
     const KvView &v = p.kv;
@@ -704,6 +728,8 @@ __global__ void __launch_bounds__(256) attn_prompt_join_kernel(const __grid_cons
     if (row >= rows) return;
     const int tok = (int)(row / v.QH), qh = (int)(row % v.QH);
     const float lse = lane < p.parts ? p.part_lse[lane * rows + row] : -INFINITY;
+    const uint32_t there = __ballot_sync(0xffffffffu, lse != -INFINITY);
+    if (__shfl_sync(0xffffffffu, lse, 0) == INFINITY) return;  // one part: its block has written the row
     const int b = __popc(__ballot_sync(0xffffffffu, lane < v.n_seqs && v.q_start[min(lane + 1, v.n_seqs)] <= tok));
     if (b >= v.n_seqs) return;
     const Seq q = load_seq(v, b);
@@ -723,7 +749,7 @@ __global__ void __launch_bounds__(256) attn_prompt_join_kernel(const __grid_cons
         float4 o[kPromptParts];
 #pragma unroll
         for (int i = 0; i < kPromptParts; ++i)
-            o[i] = i < p.parts && d < D ? *reinterpret_cast<const float4 *>(p.part_out + (i * rows + row) * D + d) : acc;
+            o[i] = (there >> i & 1) && d < D ? *reinterpret_cast<const float4 *>(p.part_out + (i * rows + row) * D + d) : acc;
 #pragma unroll
         for (int i = 0; i < kPromptParts; ++i) {
             const float wi = __shfl_sync(0xffffffffu, w, i);

@@ -55,8 +55,9 @@ struct AttnArgs {
     // sequences with at least this many query rows a kv head (new tokens x G) are the prompt
     // kernel's, the others the split kernel's
     int prompt_rows;
-    // prompt kernel: the keys of a block in so many parts, and with more than one each part's rows, [parts, T, QH, D]
-    // normalised and [parts, T, QH] the log2 of their sums
+    // prompt kernel: the keys of a block in so many parts at most, and with more than one each part's rows, [parts, T, QH, D]
+    // normalised and [parts, T, QH] the log2 of their sums: -infinity where a part has nothing, and in the first
+    // +infinity where it has all and its block has written the output
     int parts;
     float *part_out, *part_lse;
 };
