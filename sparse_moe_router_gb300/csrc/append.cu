@@ -10,8 +10,9 @@
 //
 // Bound: every value is read and written once (HBM) for prompts; a decode step is two or three
 // dependent reads (sequence, page, values) and the launch.  Measured: one token of each of 48 sequences
-// 5.9 us; 8192 tokens of 16 q and 2 kv heads 20.8 us (4.0 TB/s, of which the rotation of q, with its reads of
-// the table, is the longer part); 11 sequences of up to 700 tokens, 24 and 8 heads of 64 dims, pages of 16, 11.2 us
+// 5.7 us; 8192 tokens of 16 q and 2 kv heads 21.0 us (4.0 TB/s, of which the rotation of q, with its reads of
+// the table, is the longer part; issue slots are 58% used, DRAM 27%: it is the latency of the warps that 64 registers
+// leave room for); 11 sequences of up to 700 tokens, 24 and 8 heads of 64 dims, pages of 16, 11.1 us
 // (23.9 with a block for each small page, 12.8 with q's heads one by one).
 //
 // Exact codes.  The rotation a cos - b sin of 16-bit a, b with an fp32 table is carried as an

@@ -21,7 +21,7 @@
 // a block, whatever the lengths.  A run that ends inside a segment leaves partial sums, which a second
 // kernel joins in order.
 //
-// Measured, with the join: one token behind 1500 9.7 us, most of it five dependent reads and two
+// Measured, with the join: one token behind 1500 9.9 us, most of it five dependent reads and two
 // launches; one behind 131,071, 32 q and 8 kv heads, 54 us (5.0 TB/s, 74% of the measured copy); 48 of very different
 // length, up to 32,768, 36 us (4.0 TB/s); 8 runs of up to 4 tokens, D = 256, window 4096, 15 us.  About 10 us
 // of each is the same start and end; between them the codes stream at 6 TB/s.

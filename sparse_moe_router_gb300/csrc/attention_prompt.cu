@@ -26,16 +26,17 @@
 // softmax then goes by 16 keys, which share a page, with the key scale in the factor of the logits and the
 // value's exponent in the weights, z = S 2^ek c + ev, w = 2^(z - m), the row's sum taking w 2^-ev.  The converters, which look the
 // pages up anyway, hand the scales over in shared memory.  So a row's result does not depend on pages that it does
-// not see.  (That form for all blocks: the five pieces below 79.6 us instead of 72.0.)
+// not see.  (A page of zeros in each sequence: the five pieces below 82.4 us instead
+// of 70.8, 8192 tokens 218.5 instead of 200.7.)
 //
 // Parts: where the blocks leave SMs idle, several share one's keys, and the rows' parts are joined by a second
 // kernel (a warp a row, all parts' loads at once).  8 q heads and 1 kv head of 128 dims, 16,384 keys: 128
-// tokens 30 us, 512 42, 1024 71, where one block for all keys takes 200.
+// tokens 31 us, 512 44, 1024 72, where one block for all keys takes 200.
 //
-// Measured, causal: 8192 tokens, 16 q heads and 2 kv heads of 128 dims 202 us (1360 TFLOP/s, 72% of the
-// cuBLAS rate measured here, 80% of the sustained one); of 64 dims 162 us (850); 16 and 4 heads of 256
-// 510 us (1077), where the split kernel takes 4635; five pieces of up to 1031 tokens behind up to 6007, 24 q heads in groups of 3 of
-// 64 dims, 69.5 us (its 152 blocks run at once, and the longest has 1.3 times the mean's keys).  On the way at
+// Measured, causal: 8192 tokens, 16 q heads and 2 kv heads of 128 dims 201 us (1368 TFLOP/s, 73% of the
+// cuBLAS rate measured here, 80% of the sustained one); of 64 dims 161 us (851); 16 and 4 heads of 256
+// 519 us (1060), where the split kernel takes 4635; five pieces of up to 1031 tokens behind up to 6007, 24 q heads in groups of 3 of
+// 64 dims, 70.6 us (its 152 blocks run at once, and the longest has 1.3 times the mean's keys).  On the way, each against the kernel of its time, at
 // D = 128: whole tiles of logits in the place their weights take 214 us; halves from one MMA warp 284 (its waits
 // for one row tile hold up the other); two threads a row 232 (a barrier a half tile); four converter warps 277; the
 // maximum looked for in every tile 221; scalar instead of paired fp32 in the softmax 219; the next logits

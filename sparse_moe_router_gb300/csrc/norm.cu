@@ -8,8 +8,8 @@
 // else touches memory.  Both sums of squares are fp32.
 //
 // Bound: HBM from a few hundred rows on, below that the launch and two dependent sums.  Measured: one
-// row of 2048 2.7 us; 1031 rows of 4096 with a channel gate 10.1 us (3.3 TB/s: 7 rows an SM, so the first
-// row's way through the chip is a quarter of it); 8192 rows of 2048 with a gate on each element 32.6 us (5.1 TB/s,
+// row of 2048 2.7 us; 1031 rows of 4096 with a channel gate 10.1 us (3.3 TB/s: 16 warps an SM, each with
+// one row of its seven ahead); 8192 rows of 2048 with a gate on each element 32.6 us (5.1 TB/s,
 // 77% of the measured copy; before a block kept its weights and had its next row under way, 45).
 #include "layer.h"
 
