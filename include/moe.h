@@ -445,6 +445,125 @@ moe_status moe_attention(const moe_attn_config *cfg, const moe_kv_cache *cache, 
                          const void *q, int64_t q_ld, float softmax_scale, int causal, int window, void *out,
                          int64_t out_ld, float *lse, void *ws, size_t ws_bytes, void *stream);
 
+/* ---- a recurrent token mixer: linear attention over a state, the heads' norm, products ----
+ *
+ * What a decoder layer without a key/value cache runs in place of the attention above ("AIMA AMD395 Qwen3.6
+ * 35B Linux Engine", the HTTP prompt-length paragraph: the engine's model carries a recurrent state from piece to
+ * piece of a prompt; the page gives no formula, so the readings are this library's).  The conventions of the
+ * calls above hold: activations in bf16 or fp16, rows that may lie apart, a status word at the begin of the workspace. */
+
+/* Heads.  Key head j serves the value heads j*G .. j*G+G-1, G = value_heads / key_heads. */
+typedef struct {
+    int key_heads;   /* KH */
+    int value_heads; /* VH, a multiple of KH, at most 1024 */
+    int key_dim;     /* DK: 64 or 128 */
+    int value_dim;   /* DV: 64, 128 or 256 */
+    int dtype;       /* moe_dtype of q, k, v and out */
+} moe_linear_config;
+
+/* The sequences' states, each [VH, DK, DV] in fp32: 16-byte aligned. */
+typedef struct {
+    float *states; /* [n_slots, VH, DK, DV] */
+    int n_slots;
+} moe_state_pool;
+
+/* A batch of sequences.  Sequence b's new tokens are rows q_start[b] .. q_start[b+1]-1 of q, k and v; with n of
+ * them they have positions kv_len[b] - n .. kv_len[b] - 1, as in moe_kv_batch. */
+typedef struct {
+    int n_seqs;             /* B >= 0, at most 65536 */
+    int n_tokens;           /* T = q_start[B], at most 2^22 */
+    const int32_t *q_start; /* [B+1], q_start[0] = 0, not descending */
+    const int32_t *kv_len;  /* [B] tokens of the sequence so far, this batch's included */
+    const int32_t *slots;   /* [B] where its state lies in the pool */
+} moe_state_batch;
+
+/* Bytes of workspace for moe_linear_attention on batches of up to max_seqs sequences and max_tokens new
+ * tokens.  0 for an invalid or unsupported config.  256-byte aligned; zero its first 256 bytes once after
+ * allocating (the status word).  The rest is scratch.  Calls that overlap must not share one. */
+size_t moe_linear_workspace_size(const moe_linear_config *cfg, int max_seqs, int max_tokens);
+
+/* Linear attention with a decay for each value head.  Token by token, for every value head h and its key head j:
+ *   S   = e^g S + k v^T          S [DK, DV] the sequence's state, g the token's log decay
+ *   out = scale * S^T q
+ * A sequence whose first new token has position 0 (kv_len = n) begins with S = 0, whatever its slot holds; any other
+ * begins with its slot's state.  The state after its last new token is written to the slot.  A sequence without new
+ * tokens leaves its slot alone.  Tokens at negative positions (padding in front) do not count, and get out rows of 0.
+ * Rows from q_start[B] on stay untouched.
+ * q, k [T, KH, DK], v, out [T, VH, DV], row strides q_ld, k_ld, v_ld, out_ld.  decay fp32, g <= 0: [T, VH] with row
+ * stride decay_ld >= VH, or with decay_ld = 0 one value a head, [VH]; NULL: g = 0.  g = -infinity forgets the
+ * state; below -10,000 a decay counts as that (its factor is 0 either way).
+ * States and sums are fp32.  Long runs are computed chunk by chunk on tensor cores, with decays, weighted values,
+ * states and products of queries and keys as sums of two or three 16-bit values (at least 16 bits, states 22); out is
+ * rounded once.  Deterministic, but a run's length decides which kernel takes it, so the last bits of a
+ * state depend on how a prompt is cut.  A value of v that is not finite makes its channel not finite from its token on.
+ * Reported as MOE_ERR_INVALID_ARG in the status word: a slot outside [0, n_slots) (the sequence begins with S = 0
+ * and its state is not kept); a range of rows outside the batch (no tokens); a decay above 0 or NaN (taken as 0).
+ * Two sequences of a call must not have the same slot.  out must not overlap q, k, v or decay. */
+moe_status moe_linear_attention(const moe_linear_config *cfg, const moe_state_pool *pool, const moe_state_batch *batch,
+                                const void *q, int64_t q_ld, const void *k, int64_t k_ld, const void *v, int64_t v_ld,
+                                const float *decay, int64_t decay_ld, float scale, void *out, int64_t out_ld, void *ws,
+                                size_t ws_bytes, void *stream);
+
+typedef enum {
+    MOE_HEAD_GATE_NONE = 0,
+    MOE_HEAD_GATE_SIGMOID = 1, /* 1 / (1 + e^-gate) */
+    MOE_HEAD_GATE_SILU = 2     /* gate / (1 + e^-gate) */
+} moe_head_gate;
+
+typedef struct {
+    int heads;       /* >= 1; heads * dim at most 65536 */
+    int dim;         /* D, a multiple of 8, at most 1024 */
+    int dtype;       /* moe_dtype of every tensor of the call */
+    int center;      /* 1: the head's mean is taken off first */
+    int gate;        /* moe_head_gate */
+    int weight_each; /* 0: one weight [D] for all heads; 1: [heads, D] */
+    int unit_offset; /* 1: the weights are stored as w - 1 */
+    float eps;       /* added to the mean square, >= 0 */
+} moe_head_norm_config;
+
+/* The norm of each head of each row, with its weight and gate, in fp32, rounded once:
+ *   y = (x - m) * w / sqrt(mean((x - m)^2) + eps) * act(gate),  m = mean(x) with center, else 0
+ * x, gate, y [T, heads, D], row strides x_ld, gate_ld, y_ld in elements (multiples of 8, at least heads * D); y may be
+ * x or gate.  weight may be NULL (1); gate is NULL with MOE_HEAD_GATE_NONE only.  16-byte aligned.  No
+ * workspace; deterministic. */
+moe_status moe_head_norm(const moe_head_norm_config *cfg, const void *x, int64_t x_ld, const void *weight,
+                         const void *gate, int64_t gate_ld, void *y, int64_t y_ld, int T, void *stream);
+
+typedef enum {
+    MOE_ACT_NONE = 0,
+    MOE_ACT_RELU = 1,
+    MOE_ACT_GELU = 2, /* z (1 + erf(z / sqrt(2))) / 2 */
+    MOE_ACT_SILU = 3,
+    MOE_ACT_SIGMOID = 4,
+    MOE_ACT_LOG_SIGMOID = 5 /* -log(1 + e^-z): a log decay */
+} moe_act;
+
+typedef struct {
+    int inputs;  /* K, a multiple of 8, at most 65536 */
+    int outputs; /* N, a multiple of 8, at most 2^20 */
+    int dtype;   /* moe_dtype of x, w and bias */
+    int out_f32; /* 1: y and resid are fp32, 0: of dtype */
+    int act;     /* moe_act */
+    float scale; /* alpha */
+} moe_project_config;
+
+typedef struct {
+    const void *x;     /* [T,K] */
+    const void *w;     /* [N,K] */
+    const void *bias;  /* [N] or NULL */
+    const void *resid; /* [T,N] or NULL; may be y */
+    void *y;           /* [T,N] */
+    int64_t x_ld, w_ld, resid_ld, y_ld; /* row strides in elements, multiples of 8 */
+} moe_project_io;
+
+/* Bytes of workspace for moe_project on up to max_T rows, as above (status word, then scratch). */
+size_t moe_project_workspace_size(const moe_project_config *cfg, int max_T);
+
+/* y = resid + alpha * act(x w^T + bias): 16-bit products, sums and epilogue in fp32, rounded once.
+ * Deterministic.  T of 0 does nothing.  y must not overlap x or w. */
+moe_status moe_project(const moe_project_config *cfg, const moe_project_io *io, int T, void *ws, size_t ws_bytes,
+                       void *stream);
+
 /* Reads and clears the device status word in `ws` (synchronises `stream`).  *device_status
  * receives MOE_OK or the first error recorded by a kernel (MOE_ERR_TIMEOUT for a wait that
  * ran out, MOE_ERR_INVALID_ARG for an out-of-range expert id).  Returns MOE_ERR_CUDA if the

@@ -28,7 +28,8 @@ EXPORTS = ["moe_status_string", "moe_workspace_size", "moe_route", "moe_route_fr
            "moe_decode_chain_q8", "moe_quantize_e4m3", "moe_graph_create", "moe_graph_launch",
            "moe_graph_kernel_count", "moe_graph_destroy", "moe_forward_q8", "moe_debug_build",
            "moe_decode_chain_q4", "moe_quantize_q4", "moe_block_norm", "moe_attn_workspace_size",
-           "moe_kv_append", "moe_attention"]
+           "moe_kv_append", "moe_attention", "moe_linear_workspace_size", "moe_linear_attention", "moe_head_norm",
+           "moe_project_workspace_size", "moe_project"]
 
 
 class MoeError(RuntimeError):
@@ -84,6 +85,33 @@ class _KVBatch(ctypes.Structure):
                 ("q_start", ctypes.c_void_p), ("kv_len", ctypes.c_void_p), ("page_table", ctypes.c_void_p)]
 
 
+class LinearConfig(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int) for n in ("key_heads", "value_heads", "key_dim", "value_dim", "dtype")]
+
+
+class _StatePool(ctypes.Structure):
+    _fields_ = [("states", ctypes.c_void_p), ("n_slots", ctypes.c_int)]
+
+
+class _StateBatch(ctypes.Structure):
+    _fields_ = [("n_seqs", ctypes.c_int), ("n_tokens", ctypes.c_int), ("q_start", ctypes.c_void_p), ("kv_len", ctypes.c_void_p),
+                ("slots", ctypes.c_void_p)]
+
+
+class HeadNormConfig(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int) for n in ("heads", "dim", "dtype", "center", "gate", "weight_each", "unit_offset")] + \
+               [("eps", ctypes.c_float)]
+
+
+class ProjectConfig(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int) for n in ("inputs", "outputs", "dtype", "out_f32", "act")] + [("scale", ctypes.c_float)]
+
+
+class ProjectIO(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("x", "w", "bias", "resid", "y")] + \
+               [(n, ctypes.c_int64) for n in ("x_ld", "w_ld", "resid_ld", "y_ld")]
+
+
 _P = ctypes.c_void_p
 _I = ctypes.c_int
 _I64 = ctypes.c_int64
@@ -124,6 +152,15 @@ def load(path: str = LIB_PATH):
     L.moe_attn_workspace_size.restype = _SZ
     L.moe_kv_append.argtypes = [A, KC, KB, _P, _I64, _P, _I64, _P, _I64, _P, _I, _P, _I64, _P, _SZ, _P]
     L.moe_attention.argtypes = [A, KC, KB, _P, _I64, ctypes.c_float, _I, _I, _P, _I64, _P, _P, _SZ, _P]
+    LC, HC, PC = ctypes.POINTER(LinearConfig), ctypes.POINTER(HeadNormConfig), ctypes.POINTER(ProjectConfig)
+    L.moe_linear_workspace_size.argtypes = [LC, _I, _I]
+    L.moe_linear_workspace_size.restype = _SZ
+    L.moe_linear_attention.argtypes = [LC, ctypes.POINTER(_StatePool), ctypes.POINTER(_StateBatch), _P, _I64, _P, _I64, _P, _I64, _P,
+                                       _I64, ctypes.c_float, _P, _I64, _P, _SZ, _P]
+    L.moe_head_norm.argtypes = [HC, _P, _I64, _P, _P, _I64, _P, _I64, _I, _P]
+    L.moe_project_workspace_size.argtypes = [PC, _I]
+    L.moe_project_workspace_size.restype = _SZ
+    L.moe_project.argtypes = [PC, ctypes.POINTER(ProjectIO), _I, _P, _SZ, _P]
     L.moe_check_status.argtypes = [_P, _SZ, ctypes.POINTER(_I), _P]
     L.moe_selftest_wait.argtypes = [_P, _SZ, ctypes.c_ulonglong, _I, _P]
     L.moe_graph_create.argtypes = [C, W, _I, _I, _P, _P, _P, _P, _P, _P, _SZ, _P, ctypes.POINTER(_P)]
@@ -147,7 +184,7 @@ def load(path: str = LIB_PATH):
                "moe_timing_read", "moe_timing_classes", "moe_selftest_wait", "moe_decode_chain",
                "moe_decode_chain_q8", "moe_quantize_e4m3", "moe_graph_create", "moe_graph_launch",
                "moe_graph_destroy", "moe_forward_q8", "moe_decode_chain_q4", "moe_quantize_q4", "moe_block_norm",
-               "moe_kv_append", "moe_attention"):
+               "moe_kv_append", "moe_attention", "moe_linear_attention", "moe_head_norm", "moe_project"):
         getattr(L, fn).restype = _I
     _lib = L
     return L
@@ -572,6 +609,137 @@ def moe_attention(cfg: AttnConfig, cache: KVCache, batch: KVBatch, q, out, ws, l
         _rows(out, "out", qw, dt, T), lse_p, _device_array(ws, "ws", torch.uint8), ws.numel(),
         _raw_stream(stream, q.device.index))
     _check("moe_attention", st)
+
+
+# ------------------------------------------------ the recurrent token mixer (include/moe.h) --
+
+_HEAD_GATES = {"none": 0, "sigmoid": 1, "silu": 2}
+_ACTS = {"none": 0, "relu": 1, "gelu": 2, "silu": 3, "sigmoid": 4, "log_sigmoid": 5}
+
+
+def linear_config(key_heads, value_heads, key_dim, value_dim, dtype=torch.bfloat16) -> LinearConfig:
+    return LinearConfig(int(key_heads), int(value_heads), int(key_dim), int(value_dim), _DTYPES[dtype])
+
+
+class StatePool:
+    """The sequences' states (moe_state_pool): fp32 [n_slots, value_heads, key_dim, value_dim].  Keeps the tensor
+    alive."""
+
+    def __init__(self, cfg: LinearConfig, states):
+        self.layout = (cfg.value_heads, cfg.key_dim, cfg.value_dim)
+        self.c = _StatePool(_device_array(states, "states", torch.float32, (states.shape[0],) + self.layout), states.shape[0])
+        self.states = states
+
+    def check(self, cfg: LinearConfig):
+        """A call of another layout would read and write past the states."""
+        if (cfg.value_heads, cfg.key_dim, cfg.value_dim) != self.layout:
+            raise ValueError("the pool has (value_heads, key_dim, value_dim) %s, the config %s" %
+                             (self.layout, (cfg.value_heads, cfg.key_dim, cfg.value_dim)))
+
+    @classmethod
+    def alloc(cls, cfg: LinearConfig, n_slots, device="cuda"):
+        return cls(cfg, torch.zeros(int(n_slots), cfg.value_heads, cfg.key_dim, cfg.value_dim, dtype=torch.float32, device=device))
+
+
+class StateBatch:
+    """A batch of sequences (moe_state_batch): q_start int32 [B + 1], kv_len and slots int32 [B], all on the device;
+    their contents may change between calls, n_tokens may not."""
+
+    def __init__(self, q_start, kv_len, slots, n_tokens):
+        B = kv_len.shape[0]
+        self.c = _StateBatch(B, int(n_tokens), _device_array(q_start, "q_start", torch.int32, (B + 1,)),
+                             _device_array(kv_len, "kv_len", torch.int32, (B,)), _device_array(slots, "slots", torch.int32, (B,)))
+        self.q_start, self.kv_len, self.slots = q_start, kv_len, slots
+        self.n_tokens = int(n_tokens)
+
+
+def linear_workspace_size(cfg: LinearConfig, max_seqs, max_tokens) -> int:
+    return int(lib().moe_linear_workspace_size(ctypes.byref(cfg), int(max_seqs), int(max_tokens)))
+
+
+def alloc_linear_workspace(cfg: LinearConfig, max_seqs, max_tokens, device="cuda") -> torch.Tensor:
+    n = linear_workspace_size(cfg, max_seqs, max_tokens)
+    if n == 0:
+        raise MoeError("moe_linear_workspace_size", 3)
+    # zeroed once: the first 256 bytes are the device status word
+    return torch.zeros(n, dtype=torch.uint8, device=device)
+
+
+def moe_linear_attention(cfg: LinearConfig, pool: StatePool, batch: StateBatch, q, k, v, decay, out, ws, scale=None, stream=None):
+    """S = e^g S + k v^T, out = scale S^T q for the batch's tokens: q, k [T, key_heads, key_dim], v, out [T, value_heads,
+    value_dim] (or [T, heads * dim]); decay fp32 g <= 0, [T, value_heads] or [value_heads], None: 0.  scale None:
+    1 / sqrt(key_dim)."""
+    pool.check(cfg)
+    T, VH, dt = batch.n_tokens, cfg.value_heads, _TORCH_DTYPES[cfg.dtype]
+    kw, vw = cfg.key_heads * cfg.key_dim, VH * cfg.value_dim
+    g_p, g_ld = None, 0
+    if decay is not None:
+        g_p = decay.data_ptr()
+        if decay.dim() == 2:
+            g_ld = _rows(decay, "decay", VH, torch.float32, T)
+        else:
+            _vector(decay, "decay", VH, torch.float32)
+    st = lib().moe_linear_attention(
+        cfg, pool.c, batch.c, q.data_ptr(), _rows(q, "q", kw, dt, T), k.data_ptr(), _rows(k, "k", kw, dt, T), v.data_ptr(),
+        _rows(v, "v", vw, dt, T), g_p, g_ld, cfg.key_dim ** -0.5 if scale is None else scale, out.data_ptr(),
+        _rows(out, "out", vw, dt, T), _device_array(ws, "ws", torch.uint8), ws.numel(), _raw_stream(stream, q.device.index))
+    _check("moe_linear_attention", st)
+
+
+def head_norm_config(heads, dim, dtype=torch.bfloat16, center=False, gate="none", unit_offset=False, eps=1e-6) -> HeadNormConfig:
+    return HeadNormConfig(int(heads), int(dim), _DTYPES[dtype], int(center), _HEAD_GATES[gate], 0, int(unit_offset), eps)
+
+
+def moe_head_norm(cfg: HeadNormConfig, x, y, weight=None, gate=None, stream=None):
+    """y = norm of each head of x, times weight and act(gate): x, gate, y [T, heads, dim] or [T, heads * dim]; weight [dim]
+    for all heads, [heads, dim] or None."""
+    width, dt, T = cfg.heads * cfg.dim, _TORCH_DTYPES[cfg.dtype], x.shape[0]
+    w_p = g_p = None
+    g_ld = 0
+    if weight is not None:
+        each = 1 if weight.dim() == 2 else 0
+        w_p = _vector(weight, "weight", width if each else cfg.dim, dt)
+        if each != cfg.weight_each:
+            cfg = HeadNormConfig(cfg.heads, cfg.dim, cfg.dtype, cfg.center, cfg.gate, each, cfg.unit_offset, cfg.eps)
+    if gate is not None:
+        g_p, g_ld = gate.data_ptr(), _rows(gate, "gate", width, dt, T)
+    st = lib().moe_head_norm(cfg, x.data_ptr(), _rows(x, "x", width, dt, T), w_p, g_p, g_ld, y.data_ptr(),
+                             _rows(y, "y", width, dt, T), T, _raw_stream(stream, x.device.index))
+    _check("moe_head_norm", st)
+
+
+def project_config(inputs, outputs, dtype=torch.bfloat16, out_dtype=None, act="none", scale=1.0) -> ProjectConfig:
+    """out_dtype: dtype (None) or torch.float32, of y and resid."""
+    if out_dtype not in (None, dtype, torch.float32):
+        raise ValueError("out_dtype %s is neither %s nor torch.float32" % (out_dtype, dtype))
+    return ProjectConfig(int(inputs), int(outputs), _DTYPES[dtype], int(out_dtype is torch.float32), _ACTS[act], scale)
+
+
+def project_workspace_size(cfg: ProjectConfig, max_T) -> int:
+    return int(lib().moe_project_workspace_size(ctypes.byref(cfg), int(max_T)))
+
+
+def alloc_project_workspace(cfg: ProjectConfig, max_T, device="cuda") -> torch.Tensor:
+    n = project_workspace_size(cfg, max_T)
+    if n == 0:
+        raise MoeError("moe_project_workspace_size", 3)
+    # zeroed once: the first 256 bytes are the device status word
+    return torch.zeros(n, dtype=torch.uint8, device=device)
+
+
+def moe_project(cfg: ProjectConfig, x, w, y, ws, bias=None, resid=None, stream=None):
+    """y = resid + scale * act(x w^T + bias): x [T, inputs], w [outputs, inputs], bias [outputs] or None, resid and y
+    [T, outputs]."""
+    K, N, dt, T = cfg.inputs, cfg.outputs, _TORCH_DTYPES[cfg.dtype], x.shape[0]
+    ot = torch.float32 if cfg.out_f32 else dt
+    io = ProjectIO(x.data_ptr(), w.data_ptr(), None, None, y.data_ptr(), _rows(x, "x", K, dt, T), _rows(w, "w", K, dt, N), 0,
+                   _rows(y, "y", N, ot, T))
+    if bias is not None:
+        io.bias = _vector(bias, "bias", N, dt)
+    if resid is not None:
+        io.resid, io.resid_ld = resid.data_ptr(), _rows(resid, "resid", N, ot, T)
+    st = lib().moe_project(cfg, io, T, _device_array(ws, "ws", torch.uint8), ws.numel(), _raw_stream(stream, x.device.index))
+    _check("moe_project", st)
 
 
 def moe_forward_status(cfg, w: Weights, x, T, out, x_next, ws, stream=None, resid=None) -> int:

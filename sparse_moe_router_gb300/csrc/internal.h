@@ -32,6 +32,9 @@ enum KernelClass {
     KC_ATTN_SPLIT,        // attention over the cache, split along the keys (decode)
     KC_ATTN_JOIN,         // the split parts of a sequence joined
     KC_ATTN_PROMPT,       // attention over the cache on the 5th-generation tensor cores (prompts)
+    KC_LINEAR_TOKENS,     // linear attention, token by token
+    KC_HEAD_NORM,         // the heads' norm with its gate
+    KC_PROJECT_ROWS,      // a product with its epilogue, few rows
     KC_COUNT
 };
 

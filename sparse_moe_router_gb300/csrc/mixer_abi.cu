@@ -1,0 +1,191 @@
+// mixer_abi.cu -- the extern "C" entry points of the recurrent token mixer (include/moe.h): argument checks,
+// workspace carving, launches.
+#include <climits>
+#include <cmath>
+
+#include <nvtx3/nvToolsExt.h>
+
+#include "mixer.h"
+
+namespace moe {
+namespace {
+
+struct NvtxRange {
+    explicit NvtxRange(const char *name) { nvtxRangePushA(name); }
+    ~NvtxRange() { nvtxRangePop(); }
+};
+
+bool aligned(const void *p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+bool good_dtype(int d) { return d == MOE_DTYPE_BF16 || d == MOE_DTYPE_F16; }
+
+#define MOE_TRY(expr)                  \
+    do {                               \
+        moe_status _st = (expr);       \
+        if (_st != MOE_OK) return _st; \
+    } while (0)
+#define MOE_CUDA(expr) MOE_TRY((expr) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA)
+
+// A row of `width` values read or written in 16-byte pieces.
+bool good_rows(const void *p, int64_t ld, int64_t width) { return p && aligned(p, 16) && ld >= width && ld % 8 == 0; }
+
+// Limits on a batch's size: they keep counts of rows inside 32 bits.
+constexpr int kMaxSeqs = 65536;
+constexpr int kMaxTokens = 1 << 22;
+
+moe_status check_linear_config(const moe_linear_config *c) {
+    if (!c || c->key_heads <= 0 || c->value_heads <= 0 || !good_dtype(c->dtype)) return MOE_ERR_INVALID_ARG;
+    if (c->value_heads % c->key_heads) return MOE_ERR_INVALID_ARG;
+    if (c->value_heads > 1024) return MOE_ERR_UNSUPPORTED_SHAPE;
+    if (c->key_dim != 64 && c->key_dim != 128) return MOE_ERR_UNSUPPORTED_SHAPE;
+    if (c->value_dim != 64 && c->value_dim != 128 && c->value_dim != 256) return MOE_ERR_UNSUPPORTED_SHAPE;
+    return MOE_OK;
+}
+
+size_t linear_workspace(const moe_linear_config &, int, int) { return 256; }
+
+moe_status check_project_config(const moe_project_config *c) {
+    if (!c || c->inputs <= 0 || c->outputs <= 0 || !good_dtype(c->dtype)) return MOE_ERR_INVALID_ARG;
+    if (c->out_f32 != 0 && c->out_f32 != 1) return MOE_ERR_INVALID_ARG;
+    if (c->act < MOE_ACT_NONE || c->act > MOE_ACT_LOG_SIGMOID || !std::isfinite(c->scale)) return MOE_ERR_INVALID_ARG;
+    if (c->inputs % 8 || c->outputs % 8 || c->inputs > 65536 || c->outputs > 1 << 20) return MOE_ERR_UNSUPPORTED_SHAPE;
+    return MOE_OK;
+}
+
+size_t project_workspace(const moe_project_config &, int) { return 256; }
+
+moe_status check_ws(const void *ws, size_t bytes, size_t need) {
+    if (!ws || !aligned(ws, 256)) return MOE_ERR_INVALID_ARG;
+    return bytes < need ? MOE_ERR_WORKSPACE_TOO_SMALL : MOE_OK;
+}
+
+}  // namespace
+}  // namespace moe
+
+using namespace moe;
+
+extern "C" {
+
+size_t moe_linear_workspace_size(const moe_linear_config *cfg, int max_seqs, int max_tokens) {
+    if (check_linear_config(cfg) != MOE_OK || max_seqs < 0 || max_tokens < 0) return 0;
+    if (max_seqs > kMaxSeqs || max_tokens > kMaxTokens) return 0;
+    return linear_workspace(*cfg, max_seqs, max_tokens);
+}
+
+moe_status moe_linear_attention(const moe_linear_config *cfg, const moe_state_pool *pool, const moe_state_batch *batch,
+                                const void *q, int64_t q_ld, const void *k, int64_t k_ld, const void *v, int64_t v_ld,
+                                const float *decay, int64_t decay_ld, float scale, void *out, int64_t out_ld, void *ws,
+                                size_t ws_bytes, void *stream) {
+    NvtxRange nvtx_range("moe_linear_attention");
+    MOE_TRY(check_linear_config(cfg));
+    const moe_linear_config &c = *cfg;
+    if (!pool || !batch || batch->n_seqs < 0 || batch->n_tokens < 0 || pool->n_slots < 0) return MOE_ERR_INVALID_ARG;
+    if (batch->n_seqs == 0 && batch->n_tokens > 0) return MOE_ERR_INVALID_ARG;
+    if (batch->n_seqs > kMaxSeqs || batch->n_tokens > kMaxTokens) return MOE_ERR_UNSUPPORTED_SHAPE;
+    if (!std::isfinite(scale)) return MOE_ERR_INVALID_ARG;
+    if (batch->n_tokens == 0) return MOE_OK;
+    if (!batch->q_start || !batch->kv_len || !batch->slots) return MOE_ERR_INVALID_ARG;
+    if (pool->n_slots < 1 || !pool->states || !aligned(pool->states, 16)) return MOE_ERR_INVALID_ARG;
+    const int64_t kw = (int64_t)c.key_heads * c.key_dim, vw = (int64_t)c.value_heads * c.value_dim;
+    if (!good_rows(q, q_ld, kw) || !good_rows(k, k_ld, kw) || !good_rows(v, v_ld, vw) || !good_rows(out, out_ld, vw))
+        return MOE_ERR_INVALID_ARG;
+    if (decay && (!aligned(decay, 4) || (decay_ld != 0 && decay_ld < c.value_heads))) return MOE_ERR_INVALID_ARG;
+    MOE_TRY(check_ws(ws, ws_bytes, linear_workspace(c, batch->n_seqs, batch->n_tokens)));
+    LinearArgs a{};
+    a.q_start = batch->q_start;
+    a.kv_len = batch->kv_len;
+    a.slots = batch->slots;
+    a.states = pool->states;
+    a.q = static_cast<const uint16_t *>(q);
+    a.k = static_cast<const uint16_t *>(k);
+    a.v = static_cast<const uint16_t *>(v);
+    a.decay = decay;
+    a.out = static_cast<uint16_t *>(out);
+    a.q_ld = q_ld;
+    a.k_ld = k_ld;
+    a.v_ld = v_ld;
+    a.out_ld = out_ld;
+    a.decay_ld = decay_ld;
+    a.n_seqs = batch->n_seqs;
+    a.n_tokens = batch->n_tokens;
+    a.n_slots = pool->n_slots;
+    a.KH = c.key_heads;
+    a.VH = c.value_heads;
+    a.G = c.value_heads / c.key_heads;
+    a.DK = c.key_dim;
+    a.DV = c.value_dim;
+    a.scale = scale;
+    a.status = static_cast<int *>(ws);
+    MOE_CUDA(launch_linear_tokens(a, c.dtype, static_cast<cudaStream_t>(stream)));
+    return MOE_OK;
+}
+
+moe_status moe_head_norm(const moe_head_norm_config *cfg, const void *x, int64_t x_ld, const void *weight,
+                         const void *gate, int64_t gate_ld, void *y, int64_t y_ld, int T, void *stream) {
+    NvtxRange nvtx_range("moe_head_norm");
+    if (!cfg || T < 0 || cfg->heads <= 0 || cfg->dim <= 0 || !good_dtype(cfg->dtype)) return MOE_ERR_INVALID_ARG;
+    if (cfg->gate < MOE_HEAD_GATE_NONE || cfg->gate > MOE_HEAD_GATE_SILU) return MOE_ERR_INVALID_ARG;
+    if (!(cfg->eps >= 0.f) || !std::isfinite(cfg->eps)) return MOE_ERR_INVALID_ARG;
+    if (cfg->dim % 8 || cfg->dim > 1024 || (int64_t)cfg->heads * cfg->dim > 65536) return MOE_ERR_UNSUPPORTED_SHAPE;
+    if (T == 0) return MOE_OK;
+    const int64_t width = (int64_t)cfg->heads * cfg->dim;
+    if (!good_rows(x, x_ld, width) || !good_rows(y, y_ld, width) || !aligned(weight, 16)) return MOE_ERR_INVALID_ARG;
+    if ((cfg->gate == MOE_HEAD_GATE_NONE) != (gate == nullptr)) return MOE_ERR_INVALID_ARG;
+    if (gate && !good_rows(gate, gate_ld, width)) return MOE_ERR_INVALID_ARG;
+    HeadNormArgs a{};
+    a.x = static_cast<const uint16_t *>(x);
+    a.weight = static_cast<const uint16_t *>(weight);
+    a.gate = static_cast<const uint16_t *>(gate);
+    a.y = static_cast<uint16_t *>(y);
+    a.x_ld = x_ld;
+    a.gate_ld = gate_ld;
+    a.y_ld = y_ld;
+    a.T = T;
+    a.heads = cfg->heads;
+    a.dim = cfg->dim;
+    a.center = cfg->center;
+    a.gate_kind = cfg->gate;
+    a.weight_each = cfg->weight_each;
+    a.unit_offset = cfg->unit_offset;
+    a.eps = cfg->eps;
+    MOE_CUDA(launch_head_norm(a, cfg->dtype, static_cast<cudaStream_t>(stream)));
+    return MOE_OK;
+}
+
+size_t moe_project_workspace_size(const moe_project_config *cfg, int max_T) {
+    if (check_project_config(cfg) != MOE_OK || max_T < 0) return 0;
+    return project_workspace(*cfg, max_T);
+}
+
+moe_status moe_project(const moe_project_config *cfg, const moe_project_io *io, int T, void *ws, size_t ws_bytes,
+                       void *stream) {
+    NvtxRange nvtx_range("moe_project");
+    MOE_TRY(check_project_config(cfg));
+    const moe_project_config &c = *cfg;
+    if (T < 0) return MOE_ERR_INVALID_ARG;
+    if (T == 0) return MOE_OK;
+    if (!io || !good_rows(io->x, io->x_ld, c.inputs) || !good_rows(io->w, io->w_ld, c.inputs)) return MOE_ERR_INVALID_ARG;
+    if (!good_rows(io->y, io->y_ld, c.outputs) || !aligned(io->bias, 16)) return MOE_ERR_INVALID_ARG;
+    if (io->resid && !good_rows(io->resid, io->resid_ld, c.outputs)) return MOE_ERR_INVALID_ARG;
+    MOE_TRY(check_ws(ws, ws_bytes, project_workspace(c, T)));
+    ProjectArgs a{};
+    a.x = static_cast<const uint16_t *>(io->x);
+    a.w = static_cast<const uint16_t *>(io->w);
+    a.bias = static_cast<const uint16_t *>(io->bias);
+    a.resid = io->resid;
+    a.y = io->y;
+    a.x_ld = io->x_ld;
+    a.w_ld = io->w_ld;
+    a.resid_ld = io->resid_ld;
+    a.y_ld = io->y_ld;
+    a.T = T;
+    a.K = c.inputs;
+    a.N = c.outputs;
+    a.act = c.act;
+    a.out_f32 = c.out_f32;
+    a.scale = c.scale;
+    a.status = static_cast<int *>(ws);
+    MOE_CUDA(launch_project_rows(a, c.dtype, static_cast<cudaStream_t>(stream)));
+    return MOE_OK;
+}
+
+}  // extern "C"

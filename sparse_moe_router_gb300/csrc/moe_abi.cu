@@ -36,7 +36,8 @@ const char *const kClassNames[KC_COUNT] = {
     "router_gemm", "topk",          "permute",     "tile_prefix",   "gateup_gemm",
     "down_gemm",   "shared_gateup", "shared_down", "finalize",      "combine",
     "zero",        "decode_router", "decode_experts", "gather_x",
-    "decode_chain", "quantize", "block_norm", "kv_append", "attn_split", "attn_join", "attn_prompt"};
+    "decode_chain", "quantize", "block_norm", "kv_append", "attn_split", "attn_join", "attn_prompt",
+    "linear_tokens", "head_norm", "project_rows"};
 }  // namespace
 
 const char *kernel_class_name(int kc) { return (kc >= 0 && kc < KC_COUNT) ? kClassNames[kc] : nullptr; }
