@@ -33,6 +33,8 @@ enum KernelClass {
     KC_ATTN_JOIN,         // the split parts of a sequence joined
     KC_ATTN_PROMPT,       // attention over the cache on the 5th-generation tensor cores (prompts)
     KC_LINEAR_TOKENS,     // linear attention, token by token
+    KC_LINEAR_CHUNKS,     // linear attention in chunks, on the 5th-generation tensor cores
+    KC_LINEAR_STATES,     // the states at the begin of a run's segments
     KC_HEAD_NORM,         // the heads' norm with its gate
     KC_PROJECT_ROWS,      // a product with its epilogue, few rows
     KC_COUNT
@@ -60,6 +62,10 @@ const DeviceInfo &device_info();
 // none: plain row-major boxes).
 bool encode_tmap_2d_bf16(CUtensorMap *map, const void *base, uint64_t rows, uint64_t cols,
                          uint32_t box_rows, uint32_t box_cols, bool swizzle128 = true);
+
+// The same over rows of 16-bit values (either type) that lie `ld` elements apart.
+bool encode_tmap_rows(CUtensorMap *map, const void *base, uint64_t rows, uint64_t cols, uint64_t ld, uint32_t box_rows,
+                      uint32_t box_cols);
 
 // ---- GEMM (tcgen05, swap-AB: weight rows on M, tokens on N) ---------------------------
 

@@ -20,6 +20,7 @@ __global__ void __launch_bounds__(kThreads) linear_tokens_kernel(const __grid_co
     const int tiles = p.DV / kCols, b = (int)blockIdx.x / tiles, h = (int)blockIdx.y;
     const int col0 = ((int)blockIdx.x - b * tiles) * kCols, col = col0 + c * 4;
     const Run run = load_run(p, b);
+    if (run.n >= p.chunk_tokens) return;  // the chunk kernel's
     for (int i = tid; i < run.pad * kCols; i += kThreads)
         p.out[(int64_t)(run.q0 - run.pad + i / kCols) * p.out_ld + (int64_t)h * p.DV + col0 + i % kCols] = 0;
     if (run.n <= 0) return;

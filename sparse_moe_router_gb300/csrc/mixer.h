@@ -17,7 +17,18 @@ struct LinearArgs {
     int KH, VH, G, DK, DV;
     float scale;
     int *status;
+    // sequences with at least this many new tokens are the chunk kernel's, the others the token kernel's
+    int chunk_tokens;
+    // chunk kernel: a run's chunks in segments of so many; with several, the state that each adds and its decay
+    int segment_chunks;
+    float *seg_states, *seg_decay;
 };
+constexpr int kChunk = 64;  // tokens a chunk
+// Segments of a batch, at most (sequence b owns the places base(b) .. base(b+1)-1, base(b) = q_start[b] / tokens + b).
+inline int64_t linear_segments(int64_t n_tokens, int64_t n_seqs, int64_t segment_chunks) {
+    return n_tokens / (segment_chunks * kChunk) + n_seqs;
+}
+cudaError_t launch_linear_chunks(const LinearArgs &a, int dtype, cudaStream_t s);
 cudaError_t launch_linear_tokens(const LinearArgs &a, int dtype, cudaStream_t s);
 
 struct HeadNormArgs {

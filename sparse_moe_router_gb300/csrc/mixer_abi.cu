@@ -41,7 +41,47 @@ moe_status check_linear_config(const moe_linear_config *c) {
     return MOE_OK;
 }
 
-size_t linear_workspace(const moe_linear_config &, int, int) { return 256; }
+// New tokens from which a run is the chunk kernel's.
+constexpr int kChunkTokens = 32;
+// Segments times heads times column tiles that a batch may have when its runs are cut: the states they add are in the workspace.
+constexpr int64_t kMostSegments = 640;
+
+int value_tiles(const moe_linear_config &c) { return c.value_dim > 128 ? 2 : 1; }
+int64_t most_segments(const moe_linear_config &c, int64_t n_seqs, int64_t n_tokens) {
+    const int64_t n = (n_tokens / kChunk + n_seqs) * c.value_heads * value_tiles(c);
+    return n < kMostSegments ? n : kMostSegments;
+}
+struct LinearLayout {
+    size_t decay, states, total;
+};
+LinearLayout linear_layout(const moe_linear_config &c, int n_seqs, int n_tokens) {
+    const size_t n = (size_t)most_segments(c, n_seqs, n_tokens);
+    LinearLayout l;
+    l.decay = 256;  // behind the status word
+    l.states = l.decay + (n * sizeof(float) + 255) / 256 * 256;
+    l.total = l.states + n * c.key_dim * (c.value_dim / value_tiles(c)) * sizeof(float);
+    return l;
+}
+
+// Chunks a segment: as many as end soonest, counted in chunks of the output kernel on every SM; a block's start and end
+// count as 3, a chunk of the first kernel as 2/3.
+int segment_chunks(const moe_linear_config &c, int64_t n_seqs, int64_t n_tokens) {
+    const int sms = device_info().sm_count;
+    const int64_t chunks = (n_tokens + kChunk - 1) / kChunk, per = (int64_t)c.value_heads * value_tiles(c);
+    // a batch's longest run: all of it, or of several three times the mean
+    const int64_t longest = n_seqs == 1 ? chunks : chunks < 3 * chunks / n_seqs + 1 ? chunks : 3 * chunks / n_seqs + 1;
+    auto waves = [&](int64_t blocks) { return (double)((blocks + sms - 1) / sms); };
+    int64_t best = chunks;
+    const double even = (double)chunks * per / sms;
+    double least = fmax((double)longest, even) + 3 * waves(n_seqs * per);
+    for (int64_t l = 2; l < longest; l += l < 32 ? 1 : l / 16) {
+        const int64_t cut = n_seqs == 1 ? (chunks + l - 1) / l : chunks / l + n_seqs;
+        if ((n_tokens / (l * kChunk) + n_seqs) * per > kMostSegments) continue;
+        const double cost = waves(cut * per) * (l + 3) + waves((cut - n_seqs) * per) * (l * 0.67 + 3) + 2;
+        if (cost < least) least = cost, best = l;
+    }
+    return (int)best;
+}
 
 moe_status check_project_config(const moe_project_config *c) {
     if (!c || c->inputs <= 0 || c->outputs <= 0 || !good_dtype(c->dtype)) return MOE_ERR_INVALID_ARG;
@@ -68,7 +108,7 @@ extern "C" {
 size_t moe_linear_workspace_size(const moe_linear_config *cfg, int max_seqs, int max_tokens) {
     if (check_linear_config(cfg) != MOE_OK || max_seqs < 0 || max_tokens < 0) return 0;
     if (max_seqs > kMaxSeqs || max_tokens > kMaxTokens) return 0;
-    return linear_workspace(*cfg, max_seqs, max_tokens);
+    return linear_layout(*cfg, max_seqs, max_tokens).total;
 }
 
 moe_status moe_linear_attention(const moe_linear_config *cfg, const moe_state_pool *pool, const moe_state_batch *batch,
@@ -89,7 +129,7 @@ moe_status moe_linear_attention(const moe_linear_config *cfg, const moe_state_po
     if (!good_rows(q, q_ld, kw) || !good_rows(k, k_ld, kw) || !good_rows(v, v_ld, vw) || !good_rows(out, out_ld, vw))
         return MOE_ERR_INVALID_ARG;
     if (decay && (!aligned(decay, 4) || (decay_ld != 0 && decay_ld < c.value_heads))) return MOE_ERR_INVALID_ARG;
-    MOE_TRY(check_ws(ws, ws_bytes, linear_workspace(c, batch->n_seqs, batch->n_tokens)));
+    MOE_TRY(check_ws(ws, ws_bytes, linear_layout(c, batch->n_seqs, batch->n_tokens).total));
     LinearArgs a{};
     a.q_start = batch->q_start;
     a.kv_len = batch->kv_len;
@@ -115,7 +155,21 @@ moe_status moe_linear_attention(const moe_linear_config *cfg, const moe_state_po
     a.DV = c.value_dim;
     a.scale = scale;
     a.status = static_cast<int *>(ws);
-    MOE_CUDA(launch_linear_tokens(a, c.dtype, static_cast<cudaStream_t>(stream)));
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    // Which runs the chunk kernel takes goes by their own lengths, which only the device knows.  The host leaves a
+    // kernel out that has none for sure, and the chunk kernel in a step of one token a sequence.
+    const bool chunks = batch->n_tokens >= kChunkTokens && batch->n_tokens > batch->n_seqs;
+    a.chunk_tokens = !chunks ? INT_MAX : batch->n_seqs == 1 ? 0 : kChunkTokens;
+    if (chunks) {
+        a.segment_chunks = segment_chunks(c, batch->n_seqs, batch->n_tokens);
+        const LinearLayout l = linear_layout(c, batch->n_seqs, batch->n_tokens);
+        if ((int64_t)a.segment_chunks * kChunk < batch->n_tokens) {
+            a.seg_decay = reinterpret_cast<float *>(static_cast<char *>(ws) + l.decay);
+            a.seg_states = reinterpret_cast<float *>(static_cast<char *>(ws) + l.states);
+        }
+        MOE_CUDA(launch_linear_chunks(a, c.dtype, s));
+    }
+    if (!chunks || batch->n_seqs > 1) MOE_CUDA(launch_linear_tokens(a, c.dtype, s));
     return MOE_OK;
 }
 

@@ -375,5 +375,21 @@ __device__ __forceinline__ uint32_t idesc_f16_f32(uint32_t M, uint32_t N, bool b
     return (1u << 4) | (b_mn ? 1u << 16 : 0u) | ((N >> 3) << 17) | ((M >> 4) << 24);
 }
 
+// Instruction descriptor for kind::f16 with fp32 D and either 16-bit type (format 0: fp16, 1: bf16, of A at [7,10) and of B
+// at [10,13)); a_mn, b_mn: that operand is MN-major (bits 15 and 16).
+__device__ __forceinline__ uint32_t idesc_16_f32(bool f16, uint32_t M, uint32_t N, bool a_mn, bool b_mn) {
+    return (1u << 4) | (f16 ? 0u : (1u << 7) | (1u << 10)) | (a_mn ? 1u << 15 : 0u) | (b_mn ? 1u << 16 : 0u) | ((N >> 3) << 17) |
+           ((M >> 4) << 24);
+}
+
+template <int R>
+__device__ __forceinline__ void regs_up() {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R));
+}
+template <int R>
+__device__ __forceinline__ void regs_down() {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R));
+}
+
 }  // namespace ptx
 }  // namespace moe
