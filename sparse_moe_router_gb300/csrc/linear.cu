@@ -45,7 +45,7 @@ __global__ void __launch_bounds__(kThreads) linear_tokens_kernel(const __grid_co
         if (tid >= kThreads - DK) qk[buf][1][tid - (kThreads - DK)] = next;
         const int64_t row = run.q0 + t;
         const uint2 vw = *reinterpret_cast<const uint2 *>(p.v + row * p.v_ld + (int64_t)h * p.DV + col);
-        const float f = expf(load_decay(p, row, h));
+        const float f = expf(checked_decay(p, raw_decay(p, row, h)));
         const float2 v0 = unpack2<F16>(vw.x), v1 = unpack2<F16>(vw.y);
         if (t + 1 < run.n) next = load(t + 1);
         __syncthreads();

@@ -26,19 +26,21 @@ namespace {
 
 constexpr int kThreads = 512;
 constexpr int kOutWarp = 4, kValueWarp = 8, kWeightWarp = 12, kLoadWarp = 14, kMmaWarp = 15;
-// Registers a thread: 128 at launch; of a scheduler's 4 x 128 the state's warp, which holds 128 of them, takes 200.
-constexpr int kStateRegs = 200, kOutRegs = 104, kValueRegs = 96, kOtherRegs = 112;
+// Registers a thread: 128 at launch; of a scheduler's 4 x 128 the state's warp, which holds 128 of them, takes 216.
+constexpr int kStateRegs = 216, kOutRegs = 96, kValueRegs = 80, kOtherRegs = 120;
 static_assert(kStateRegs + kOutRegs + kValueRegs + kOtherRegs <= 512, "more registers than the block has");
-constexpr uint64_t kWaitNs = 2000000000ull;  // 2 s: far above any legitimate wait
+constexpr uint64_t kWaitNs = 2000000000ull;  // 2 s, of the waits when a block gives up
 constexpr int kBlockBytes = kChunk * 128;    // 64 tokens x 64 channels
+constexpr int kFetch = 2;                    // chunks beyond the stages that are brought into L2
+constexpr int kTurnRow = 36;                 // words of 32 channels in a transpose buffer, padded for the banks
 constexpr int kSlots = 4;                    // chunks whose decays are in shared memory
 
 // What the warps tell one another of a chunk.
 struct alignas(16) Slot {
-    float g_hi[kChunk], g_lo[kChunk];  // log2 of the decay from the chunk's begin, in two parts
+    float g_hi[kChunk], g_lo[kChunk];  // -log2 of the decay from the chunk's begin, in two parts
     float weight[kChunk];              // e^{G_64 - G_j}
-    float fade[kChunk];                // e^{G_i}
-    float p_unit[kChunk];              // fp16: P's rows hold 1 / p_unit of their values
+    float fade[kChunk];                // scale e^{G_i}
+    float p_unit[kChunk];              // fp16: P's rows hold scale / p_unit of their values
     float s_unit[128];                 // fp16: and S0's channels
     int bad[128];                      // first token whose value is not finite, of each channel
     float whole;                       // e^{G_64}
@@ -49,13 +51,13 @@ struct alignas(16) Slot {
 template <int DK, int DV, bool F16>
 struct Shape {
     static constexpr int kKBlocks = DK / 64, kVBlocks = DV / 64;
-    static constexpr int kQ = 0, kK = kKBlocks * kBlockBytes, kV = 2 * kK;  // offsets in a stage
+    static constexpr int kK = kKBlocks * kBlockBytes, kV = 2 * kK;  // offsets in a stage, of Q 0
     static constexpr int kStageBytes = kV + kVBlocks * kBlockBytes;
     static constexpr int kStages = 3;
     static constexpr int kParts = F16 ? 2 : 3;  // of a weighted value
     static constexpr int kPartBytes = kVBlocks * kBlockBytes;
     static constexpr int kValues = kStages * kStageBytes, kP = kValues + kParts * kPartBytes;
-    static constexpr int kBars = kP + 2 * kBlockBytes, kSlotAt = kBars + 256;
+    static constexpr int kTurn = kP + 2 * kBlockBytes, kBars = kTurn + kVBlocks * 2 * 8 * kTurnRow * 4, kSlotAt = kBars + 320;
     static constexpr int kSmem = 1024 + kSlotAt + kSlots * (int)sizeof(Slot);
     static constexpr int kLaneWarps = DV / 32;  // warps that hold channels
     // TMEM columns: S0 in two parts, U, A, O1, O2
@@ -66,6 +68,10 @@ struct Shape {
     static_assert(kP + 2 * kBlockBytes <= kSmem - 1024, "operands end in shared memory");
 };
 
+template <bool B>
+struct Flag {
+    static constexpr bool value = B;
+};
 struct Maps {
     CUtensorMap q, k, v;
 };
@@ -85,12 +91,27 @@ __device__ __forceinline__ void tie32(uint32_t (&r)[32]) {
 #pragma unroll
     for (int k = 0; k < 32; ++k) asm volatile("" : "+r"(r[k]));
 }
-// (a, b) = hi + lo, both of the 16-bit type.
+__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
+// What a rounding to 16 bits left out of x.
 template <bool F16>
-__device__ __forceinline__ void split2(float a, float b, uint32_t &hi, uint32_t &lo) {
-    hi = pack2<F16>(a, b);
-    const float2 h = unpack2<F16>(hi);
-    lo = pack2<F16>(a - h.x, b - h.y);
+__device__ __forceinline__ float2 rest(float2 x, uint32_t rounded) {
+    return __ffma2_rn(unpack2<F16>(rounded), both(-1.f), x);
+}
+// x = hi + lo, both of the 16-bit type.
+template <bool F16>
+__device__ __forceinline__ void split2(float2 x, uint32_t &hi, uint32_t &lo) {
+    hi = pack2<F16>(x.x, x.y);
+    const float2 r = rest<F16>(x, hi);
+    lo = pack2<F16>(r.x, r.y);
+}
+
+// log2 of a decay in units of 2^-40: sums of 64 of them (2^20 at most) are exact, and 64-bit integers cost a fraction of
+// what 64-bit floats do here.
+constexpr float kFixed = 1.f / (1ull << 40);
+__device__ __forceinline__ int64_t fixed_log2(float g) {
+    constexpr float kHi = 1.44269502f, kLo = 1.92596303e-8f;  // log2(e)
+    const float hi = g * kHi, lo = fmaf(g, kHi, -hi) + g * kLo;
+    return __float2ll_rn(hi * (1.f / kFixed)) + __float2ll_rn(lo * (1.f / kFixed));
 }
 
 // Where sequence b's segments lie among the batch's.
@@ -109,8 +130,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint64_t *g_full = empty + kStages, *g_empty = g_full + kSlots;  // [kSlots] decays
     uint64_t *a_full = g_empty + kSlots, *a_free = a_full + 1;       // A in TMEM; read
     uint64_t *p_full = a_free + 1;                                   // P in shared memory
-    uint64_t *v_full = p_full + 1;                                   // weighted values there
-    uint64_t *u_full = v_full + 1, *u_free = u_full + 1;             // U in TMEM (and the values read); read
+    uint64_t *v_full = p_full + 1, *v_free = v_full + 2;             // [2] weighted values of 32 tokens there; read
+    uint64_t *u_full = v_free + 2, *u_free = u_full + 1;             // U in TMEM; read
     uint64_t *s_full = u_free + 1, *s_free = s_full + 1;             // S0 in TMEM; read by its product
     uint64_t *o_full = s_free + 1, *o_free = o_full + 1;             // O1 and O2 in TMEM (and P read); read
     uint64_t *m_full = o_free + 1;                                   // fp16: the warps' largest weighted values
@@ -157,7 +178,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         ptx::mbar_init(a_full, 1), ptx::mbar_init(a_free, 2);
         ptx::mbar_init(p_full, 2);
-        ptx::mbar_init(v_full, 4);
+        for (int i = 0; i < 2; ++i) ptx::mbar_init(&v_full[i], 4), ptx::mbar_init(&v_free[i], 1);
         // (u_full and o_full: the MMAs' end, and the arrival of the warp that has seen the units of their operands)
         ptx::mbar_init(m_full, 4);
         ptx::mbar_init(u_full, 2), ptx::mbar_init(u_free, C::kLaneWarps);
@@ -173,7 +194,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     ptx::tc_fence_after();
     const uint32_t tmem = *tmem_holder;
     auto wait = [&](uint64_t *bar, int phase) {  // of the whole warp
-        return __all_sync(0xffffffffu, ptx::mbar_wait(bar, phase & 1, kWaitNs, abort_flag)) != 0;
+        return __all_sync(0xffffffffu, ptx::mbar_sleep_wait(bar, phase & 1, abort_flag)) != 0;
     };
     auto arrive = [&](uint64_t *bar) {
         __syncwarp();
@@ -192,58 +213,63 @@ __global__ void __launch_bounds__(kThreads, 1)
             auto place_at = [&](int i) {  // of segment i of this run
                 return p.seg_states + ((int64_t)(base + i) * p.VH + head) * state_size + tile * DV + tid;
             };
-            float S[DK];
+            float2 S[DK / 2];  // channels 2 d and 2 d + 1
+            auto store = [&](float *dst) {
 #pragma unroll
-            for (int d = 0; d < DK; ++d) S[d] = 0.f;
-            if (seg == 0) {
-                // with several segments, whose last writes the slot, the others find the slot's state at the last one's place
-                const float *src = !STATES && segs > 1 ? place_at(segs - 1) : own;
-                if (!run.fresh) {
-#pragma unroll
-                    for (int d = 0; d < DK; ++d) S[d] = src[(int64_t)d * p.DV];
+                for (int d = 0; d < DK / 2; ++d) {
+                    dst[0] = S[d].x;
+                    dst[p.DV] = S[d].y;
+                    dst += 2 * p.DV;
                 }
-                if (STATES && !run.fresh) {
-                    float *dst = place_at(segs - 1);
-#pragma unroll
-                    for (int d = 0; d < DK; ++d) dst[(int64_t)d * p.DV] = S[d];
-                }
-            } else if (!STATES) {
-                for (int i = 0; i < seg; ++i) {
-                    const float *src = place_at(i), f = p.seg_decay[(int64_t)(base + i) * p.VH + head];
-#pragma unroll
-                    for (int d = 0; d < DK; ++d) S[d] = fmaf(S[d], i == 0 ? 0.f : f, src[(int64_t)d * p.DV]);
-                }
-            }
-            const uint32_t lanes = tmem + ((uint32_t)(warp * 32) << 16);
-            auto publish = [&](int c) {  // S0 of chunk c, in two parts
-                float f = 1.f;
-                if (F16) {
-                    float m = 0.f;
-#pragma unroll
-                    for (int d = 0; d < DK; ++d) m = fmaxf(m, fabsf(S[d]));
-                    const int e = lift(m);
-                    f = pow2f(e);
-                    slots[c % kSlots].s_unit[tid] = pow2f(-e);
-                }
-#pragma unroll
-                for (int g = 0; g < DK / 32; ++g) {
-                    uint32_t hi[16], lo[16];
-#pragma unroll
-                    for (int d = 0; d < 16; ++d) split2<F16>(S[g * 32 + 2 * d] * f, S[g * 32 + 2 * d + 1] * f, hi[d], lo[d]);
-                    ptx::tmem_st_16(lanes + C::kColS + g * 16, hi);
-                    ptx::tmem_st_16(lanes + C::kColS + DK / 2 + g * 16, lo);
-                }
-                ptx::tmem_st_wait();
-                ptx::tc_fence_before();
-                arrive(s_full);
             };
-            if (!STATES) {
-                ok = wait(&g_full[0], 0);
-                if (ok) publish(0);
+#pragma unroll
+            for (int d = 0; d < DK / 2; ++d) S[d] = both(0.f);
+            // The first segment begins with the slot's state (of several segments the last writes the slot: the output's
+            // kernel finds the state at the last one's place), the others with what those before them add.
+            const int sources = seg > 0 ? (STATES ? 0 : seg) : run.fresh ? 0 : 1;
+#pragma unroll 1
+            for (int i = 0; i < sources; ++i) {
+                const float *src = seg > 0 ? place_at(i) : !STATES && segs > 1 ? place_at(segs - 1) : own;
+                const float f = i == 0 ? 0.f : p.seg_decay[(int64_t)(base + i) * p.VH + head];
+#pragma unroll
+                for (int d = 0; d < DK / 2; ++d) {
+                    S[d] = __ffma2_rn(S[d], both(f), make_float2(src[0], src[p.DV]));
+                    src += 2 * p.DV;
+                    if (d % 16 == 15) asm volatile("" ::: "memory");  // (no more loads at once than there are registers for)
+                }
             }
-            for (int c = 0; c < chunks && ok; ++c) {
-                const Slot &sl = slots[c % kSlots];
-                if (!(ok = wait(&g_full[c % kSlots], c / kSlots) && wait(u_full, c))) break;
+            if (STATES && seg == 0 && !run.fresh) store(place_at(segs - 1));
+            const uint32_t lanes = tmem + ((uint32_t)(warp * 32) << 16);
+            for (int c = 0; c < chunks; ++c) {
+                Slot &sl = slots[c % kSlots];
+                if (!(ok = wait(&g_full[c % kSlots], c / kSlots))) break;
+                if (!STATES) {  // S0 in two parts
+                    if (c > 0 && !(ok = wait(s_free, c - 1))) break;
+                    ptx::tc_fence_after();
+                    float f = 1.f;
+                    if (F16) {
+                        float m = 0.f;
+#pragma unroll
+                        for (int d = 0; d < DK / 2; ++d) m = fmaxf(m, fmaxf(fabsf(S[d].x), fabsf(S[d].y)));
+                        const int e = lift(m);
+                        f = pow2f(e);
+                        sl.s_unit[tid] = pow2f(-e);
+                    }
+#pragma unroll
+                    for (int g = 0; g < DK / 32; ++g) {
+                        uint32_t hi[16], lo[16];
+#pragma unroll
+                        for (int d = 0; d < 16; ++d) asm volatile("" : "+f"(S[g * 16 + d].x), "+f"(S[g * 16 + d].y));  // (one group after another)
+#pragma unroll
+                        for (int d = 0; d < 16; ++d) split2<F16>(F16 ? __fmul2_rn(S[g * 16 + d], both(f)) : S[g * 16 + d], hi[d], lo[d]);
+                        ptx::tmem_st_16(lanes + C::kColS + g * 16, hi);
+                        ptx::tmem_st_16(lanes + C::kColS + DK / 2 + g * 16, lo);
+                    }
+                    ptx::tmem_st_wait();
+                    ptx::tc_fence_before();
+                    arrive(s_full);
+                }
+                if (!(ok = wait(u_full, c))) break;
                 ptx::tc_fence_after();
                 const float f = sl.whole, unit = F16 ? sl.u_unit : 1.f;
 #pragma unroll
@@ -253,63 +279,75 @@ __global__ void __launch_bounds__(kThreads, 1)
                     ptx::tmem_ld_wait();
                     tie32(u);
 #pragma unroll
-                    for (int d = 0; d < 32; ++d) {
-                        const float x = F16 ? __uint_as_float(u[d]) * unit : __uint_as_float(u[d]);
-                        S[g * 32 + d] = fmaf(S[g * 32 + d], f, x);
+                    for (int d = 0; d < 16; ++d) {
+                        float2 x = make_float2(__uint_as_float(u[2 * d]), __uint_as_float(u[2 * d + 1]));
+                        if (F16) x = __fmul2_rn(x, both(unit));
+                        S[g * 16 + d] = __ffma2_rn(S[g * 16 + d], both(f), x);
                     }
                 }
                 ptx::tc_fence_before();
                 arrive(u_free);
                 arrive(&g_empty[c % kSlots]);
-                if (!STATES && c + 1 < chunks) {
-                    if (!(ok = wait(s_free, c) && wait(&g_full[(c + 1) % kSlots], (c + 1) / kSlots))) break;
-                    ptx::tc_fence_after();
-                    publish(c + 1);
-                }
             }
-            if (ok && STATES) {
-                float *dst = place_at(seg);
-#pragma unroll
-                for (int d = 0; d < DK; ++d) dst[(int64_t)d * p.DV] = S[d];
-            } else if (ok && seg == segs - 1 && run.slot >= 0) {
-#pragma unroll
-                for (int d = 0; d < DK; ++d) own[(int64_t)d * p.DV] = S[d];
-            }
+            if (ok && (STATES || (seg == segs - 1 && run.slot >= 0))) store(STATES ? place_at(seg) : own);
         }
     } else if (warp < kValueWarp) {
         ptx::regs_down<kOutRegs>();
         if (!STATES && warp - kOutWarp < C::kLaneWarps) {
             // ------------------------------------------------------------------ the output --
-            const int ch = (warp - kOutWarp) * 32 + lane;
-            const uint32_t lanes = tmem + ((uint32_t)((warp - kOutWarp) * 32) << 16);
+            // Thread t has channel t of all tokens.  16 tokens at a time go through the warp's own transpose buffer, two tokens
+            // of a channel a word, and leave as 16-byte pieces of a token's row.
+            const int w = warp - kOutWarp, ch = w * 32 + lane, m = lane >> 2, piece = lane & 3;
+            const uint32_t lanes = tmem + ((uint32_t)(w * 32) << 16);
+            uint32_t *turn = reinterpret_cast<uint32_t *>(smem + C::kTurn) + w * (8 * kTurnRow);
             for (int c = 0; c < chunks && ok; ++c) {
                 const Slot &sl = slots[c % kSlots];
                 if (!(ok = wait(&g_full[c % kSlots], c / kSlots) && wait(o_full, c))) break;
                 ptx::tc_fence_after();
                 const int valid = min(rows - c * kChunk, kChunk);
-                const float f = p.scale * (F16 ? sl.s_unit[ch] : 1.f);
-                const int bad = sl.any_bad ? sl.bad[ch] : kChunk;
-                uint16_t *dst = p.out + (row0 + (int64_t)c * kChunk) * p.out_ld + col0 + ch;
-#pragma unroll
-                for (int g = 0; g < 2; ++g) {
-                    uint32_t a[32], x[32];
-                    ptx::tmem_ld_32(lanes + C::kColO1 + g * 32, a);
-                    ptx::tmem_ld_32(lanes + C::kColO2 + g * 32, x);
+                const float unit = F16 ? sl.s_unit[ch] : 1.f;
+                const bool some = sl.any_bad != 0;
+                const int bad = some ? sl.bad[ch] : kChunk;
+                uint16_t *dst = p.out + (row0 + (int64_t)c * kChunk + 2 * m) * p.out_ld + col0 + w * 32 + piece * 8;
+#pragma unroll 1
+                for (int g = 0; g < kChunk; g += 16) {
+                    uint32_t a[16], x[16];
+                    ptx::tmem_ld_16(lanes + C::kColO1 + g, a);
+                    ptx::tmem_ld_16(lanes + C::kColO2 + g, x);
                     ptx::tmem_ld_wait();
-                    tie32(a);
-                    tie32(x);
-                    if (g == 1) {
+#pragma unroll
+                    for (int t = 0; t < 16; ++t) asm volatile("" : "+r"(a[t]), "+r"(x[t]));
+                    if (g == kChunk - 16) {
                         ptx::tc_fence_before();
                         arrive(o_free);
                     }
+                    __syncwarp();
 #pragma unroll
-                    for (int t = 0; t < 32; ++t) {
-                        const int i = g * 32 + t;
-                        float o = __uint_as_float(a[t]) * (f * sl.fade[i]);
-                        o = fmaf(__uint_as_float(x[t]), F16 ? p.scale * sl.p_unit[i] : p.scale, o);
-                        if (i >= bad) o = __int_as_float(0x7fffffff);
-                        if (i < valid) dst[(int64_t)i * p.out_ld] = (uint16_t)pack2<F16>(o, 0.f);
+                    for (int t = 0; t < 16; t += 2) {
+                        float2 f = *reinterpret_cast<const float2 *>(&sl.fade[g + t]), pu = both(p.scale);
+                        if (F16) {
+                            pu = *reinterpret_cast<const float2 *>(&sl.p_unit[g + t]);
+                            f = __fmul2_rn(f, both(unit));
+                        }
+                        float2 v = __fmul2_rn(make_float2(__uint_as_float(a[t]), __uint_as_float(a[t + 1])), f);
+                        v = __ffma2_rn(make_float2(__uint_as_float(x[t]), __uint_as_float(x[t + 1])), pu, v);
+                        if (some) {
+                            if (g + t >= bad) v.x = __int_as_float(0x7fffffff);
+                            if (g + t + 1 >= bad) v.y = __int_as_float(0x7fffffff);
+                        }
+                        turn[t / 2 * kTurnRow + lane] = pack2<F16>(v.x, v.y);
                     }
+                    __syncwarp();
+                    const uint4 y = *reinterpret_cast<const uint4 *>(&turn[m * kTurnRow + piece * 8]);
+                    const uint4 z = *reinterpret_cast<const uint4 *>(&turn[m * kTurnRow + piece * 8 + 4]);
+                    if (g + 2 * m < valid)
+                        *reinterpret_cast<uint4 *>(dst) = make_uint4(__byte_perm(y.x, y.y, 0x5410), __byte_perm(y.z, y.w, 0x5410),
+                                                                     __byte_perm(z.x, z.y, 0x5410), __byte_perm(z.z, z.w, 0x5410));
+                    if (g + 2 * m + 1 < valid)
+                        *reinterpret_cast<uint4 *>(dst + p.out_ld) =
+                            make_uint4(__byte_perm(y.x, y.y, 0x7632), __byte_perm(y.z, y.w, 0x7632), __byte_perm(z.x, z.y, 0x7632),
+                                       __byte_perm(z.z, z.w, 0x7632));
+                    dst += 16 * p.out_ld;
                 }
                 arrive(&g_empty[c % kSlots]);
             }
@@ -327,50 +365,47 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint8_t *stage = smem + c % kStages * C::kStageBytes;
             if (!(ok = wait(&g_full[c % kSlots], c / kSlots) && wait(&full[c % kStages], c / kStages))) break;
             const int valid = min(rows - c * kChunk, kChunk);
-            float x[kPieces][8], sum = 0.f, m = 0.f;
-#pragma unroll
-            for (int i = 0; i < kPieces; ++i) {
-                const int row = r0 + (i & 3) * 16;
-                uint4 *src = reinterpret_cast<uint4 *>(stage + C::kV + t * 16 + i * 2048);
-                uint4 w = *src;
-                if (row >= valid) {  // behind the run's end, where whatever comes there lies: the products must not see it
-                    w = make_uint4(0, 0, 0, 0);
-                    *src = w;
-                }
-                const float f = sl.weight[row];
-                unpack8<F16>(w, x[i]);
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    sum = fmaf(x[i][j], 0.f, sum);
-                    x[i][j] *= f;
-                    if (F16) m = fmaxf(m, fabsf(x[i][j]));
-                }
-            }
-            if (valid < kChunk) {
-#pragma unroll
-                for (int i = 0; i < C::kKBlocks * 4; ++i)
+            // a piece's values, weighted
+            auto load = [&](int i, float2 (&x)[4]) {
+                const uint4 w = *reinterpret_cast<const uint4 *>(stage + C::kV + t * 16 + i * 2048);
+                x[0] = unpack2<F16>(w.x), x[1] = unpack2<F16>(w.y), x[2] = unpack2<F16>(w.z), x[3] = unpack2<F16>(w.w);
+            };
+            if (valid < kChunk) {  // behind the run's end, where whatever comes there lies: the products must not see it
+#pragma unroll 1
+                for (int i = 0; i < (C::kKBlocks + C::kVBlocks) * 4; ++i)
                     if (r0 + (i & 3) * 16 >= valid)
                         *reinterpret_cast<uint4 *>(stage + C::kK + t * 16 + i * 2048) = make_uint4(0, 0, 0, 0);
             }
-            if (__any_sync(0xffffffffu, sum != 0.f)) {  // a value that is not finite: taken out of V, remembered
-                m = 0.f;
+            float2 sum = both(0.f);
+            float m = 0.f;
+#pragma unroll 2
+            for (int i = 0; i < kPieces; ++i) {
+                float2 x[4];
+                load(i, x);
+                const float f = sl.weight[r0 + (i & 3) * 16];
 #pragma unroll
-                for (int i = 0; i < kPieces; ++i) {
-                    const int row = r0 + (i & 3) * 16;
-                    uint16_t *src = reinterpret_cast<uint16_t *>(stage + C::kV + t * 16 + i * 2048);
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        const float raw = load1<F16>(src + j);
-                        if (!(fabsf(raw) <= 3.4028234e38f)) {
-                            src[j] = 0;
-                            atomicMin(&sl.bad[(i >> 2) * 64 + ch0 + j], row);
-                            sl.any_bad = 1;
-                        } else if (F16) {
-                            m = fmaxf(m, fabsf(x[i][j]));
-                        }
-                    }
+                for (int j = 0; j < 4; ++j) {
+                    sum = __ffma2_rn(x[j], both(0.f), sum);
+                    if (F16) m = fmaxf(m, f * fmaxf(fabsf(x[j].x), fabsf(x[j].y)));
                 }
             }
+            // A value that is not finite makes its channel of the state that; of the tokens before it the product with P must not
+            // see it (0 times it), so it is taken out of V in the end, and remembered for the tokens from it on.
+            const bool found = __any_sync(0xffffffffu, sum.x != 0.f || sum.y != 0.f);
+            auto each = [&](auto what) {
+#pragma unroll 1
+                for (int e = 0; e < kPieces * 8; ++e) {
+                    const int i = e >> 3, row = r0 + (i & 3) * 16;
+                    uint16_t *src = reinterpret_cast<uint16_t *>(stage + C::kV + t * 16 + i * 2048) + (e & 7);
+                    const float raw = load1<F16>(src);
+                    what(src, raw, fabsf(raw) <= 3.4028234e38f, row, (i >> 2) * 64 + ch0 + (e & 7));
+                }
+            };
+            if (F16 && found) {
+                m = 0.f;
+                each([&](uint16_t *, float raw, bool fine, int row, int) { m = fine ? fmaxf(m, fabsf(raw) * sl.weight[row]) : m; });
+            }
+            float unit = 1.f;
             if (F16) {
                 m = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(m)));
                 float *all = most + (c & 1) * 4;
@@ -378,31 +413,43 @@ __global__ void __launch_bounds__(kThreads, 1)
                 arrive(m_full);
                 if (!(ok = wait(m_full, c))) break;
                 const int e = lift(fmaxf(fmaxf(all[0], all[1]), fmaxf(all[2], all[3])));
-                const float f = pow2f(e);
+                unit = pow2f(e);
                 if (t == 0) sl.u_unit = pow2f(-e);
-#pragma unroll
-                for (int i = 0; i < kPieces; ++i)
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) x[i][j] *= f;
             }
-            if (c > 0 && !(ok = wait(u_full, c - 1))) break;  // the last chunk's values have been read
             uint8_t *dst = smem + C::kValues + t * 16;
+#pragma unroll 1
+            for (int half = 0; half < 2; ++half) {  // tokens 0..31, 32..63
+                if (c > 0 && !(ok = wait(&v_free[half], c - 1))) break;  // the last chunk's have been read
+#pragma unroll 2
+                for (int n = 0; n < kPieces / 2; ++n) {
+                    const int i = (n >> 1) * 4 + half * 2 + (n & 1);
+                    float2 x[4];
+                    load(i, x);
+                    const float2 f = both(sl.weight[r0 + (i & 3) * 16] * unit);
 #pragma unroll
-            for (int i = 0; i < kPieces; ++i) {
+                    for (int j = 0; j < 4; ++j) x[j] = __fmul2_rn(x[j], f);
 #pragma unroll
-                for (int part = 0; part < C::kParts; ++part) {
-                    const uint4 w = pack8<F16>(x[i]);
-                    *reinterpret_cast<uint4 *>(dst + part * C::kPartBytes + i * 2048) = w;
-                    if (part + 1 < C::kParts) {
-                        float h[8];
-                        unpack8<F16>(w, h);
+                    for (int part = 0; part < C::kParts; ++part) {
+                        uint32_t w[4];
 #pragma unroll
-                        for (int j = 0; j < 8; ++j) x[i][j] -= h[j];
+                        for (int j = 0; j < 4; ++j) {
+                            w[j] = pack2<F16>(x[j].x, x[j].y);
+                            if (part + 1 < C::kParts) x[j] = rest<F16>(x[j], w[j]);
+                        }
+                        *reinterpret_cast<uint4 *>(dst + part * C::kPartBytes + i * 2048) = make_uint4(w[0], w[1], w[2], w[3]);
                     }
                 }
+                if (half == 1 && found)
+                    each([&](uint16_t *src, float, bool fine, int row, int ch) {
+                        if (fine) return;
+                        *src = 0;
+                        atomicMin(&sl.bad[ch], row);
+                        sl.any_bad = 1;
+                    });
+                ptx::fence_proxy_async_smem();
+                arrive(&v_full[half]);
             }
-            ptx::fence_proxy_async_smem();
-            arrive(v_full);
+            if (!ok) break;
             arrive(&g_empty[c % kSlots]);
         }
     } else {
@@ -410,55 +457,73 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (warp < kLoadWarp) {
             if (!STATES) {
                 // -------------------------------------------------------------------------- P --
-                const int i = tid - kWeightWarp * 32;  // its row
+                // Rows 0..31 are one warp's, 32..63 the other's: of the four 32 x 32 blocks the first warp has one below the
+                // diagonal's and one of zeros, which stays, the second one that no mask touches.
+                const int i = tid - kWeightWarp * 32, halves = warp - kWeightWarp + 1;  // its row; its blocks
                 const uint32_t lanes = tmem + ((uint32_t)((warp - kWeightWarp) * 32) << 16);
                 uint8_t *dst = smem + C::kP + i * 128;
+                if (halves == 1) {
+#pragma unroll
+                    for (int j = 4; j < 8; ++j) {
+                        *reinterpret_cast<uint4 *>(dst + ((j ^ (i & 7)) << 4)) = make_uint4(0, 0, 0, 0);
+                        *reinterpret_cast<uint4 *>(dst + ((j ^ (i & 7)) << 4) + kBlockBytes) = make_uint4(0, 0, 0, 0);
+                    }
+                }
                 for (int c = 0; c < chunks && ok; ++c) {
                     Slot &sl = slots[c % kSlots];
                     if (!(ok = wait(&g_full[c % kSlots], c / kSlots) && wait(a_full, c))) break;
+                    if (c > 0 && !(ok = wait(o_full, c - 1))) break;  // the last chunk's P has been read
                     ptx::tc_fence_after();
-                    uint32_t a[2][32];
-                    ptx::tmem_ld_32(lanes + C::kColA, a[0]);
-                    ptx::tmem_ld_32(lanes + C::kColA + 32, a[1]);
-                    ptx::tmem_ld_wait();
-                    tie32(a[0]);
-                    tie32(a[1]);
+                    const float2 gh = both(-sl.g_hi[i]), gl = both(-sl.g_lo[i]);
+                    float m = 0.f, f = 1.f;
+                    // 16 columns from j0 on: their largest (with fp16, whose rows are scaled), or their two parts into shared memory
+                    auto weigh = [&](int j0, auto diagonal, bool put) {
+                        uint32_t a[16];
+                        ptx::tmem_ld_16(lanes + C::kColA + j0, a);
+                        ptx::tmem_ld_wait();
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) asm volatile("" : "+r"(a[j]));
+                        uint32_t hi[8], lo[8];
+                        const int last = i - j0;
+#pragma unroll
+                        for (int j = 0; j < 16; j += 2) {
+                            const float2 h = *reinterpret_cast<const float2 *>(&sl.g_hi[j0 + j]), l = *reinterpret_cast<const float2 *>(&sl.g_lo[j0 + j]);
+                            const float2 g = __fadd2_rn(__fadd2_rn(gh, h), __fadd2_rn(gl, l));
+                            float2 x = __fmul2_rn(make_float2(__uint_as_float(a[j]), __uint_as_float(a[j + 1])),
+                                                  make_float2(exp2_fast(g.x), exp2_fast(g.y)));
+                            if (decltype(diagonal)::value) {
+                                if (j > last) x.x = 0.f;
+                                if (j + 1 > last) x.y = 0.f;
+                            }
+                            if (F16) {
+                                m = fmaxf(m, fmaxf(fabsf(x.x), fabsf(x.y)));
+                                x = __fmul2_rn(x, both(f));
+                            }
+                            split2<F16>(x, hi[j / 2], lo[j / 2]);
+                        }
+                        if (F16 && !put) return;
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) {
+                            uint8_t *at = dst + ((j0 / 8 + k) ^ (i & 7)) * 16;
+                            *reinterpret_cast<uint4 *>(at) = make_uint4(hi[4 * k], hi[4 * k + 1], hi[4 * k + 2], hi[4 * k + 3]);
+                            *reinterpret_cast<uint4 *>(at + kBlockBytes) = make_uint4(lo[4 * k], lo[4 * k + 1], lo[4 * k + 2], lo[4 * k + 3]);
+                        }
+                    };
+#pragma unroll 1
+                    for (int pass = F16 ? 0 : 1; pass < 2; ++pass) {
+                        int j0 = 0;
+#pragma unroll 1
+                        for (; j0 < (halves - 1) * 32; j0 += 16) weigh(j0, Flag<false>{}, pass == 1);
+#pragma unroll 1
+                        for (; j0 < halves * 32; j0 += 16) weigh(j0, Flag<true>{}, pass == 1);
+                        if (F16 && pass == 0) {
+                            const int e = lift(m);
+                            f = pow2f(e);
+                            sl.p_unit[i] = p.scale * pow2f(-e);
+                        }
+                    }
                     ptx::tc_fence_before();
                     arrive(a_free);
-                    const float gh = sl.g_hi[i], gl = sl.g_lo[i];
-                    float m = 0.f;
-#pragma unroll
-                    for (int j0 = 0; j0 < kChunk; j0 += 4) {
-                        const float4 h4 = *reinterpret_cast<const float4 *>(&sl.g_hi[j0]), l4 = *reinterpret_cast<const float4 *>(&sl.g_lo[j0]);
-                        const float h[4] = {h4.x, h4.y, h4.z, h4.w}, l[4] = {l4.x, l4.y, l4.z, l4.w};
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const int j = j0 + e;
-                            const float w = exp2_fast((gh - h[e]) + (gl - l[e]));
-                            const float x = j <= i ? __uint_as_float(a[j >> 5][j & 31]) * w : 0.f;
-                            a[j >> 5][j & 31] = __float_as_uint(x);
-                            if (F16) m = fmaxf(m, fabsf(x));
-                        }
-                    }
-                    float f = 1.f;
-                    if (F16) {
-                        const int e = lift(m);
-                        f = pow2f(e);
-                        sl.p_unit[i] = pow2f(-e);
-                    }
-                    if (c > 0 && !(ok = wait(o_full, c - 1))) break;  // the last chunk's P has been read
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        uint32_t hi[4], lo[4];
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const uint32_t *x = &a[j >> 2][(j & 3) * 8 + 2 * e];
-                            split2<F16>(__uint_as_float(x[0]) * f, __uint_as_float(x[1]) * f, hi[e], lo[e]);
-                        }
-                        uint8_t *at = dst + ((j ^ (i & 7)) << 4);
-                        *reinterpret_cast<uint4 *>(at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-                        *reinterpret_cast<uint4 *>(at + kBlockBytes) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-                    }
                     ptx::fence_proxy_async_smem();
                     arrive(p_full);
                     arrive(&g_empty[c % kSlots]);
@@ -466,62 +531,76 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         } else if (warp == kLoadWarp) {
             // -------------------------------------------------------------- copies, decays --
-            double total = 0.0;  // log2 of the segment's decay
+            int64_t total = 0;  // log2 of the segment's decay
             if (lane == 0) {
                 ptx::tma_prefetch_desc(&maps.k);
                 ptx::tma_prefetch_desc(&maps.v);
                 if (!STATES) ptx::tma_prefetch_desc(&maps.q);
             }
+            // the decays of two tokens a lane, on their way two chunks ahead
+            auto decays = [&](int c) {
+                const int i = c * kChunk + 2 * lane;
+                return make_float2(i < rows ? raw_decay(p, row0 + i, head) : 0.f, i + 1 < rows ? raw_decay(p, row0 + i + 1, head) : 0.f);
+            };
+            auto copies = [&](auto copy, int c) {  // of a chunk, each a box of 64 tokens and 64 channels
+                const int row = (int)row0 + c * kChunk;
+#pragma unroll
+                for (int i = 0; i < C::kKBlocks; ++i) {
+                    copy(&maps.k, kh * DK + i * 64, row, C::kK + i * kBlockBytes);
+                    if (!STATES) copy(&maps.q, kh * DK + i * 64, row, i * kBlockBytes);
+                }
+#pragma unroll
+                for (int i = 0; i < C::kVBlocks; ++i) copy(&maps.v, col0 + i * 64, row, C::kV + i * kBlockBytes);
+            };
+            auto fetch = [](const CUtensorMap *map, int x, int row, int) { ptx::tma_prefetch_2d(map, x, row); };
+            float2 g = decays(0), g1 = decays(1);
+            if (lane == 0)
+                for (int c = kStages; c < min(kStages + kFetch, chunks); ++c) copies(fetch, c);
             for (int c = 0; c < chunks && ok; ++c) {
                 const int st = c % kStages;
-                const int64_t row = row0 + (int64_t)c * kChunk;
-                const int valid = min(rows - c * kChunk, kChunk);
-                // the decays of two tokens a lane, on their way while the stage is waited for
-                const float g0 = 2 * lane < valid ? load_decay(p, row + 2 * lane, head) : 0.f;
-                const float g1 = 2 * lane + 1 < valid ? load_decay(p, row + 2 * lane + 1, head) : 0.f;
+                const float2 g2 = decays(c + 2);
                 if (c >= kStages && !(ok = wait(&empty[st], c / kStages - 1))) break;
                 if (lane == 0) {
                     uint8_t *stage = smem + st * C::kStageBytes;
                     ptx::mbar_arrive_expect_tx(&full[st], (uint32_t)(C::kStageBytes - (STATES ? C::kK : 0)));
-#pragma unroll
-                    for (int i = 0; i < C::kKBlocks; ++i) {
-                        ptx::tma_load_2d(stage + C::kK + i * kBlockBytes, &maps.k, kh * DK + i * 64, (int)row, &full[st]);
-                        if (!STATES) ptx::tma_load_2d(stage + i * kBlockBytes, &maps.q, kh * DK + i * 64, (int)row, &full[st]);
-                    }
-#pragma unroll
-                    for (int i = 0; i < C::kVBlocks; ++i)
-                        ptx::tma_load_2d(stage + C::kV + i * kBlockBytes, &maps.v, col0 + i * 64, (int)row, &full[st]);
+                    copies([&](const CUtensorMap *map, int x, int row, int to) { ptx::tma_load_2d(stage + to, map, x, row, &full[st]); }, c);
+                    if (c + kStages + kFetch < chunks) copies(fetch, c + kStages + kFetch);
                 }
                 issued = c + 1;
                 if (c >= kSlots && !(ok = wait(&g_empty[c % kSlots], c / kSlots - 1))) break;
-                constexpr double kLog2e = 1.4426950408889634074;
-                const double l0 = g0 * kLog2e, l1 = g1 * kLog2e;
-                double sum = l0 + l1;
+                const int64_t l0 = fixed_log2(checked_decay(p, g.x)), l1 = fixed_log2(checked_decay(p, g.y));
+                g = g1, g1 = g2;
+                int64_t sum = l0 + l1;
 #pragma unroll
                 for (int o = 1; o < 32; o <<= 1) {
-                    const double x = __shfl_up_sync(0xffffffffu, sum, o);
+                    const int64_t x = __shfl_up_sync(0xffffffffu, sum, o);
                     if (lane >= o) sum += x;
                 }
-                const double end = __shfl_sync(0xffffffffu, sum, 31), G[2] = {sum - l1, sum};
-                total += end;
+                const int64_t end = __shfl_sync(0xffffffffu, sum, 31);
+                total = max((long long)(total + end), -(1ll << 60));
                 Slot &sl = slots[c % kSlots];
+                float hi[2], lo[2], fade[2], weight[2];
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    const int j = 2 * lane + e;
-                    const float hi = (float)G[e];
-                    sl.g_hi[j] = hi;
-                    sl.g_lo[j] = (float)(G[e] - (double)hi);
-                    sl.fade[j] = exp2_fast(hi);
-                    sl.weight[j] = exp2_fast((float)(end - G[e]));
+                    const int64_t G = e ? sum : sum - l1;
+                    hi[e] = __ll2float_rn(G);
+                    lo[e] = __ll2float_rn(__float2ll_rn(hi[e]) - G) * kFixed;
+                    hi[e] *= -kFixed;
+                    fade[e] = p.scale * exp2_fast(-hi[e]);
+                    weight[e] = exp2_fast(__ll2float_rn(end - G) * kFixed);
                 }
+                reinterpret_cast<float2 *>(sl.g_hi)[lane] = make_float2(hi[0], hi[1]);
+                reinterpret_cast<float2 *>(sl.g_lo)[lane] = make_float2(lo[0], lo[1]);
+                reinterpret_cast<float2 *>(sl.fade)[lane] = make_float2(fade[0], fade[1]);
+                reinterpret_cast<float2 *>(sl.weight)[lane] = make_float2(weight[0], weight[1]);
                 for (int i = lane; i < 128; i += 32) sl.bad[i] = kChunk;
                 if (lane == 0) {
-                    sl.whole = exp2_fast((float)end);
+                    sl.whole = exp2_fast(__ll2float_rn(end) * kFixed);
                     sl.any_bad = 0;
                 }
                 arrive(&g_full[c % kSlots]);
             }
-            if (STATES && ok && lane == 0 && tile == 0) p.seg_decay[(int64_t)place * p.VH + head] = exp2_fast((float)total);
+            if (STATES && ok && lane == 0 && tile == 0) p.seg_decay[(int64_t)place * p.VH + head] = exp2_fast(__ll2float_rn(total) * kFixed);
         } else {
             // -------------------------------------------------------------------- the MMAs --
             const uint32_t idesc_a = ptx::idesc_16_f32(F16, 128, kChunk, false, false);
@@ -535,7 +614,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             auto logits = [&](int c) {  // A = Q K^T: 64 rows, and 64 that nobody reads
                 if (ptx::elect_one()) {
                     const uint64_t st = desc_k + at(c % kStages * C::kStageBytes);
-#pragma unroll
+#pragma unroll 2
                     for (int k = 0; k < DK / 16; ++k) {
                         const int off = (k >> 2) * kBlock16 + (k & 3) * 2;
                         ptx::mma_f16_ss(tmem + C::kColA, st + off, st + at(C::kK) + off, idesc_a, k > 0);
@@ -558,28 +637,36 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 // U^T = (w V)^T K
                 if (STATES && !(ok = wait(&full[c % kStages], c / kStages))) break;
-                if (!(ok = wait(v_full, c) && (c == 0 || wait(u_free, c - 1)))) break;
-                ptx::tc_fence_after();
-                if (ptx::elect_one()) {
+                if (!(ok = c == 0 || wait(u_free, c - 1))) break;
+#pragma unroll 1
+                for (int half = 0; half < 2; ++half) {
+                    if (!(ok = wait(&v_full[half], c))) break;
+                    ptx::tc_fence_after();
+                    if (ptx::elect_one()) {
+#pragma unroll 1
+                        for (int part = 0; part < C::kParts; ++part)
 #pragma unroll
-                    for (int part = 0; part < C::kParts; ++part)
-#pragma unroll
-                        for (int k = 0; k < kChunk / 16; ++k)
-                            ptx::mma_f16_ss(tmem + C::kColU, desc_mn + at(C::kValues + part * C::kPartBytes + k * 2048),
-                                            desc_mn + at(stage + C::kK + k * 2048), idesc_u, part > 0 || k > 0);
-                    ptx::mma_commit(u_full);
-                    ptx::mbar_arrive(u_full);
-                    if (STATES) ptx::mma_commit(&empty[c % kStages]);
+                            for (int k = 2 * half; k < 2 * half + 2; ++k)
+                                ptx::mma_f16_ss(tmem + C::kColU, desc_mn + at(C::kValues + part * C::kPartBytes + k * 2048),
+                                                desc_mn + at(stage + C::kK + k * 2048), idesc_u, part > 0 || k > 0);
+                        ptx::mma_commit(&v_free[half]);
+                        if (half == 1) {
+                            ptx::mma_commit(u_full);
+                            ptx::mbar_arrive(u_full);
+                            if (STATES) ptx::mma_commit(&empty[c % kStages]);
+                        }
+                    }
+                    __syncwarp();
                 }
-                __syncwarp();
+                if (!ok) break;
                 if (STATES) continue;
                 // O1^T = S0^T Q^T
                 if (!(ok = wait(s_full, c) && (c == 0 || wait(o_free, c - 1)))) break;
                 ptx::tc_fence_after();
                 if (ptx::elect_one()) {
-#pragma unroll
+#pragma unroll 1
                     for (int part = 0; part < 2; ++part)
-#pragma unroll
+#pragma unroll 2
                         for (int k = 0; k < DK / 16; ++k)
                             ptx::mma_f16_ts(tmem + C::kColO1, tmem + C::kColS + part * (DK / 2) + k * 8,
                                             desc_k + at(stage) + (k >> 2) * kBlock16 + (k & 3) * 2, idesc_o1, part > 0 || k > 0);
@@ -590,9 +677,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (!(ok = wait(p_full, c))) break;
                 ptx::tc_fence_after();
                 if (ptx::elect_one()) {
-#pragma unroll
+#pragma unroll 1
                     for (int part = 0; part < 2; ++part)
-#pragma unroll
+#pragma unroll 2
                         for (int k = 0; k < kChunk / 16; ++k)
                             ptx::mma_f16_ss(tmem + C::kColO2, desc_mn + at(stage + C::kV + k * 2048),
                                             desc_k + at(C::kP + part * kBlockBytes) + k * 2, idesc_o2, part > 0 || k > 0);

@@ -104,10 +104,11 @@ __device__ __forceinline__ Run load_run(const LinearArgs &a, int b) {
     return r;
 }
 
-// Log decay of row t (of value head h), checked.
-__device__ __forceinline__ float load_decay(const LinearArgs &a, int64_t t, int h) {
-    if (!a.decay) return 0.f;
-    const float g = __ldg(a.decay + (a.decay_ld ? t * a.decay_ld : 0) + h);
+// Log decay of row t (of value head h) as it is given, and checked.
+__device__ __forceinline__ float raw_decay(const LinearArgs &a, int64_t t, int h) {
+    return a.decay ? __ldg(a.decay + (a.decay_ld ? t * a.decay_ld : 0) + h) : 0.f;
+}
+__device__ __forceinline__ float checked_decay(const LinearArgs &a, float g) {
     if (!(g <= 0.f)) layer_error(a.status);
     return g <= 0.f ? fmaxf(g, kLeastDecay) : 0.f;
 }

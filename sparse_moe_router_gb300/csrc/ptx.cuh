@@ -131,6 +131,24 @@ __device__ __forceinline__ bool mbar_wait(uint64_t *bar, uint32_t parity, uint64
     }
 }
 
+// mbar_wait in few instructions, for kernels whose warps wait in many places: a try may sleep up to 2 us in the hardware
+// (it wakes when the phase completes), and 2^20 of them (2 s, less where the hardware does not sleep) are the limit.
+__device__ __forceinline__ bool mbar_sleep_wait(uint64_t *bar, uint32_t parity, volatile int *abort) {
+    for (int n = 0; n < 1 << 20; ++n) {
+        uint32_t ok;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(ok)
+            : "r"(smem_u32(bar)), "r"(parity), "r"(2000u)
+            : "memory");
+        if (ok) return true;
+        if (*abort) return false;
+    }
+    return false;
+}
+
 // ------------------------------------------------------------------------------ TMA --
 
 __device__ __forceinline__ void tma_prefetch_desc(const void *tmap) {
@@ -146,6 +164,13 @@ __device__ __forceinline__ void tma_load_2d(void *smem_dst, const void *tmap, in
         " [%0], [%1, {%2, %3}], [%4];" ::"r"(smem_u32(smem_dst)),
         "l"(reinterpret_cast<uint64_t>(tmap)), "r"(c0), "r"(c1), "r"(smem_u32(bar))
         : "memory");
+}
+
+// The box of a later load, brought into L2.
+__device__ __forceinline__ void tma_prefetch_2d(const void *tmap, int c0, int c1) {
+    asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];" ::"l"(reinterpret_cast<uint64_t>(tmap)), "r"(c0),
+                 "r"(c1)
+                 : "memory");
 }
 
 // Pair form: the box lands in this CTA's shared memory and completes its bytes on the mbarrier
