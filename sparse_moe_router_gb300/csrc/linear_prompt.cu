@@ -57,11 +57,11 @@ struct Shape {
     static constexpr int kParts = F16 ? 2 : 3;  // of a weighted value
     static constexpr int kPartBytes = kVBlocks * kBlockBytes;
     static constexpr int kValues = kStages * kStageBytes, kP = kValues + kParts * kPartBytes;
-    static constexpr int kTurn = kP + 2 * kBlockBytes, kBars = kTurn + kVBlocks * 2 * 8 * kTurnRow * 4, kSlotAt = kBars + 320;
+    static constexpr int kTurn = kP + 2 * kBlockBytes, kBars = kTurn + kVBlocks * 2 * 8 * kTurnRow * 4, kSlotAt = kBars + 384;
     static constexpr int kSmem = 1024 + kSlotAt + kSlots * (int)sizeof(Slot);
     static constexpr int kLaneWarps = DV / 32;  // warps that hold channels
-    // TMEM columns: S0 in two parts, U, A, O1, O2
-    static constexpr uint32_t kColS = 0, kColU = DK, kColA = 2 * DK, kColO1 = kColA + 64, kColO2 = kColO1 + 64, kCols = 512;
+    // TMEM columns: S0 in two parts, U, A of even and odd chunks, O1, O2
+    static constexpr uint32_t kColS = 0, kColU = DK, kColA = 2 * DK, kColO1 = kColA + 2 * 64, kColO2 = kColO1 + 64, kCols = 512;
     static_assert(kColO2 + 64 <= kCols, "TMEM");
     static_assert(kSmem <= 227 * 1024, "shared memory over the per-block limit");
     // (operands of 128 rows whose second half is none of theirs read up to a block further; it is never looked at)
@@ -123,22 +123,24 @@ __global__ void __launch_bounds__(kThreads, 1)
     linear_chunk_kernel(const __grid_constant__ LinearArgs p, const __grid_constant__ Maps maps) {
     using C = Shape<DK, DV, F16>;
     constexpr int kStages = C::kStages;
+    constexpr int kUs = STATES ? 2 : 1;            // places for U
+    constexpr int kConvWarps = STATES ? 8 : 4;  // (without outputs their warps weigh values too)
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = smem_raw + ((1024u - (ptx::smem_u32(smem_raw) & 1023u)) & 1023u);
     uint64_t *full = reinterpret_cast<uint64_t *>(smem + C::kBars);  // [kStages] Q, K, V of a chunk
     uint64_t *empty = full + kStages;                                // [kStages]
     uint64_t *g_full = empty + kStages, *g_empty = g_full + kSlots;  // [kSlots] decays
-    uint64_t *a_full = g_empty + kSlots, *a_free = a_full + 1;       // A in TMEM; read
-    uint64_t *p_full = a_free + 1;                                   // P in shared memory
+    uint64_t *a_full = g_empty + kSlots, *a_free = a_full + 2;       // [2] A of an even or odd chunk in TMEM; read
+    uint64_t *p_full = a_free + 2;                                   // P in shared memory
     uint64_t *v_full = p_full + 1, *v_free = v_full + 2;             // [2] weighted values of 32 tokens there; read
-    uint64_t *u_full = v_free + 2, *u_free = u_full + 1;             // U in TMEM; read
-    uint64_t *s_full = u_free + 1, *s_free = s_full + 1;             // S0 in TMEM; read by its product
+    uint64_t *u_full = v_free + 2, *u_free = u_full + 2;             // [2] U in TMEM; read (without outputs: of even and odd chunks)
+    uint64_t *s_full = u_free + 2, *s_free = s_full + 1;             // S0 in TMEM; read by its product
     uint64_t *o_full = s_free + 1, *o_free = o_full + 1;             // O1 and O2 in TMEM (and P read); read
     uint64_t *m_full = o_free + 1;                                   // fp16: the warps' largest weighted values
     uint64_t *drain = m_full + 1;
     uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(drain + 1);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_holder + 1);
-    float *most = reinterpret_cast<float *>(tmem_holder + 2);  // [2 x 4] those, of even and odd chunks
+    float *most = reinterpret_cast<float *>(tmem_holder + 2);  // [2 x 8] those, of even and odd chunks
     Slot *slots = reinterpret_cast<Slot *>(smem + C::kSlotAt);
 
     const int tid = (int)threadIdx.x, lane = tid & 31;
@@ -174,14 +176,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int s = 0; s < kStages; ++s) ptx::mbar_init(&full[s], 1), ptx::mbar_init(&empty[s], 1);
         for (int s = 0; s < kSlots; ++s) {
             ptx::mbar_init(&g_full[s], 1);
-            ptx::mbar_init(&g_empty[s], 4 + C::kLaneWarps + (STATES ? 0 : 2 + C::kLaneWarps));
+            ptx::mbar_init(&g_empty[s], kConvWarps + C::kLaneWarps + (STATES ? 0 : 2 + C::kLaneWarps));
         }
-        ptx::mbar_init(a_full, 1), ptx::mbar_init(a_free, 2);
         ptx::mbar_init(p_full, 2);
-        for (int i = 0; i < 2; ++i) ptx::mbar_init(&v_full[i], 4), ptx::mbar_init(&v_free[i], 1);
+        for (int i = 0; i < 2; ++i) {
+            ptx::mbar_init(&a_full[i], 1), ptx::mbar_init(&a_free[i], 2);
+            ptx::mbar_init(&v_full[i], kConvWarps), ptx::mbar_init(&v_free[i], 1);
+        }
         // (u_full and o_full: the MMAs' end, and the arrival of the warp that has seen the units of their operands)
-        ptx::mbar_init(m_full, 4);
-        ptx::mbar_init(u_full, 2), ptx::mbar_init(u_free, C::kLaneWarps);
+        ptx::mbar_init(m_full, kConvWarps);
+        for (int i = 0; i < 2; ++i) ptx::mbar_init(&u_full[i], 2), ptx::mbar_init(&u_free[i], C::kLaneWarps);
         ptx::mbar_init(s_full, C::kLaneWarps), ptx::mbar_init(s_free, 1);
         ptx::mbar_init(o_full, 2), ptx::mbar_init(o_free, C::kLaneWarps);
         ptx::mbar_init(drain, 1);
@@ -202,6 +206,104 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     bool ok = true;
     int issued = 0;  // chunks whose copies were begun
+
+    // ----------------------------------------------------------------- weighted values --
+    // Thread t has 16-byte pieces t, t + 128 (256), ... of the tile as it lies in shared memory (swizzled): of rows t / 8 + 16 i
+    // (32 i) of each block.  What comes out lies in the same places.  Two halves of 32 tokens, the one's products under way
+    // while the other is weighed.
+    auto weigh_values = [&]() {
+        constexpr int kStep = kConvWarps * 512, kRowStep = kConvWarps * 4;  // bytes and rows from one piece to a thread's next
+        constexpr int kPieces = C::kVBlocks * kBlockBytes / kStep, kHalf = 32 / kRowStep;
+        const int conv = warp - (kWeightWarp - kConvWarps), t = conv * 32 + lane, r0 = t >> 3;
+        const int ch0 = ((t & 7) ^ (r0 & 7)) * 8;  // its channels in each block (rows differ by multiples of 8)
+        for (int c = 0; c < chunks && ok; ++c) {
+            Slot &sl = slots[c % kSlots];
+            uint8_t *stage = smem + c % kStages * C::kStageBytes;
+            if (!(ok = wait(&g_full[c % kSlots], c / kSlots) && wait(&full[c % kStages], c / kStages))) break;
+            const int valid = min(rows - c * kChunk, kChunk);
+            auto row_of = [&](int i) { return r0 + i * kRowStep % kChunk; };
+            auto load = [&](int i, float2 (&x)[4]) {
+                const uint4 w = *reinterpret_cast<const uint4 *>(stage + C::kV + t * 16 + i * kStep);
+                x[0] = unpack2<F16>(w.x), x[1] = unpack2<F16>(w.y), x[2] = unpack2<F16>(w.z), x[3] = unpack2<F16>(w.w);
+            };
+            if (valid < kChunk) {  // behind the run's end, where whatever comes there lies: the products must not see it
+#pragma unroll 1
+                for (int i = 0; i < (C::kKBlocks + C::kVBlocks) * kBlockBytes / kStep; ++i)
+                    if (row_of(i) >= valid) *reinterpret_cast<uint4 *>(stage + C::kK + t * 16 + i * kStep) = make_uint4(0, 0, 0, 0);
+            }
+            float unit = 1.f;
+            if (F16) {  // the chunk's largest finite one
+                float m = 0.f;
+#pragma unroll 2
+                for (int i = 0; i < kPieces; ++i) {
+                    float2 x[4];
+                    load(i, x);
+                    const float f = sl.weight[row_of(i)];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const float a = f * fabsf(x[j].x), b = f * fabsf(x[j].y);
+                        m = fmaxf(m, fmaxf(a <= 3.4028234e38f ? a : 0.f, b <= 3.4028234e38f ? b : 0.f));
+                    }
+                }
+                m = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(m)));
+                float *all = most + (c & 1) * 8;
+                if (lane == 0) all[conv] = m;
+                arrive(m_full);
+                if (!(ok = wait(m_full, c))) break;
+#pragma unroll
+                for (int i = 0; i < kConvWarps; ++i) m = fmaxf(m, all[i]);
+                const int e = lift(m);
+                unit = pow2f(e);
+                if (t == 0) sl.u_unit = pow2f(-e);
+            }
+            uint8_t *dst = smem + C::kValues + t * 16;
+            float2 sum = both(0.f);
+#pragma unroll 1
+            for (int half = 0; half < 2; ++half) {  // tokens 0..31, 32..63
+                if (c > 0 && !(ok = wait(&v_free[half], c - 1))) break;  // the last chunk's have been read
+#pragma unroll 2
+                for (int n = 0; n < kPieces / 2; ++n) {
+                    const int i = n / kHalf * (2 * kHalf) + half * kHalf + n % kHalf;
+                    float2 x[4];
+                    load(i, x);
+                    const float2 f = both(sl.weight[row_of(i)] * unit);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        sum = __ffma2_rn(x[j], both(0.f), sum);
+                        x[j] = __fmul2_rn(x[j], f);
+                    }
+#pragma unroll
+                    for (int part = 0; part < C::kParts; ++part) {
+                        uint32_t w[4];
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            w[j] = pack2<F16>(x[j].x, x[j].y);
+                            if (part + 1 < C::kParts) x[j] = rest<F16>(x[j], w[j]);
+                        }
+                        *reinterpret_cast<uint4 *>(dst + part * C::kPartBytes + i * kStep) = make_uint4(w[0], w[1], w[2], w[3]);
+                    }
+                }
+                // A value that is not finite makes its channel of the state that; of the tokens before it the product with P must
+                // not see it (0 times it), so it is taken out of V in the end, and remembered for the tokens from it on.
+                if (half == 1 && __any_sync(0xffffffffu, sum.x != 0.f || sum.y != 0.f)) {
+#pragma unroll 1
+                    for (int e = 0; e < kPieces * 8; ++e) {
+                        const int i = e >> 3;
+                        uint16_t *src = reinterpret_cast<uint16_t *>(stage + C::kV + t * 16 + i * kStep) + (e & 7);
+                        if (fabsf(load1<F16>(src)) <= 3.4028234e38f) continue;
+                        *src = 0;
+                        atomicMin(&sl.bad[i * kRowStep / kChunk * 64 + ch0 + (e & 7)], row_of(i));
+                        sl.any_bad = 1;
+                    }
+                    __syncwarp();
+                }
+                ptx::fence_proxy_async_smem();
+                arrive(&v_full[half]);
+            }
+            if (!ok) break;
+            arrive(&g_empty[c % kSlots]);
+        }
+    };
 
     if (warp < kOutWarp) {
         ptx::regs_up<kStateRegs>();
@@ -269,13 +371,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                     ptx::tc_fence_before();
                     arrive(s_full);
                 }
-                if (!(ok = wait(u_full, c))) break;
+                if (!(ok = wait(&u_full[c % kUs], c / kUs))) break;
                 ptx::tc_fence_after();
                 const float f = sl.whole, unit = F16 ? sl.u_unit : 1.f;
 #pragma unroll
                 for (int g = 0; g < DK / 32; ++g) {
                     uint32_t u[32];
-                    ptx::tmem_ld_32(lanes + C::kColU + g * 32, u);
+                    ptx::tmem_ld_32(lanes + C::kColU + c % kUs * 128 + g * 32, u);
                     ptx::tmem_ld_wait();
                     tie32(u);
 #pragma unroll
@@ -286,14 +388,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
                 ptx::tc_fence_before();
-                arrive(u_free);
+                arrive(&u_free[c % kUs]);
                 arrive(&g_empty[c % kSlots]);
             }
             if (ok && (STATES || (seg == segs - 1 && run.slot >= 0))) store(STATES ? place_at(seg) : own);
         }
     } else if (warp < kValueWarp) {
         ptx::regs_down<kOutRegs>();
-        if (!STATES && warp - kOutWarp < C::kLaneWarps) {
+        if (STATES) {
+            weigh_values();
+        } else if (warp - kOutWarp < C::kLaneWarps) {
             // ------------------------------------------------------------------ the output --
             // Thread t has channel t of all tokens.  16 tokens at a time go through the warp's own transpose buffer, two tokens
             // of a channel a word, and leave as 16-byte pieces of a token's row.
@@ -308,42 +412,50 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const float unit = F16 ? sl.s_unit[ch] : 1.f;
                 const bool some = sl.any_bad != 0;
                 const int bad = some ? sl.bad[ch] : kChunk;
-                uint16_t *dst = p.out + (row0 + (int64_t)c * kChunk + 2 * m) * p.out_ld + col0 + w * 32 + piece * 8;
-#pragma unroll 1
-                for (int g = 0; g < kChunk; g += 16) {
+                uint32_t o[32];  // token pairs
+#pragma unroll
+                for (int g = 0; g < 4; ++g) {
                     uint32_t a[16], x[16];
-                    ptx::tmem_ld_16(lanes + C::kColO1 + g, a);
-                    ptx::tmem_ld_16(lanes + C::kColO2 + g, x);
+                    ptx::tmem_ld_16(lanes + C::kColO1 + g * 16, a);
+                    ptx::tmem_ld_16(lanes + C::kColO2 + g * 16, x);
                     ptx::tmem_ld_wait();
 #pragma unroll
                     for (int t = 0; t < 16; ++t) asm volatile("" : "+r"(a[t]), "+r"(x[t]));
-                    if (g == kChunk - 16) {
-                        ptx::tc_fence_before();
-                        arrive(o_free);
+#pragma unroll
+                    for (int t = 0; t < 16; t += 4) {
+                        const float4 f4 = *reinterpret_cast<const float4 *>(&sl.fade[g * 16 + t]);
+                        float4 p4 = make_float4(p.scale, p.scale, p.scale, p.scale);
+                        if (F16) p4 = *reinterpret_cast<const float4 *>(&sl.p_unit[g * 16 + t]);
+#pragma unroll
+                        for (int e = 0; e < 4; e += 2) {
+                            float2 f = e ? make_float2(f4.z, f4.w) : make_float2(f4.x, f4.y);
+                            if (F16) f = __fmul2_rn(f, both(unit));
+                            float2 v = __fmul2_rn(make_float2(__uint_as_float(a[t + e]), __uint_as_float(a[t + e + 1])), f);
+                            v = __ffma2_rn(make_float2(__uint_as_float(x[t + e]), __uint_as_float(x[t + e + 1])),
+                                           e ? make_float2(p4.z, p4.w) : make_float2(p4.x, p4.y), v);
+                            o[g * 8 + (t + e) / 2] = pack2<F16>(v.x, v.y);
+                        }
                     }
+                }
+                ptx::tc_fence_before();
+                arrive(o_free);
+                if (some) {
+#pragma unroll
+                    for (int t = 0; t < 32; ++t) o[t] |= (2 * t >= bad ? 0x7fffu : 0u) | (2 * t + 1 >= bad ? 0x7fff0000u : 0u);
+                }
+                uint16_t *dst = p.out + (row0 + (int64_t)c * kChunk + 2 * m) * p.out_ld + col0 + w * 32 + piece * 8;
+#pragma unroll
+                for (int g = 0; g < 4; ++g) {
                     __syncwarp();
 #pragma unroll
-                    for (int t = 0; t < 16; t += 2) {
-                        float2 f = *reinterpret_cast<const float2 *>(&sl.fade[g + t]), pu = both(p.scale);
-                        if (F16) {
-                            pu = *reinterpret_cast<const float2 *>(&sl.p_unit[g + t]);
-                            f = __fmul2_rn(f, both(unit));
-                        }
-                        float2 v = __fmul2_rn(make_float2(__uint_as_float(a[t]), __uint_as_float(a[t + 1])), f);
-                        v = __ffma2_rn(make_float2(__uint_as_float(x[t]), __uint_as_float(x[t + 1])), pu, v);
-                        if (some) {
-                            if (g + t >= bad) v.x = __int_as_float(0x7fffffff);
-                            if (g + t + 1 >= bad) v.y = __int_as_float(0x7fffffff);
-                        }
-                        turn[t / 2 * kTurnRow + lane] = pack2<F16>(v.x, v.y);
-                    }
+                    for (int k = 0; k < 8; ++k) turn[k * kTurnRow + lane] = o[g * 8 + k];
                     __syncwarp();
                     const uint4 y = *reinterpret_cast<const uint4 *>(&turn[m * kTurnRow + piece * 8]);
                     const uint4 z = *reinterpret_cast<const uint4 *>(&turn[m * kTurnRow + piece * 8 + 4]);
-                    if (g + 2 * m < valid)
+                    if (g * 16 + 2 * m < valid)
                         *reinterpret_cast<uint4 *>(dst) = make_uint4(__byte_perm(y.x, y.y, 0x5410), __byte_perm(y.z, y.w, 0x5410),
                                                                      __byte_perm(z.x, z.y, 0x5410), __byte_perm(z.z, z.w, 0x5410));
-                    if (g + 2 * m + 1 < valid)
+                    if (g * 16 + 2 * m + 1 < valid)
                         *reinterpret_cast<uint4 *>(dst + p.out_ld) =
                             make_uint4(__byte_perm(y.x, y.y, 0x7632), __byte_perm(y.z, y.w, 0x7632), __byte_perm(z.x, z.y, 0x7632),
                                        __byte_perm(z.z, z.w, 0x7632));
@@ -354,104 +466,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     } else if (warp < kWeightWarp) {
         ptx::regs_down<kValueRegs>();
-        // ------------------------------------------------------------- weighted values --
-        // Thread t has 16-byte pieces t, t + 128, ... of the tile as it lies in shared memory (swizzled): of rows t / 8 + 16 i
-        // of each block.  What comes out lies in the same places.
-        const int t = tid - kValueWarp * 32, r0 = t >> 3;
-        constexpr int kPieces = C::kVBlocks * 4;
-        const int ch0 = ((t & 7) ^ (r0 & 7)) * 8;  // its channels in each block (rows differ by multiples of 8)
-        for (int c = 0; c < chunks && ok; ++c) {
-            Slot &sl = slots[c % kSlots];
-            uint8_t *stage = smem + c % kStages * C::kStageBytes;
-            if (!(ok = wait(&g_full[c % kSlots], c / kSlots) && wait(&full[c % kStages], c / kStages))) break;
-            const int valid = min(rows - c * kChunk, kChunk);
-            // a piece's values, weighted
-            auto load = [&](int i, float2 (&x)[4]) {
-                const uint4 w = *reinterpret_cast<const uint4 *>(stage + C::kV + t * 16 + i * 2048);
-                x[0] = unpack2<F16>(w.x), x[1] = unpack2<F16>(w.y), x[2] = unpack2<F16>(w.z), x[3] = unpack2<F16>(w.w);
-            };
-            if (valid < kChunk) {  // behind the run's end, where whatever comes there lies: the products must not see it
-#pragma unroll 1
-                for (int i = 0; i < (C::kKBlocks + C::kVBlocks) * 4; ++i)
-                    if (r0 + (i & 3) * 16 >= valid)
-                        *reinterpret_cast<uint4 *>(stage + C::kK + t * 16 + i * 2048) = make_uint4(0, 0, 0, 0);
-            }
-            float2 sum = both(0.f);
-            float m = 0.f;
-#pragma unroll 2
-            for (int i = 0; i < kPieces; ++i) {
-                float2 x[4];
-                load(i, x);
-                const float f = sl.weight[r0 + (i & 3) * 16];
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    sum = __ffma2_rn(x[j], both(0.f), sum);
-                    if (F16) m = fmaxf(m, f * fmaxf(fabsf(x[j].x), fabsf(x[j].y)));
-                }
-            }
-            // A value that is not finite makes its channel of the state that; of the tokens before it the product with P must not
-            // see it (0 times it), so it is taken out of V in the end, and remembered for the tokens from it on.
-            const bool found = __any_sync(0xffffffffu, sum.x != 0.f || sum.y != 0.f);
-            auto each = [&](auto what) {
-#pragma unroll 1
-                for (int e = 0; e < kPieces * 8; ++e) {
-                    const int i = e >> 3, row = r0 + (i & 3) * 16;
-                    uint16_t *src = reinterpret_cast<uint16_t *>(stage + C::kV + t * 16 + i * 2048) + (e & 7);
-                    const float raw = load1<F16>(src);
-                    what(src, raw, fabsf(raw) <= 3.4028234e38f, row, (i >> 2) * 64 + ch0 + (e & 7));
-                }
-            };
-            if (F16 && found) {
-                m = 0.f;
-                each([&](uint16_t *, float raw, bool fine, int row, int) { m = fine ? fmaxf(m, fabsf(raw) * sl.weight[row]) : m; });
-            }
-            float unit = 1.f;
-            if (F16) {
-                m = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(m)));
-                float *all = most + (c & 1) * 4;
-                if (lane == 0) all[warp - kValueWarp] = m;
-                arrive(m_full);
-                if (!(ok = wait(m_full, c))) break;
-                const int e = lift(fmaxf(fmaxf(all[0], all[1]), fmaxf(all[2], all[3])));
-                unit = pow2f(e);
-                if (t == 0) sl.u_unit = pow2f(-e);
-            }
-            uint8_t *dst = smem + C::kValues + t * 16;
-#pragma unroll 1
-            for (int half = 0; half < 2; ++half) {  // tokens 0..31, 32..63
-                if (c > 0 && !(ok = wait(&v_free[half], c - 1))) break;  // the last chunk's have been read
-#pragma unroll 2
-                for (int n = 0; n < kPieces / 2; ++n) {
-                    const int i = (n >> 1) * 4 + half * 2 + (n & 1);
-                    float2 x[4];
-                    load(i, x);
-                    const float2 f = both(sl.weight[r0 + (i & 3) * 16] * unit);
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) x[j] = __fmul2_rn(x[j], f);
-#pragma unroll
-                    for (int part = 0; part < C::kParts; ++part) {
-                        uint32_t w[4];
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            w[j] = pack2<F16>(x[j].x, x[j].y);
-                            if (part + 1 < C::kParts) x[j] = rest<F16>(x[j], w[j]);
-                        }
-                        *reinterpret_cast<uint4 *>(dst + part * C::kPartBytes + i * 2048) = make_uint4(w[0], w[1], w[2], w[3]);
-                    }
-                }
-                if (half == 1 && found)
-                    each([&](uint16_t *src, float, bool fine, int row, int ch) {
-                        if (fine) return;
-                        *src = 0;
-                        atomicMin(&sl.bad[ch], row);
-                        sl.any_bad = 1;
-                    });
-                ptx::fence_proxy_async_smem();
-                arrive(&v_full[half]);
-            }
-            if (!ok) break;
-            arrive(&g_empty[c % kSlots]);
-        }
+        weigh_values();
     } else {
         ptx::regs_down<kOtherRegs>();
         if (warp < kLoadWarp) {
@@ -471,7 +486,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 for (int c = 0; c < chunks && ok; ++c) {
                     Slot &sl = slots[c % kSlots];
-                    if (!(ok = wait(&g_full[c % kSlots], c / kSlots) && wait(a_full, c))) break;
+                    if (!(ok = wait(&g_full[c % kSlots], c / kSlots) && wait(&a_full[c & 1], c >> 1))) break;
                     if (c > 0 && !(ok = wait(o_full, c - 1))) break;  // the last chunk's P has been read
                     ptx::tc_fence_after();
                     const float2 gh = both(-sl.g_hi[i]), gl = both(-sl.g_lo[i]);
@@ -479,7 +494,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     // 16 columns from j0 on: their largest (with fp16, whose rows are scaled), or their two parts into shared memory
                     auto weigh = [&](int j0, auto diagonal, bool put) {
                         uint32_t a[16];
-                        ptx::tmem_ld_16(lanes + C::kColA + j0, a);
+                        ptx::tmem_ld_16(lanes + C::kColA + (c & 1) * 64 + j0, a);
                         ptx::tmem_ld_wait();
 #pragma unroll
                         for (int j = 0; j < 16; ++j) asm volatile("" : "+r"(a[j]));
@@ -487,7 +502,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                         const int last = i - j0;
 #pragma unroll
                         for (int j = 0; j < 16; j += 2) {
-                            const float2 h = *reinterpret_cast<const float2 *>(&sl.g_hi[j0 + j]), l = *reinterpret_cast<const float2 *>(&sl.g_lo[j0 + j]);
+                            const float4 h4 = *reinterpret_cast<const float4 *>(&sl.g_hi[j0 + (j & ~3)]);
+                            const float4 l4 = *reinterpret_cast<const float4 *>(&sl.g_lo[j0 + (j & ~3)]);
+                            const float2 h = j & 2 ? make_float2(h4.z, h4.w) : make_float2(h4.x, h4.y);
+                            const float2 l = j & 2 ? make_float2(l4.z, l4.w) : make_float2(l4.x, l4.y);
                             const float2 g = __fadd2_rn(__fadd2_rn(gh, h), __fadd2_rn(gl, l));
                             float2 x = __fmul2_rn(make_float2(__uint_as_float(a[j]), __uint_as_float(a[j + 1])),
                                                   make_float2(exp2_fast(g.x), exp2_fast(g.y)));
@@ -523,7 +541,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                     }
                     ptx::tc_fence_before();
-                    arrive(a_free);
+                    arrive(&a_free[c & 1]);
                     ptx::fence_proxy_async_smem();
                     arrive(p_full);
                     arrive(&g_empty[c % kSlots]);
@@ -614,12 +632,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             auto logits = [&](int c) {  // A = Q K^T: 64 rows, and 64 that nobody reads
                 if (ptx::elect_one()) {
                     const uint64_t st = desc_k + at(c % kStages * C::kStageBytes);
-#pragma unroll 2
+#pragma unroll
                     for (int k = 0; k < DK / 16; ++k) {
                         const int off = (k >> 2) * kBlock16 + (k & 3) * 2;
-                        ptx::mma_f16_ss(tmem + C::kColA, st + off, st + at(C::kK) + off, idesc_a, k > 0);
+                        ptx::mma_f16_ss(tmem + C::kColA + (c & 1) * 64, st + off, st + at(C::kK) + off, idesc_a, k > 0);
                     }
-                    ptx::mma_commit(a_full);
+                    ptx::mma_commit(&a_full[c & 1]);
                 }
                 __syncwarp();
             };
@@ -631,13 +649,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int c = 0; c < chunks && ok; ++c) {
                 const int stage = c % kStages * C::kStageBytes;
                 if (!STATES && c + 1 < chunks) {
-                    if (!(ok = wait(&full[(c + 1) % kStages], (c + 1) / kStages) && wait(a_free, c))) break;
+                    if (!(ok = wait(&full[(c + 1) % kStages], (c + 1) / kStages) && (c == 0 || wait(&a_free[(c + 1) & 1], (c - 1) >> 1)))) break;
                     ptx::tc_fence_after();
                     logits(c + 1);
                 }
                 // U^T = (w V)^T K
                 if (STATES && !(ok = wait(&full[c % kStages], c / kStages))) break;
-                if (!(ok = c == 0 || wait(u_free, c - 1))) break;
+                if (!(ok = c < kUs || wait(&u_free[c % kUs], c / kUs - 1))) break;
 #pragma unroll 1
                 for (int half = 0; half < 2; ++half) {
                     if (!(ok = wait(&v_full[half], c))) break;
@@ -647,12 +665,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                         for (int part = 0; part < C::kParts; ++part)
 #pragma unroll
                             for (int k = 2 * half; k < 2 * half + 2; ++k)
-                                ptx::mma_f16_ss(tmem + C::kColU, desc_mn + at(C::kValues + part * C::kPartBytes + k * 2048),
+                                ptx::mma_f16_ss(tmem + C::kColU + c % kUs * 128, desc_mn + at(C::kValues + part * C::kPartBytes + k * 2048),
                                                 desc_mn + at(stage + C::kK + k * 2048), idesc_u, part > 0 || k > 0);
                         ptx::mma_commit(&v_free[half]);
                         if (half == 1) {
-                            ptx::mma_commit(u_full);
-                            ptx::mbar_arrive(u_full);
+                            ptx::mma_commit(&u_full[c % kUs]);
+                            ptx::mbar_arrive(&u_full[c % kUs]);
                             if (STATES) ptx::mma_commit(&empty[c % kStages]);
                         }
                     }
@@ -666,7 +684,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (ptx::elect_one()) {
 #pragma unroll 1
                     for (int part = 0; part < 2; ++part)
-#pragma unroll 2
+#pragma unroll
                         for (int k = 0; k < DK / 16; ++k)
                             ptx::mma_f16_ts(tmem + C::kColO1, tmem + C::kColS + part * (DK / 2) + k * 8,
                                             desc_k + at(stage) + (k >> 2) * kBlock16 + (k & 3) * 2, idesc_o1, part > 0 || k > 0);
@@ -679,7 +697,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (ptx::elect_one()) {
 #pragma unroll 1
                     for (int part = 0; part < 2; ++part)
-#pragma unroll 2
+#pragma unroll
                         for (int k = 0; k < kChunk / 16; ++k)
                             ptx::mma_f16_ss(tmem + C::kColO2, desc_mn + at(stage + C::kV + k * 2048),
                                             desc_k + at(C::kP + part * kBlockBytes) + k * 2, idesc_o2, part > 0 || k > 0);
