@@ -63,9 +63,10 @@ const DeviceInfo &device_info();
 bool encode_tmap_2d_bf16(CUtensorMap *map, const void *base, uint64_t rows, uint64_t cols,
                          uint32_t box_rows, uint32_t box_cols, bool swizzle128 = true);
 
-// The same over rows of 16-bit values (either type) that lie `ld` elements apart.
-bool encode_tmap_rows(CUtensorMap *map, const void *base, uint64_t rows, uint64_t cols, uint64_t ld, uint32_t box_rows,
-                      uint32_t box_cols);
+// Rows of 16-bit values (either type) that lie `ld` elements apart, in blocks of 64 columns: a box holds box_blocks
+// blocks, one after another, of box_rows rows of 128 bytes each, 128-byte swizzle.
+bool encode_tmap_blocks(CUtensorMap *map, const void *base, uint64_t rows, uint64_t cols, uint64_t ld, uint32_t box_rows,
+                        uint32_t box_blocks);
 
 // ---- GEMM (tcgen05, swap-AB: weight rows on M, tokens on N) ---------------------------
 

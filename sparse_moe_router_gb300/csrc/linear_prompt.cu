@@ -105,13 +105,24 @@ __device__ __forceinline__ void split2(float2 x, uint32_t &hi, uint32_t &lo) {
     lo = pack2<F16>(r.x, r.y);
 }
 
-// log2 of a decay in units of 2^-40: sums of 64 of them (2^20 at most) are exact, and 64-bit integers cost a fraction of
-// what 64-bit floats do here.
-constexpr float kFixed = 1.f / (1ull << 40);
-__device__ __forceinline__ int64_t fixed_log2(float g) {
-    constexpr float kHi = 1.44269502f, kLo = 1.92596303e-8f;  // log2(e)
-    const float hi = g * kHi, lo = fmaf(g, kHi, -hi) + g * kLo;
-    return __float2ll_rn(hi * (1.f / kFixed)) + __float2ll_rn(lo * (1.f / kFixed));
+// A sum of logs in two floats (48 bits): a chunk's decays differ by what is small beside their sum from its begin, and
+// 64-bit floats cost 16 cycles each here.
+struct Two {
+    float hi, lo;
+};
+__device__ __forceinline__ Two two_sum(float a, float b) {  // a + b exactly (Knuth)
+    const float s = a + b, v = s - a;
+    return {s, (a - (s - v)) + (b - v)};
+}
+__device__ __forceinline__ Two operator+(Two a, Two b) {
+    const Two s = two_sum(a.hi, b.hi);
+    const float lo = s.lo + (a.lo + b.lo), hi = s.hi + lo;
+    return {hi, lo - (hi - s.hi)};
+}
+__device__ __forceinline__ Two log2_of(float g) {  // g log2(e)
+    constexpr float kHi = 1.44269502f, kLo = 1.92596303e-8f;
+    const float hi = g * kHi;
+    return {hi, fmaf(g, kLo, fmaf(g, kHi, -hi))};
 }
 
 // Where sequence b's segments lie among the batch's.
@@ -549,76 +560,57 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         } else if (warp == kLoadWarp) {
             // -------------------------------------------------------------- copies, decays --
-            int64_t total = 0;  // log2 of the segment's decay
-            if (lane == 0) {
-                ptx::tma_prefetch_desc(&maps.k);
-                ptx::tma_prefetch_desc(&maps.v);
-                if (!STATES) ptx::tma_prefetch_desc(&maps.q);
-            }
+            Two total{0.f, 0.f};  // log2 of the segment's decay
+            // Lanes 0, 1 (, 2) copy a chunk's tokens of K, V (and Q); lanes 8, 9 (, 10) bring those of a later chunk into L2.
+            constexpr int kBoxes = STATES ? 2 : 3;
+            const int box = lane & 7;
+            const CUtensorMap *map = box == 0 ? &maps.k : box == 1 ? &maps.v : &maps.q;
+            const int box_block = box == 1 ? col0 / 64 : kh * C::kKBlocks, box_at = box == 0 ? C::kK : box == 1 ? C::kV : 0;
+            if (lane < kBoxes) ptx::tma_prefetch_desc(map);
             // the decays of two tokens a lane, on their way two chunks ahead
             auto decays = [&](int c) {
                 const int i = c * kChunk + 2 * lane;
                 return make_float2(i < rows ? raw_decay(p, row0 + i, head) : 0.f, i + 1 < rows ? raw_decay(p, row0 + i + 1, head) : 0.f);
             };
-            auto copies = [&](auto copy, int c) {  // of a chunk, each a box of 64 tokens and 64 channels
-                const int row = (int)row0 + c * kChunk;
-#pragma unroll
-                for (int i = 0; i < C::kKBlocks; ++i) {
-                    copy(&maps.k, kh * DK + i * 64, row, C::kK + i * kBlockBytes);
-                    if (!STATES) copy(&maps.q, kh * DK + i * 64, row, i * kBlockBytes);
-                }
-#pragma unroll
-                for (int i = 0; i < C::kVBlocks; ++i) copy(&maps.v, col0 + i * 64, row, C::kV + i * kBlockBytes);
-            };
-            auto fetch = [](const CUtensorMap *map, int x, int row, int) { ptx::tma_prefetch_2d(map, x, row); };
             float2 g = decays(0), g1 = decays(1);
-            if (lane == 0)
-                for (int c = kStages; c < min(kStages + kFetch, chunks); ++c) copies(fetch, c);
+            if (lane >= 8 && lane < 8 + kBoxes)
+                for (int c = kStages; c < min(kStages + kFetch, chunks); ++c) ptx::tma_prefetch_3d(map, 0, (int)row0 + c * kChunk, box_block);
             for (int c = 0; c < chunks && ok; ++c) {
-                const int st = c % kStages;
+                const int st = c % kStages, row = (int)row0 + c * kChunk;
                 const float2 g2 = decays(c + 2);
                 if (c >= kStages && !(ok = wait(&empty[st], c / kStages - 1))) break;
-                if (lane == 0) {
-                    uint8_t *stage = smem + st * C::kStageBytes;
-                    ptx::mbar_arrive_expect_tx(&full[st], (uint32_t)(C::kStageBytes - (STATES ? C::kK : 0)));
-                    copies([&](const CUtensorMap *map, int x, int row, int to) { ptx::tma_load_2d(stage + to, map, x, row, &full[st]); }, c);
-                    if (c + kStages + kFetch < chunks) copies(fetch, c + kStages + kFetch);
-                }
+                if (lane == 0) ptx::mbar_arrive_expect_tx(&full[st], (uint32_t)(C::kStageBytes - (STATES ? C::kK : 0)));
+                __syncwarp();
+                if (lane < kBoxes) ptx::tma_load_3d(smem + st * C::kStageBytes + box_at, map, 0, row, box_block, &full[st]);
+                else if (lane >= 8 && lane < 8 + kBoxes && c + kStages + kFetch < chunks)
+                    ptx::tma_prefetch_3d(map, 0, row + (kStages + kFetch) * kChunk, box_block);
                 issued = c + 1;
                 if (c >= kSlots && !(ok = wait(&g_empty[c % kSlots], c / kSlots - 1))) break;
-                const int64_t l0 = fixed_log2(checked_decay(p, g.x)), l1 = fixed_log2(checked_decay(p, g.y));
+                const Two l0 = log2_of(checked_decay(p, g.x)), l1 = log2_of(checked_decay(p, g.y));
                 g = g1, g1 = g2;
-                int64_t sum = l0 + l1;
+                Two G = l0 + l1;  // up to the lane's second token
 #pragma unroll
                 for (int o = 1; o < 32; o <<= 1) {
-                    const int64_t x = __shfl_up_sync(0xffffffffu, sum, o);
-                    if (lane >= o) sum += x;
+                    const Two x{__shfl_up_sync(0xffffffffu, G.hi, o), __shfl_up_sync(0xffffffffu, G.lo, o)}, y = x + G;
+                    if (lane >= o) G = y;
                 }
-                const int64_t end = __shfl_sync(0xffffffffu, sum, 31);
-                total = max((long long)(total + end), -(1ll << 60));
+                const Two end{__shfl_sync(0xffffffffu, G.hi, 31), __shfl_sync(0xffffffffu, G.lo, 31)};
+                const Two G0 = G + Two{-l1.hi, -l1.lo};
+                total = total + end;
                 Slot &sl = slots[c % kSlots];
-                float hi[2], lo[2], fade[2], weight[2];
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const int64_t G = e ? sum : sum - l1;
-                    hi[e] = __ll2float_rn(G);
-                    lo[e] = __ll2float_rn(__float2ll_rn(hi[e]) - G) * kFixed;
-                    hi[e] *= -kFixed;
-                    fade[e] = p.scale * exp2_fast(-hi[e]);
-                    weight[e] = exp2_fast(__ll2float_rn(end - G) * kFixed);
-                }
-                reinterpret_cast<float2 *>(sl.g_hi)[lane] = make_float2(hi[0], hi[1]);
-                reinterpret_cast<float2 *>(sl.g_lo)[lane] = make_float2(lo[0], lo[1]);
-                reinterpret_cast<float2 *>(sl.fade)[lane] = make_float2(fade[0], fade[1]);
-                reinterpret_cast<float2 *>(sl.weight)[lane] = make_float2(weight[0], weight[1]);
+                reinterpret_cast<float2 *>(sl.g_hi)[lane] = make_float2(-G0.hi, -G.hi);
+                reinterpret_cast<float2 *>(sl.g_lo)[lane] = make_float2(-G0.lo, -G.lo);
+                reinterpret_cast<float2 *>(sl.fade)[lane] = make_float2(p.scale * exp2_fast(G0.hi), p.scale * exp2_fast(G.hi));
+                reinterpret_cast<float2 *>(sl.weight)[lane] =
+                    make_float2(exp2_fast((end.hi - G0.hi) + (end.lo - G0.lo)), exp2_fast((end.hi - G.hi) + (end.lo - G.lo)));
                 for (int i = lane; i < 128; i += 32) sl.bad[i] = kChunk;
                 if (lane == 0) {
-                    sl.whole = exp2_fast(__ll2float_rn(end) * kFixed);
+                    sl.whole = exp2_fast(end.hi);
                     sl.any_bad = 0;
                 }
                 arrive(&g_full[c % kSlots]);
             }
-            if (STATES && ok && lane == 0 && tile == 0) p.seg_decay[(int64_t)place * p.VH + head] = exp2_fast(__ll2float_rn(total) * kFixed);
+            if (STATES && ok && lane == 0 && tile == 0) p.seg_decay[(int64_t)place * p.VH + head] = exp2_fast(total.hi);
         } else {
             // -------------------------------------------------------------------- the MMAs --
             const uint32_t idesc_a = ptx::idesc_16_f32(F16, 128, kChunk, false, false);
@@ -745,9 +737,9 @@ cudaError_t launch_kernel(const LinearArgs &a, const Maps &m, cudaStream_t s) {
 template <int DK, int DV, bool F16>
 cudaError_t launch(const LinearArgs &a, cudaStream_t s) {
     Maps m;
-    if (!encode_tmap_rows(&m.q, a.q, a.n_tokens, (uint64_t)a.KH * DK, a.q_ld, kChunk, 64) ||
-        !encode_tmap_rows(&m.k, a.k, a.n_tokens, (uint64_t)a.KH * DK, a.k_ld, kChunk, 64) ||
-        !encode_tmap_rows(&m.v, a.v, a.n_tokens, (uint64_t)a.VH * a.DV, a.v_ld, kChunk, 64))
+    if (!encode_tmap_blocks(&m.q, a.q, a.n_tokens, (uint64_t)a.KH * DK, a.q_ld, kChunk, DK / 64) ||
+        !encode_tmap_blocks(&m.k, a.k, a.n_tokens, (uint64_t)a.KH * DK, a.k_ld, kChunk, DK / 64) ||
+        !encode_tmap_blocks(&m.v, a.v, a.n_tokens, (uint64_t)a.VH * a.DV, a.v_ld, kChunk, DV / 64))
         return cudaErrorInvalidValue;
     if (a.seg_states) {
         const cudaError_t e = launch_kernel<DK, DV, F16, true>(a, m, s);

@@ -103,11 +103,11 @@ PFN_cuTensorMapEncodeTiled_v12000 get_encode() {
 
 namespace {
 bool encode_tmap_2d(CUtensorMap *map, const void *base, uint64_t rows, uint64_t cols, uint32_t box_rows,
-                    uint32_t box_cols, bool swizzle128, CUtensorMapDataType dtype, uint64_t esize, uint64_t ld = 0) {
+                    uint32_t box_cols, bool swizzle128, CUtensorMapDataType dtype, uint64_t esize) {
     PFN_cuTensorMapEncodeTiled_v12000 enc = get_encode();
     if (!enc) return false;
     cuuint64_t dims[2] = {cols, rows};
-    cuuint64_t strides[1] = {(ld ? ld : cols) * esize};
+    cuuint64_t strides[1] = {cols * esize};
     cuuint32_t box[2] = {box_cols, box_rows};
     cuuint32_t estr[2] = {1, 1};
     CUresult r = enc(map, dtype, 2, const_cast<void *>(base), dims, strides, box,
@@ -123,9 +123,16 @@ bool encode_tmap_2d_bf16(CUtensorMap *map, const void *base, uint64_t rows, uint
     return encode_tmap_2d(map, base, rows, cols, box_rows, box_cols, swizzle128, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2);
 }
 
-bool encode_tmap_rows(CUtensorMap *map, const void *base, uint64_t rows, uint64_t cols, uint64_t ld, uint32_t box_rows,
-                      uint32_t box_cols) {
-    return encode_tmap_2d(map, base, rows, cols, box_rows, box_cols, true, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, ld);
+bool encode_tmap_blocks(CUtensorMap *map, const void *base, uint64_t rows, uint64_t cols, uint64_t ld, uint32_t box_rows,
+                        uint32_t box_blocks) {
+    PFN_cuTensorMapEncodeTiled_v12000 enc = get_encode();
+    if (!enc || cols % 64) return false;
+    cuuint64_t dims[3] = {64, rows, cols / 64};
+    cuuint64_t strides[2] = {ld * 2, 128};
+    cuuint32_t box[3] = {64, box_rows, box_blocks};
+    cuuint32_t estr[3] = {1, 1, 1};
+    return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 bool encode_token_maps(TokenMaps *tm, const void *base, uint64_t rows, uint64_t cols) {
