@@ -37,6 +37,8 @@ enum KernelClass {
     KC_LINEAR_STATES,     // the states at the begin of a run's segments
     KC_HEAD_NORM,         // the heads' norm with its gate
     KC_PROJECT_ROWS,      // a product with its epilogue, few rows
+    KC_PROJECT_BATCH,     // ... a few hundred rows, or few outputs
+    KC_PROJECT_TILES,     // ... many
     KC_COUNT
 };
 
@@ -63,7 +65,10 @@ const DeviceInfo &device_info();
 bool encode_tmap_2d_bf16(CUtensorMap *map, const void *base, uint64_t rows, uint64_t cols,
                          uint32_t box_rows, uint32_t box_cols, bool swizzle128 = true);
 
-// Rows of 16-bit values (either type) that lie `ld` elements apart, in blocks of 64 columns: a box holds box_blocks
+// Rows of 16-bit values (either type) that lie `ld` elements apart: boxes of box_rows rows and 64 columns, 128-byte
+// swizzle; what lies outside reads as 0.
+bool encode_tmap_rows(CUtensorMap *map, const void *base, uint64_t rows, uint64_t cols, uint64_t ld, uint32_t box_rows);
+// The same in blocks of 64 columns: a box holds box_blocks
 // blocks, one after another, of box_rows rows of 128 bytes each, 128-byte swizzle.
 bool encode_tmap_blocks(CUtensorMap *map, const void *base, uint64_t rows, uint64_t cols, uint64_t ld, uint32_t box_rows,
                         uint32_t box_blocks);

@@ -18,6 +18,8 @@
 //
 // Roles (16 warps): 0-3 the state; 4-7 the output; 8-11 weighted values; 12, 13 P (a row a thread); 14 copies (TMA)
 // and decays; 15 the MMAs.
+#include <atomic>
+
 #include "mixer.h"
 #include "ptx.cuh"
 
@@ -725,8 +727,15 @@ template <int DK, int DV, bool F16, bool STATES>
 cudaError_t launch_kernel(const LinearArgs &a, const Maps &m, cudaStream_t s) {
     constexpr int smem = Shape<DK, DV, F16>::kSmem;
     auto *kernel = linear_chunk_kernel<DK, DV, F16, STATES>;
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e != cudaSuccess) return e;
+    static std::atomic<bool> ready[64];  // of each device: the shared-memory opt-in
+    int dev = 0;
+    cudaGetDevice(&dev);
+    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    if (!ready[dev].load(std::memory_order_acquire)) {
+        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        if (e != cudaSuccess) return e;
+        ready[dev].store(true, std::memory_order_release);
+    }
     const int64_t segments = linear_segments(a.n_tokens, a.n_seqs, a.segment_chunks), blocks = segments * a.VH * (a.DV / DV);
     if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
     LaunchScope scope(STATES ? KC_LINEAR_STATES : KC_LINEAR_CHUNKS, s);

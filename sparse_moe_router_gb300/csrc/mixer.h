@@ -49,7 +49,9 @@ struct ProjectArgs {
     float scale;
     int *status;
 };
-cudaError_t launch_project_rows(const ProjectArgs &a, int dtype, cudaStream_t s);
+cudaError_t launch_project_rows(const ProjectArgs &a, int dtype, cudaStream_t s);   // a few rows
+cudaError_t launch_project_batch(const ProjectArgs &a, int dtype, cudaStream_t s);  // at most 256 rows or outputs
+cudaError_t launch_project_tiles(const ProjectArgs &a, int dtype, cudaStream_t s);  // any
 
 // A log decay below this counts as this: its factor is 0 in fp32, and sums of 64 stay finite.
 constexpr float kLeastDecay = -10000.f;
@@ -72,6 +74,56 @@ __device__ __forceinline__ float activate(float z, int act) {
         case MOE_ACT_SIGMOID: return sigmoid_fast(z);
         case MOE_ACT_LOG_SIGMOID: return fminf(z, 0.f) - log1pf(expf(-fabsf(z)));
         default: return z;
+    }
+}
+
+// The epilogue of V outputs of one row from output n on: z + bias, activation, scale, residual, one rounding, one store.
+template <int V, bool F16>
+__device__ __forceinline__ void finish(const ProjectArgs &p, int64_t t, int n, float (&z)[V], const float (&bias)[V]) {
+#pragma unroll
+    for (int j = 0; j < V; ++j) z[j] += bias[j];
+    if (p.act != MOE_ACT_NONE) {
+#pragma unroll
+        for (int j = 0; j < V; ++j) z[j] = activate(z[j], p.act);
+    }
+#pragma unroll
+    for (int j = 0; j < V; ++j) z[j] *= p.scale;
+    if (p.out_f32) {
+        if (p.resid) {
+            const float4 *r = reinterpret_cast<const float4 *>(static_cast<const float *>(p.resid) + t * p.resid_ld + n);
+#pragma unroll
+            for (int j = 0; j < V / 4; ++j) z[4 * j] += r[j].x, z[4 * j + 1] += r[j].y, z[4 * j + 2] += r[j].z, z[4 * j + 3] += r[j].w;
+        }
+        float4 *y = reinterpret_cast<float4 *>(static_cast<float *>(p.y) + t * p.y_ld + n);
+#pragma unroll
+        for (int j = 0; j < V / 4; ++j) y[j] = make_float4(z[4 * j], z[4 * j + 1], z[4 * j + 2], z[4 * j + 3]);
+    } else {
+        if (p.resid) {
+            const uint2 *r = reinterpret_cast<const uint2 *>(static_cast<const uint16_t *>(p.resid) + t * p.resid_ld + n);
+#pragma unroll
+            for (int j = 0; j < V / 4; ++j) {
+                const uint2 w = r[j];
+                const float2 a = unpack2<F16>(w.x), b = unpack2<F16>(w.y);
+                z[4 * j] += a.x, z[4 * j + 1] += a.y, z[4 * j + 2] += b.x, z[4 * j + 3] += b.y;
+            }
+        }
+        uint32_t w[V / 2];
+#pragma unroll
+        for (int j = 0; j < V / 2; ++j) w[j] = pack2<F16>(z[2 * j], z[2 * j + 1]);
+        uint16_t *y = static_cast<uint16_t *>(p.y) + t * p.y_ld + n;
+        if constexpr (V == 8) *reinterpret_cast<uint4 *>(y) = make_uint4(w[0], w[1], w[2], w[3]);
+        else *reinterpret_cast<uint2 *>(y) = make_uint2(w[0], w[1]);
+    }
+}
+// (0 without a bias)
+template <int V, bool F16>
+__device__ __forceinline__ void load_bias(const ProjectArgs &p, int n, float (&bias)[V]) {
+#pragma unroll
+    for (int j = 0; j < V; j += 4) {
+        uint2 w = make_uint2(0, 0);
+        if (p.bias) w = __ldg(reinterpret_cast<const uint2 *>(p.bias + n + j));
+        const float2 a = unpack2<F16>(w.x), b = unpack2<F16>(w.y);
+        bias[j] = a.x, bias[j + 1] = a.y, bias[j + 2] = b.x, bias[j + 3] = b.y;
     }
 }
 

@@ -238,7 +238,10 @@ moe_status moe_project(const moe_project_config *cfg, const moe_project_io *io, 
     a.out_f32 = c.out_f32;
     a.scale = c.scale;
     a.status = static_cast<int *>(ws);
-    MOE_CUDA(launch_project_rows(a, c.dtype, static_cast<cudaStream_t>(stream)));
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (T <= 4) MOE_CUDA(launch_project_rows(a, c.dtype, s));
+    else if (T <= 256 || c.outputs <= 64) MOE_CUDA(launch_project_batch(a, c.dtype, s));
+    else MOE_CUDA(launch_project_tiles(a, c.dtype, s));
     return MOE_OK;
 }
 

@@ -37,7 +37,8 @@ const char *const kClassNames[KC_COUNT] = {
     "down_gemm",   "shared_gateup", "shared_down", "finalize",      "combine",
     "zero",        "decode_router", "decode_experts", "gather_x",
     "decode_chain", "quantize", "block_norm", "kv_append", "attn_split", "attn_join", "attn_prompt",
-    "linear_tokens", "linear_chunks", "linear_states", "head_norm", "project_rows"};
+    "linear_tokens", "linear_chunks", "linear_states", "head_norm", "project_rows",
+    "project_batch", "project_tiles"};
 }  // namespace
 
 const char *kernel_class_name(int kc) { return (kc >= 0 && kc < KC_COUNT) ? kClassNames[kc] : nullptr; }
@@ -121,6 +122,17 @@ bool encode_tmap_2d(CUtensorMap *map, const void *base, uint64_t rows, uint64_t 
 bool encode_tmap_2d_bf16(CUtensorMap *map, const void *base, uint64_t rows, uint64_t cols,
                          uint32_t box_rows, uint32_t box_cols, bool swizzle128) {
     return encode_tmap_2d(map, base, rows, cols, box_rows, box_cols, swizzle128, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2);
+}
+
+bool encode_tmap_rows(CUtensorMap *map, const void *base, uint64_t rows, uint64_t cols, uint64_t ld, uint32_t box_rows) {
+    PFN_cuTensorMapEncodeTiled_v12000 enc = get_encode();
+    if (!enc) return false;
+    cuuint64_t dims[2] = {cols, rows};
+    cuuint64_t strides[1] = {ld * 2};
+    cuuint32_t box[2] = {64, box_rows};
+    cuuint32_t estr[2] = {1, 1};
+    return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 bool encode_tmap_blocks(CUtensorMap *map, const void *base, uint64_t rows, uint64_t cols, uint64_t ld, uint32_t box_rows,
