@@ -158,7 +158,7 @@ moe_status moe_linear_attention(const moe_linear_config *cfg, const moe_state_po
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     // Which runs the chunk kernel takes goes by their own lengths, which only the device knows.  The host leaves a
     // kernel out that has none for sure, and the chunk kernel in a step of one token a sequence.
-    const bool chunks = batch->n_tokens >= kChunkTokens && batch->n_tokens > batch->n_seqs;
+    const bool chunks = batch->n_seqs == 1 ? batch->n_tokens >= kChunkTokens : batch->n_tokens - batch->n_seqs >= kChunkTokens;
     a.chunk_tokens = !chunks ? INT_MAX : batch->n_seqs == 1 ? 0 : kChunkTokens;
     if (chunks) {
         a.segment_chunks = segment_chunks(c, batch->n_seqs, batch->n_tokens);

@@ -68,7 +68,9 @@ __global__ void __launch_bounds__(kThreads) project_rows_kernel(const __grid_con
 #pragma unroll
         for (int s = 0; s < S; ++s) z += part[g * S + s][i * X + j];
         if (p.bias) z += load1<F16>(p.bias + n);
-        z = p.scale * activate(z, p.act);
+        float v[1] = {z};
+        activate(v, p.act);
+        z = p.scale * v[0];
         if (p.out_f32) {
             if (p.resid) z += static_cast<const float *>(p.resid)[t * p.resid_ld + n];
             static_cast<float *>(p.y)[t * p.y_ld + n] = z;
