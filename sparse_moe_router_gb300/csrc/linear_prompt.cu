@@ -28,9 +28,13 @@ namespace {
 
 constexpr int kThreads = 512;
 constexpr int kOutWarp = 4, kValueWarp = 8, kWeightWarp = 12, kLoadWarp = 14, kMmaWarp = 15;
-// Registers a thread: 128 at launch; of a scheduler's 4 x 128 the state's warp, which holds 128 of them, takes 216.
-constexpr int kStateRegs = 216, kOutRegs = 96, kValueRegs = 80, kOtherRegs = 120;
-static_assert(kStateRegs + kOutRegs + kValueRegs + kOtherRegs <= 512, "more registers than the block has");
+// Registers a thread: 128 at launch; of a scheduler's 4 x 128 the state's warp, which holds 128 of them, takes most (less
+// and the roles spill, into an L1 that shared memory has left next to nothing of).
+template <bool STATES>
+struct Regs {
+    static constexpr int kState = STATES ? 216 : 232, kOut = STATES ? 96 : 80, kValue = 80, kOther = 120;
+    static_assert(kState + kOut + kValue + kOther <= 512, "more registers than the block has");
+};
 constexpr uint64_t kWaitNs = 2000000000ull;  // 2 s, of the waits when a block gives up
 constexpr int kBlockBytes = kChunk * 128;    // 64 tokens x 64 channels
 constexpr int kFetch = 2;                    // chunks beyond the stages that are brought into L2
@@ -159,6 +163,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int tid = (int)threadIdx.x, lane = tid & 31;
     const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);  // known to be the same in all lanes
 
+    if (!STATES) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // (the token kernel does not depend on this one)
+
     // ------------------------------------------------------------------- the block's chunks --
     const int tiles = p.DV / DV;
     const int tile = (int)blockIdx.x % tiles, head = (int)blockIdx.x / tiles % p.VH, place = (int)blockIdx.x / tiles / p.VH;
@@ -235,10 +241,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!(ok = wait(&g_full[c % kSlots], c / kSlots) && wait(&full[c % kStages], c / kStages))) break;
             const int valid = min(rows - c * kChunk, kChunk);
             auto row_of = [&](int i) { return r0 + i * kRowStep % kChunk; };
-            auto load = [&](int i, float2 (&x)[4]) {
-                const uint4 w = *reinterpret_cast<const uint4 *>(stage + C::kV + t * 16 + i * kStep);
-                x[0] = unpack2<F16>(w.x), x[1] = unpack2<F16>(w.y), x[2] = unpack2<F16>(w.z), x[3] = unpack2<F16>(w.w);
-            };
+            auto piece = [&](int i) { return reinterpret_cast<uint4 *>(stage + C::kV + t * 16 + i * kStep); };
             if (valid < kChunk) {  // behind the run's end, where whatever comes there lies: the products must not see it
 #pragma unroll 1
                 for (int i = 0; i < (C::kKBlocks + C::kVBlocks) * kBlockBytes / kStep; ++i)
@@ -247,16 +250,24 @@ __global__ void __launch_bounds__(kThreads, 1)
             float unit = 1.f;
             if (F16) {  // the chunk's largest finite one
                 float m = 0.f;
-#pragma unroll 2
-                for (int i = 0; i < kPieces; ++i) {
-                    float2 x[4];
-                    load(i, x);
-                    const float f = sl.weight[row_of(i)];
+                uint4 w[kPieces];
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const float a = f * fabsf(x[j].x), b = f * fabsf(x[j].y);
-                        m = fmaxf(m, fmaxf(a <= 3.4028234e38f ? a : 0.f, b <= 3.4028234e38f ? b : 0.f));
+                for (int i = 0; i < kPieces; ++i) w[i] = *piece(i);
+#pragma unroll
+                for (int i = 0; i < kPieces; ++i) {
+                    const __half2 *h = reinterpret_cast<const __half2 *>(&w[i]);
+                    const __half2 most2 = __hmax2(__hmax2(__habs2(h[0]), __habs2(h[1])), __hmax2(__habs2(h[2]), __habs2(h[3])));
+                    const float2 a = __half22float2(most2);
+                    float top = fmaxf(a.x, a.y);
+                    if (top > 65504.f) {  // an infinity: the largest of the others
+                        top = 0.f;
+#pragma unroll 1
+                        for (int j = 0; j < 8; ++j) {
+                            const float x = fabsf(load1<F16>(reinterpret_cast<const uint16_t *>(piece(i)) + j));
+                            if (x <= 65504.f) top = fmaxf(top, x);
+                        }
                     }
+                    m = fmaxf(m, top * sl.weight[row_of(i)]);
                 }
                 m = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(m)));
                 float *all = most + (c & 1) * 8;
@@ -274,16 +285,18 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
             for (int half = 0; half < 2; ++half) {  // tokens 0..31, 32..63
                 if (c > 0 && !(ok = wait(&v_free[half], c - 1))) break;  // the last chunk's have been read
-#pragma unroll 2
+                uint4 raw[kPieces / 2];  // (loads cannot pass the stores by themselves)
+                float weight[kPieces / 2];
+                auto number = [&](int n) { return n / kHalf * (2 * kHalf) + half * kHalf + n % kHalf; };
+#pragma unroll
+                for (int n = 0; n < kPieces / 2; ++n) raw[n] = *piece(number(n)), weight[n] = sl.weight[row_of(number(n))] * unit;
+#pragma unroll
                 for (int n = 0; n < kPieces / 2; ++n) {
-                    const int i = n / kHalf * (2 * kHalf) + half * kHalf + n % kHalf;
-                    float2 x[4];
-                    load(i, x);
-                    const float2 f = both(sl.weight[row_of(i)] * unit);
+                    float2 x[4] = {unpack2<F16>(raw[n].x), unpack2<F16>(raw[n].y), unpack2<F16>(raw[n].z), unpack2<F16>(raw[n].w)};
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
                         sum = __ffma2_rn(x[j], both(0.f), sum);
-                        x[j] = __fmul2_rn(x[j], f);
+                        x[j] = __fmul2_rn(x[j], both(weight[n]));
                     }
 #pragma unroll
                     for (int part = 0; part < C::kParts; ++part) {
@@ -293,7 +306,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             w[j] = pack2<F16>(x[j].x, x[j].y);
                             if (part + 1 < C::kParts) x[j] = rest<F16>(x[j], w[j]);
                         }
-                        *reinterpret_cast<uint4 *>(dst + part * C::kPartBytes + i * kStep) = make_uint4(w[0], w[1], w[2], w[3]);
+                        *reinterpret_cast<uint4 *>(dst + part * C::kPartBytes + number(n) * kStep) = make_uint4(w[0], w[1], w[2], w[3]);
                     }
                 }
                 // A value that is not finite makes its channel of the state that; of the tokens before it the product with P must
@@ -302,7 +315,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
                     for (int e = 0; e < kPieces * 8; ++e) {
                         const int i = e >> 3;
-                        uint16_t *src = reinterpret_cast<uint16_t *>(stage + C::kV + t * 16 + i * kStep) + (e & 7);
+                        uint16_t *src = reinterpret_cast<uint16_t *>(piece(i)) + (e & 7);
                         if (fabsf(load1<F16>(src)) <= 3.4028234e38f) continue;
                         *src = 0;
                         atomicMin(&sl.bad[i * kRowStep / kChunk * 64 + ch0 + (e & 7)], row_of(i));
@@ -319,7 +332,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
 
     if (warp < kOutWarp) {
-        ptx::regs_up<kStateRegs>();
+        ptx::regs_up<Regs<STATES>::kState>();
         if (warp < C::kLaneWarps) {
             // ------------------------------------------------------------------ the state --
             // Thread t has channel t: S[d] of all key channels d.
@@ -407,7 +420,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (ok && (STATES || (seg == segs - 1 && run.slot >= 0))) store(STATES ? place_at(seg) : own);
         }
     } else if (warp < kValueWarp) {
-        ptx::regs_down<kOutRegs>();
+        ptx::regs_down<Regs<STATES>::kOut>();
         if (STATES) {
             weigh_values();
         } else if (warp - kOutWarp < C::kLaneWarps) {
@@ -478,10 +491,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         }
     } else if (warp < kWeightWarp) {
-        ptx::regs_down<kValueRegs>();
+        ptx::regs_down<Regs<STATES>::kValue>();
         weigh_values();
     } else {
-        ptx::regs_down<kOtherRegs>();
+        ptx::regs_down<Regs<STATES>::kOther>();
         if (warp < kLoadWarp) {
             if (!STATES) {
                 // -------------------------------------------------------------------------- P --
@@ -500,7 +513,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int c = 0; c < chunks && ok; ++c) {
                     Slot &sl = slots[c % kSlots];
                     if (!(ok = wait(&g_full[c % kSlots], c / kSlots) && wait(&a_full[c & 1], c >> 1))) break;
-                    if (c > 0 && !(ok = wait(o_full, c - 1))) break;  // the last chunk's P has been read
                     ptx::tc_fence_after();
                     const float2 gh = both(-sl.g_hi[i]), gl = both(-sl.g_lo[i]);
                     float m = 0.f, f = 1.f;
@@ -542,6 +554,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     };
 #pragma unroll 1
                     for (int pass = F16 ? 0 : 1; pass < 2; ++pass) {
+                        if (pass == 1 && c > 0 && !(ok = wait(o_full, c - 1))) break;  // the last chunk's P has been read
                         int j0 = 0;
 #pragma unroll 1
                         for (; j0 < (halves - 1) * 32; j0 += 16) weigh(j0, Flag<false>{}, pass == 1);
@@ -553,6 +566,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             sl.p_unit[i] = p.scale * pow2f(-e);
                         }
                     }
+                    if (!ok) break;
                     ptx::tc_fence_before();
                     arrive(&a_free[c & 1]);
                     ptx::fence_proxy_async_smem();

@@ -29,7 +29,7 @@ inline int64_t linear_segments(int64_t n_tokens, int64_t n_seqs, int64_t segment
     return n_tokens / (segment_chunks * kChunk) + n_seqs;
 }
 cudaError_t launch_linear_chunks(const LinearArgs &a, int dtype, cudaStream_t s);
-cudaError_t launch_linear_tokens(const LinearArgs &a, int dtype, cudaStream_t s);
+cudaError_t launch_linear_tokens(const LinearArgs &a, int dtype, bool after_chunks, cudaStream_t s);
 
 struct HeadNormArgs {
     const uint16_t *x, *weight, *gate;

@@ -42,7 +42,7 @@ moe_status check_linear_config(const moe_linear_config *c) {
 }
 
 // New tokens from which a run is the chunk kernel's.
-constexpr int kChunkTokens = 32;
+constexpr int kChunkTokens = 8;
 // Segments times heads times column tiles that a batch may have when its runs are cut: the states they add are in the workspace.
 constexpr int64_t kMostSegments = 640;
 
@@ -169,7 +169,7 @@ moe_status moe_linear_attention(const moe_linear_config *cfg, const moe_state_po
         }
         MOE_CUDA(launch_linear_chunks(a, c.dtype, s));
     }
-    if (!chunks || batch->n_seqs > 1) MOE_CUDA(launch_linear_tokens(a, c.dtype, s));
+    if (!chunks || batch->n_seqs > 1) MOE_CUDA(launch_linear_tokens(a, c.dtype, chunks, s));
     return MOE_OK;
 }
 
