@@ -44,6 +44,7 @@ constexpr int kSlots = 4;                    // chunks whose decays are in share
 // What the warps tell one another of a chunk.
 struct alignas(16) Slot {
     float g_hi[kChunk], g_lo[kChunk];  // -log2 of the decay from the chunk's begin, in two parts
+    float to_end[kChunk];              // e^{G_l - G_j}, l the last of the 16 tokens that j is among
     float weight[kChunk];              // e^{G_64 - G_j}
     float fade[kChunk];                // scale e^{G_i}
     float p_unit[kChunk];              // fp16: P's rows hold scale / p_unit of their values
@@ -495,7 +496,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         weigh_values();
     } else {
         ptx::regs_down<Regs<STATES>::kOther>();
-        if (warp < kLoadWarp) {
+        if (warp < kLoadWarp && !(STATES && warp == kWeightWarp)) {
             if (!STATES) {
                 // -------------------------------------------------------------------------- P --
                 // Rows 0..31 are one warp's, 32..63 the other's: of the four 32 x 32 blocks the first warp has one below the
@@ -516,10 +517,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                     ptx::tc_fence_after();
                     const float2 gh = both(-sl.g_hi[i]), gl = both(-sl.g_lo[i]);
                     float m = 0.f, f = 1.f;
-                    // 16 columns from j0 on: their largest (with fp16, whose rows are scaled), or their two parts into shared memory
+                    // 16 columns from j0 on: their largest (with fp16, whose rows are scaled), or their two parts into shared memory.
+                    // Where all of them lie before the row, their weights are e^{G_i - G_l} e^{G_l - G_j}, l the last of them.
                     auto weigh = [&](int j0, auto diagonal, bool put) {
                         uint32_t a[16];
                         ptx::tmem_ld_16(lanes + C::kColA + (c & 1) * 64 + j0, a);
+                        const float since = exp2_fast((gh.x + sl.g_hi[j0 + 15]) + (gl.x + sl.g_lo[j0 + 15])) * f;
                         ptx::tmem_ld_wait();
 #pragma unroll
                         for (int j = 0; j < 16; ++j) asm volatile("" : "+r"(a[j]));
@@ -527,22 +530,23 @@ __global__ void __launch_bounds__(kThreads, 1)
                         const int last = i - j0;
 #pragma unroll
                         for (int j = 0; j < 16; j += 2) {
-                            const float4 h4 = *reinterpret_cast<const float4 *>(&sl.g_hi[j0 + (j & ~3)]);
-                            const float4 l4 = *reinterpret_cast<const float4 *>(&sl.g_lo[j0 + (j & ~3)]);
-                            const float2 h = j & 2 ? make_float2(h4.z, h4.w) : make_float2(h4.x, h4.y);
-                            const float2 l = j & 2 ? make_float2(l4.z, l4.w) : make_float2(l4.x, l4.y);
-                            const float2 g = __fadd2_rn(__fadd2_rn(gh, h), __fadd2_rn(gl, l));
-                            float2 x = __fmul2_rn(make_float2(__uint_as_float(a[j]), __uint_as_float(a[j + 1])),
-                                                  make_float2(exp2_fast(g.x), exp2_fast(g.y)));
-                            if (decltype(diagonal)::value) {
+                            float2 x = make_float2(__uint_as_float(a[j]), __uint_as_float(a[j + 1]));
+                            if constexpr (decltype(diagonal)::value) {
+                                const float4 h4 = *reinterpret_cast<const float4 *>(&sl.g_hi[j0 + (j & ~3)]);
+                                const float4 l4 = *reinterpret_cast<const float4 *>(&sl.g_lo[j0 + (j & ~3)]);
+                                const float2 h = j & 2 ? make_float2(h4.z, h4.w) : make_float2(h4.x, h4.y);
+                                const float2 l = j & 2 ? make_float2(l4.z, l4.w) : make_float2(l4.x, l4.y);
+                                const float2 g = __fadd2_rn(__fadd2_rn(gh, h), __fadd2_rn(gl, l));
+                                x = __fmul2_rn(x, make_float2(exp2_fast(g.x), exp2_fast(g.y)));
                                 if (j > last) x.x = 0.f;
                                 if (j + 1 > last) x.y = 0.f;
+                                if (F16) x = __fmul2_rn(x, both(f));
+                            } else {
+                                const float4 w4 = *reinterpret_cast<const float4 *>(&sl.to_end[j0 + (j & ~3)]);
+                                x = __fmul2_rn(x, __fmul2_rn(j & 2 ? make_float2(w4.z, w4.w) : make_float2(w4.x, w4.y), both(since)));
                             }
-                            if (F16) {
-                                m = fmaxf(m, fmaxf(fabsf(x.x), fabsf(x.y)));
-                                x = __fmul2_rn(x, both(f));
-                            }
-                            split2<F16>(x, hi[j / 2], lo[j / 2]);
+                            if (F16 && !put) m = fmaxf(m, fmaxf(fabsf(x.x), fabsf(x.y)));
+                            else split2<F16>(x, hi[j / 2], lo[j / 2]);
                         }
                         if (F16 && !put) return;
 #pragma unroll
@@ -574,33 +578,38 @@ __global__ void __launch_bounds__(kThreads, 1)
                     arrive(&g_empty[c % kSlots]);
                 }
             }
-        } else if (warp == kLoadWarp) {
+        } else if (warp <= kLoadWarp) {
             // -------------------------------------------------------------- copies, decays --
+            // (without outputs each has a warp of its own)
+            const bool copy = !STATES || warp == kWeightWarp, weigh = warp == kLoadWarp;
             Two total{0.f, 0.f};  // log2 of the segment's decay
             // Lanes 0, 1 (, 2) copy a chunk's tokens of K, V (and Q); lanes 8, 9 (, 10) bring those of a later chunk into L2.
             constexpr int kBoxes = STATES ? 2 : 3;
             const int box = lane & 7;
             const CUtensorMap *map = box == 0 ? &maps.k : box == 1 ? &maps.v : &maps.q;
             const int box_block = box == 1 ? col0 / 64 : kh * C::kKBlocks, box_at = box == 0 ? C::kK : box == 1 ? C::kV : 0;
-            if (lane < kBoxes) ptx::tma_prefetch_desc(map);
+            if (copy && lane < kBoxes) ptx::tma_prefetch_desc(map);
             // the decays of two tokens a lane, on their way two chunks ahead
             auto decays = [&](int c) {
                 const int i = c * kChunk + 2 * lane;
-                return make_float2(i < rows ? raw_decay(p, row0 + i, head) : 0.f, i + 1 < rows ? raw_decay(p, row0 + i + 1, head) : 0.f);
+                return make_float2(weigh && i < rows ? raw_decay(p, row0 + i, head) : 0.f, weigh && i + 1 < rows ? raw_decay(p, row0 + i + 1, head) : 0.f);
             };
             float2 g = decays(0), g1 = decays(1);
-            if (lane >= 8 && lane < 8 + kBoxes)
+            if (copy && lane >= 8 && lane < 8 + kBoxes)
                 for (int c = kStages; c < min(kStages + kFetch, chunks); ++c) ptx::tma_prefetch_3d(map, 0, (int)row0 + c * kChunk, box_block);
             for (int c = 0; c < chunks && ok; ++c) {
                 const int st = c % kStages, row = (int)row0 + c * kChunk;
                 const float2 g2 = decays(c + 2);
-                if (c >= kStages && !(ok = wait(&empty[st], c / kStages - 1))) break;
-                if (lane == 0) ptx::mbar_arrive_expect_tx(&full[st], (uint32_t)(C::kStageBytes - (STATES ? C::kK : 0)));
-                __syncwarp();
-                if (lane < kBoxes) ptx::tma_load_3d(smem + st * C::kStageBytes + box_at, map, 0, row, box_block, &full[st]);
-                else if (lane >= 8 && lane < 8 + kBoxes && c + kStages + kFetch < chunks)
-                    ptx::tma_prefetch_3d(map, 0, row + (kStages + kFetch) * kChunk, box_block);
-                issued = c + 1;
+                if (copy) {
+                    if (c >= kStages && !(ok = wait(&empty[st], c / kStages - 1))) break;
+                    if (lane == 0) ptx::mbar_arrive_expect_tx(&full[st], (uint32_t)(C::kStageBytes - (STATES ? C::kK : 0)));
+                    __syncwarp();
+                    if (lane < kBoxes) ptx::tma_load_3d(smem + st * C::kStageBytes + box_at, map, 0, row, box_block, &full[st]);
+                    else if (lane >= 8 && lane < 8 + kBoxes && c + kStages + kFetch < chunks)
+                        ptx::tma_prefetch_3d(map, 0, row + (kStages + kFetch) * kChunk, box_block);
+                    issued = c + 1;
+                }
+                if (!weigh) continue;
                 if (c >= kSlots && !(ok = wait(&g_empty[c % kSlots], c / kSlots - 1))) break;
                 const Two l0 = log2_of(checked_decay(p, g.x)), l1 = log2_of(checked_decay(p, g.y));
                 g = g1, g1 = g2;
@@ -614,6 +623,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const Two G0 = G + Two{-l1.hi, -l1.lo};
                 total = total + end;
                 Slot &sl = slots[c % kSlots];
+                const Two last{__shfl_sync(0xffffffffu, G.hi, lane | 7), __shfl_sync(0xffffffffu, G.lo, lane | 7)};  // of 16 tokens
+                reinterpret_cast<float2 *>(sl.to_end)[lane] =
+                    make_float2(exp2_fast((last.hi - G0.hi) + (last.lo - G0.lo)), exp2_fast((last.hi - G.hi) + (last.lo - G.lo)));
                 reinterpret_cast<float2 *>(sl.g_hi)[lane] = make_float2(-G0.hi, -G.hi);
                 reinterpret_cast<float2 *>(sl.g_lo)[lane] = make_float2(-G0.lo, -G.lo);
                 reinterpret_cast<float2 *>(sl.fade)[lane] = make_float2(p.scale * exp2_fast(G0.hi), p.scale * exp2_fast(G.hi));
@@ -626,7 +638,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 arrive(&g_full[c % kSlots]);
             }
-            if (STATES && ok && lane == 0 && tile == 0) p.seg_decay[(int64_t)place * p.VH + head] = exp2_fast(total.hi);
+            if (STATES && weigh && ok && lane == 0 && tile == 0) p.seg_decay[(int64_t)place * p.VH + head] = exp2_fast(total.hi);
         } else {
             // -------------------------------------------------------------------- the MMAs --
             const uint32_t idesc_a = ptx::idesc_16_f32(F16, 128, kChunk, false, false);
@@ -725,7 +737,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (!ok) {
         *abort_flag = 1;
         atomicCAS(p.status, 0, (int)MOE_ERR_TIMEOUT);
-        if (warp == kLoadWarp && lane == 0) {  // copies under way land before the shared memory is given up
+        if (issued > 0 && lane == 0) {  // copies under way land before the shared memory is given up
             int zero = 0;
             for (int c = max(issued - kStages, 0); c < issued; ++c) ptx::mbar_wait(&full[c % kStages], c / kStages & 1, kWaitNs, &zero);
         }

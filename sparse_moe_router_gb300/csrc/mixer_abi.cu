@@ -63,21 +63,24 @@ LinearLayout linear_layout(const moe_linear_config &c, int n_seqs, int n_tokens)
     return l;
 }
 
-// Chunks a segment: as many as end soonest, counted in chunks of the output kernel on every SM; a block's start and end
-// count as 3, a chunk of the first kernel as 2/3.
+// Chunks a segment: as many as end soonest.  Measured, us: a block of the output kernel 8, 2.2 a chunk and 0.6 a segment
+// before its own, a block of the first kernel 5 and 1.2 a chunk.
 int segment_chunks(const moe_linear_config &c, int64_t n_seqs, int64_t n_tokens) {
     const int sms = device_info().sm_count;
-    const int64_t chunks = (n_tokens + kChunk - 1) / kChunk, per = (int64_t)c.value_heads * value_tiles(c);
-    // a batch's longest run: all of it, or of several three times the mean
-    const int64_t longest = n_seqs == 1 ? chunks : chunks < 3 * chunks / n_seqs + 1 ? chunks : 3 * chunks / n_seqs + 1;
-    auto waves = [&](int64_t blocks) { return (double)((blocks + sms - 1) / sms); };
-    int64_t best = chunks;
-    const double even = (double)chunks * per / sms;
-    double least = fmax((double)longest, even) + 3 * waves(n_seqs * per);
+    const double chunks = (double)((n_tokens + kChunk - 1) / kChunk), per = (double)c.value_heads * value_tiles(c) / sms;
+    // a batch's longest run: all of it, or of several four times the mean
+    const double longest = n_seqs == 1 ? chunks : fmin(chunks, 4 * chunks / n_seqs + 1);
+    // time of `n` blocks a head of up to l chunks: equal ones go by rounds, ragged ones fill gaps
+    auto walk = [&](double n, double l, double start, double each) {
+        if (n_seqs == 1) return ceil(n * per) * (start + each * l);
+        return fmax(start + each * l, n * per * start + chunks * per * each + each * l / 2);
+    };
+    int64_t best = (int64_t)chunks;
+    double least = walk((double)n_seqs, longest, 8, 2.2);
     for (int64_t l = 2; l < longest; l += l < 32 ? 1 : l / 16) {
-        const int64_t cut = n_seqs == 1 ? (chunks + l - 1) / l : chunks / l + n_seqs;
-        if ((n_tokens / (l * kChunk) + n_seqs) * per > kMostSegments) continue;
-        const double cost = waves(cut * per) * (l + 3) + waves((cut - n_seqs) * per) * (l * 0.67 + 3) + 2;
+        if ((n_tokens / (l * kChunk) + n_seqs) * c.value_heads * value_tiles(c) > kMostSegments) continue;
+        const double n = n_seqs == 1 ? ceil(chunks / l) : chunks / l + 0.6 * n_seqs;
+        const double cost = walk(n, (double)l, 8 + 0.6 * (n_seqs == 1 ? n : longest / l), 2.2) + walk(n_seqs == 1 ? n - 1 : chunks / l, (double)l, 5, 1.2);
         if (cost < least) least = cost, best = l;
     }
     return (int)best;
