@@ -1,6 +1,6 @@
 // linear.cu -- moe_linear_attention token by token: S = e^g S + k v^T, out = scale S^T q.
 //
-// Columns of a state (value channels) do not meet, so a block takes 32 of them with all DK rows in registers, from the
+// Columns of a state (value channels) do not meet, so a block takes some of them with all DK rows in registers, from the
 // first new token to the last: the state is read once and written once, however many tokens there are.  Eight tokens
 // at a time share two barriers: their queries and keys go to shared memory together, and the warps' parts of their
 // outputs are joined together.
@@ -9,17 +9,16 @@
 namespace moe {
 namespace {
 
-constexpr int kCols = 32;      // value channels a block: 8 threads of 4
-constexpr int kThreads = 256;  // 32 rows at once
-constexpr int kRowsAtOnce = kThreads / (kCols / 4);
+constexpr int kThreads = 256;
 constexpr int kAtOnce = 8;     // tokens
 
-template <int DK, bool F16>
-__global__ void __launch_bounds__(kThreads) linear_tokens_kernel(const __grid_constant__ LinearArgs p) {
-    constexpr int R = DK / kRowsAtOnce;
+// kCols value channels a block, 4 a thread.
+template <int DK, int kCols, bool F16>
+__global__ void __launch_bounds__(kThreads, 2) linear_tokens_kernel(const __grid_constant__ LinearArgs p) {
+    constexpr int kRowsAtOnce = kThreads / (kCols / 4), R = DK / kRowsAtOnce;
     __shared__ float ks[kAtOnce][DK], qs[kAtOnce][DK], fs[kAtOnce];
     __shared__ float4 part[kAtOnce][kThreads / 32][kCols / 4];
-    const int tid = (int)threadIdx.x, c = tid & 7, r = tid >> 3;
+    const int tid = (int)threadIdx.x, c = tid & (kCols / 4 - 1), r = tid / (kCols / 4);
     const int tiles = p.DV / kCols, b = (int)blockIdx.x / tiles, h = (int)blockIdx.y;
     const int col0 = ((int)blockIdx.x - b * tiles) * kCols, col = col0 + c * 4;
     const Run run = load_run(p, b);
@@ -62,19 +61,19 @@ __global__ void __launch_bounds__(kThreads) linear_tokens_kernel(const __grid_co
                     acc.z = fmaf(q, S[i].z, acc.z), acc.w = fmaf(q, S[i].w, acc.w);
                 }
 #pragma unroll
-                for (int o = 8; o < 32; o <<= 1) {
+                for (int o = kCols / 4; o < 32; o <<= 1) {
                     acc.x += __shfl_xor_sync(0xffffffffu, acc.x, o), acc.y += __shfl_xor_sync(0xffffffffu, acc.y, o);
                     acc.z += __shfl_xor_sync(0xffffffffu, acc.z, o), acc.w += __shfl_xor_sync(0xffffffffu, acc.w, o);
                 }
-                if ((tid & 31) < 8) part[t][tid >> 5][c] = acc;
+                if ((tid & 31) < kCols / 4) part[t][tid >> 5][c] = acc;
             }
             if (t0 + m >= run.n && run.slot >= 0) {
 #pragma unroll
                 for (int i = 0; i < R; ++i) *reinterpret_cast<float4 *>(state + (int64_t)(r + i * kRowsAtOnce) * p.DV) = S[i];
             }
             __syncthreads();
-            if (tid < m * (kCols / 2)) {  // two channels a thread
-                const int t = tid / (kCols / 2), e = tid % (kCols / 2);
+            for (int y = tid; y < m * (kCols / 2); y += kThreads) {  // two channels a thread
+                const int t = y / (kCols / 2), e = y % (kCols / 2);
                 float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
                 for (int w = 0; w < kThreads / 32; ++w) {
@@ -89,8 +88,8 @@ __global__ void __launch_bounds__(kThreads) linear_tokens_kernel(const __grid_co
     asm volatile("griddepcontrol.wait;" ::: "memory");  // the chunk kernel's end: what follows this grid follows both
 }
 
-template <int DK, bool F16>
-cudaError_t launch(const LinearArgs &a, bool after_chunks, cudaStream_t s) {
+template <int DK, int kCols, bool F16>
+cudaError_t launch_cols(const LinearArgs &a, bool after_chunks, cudaStream_t s) {
     cudaLaunchAttribute attr{};
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr.val.programmaticStreamSerializationAllowed = 1;
@@ -101,8 +100,18 @@ cudaError_t launch(const LinearArgs &a, bool after_chunks, cudaStream_t s) {
     cfg.attrs = &attr;
     cfg.numAttrs = after_chunks ? 1 : 0;
     LaunchScope scope(KC_LINEAR_TOKENS, s);
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, linear_tokens_kernel<DK, F16>, a);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, linear_tokens_kernel<DK, kCols, F16>, a);
     return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+template <int DK, bool F16>
+cudaError_t launch(const LinearArgs &a, bool after_chunks, cudaStream_t s) {
+    // Whole heads (of up to 128 channels) a block, with 64 KB under way in it, where they give every SM one; else 32 channels,
+    // so that few heads reach all SMs.  us with 32 and 128 channels, 32 heads of 128 and 128: 1 sequence 2.9 and 4.1, 8 6.7
+    // and 5.8, 48 41.5 and 35.5, 200 160 and 130 (64 channels: 3.1, 6.9, 44.7, 173).
+    const bool many = (int64_t)a.n_seqs * a.VH >= device_info().sm_count;
+    if (!many) return launch_cols<DK, 32, F16>(a, after_chunks, s);
+    return a.DV == 64 ? launch_cols<DK, 64, F16>(a, after_chunks, s) : launch_cols<DK, 128, F16>(a, after_chunks, s);
 }
 
 }  // namespace

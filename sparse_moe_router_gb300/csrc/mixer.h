@@ -63,8 +63,7 @@ __device__ __forceinline__ float sigmoid_fast(float x) {
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + __expf(-x)));
     return r;
 }
-// x / (1 + e^-x): at x -> -inf the product would be -inf * 0.
-__device__ __forceinline__ float silu_fast(float x) { return x < -88.f ? x * __expf(x) : x * sigmoid_fast(x); }
+__device__ __forceinline__ float silu_fast(float x) { return x * sigmoid_fast(x); }
 
 // z Phi(z), Phi(-x) = erfc(x / sqrt(2)) / 2, by the Chebyshev fit of erfc whose error is below 1.2e-7 of the value
 // everywhere (Press et al., Numerical Recipes, "erfcc"): erff, with its branches, made the epilogue of 4 M outputs
