@@ -5,6 +5,7 @@
 // once, y written once.  The mean comes first and the squares are taken of what is left (the difference
 // of the two sums would lose a head whose mean is large).
 #include "mixer.h"
+#include "ptx.cuh"
 
 namespace moe {
 namespace {
@@ -21,6 +22,7 @@ __device__ __forceinline__ float lanes_sum(float v) {
 // L lanes a head, C 16-byte chunks (8 values) a lane: chunk i of lane l is chunk l + i L.
 template <int L, int C, bool F16>
 __global__ void __launch_bounds__(kThreads) head_norm_kernel(const __grid_constant__ HeadNormArgs p) {
+    ptx::launch_dependents();
     // (32 bits: a launch has fewer than 2^30 heads)
     const uint32_t item = blockIdx.x * (kThreads / L) + threadIdx.x / L;
     const bool live = item < (uint32_t)p.T * p.heads;
@@ -28,6 +30,7 @@ __global__ void __launch_bounds__(kThreads) head_norm_kernel(const __grid_consta
     const int lane = (int)threadIdx.x & (L - 1), chunks = p.dim >> 3, at = live ? (int)(item - row * p.heads) * p.dim : 0;
     const uint4 zero = make_uint4(0, 0, 0, 0);
     uint4 xv[C], gv[C], wv[C];
+    ptx::wait_prior_grid();
 #pragma unroll
     for (int i = 0; i < C; ++i) {
         const int c = lane + i * L;
@@ -82,8 +85,16 @@ template <int L, int C, bool F16>
 cudaError_t launch_lanes(const HeadNormArgs &a, cudaStream_t s) {
     LaunchScope scope(KC_HEAD_NORM, s);
     const int each = kThreads / L;
-    head_norm_kernel<L, C, F16><<<(unsigned)((a.T * a.heads + each - 1) / each), kThreads, 0, s>>>(a);
-    return cudaGetLastError();
+    cudaLaunchAttribute attr[1];
+    overlap_prior(attr[0]);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)((a.T * a.heads + each - 1) / each));
+    cfg.blockDim = dim3(kThreads);
+    cfg.stream = s;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, head_norm_kernel<L, C, F16>, a);
+    return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 template <bool F16>

@@ -53,6 +53,12 @@ cudaError_t launch_project_rows(const ProjectArgs &a, int dtype, cudaStream_t s)
 cudaError_t launch_project_batch(const ProjectArgs &a, int dtype, cudaStream_t s);  // at most 256 rows or outputs
 cudaError_t launch_project_tiles(const ProjectArgs &a, int dtype, cudaStream_t s);  // any
 
+// Lets a kernel's setup run under the end of the one before it on the stream (it then waits before its first access).
+inline void overlap_prior(cudaLaunchAttribute &attr) {
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+}
+
 // A log decay below this counts as this: its factor is 0 in fp32, and sums of 64 stay finite.
 constexpr float kLeastDecay = -10000.f;
 

@@ -4,6 +4,7 @@
 // walk K in 16-byte pieces (8 weights), so that every piece of x serves 4 weights and every weight all rows of x.  Where
 // N gives too few warps, the warps of a block share K.
 #include "mixer.h"
+#include "ptx.cuh"
 
 namespace moe {
 namespace {
@@ -15,6 +16,8 @@ constexpr int kWRows = 4;  // rows of w a warp
 template <int X, int S, bool F16>
 __global__ void __launch_bounds__(kThreads) project_rows_kernel(const __grid_constant__ ProjectArgs p) {
     __shared__ float part[kWarps][kWRows * X];
+    ptx::launch_dependents();
+    ptx::wait_prior_grid();
     const int warp = (int)threadIdx.x >> 5, lane = (int)threadIdx.x & 31;
     const int group = warp / S, share = warp % S;
     const int n0 = ((int)blockIdx.y * (kWarps / S) + group) * kWRows, t0 = (int)blockIdx.x * X;
@@ -85,8 +88,16 @@ template <int X, int S, bool F16>
 cudaError_t launch_shape(const ProjectArgs &a, cudaStream_t s) {
     LaunchScope scope(KC_PROJECT_ROWS, s);
     const int rows = kWarps / S * kWRows;
-    project_rows_kernel<X, S, F16><<<dim3((a.T + X - 1) / X, (a.N + rows - 1) / rows), kThreads, 0, s>>>(a);
-    return cudaGetLastError();
+    cudaLaunchAttribute attr[1];
+    overlap_prior(attr[0]);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((a.T + X - 1) / X, (a.N + rows - 1) / rows);
+    cfg.blockDim = dim3(kThreads);
+    cfg.stream = s;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, project_rows_kernel<X, S, F16>, a);
+    return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 template <int X, bool F16>

@@ -49,6 +49,8 @@ __global__ void __launch_bounds__(kThreads)
     __syncthreads();
     ptx::tc_fence_after();
     const uint32_t tmem = tmem_holder;
+    ptx::launch_dependents();
+    ptx::wait_prior_grid();
     bool ok = true;
     if (warp == 0) {
         if (lane == 0) {
@@ -190,16 +192,17 @@ cudaError_t launch(const ProjectArgs &a, cudaStream_t s) {
         ready[dev].store(true, std::memory_order_release);
     }
     cudaLaunchConfig_t cfg = {};
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = split;
-    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cudaLaunchAttribute attr[2];
+    overlap_prior(attr[0]);
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = split;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.gridDim = dim3((unsigned)(tiles * split));
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
     cfg.attrs = attr;
-    cfg.numAttrs = split > 1 ? 1 : 0;
+    cfg.numAttrs = split > 1 ? 2 : 1;
     LaunchScope scope(KC_PROJECT_BATCH, s);
     e = cudaLaunchKernelEx(&cfg, kernel, a, m, sh, split);
     return e != cudaSuccess ? e : cudaGetLastError();

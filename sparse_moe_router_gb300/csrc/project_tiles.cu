@@ -1,6 +1,6 @@
 // project_tiles.cu -- moe_project for many rows and outputs on the 5th-generation tensor cores.
 //
-// A pair of blocks (two SMs, cta_group::2) computes 256 rows of x by BN outputs with one stream of MMAs: each block
+// A pair of blocks (two SMs, cta_group::2) computes 256 rows of x by bn outputs with one stream of MMAs: each block
 // holds its own 128 rows of x and half of the outputs' rows of w, and its 128 rows of the sums in TMEM, twice, so
 // that the epilogue of one tile runs under the products of the next.  Pairs walk the tiles in turn, rows first, so that
 // what runs at once shares rows of w.
@@ -8,7 +8,8 @@
 // Roles: warps 0-7 epilogue (two for each quarter of the lanes, half of the columns each), 8 copies, 9 the MMAs.  A lane of
 // TMEM is a row: 32 columns at a time go through the warp's own buffer, in 32 bits, so that rows leave in 64-byte pieces
 // and bias, activation and residual are taken there, before the only rounding.
-#include <mutex>
+#include <atomic>
+#include <cmath>
 
 #include "mixer.h"
 #include "ptx.cuh"
@@ -22,50 +23,50 @@ constexpr int kXBytes = kRows * 128;
 constexpr int kTurnLd = 36;  // floats of a row of 32 columns, padded for the banks
 constexpr int kTurnBytes = kEpiWarps * 32 * kTurnLd * 4;
 
-template <int BN>
+constexpr int kMostStages = 8, kStageRoom = 186 * 1024;
+constexpr int kBarBytes = (2 * kMostStages + 5) * 8 + 16;
+constexpr int kSmem = 1024 + kStageRoom + kTurnBytes + kBarBytes;
+static_assert(kSmem <= 227 * 1024, "shared memory over the per-block limit");
+constexpr int kBuf = 256;  // TMEM columns of a tile's sums
 struct Shape {
-    static constexpr int kWBytes = BN / 2 * 128;
-    static constexpr int kStageBytes = kXBytes + kWBytes;
-    static constexpr int kStages = 186 * 1024 / kStageBytes < 8 ? 186 * 1024 / kStageBytes : 8;
-    static constexpr int kSmem = 1024 + kStages * kStageBytes + kTurnBytes + (2 * kStages + 5) * 8 + 16;
-    static constexpr uint32_t kCols = 2 * BN < 32 ? 32 : 2 * BN;
-    static_assert(kSmem <= 227 * 1024, "shared memory over the per-block limit");
+    int bn, stage_bytes, stages;  // outputs a tile (a multiple of 16, at most 256)
 };
 
 struct Maps {
     CUtensorMap x, w;
 };
 
-template <int BN, bool F16>
+template <bool F16>
 __global__ void __launch_bounds__(kThreads, 1)
-    project_tiles_kernel(const __grid_constant__ ProjectArgs p, const __grid_constant__ Maps maps) {
-    using C = Shape<BN>;
-    constexpr int kStages = C::kStages;
+    project_tiles_kernel(const __grid_constant__ ProjectArgs p, const __grid_constant__ Maps maps, const Shape sh) {
+    const int stages = sh.stages, bn = sh.bn;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = smem_raw + ((1024u - (ptx::smem_u32(smem_raw) & 1023u)) & 1023u);
-    float *turn = reinterpret_cast<float *>(smem + kStages * C::kStageBytes);
-    uint64_t *full = reinterpret_cast<uint64_t *>(smem + kStages * C::kStageBytes + kTurnBytes), *empty = full + kStages;
-    uint64_t *sums_full = empty + kStages, *sums_empty = sums_full + 2, *drain = sums_empty + 2;
+    float *turn = reinterpret_cast<float *>(smem + kStageRoom);
+    uint64_t *full = reinterpret_cast<uint64_t *>(smem + kStageRoom + kTurnBytes), *empty = full + kMostStages;
+    uint64_t *sums_full = empty + kMostStages, *sums_empty = sums_full + 2, *drain = sums_empty + 2;
     uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(drain + 1);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_holder + 1);
     volatile int *fills = abort_flag + 1;  // stages filled and used, read when a wait ran out
     const int tid = (int)threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
     const int rank = (int)ptx::cluster_ctarank();
     if (tid == 0) {
-        for (int s = 0; s < kStages; ++s) ptx::mbar_init(&full[s], 1), ptx::mbar_init(&empty[s], 1);
+        for (int s = 0; s < stages; ++s) ptx::mbar_init(&full[s], 1), ptx::mbar_init(&empty[s], 1);
         for (int i = 0; i < 2; ++i) ptx::mbar_init(&sums_full[i], 1), ptx::mbar_init(&sums_empty[i], 2 * kEpiWarps);
         ptx::mbar_init(drain, 1);
         *abort_flag = 0;
         fills[0] = fills[1] = 0;
         ptx::fence_mbar_init();
     }
-    if (warp == kMmaWarp) ptx::tmem_alloc_pair(tmem_holder, C::kCols);
+    if (warp == kMmaWarp) ptx::tmem_alloc_pair(tmem_holder, 2 * kBuf);
     ptx::tc_fence_before();
     __syncthreads();
     ptx::cluster_sync();  // the other block's barriers are ready before anyone signals them
     ptx::tc_fence_after();
     const uint32_t tmem = *tmem_holder;
-    const int tiles_t = (p.T + 2 * kRows - 1) / (2 * kRows), tiles = tiles_t * ((p.N + BN - 1) / BN);
+    ptx::launch_dependents();
+    ptx::wait_prior_grid();
+    const int tiles_t = (p.T + 2 * kRows - 1) / (2 * kRows), tiles = tiles_t * ((p.N + bn - 1) / bn);
     const int pair = (int)blockIdx.x >> 1, pairs = (int)gridDim.x >> 1, blocks = (p.K + 63) / 64;
     bool ok = true;
     if (warp == kLoadWarp) {
@@ -76,21 +77,21 @@ __global__ void __launch_bounds__(kThreads, 1)
             int it = 0, s = 0;
             uint32_t phase = 1;
             for (int tile = pair; tile < tiles && ok; tile += pairs) {
-                const int t0 = tile % tiles_t * (2 * kRows) + rank * kRows, n0 = tile / tiles_t * BN + rank * (BN / 2);
+                const int t0 = tile % tiles_t * (2 * kRows) + rank * kRows, n0 = tile / tiles_t * bn + rank * (bn / 2);
                 for (int k = 0; k < blocks; ++k, ++it) {
                     if (!(ok = ptx::mbar_sleep_wait(&empty[s], phase, abort_flag))) break;
-                    uint8_t *stage = smem + s * C::kStageBytes;
-                    if (rank == 0) ptx::mbar_arrive_expect_tx(&full[s], 2 * C::kStageBytes);
+                    uint8_t *stage = smem + s * sh.stage_bytes;
+                    if (rank == 0) ptx::mbar_arrive_expect_tx(&full[s], 2 * sh.stage_bytes);
                     ptx::tma_load_2d_pair(stage, &maps.x, k * 64, t0, full_even + s * 8);
                     ptx::tma_load_2d_pair(stage + kXBytes, &maps.w, k * 64, n0, full_even + s * 8);
-                    if (++s == kStages) s = 0, phase ^= 1;
+                    if (++s == stages) s = 0, phase ^= 1;
                 }
             }
             fills[0] = it;
         }
     } else if (warp == kMmaWarp) {
         if (lane == 0 && rank == 0) {
-            const uint32_t idesc = ptx::idesc_16_f32(F16, 2 * kRows, BN, false, false);
+            const uint32_t idesc = ptx::idesc_16_f32(F16, 2 * kRows, bn, false, false);
             const uint64_t desc0 = ptx::sw128_desc(ptx::smem_u32(smem));
             int it = 0, s = 0, n = 0;
             uint32_t phase = 0;
@@ -101,12 +102,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int k = 0; k < blocks; ++k, ++it) {
                     if (!(ok = ptx::mbar_wait_cluster(&full[s], phase, 2000000000ull, abort_flag))) break;
                     ptx::tc_fence_after();
-                    const uint64_t da = desc0 + (uint64_t)(s * C::kStageBytes >> 4), db = da + (kXBytes >> 4);
-                    ptx::mma_bf16_pair(tmem + buf * BN, da, db, idesc, k > 0);
+                    const uint64_t da = desc0 + (uint64_t)(s * sh.stage_bytes >> 4), db = da + (kXBytes >> 4);
+                    ptx::mma_bf16_pair(tmem + buf * kBuf, da, db, idesc, k > 0);
 #pragma unroll
-                    for (int j = 1; j < 4; ++j) ptx::mma_bf16_pair(tmem + buf * BN, da + 2 * j, db + 2 * j, idesc, 1);
+                    for (int j = 1; j < 4; ++j) ptx::mma_bf16_pair(tmem + buf * kBuf, da + 2 * j, db + 2 * j, idesc, 1);
                     ptx::mma_commit_pair(&empty[s], 3);
-                    if (++s == kStages) s = 0, phase ^= 1;
+                    if (++s == stages) s = 0, phase ^= 1;
                 }
                 if (ok) ptx::mma_commit_pair(&sums_full[buf], 3);
             }
@@ -117,8 +118,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         __syncwarp();
     } else {
-        const int quarter = warp & 3, c0 = (warp >> 2) * (BN / 2);
-        constexpr int kEach = BN / 2 < 32 ? 32 : BN / 2;  // columns of a warp
+        // the two warps of a quarter take turns of 32 columns
+        const int quarter = warp & 3, half = warp >> 2;
         float *mine = turn + warp * (32 * kTurnLd);
         const uint32_t empty_even = ptx::mapa_shared(ptx::smem_u32(sums_empty), 0);
         int n = 0;
@@ -127,32 +128,33 @@ __global__ void __launch_bounds__(kThreads, 1)
             ok = __all_sync(0xffffffffu, ptx::mbar_sleep_wait(&sums_full[buf], (n >> 1) & 1, abort_flag)) != 0;
             if (!ok) break;
             ptx::tc_fence_after();
-            const int t0 = tile % tiles_t * (2 * kRows) + rank * kRows + quarter * 32, n0 = tile / tiles_t * BN + c0;
-            const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16) + buf * BN + c0;
+            const int t0 = tile % tiles_t * (2 * kRows) + rank * kRows + quarter * 32, n0 = tile / tiles_t * bn, n1 = min(n0 + bn, p.N);
+            const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16) + buf * kBuf;
+            auto done = [&]() {  // the sums are in registers
+                ptx::tc_fence_before();
+                __syncwarp();
+                if (lane != 0) return;
+                if (rank == 0) ptx::mbar_arrive(&sums_empty[buf]);
+                else ptx::mbar_arrive_remote(empty_even + buf * 8);
+            };
+            if (half * 32 >= bn) done();
 #pragma unroll 1
-            for (int c = 0; c < kEach; c += 32) {
+            for (int c = half * 32; c < bn; c += 64) {
                 uint32_t r[32];
                 __syncwarp();
                 ptx::tmem_ld_32(lanes + c, r);
                 ptx::tmem_ld_wait();
 #pragma unroll
                 for (int j = 0; j < 32; ++j) asm volatile("" : "+r"(r[j]));
-                if (c + 32 >= kEach) {
-                    ptx::tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) {
-                        if (rank == 0) ptx::mbar_arrive(&sums_empty[buf]);
-                        else ptx::mbar_arrive_remote(empty_even + buf * 8);
-                    }
-                }
-                if (t0 >= p.T || n0 + c >= p.N) continue;
+                if (c + 64 >= bn) done();
+                if (t0 >= p.T || n0 + c >= n1) continue;
                 __syncwarp();
 #pragma unroll
                 for (int j = 0; j < 32; j += 4)
                     *reinterpret_cast<uint4 *>(mine + lane * kTurnLd + j) = make_uint4(r[j], r[j + 1], r[j + 2], r[j + 3]);
                 __syncwarp();
                 const int col = n0 + c + (lane & 3) * 8;
-                if (col >= p.N) continue;
+                if (col >= n1) continue;
                 float bias[8];
                 load_bias<8, F16>(p, col, bias);
 #pragma unroll 1
@@ -178,7 +180,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (tid == kLoadWarp * 32) {
             int zero = 0;
             if (rank == 0) {
-                for (int i = fills[1]; i < fills[0]; ++i) ptx::mbar_sleep_wait(&full[i % kStages], i / kStages & 1, &zero);
+                for (int i = fills[1]; i < fills[0]; ++i) ptx::mbar_sleep_wait(&full[i % stages], i / stages & 1, &zero);
             } else {
                 const uint64_t begun = ptx::globaltimer();
                 while (ptx::globaltimer() - begun < 100000ull) {}
@@ -189,83 +191,79 @@ __global__ void __launch_bounds__(kThreads, 1)
     ptx::cluster_sync();  // neither block leaves, or frees TMEM, while the other may still signal it
     if (warp == kMmaWarp) {
         ptx::tc_fence_after();
-        ptx::tmem_dealloc_pair(tmem, C::kCols);
+        ptx::tmem_dealloc_pair(tmem, 2 * kBuf);
     }
 }
 
-// Pairs of blocks that the device holds at once.
-template <int BN, bool F16>
-cudaError_t resident_pairs(int *pairs) {
-    static int most[64] = {0};
-    static std::mutex mu;
-    int dev = 0;
-    cudaGetDevice(&dev);
-    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
-    std::lock_guard<std::mutex> lk(mu);
-    if (most[dev] == 0) {
-        auto *kernel = project_tiles_kernel<BN, F16>;
-        cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Shape<BN>::kSmem);
-        if (e != cudaSuccess) return e;
-        cudaLaunchConfig_t cfg = {};
-        cudaLaunchAttribute attr[1];
-        attr[0].id = cudaLaunchAttributeClusterDimension;
-        attr[0].val.clusterDim.x = 2;
-        attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-        cfg.gridDim = dim3(device_info().sm_count & ~1);
-        cfg.blockDim = dim3(kThreads);
-        cfg.dynamicSmemBytes = Shape<BN>::kSmem;
-        cfg.attrs = attr;
-        cfg.numAttrs = 1;
-        int n = 0;
-        e = cudaOccupancyMaxActiveClusters(&n, kernel, &cfg);
-        if (e != cudaSuccess) return e;
-        if (n < 1) return cudaErrorInvalidConfiguration;
-        most[dev] = n;
-    }
-    *pairs = most[dev];
-    return cudaSuccess;
-}
-
-template <int BN, bool F16>
-cudaError_t launch_shape(const ProjectArgs &a, cudaStream_t s) {
-    int pairs = 0;
-    cudaError_t e = resident_pairs<BN, F16>(&pairs);
-    if (e != cudaSuccess) return e;
-    const int64_t tiles = (int64_t)((a.T + 2 * kRows - 1) / (2 * kRows)) * ((a.N + BN - 1) / BN);
-    if (tiles > 0x7fffffff) return cudaErrorInvalidValue;
-    if (tiles < pairs) pairs = (int)tiles;
-    Maps m;
-    if (!encode_tmap_rows(&m.x, a.x, a.T, a.K, a.x_ld, kRows) || !encode_tmap_rows(&m.w, a.w, a.N, a.K, a.w_ld, BN / 2))
-        return cudaErrorInvalidValue;
+cudaLaunchConfig_t config(cudaLaunchAttribute *attr, int blocks, cudaStream_t s) {
     cudaLaunchConfig_t cfg = {};
-    cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = 2;
     attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-    cfg.gridDim = dim3(2 * pairs);
+    cfg.gridDim = dim3(blocks);
     cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = Shape<BN>::kSmem;
+    cfg.dynamicSmemBytes = kSmem;
     cfg.stream = s;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    LaunchScope scope(KC_PROJECT_TILES, s);
-    e = cudaLaunchKernelEx(&cfg, project_tiles_kernel<BN, F16>, a, m);
-    return e != cudaSuccess ? e : cudaGetLastError();
+    overlap_prior(attr[1]);
+    cfg.numAttrs = 2;
+    return cfg;
+}
+
+// Pairs of blocks that the device holds at once.
+template <bool F16>
+cudaError_t resident_pairs(int *pairs) {
+    static std::atomic<int> most[64];
+    int dev = 0;
+    cudaGetDevice(&dev);
+    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    int n = most[dev].load(std::memory_order_acquire);
+    if (n == 0) {
+        auto *kernel = project_tiles_kernel<F16>;
+        cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+        if (e != cudaSuccess) return e;
+        cudaLaunchAttribute attr[2];
+        cudaLaunchConfig_t cfg = config(attr, device_info().sm_count & ~1, nullptr);
+        e = cudaOccupancyMaxActiveClusters(&n, kernel, &cfg);
+        if (e != cudaSuccess) return e;
+        if (n < 1) return cudaErrorInvalidConfiguration;
+        most[dev].store(n, std::memory_order_release);
+    }
+    *pairs = n;
+    return cudaSuccess;
 }
 
 template <bool F16>
 cudaError_t launch(const ProjectArgs &a, cudaStream_t s) {
-    // The tile that ends soonest: rounds of all pairs times a tile's time, in columns; a narrow tile's products wait for
-    // their operands (128 columns: about 1.15 of its share), and its start and end count as 24.
-    const int pairs = device_info().sm_count / 2;
-    const int64_t rows = (a.T + 2 * kRows - 1) / (2 * kRows);
-    auto cost = [&](int bn, double slow) {
-        const int64_t tiles = rows * ((a.N + bn - 1) / bn);
-        return (double)((tiles + pairs - 1) / pairs) * (bn * slow + 24);
-    };
-    const double c256 = cost(256, 1.0), c128 = cost(128, 1.15), c64 = cost(64, 1.6);
-    if (c256 <= c128 && c256 <= c64) return launch_shape<256, F16>(a, s);
-    return c128 <= c64 ? launch_shape<128, F16>(a, s) : launch_shape<64, F16>(a, s);
+    int pairs = 0;
+    cudaError_t e = resident_pairs<F16>(&pairs);
+    if (e != cudaSuccess) return e;
+    // The tile that ends soonest, in cycles: rounds of all pairs, each of K / 64 steps and about 800 for its start and end.  A
+    // step's MMAs take 2 cycles a column; its operands, (128 + bn / 2) rows of 128 bytes, come at about 66 bytes a cycle
+    // from L2, which is more below 256 columns (and narrower tiles have to gain 3%).
+    const int64_t rows = (a.T + 2 * kRows - 1) / (2 * kRows), steps = (a.K + 63) / 64;
+    int bn = 256;
+    double least = 1e30;
+    for (int n = 256; n >= 48; n -= 16) {
+        const int64_t rounds = (rows * ((a.N + n - 1) / n) + pairs - 1) / pairs;
+        const double cost = (double)rounds * (steps * fmax(2.0 * n, 248 + 0.97 * n) + 800) * (n == 256 ? 1.0 : 1.03);
+        if (cost < least) least = cost, bn = n;
+    }
+    Shape sh;
+    sh.bn = bn;
+    sh.stage_bytes = kXBytes + bn / 2 * 128;
+    sh.stages = min(kStageRoom / sh.stage_bytes, kMostStages);
+    const int64_t tiles = rows * ((a.N + bn - 1) / bn);
+    if (tiles > 0x7fffffff) return cudaErrorInvalidValue;
+    if (tiles < pairs) pairs = (int)tiles;
+    Maps m;
+    if (!encode_tmap_rows(&m.x, a.x, a.T, a.K, a.x_ld, kRows) || !encode_tmap_rows(&m.w, a.w, a.N, a.K, a.w_ld, bn / 2))
+        return cudaErrorInvalidValue;
+    cudaLaunchAttribute attr[2];
+    cudaLaunchConfig_t cfg = config(attr, 2 * pairs, s);
+    LaunchScope scope(KC_PROJECT_TILES, s);
+    e = cudaLaunchKernelEx(&cfg, project_tiles_kernel<F16>, a, m, sh);
+    return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 }  // namespace
