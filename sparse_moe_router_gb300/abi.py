@@ -447,6 +447,8 @@ _GATES = {"none": 0, "channel": 1, "token": 2, "element": 3}
 def _rows(t, name, width, dtype, rows):
     """Row stride of an activation tensor: [T, width], or [T, heads, dim] with heads * dim == width,
     whose rows may lie apart but are themselves contiguous.  rows: T, or -1 if it is not known yet."""
+    if t.is_contiguous() and t.shape == (rows, width) and t.dtype is dtype and t.is_cuda:  # (most calls, in half the time)
+        return width
     shape, stride = t.shape, t.stride()
     if len(shape) == 2:
         ok = shape[1] == width and (stride[1] == 1 or width == 1)
@@ -682,7 +684,7 @@ def moe_linear_attention(cfg: LinearConfig, pool: StatePool, batch: StateBatch, 
     st = lib().moe_linear_attention(
         cfg, pool.c, batch.c, q.data_ptr(), _rows(q, "q", kw, dt, T), k.data_ptr(), _rows(k, "k", kw, dt, T), v.data_ptr(),
         _rows(v, "v", vw, dt, T), g_p, g_ld, cfg.key_dim ** -0.5 if scale is None else scale, out.data_ptr(),
-        _rows(out, "out", vw, dt, T), _device_array(ws, "ws", torch.uint8), ws.numel(), _raw_stream(stream, q.device.index))
+        _rows(out, "out", vw, dt, T), _device_array(ws, "ws", torch.uint8), ws.numel(), _raw_stream(stream, q.get_device()))
     _check("moe_linear_attention", st)
 
 
@@ -704,7 +706,7 @@ def moe_head_norm(cfg: HeadNormConfig, x, y, weight=None, gate=None, stream=None
     if gate is not None:
         g_p, g_ld = gate.data_ptr(), _rows(gate, "gate", width, dt, T)
     st = lib().moe_head_norm(cfg, x.data_ptr(), _rows(x, "x", width, dt, T), w_p, g_p, g_ld, y.data_ptr(),
-                             _rows(y, "y", width, dt, T), T, _raw_stream(stream, x.device.index))
+                             _rows(y, "y", width, dt, T), T, _raw_stream(stream, x.get_device()))
     _check("moe_head_norm", st)
 
 
@@ -738,7 +740,7 @@ def moe_project(cfg: ProjectConfig, x, w, y, ws, bias=None, resid=None, stream=N
         io.bias = _vector(bias, "bias", N, dt)
     if resid is not None:
         io.resid, io.resid_ld = resid.data_ptr(), _rows(resid, "resid", N, ot, T)
-    st = lib().moe_project(cfg, io, T, _device_array(ws, "ws", torch.uint8), ws.numel(), _raw_stream(stream, x.device.index))
+    st = lib().moe_project(cfg, io, T, _device_array(ws, "ws", torch.uint8), ws.numel(), _raw_stream(stream, x.get_device()))
     _check("moe_project", st)
 
 

@@ -3,12 +3,17 @@
     x -> norm -> qkv product -> moe_kv_append -> moe_attention -> output product
       -> norm, gate, residual, norm (moe_block_norm) -> moe_forward -> norm, residual, norm -> ...
 
+A layer may have a recurrent mixer instead of attention, with a state a sequence instead of cached keys and values:
+
+    norm -> moe_project (q, k, v, gate) -> moe_head_norm (q, k) -> moe_linear_attention, its log decays a second
+      moe_project -> moe_head_norm with the gate -> moe_project -> norm, gate, residual, norm -> ...
+
 One object holds a stack of layers with their caches and buffers; `prefill` runs a piece of one or more
 prompts, `decode` one token a sequence.  Both run the same calls, so a prompt may come in pieces of any
 size and a step may mix prompts and single tokens.  All work is asynchronous on the current stream;
 `capture` records a decode step as a CUDA graph whose lengths are read from the device.
 
-The two projections are plain matrix products (torch.mm); everything else is a call of include/moe.h.
+The attention layers' two projections are plain matrix products (torch.mm); everything else is a call of include/moe.h.
 
     python -m sparse_moe_router_gb300.block        # a small stack: a prompt in two pieces, then tokens
 """
@@ -68,14 +73,21 @@ class Pages:
 class DecoderLayers:
     """layers: a list of dicts with w_qkv [(QH + 2 KH) D, H], w_o [H, QH D], norm_attn, norm_attn_out,
     norm_moe, norm_moe_out [H] (a missing *_out: no norm after that block), attn_gate [H] (optional, layer by layer), and the MoE
-    weights of abi.weights.  All bf16 on the device."""
+    weights of abi.weights.  A recurrent layer (linear_cfg, an abi.LinearConfig) has w_mix [2 KH DK + 2 VH DV, H]: queries, keys,
+    values and gates, w_decay [VH, H] and b_decay [VH]: log decays, w_mix_out [H, VH DV] and mix_norm [DV] or [VH, DV]
+    in place of w_qkv and w_o.  All bf16 on the device."""
 
-    def __init__(self, moe_cfg, attn_cfg, layers, pages: Pages, max_tokens, rope, eps=1e-6, residual_scale=1.0):
+    def __init__(self, moe_cfg, attn_cfg, layers, pages: Pages, max_tokens, rope, eps=1e-6, residual_scale=1.0, linear_cfg=None):
         self.moe, self.attn, self.layers, self.pages, self.rope = moe_cfg, attn_cfg, layers, pages, rope
         if attn_cfg.rotary_dim and rope.shape[0] < pages.max_len:
             raise ValueError("angles for %d positions, sequences of up to %d" % (rope.shape[0], pages.max_len))
         H, dev = moe_cfg.hidden, rope.device
-        self.caches = [abi.KVCache.alloc(attn_cfg, pages.n_pages, dev) for _ in layers]
+        self.linear = linear_cfg
+        if linear_cfg is None and any("w_mix" in l for l in layers):
+            raise ValueError("a recurrent layer needs linear_cfg")
+        if linear_cfg is not None and linear_cfg.value_heads % 8:
+            raise ValueError("the decays' product has a multiple of 8 outputs, not %d value heads" % linear_cfg.value_heads)
+        self.caches = [None if "w_mix" in l else abi.KVCache.alloc(attn_cfg, pages.n_pages, dev) for l in layers]
         self.weights = [abi.weights(l) for l in layers]
         self.moe_ws = abi.alloc_workspace(moe_cfg, max_tokens, dev)
         self.attn_ws = abi.alloc_attn_workspace(attn_cfg, len(pages.lens), max_tokens, dev)
@@ -88,6 +100,21 @@ class DecoderLayers:
         self.resid, self.y, self.block = new(max_tokens, H), new(max_tokens, H), new(max_tokens, H)
         self.qkv, self.ctx = new(max_tokens, QD + 2 * KD), new(max_tokens, QD)
         self.max_tokens = max_tokens
+        self.slots = torch.arange(len(pages.lens), dtype=torch.int32, device=dev)
+        if linear_cfg is not None:
+            c = linear_cfg
+            dt = torch.bfloat16
+            self.states = [abi.StatePool.alloc(c, len(pages.lens), dev) if "w_mix" in l else None for l in layers]
+            self.linear_ws = abi.alloc_linear_workspace(c, len(pages.lens), max_tokens, dev)
+            kd, vd = c.key_heads * c.key_dim, c.value_heads * c.value_dim
+            self.mix_in = abi.project_config(H, 2 * kd + 2 * vd)
+            self.mix_decay = abi.project_config(H, c.value_heads, out_dtype=torch.float32, act="log_sigmoid", scale=1 / 16)
+            self.mix_out = abi.project_config(vd, H)
+            self.mix_ws = abi.alloc_project_workspace(self.mix_in, max_tokens, dev)
+            self.mix_qk = abi.head_norm_config(2 * c.key_heads, c.key_dim, dtype=dt, eps=eps)
+            self.mix_norm = abi.head_norm_config(c.value_heads, c.value_dim, dtype=dt, gate="silu", eps=eps)
+            self.mix, self.mixed = new(max_tokens, 2 * kd + 2 * vd), new(max_tokens, vd)
+            self.decay = torch.empty(max_tokens, c.value_heads, dtype=torch.float32, device=dev)
 
     def batch(self, new_tokens):
         """The abi.KVBatch of a step with new_tokens[b] new tokens of sequence b; takes their pages, all or none."""
@@ -103,8 +130,26 @@ class DecoderLayers:
             if n:
                 self.pages.grow(b, n)
         dev = self.rope.device
-        return abi.KVBatch(torch.tensor(starts, dtype=torch.int32, device=dev),
-                           torch.tensor(self.pages.lens, dtype=torch.int32, device=dev), self.pages.table, starts[-1])
+        return self.with_states(abi.KVBatch(torch.tensor(starts, dtype=torch.int32, device=dev),
+                                            torch.tensor(self.pages.lens, dtype=torch.int32, device=dev), self.pages.table, starts[-1]))
+
+    def with_states(self, batch):
+        """The batch with what the recurrent layers read of it; a sequence's state has its own number."""
+        batch.states = abi.StateBatch(batch.q_start, batch.kv_len, self.slots, batch.n_tokens)
+        return batch
+
+    def recurrent(self, i, batch, y, out):
+        """The mixer of recurrent layer i: y [T, H] -> out [T, H]."""
+        l, c, T = self.layers[i], self.linear, batch.n_tokens
+        kd, vd = c.key_heads * c.key_dim, c.value_heads * c.value_dim
+        mix, mixed, decay = self.mix[:T], self.mixed[:T], self.decay[:T]
+        qk, q, k, v, gate = mix[:, :2 * kd], mix[:, :kd], mix[:, kd:2 * kd], mix[:, 2 * kd:2 * kd + vd], mix[:, 2 * kd + vd:]
+        abi.moe_project(self.mix_in, y, l["w_mix"], mix, self.mix_ws)
+        abi.moe_project(self.mix_decay, y, l["w_decay"], decay, self.mix_ws, bias=l["b_decay"])
+        abi.moe_head_norm(self.mix_qk, qk, qk)
+        abi.moe_linear_attention(c, self.states[i], batch.states, q, k, v, decay, mixed, self.linear_ws, scale=1 / c.key_dim)
+        abi.moe_head_norm(self.mix_norm, mixed, mixed, weight=l["mix_norm"], gate=gate)
+        abi.moe_project(self.mix_out, mixed, l["w_mix_out"], out, self.mix_ws)
 
     def run(self, x, batch):
         """x [T, H] through all layers; returns the residual stream after the last (a view of its buffer)."""
@@ -116,10 +161,13 @@ class DecoderLayers:
         resid.copy_(x)
         abi.moe_block_norm(self.norm_in, None, resid, None, y, w_pre=self.layers[0]["norm_attn"])
         for i, l in enumerate(self.layers):
-            torch.mm(y, l["w_qkv"].T, out=qkv)
-            abi.moe_kv_append(c, self.caches[i], batch, q, k, v, self.rope, q, self.attn_ws)
-            abi.moe_attention(c, self.caches[i], batch, q, ctx.view(T, QH, D), self.attn_ws)
-            torch.mm(ctx, l["w_o"].T, out=block)
+            if "w_mix" in l:
+                self.recurrent(i, batch, y, block)
+            else:
+                torch.mm(y, l["w_qkv"].T, out=qkv)
+                abi.moe_kv_append(c, self.caches[i], batch, q, k, v, self.rope, q, self.attn_ws)
+                abi.moe_attention(c, self.caches[i], batch, q, ctx.view(T, QH, D), self.attn_ws)
+                torch.mm(ctx, l["w_o"].T, out=block)
             abi.moe_block_norm(self.norm_attn[i], block, resid, resid, y, gate=l.get("attn_gate"), w_post=l.get("norm_attn_out"),
                                w_pre=l["norm_moe"])
             abi.moe_forward(self.moe, self.weights[i], y, T, block, None, self.moe_ws)
@@ -144,7 +192,10 @@ class DecoderLayers:
 
     def check(self):
         """Raises if a kernel recorded an error (waits for the current stream)."""
-        for name, ws in (("attention", self.attn_ws), ("moe", self.moe_ws)):
+        spaces = [("attention", self.attn_ws), ("moe", self.moe_ws)]
+        if self.linear is not None:
+            spaces += [("linear attention", self.linear_ws), ("project", self.mix_ws)]
+        for name, ws in spaces:
             st = abi.moe_check_status(ws)
             if st:
                 raise abi.MoeError("%s (device status)" % name, st)
@@ -160,8 +211,8 @@ class DecodeGraph:
         self.x = torch.zeros(B, H, dtype=torch.bfloat16, device=model.rope.device)
         self.kv_len = torch.zeros(B, dtype=torch.int32, device=model.rope.device)
         starts = torch.arange(B + 1, dtype=torch.int32, device=model.rope.device)
-        self.batch = abi.KVBatch(starts, self.kv_len, model.pages.table, B)
-        model.run(self.x, self.batch)  # warms up; with length 0 the tokens' position is negative: nothing is cached
+        self.batch = model.with_states(abi.KVBatch(starts, self.kv_len, model.pages.table, B))
+        model.run(self.x, self.batch)  # warms up; with length 0 the tokens' position is negative: nothing is cached, no state changes
         torch.cuda.current_stream().synchronize()
         self.graph = torch.cuda.CUDAGraph()
         with torch.cuda.graph(self.graph):
@@ -178,8 +229,9 @@ class DecodeGraph:
         return self.out
 
 
-def random_layers(moe_cfg, attn_cfg, n_layers, seed=0, device="cuda"):
-    """Random weights of a stack (a small example, or a benchmark's shapes)."""
+def random_layers(moe_cfg, attn_cfg, n_layers, seed=0, device="cuda", linear_cfg=None, recurrent=()):
+    """Random weights of a stack (a small example, or a benchmark's shapes); the layers numbered in `recurrent` have a
+    recurrent mixer of linear_cfg."""
     gen = torch.Generator(device=device).manual_seed(seed)
     r = lambda *s, std=0.02: (torch.randn(*s, device=device, generator=gen) * std).to(torch.bfloat16)  # noqa: E731
     H, E, I, Is = moe_cfg.hidden, moe_cfg.n_experts, moe_cfg.inter, moe_cfg.shared_inter
@@ -193,24 +245,33 @@ def random_layers(moe_cfg, attn_cfg, n_layers, seed=0, device="cuda"):
         for n in ("norm_attn", "norm_attn_out", "norm_moe", "norm_moe_out"):
             l[n] = 1 + r(H, std=0.1)
         out.append(l)
+    for i in recurrent:
+        c, l = linear_cfg, out[i]
+        kd, vd = c.key_heads * c.key_dim, c.value_heads * c.value_dim
+        del l["w_qkv"], l["w_o"]
+        l.update(w_mix=r(2 * kd + 2 * vd, H, std=H ** -0.5), w_decay=r(c.value_heads, H), w_mix_out=r(H, vd), mix_norm=1 + r(c.value_dim, std=0.1),
+                 b_decay=torch.linspace(0, 6, c.value_heads, device=device).to(torch.bfloat16))
     return out
 
 
 def main():
     moe = abi.config(hidden=256, n_experts=16, top_k=4, inter=128, shared_inter=128)
     attn = abi.attn_config(8, 2, 64, 16, rotary_dim=32)
-    layers = random_layers(moe, attn, 2)
-    model = DecoderLayers(moe, attn, layers, Pages(2, 512, 16, 80), 256, rope_table(512, 32), residual_scale=0.7)
     x = torch.randn(150, 256, device="cuda").to(torch.bfloat16)
-    model.prefill(x, [100, 50])
-    out = model.prefill(x[:60], [20, 40])
-    for _ in range(8):
-        out = model.decode(torch.randn(2, 256, device="cuda").to(torch.bfloat16))
-    graph = DecodeGraph(model)
-    for _ in range(8):
-        out = graph.step(torch.randn(2, 256, device="cuda").to(torch.bfloat16))
-    model.check()
-    print("two prompts in two pieces, 16 tokens each: lengths %s, |x| %.3f" % (model.pages.lens, float(out.float().abs().mean())))
+    for recurrent in ((), (0, 1, 2)):
+        linear = abi.linear_config(4, 8, 64, 64)
+        layers = random_layers(moe, attn, 4 if recurrent else 2, linear_cfg=linear, recurrent=recurrent)
+        model = DecoderLayers(moe, attn, layers, Pages(2, 512, 16, 80), 256, rope_table(512, 32), residual_scale=0.7, linear_cfg=linear)
+        model.prefill(x, [100, 50])
+        out = model.prefill(x[:60], [20, 40])
+        for _ in range(8):
+            out = model.decode(torch.randn(2, 256, device="cuda").to(torch.bfloat16))
+        graph = DecodeGraph(model)
+        for _ in range(8):
+            out = graph.step(torch.randn(2, 256, device="cuda").to(torch.bfloat16))
+        model.check()
+        print("%d layers, %d of them recurrent: two prompts in two pieces, 16 tokens each: lengths %s, |x| %.3f" %
+              (len(layers), len(recurrent), model.pages.lens, float(out.float().abs().mean())))
 
 
 if __name__ == "__main__":
