@@ -169,14 +169,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ------------------------------------------------------------------- the block's chunks --
     const int tiles = p.DV / DV;
     const int tile = (int)blockIdx.x % tiles, head = (int)blockIdx.x / tiles % p.VH, place = (int)blockIdx.x / tiles / p.VH;
-    int b;
-    {
-        int lo = 0, hi = p.n_seqs - 1;
-        while (lo < hi) {
-            const int mid = (lo + hi + 1) >> 1;
-            if (segment_base(p, mid) <= place) lo = mid; else hi = mid - 1;
-        }
-        b = lo;
+    int b = 0;  // the last sequence whose places begin at or before this one: 32 probes at a time
+    for (int end = p.n_seqs; end - b > 1;) {
+        const int step = (end - b + 31) / 32, at = b + lane * step;
+        const int n = __popc(__ballot_sync(0xffffffffu, at < end && segment_base(p, at) <= place));
+        b += max(n - 1, 0) * step;
+        end = min(b + step, end);
     }
     const Run run = load_run(p, b);
     // (where there is no other kernel, chunk_tokens is 0: a run of padding alone is this one's too)
@@ -364,7 +362,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int d = 0; d < DK / 2; ++d) {
                     S[d] = __ffma2_rn(S[d], both(f), make_float2(src[0], src[p.DV]));
                     src += 2 * p.DV;
-                    if (d % 16 == 15) asm volatile("" ::: "memory");  // (no more loads at once than there are registers for)
+                    if (d % 32 == 31) asm volatile("" ::: "memory");  // (no more loads at once than there are registers for)
                 }
             }
             if (STATES && seg == 0 && !run.fresh) store(place_at(segs - 1));

@@ -160,8 +160,10 @@ moe_status moe_linear_attention(const moe_linear_config *cfg, const moe_state_po
     a.status = static_cast<int *>(ws);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     // Which runs the chunk kernel takes goes by their own lengths, which only the device knows.  The host leaves a
-    // kernel out that has none for sure, and the chunk kernel in a step of one token a sequence.
-    const bool chunks = batch->n_seqs == 1 ? batch->n_tokens >= kChunkTokens : batch->n_tokens - batch->n_seqs >= kChunkTokens;
+    // kernel out that has none for sure, and the chunk kernel in steps of a few tokens a sequence (drafts), where its launch
+    // would cost more than a longer run among them: of up to 64 tokens, 8 us at one after another.
+    const int more = batch->n_tokens - batch->n_seqs;
+    const bool chunks = batch->n_seqs == 1 ? batch->n_tokens >= kChunkTokens : more >= 64 || batch->n_tokens >= kChunkTokens * batch->n_seqs;
     a.chunk_tokens = !chunks ? INT_MAX : batch->n_seqs == 1 ? 0 : kChunkTokens;
     if (chunks) {
         a.segment_chunks = segment_chunks(c, batch->n_seqs, batch->n_tokens);
