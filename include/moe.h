@@ -560,7 +560,7 @@ typedef struct {
 size_t moe_project_workspace_size(const moe_project_config *cfg, int max_T);
 
 /* y = resid + alpha * act(x w^T + bias): 16-bit products, sums and epilogue in fp32, rounded once.
- * Deterministic.  T of 0 does nothing.  y must not overlap x or w. */
+ * Deterministic.  T of 0 does nothing, more than 2^30 rows are not supported.  y must not overlap x or w. */
 moe_status moe_project(const moe_project_config *cfg, const moe_project_io *io, int T, void *ws, size_t ws_bytes,
                        void *stream);
 

@@ -133,7 +133,9 @@ __device__ __forceinline__ Two log2_of(float g) {  // g log2(e)
 }
 
 // Where sequence b's segments lie among the batch's.
-__device__ __forceinline__ int segment_base(const LinearArgs &p, int b) { return p.q_start[b] / (p.segment_chunks * kChunk) + b; }
+__device__ __forceinline__ int first_place(const LinearArgs &p, int b) {
+    return segment_base(p.q_start[b], b, p.segment_chunks, p.place_tokens);
+}
 
 // STATES: what each segment but a run's last adds to the state, and its decay; otherwise the outputs.
 template <int DK, int DV, bool F16, bool STATES>
@@ -172,14 +174,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     int b = 0;  // the last sequence whose places begin at or before this one: 32 probes at a time
     for (int end = p.n_seqs; end - b > 1;) {
         const int step = (end - b + 31) / 32, at = b + lane * step;
-        const int n = __popc(__ballot_sync(0xffffffffu, at < end && segment_base(p, at) <= place));
+        const int n = __popc(__ballot_sync(0xffffffffu, at < end && first_place(p, at) <= place));
         b += max(n - 1, 0) * step;
         end = min(b + step, end);
     }
     const Run run = load_run(p, b);
     // (where there is no other kernel, chunk_tokens is 0: a run of padding alone is this one's too)
     if (run.n < p.chunk_tokens) return;
-    const int all = (run.n + kChunk - 1) / kChunk, base = segment_base(p, b), seg = place - base;
+    const int all = (run.n + kChunk - 1) / kChunk, base = first_place(p, b), seg = place - base;
     const int segs = (all + p.segment_chunks - 1) / p.segment_chunks;
     const int kh = head / p.G, col0 = head * p.DV + tile * DV;  // the block's columns of v and out
     if (!STATES && seg == 0)
@@ -760,7 +762,7 @@ cudaError_t launch_kernel(const LinearArgs &a, const Maps &m, cudaStream_t s) {
         if (e != cudaSuccess) return e;
         ready[dev].store(true, std::memory_order_release);
     }
-    const int64_t segments = linear_segments(a.n_tokens, a.n_seqs, a.segment_chunks), blocks = segments * a.VH * (a.DV / DV);
+    const int64_t places = segment_base(a.n_tokens, a.n_seqs, a.segment_chunks, a.place_tokens), blocks = places * a.VH * (a.DV / DV);
     if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
     LaunchScope scope(STATES ? KC_LINEAR_STATES : KC_LINEAR_CHUNKS, s);
     kernel<<<(unsigned)blocks, kThreads, smem, s>>>(a, m);

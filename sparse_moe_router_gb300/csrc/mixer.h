@@ -20,13 +20,15 @@ struct LinearArgs {
     // sequences with at least this many new tokens are the chunk kernel's, the others the token kernel's
     int chunk_tokens;
     // chunk kernel: a run's chunks in segments of so many; with several, the state that each adds and its decay
-    int segment_chunks;
+    int segment_chunks, place_tokens;
     float *seg_states, *seg_decay;
 };
 constexpr int kChunk = 64;  // tokens a chunk
-// Segments of a batch, at most (sequence b owns the places base(b) .. base(b+1)-1, base(b) = q_start[b] / tokens + b).
-inline int64_t linear_segments(int64_t n_tokens, int64_t n_seqs, int64_t segment_chunks) {
-    return n_tokens / (segment_chunks * kChunk) + n_seqs;
+// Places of a batch's segments.  Sequence b owns the places base(q_start[b], b) .. base(q_start[b+1], b+1)-1: at least as many
+// as its run of n has segments of W tokens.  With place_tokens 0 one more than n / W for each sequence, else for each
+// place_tokens tokens (runs of fewer are not the chunk kernel's): of many sequences with few tokens, that is fewer.
+__host__ __device__ __forceinline__ int segment_base(int q_start, int b, int segment_chunks, int place_tokens) {
+    return q_start / (segment_chunks * kChunk) + (place_tokens > 0 ? q_start / place_tokens : b);
 }
 cudaError_t launch_linear_chunks(const LinearArgs &a, int dtype, cudaStream_t s);
 cudaError_t launch_linear_tokens(const LinearArgs &a, int dtype, bool after_chunks, cudaStream_t s);
@@ -196,7 +198,7 @@ __device__ __forceinline__ Run load_run(const LinearArgs &a, int b) {
         bad = bad || r.n > 0;
     }
     r.fresh = kv <= r.n || r.slot < 0;
-    r.pad = min(max(r.n - kv, 0), r.n);
+    r.pad = max(r.n - max(kv, 0), 0);
     r.q0 += r.pad;
     r.n -= r.pad;
     if (bad) layer_error(a.status);

@@ -41,8 +41,10 @@ moe_status check_linear_config(const moe_linear_config *c) {
     return MOE_OK;
 }
 
-// New tokens from which a run is the chunk kernel's.
-constexpr int kChunkTokens = 8;
+// New tokens from which a run is the chunk kernel's, and the same with several heads an SM, where the SMs are busy either way.
+// us token by token and in chunks, 32 heads of 128 and 128: one run of 8 tokens 12 and 8; 16 sequences of 8 30 and 38, of 16 47 and
+// 39; 64 of 16 159 and 137, of 32 275 and 139; 200 of 8 289 and 410.
+constexpr int kChunkTokens = 8, kManyTokens = 16;
 // Segments times heads times column tiles that a batch may have when its runs are cut: the states they add are in the workspace.
 constexpr int64_t kMostSegments = 640;
 
@@ -164,8 +166,10 @@ moe_status moe_linear_attention(const moe_linear_config *cfg, const moe_state_po
     // would cost more than a longer run among them: of up to 64 tokens, 8 us at one after another.
     const int more = batch->n_tokens - batch->n_seqs;
     const bool chunks = batch->n_seqs == 1 ? batch->n_tokens >= kChunkTokens : more >= 64 || batch->n_tokens >= kChunkTokens * batch->n_seqs;
-    a.chunk_tokens = !chunks ? INT_MAX : batch->n_seqs == 1 ? 0 : kChunkTokens;
+    const bool many = (int64_t)batch->n_seqs * c.value_heads * value_tiles(c) > 2 * device_info().sm_count;
+    a.chunk_tokens = !chunks ? INT_MAX : batch->n_seqs == 1 ? 0 : many ? kManyTokens : kChunkTokens;
     if (chunks) {
+        a.place_tokens = many && batch->n_tokens / kManyTokens < batch->n_seqs ? kManyTokens : 0;
         a.segment_chunks = segment_chunks(c, batch->n_seqs, batch->n_tokens);
         const LinearLayout l = linear_layout(c, batch->n_seqs, batch->n_tokens);
         if ((int64_t)a.segment_chunks * kChunk < batch->n_tokens) {
@@ -221,6 +225,7 @@ moe_status moe_project(const moe_project_config *cfg, const moe_project_io *io, 
     MOE_TRY(check_project_config(cfg));
     const moe_project_config &c = *cfg;
     if (T < 0) return MOE_ERR_INVALID_ARG;
+    if (T > 1 << 30) return MOE_ERR_UNSUPPORTED_SHAPE;
     if (T == 0) return MOE_OK;
     if (!io || !good_rows(io->x, io->x_ld, c.inputs) || !good_rows(io->w, io->w_ld, c.inputs)) return MOE_ERR_INVALID_ARG;
     if (!good_rows(io->y, io->y_ld, c.outputs) || !aligned(io->bias, 16)) return MOE_ERR_INVALID_ARG;

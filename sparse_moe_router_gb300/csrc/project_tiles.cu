@@ -97,10 +97,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint32_t phase = 0;
             for (int tile = pair; tile < tiles && ok; tile += pairs, ++n) {
                 const int buf = n & 1;
-                if (!(ok = ptx::mbar_wait_cluster(&sums_empty[buf], ((n >> 1) & 1) ^ 1, 2000000000ull, abort_flag))) break;
+                if (!(ok = ptx::mbar_sleep_wait<true>(&sums_empty[buf], ((n >> 1) & 1) ^ 1, abort_flag))) break;
                 ptx::tc_fence_after();
                 for (int k = 0; k < blocks; ++k, ++it) {
-                    if (!(ok = ptx::mbar_wait_cluster(&full[s], phase, 2000000000ull, abort_flag))) break;
+                    if (!(ok = ptx::mbar_sleep_wait<true>(&full[s], phase, abort_flag))) break;
                     ptx::tc_fence_after();
                     const uint64_t da = desc0 + (uint64_t)(s * sh.stage_bytes >> 4), db = da + (kXBytes >> 4);
                     ptx::mma_bf16_pair(tmem + buf * kBuf, da, db, idesc, k > 0);

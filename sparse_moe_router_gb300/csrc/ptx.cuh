@@ -147,17 +147,28 @@ __device__ __forceinline__ bool mbar_wait(uint64_t *bar, uint32_t parity, uint64
 }
 
 // mbar_wait in few instructions, for kernels whose warps wait in many places: a try may sleep up to 2 us in the hardware
-// (it wakes when the phase completes), and 2^20 of them (2 s, less where the hardware does not sleep) are the limit.
+// (it wakes when the phase completes), and 2^20 of them (2 s, less where the hardware does not sleep) are the limit.  The
+// clock that mbar_wait reads after a first try costs more than most waits.  CLUSTER: threads of the peer CTA arrive too.
+template <bool CLUSTER = false>
 __device__ __forceinline__ bool mbar_sleep_wait(uint64_t *bar, uint32_t parity, volatile int *abort) {
     for (int n = 0; n < 1 << 20; ++n) {
         uint32_t ok;
-        asm volatile(
-            "{\n\t.reg .pred p;\n\t"
-            "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
-            "selp.u32 %0, 1, 0, p;\n\t}"
-            : "=r"(ok)
-            : "r"(smem_u32(bar)), "r"(parity), "r"(2000u)
-            : "memory");
+        if (CLUSTER)
+            asm volatile(
+                "{\n\t.reg .pred p;\n\t"
+                "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n\t"
+                "selp.u32 %0, 1, 0, p;\n\t}"
+                : "=r"(ok)
+                : "r"(smem_u32(bar)), "r"(parity), "r"(2000u)
+                : "memory");
+        else
+            asm volatile(
+                "{\n\t.reg .pred p;\n\t"
+                "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+                "selp.u32 %0, 1, 0, p;\n\t}"
+                : "=r"(ok)
+                : "r"(smem_u32(bar)), "r"(parity), "r"(2000u)
+                : "memory");
         if (ok) return true;
         if (*abort) return false;
     }

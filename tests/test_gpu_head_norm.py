@@ -114,3 +114,18 @@ def test_other_stream_graph_replay_and_no_rows():
     torch.cuda.synchronize()
     assert torch.equal(a.flip(0), b)
     abi.moe_head_norm(cfg, x[:0], b[:0], weight=weight, gate=gate[:0])
+
+
+def test_rows_past_32_bits():
+    T, heads, dim, ld = 33000, 2, 64, 66048
+    x = torch.empty((T - 1) * ld + heads * dim, dtype=torch.bfloat16, device="cuda").as_strided((T, heads * dim), (ld, 1))
+    x.copy_(torch.randn(T, heads * dim, device="cuda"))
+    assert (T - 1) * ld > 2 ** 31
+    cfg = abi.head_norm_config(heads, dim)
+    y = torch.empty(T, heads * dim, dtype=torch.bfloat16, device="cuda")
+    abi.moe_head_norm(cfg, x, y)
+    z = torch.empty_like(y)
+    abi.moe_head_norm(cfg, x.contiguous(), z)
+    assert torch.equal(y, z)
+    abi.moe_head_norm(cfg, x, x)
+    assert torch.equal(x.contiguous(), z)

@@ -104,6 +104,38 @@ def test_long_and_mixed_batches(decay, KH, VH):
     c.check(*c.run())
 
 
+def test_a_few_runs_among_many_single_tokens():
+    """More heads than SMs, and few tokens a sequence: the chunk kernel's blocks go by tokens, not by sequences."""
+    new = [1] * 120
+    for at, n in ((0, 15), (7, 200), (8, 16), (30, 0), (31, 17), (64, 64), (119, 130)):
+        new[at] = n
+    c = Case(abi.linear_config(2, 4, 64, 64), new, [3 * (i % 3) for i in range(120)], seed=3, behind=2)
+    assert 120 * 4 > 304 and c.T // 16 < 120
+    c.check(*c.run())
+    c.starts[60] = 5  # a range that ends before it begins counts as none, the one before it overlaps others' rows
+    c.run(status=1)
+
+
+def test_slots_past_32_bits():
+    """The last slots of a pool of more than 2^31 values."""
+    cfg = abi.linear_config(2, 8, 128, 256)
+    n_slots = 8200
+    assert n_slots * 8 * 128 * 256 > 2 ** 31
+    states = torch.empty(n_slots, 8, 128, 256, device="cuda")
+    for new in ([3, 1], [150, 9]):
+        c = Case(cfg, new, [4, 4], seed=1, n_slots=2)
+        out, small = c.run()
+        far = [n_slots - 1, 8193]
+        for b in (0, 1):
+            states[far[b]] = c.states[c.slots[b]]
+        near = list(c.slots)
+        c.slots = far
+        got, _ = c.run(states=states)
+        assert torch.equal(got, out)
+        for b in (0, 1):
+            assert torch.equal(states[far[b]], small[near[b]])
+
+
 def test_many_chunks_over_few_heads():
     """One head of a long prompt: its chunks are shared out over the SMs."""
     for n, VH, past in ((3000, 1, 0), (3001, 2, 17), (2047, 3, 0)):

@@ -123,6 +123,23 @@ def test_repeats_and_streams_and_graphs_agree():
         assert torch.equal(a.flip(0), b), T
 
 
+def test_rows_past_32_bits():
+    """Rows so far apart that the last lie more than 2^32 bytes and 2^31 values behind the first."""
+    T, K, N, ld = 33000, 64, 32, 66048
+    x = torch.empty((T - 1) * ld + K, dtype=BF, device="cuda").as_strided((T, K), (ld, 1))
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    x.copy_(torch.randn(T, K, device="cuda", generator=gen))
+    w = torch.randn(N, K, device="cuda", generator=gen).to(BF)
+    wide = torch.randn(520, K, device="cuda", generator=gen).to(BF)
+    assert (T - 1) * ld > 2 ** 31
+    for weights in (w, wide):
+        y = _run(x, weights)
+        _check(y[-300:], x[-300:], weights, None, None, "none", 1.0)
+        _check(y[:300], x[:300], weights, None, None, "none", 1.0)
+    _check(_run(x[-3:], wide), x[-3:], wide, None, None, "none", 1.0)
+    _check(_run(x[-90:], wide), x[-90:], wide, None, None, "none", 1.0)
+
+
 def test_no_rows_is_a_no_op():
     x, w, _, _ = _make(1, 64, 64, BF)
     cfg = abi.project_config(64, 64)

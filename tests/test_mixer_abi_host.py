@@ -102,6 +102,7 @@ def test_project_refusals():
         return L.moe_project(ctypes.byref(c), None if drop_io else ctypes.byref(d), T, ws, ws_bytes, None)
 
     assert call(T=0, drop_io=True) == OK and call(T=-1) == INVALID and call(drop_io=True) == INVALID
+    assert call(T=(1 << 30) + 1) == UNSUPPORTED
     assert L.moe_project(None, None, 1, A, 256, None) == INVALID
     for kw in (dict(inputs=252), dict(outputs=60), dict(inputs=65544), dict(outputs=(1 << 20) + 8)):
         assert call(**kw) == UNSUPPORTED, kw
