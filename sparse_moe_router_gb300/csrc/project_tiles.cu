@@ -90,31 +90,36 @@ __global__ void __launch_bounds__(kThreads, 1)
             fills[0] = it;
         }
     } else if (warp == kMmaWarp) {
-        if (lane == 0 && rank == 0) {
+        if (rank == 0) {  // the whole warp waits, one lane of it issues (its operands then stay in uniform registers)
             const uint32_t idesc = ptx::idesc_16_f32(F16, 2 * kRows, bn, false, false);
             const uint64_t desc0 = ptx::sw128_desc(ptx::smem_u32(smem));
+            auto wait = [&](uint64_t *bar, uint32_t parity) {
+                return __all_sync(0xffffffffu, ptx::mbar_sleep_wait<true>(bar, parity, abort_flag)) != 0;
+            };
             int it = 0, s = 0, n = 0;
             uint32_t phase = 0;
             for (int tile = pair; tile < tiles && ok; tile += pairs, ++n) {
                 const int buf = n & 1;
-                if (!(ok = ptx::mbar_sleep_wait<true>(&sums_empty[buf], ((n >> 1) & 1) ^ 1, abort_flag))) break;
+                if (!(ok = wait(&sums_empty[buf], ((n >> 1) & 1) ^ 1))) break;
                 ptx::tc_fence_after();
                 for (int k = 0; k < blocks; ++k, ++it) {
-                    if (!(ok = ptx::mbar_sleep_wait<true>(&full[s], phase, abort_flag))) break;
+                    if (!(ok = wait(&full[s], phase))) break;
                     ptx::tc_fence_after();
-                    const uint64_t da = desc0 + (uint64_t)(s * sh.stage_bytes >> 4), db = da + (kXBytes >> 4);
-                    ptx::mma_bf16_pair(tmem + buf * kBuf, da, db, idesc, k > 0);
+                    if (ptx::elect_one()) {
+                        const uint64_t da = desc0 + (uint64_t)(s * sh.stage_bytes >> 4), db = da + (kXBytes >> 4);
 #pragma unroll
-                    for (int j = 1; j < 4; ++j) ptx::mma_bf16_pair(tmem + buf * kBuf, da + 2 * j, db + 2 * j, idesc, 1);
-                    ptx::mma_commit_pair(&empty[s], 3);
+                        for (int j = 0; j < 4; ++j) ptx::mma_bf16_pair(tmem + buf * kBuf, da + 2 * j, db + 2 * j, idesc, k > 0 || j > 0);
+                        ptx::mma_commit_pair(&empty[s], 3);
+                        if (k + 1 == blocks) ptx::mma_commit_pair(&sums_full[buf], 3);
+                    }
+                    __syncwarp();
                     if (++s == stages) s = 0, phase ^= 1;
                 }
-                if (ok) ptx::mma_commit_pair(&sums_full[buf], 3);
             }
             fills[1] = it;
-            ptx::mma_commit_pair(drain, 1);  // nothing of the pair may run on when TMEM is freed
+            if (ptx::elect_one()) ptx::mma_commit_pair(drain, 1);  // nothing of the pair may run on when TMEM is freed
             int zero = 0;
-            if (!ptx::mbar_sleep_wait(drain, 0, &zero)) ok = false;
+            if (!__all_sync(0xffffffffu, ptx::mbar_sleep_wait(drain, 0, &zero))) ok = false;
         }
         __syncwarp();
     } else {
@@ -240,13 +245,13 @@ cudaError_t launch(const ProjectArgs &a, cudaStream_t s) {
     if (e != cudaSuccess) return e;
     // The tile that ends soonest, in cycles: rounds of all pairs, each of K / 64 steps and about 800 for its start and end.  A
     // step's MMAs take 2 cycles a column; its operands, (128 + bn / 2) rows of 128 bytes, come at about 66 bytes a cycle
-    // from L2, which is more below 256 columns (and narrower tiles have to gain 3%).
+    // from L2, which is more below 256 columns (and narrower tiles have to gain 3%); a step alone takes 340.
     const int64_t rows = (a.T + 2 * kRows - 1) / (2 * kRows), steps = (a.K + 63) / 64;
     int bn = 256;
     double least = 1e30;
     for (int n = 256; n >= 48; n -= 16) {
         const int64_t rounds = (rows * ((a.N + n - 1) / n) + pairs - 1) / pairs;
-        const double cost = (double)rounds * (steps * fmax(2.0 * n, 248 + 0.97 * n) + 800) * (n == 256 ? 1.0 : 1.03);
+        const double cost = (double)rounds * (steps * fmax(2.0 * n, fmax(340, 248 + 0.97 * n)) + 800) * (n == 256 ? 1.0 : 1.03);
         if (cost < least) least = cost, bn = n;
     }
     Shape sh;
