@@ -16,8 +16,20 @@
 // run's chunks are cut into segments: a first kernel computes what each segment adds to the state (K and V only),
 // and each segment's block begins with the sum of those before it.
 //
+// Bound: shared memory.  At DK = DV = 128 a chunk's operands, copies, splits and transposes move some 3800 times 128 bytes (U
+// alone, whose values come in three parts, 1280), and 4250 cycles are measured; the tensor cores are busy for 1790 of them.
+// Beside that the instruction cache: all loops that need not be unrolled are not (92 KB of straight-line roles took 10,900
+// cycles a chunk, most of them waiting for instructions), nothing may spill (shared memory leaves no L1: 52 bytes of spills
+// cost 30%), and what a chunk's decays need is read two chunks ahead.
+//
+// Measured, 32 value heads and 16 key heads of 128: 8192 tokens 112 us (39 of them the first kernel's) where token by token
+// takes 10,270; 512 tokens 21, 64 tokens 7.7; 12 runs of up to 1031 tokens, 20 heads of 64 and 128 in fp16, 50 (its longest run's
+// 17 chunks, one after another: fp16's scales of P take a pass of their own).  On the way: decays in 64-bit floats 3000 cycles a
+// chunk; outputs stored 2 bytes at a time 10,000; A in one place 97 us for the second kernel where two take 84; weighted values as
+// an operand in TMEM, 16 or 32 tokens at a time, 116 to 126 in all.
+//
 // Roles (16 warps): 0-3 the state; 4-7 the output; 8-11 weighted values; 12, 13 P (a row a thread); 14 copies (TMA)
-// and decays; 15 the MMAs.
+// and decays; 15 the MMAs.  Without outputs 4-11 weigh values and 12 copies.
 #include <atomic>
 
 #include "mixer.h"

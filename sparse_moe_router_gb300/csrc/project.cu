@@ -3,6 +3,9 @@
 // With few rows the weights are all there is to move.  A warp takes 4 rows of w and up to 4 rows of x; its lanes
 // walk K in 16-byte pieces (8 weights), so that every piece of x serves 4 weights and every weight all rows of x.  Where
 // N gives too few warps, the warps of a block share K.
+//
+// Bound: HBM, the weights.  Measured, one row of 2048 and 12,288 outputs: 10.0 us (5.0 TB/s, 74% of the measured copy; the
+// rest is its start and end), as with 2 rows of w a warp (9.9); 8 rows 10.3.
 #include "mixer.h"
 #include "ptx.cuh"
 

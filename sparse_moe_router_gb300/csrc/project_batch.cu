@@ -5,6 +5,10 @@
 // the short side on its N side.  There are fewer such tiles than SMs, so a cluster of blocks shares K, each with its
 // own part, and joins the parts through distributed shared memory, each block a share of the outputs, in the order
 // of the blocks.
+//
+// Bound: its start and end, then the long side's bytes.  Measured: 48 rows of 4096, 2048 outputs and a residual 7.4 us (16
+// tiles in 8 parts; the weights alone would take 2.6), 8192 rows of 2048 and 32 outputs 9.6 (the rows 5.2).  The setup runs
+// under the end of the kernel before: without that 8.7 and 10.2.
 #include <atomic>
 
 #include "mixer.h"
