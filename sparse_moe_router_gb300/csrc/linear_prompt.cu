@@ -19,7 +19,7 @@
 // Bound: shared memory.  At DK = DV = 128 a chunk's operands, copies, splits and transposes move some 3800 times 128 bytes (U
 // alone, whose values come in three parts, 1280), and 4250 cycles are measured; the tensor cores are busy for 1790 of them.
 // Beside that the instruction cache: all loops that need not be unrolled are not (92 KB of straight-line roles took 10,900
-// cycles a chunk, most of them waiting for instructions), nothing may spill (shared memory leaves no L1: 52 bytes of spills
+// cycles a chunk, most of them waiting for instructions), little may spill (28 bytes of fp16's do; shared memory leaves no L1: 52 bytes
 // cost 30%), and what a chunk's decays need is read two chunks ahead.
 //
 // Measured, 32 value heads and 16 key heads of 128: 8192 tokens 112 us (39 of them the first kernel's) where token by token

@@ -54,6 +54,9 @@ struct ProjectArgs {
 cudaError_t launch_project_rows(const ProjectArgs &a, int dtype, cudaStream_t s);   // a few rows
 cudaError_t launch_project_batch(const ProjectArgs &a, int dtype, cudaStream_t s);  // at most 256 rows or outputs
 cudaError_t launch_project_tiles(const ProjectArgs &a, int dtype, cudaStream_t s);  // any
+// Estimates, us, of the last two, for at most 256 rows or outputs.
+cudaError_t project_batch_time(const ProjectArgs &a, int dtype, double *us);
+double project_tiles_time(const ProjectArgs &a);
 
 // Lets a kernel's setup run under the end of the one before it on the stream (it then waits before its first access).
 inline void overlap_prior(cudaLaunchAttribute &attr) {

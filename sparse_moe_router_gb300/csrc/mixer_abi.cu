@@ -163,7 +163,7 @@ moe_status moe_linear_attention(const moe_linear_config *cfg, const moe_state_po
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     // Which runs the chunk kernel takes goes by their own lengths, which only the device knows.  The host leaves a
     // kernel out that has none for sure, and the chunk kernel in steps of a few tokens a sequence (drafts), where its launch
-    // would cost more than a longer run among them: of up to 64 tokens, 8 us at one after another.
+    // would cost more than a longer run among them: where no sequence is empty, of up to 64 tokens, 1.2 us each.
     const int more = batch->n_tokens - batch->n_seqs;
     const bool chunks = batch->n_seqs == 1 ? batch->n_tokens >= kChunkTokens : more >= 64 || batch->n_tokens >= kChunkTokens * batch->n_seqs;
     const bool many = (int64_t)batch->n_seqs * c.value_heads * value_tiles(c) > 2 * device_info().sm_count;
@@ -249,9 +249,26 @@ moe_status moe_project(const moe_project_config *cfg, const moe_project_io *io, 
     a.scale = c.scale;
     a.status = static_cast<int *>(ws);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    if (T <= 4) MOE_CUDA(launch_project_rows(a, c.dtype, s));
-    else if (T <= 256 || c.outputs <= 64) MOE_CUDA(launch_project_batch(a, c.dtype, s));
-    else MOE_CUDA(launch_project_tiles(a, c.dtype, s));
+    // One row, or a few and few weights, go row by row: the tensor cores' start and end would take longer.  us by rows and in a
+    // batch: 1 row of 2048, 12,288 outputs 10.0 and 11.6, of 4096, 2048 outputs 4.0 and 6.0; 2 of 2048 and 12,288 16.8 and 11.8;
+    // 4 of 1024 and 4096 (2^22 products for each four rows) 4.6 and 4.6; 16 of 2048 and 256 2.9 and 4.6, and 1024 5.8 and 4.9.
+    if (T == 1 || (T <= 32 && (int64_t)((T + 3) / 4) * c.inputs * c.outputs <= 1 << 22)) {
+        MOE_CUDA(launch_project_rows(a, c.dtype, s));
+        return MOE_OK;
+    }
+    // A short side is a batch's while its parts of K share the SMs in one round; with more tiles than that the other kernel,
+    // whose blocks stay, is ahead.  By estimates; measured, us, in a batch and in tiles: 256 rows of 8192, 4096 outputs 25 and 32,
+    // 8192 outputs 43 and 34; 64 rows of 2048, 12,288 outputs 14 and 15, 256 rows 29 and 17; 2048 rows of 2048, 96 outputs 8.0
+    // and 11.3, 256 outputs 13.4 and 11.5.
+    if (T <= 256 || c.outputs <= 256) {
+        double us = 0;
+        MOE_CUDA(project_batch_time(a, c.dtype, &us));
+        if (us <= project_tiles_time(a)) {
+            MOE_CUDA(launch_project_batch(a, c.dtype, s));
+            return MOE_OK;
+        }
+    }
+    MOE_CUDA(launch_project_tiles(a, c.dtype, s));
     return MOE_OK;
 }
 

@@ -5,7 +5,7 @@
 // N gives too few warps, the warps of a block share K.
 //
 // Bound: HBM, the weights.  Measured, one row of 2048 and 12,288 outputs: 10.0 us (5.0 TB/s, 74% of the measured copy; the
-// rest is its start and end), as with 2 rows of w a warp (9.9); 8 rows 10.3.
+// rest is its start and end); with 2 rows of w a warp 9.9, so no gain.  One row of 4096 and 2048 outputs 3.4, of 2048 and 256 1.7.
 #include "mixer.h"
 #include "ptx.cuh"
 
@@ -106,8 +106,13 @@ cudaError_t launch_shape(const ProjectArgs &a, cudaStream_t s) {
 template <int X, bool F16>
 cudaError_t launch(const ProjectArgs &a, cudaStream_t s) {
     const int64_t warps = (int64_t)(a.N + kWRows - 1) / kWRows * ((a.T + X - 1) / X);
-    if (warps >= 16 * device_info().sm_count) return launch_shape<X, 1, F16>(a, s);
-    return launch_shape<X, 8, F16>(a, s);
+    // Warps that share K, the fewer the more there are: us with 1, 2, 4 and 8, one row of 2048: 2048 outputs 3.5, 2.9, 2.7, 2.4;
+    // 4096 6.3, 5.1, 3.4, 4.1; 8192 7.7, 6.6, 6.8, 7.7; 12,288 10.0, 11.8, 10.3, 10.9.  Long rows want several all the same:
+    // of 4096, 12,288 outputs 17.9, 20.7, 17.2, 17.5; 24,576 34.6, 33.4, 31.5, 31.7.
+    const int sms = device_info().sm_count;
+    if (warps <= 4 * sms) return launch_shape<X, 8, F16>(a, s);
+    if (warps <= 8 * sms || a.K >= 4096) return launch_shape<X, 4, F16>(a, s);
+    return warps <= 16 * sms ? launch_shape<X, 2, F16>(a, s) : launch_shape<X, 1, F16>(a, s);
 }
 
 }  // namespace

@@ -1,5 +1,5 @@
-// project_batch.cu -- moe_project on the 5th-generation tensor cores where one side is short: a batch of up to 256 rows (a
-// decode step), or up to 256 outputs.
+// project_batch.cu -- moe_project on the 5th-generation tensor cores where one side is short: up to 256 rows (a decode
+// step), or up to 256 outputs.
 //
 // The long side's rows (w, or x) are what there is to read, and go by once: 128 of them on the M side of a tile, all rows of
 // the short side on its N side.  There are fewer such tiles than SMs, so a cluster of blocks shares K, each with its
@@ -8,8 +8,10 @@
 //
 // Bound: its start and end, then the long side's bytes.  Measured: 48 rows of 4096, 2048 outputs and a residual 7.4 us (16
 // tiles in 8 parts; the weights alone would take 2.6), 8192 rows of 2048 and 32 outputs 9.6 (the rows 5.2).  The setup runs
-// under the end of the kernel before: without that 8.7 and 10.2.
+// under the end of the kernel before.  More warps that read the sums (8 or 16 for 4) gained nothing: 7.6 and 7.7, 8.9 and 9.4.
 #include <atomic>
+#include <cmath>
+#include <mutex>
 
 #include "mixer.h"
 #include "ptx.cuh"
@@ -158,61 +160,121 @@ __global__ void __launch_bounds__(kThreads)
     if (split > 1) ptx::cluster_sync();  // nobody leaves while others read its sums
 }
 
+// Rows of the long and the short side; blocks whose shared memory goes twice on an SM where the short side leaves room.
+struct Sides {
+    int64_t a;
+    int b, nb, room, per_sm;
+    explicit Sides(const ProjectArgs &p) {
+        a = p.T <= p.N ? p.N : p.T, b = p.T <= p.N ? p.T : p.N;
+        nb = (b + 15) / 16 * 16;
+        per_sm = nb <= 128 ? 2 : 1;
+        room = per_sm == 2 ? 108 * 1024 : 220 * 1024;
+    }
+};
+
 template <bool SWAP, bool F16>
-cudaError_t launch(const ProjectArgs &a, cudaStream_t s) {
-    const int64_t rows_a = SWAP ? a.N : a.T;
-    const int rows_b = SWAP ? a.T : a.N;
-    Shape sh;
-    sh.nb = (rows_b + 15) / 16 * 16;
-    sh.stage_bytes = kLongBytes + sh.nb * 128;
-    sh.cols = sh.nb <= 32 ? 32 : sh.nb <= 64 ? 64 : sh.nb <= 128 ? 128 : 256;
-    const int sums = kLong * (SWAP ? sh.nb : sh.nb + 4) * 4;
-    // two blocks an SM where the sums and enough stages leave room
-    const int room = sh.nb <= 128 ? 108 * 1024 : 220 * 1024;
-    sh.stages = min(room / sh.stage_bytes, kMaxStages);
-    const int smem = 1024 + max(sh.stages * sh.stage_bytes, sums);
-    // As many blocks a tile as end soonest, in blocks of 64 of K; a block's start and end count as 6, each part to join as 1/2.
-    const int sms = device_info().sm_count * (room > 110 * 1024 ? 1 : 2), blocks = (a.K + 63) / 64;
-    const int64_t tiles = (rows_a + kLong - 1) / kLong;
-    int split = 1;
-    double least = 1e30;
-    for (int n = 1; n <= min(kMaxSplit, blocks); ++n) {
-        const double cost = (double)((tiles * n + sms - 1) / sms) * ((blocks + n - 1) / n + 6) + 0.5 * n;
-        if (cost < least) least = cost, split = n;
-    }
-    Maps m;
-    if (!encode_tmap_rows(&m.a, SWAP ? a.w : a.x, rows_a, a.K, SWAP ? a.w_ld : a.x_ld, kLong) ||
-        !encode_tmap_rows(&m.b, SWAP ? a.x : a.w, rows_b, a.K, SWAP ? a.x_ld : a.w_ld, sh.nb))
-        return cudaErrorInvalidValue;
-    auto *kernel = project_batch_kernel<SWAP, F16>;
-    static std::atomic<bool> ready[64];  // of each device: the shared-memory opt-in
-    int dev = 0;
-    cudaGetDevice(&dev);
-    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
-    cudaError_t e = cudaSuccess;
-    if (!ready[dev].load(std::memory_order_acquire)) {
-        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMostSmem);
-        if (e != cudaSuccess) return e;
-        ready[dev].store(true, std::memory_order_release);
-    }
+cudaLaunchConfig_t config(cudaLaunchAttribute (&attr)[2], int64_t blocks, int split, int smem, cudaStream_t s) {
     cudaLaunchConfig_t cfg = {};
-    cudaLaunchAttribute attr[2];
     overlap_prior(attr[0]);
     attr[1].id = cudaLaunchAttributeClusterDimension;
     attr[1].val.clusterDim.x = split;
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
-    cfg.gridDim = dim3((unsigned)(tiles * split));
+    cfg.gridDim = dim3((unsigned)blocks);
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
     cfg.attrs = attr;
     cfg.numAttrs = split > 1 ? 2 : 1;
+    return cfg;
+}
+
+// Clusters of each size that the device holds at once with one block an SM: fewer than SMs / size, as a cluster stays within
+// a group of SMs (76 clusters of 2, 36 of 4, 23 of 6, 15 of 8).
+struct Held {
+    std::atomic<bool> ready;
+    int clusters[kMaxSplit + 1];
+};
+template <bool SWAP, bool F16>
+cudaError_t held(const Held **out) {
+    static Held all[64];
+    static std::mutex lock;
+    int dev = 0;
+    cudaGetDevice(&dev);
+    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    Held &h = all[dev];
+    if (!h.ready.load(std::memory_order_acquire)) {
+        std::lock_guard<std::mutex> hold(lock);
+        auto *kernel = project_batch_kernel<SWAP, F16>;
+        cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMostSmem);
+        if (e != cudaSuccess) return e;
+        h.clusters[1] = device_info().sm_count;
+        for (int n = 2; n <= kMaxSplit; ++n) {
+            cudaLaunchAttribute attr[2];
+            const cudaLaunchConfig_t cfg = config<SWAP, F16>(attr, (int64_t)n * device_info().sm_count, n, kMostSmem, nullptr);
+            if ((e = cudaOccupancyMaxActiveClusters(&h.clusters[n], kernel, &cfg)) != cudaSuccess) return e;
+        }
+        h.ready.store(true, std::memory_order_release);
+    }
+    *out = &h;
+    return cudaSuccess;
+}
+
+// How many blocks share a tile's K, and about how long the whole takes (us): rounds of as many clusters as the device holds,
+// each of K / 64 steps (0.26 us of 16 columns, 0.39 of 256) or of its share of the bytes at 6.5 TB/s, if that is longer, and of
+// a start and end of 2.8 and more for each column that is laid down and joined.  Measured, us, with 1, 2, 4 and 8 blocks a tile:
+// 48 rows of 4096 and 2048 outputs 23, 14, 9, 7.3; 8192 of 2048 and 32 14.4, 10.3, 9.0, 14.3; 256 of 4096 and 2048 33.5,
+// 23.3, 15.3, 23.9 (6: 14.8).
+template <bool SWAP, bool F16>
+cudaError_t plan(const ProjectArgs &p, int *split, double *us) {
+    const Held *h = nullptr;
+    const cudaError_t e = held<SWAP, F16>(&h);
+    if (e != cudaSuccess) return e;
+    const Sides d(p);
+    const int blocks = (p.K + 63) / 64;
+    const int64_t tiles = (d.a + kLong - 1) / kLong;
+    const double step = 0.252 + 0.00054 * d.nb, move = 2e-6 * p.K * (d.a + d.b) / 6.5;
+    *us = 1e30;
+    for (int n = 1; n <= min(kMaxSplit, blocks); ++n) {
+        const int64_t most = max(h->clusters[n] * d.per_sm, 1), rounds = (tiles + most - 1) / most;
+        const double t = fmax(rounds * step * ((blocks + n - 1) / n), move) + rounds * (2.8 + d.nb * (0.023 + 0.022 / n));
+        if (t < *us) *us = t, *split = n;
+    }
+    return cudaSuccess;
+}
+
+template <bool SWAP, bool F16>
+cudaError_t launch(const ProjectArgs &a, cudaStream_t s) {
+    int split = 1;
+    double us = 0;
+    cudaError_t e = plan<SWAP, F16>(a, &split, &us);
+    if (e != cudaSuccess) return e;
+    const Sides d(a);
+    Shape sh;
+    sh.nb = d.nb;
+    sh.stage_bytes = kLongBytes + sh.nb * 128;
+    sh.cols = sh.nb <= 32 ? 32 : sh.nb <= 64 ? 64 : sh.nb <= 128 ? 128 : 256;
+    const int sums = kLong * (SWAP ? sh.nb : sh.nb + 4) * 4;
+    sh.stages = min(d.room / sh.stage_bytes, kMaxStages);
+    const int smem = 1024 + max(sh.stages * sh.stage_bytes, sums);
+    Maps m;
+    if (!encode_tmap_rows(&m.a, SWAP ? a.w : a.x, d.a, a.K, SWAP ? a.w_ld : a.x_ld, kLong) ||
+        !encode_tmap_rows(&m.b, SWAP ? a.x : a.w, d.b, a.K, SWAP ? a.x_ld : a.w_ld, sh.nb))
+        return cudaErrorInvalidValue;
+    cudaLaunchAttribute attr[2];
+    const cudaLaunchConfig_t cfg = config<SWAP, F16>(attr, (d.a + kLong - 1) / kLong * split, split, smem, s);
     LaunchScope scope(KC_PROJECT_BATCH, s);
-    e = cudaLaunchKernelEx(&cfg, kernel, a, m, sh, split);
+    e = cudaLaunchKernelEx(&cfg, project_batch_kernel<SWAP, F16>, a, m, sh, split);
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 }  // namespace
+
+cudaError_t project_batch_time(const ProjectArgs &a, int dtype, double *us) {
+    const bool f16 = dtype == MOE_DTYPE_F16;
+    int split;
+    if (a.T <= a.N) return f16 ? plan<true, true>(a, &split, us) : plan<true, false>(a, &split, us);
+    return f16 ? plan<false, true>(a, &split, us) : plan<false, false>(a, &split, us);
+}
 
 cudaError_t launch_project_batch(const ProjectArgs &a, int dtype, cudaStream_t s) {
     const bool f16 = dtype == MOE_DTYPE_F16;

@@ -280,6 +280,13 @@ cudaError_t launch(const ProjectArgs &a, cudaStream_t s) {
 
 }  // namespace
 
+// About how long it takes with a short side of at most 256: steps of K, or the bytes at 85% of 6.5 TB/s, and a start and end.
+double project_tiles_time(const ProjectArgs &a) {
+    const int64_t tiles = (int64_t)((a.T + 255) / 256) * ((a.N + 255) / 256), pairs = max(device_info().sm_count / 2, 1);
+    const double steps = (double)((tiles + pairs - 1) / pairs) * ((a.K + 63) / 64);
+    return fmax(0.21 * steps, 2e-6 * a.K * ((double)a.T + a.N) / 5.6) + 5;
+}
+
 cudaError_t launch_project_tiles(const ProjectArgs &a, int dtype, cudaStream_t s) {
     return dtype == MOE_DTYPE_F16 ? launch<true>(a, s) : launch<false>(a, s);
 }

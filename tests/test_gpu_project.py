@@ -144,3 +144,11 @@ def test_no_rows_is_a_no_op():
     x, w, _, _ = _make(1, 64, 64, BF)
     cfg = abi.project_config(64, 64)
     abi.moe_project(cfg, x[:0], w, torch.empty(0, 64, dtype=BF, device="cuda"), abi.alloc_project_workspace(cfg, 0))
+
+
+@pytest.mark.parametrize("T,K,N", [(2, 1024, 4104), (5, 1032, 8200), (16, 2048, 2056), (32, 264, 2008), (33, 2048, 256), (160, 1024, 8200),
+                                   (256, 520, 4104), (192, 2048, 1032), (1100, 1032, 96), (520, 2048, 200), (900, 2048, 256), (40, 512, 65536)])
+def test_either_side_of_each_choice_of_kernel(T, K, N):
+    """Few rows with many and few weights, and short sides of which the long one has few and many tiles."""
+    x, w, bias, resid = _make(T, K, N, F16, seed=T + N)
+    _check(_run(x, w, act="gelu", bias=bias, resid=resid), x, w, bias, resid, "gelu", 1.0, (T, K, N))
