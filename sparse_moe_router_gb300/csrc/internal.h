@@ -9,6 +9,14 @@
 
 namespace moe {
 
+// A CUDA call's outcome.  One that failed is reported by the entry point that made it, and by none after it: launches look
+// at the thread's last error, which would still hold this one.
+inline moe_status cuda_status(cudaError_t e) {
+    if (e == cudaSuccess) return MOE_OK;
+    cudaGetLastError();
+    return MOE_ERR_CUDA;
+}
+
 // Kernel classes for launch counting and optional per-kernel timing.
 enum KernelClass {
     KC_ROUTER_GEMM = 0,   // router logits on tensor cores

@@ -23,7 +23,7 @@ bool good_dtype(int d) { return d == MOE_DTYPE_BF16 || d == MOE_DTYPE_F16; }
         moe_status _st = (expr);       \
         if (_st != MOE_OK) return _st; \
     } while (0)
-#define MOE_CUDA(expr) MOE_TRY((expr) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA)
+#define MOE_CUDA(expr) MOE_TRY(cuda_status(expr))
 
 // A row of `width` 16-bit values read or written in 16-byte pieces.
 bool good_rows(const void *p, int64_t ld, int64_t width) { return p && aligned16(p) && ld >= width && ld % 8 == 0; }

@@ -273,11 +273,6 @@ moe_status check_ws(const moe_config *c, void *ws, size_t ws_bytes, int T) {
     return MOE_OK;
 }
 
-moe_status cuda_status(cudaError_t e) {
-    if (e == cudaSuccess) return MOE_OK;
-    return MOE_ERR_CUDA;
-}
-
 #define MOE_TRY(expr)                          \
     do {                                       \
         moe_status _st = (expr);               \
