@@ -23,7 +23,7 @@ __global__ void __launch_bounds__(kThreads) project_rows_kernel(const __grid_con
     ptx::wait_prior_grid();
     const int warp = (int)threadIdx.x >> 5, lane = (int)threadIdx.x & 31;
     const int group = warp / S, share = warp % S;
-    const int n0 = ((int)blockIdx.y * (kWarps / S) + group) * kWRows, t0 = (int)blockIdx.x * X;
+    const int n0 = ((int)blockIdx.x * (kWarps / S) + group) * kWRows, t0 = (int)blockIdx.y * X;
     float acc[kWRows][X];
 #pragma unroll
     for (int i = 0; i < kWRows; ++i)
@@ -68,7 +68,7 @@ __global__ void __launch_bounds__(kThreads) project_rows_kernel(const __grid_con
     __syncthreads();
     for (int e = (int)threadIdx.x; e < kWarps / S * kWRows * X; e += kThreads) {
         const int g = e / (kWRows * X), i = e / X % kWRows, j = e % X;
-        const int n = ((int)blockIdx.y * (kWarps / S) + g) * kWRows + i, t = t0 + j;
+        const int n = ((int)blockIdx.x * (kWarps / S) + g) * kWRows + i, t = t0 + j;
         if (n >= p.N || t >= p.T) continue;
         float z = 0.f;
 #pragma unroll
@@ -94,7 +94,7 @@ cudaError_t launch_shape(const ProjectArgs &a, cudaStream_t s) {
     cudaLaunchAttribute attr[1];
     overlap_prior(attr[0]);
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((a.T + X - 1) / X, (a.N + rows - 1) / rows);
+    cfg.gridDim = dim3((a.N + rows - 1) / rows, (a.T + X - 1) / X);  // (2^20 outputs are more blocks than y has places)
     cfg.blockDim = dim3(kThreads);
     cfg.stream = s;
     cfg.attrs = attr;

@@ -4,6 +4,9 @@ import torch
 
 from sparse_moe_router_gb300 import abi
 
+import layer_ref
+import mixer_ref as ref
+
 pytestmark = pytest.mark.gpu
 BF = torch.bfloat16
 
@@ -28,3 +31,18 @@ def test_a_call_that_fails_leaves_no_error_to_the_next():
     y = torch.empty(1, 8, dtype=BF, device="cuda")
     abi.moe_project(small, torch.ones_like(x), torch.ones_like(w[:8]), y, ws)
     assert y.tolist() == [[4096.0] * 8]
+
+
+@pytest.mark.parametrize("K,N", [(4096, 524280), (4096, 524288), (4096, 1 << 20), (8192, 524296), (8, 1 << 20), (1032, 1 << 20)])
+def test_one_row_of_many_outputs(K, N):
+    """On either side of 65,535 blocks of 8 outputs: every output is that of the 8 rows it repeats."""
+    x, base, w = _make(K, N)
+    cfg = abi.project_config(K, N)
+    ws = abi.alloc_project_workspace(cfg, 1)
+    y = torch.full((1, N), 7.0, dtype=BF, device="cuda")
+    abi.moe_project(cfg, x, w, y, ws)
+    assert abi.moe_check_status(ws) == 0
+    want, size = ref.project(x, base, None, None, "none", 1.0)
+    bound = layer_ref.HALF_STEP[BF] * want.abs() + 2 * ref.EPS32 * (K / 4 + 256) * size
+    assert float(((y[:, :8].cpu().double() - want).abs() - bound).max()) <= 0
+    assert torch.equal(y.view(N // 8, 8), y[:, :8].expand(N // 8, 8))
