@@ -492,9 +492,11 @@ size_t moe_linear_workspace_size(const moe_linear_config *cfg, int max_seqs, int
  * q, k [T, KH, DK], v, out [T, VH, DV], row strides q_ld, k_ld, v_ld, out_ld.  decay fp32, g <= 0: [T, VH] with row
  * stride decay_ld >= VH, or with decay_ld = 0 one value a head, [VH]; NULL: g = 0.  g = -infinity forgets the
  * state; below -10,000 a decay counts as that (its factor is 0 either way).
- * States and sums are fp32.  Long runs are computed chunk by chunk on tensor cores, with decays, weighted values,
- * states and products of queries and keys as sums of two or three 16-bit values (at least 16 bits, states 22); out is
- * rounded once.  Deterministic, but a run's length decides which kernel takes it, so the last bits of a
+ * States and sums are fp32.  Long runs are computed chunk by chunk, 64 tokens each, on tensor cores, whose operands are sums
+ * of 16-bit values.  What enters a state, a token's value times its decay up to the chunk's end, has 24 bits with bf16 and 22
+ * with fp16; what an output sees, the state at the chunk's begin and the decayed products of queries and keys, 16 with bf16
+ * and 22 with fp16.  With fp16 that holds down to 2^-17, and what is smaller is kept to 2^-39, of the largest one of the same
+ * channel and chunk, channel of the state, or query.  out is rounded once.  Factors below 2^-126 count as 0.  Deterministic, but a run's length decides which kernel takes it, so the last bits of a
  * state depend on how a prompt is cut.  A value of v that is not finite makes its channel not finite from its token on.
  * Reported as MOE_ERR_INVALID_ARG in the status word: a slot outside [0, n_slots) (the sequence begins with S = 0
  * and its state is not kept); a range of rows outside the batch (no tokens); a decay above 0 or NaN (taken as 0).

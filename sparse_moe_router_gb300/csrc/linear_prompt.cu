@@ -8,8 +8,9 @@
 //   A = Q K^T (tokens x tokens), U^T = (w V)^T K (channels x DK), O1^T = S0^T Q^T, O2^T = V^T P^T (channels x tokens),
 // P = A weighted and masked.  The tensor cores take 16-bit operands, so what is rounded for them is split: P and S0
 // into two parts, the weighted values into three in bf16 and two in fp16 (a state's error stays below
-// that of its fp32 sums).  With fp16, whose range is short, each row of P, each channel of S0 and each chunk's weighted
-// values are scaled by a power of two.
+// that of its fp32 sums).  With fp16, whose range is short, each row of P, each channel of S0 and each channel of a chunk's
+// weighted values are scaled by a power of two of their own: two parts then hold 22 bits, down to 2^-39 of the largest.  (One power
+// for all channels of a chunk took 4% less time, and left a channel 2^-26 as large as another 11 bits.)
 //
 // A block walks one value head's chunks (128 value channels at most) in order.  The state is what makes it wait: U(c) ->
 // registers -> S0(c+1) in TMEM; everything else runs ahead.  Where heads and sequences leave SMs idle, a
@@ -44,7 +45,7 @@ constexpr int kOutWarp = 4, kValueWarp = 8, kWeightWarp = 12, kLoadWarp = 14, kM
 // and the roles spill, into an L1 that shared memory has left next to nothing of).
 template <bool STATES>
 struct Regs {
-    static constexpr int kState = STATES ? 216 : 232, kOut = STATES ? 96 : 80, kValue = 80, kOther = 120;
+    static constexpr int kState = STATES ? 216 : 232, kOut = 96, kValue = STATES ? 80 : 64, kOther = 120;
     static_assert(kState + kOut + kValue + kOther <= 512, "more registers than the block has");
 };
 constexpr uint64_t kWaitNs = 2000000000ull;  // 2 s, of the waits when a block gives up
@@ -61,9 +62,9 @@ struct alignas(16) Slot {
     float fade[kChunk];                // scale e^{G_i}
     float p_unit[kChunk];              // fp16: P's rows hold scale / p_unit of their values
     float s_unit[128];                 // fp16: and S0's channels
+    float u_unit[128];                 // fp16: U's channels hold 1 / u_unit of their values
     int bad[128];                      // first token whose value is not finite, of each channel
     float whole;                       // e^{G_64}
-    float u_unit;                      // fp16: U holds 1 / u_unit of its values
     int any_bad;
 };
 
@@ -168,11 +169,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint64_t *u_full = v_free + 2, *u_free = u_full + 2;             // [2] U in TMEM; read (without outputs: of even and odd chunks)
     uint64_t *s_full = u_free + 2, *s_free = s_full + 1;             // S0 in TMEM; read by its product
     uint64_t *o_full = s_free + 1, *o_free = o_full + 1;             // O1 and O2 in TMEM (and P read); read
-    uint64_t *m_full = o_free + 1;                                   // fp16: the warps' largest weighted values
-    uint64_t *drain = m_full + 1;
+    uint64_t *drain = o_free + 1;
     uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(drain + 1);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_holder + 1);
-    float *most = reinterpret_cast<float *>(tmem_holder + 2);  // [2 x 8] those, of even and odd chunks
     Slot *slots = reinterpret_cast<Slot *>(smem + C::kSlotAt);
 
     const int tid = (int)threadIdx.x, lane = tid & 31;
@@ -216,7 +215,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             ptx::mbar_init(&v_full[i], kConvWarps), ptx::mbar_init(&v_free[i], 1);
         }
         // (u_full and o_full: the MMAs' end, and the arrival of the warp that has seen the units of their operands)
-        ptx::mbar_init(m_full, kConvWarps);
         for (int i = 0; i < 2; ++i) ptx::mbar_init(&u_full[i], 2), ptx::mbar_init(&u_free[i], C::kLaneWarps);
         ptx::mbar_init(s_full, C::kLaneWarps), ptx::mbar_init(s_free, 1);
         ptx::mbar_init(o_full, 2), ptx::mbar_init(o_free, C::kLaneWarps);
@@ -240,69 +238,70 @@ __global__ void __launch_bounds__(kThreads, 1)
     int issued = 0;  // chunks whose copies were begun
 
     // ----------------------------------------------------------------- weighted values --
-    // Thread t has 16-byte pieces t, t + 128 (256), ... of the tile as it lies in shared memory (swizzled): of rows t / 8 + 16 i
-    // (32 i) of each block.  What comes out lies in the same places.  Two halves of 32 tokens, the one's products under way
-    // while the other is weighed.
+    // A thread has the 8 channels of one 16-byte column of the tile, of every kRows-th token from r0 on, as they lie in shared
+    // memory (swizzled: 8 lanes on 8 rows touch all banks); a warp has all 64 tokens of its channels.  What comes out lies in the
+    // same places.  Two halves of 32 tokens, the one's products under way while the other is weighed.
     auto weigh_values = [&]() {
-        constexpr int kStep = kConvWarps * 512, kRowStep = kConvWarps * 4;  // bytes and rows from one piece to a thread's next
-        constexpr int kPieces = C::kVBlocks * kBlockBytes / kStep, kHalf = 32 / kRowStep;
-        const int conv = warp - (kWeightWarp - kConvWarps), t = conv * 32 + lane, r0 = t >> 3;
-        const int ch0 = ((t & 7) ^ (r0 & 7)) * 8;  // its channels in each block (rows differ by multiples of 8)
+        constexpr int kGroups = DV / 8 / kConvWarps, kRows = 32 / kGroups, kPieces = kChunk / kRows;
+        const int conv = warp - (kWeightWarp - kConvWarps), t = conv * 32 + lane, r0 = lane % kRows, group = conv * kGroups + lane / kRows;
+        const int place = (group >> 3) * kBlockBytes + r0 * 128 + (((group ^ r0) & 7) << 4);
         for (int c = 0; c < chunks && ok; ++c) {
             Slot &sl = slots[c % kSlots];
             uint8_t *stage = smem + c % kStages * C::kStageBytes;
             if (!(ok = wait(&g_full[c % kSlots], c / kSlots) && wait(&full[c % kStages], c / kStages))) break;
             const int valid = min(rows - c * kChunk, kChunk);
-            auto row_of = [&](int i) { return r0 + i * kRowStep % kChunk; };
-            auto piece = [&](int i) { return reinterpret_cast<uint4 *>(stage + C::kV + t * 16 + i * kStep); };
+            auto piece = [&](int i) { return reinterpret_cast<uint4 *>(stage + C::kV + place + i * (kRows * 128)); };
             if (valid < kChunk) {  // behind the run's end, where whatever comes there lies: the products must not see it
+                const uint4 zero = make_uint4(0, 0, 0, 0);
 #pragma unroll 1
-                for (int i = 0; i < (C::kKBlocks + C::kVBlocks) * kBlockBytes / kStep; ++i)
-                    if (row_of(i) >= valid) *reinterpret_cast<uint4 *>(stage + C::kK + t * 16 + i * kStep) = make_uint4(0, 0, 0, 0);
+                for (int i = 0; i < kPieces; ++i)
+                    if (r0 + i * kRows >= valid) *piece(i) = zero;
+#pragma unroll 1
+                for (int at = t * 16; at < C::kKBlocks * kBlockBytes; at += kConvWarps * 512)
+                    if ((at >> 7) % kChunk >= valid) *reinterpret_cast<uint4 *>(stage + C::kK + at) = zero;
             }
-            float unit = 1.f;
-            if (F16) {  // the chunk's largest finite one
-                float m = 0.f;
-                uint4 w[kPieces];
-#pragma unroll
-                for (int i = 0; i < kPieces; ++i) w[i] = *piece(i);
+            float2 unit[4];  // fp16: a power of two for each channel, by its largest weighted value of the chunk
+            if (F16) {
+                uint32_t most[4] = {0, 0, 0, 0};  // (rounded to bf16, which has the exponents; a NaN does not count)
+                auto larger = [](uint32_t a, uint32_t b) {
+                    const __nv_bfloat162 m = __hmax2(*reinterpret_cast<const __nv_bfloat162 *>(&a), *reinterpret_cast<const __nv_bfloat162 *>(&b));
+                    return *reinterpret_cast<const uint32_t *>(&m);
+                };
 #pragma unroll
                 for (int i = 0; i < kPieces; ++i) {
-                    const __half2 *h = reinterpret_cast<const __half2 *>(&w[i]);
-                    const __half2 most2 = __hmax2(__hmax2(__habs2(h[0]), __habs2(h[1])), __hmax2(__habs2(h[2]), __habs2(h[3])));
-                    const float2 a = __half22float2(most2);
-                    float top = fmaxf(a.x, a.y);
-                    if (top > 65504.f) {  // an infinity: the largest of the others
-                        top = 0.f;
-#pragma unroll 1
-                        for (int j = 0; j < 8; ++j) {
-                            const float x = fabsf(load1<F16>(reinterpret_cast<const uint16_t *>(piece(i)) + j));
-                            if (x <= 65504.f) top = fmaxf(top, x);
-                        }
-                    }
-                    m = fmaxf(m, top * sl.weight[row_of(i)]);
-                }
-                m = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(m)));
-                float *all = most + (c & 1) * 8;
-                if (lane == 0) all[conv] = m;
-                arrive(m_full);
-                if (!(ok = wait(m_full, c))) break;
+                    const uint4 w = *piece(i);
+                    const uint32_t raw[4] = {w.x, w.y, w.z, w.w};
+                    const float2 f = both(sl.weight[r0 + i * kRows]);
 #pragma unroll
-                for (int i = 0; i < kConvWarps; ++i) m = fmaxf(m, all[i]);
-                const int e = lift(m);
-                unit = pow2f(e);
-                if (t == 0) sl.u_unit = pow2f(-e);
+                    for (int j = 0; j < 4; ++j) {
+                        const float2 x = __fmul2_rn(unpack2<F16>(raw[j]), f);
+                        most[j] = larger(most[j], pack2<false>(x.x, x.y) & 0x7fff7fffu);
+                    }
+                }
+#pragma unroll
+                for (int o = kRows / 2; o > 0; o >>= 1)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) most[j] = larger(most[j], __shfl_xor_sync(0xffffffffu, most[j], o));
+                // from an exponent E of at least 15 to 268 - E, two at a time: the largest comes to lie between 2^14 and 2^15
+#pragma unroll
+                for (int j = 0; j < 4; ++j) unit[j] = unpack2<false>(0x86008600u - larger(most[j] & 0x7f807f80u, 0x07800780u));
+                if (r0 == 0) {  // what undoes them, exponents 254 - (268 - E)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        *reinterpret_cast<float2 *>(&sl.u_unit[group * 8 + 2 * j]) =
+                            make_float2(__int_as_float((254 << 23) - __float_as_int(unit[j].x)), __int_as_float((254 << 23) - __float_as_int(unit[j].y)));
+                }
             }
-            uint8_t *dst = smem + C::kValues + t * 16;
+            uint8_t *dst = smem + C::kValues + place;
             float2 sum = both(0.f);
 #pragma unroll 1
             for (int half = 0; half < 2; ++half) {  // tokens 0..31, 32..63
                 if (c > 0 && !(ok = wait(&v_free[half], c - 1))) break;  // the last chunk's have been read
                 uint4 raw[kPieces / 2];  // (loads cannot pass the stores by themselves)
                 float weight[kPieces / 2];
-                auto number = [&](int n) { return n / kHalf * (2 * kHalf) + half * kHalf + n % kHalf; };
+                const int first = half * (kPieces / 2);
 #pragma unroll
-                for (int n = 0; n < kPieces / 2; ++n) raw[n] = *piece(number(n)), weight[n] = sl.weight[row_of(number(n))] * unit;
+                for (int n = 0; n < kPieces / 2; ++n) raw[n] = *piece(first + n), weight[n] = sl.weight[r0 + (first + n) * kRows];
 #pragma unroll
                 for (int n = 0; n < kPieces / 2; ++n) {
                     float2 x[4] = {unpack2<F16>(raw[n].x), unpack2<F16>(raw[n].y), unpack2<F16>(raw[n].z), unpack2<F16>(raw[n].w)};
@@ -310,6 +309,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int j = 0; j < 4; ++j) {
                         sum = __ffma2_rn(x[j], both(0.f), sum);
                         x[j] = __fmul2_rn(x[j], both(weight[n]));
+                        if (F16) x[j] = __fmul2_rn(x[j], unit[j]);
                     }
 #pragma unroll
                     for (int part = 0; part < C::kParts; ++part) {
@@ -319,7 +319,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             w[j] = pack2<F16>(x[j].x, x[j].y);
                             if (part + 1 < C::kParts) x[j] = rest<F16>(x[j], w[j]);
                         }
-                        *reinterpret_cast<uint4 *>(dst + part * C::kPartBytes + number(n) * kStep) = make_uint4(w[0], w[1], w[2], w[3]);
+                        *reinterpret_cast<uint4 *>(dst + part * C::kPartBytes + (first + n) * (kRows * 128)) = make_uint4(w[0], w[1], w[2], w[3]);
                     }
                 }
                 // A value that is not finite makes its channel of the state that; of the tokens before it the product with P must
@@ -327,11 +327,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (half == 1 && __any_sync(0xffffffffu, sum.x != 0.f || sum.y != 0.f)) {
 #pragma unroll 1
                     for (int e = 0; e < kPieces * 8; ++e) {
-                        const int i = e >> 3;
-                        uint16_t *src = reinterpret_cast<uint16_t *>(piece(i)) + (e & 7);
+                        uint16_t *src = reinterpret_cast<uint16_t *>(piece(e >> 3)) + (e & 7);
                         if (fabsf(load1<F16>(src)) <= 3.4028234e38f) continue;
                         *src = 0;
-                        atomicMin(&sl.bad[i * kRowStep / kChunk * 64 + ch0 + (e & 7)], row_of(i));
+                        atomicMin(&sl.bad[group * 8 + (e & 7)], r0 + (e >> 3) * kRows);
                         sl.any_bad = 1;
                     }
                     __syncwarp();
@@ -412,7 +411,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 if (!(ok = wait(&u_full[c % kUs], c / kUs))) break;
                 ptx::tc_fence_after();
-                const float f = sl.whole, unit = F16 ? sl.u_unit : 1.f;
+                const float f = sl.whole, unit = F16 ? sl.u_unit[tid] : 1.f;
 #pragma unroll
                 for (int g = 0; g < DK / 32; ++g) {
                     uint32_t u[32];
