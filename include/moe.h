@@ -475,6 +475,8 @@ typedef struct {
     const int32_t *q_start; /* [B+1], q_start[0] = 0, not descending */
     const int32_t *kv_len;  /* [B] tokens of the sequence so far, this batch's included */
     const int32_t *slots;   /* [B] where its state lies in the pool */
+    int longest;            /* the most new tokens that a sequence has, or 0 where the host does not know.  Kernels are
+                             * chosen by it: a value that is not so costs time, no result hangs on it */
 } moe_state_batch;
 
 /* Bytes of workspace for moe_linear_attention on batches of up to max_seqs sequences and max_tokens new

@@ -95,7 +95,7 @@ class _StatePool(ctypes.Structure):
 
 class _StateBatch(ctypes.Structure):
     _fields_ = [("n_seqs", ctypes.c_int), ("n_tokens", ctypes.c_int), ("q_start", ctypes.c_void_p), ("kv_len", ctypes.c_void_p),
-                ("slots", ctypes.c_void_p)]
+                ("slots", ctypes.c_void_p), ("longest", ctypes.c_int)]
 
 
 class HeadNormConfig(ctypes.Structure):
@@ -645,12 +645,13 @@ class StatePool:
 
 class StateBatch:
     """A batch of sequences (moe_state_batch): q_start int32 [B + 1], kv_len and slots int32 [B], all on the device;
-    their contents may change between calls, n_tokens may not."""
+    their contents may change between calls, n_tokens may not.  longest: the most new tokens that a sequence has, 0: not
+    known (kernels are chosen by it, no result hangs on it)."""
 
-    def __init__(self, q_start, kv_len, slots, n_tokens):
+    def __init__(self, q_start, kv_len, slots, n_tokens, longest=0):
         B = kv_len.shape[0]
         self.c = _StateBatch(B, int(n_tokens), _device_array(q_start, "q_start", torch.int32, (B + 1,)),
-                             _device_array(kv_len, "kv_len", torch.int32, (B,)), _device_array(slots, "slots", torch.int32, (B,)))
+                             _device_array(kv_len, "kv_len", torch.int32, (B,)), _device_array(slots, "slots", torch.int32, (B,)), int(longest))
         self.q_start, self.kv_len, self.slots = q_start, kv_len, slots
         self.n_tokens = int(n_tokens)
 
