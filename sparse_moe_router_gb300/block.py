@@ -131,11 +131,22 @@ class DecoderLayers:
                 self.pages.grow(b, n)
         dev = self.rope.device
         return self.with_states(abi.KVBatch(torch.tensor(starts, dtype=torch.int32, device=dev),
-                                            torch.tensor(self.pages.lens, dtype=torch.int32, device=dev), self.pages.table, starts[-1]))
+                                            torch.tensor(self.pages.lens, dtype=torch.int32, device=dev), self.pages.table, starts[-1]),
+                                new_tokens)
 
-    def with_states(self, batch):
-        """The batch with what the recurrent layers read of it; a sequence's state has its own number."""
-        batch.states = abi.StateBatch(batch.q_start, batch.kv_len, self.slots, batch.n_tokens)
+    def with_states(self, batch, new_tokens):
+        """The batch with what the recurrent layers read of it; a sequence's state has its own number.  Sequences without new
+        tokens are left out: a run is cut by how many sequences there are."""
+        if self.linear is None:
+            return batch
+        q_start, kv_len, slots, live = batch.q_start, batch.kv_len, self.slots, [b for b, n in enumerate(new_tokens) if n]
+        if len(live) < len(new_tokens):
+            starts = [0]
+            for b in live:
+                starts.append(starts[-1] + new_tokens[b])
+            arrays = torch.tensor(starts + [self.pages.lens[b] for b in live] + live, dtype=torch.int32, device=self.rope.device)
+            q_start, kv_len, slots = arrays.split([len(live) + 1, len(live), len(live)])
+        batch.states = abi.StateBatch(q_start, kv_len, slots, batch.n_tokens, longest=max(new_tokens))
         return batch
 
     def recurrent(self, i, batch, y, out):
@@ -211,7 +222,7 @@ class DecodeGraph:
         self.x = torch.zeros(B, H, dtype=torch.bfloat16, device=model.rope.device)
         self.kv_len = torch.zeros(B, dtype=torch.int32, device=model.rope.device)
         starts = torch.arange(B + 1, dtype=torch.int32, device=model.rope.device)
-        self.batch = model.with_states(abi.KVBatch(starts, self.kv_len, model.pages.table, B))
+        self.batch = model.with_states(abi.KVBatch(starts, self.kv_len, model.pages.table, B), [1] * B)
         model.run(self.x, self.batch)  # warms up; with length 0 the tokens' position is negative: nothing is cached, no state changes
         torch.cuda.current_stream().synchronize()
         self.graph = torch.cuda.CUDAGraph()
