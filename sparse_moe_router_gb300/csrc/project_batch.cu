@@ -204,16 +204,18 @@ cudaError_t held(const Held **out) {
     Held &h = all[dev];
     if (!h.ready.load(std::memory_order_acquire)) {
         std::lock_guard<std::mutex> hold(lock);
-        auto *kernel = project_batch_kernel<SWAP, F16>;
-        cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMostSmem);
-        if (e != cudaSuccess) return e;
-        h.clusters[1] = device_info().sm_count;
-        for (int n = 2; n <= kMaxSplit; ++n) {
-            cudaLaunchAttribute attr[2];
-            const cudaLaunchConfig_t cfg = config<SWAP, F16>(attr, (int64_t)n * device_info().sm_count, n, kMostSmem, nullptr);
-            if ((e = cudaOccupancyMaxActiveClusters(&h.clusters[n], kernel, &cfg)) != cudaSuccess) return e;
+        if (!h.ready.load(std::memory_order_relaxed)) {  // (another thread may have filled it, and others read it, meanwhile)
+            auto *kernel = project_batch_kernel<SWAP, F16>;
+            cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMostSmem);
+            if (e != cudaSuccess) return e;
+            h.clusters[1] = device_info().sm_count;
+            for (int n = 2; n <= kMaxSplit; ++n) {
+                cudaLaunchAttribute attr[2];
+                const cudaLaunchConfig_t cfg = config<SWAP, F16>(attr, (int64_t)n * device_info().sm_count, n, kMostSmem, nullptr);
+                if ((e = cudaOccupancyMaxActiveClusters(&h.clusters[n], kernel, &cfg)) != cudaSuccess) return e;
+            }
+            h.ready.store(true, std::memory_order_release);
         }
-        h.ready.store(true, std::memory_order_release);
     }
     *out = &h;
     return cudaSuccess;
