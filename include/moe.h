@@ -528,8 +528,8 @@ typedef struct {
 /* The norm of each head of each row, with its weight and gate, in fp32, rounded once:
  *   y = (x - m) * w / sqrt(mean((x - m)^2) + eps) * act(gate),  m = mean(x) with center, else 0
  * x, gate, y [T, heads, D], row strides x_ld, gate_ld, y_ld in elements (multiples of 8, at least heads * D); y may be
- * x or gate.  weight may be NULL (1); gate is NULL with MOE_HEAD_GATE_NONE only.  16-byte aligned.  No
- * workspace; deterministic. */
+ * x or gate.  act is good to 2^-16, and 0 below gate = -87.  weight may be NULL (1); gate is NULL with MOE_HEAD_GATE_NONE
+ * only.  16-byte aligned.  No workspace; deterministic. */
 moe_status moe_head_norm(const moe_head_norm_config *cfg, const void *x, int64_t x_ld, const void *weight,
                          const void *gate, int64_t gate_ld, void *y, int64_t y_ld, int T, void *stream);
 
@@ -564,6 +564,8 @@ typedef struct {
 size_t moe_project_workspace_size(const moe_project_config *cfg, int max_T);
 
 /* y = resid + alpha * act(x w^T + bias): 16-bit products, sums and epilogue in fp32, rounded once.
+ * With 16-bit y the sigmoid's e^-z is good to 2^-16, and below z = -87 sigmoid and SiLU are 0; with fp32 y both keep a few
+ * ulp of the result down to fp32's least value.
  * Deterministic.  T of 0 does nothing, more than 2^30 rows are not supported.  y must not overlap x or w. */
 moe_status moe_project(const moe_project_config *cfg, const moe_project_io *io, int T, void *ws, size_t ws_bytes,
                        void *stream);

@@ -252,7 +252,7 @@ moe_status moe_project(const moe_project_config *cfg, const moe_project_io *io, 
     a.T = T;
     a.K = c.inputs;
     a.N = c.outputs;
-    a.act = c.act;
+    a.act = !c.out_f32 ? c.act : c.act == MOE_ACT_SILU ? kSilu32 : c.act == MOE_ACT_SIGMOID ? kSigmoid32 : c.act;
     a.out_f32 = c.out_f32;
     a.scale = c.scale;
     a.status = static_cast<int *>(ws);
