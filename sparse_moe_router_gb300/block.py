@@ -70,6 +70,23 @@ class Pages:
         self.pages[seq], self.lens[seq] = [], 0
 
 
+def check_recurrent(H, c, layers):
+    """Raises unless the recurrent layers' calls can be made with this config and these weights: a step that one of them
+    refuses halfway would leave lengths that count tokens which were never written."""
+    kd, vd = c.key_heads * c.key_dim, c.value_heads * c.value_dim
+    if abi._TORCH_DTYPES[c.dtype] is not torch.bfloat16:
+        raise ValueError("linear_cfg is for float16, the stack is bfloat16")
+    if max(2 * kd, vd) > 65536:
+        raise ValueError("heads of %d and %d values in all, at most 65536 can be normed" % (2 * kd, vd))
+    shapes = {"w_mix": [(2 * kd + 2 * vd, H)], "w_decay": [(c.value_heads, H)], "b_decay": [(c.value_heads,)], "w_mix_out": [(H, vd)],
+              "mix_norm": [(c.value_dim,), (c.value_heads, c.value_dim)]}
+    for i, l in enumerate(layers):
+        for name in shapes if "w_mix" in l else ():
+            t = l.get(name)
+            if t is None or tuple(t.shape) not in shapes[name] or t.dtype is not torch.bfloat16:
+                raise ValueError("layer %d: %s is not bfloat16 of shape %s" % (i, name, " or ".join(map(str, shapes[name]))))
+
+
 class DecoderLayers:
     """layers: a list of dicts with w_qkv [(QH + 2 KH) D, H], w_o [H, QH D], norm_attn, norm_attn_out,
     norm_moe, norm_moe_out [H] (a missing *_out: no norm after that block), attn_gate [H] (optional, layer by layer), and the MoE
@@ -87,6 +104,8 @@ class DecoderLayers:
             raise ValueError("a recurrent layer needs linear_cfg")
         if linear_cfg is not None and linear_cfg.value_heads % 8:
             raise ValueError("the decays' product has a multiple of 8 outputs, not %d value heads" % linear_cfg.value_heads)
+        if linear_cfg is not None:
+            check_recurrent(H, linear_cfg, layers)
         self.caches = [None if "w_mix" in l else abi.KVCache.alloc(attn_cfg, pages.n_pages, dev) for l in layers]
         self.weights = [abi.weights(l) for l in layers]
         self.moe_ws = abi.alloc_workspace(moe_cfg, max_tokens, dev)
