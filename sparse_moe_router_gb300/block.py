@@ -153,19 +153,21 @@ class DecoderLayers:
                                             torch.tensor(self.pages.lens, dtype=torch.int32, device=dev), self.pages.table, starts[-1]),
                                 new_tokens)
 
-    def with_states(self, batch, new_tokens):
+    def with_states(self, batch, new_tokens=None):
         """The batch with what the recurrent layers read of it; a sequence's state has its own number.  Sequences without new
-        tokens are left out: a run is cut by how many sequences there are."""
+        tokens are left out, where new_tokens tells: a run is cut by how many sequences there are."""
         if self.linear is None:
             return batch
-        q_start, kv_len, slots, live = batch.q_start, batch.kv_len, self.slots, [b for b, n in enumerate(new_tokens) if n]
+        q_start, kv_len, slots = batch.q_start, batch.kv_len, self.slots
+        new_tokens = new_tokens or []
+        live = [b for b, n in enumerate(new_tokens) if n]
         if len(live) < len(new_tokens):
             starts = [0]
             for b in live:
                 starts.append(starts[-1] + new_tokens[b])
             arrays = torch.tensor(starts + [self.pages.lens[b] for b in live] + live, dtype=torch.int32, device=self.rope.device)
             q_start, kv_len, slots = arrays.split([len(live) + 1, len(live), len(live)])
-        batch.states = abi.StateBatch(q_start, kv_len, slots, batch.n_tokens, longest=max(new_tokens))
+        batch.states = abi.StateBatch(q_start, kv_len, slots, batch.n_tokens, longest=max(new_tokens, default=0))
         return batch
 
     def recurrent(self, i, batch, y, out):

@@ -40,3 +40,11 @@ def test_sequences_without_new_tokens_are_left_out(monkeypatch, new, starts, len
 
 def test_a_stack_without_recurrent_layers_has_no_states(monkeypatch):
     assert not hasattr(stack(monkeypatch, linear=False).batch([1, 0, 0, 2]), "states")
+
+
+def test_a_batch_of_which_only_the_device_knows(monkeypatch):
+    """All sequences are handed over, and nothing is said of the longest run."""
+    m = stack(monkeypatch)
+    i32 = lambda *v: torch.tensor(v, dtype=torch.int32)  # noqa: E731
+    s = m.with_states(HandedKV(i32(0, 1, 1, 5, 5), i32(3, 4, 5, 6), m.pages.table, 5)).states
+    assert (s.q_start, s.kv_len, s.slots, s.n_tokens, s.longest) == ([0, 1, 1, 5, 5], [3, 4, 5, 6], [0, 1, 2, 3], 5, 0)
