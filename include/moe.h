@@ -488,8 +488,8 @@ size_t moe_linear_workspace_size(const moe_linear_config *cfg, int max_seqs, int
  *   S   = e^g S + k v^T          S [DK, DV] the sequence's state, g the token's log decay
  *   out = scale * S^T q
  * A sequence whose first new token has position 0 (kv_len = n) begins with S = 0, whatever its slot holds; any other
- * begins with its slot's state.  The state after its last new token is written to the slot.  A sequence without new
- * tokens leaves its slot alone.  Tokens at negative positions (padding in front) do not count, and get out rows of 0.
+ * begins with its slot's state.  The state after its last new token is written to the slot: who may want to take tokens
+ * back copies the slot first.  A sequence without new tokens leaves its slot alone.  Tokens at negative positions (padding in front) do not count, and get out rows of 0.
  * Rows from q_start[B] on stay untouched.
  * q, k [T, KH, DK], v, out [T, VH, DV], row strides q_ld, k_ld, v_ld, out_ld.  decay fp32, g <= 0: [T, VH] with row
  * stride decay_ld >= VH, or with decay_ld = 0 one value a head, [VH]; NULL: g = 0.  g = -infinity forgets the

@@ -7,7 +7,7 @@
 //
 // Bound: instructions (issue slots 83% used; one head of 128 takes 16 lanes some 110 of them, with a gate 150), then HBM.
 // Measured: 8192 x 32 heads of 128 with a SiLU gate 35.2 us (5.7 TB/s, 84% of the measured copy), without 27.6; one row of 32
-// heads 1.4.  On the way: 64-bit places and an IEEE root and division 45.6; two, three and four heads a thread 38.0, 37.8 and
+// heads 1.4 (5.3 for a call from Python).  On the way: 64-bit places and an IEEE root and division 45.6; two, three and four heads a thread 38.0, 37.8 and
 // 40.9 where one took 36.7 (registers); paired fp32 arithmetic 36.4 against 35.2.
 #include "mixer.h"
 #include "ptx.cuh"

@@ -7,7 +7,8 @@
 //
 // Bound: HBM, 2 x 4 DK DV bytes a head and sequence; for a few heads the launch and three dependent reads (the sequence, its
 // state, the joined sums).  Measured, 32 heads of 128 and 128: one sequence 2.8 us, 48 sequences 35.6 to 38 (5.3 to 5.7 TB/s,
-// 78 to 84% of the measured copy), 200 130 (95%); 8 sequences of 4 tokens, 8 heads of 64 and 64, 3.1.
+// 78 to 84% of the measured copy), 200 130 (95%); 8 sequences of 4 tokens, 8 heads of 64 and 64, 3.1.  (A call from Python
+// takes 4 to 5 us of the host beside that.)
 #include "mixer.h"
 
 namespace moe {

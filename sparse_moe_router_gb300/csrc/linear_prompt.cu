@@ -24,7 +24,7 @@
 // cost 30%), and what a chunk's decays need is read two chunks ahead.
 //
 // Measured, 32 value heads and 16 key heads of 128: 8192 tokens 112 us (39 of them the first kernel's) where token by token
-// takes 10,270; 512 tokens 21, 64 tokens 7.7; 12 runs of up to 1031 tokens, 20 heads of 64 and 128 in fp16, 50 (its longest run's
+// takes 10,270; 512 tokens 21, 64 tokens 7.7; 12 runs of up to 1031 tokens, 20 heads of 64 and 128 in fp16, 52 (its longest run's
 // 17 chunks, one after another: fp16's scales of P take a pass of their own).  On the way: decays in 64-bit floats 3000 cycles a
 // chunk; outputs stored 2 bytes at a time 10,000; A in one place 97 us for the second kernel where two take 84; weighted values as
 // an operand in TMEM, 16 or 32 tokens at a time, 116 to 126 in all.

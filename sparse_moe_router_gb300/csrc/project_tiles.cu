@@ -6,8 +6,8 @@
 // what runs at once shares rows of w.
 //
 // Bound: the tensor cores (95% of the cycles busy) where tiles fill the rounds.  Measured: 8192 rows of 2048 and 12,288
-// outputs 209 to 220 us (1870 to 1970 TFLOP/s; cuBLAS's burst rate here is 1887), 246 when the power cap holds the clock at
-// 1.55 GHz (1675; cuBLAS's sustained rate is 1694); 1031 rows of 1032, 4104 outputs, bias and GELU
+// outputs 209 to 220 us (1870 to 1970 TFLOP/s; cuBLAS's burst rate here is 1887), 243 to 251 when the power cap holds the clock
+// at 1.55 GHz (1640 to 1700; cuBLAS's sustained rate is 1694); 1031 rows of 1032, 4104 outputs, bias and GELU
 // in fp16 20.3 us, where 5 row tiles and tiles of 144 outputs make 145 for 76 pairs (128 outputs: 27; two rounds of
 // 17 steps take 8, the epilogue of the last round, start and end the rest).  The MMAs are issued by an elected lane
 // of a warp that waits as a whole: a lane chosen by comparison takes 610 cycles a step of K whatever the tile, this
